@@ -251,6 +251,188 @@ MOE_API const char *moe_strerror(int code);
  * the caller's buffers).  NULL is allowed. */
 MOE_API void moe_destroy(moe_ctx *ctx);
 
+/* ------------------------------------------------------------------------
+ * The MoE block around the expert layer: the norms before and after it, the
+ * router with its balance loss, and dense products with FP4 weights for a
+ * few tokens (a shared expert at decode).
+ *
+ * These calls keep no context: the configuration travels with every call,
+ * device memory (workspaces, laid-out weights, outputs) is the caller's,
+ * calls are stream-ordered and asynchronous, and argument errors are found
+ * on the host before anything is launched.  They may be captured into CUDA
+ * graphs.  Row pitches `ld_*` are in elements; rows themselves are
+ * contiguous, and any pitch >= the row length and any element-aligned base
+ * works (16-byte aligned rows are the fast case).  num_tokens = 0 launches
+ * nothing that reads tokens: sums over tokens come out zero.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
+
+/* ---- block norms ---- */
+
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 } moe_gate;
+
+/* Input formats of the expert layer that the norm can write itself:
+ * MOE_QUANT_FP8_128: E4M3 codes with f32 scales amax/448 per 128 columns
+ *   (x, x_sf of MOE_W_FP8_BLK128);
+ * MOE_QUANT_UE8M0_32: E4M3 codes with UE8M0 scales 2^ceil(log2(amax/448))
+ *   per 32 columns (x, x_sf of MOE_W_FP4_E2M1_UE8M0_32).
+ * An all-zero group has scale 0 (UE8M0 code 0) and codes 0. */
+typedef enum { MOE_QUANT_NONE = 0, MOE_QUANT_FP8_128 = 1, MOE_QUANT_UE8M0_32 = 2 } moe_quant;
+
+#define MOE_NORM_MAX_HIDDEN 16384
+
+typedef struct {
+    int hidden;           /* H, 1..MOE_NORM_MAX_HIDDEN; a multiple of 128 / 32 with the quantised outputs */
+    int stream_dtype;     /* moe_dtype of residual, y, h, n and of their gradients */
+    int param_dtype;      /* moe_dtype of w_post, w_pre and gate (their gradients are f32) */
+    int gate;             /* moe_gate: shape of `gate`, [H] or [T] */
+    int quant;            /* moe_quant */
+    float eps;            /* > 0 */
+    float residual_scale; /* finite */
+} moe_norm_config;
+
+/* Forward, per token (all in f32, rounded once per output):
+ *   r1 = (mean(y^2) + eps)^-1/2,  u = y r1 w_post      (w_post NULL: u = y)
+ *   z  = residual_scale * residual + gate u            (gate NULL: 1)
+ *   r2 = (mean(z^2) + eps)^-1/2,  v = z r2 w_pre       (w_pre NULL: none of this)
+ * h = z and n = v in the stream's type, codes / sf = v quantised.  Without y
+ * the block part is absent: z = residual, and w_post, gate and h must be
+ * NULL.  h may be residual itself (same pitch). */
+typedef struct {
+    const void *residual; int64_t ld_residual;  /* [T, H] */
+    const void *y; int64_t ld_y;                /* [T, H] block output, or NULL */
+    const void *w_post;                         /* [H] or NULL */
+    const void *gate;                           /* [H] / [T] as cfg->gate says, NULL with MOE_GATE_NONE */
+    const void *w_pre;                          /* [H] or NULL */
+    void *h; int64_t ld_h;                      /* [T, H] out, with y */
+    void *n; int64_t ld_n;                      /* [T, H] out or NULL, with w_pre */
+    uint8_t *codes;                             /* [T, H] out, with cfg->quant */
+    void *sf;                                   /* f32 [T, H/128] or u8 [T, H/32] out, with cfg->quant */
+    float *rstd_post, *rstd_pre;                /* [T] out or NULL: r1, r2 for the backward pass */
+} moe_norm_io;
+
+MOE_API int moe_norm_forward(const moe_norm_config *cfg, int num_tokens, const moe_norm_io *io, void *stream);
+
+/* Backward of the same.  With a = dn w_pre, zh = h r2, yh = y r1:
+ *   D = dh + r2 (a - zh mean(a zh))           dresidual = residual_scale D
+ *   b = D gate w_post                         dy = r1 (b - yh mean(b yh))
+ *   dw_pre = sum_t dn zh                      dw_post = sum_t D gate yh
+ *   dgate  = sum D u over t (channel) or h (token)
+ * h stands for z (it is z rounded); the quantiser passes its gradient
+ * straight through (add it to dn).  Sums over tokens are taken in a fixed
+ * order: the same call gives the same bits.  dh NULL means zero; with dn NULL
+ * the pre norm takes no part (w_pre, rstd_pre, dw_pre NULL).  Without y:
+ * dresidual = D, and everything of the block is NULL.  dresidual may be dh,
+ * dy may be dn (same pitches). */
+typedef struct {
+    const void *h; int64_t ld_h;                /* [T, H] stream after the block (without y: the residual) */
+    const void *y; int64_t ld_y;
+    const void *w_post, *gate, *w_pre;
+    const float *rstd_post, *rstd_pre;          /* [T], with w_post / w_pre */
+    const void *dh; int64_t ld_dh;              /* [T, H] or NULL */
+    const void *dn; int64_t ld_dn;              /* [T, H] or NULL */
+    void *dresidual; int64_t ld_dresidual;      /* [T, H] out */
+    void *dy; int64_t ld_dy;                    /* [T, H] out, with y */
+    float *dw_post, *dgate, *dw_pre;            /* f32 out: [H], [H] / [T], [H] */
+} moe_norm_grad_io;
+
+/* Bytes of device workspace of moe_norm_backward, 256-byte aligned (0 if
+ * `cfg` is invalid or num_tokens < 0); larger batches need no less. */
+MOE_API size_t moe_norm_workspace_bytes(const moe_norm_config *cfg, int num_tokens);
+MOE_API int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const moe_norm_grad_io *io,
+                              void *d_workspace, void *stream);
+
+/* ---- router and balance loss ---- */
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+    int num_experts;      /* E, 1..1024 */
+    int topk;             /* k, 1..min(32, E) */
+    int score;            /* moe_score of the logits: s = softmax or sigmoid */
+    int renormalize;      /* weights = weight_scale * s / (sum of the chosen s), else weight_scale * s */
+    int logits_dtype;     /* moe_dtype of logits and d_logits */
+    float weight_scale;   /* finite */
+    float balance_coef;   /* alpha of the balance loss, finite */
+    float z_coef;         /* beta of the z loss, finite; 0 with MOE_SCORE_SIGMOID */
+} moe_router_config;
+
+/* The choice: the k largest logit + bias (f32 sums), ties to the lowest
+ * expert.  A logit of -inf or NaN, or a sum that is, closes its expert for
+ * the token; a slot with no open expert left gets topk_idx -1 and weight 0
+ * (moe_forward's inactive slot).  +inf counts as the largest finite f32.  The
+ * bias takes no part in the scores. */
+
+/* Losses of a batch of S sequences (token ranges), over the tokens that have
+ * an open logit (n_s of sequence s, S' sequences with n_s > 0, N in all), with
+ * p the scores scaled to sum 1 and c the chosen slots of each expert:
+ *   balance = alpha / S' sum_s sum_e (E c_se / (k n_s)) (sum_t p_te / n_s)
+ *   z       = beta / N sum_t logsumexp(logits_t)^2
+ * c is a constant for the gradient. */
+typedef struct {
+    int num_seqs;                  /* S >= 1 */
+    const int32_t *seq_offsets;    /* [S+1] nondecreasing token offsets within [0, T], or NULL: S = 1, all tokens.
+                                      Tokens outside every range are routed but enter no loss */
+    float *loss;                   /* [3]: total, balance, z */
+    int32_t *counts;               /* [S, E]: c */
+    float *prob_mean;              /* [S, E]: sum_t p / n_s (0 for an empty sequence) */
+    int32_t *seq_tokens;           /* [S + 2]: n_s of each sequence, then S' and N */
+} moe_balance_io;
+
+/* Bytes of device workspace of the calls that compute losses, 256-byte
+ * aligned (0 if the arguments are invalid). */
+MOE_API size_t moe_router_workspace_bytes(const moe_router_config *cfg, int max_tokens, int max_seqs);
+
+/* topk_idx int32 [T, k] and topk_weights f32 [T, k] (moe_forward's inputs)
+ * from logits [T, E]; bias f32 [E] or NULL.  With `loss` (else NULL, and
+ * d_workspace unused) the losses of this choice in the same pass. */
+MOE_API int moe_router_forward(const moe_router_config *cfg, int num_tokens, const void *logits, int64_t ld_logits,
+                               const float *bias, int32_t *topk_idx, float *topk_weights,
+                               const moe_balance_io *loss, void *d_workspace, void *stream);
+
+/* The losses of a choice made elsewhere: topk_idx int32 [T, k] is an input,
+ * each row's experts distinct (ids outside [0, E) are inactive slots). */
+MOE_API int moe_balance_loss(const moe_router_config *cfg, int num_tokens, const void *logits, int64_t ld_logits,
+                             const int32_t *topk_idx, const moe_balance_io *loss, void *d_workspace, void *stream);
+
+/* d_logits [T, E] = the gradient through topk_weights (d_weights f32 [T, k],
+ * or NULL) plus d_loss (f32 scalar on the device, or NULL) times that of
+ * loss[0].  `loss` holds what the forward call wrote (counts and seq_tokens
+ * are read; NULL with d_loss NULL).  Closed experts get 0. */
+MOE_API int moe_router_backward(const moe_router_config *cfg, int num_tokens, const void *logits, int64_t ld_logits,
+                                const int32_t *topk_idx, const float *d_weights, const moe_balance_io *loss,
+                                const float *d_loss, void *d_logits, int64_t ld_d_logits, void *stream);
+
+/* ---- FP4 linear for a few tokens ---- */
+
+typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
+
+#define MOE_FP4_LINEAR_MAX_TOKENS 16
+
+typedef struct {
+    int in_features;   /* K, a multiple of 32 */
+    int out_features;  /* N rows of the weight; even with MOE_ACT_SWIGLU */
+    int act;           /* moe_act; SWIGLU: rows [0, N/2) gate, [N/2, N) up, output silu(gate) * up of N/2 columns */
+    int out_dtype;     /* moe_dtype of add and y */
+    float act_clamp;   /* symmetric clamp of gate and up before SWIGLU; +INFINITY = off */
+} moe_fp4_linear_config;
+
+/* Weights in the layer's FP4 format (MOE_W_FP4_E2M1_UE8M0_32): w u8 [N, K/2]
+ * (low nibble = even k), w_sf u8 UE8M0 [N, K/32] (code 255 is not a number
+ * and must not occur).  They are laid out once into a store of
+ * moe_fp4_linear_weight_bytes() bytes (0 if `cfg` is invalid; 256-byte
+ * aligned) and may be freed once the stream has passed that call. */
+MOE_API size_t moe_fp4_linear_weight_bytes(const moe_fp4_linear_config *cfg);
+MOE_API int moe_fp4_linear_transform_weights(const moe_fp4_linear_config *cfg, const void *w, const void *w_sf,
+                                             void *d_weights, void *stream);
+
+/* y [T, N or N/2] = act(x W^T) (+ add), x bf16 [T, K], 0 <= T <=
+ * MOE_FP4_LINEAR_MAX_TOKENS, sums in f32.  add may be y itself (same pitch). */
+MOE_API int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tokens, const void *x, int64_t ld_x,
+                                   const void *d_weights, const void *add, int64_t ld_add, void *y, int64_t ld_y,
+                                   void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,6 +35,9 @@ ABI_SYMBOLS = (
     "moe_forward", "moe_forward_host", "moe_get_dispatch", "moe_get_intermediates",
     "moe_dispatch_noalloc", "moe_profile_begin", "moe_profile_end", "moe_test_arm_timeout",
     "moe_device_status", "moe_strerror", "moe_destroy",
+    "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward",
+    "moe_router_workspace_bytes", "moe_router_forward", "moe_balance_loss", "moe_router_backward",
+    "moe_fp4_linear_weight_bytes", "moe_fp4_linear_transform_weights", "moe_fp4_linear_forward",
 )
 
 
@@ -42,6 +45,40 @@ class MoEConfig(ctypes.Structure):
     _fields_ = [("max_tokens", ctypes.c_int), ("hidden", ctypes.c_int), ("inter", ctypes.c_int),
                 ("num_experts", ctypes.c_int), ("topk", ctypes.c_int), ("wfmt", ctypes.c_int),
                 ("act_clamp", ctypes.c_float), ("fast_math", ctypes.c_int)]
+
+
+def _struct(name, *fields):
+    return type(name, (ctypes.Structure,), {"_fields_": [f for g in fields for f in g]})
+
+
+def _ints(*names):
+    return [(n, ctypes.c_int) for n in names]
+
+
+def _floats(*names):
+    return [(n, ctypes.c_float) for n in names]
+
+
+def _ptrs(*names):
+    return [(n, ctypes.c_void_p) for n in names]
+
+
+def _pitched(*names):
+    return [f for n in names for f in ((n, ctypes.c_void_p), ("ld_" + n, ctypes.c_int64))]
+
+
+# the structures of include/moe.h, field for field
+NormConfig = _struct("NormConfig", _ints("hidden", "stream_dtype", "param_dtype", "gate", "quant"),
+                     _floats("eps", "residual_scale"))
+NormIO = _struct("NormIO", _pitched("residual", "y"), _ptrs("w_post", "gate", "w_pre"), _pitched("h", "n"),
+                 _ptrs("codes", "sf", "rstd_post", "rstd_pre"))
+NormGradIO = _struct("NormGradIO", _pitched("h", "y"), _ptrs("w_post", "gate", "w_pre", "rstd_post", "rstd_pre"),
+                     _pitched("dh", "dn", "dresidual", "dy"), _ptrs("dw_post", "dgate", "dw_pre"))
+RouterConfig = _struct("RouterConfig", _ints("num_experts", "topk", "score", "renormalize", "logits_dtype"),
+                       _floats("weight_scale", "balance_coef", "z_coef"))
+BalanceIO = _struct("BalanceIO", _ints("num_seqs"), _ptrs("seq_offsets", "loss", "counts", "prob_mean", "seq_tokens"))
+Fp4LinearConfig = _struct("Fp4LinearConfig", _ints("in_features", "out_features", "act", "out_dtype"),
+                          _floats("act_clamp"))
 
 
 class MoEError(RuntimeError):
@@ -93,6 +130,21 @@ def lib():
             L.moe_strerror.argtypes = [i32]
             L.moe_destroy.restype = None
             L.moe_destroy.argtypes = [vp]
+            i64, ncfg, rcfg, fcfg, bio = (ctypes.c_int64, ctypes.POINTER(NormConfig), ctypes.POINTER(RouterConfig),
+                                          ctypes.POINTER(Fp4LinearConfig), ctypes.POINTER(BalanceIO))
+            for name, res, args in (
+                    ("moe_norm_forward", i32, [ncfg, i32, ctypes.POINTER(NormIO), vp]),
+                    ("moe_norm_workspace_bytes", sz, [ncfg, i32]),
+                    ("moe_norm_backward", i32, [ncfg, i32, ctypes.POINTER(NormGradIO), vp, vp]),
+                    ("moe_router_workspace_bytes", sz, [rcfg, i32, i32]),
+                    ("moe_router_forward", i32, [rcfg, i32, vp, i64, vp, vp, vp, bio, vp, vp]),
+                    ("moe_balance_loss", i32, [rcfg, i32, vp, i64, vp, bio, vp, vp]),
+                    ("moe_router_backward", i32, [rcfg, i32, vp, i64, vp, vp, bio, vp, vp, i64, vp]),
+                    ("moe_fp4_linear_weight_bytes", sz, [fcfg]),
+                    ("moe_fp4_linear_transform_weights", i32, [fcfg, vp, vp, vp, vp]),
+                    ("moe_fp4_linear_forward", i32, [fcfg, i32, vp, i64, vp, vp, i64, vp, i64, vp])):
+                fn = getattr(L, name)
+                fn.restype, fn.argtypes = res, args
             _lib = L
     return _lib
 
@@ -264,3 +316,6 @@ class MoELayer:
             self.close()
         except Exception:
             pass
+
+
+from .block import BlockNorm, Fp4Linear, NormGrads, NormOutput, Router, RouterOutput  # noqa: E402,F401

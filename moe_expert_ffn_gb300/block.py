@@ -1,0 +1,342 @@
+"""The MoE block around the expert layer: BlockNorm, Router and Fp4Linear.
+
+Like MoELayer these allocate device memory through PyTorch, check shapes and
+types, marshal pointers and turn error codes into exceptions; everything they
+compute runs in the CUDA library (include/moe.h).  Every call takes ``out``
+buffers made once with ``buffers()`` / ``grad_buffers()``, so that a decode
+loop allocates nothing, and allocates them itself when it gets none.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import (MOE_ERR_INVALID_ARG, Fp4LinearConfig, MoEError, NormConfig, NormGradIO, NormIO, RouterConfig,
+               BalanceIO, _check, lib)
+
+DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+GATES = {None: 0, "channel": 1, "token": 2}
+QUANTS = {None: 0, "fp8": 1, "ue8m0": 2}
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTS = {None: 0, "swiglu": 1}
+FP4_LINEAR_MAX_TOKENS = 16
+
+
+def _device(device):
+    d = torch.device(device if device is not None else "cuda")
+    return torch.device(d.type, torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
+def _choice(table, key, name):
+    if key not in table:
+        raise ValueError(f"{name} must be one of {list(table)}, got {key!r}")
+    return table[key]
+
+
+def _stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _rows(t, name, dtype, rows, cols, device):
+    """(pointer, row pitch) of a [rows, cols] tensor whose rows are contiguous."""
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(rows, cols)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows < 2:
+        pitch = cols
+    elif pitch < cols:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.data_ptr(), pitch
+
+
+def _flat(t, name, dtype, shape, device):
+    """Pointer of a contiguous tensor."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+class NormOutput:
+    """What BlockNorm.forward writes: h, n, codes, sf, rstd_post, rstd_pre (None where absent)."""
+    __slots__ = ("h", "n", "codes", "sf", "rstd_post", "rstd_pre")
+
+
+class NormGrads:
+    """What BlockNorm.backward writes: dresidual, dy, dw_post, dgate, dw_pre (None where absent)."""
+    __slots__ = ("dresidual", "dy", "dw_post", "dgate", "dw_pre")
+
+
+class BlockNorm:
+    """The norms after one block and before the next in one pass:
+    h = residual_scale * residual + gate * rmsnorm(y) * w_post, then n = rmsnorm(h) * w_pre,
+    with n also as the expert layer's quantised input (``quant``: "fp8" = E4M3 with f32 scales per 128
+    columns, "ue8m0" = E4M3 with UE8M0 scales per 32).  ``gate`` is None, "channel" ([hidden]) or
+    "token" ([T]).  y is optional in forward (the first norm of a network), w_post and w_pre too."""
+
+    def __init__(self, hidden, eps=1e-6, residual_scale=1.0, gate=None, quant=None, dtype=torch.bfloat16,
+                 param_dtype=torch.float32, device=None):
+        self.hidden, self.dtype, self.param_dtype, self.gate, self.quant = int(hidden), dtype, param_dtype, gate, quant
+        self.device = _device(device)
+        self.cfg = NormConfig(int(hidden), _choice(DTYPES, dtype, "dtype"), _choice(DTYPES, param_dtype, "param_dtype"),
+                              _choice(GATES, gate, "gate"), _choice(QUANTS, quant, "quant"), float(eps), float(residual_scale))
+        if lib().moe_norm_workspace_bytes(self.cfg, 1) == 0:
+            raise MoEError(MOE_ERR_INVALID_ARG, "norm config")
+        self._workspace = None
+
+    def buffers(self, num_tokens, block=True, post=True, pre=True, normed=True) -> NormOutput:
+        """Outputs of a forward of `num_tokens`: with y (`block`), w_post (`post`), w_pre (`pre`), n (`normed`)."""
+        T, H, dev = num_tokens, self.hidden, self.device
+        o = NormOutput()
+        o.h = torch.empty(T, H, dtype=self.dtype, device=dev) if block else None
+        o.rstd_post = torch.empty(T, dtype=torch.float32, device=dev) if block and post else None
+        o.rstd_pre = torch.empty(T, dtype=torch.float32, device=dev) if pre else None
+        o.n = torch.empty(T, H, dtype=self.dtype, device=dev) if pre and (normed or not self.quant) else None
+        o.codes = o.sf = None
+        if pre and self.quant:
+            o.codes = torch.empty(T, H, dtype=torch.uint8, device=dev)
+            o.sf = (torch.empty(T, H // 128, dtype=torch.float32, device=dev) if self.quant == "fp8"
+                    else torch.empty(T, H // 32, dtype=torch.uint8, device=dev))
+        return o
+
+    def grad_buffers(self, num_tokens, block=True, post=True, pre=True) -> NormGrads:
+        T, H, dev = num_tokens, self.hidden, self.device
+        g = NormGrads()
+        g.dresidual = torch.empty(T, H, dtype=self.dtype, device=dev)
+        g.dy = torch.empty(T, H, dtype=self.dtype, device=dev) if block else None
+        g.dw_post = torch.empty(H, dtype=torch.float32, device=dev) if block and post else None
+        g.dw_pre = torch.empty(H, dtype=torch.float32, device=dev) if pre else None
+        g.dgate = (torch.empty(H if self.gate == "channel" else T, dtype=torch.float32, device=dev)
+                   if block and self.gate else None)
+        return g
+
+    def _params(self, T, w_post, gate, w_pre):
+        H, dt, dev = self.hidden, self.param_dtype, self.device
+        return (None if w_post is None else _flat(w_post, "w_post", dt, (H,), dev),
+                None if gate is None else _flat(gate, "gate", dt, (H,) if self.gate == "channel" else (T,), dev),
+                None if w_pre is None else _flat(w_pre, "w_pre", dt, (H,), dev))
+
+    def forward(self, residual, y=None, w_post=None, gate=None, w_pre=None, normed=True, out=None, stream=None) -> NormOutput:
+        T, H, dt, dev, f32 = residual.shape[0], self.hidden, self.dtype, self.device, torch.float32
+        if out is None:
+            out = self.buffers(T, y is not None, w_post is not None, w_pre is not None, normed)
+        io = NormIO()
+        io.residual, io.ld_residual = _rows(residual, "residual", dt, T, H, dev)
+        io.w_post, io.gate, io.w_pre = self._params(T, w_post, gate, w_pre)
+        if y is not None:
+            io.y, io.ld_y = _rows(y, "y", dt, T, H, dev)
+            io.h, io.ld_h = _rows(out.h, "h", dt, T, H, dev)
+            if w_post is not None and out.rstd_post is not None:
+                io.rstd_post = _flat(out.rstd_post, "rstd_post", f32, (T,), dev)
+        if w_pre is not None:
+            if out.n is not None:
+                io.n, io.ld_n = _rows(out.n, "n", dt, T, H, dev)
+            if out.rstd_pre is not None:
+                io.rstd_pre = _flat(out.rstd_pre, "rstd_pre", f32, (T,), dev)
+            if self.quant == "fp8":
+                io.codes = _flat(out.codes, "codes", torch.uint8, (T, H), dev)
+                io.sf = _flat(out.sf, "sf", f32, (T, H // 128), dev)
+            elif self.quant:
+                io.codes = _flat(out.codes, "codes", torch.uint8, (T, H), dev)
+                io.sf = _flat(out.sf, "sf", torch.uint8, (T, H // 32), dev)
+        rc = lib().moe_norm_forward(self.cfg, T, io, _stream(stream, dev))
+        if rc:
+            _check(rc, "moe_norm_forward")
+        return out
+
+    def backward(self, h, dh=None, dn=None, y=None, w_post=None, gate=None, w_pre=None, rstd_post=None, rstd_pre=None,
+                 out=None, stream=None) -> NormGrads:
+        """Gradients from dh (of the stream h) and dn (of the normed n).  Uses a workspace of this object,
+        so backward passes of one BlockNorm must not run concurrently."""
+        T, H, dt, dev, f32 = h.shape[0], self.hidden, self.dtype, self.device, torch.float32
+        if out is None:
+            out = self.grad_buffers(T, y is not None, w_post is not None, w_pre is not None)
+        io = NormGradIO()
+        io.h, io.ld_h = _rows(h, "h", dt, T, H, dev)
+        io.w_post, io.gate, io.w_pre = self._params(T, w_post, gate, w_pre)
+        if dh is not None:
+            io.dh, io.ld_dh = _rows(dh, "dh", dt, T, H, dev)
+        if dn is not None:
+            io.dn, io.ld_dn = _rows(dn, "dn", dt, T, H, dev)
+        io.dresidual, io.ld_dresidual = _rows(out.dresidual, "dresidual", dt, T, H, dev)
+        if y is not None:
+            io.y, io.ld_y = _rows(y, "y", dt, T, H, dev)
+            io.dy, io.ld_dy = _rows(out.dy, "dy", dt, T, H, dev)
+        if w_post is not None:
+            io.dw_post = _flat(out.dw_post, "dw_post", f32, (H,), dev)
+            io.rstd_post = None if rstd_post is None else _flat(rstd_post, "rstd_post", f32, (T,), dev)
+        if w_pre is not None:
+            io.dw_pre = _flat(out.dw_pre, "dw_pre", f32, (H,), dev)
+            io.rstd_pre = None if rstd_pre is None else _flat(rstd_pre, "rstd_pre", f32, (T,), dev)
+        if gate is not None:
+            io.dgate = _flat(out.dgate, "dgate", f32, (H,) if self.gate == "channel" else (T,), dev)
+        need = lib().moe_norm_workspace_bytes(self.cfg, T)
+        if self._workspace is None or self._workspace.numel() < need:
+            self._workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        rc = lib().moe_norm_backward(self.cfg, T, io, self._workspace.data_ptr(), _stream(stream, dev))
+        if rc:
+            _check(rc, "moe_norm_backward")
+        return out
+
+
+class RouterOutput:
+    """What Router writes: topk_idx, topk_weights and, with the losses, loss ([3]: total, balance, z),
+    counts [S, E], prob_mean [S, E], seq_tokens [S] (views of ``tokens`` [S + 2])."""
+    __slots__ = ("topk_idx", "topk_weights", "loss", "counts", "prob_mean", "seq_tokens", "tokens")
+
+
+class Router:
+    """Top-k router: topk_idx and topk_weights for MoELayer.forward from logits, the balance and z losses
+    with per-sequence expert counts, and the gradient of the logits.  Losses use a workspace of this
+    object: two loss calls of one Router must not run concurrently."""
+
+    def __init__(self, num_experts, topk, score="softmax", renormalize=True, weight_scale=1.0, balance_coef=0.0, z_coef=0.0,
+                 logits_dtype=torch.float32, max_tokens=None, max_seqs=1, device=None):
+        self.num_experts, self.topk, self.logits_dtype = int(num_experts), int(topk), logits_dtype
+        self.max_tokens, self.max_seqs = max_tokens, int(max_seqs)
+        self.device = _device(device)
+        self.cfg = RouterConfig(int(num_experts), int(topk), _choice(SCORES, score, "score"), int(bool(renormalize)),
+                                _choice(DTYPES, logits_dtype, "logits_dtype"), float(weight_scale), float(balance_coef),
+                                float(z_coef))
+        need = lib().moe_router_workspace_bytes(self.cfg, 0 if max_tokens is None else int(max_tokens), self.max_seqs)
+        if need == 0:
+            raise MoEError(MOE_ERR_INVALID_ARG, "router config")
+        # only the loss calls need it: they need to know max_tokens
+        self._workspace = None if max_tokens is None else torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def buffers(self, num_tokens, num_seqs=None) -> RouterOutput:
+        """Outputs of a call on `num_tokens`, with those of the losses for `num_seqs` sequences."""
+        T, k, E, dev = num_tokens, self.topk, self.num_experts, self.device
+        o = RouterOutput()
+        o.topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        o.topk_weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+        o.loss = o.counts = o.prob_mean = o.seq_tokens = o.tokens = None
+        if num_seqs is not None:
+            o.loss = torch.empty(3, dtype=torch.float32, device=dev)
+            o.counts = torch.empty(num_seqs, E, dtype=torch.int32, device=dev)
+            o.prob_mean = torch.empty(num_seqs, E, dtype=torch.float32, device=dev)
+            o.tokens = torch.empty(num_seqs + 2, dtype=torch.int32, device=dev)
+            o.seq_tokens = o.tokens[:num_seqs]
+        return o
+
+    def _losses(self, T, seq_offsets, out, write=True):
+        S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+        E, dev = self.num_experts, self.device
+        if write and (self.max_tokens is None or T > self.max_tokens or S > self.max_seqs):
+            raise ValueError(f"{T} tokens in {S} sequences: the router was made for losses of "
+                             f"{self.max_tokens} tokens in {self.max_seqs}")
+        io = BalanceIO()
+        io.num_seqs = S
+        if seq_offsets is not None:
+            io.seq_offsets = _flat(seq_offsets, "seq_offsets", torch.int32, (S + 1,), dev)
+        io.loss = _flat(out.loss, "loss", torch.float32, (3,), dev)
+        io.counts = _flat(out.counts, "counts", torch.int32, (S, E), dev)
+        io.prob_mean = _flat(out.prob_mean, "prob_mean", torch.float32, (S, E), dev)
+        io.seq_tokens = _flat(out.tokens, "tokens", torch.int32, (S + 2,), dev)
+        return io
+
+    def _forward(self, logits, bias, loss_seqs, seq_offsets, out, stream):
+        T, E, k, dev = logits.shape[0], self.num_experts, self.topk, self.device
+        if out is None:
+            out = self.buffers(T, loss_seqs)
+        ptr, ld = _rows(logits, "logits", self.logits_dtype, T, E, dev)
+        b = None if bias is None else _flat(bias, "bias", torch.float32, (E,), dev)
+        idx = _flat(out.topk_idx, "topk_idx", torch.int32, (T, k), dev)
+        wts = _flat(out.topk_weights, "topk_weights", torch.float32, (T, k), dev)
+        io = ws = None
+        if loss_seqs is not None:
+            io, ws = self._losses(T, seq_offsets, out), self._workspace.data_ptr()
+        rc = lib().moe_router_forward(self.cfg, T, ptr, ld, b, idx, wts, io, ws, _stream(stream, dev))
+        if rc:
+            _check(rc, "moe_router_forward")
+        return out
+
+    def forward(self, logits, bias=None, out=None, stream=None) -> RouterOutput:
+        """topk_idx and topk_weights of logits [T, E] (bias f32 [E]: for the choice alone)."""
+        return self._forward(logits, bias, None, None, out, stream)
+
+    def forward_train(self, logits, bias=None, seq_offsets=None, out=None, stream=None) -> RouterOutput:
+        """The same with the losses, in one pass; seq_offsets int32 [S + 1], or None for one sequence."""
+        S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
+        return self._forward(logits, bias, S, seq_offsets, out, stream)
+
+    def balance_loss(self, logits, topk_idx, seq_offsets=None, out=None, stream=None) -> RouterOutput:
+        """The losses of a choice made elsewhere."""
+        T, E, dev = logits.shape[0], self.num_experts, self.device
+        if out is None:
+            out = self.buffers(T, 1 if seq_offsets is None else seq_offsets.shape[0] - 1)
+        ptr, ld = _rows(logits, "logits", self.logits_dtype, T, E, dev)
+        idx = _flat(topk_idx, "topk_idx", torch.int32, (T, self.topk), dev)
+        io = self._losses(T, seq_offsets, out)
+        rc = lib().moe_balance_loss(self.cfg, T, ptr, ld, idx, io, self._workspace.data_ptr(), _stream(stream, dev))
+        if rc:
+            _check(rc, "moe_balance_loss")
+        return out
+
+    def backward(self, logits, fwd, d_weights=None, d_loss=None, seq_offsets=None, out=None, stream=None):
+        """d_logits through topk_weights (`d_weights` [T, k]) and through loss[0] (`d_loss`, an f32 scalar on the
+        device); `fwd` is what the forward call returned."""
+        T, E, k, dev = logits.shape[0], self.num_experts, self.topk, self.device
+        if out is None:
+            out = torch.empty(T, E, dtype=self.logits_dtype, device=dev)
+        ptr, ld = _rows(logits, "logits", self.logits_dtype, T, E, dev)
+        dptr, dld = _rows(out, "d_logits", self.logits_dtype, T, E, dev)
+        idx = dw = io = dl = None
+        if d_weights is not None:
+            idx = _flat(fwd.topk_idx, "topk_idx", torch.int32, (T, k), dev)
+            dw = _flat(d_weights, "d_weights", torch.float32, (T, k), dev)
+        if d_loss is not None:
+            io, dl = self._losses(T, seq_offsets, fwd, write=False), _flat(d_loss, "d_loss", torch.float32, d_loss.shape, dev)
+            if d_loss.numel() != 1:
+                raise ValueError("d_loss must hold one value")
+        rc = lib().moe_router_backward(self.cfg, T, ptr, ld, idx, dw, io, dl, dptr, dld, _stream(stream, dev))
+        if rc:
+            _check(rc, "moe_router_backward")
+        return out
+
+
+class Fp4Linear:
+    """y = act(x W^T) (+ add) of 1 to 16 tokens with E2M1 weights under UE8M0 scales per 32 (the layer's FP4
+    format); act "swiglu": rows [0, N/2) gate, [N/2, N) up, N/2 outputs."""
+
+    def __init__(self, in_features, out_features, act=None, out_dtype=torch.bfloat16, act_clamp=math.inf, device=None):
+        self.device, self.out_dtype = _device(device), out_dtype
+        self.in_features, self.out_features = int(in_features), int(out_features)
+        self.out_columns = self.out_features // 2 if act == "swiglu" else self.out_features
+        self.cfg = Fp4LinearConfig(int(in_features), int(out_features), _choice(ACTS, act, "act"),
+                                   _choice(DTYPES, out_dtype, "out_dtype"), float(act_clamp))
+        need = lib().moe_fp4_linear_weight_bytes(self.cfg)
+        if need == 0:
+            raise MoEError(MOE_ERR_INVALID_ARG, "fp4 linear config")
+        self.weights = torch.empty(need, dtype=torch.uint8, device=self.device)
+        self._ready = False
+
+    def transform_weights(self, w, w_sf, stream=None):
+        N, K, dev = self.out_features, self.in_features, self.device
+        wp = _flat(w, "w", torch.uint8, (N, K // 2), dev)
+        sp = _flat(w_sf, "w_sf", torch.uint8, (N, K // 32), dev)
+        _check(lib().moe_fp4_linear_transform_weights(self.cfg, wp, sp, self.weights.data_ptr(), _stream(stream, dev)),
+               "moe_fp4_linear_transform_weights")
+        self._ready = True
+
+    def buffers(self, num_tokens):
+        return torch.empty(num_tokens, self.out_columns, dtype=self.out_dtype, device=self.device)
+
+    def forward(self, x, add=None, out=None, stream=None):
+        if not self._ready:
+            raise MoEError(-6, "moe_fp4_linear_forward")
+        T, n, dev = x.shape[0], self.out_columns, self.device
+        if out is None:
+            out = self.buffers(T)
+        xp, ldx = _rows(x, "x", torch.bfloat16, T, self.in_features, dev)
+        yp, ldy = _rows(out, "y", self.out_dtype, T, n, dev)
+        ap, lda = (None, 0) if add is None else _rows(add, "add", self.out_dtype, T, n, dev)
+        rc = lib().moe_fp4_linear_forward(self.cfg, T, xp, ldx, self.weights.data_ptr(), ap, lda, yp, ldy, _stream(stream, dev))
+        if rc:
+            _check(rc, "moe_fp4_linear_forward")
+        return out

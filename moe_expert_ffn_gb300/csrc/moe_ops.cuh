@@ -1,0 +1,83 @@
+// moe_ops.cuh -- what the kernels around the expert layer (norms, router, FP4
+// linear) share: element types, reductions and the layer's quantisers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+using bf16 = __nv_bfloat16;
+
+inline bool valid_dtype(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
+inline size_t dtype_bytes(int d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
+inline bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(bf16 v) { return __bfloat162float(v); }
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+
+// Sum over the CTA in a fixed order; `red` holds one float per warp and must
+// not be used again before the next barrier of the CTA.
+template <int kWarps>
+__device__ __forceinline__ float block_sum(float v, float *red) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += red[w];
+    return s;
+}
+
+// FP8 group scale sf = amax / 448 and q = v / sf as v times 448/amax (within
+// one f32 rounding of the division, far inside an E4M3 step).  Below 2^-100
+// the reciprocal would pass the f32 range, so v is brought up by 2^64 first;
+// an all-zero group has sf 0 and codes 0.
+struct Fp8Scale {
+    float sf, up, inv;
+    __device__ __forceinline__ float apply(float v) const { return v * up * inv; }
+};
+__device__ __forceinline__ Fp8Scale fp8_scale(float amax) {
+    Fp8Scale q;
+    q.sf = amax / 448.0f;
+    q.up = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+    q.inv = amax > 0.0f ? 448.0f / (amax * q.up) : 0.0f;
+    return q;
+}
+
+// UE8M0 exponent of the smallest power of two 2^e with amax/448 <= 2^e (the
+// ratio in binary32), e in [-127, 127]; -127 for an all-zero group.
+__device__ __forceinline__ int ue8m0_exponent(float amax) {
+    const float r = amax / 448.0f;
+    if (!(r > 0.0f)) return -127;
+    int ex;
+    const float fr = frexpf(r, &ex);
+    const int e = (fr == 0.5f) ? ex - 1 : ex;
+    return min(127, max(-127, e));
+}
+// v / 2^e as v * 2^-e (exact powers of two, the same rounding): 2^-e is a
+// float for every e in [-127, 127].
+__device__ __forceinline__ float scale_down(float v, int e) { return v * ldexpf(1.0f, -e); }
+
+}  // namespace moe
