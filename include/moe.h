@@ -409,9 +409,10 @@ MOE_API int moe_router_backward(const moe_router_config *cfg, int num_tokens, co
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
 
 #define MOE_FP4_LINEAR_MAX_TOKENS 16
+#define MOE_FP4_LINEAR_MAX_IN 32768
 
 typedef struct {
-    int in_features;   /* K, a multiple of 32 */
+    int in_features;   /* K, a multiple of 32, at most MOE_FP4_LINEAR_MAX_IN */
     int out_features;  /* N rows of the weight; even with MOE_ACT_SWIGLU */
     int act;           /* moe_act; SWIGLU: rows [0, N/2) gate, [N/2, N) up, output silu(gate) * up of N/2 columns */
     int out_dtype;     /* moe_dtype of add and y */
