@@ -2,8 +2,12 @@
 // gate, the residual sum and the expert layer's input quantisation, forward
 // and backward (formulas in include/moe.h).
 //
-// One CTA per row holds the row's sum z in shared memory in f32 between the
-// two norms, so every input is read once and every output written once.
+// Both directions are bound by reading and writing the [T, H] tensors once.  A
+// row lives in the registers of the threads that own its columns, 8 columns
+// (one chunk) to a thread at a time, from the first load to the last store, so
+// every input is read once and every output written once whatever the norms in
+// between need.  Sums over a row are f32: 8 terms a chunk in order, then the
+// warp's tree, then the warps'.
 #include <float.h>
 #include <math.h>
 
@@ -16,175 +20,377 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxParts = 304;   // rows of partial column sums in the backward workspace
+// How a thread's 8 * NV columns lie in the row.
+//   kVec: chunks of 8 columns, 16-byte accesses (every row and parameter 16-byte aligned, H % 8 == 0);
+//   kChunk: the same chunks by element (any alignment; the quantised outputs need chunks);
+//   kStride: columns tid, tid + threads, ... by element: what an odd width or pitch gets, coalesced.
+enum Map { kVec, kChunk, kStride };
+
+template <Map M>
+__device__ __forceinline__ int column(int i, int j, int tr, int threads) {
+    return M == kStride ? (i * 8 + j) * threads + tr : (i * threads + tr) * 8 + j;
+}
+
+// 8 columns of a row as f32 (zero past the row's end).
+template <Map M, class S>
+__device__ __forceinline__ void load8(float (&v)[8], const S *row, int i, int tr, int threads, int H) {
+    if (M == kVec) {
+        const int c = column<M>(i, 0, tr, threads);
+        if (c < H) {
+            Raw8<S> r;
+            r.load(row + c);
+            r.get(v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = column<M>(i, j, tr, threads);
+            v[j] = c < H ? to_f32(row[c]) : 0.0f;
+        }
+    }
+}
+
+template <Map M, class S>
+__device__ __forceinline__ void store8(S *row, const float (&v)[8], int i, int tr, int threads, int H) {
+    if (M == kVec) {
+        const int c = column<M>(i, 0, tr, threads);
+        if (c < H) {
+            Raw8<S> r;
+            r.set(v);
+            r.store(row + c);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = column<M>(i, j, tr, threads);
+            if (c < H) row[c] = from_f32<S>(v[j]);
+        }
+    }
+}
+
+// The same for parameters, whose type is known at run time only (uniform branch).
+template <Map M>
+__device__ __forceinline__ void load_param8(float (&v)[8], const void *w, bool f32, int i, int tr, int threads, int H) {
+    if (f32) load8<M>(v, static_cast<const float *>(w), i, tr, threads, H);
+    else load8<M>(v, static_cast<const bf16 *>(w), i, tr, threads, H);
+}
+__device__ __forceinline__ float load_param(const void *w, bool f32, int64_t i) {
+    return f32 ? static_cast<const float *>(w)[i] : to_f32(static_cast<const bf16 *>(w)[i]);
+}
+
+// Sum over a row's threads in a fixed order: a warp, or the CTA (`red` one float per warp, not in use).
+template <bool kWarpRow>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+    v = warp_sum(v);
+    if (kWarpRow) return v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum(lane < (int)(blockDim.x >> 5) ? red[lane] : 0.0f);
+}
 
 struct NormFwd {
     moe_norm_io io;
-    int T, H, quant;
+    int T, H, quant, gate;
+    bool param_f32;
     float eps, residual_scale;
 };
 
-template <class S, class P, int kGate>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormFwd p) {
-    extern __shared__ float z[];
-    __shared__ float red[2][kWarps];
-    const int H = p.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t t = blockIdx.x;
+// One row per CTA, or with kWarpRow per warp.
+template <class S, int NV, Map M, bool kWarpRow, int kMaxThreads>
+__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const __grid_constant__ NormFwd p) {
+    __shared__ float red[2][32];
+    const int64_t t = kWarpRow ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    if (kWarpRow && t >= p.T) return;
+    const int tr = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
+    const int H = p.H;
+    const float inv_h = 1.0f / (float)H;
     const S *res = static_cast<const S *>(p.io.residual) + t * p.io.ld_residual;
-    const P *w_pre = static_cast<const P *>(p.io.w_pre);
+    float z[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load8<M>(z[i], res, i, tr, threads, H);
     float s2 = 0.0f;
     if (p.io.y) {
         const S *y = static_cast<const S *>(p.io.y) + t * p.io.ld_y;
-        S *h = static_cast<S *>(p.io.h) + t * p.io.ld_h;
-        const P *w_post = static_cast<const P *>(p.io.w_post);
-        const P *gate = static_cast<const P *>(p.io.gate);
+        float u[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) load8<M>(u[i], y, i, tr, threads, H);
         float r1 = 1.0f;
-        if (w_post) {
+        if (p.io.w_post) {
             float s1 = 0.0f;
-            for (int i = tid; i < H; i += kThreads) {
-                const float v = to_f32(y[i]);
-                s1 += v * v;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s1 = fmaf(u[i][j], u[i][j], s1);
+            r1 = 1.0f / sqrtf(fmaf(row_sum<kWarpRow>(s1, red[0]), inv_h, p.eps));
+            if (tr == 0 && p.io.rstd_post) p.io.rstd_post[t] = r1;
+        }
+        if (p.gate == MOE_GATE_TOKEN) r1 *= load_param(p.io.gate, p.param_f32, t);
+        S *h = static_cast<S *>(p.io.h) + t * p.io.ld_h;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[8];
+            if (p.io.w_post) {
+                load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
             }
-            s1 = block_sum<kWarps>(s1, red[0]);
-            r1 = 1.0f / sqrtf(s1 / (float)H + p.eps);
-            if (tid == 0 && p.io.rstd_post) p.io.rstd_post[t] = r1;
-        }
-        const float gt = kGate == MOE_GATE_TOKEN ? to_f32(gate[t]) : 1.0f;
-        for (int i = tid; i < H; i += kThreads) {
-            float u = to_f32(y[i]);
-            if (w_post) u *= r1 * to_f32(w_post[i]);
-            const float g = kGate == MOE_GATE_CHANNEL ? to_f32(gate[i]) : gt;
-            const float v = fmaf(g, u, p.residual_scale * to_f32(res[i]));
-            z[i] = v;
-            h[i] = from_f32<S>(v);
-            s2 += v * v;
-        }
-    } else {
-        for (int i = tid; i < H; i += kThreads) {
-            const float v = to_f32(res[i]);
-            z[i] = v;
-            s2 += v * v;
+            if (p.gate == MOE_GATE_CHANNEL) {
+                load_param8<M>(w, p.io.gate, p.param_f32, i, tr, threads, H);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z[i][j] = fmaf(u[i][j], r1, p.residual_scale * z[i][j]);
+            store8<M>(h, z[i], i, tr, threads, H);
         }
     }
-    if (!w_pre) return;
-    s2 = block_sum<kWarps>(s2, red[1]);   // also orders the writes of z before the reads below
-    const float r2 = 1.0f / sqrtf(s2 / (float)H + p.eps);
-    if (tid == 0 && p.io.rstd_pre) p.io.rstd_pre[t] = r2;
+    if (!p.io.w_pre) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s2 = fmaf(z[i][j], z[i][j], s2);
+    const float r2 = 1.0f / sqrtf(fmaf(row_sum<kWarpRow>(s2, red[1]), inv_h, p.eps));
+    if (tr == 0 && p.io.rstd_pre) p.io.rstd_pre[t] = r2;
     S *n = p.io.n ? static_cast<S *>(p.io.n) + t * p.io.ld_n : nullptr;
-    // a warp takes 128 columns at a time, 32 per step
-    for (int c = warp * 128; c < H; c += kWarps * 128) {
-        float v[4], top = 0.0f, amax[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = c + 32 * j + lane;
-            v[j] = i < H ? z[i] * r2 * to_f32(w_pre[i]) : 0.0f;
-            if (n && i < H) n[i] = from_f32<S>(v[j]);
-            amax[j] = warp_max(fabsf(v[j]));
-            top = fmaxf(top, amax[j]);
-        }
-        if (p.quant == MOE_QUANT_NONE) continue;
-        uint8_t *codes = p.io.codes + t * H;
+    for (int i = 0; i < NV; ++i) {
+        float w[8];
+        load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * r2 * w[j];
+        if (n) store8<M>(n, z[i], i, tr, threads, H);
+        if (M == kStride || p.quant == MOE_QUANT_NONE) continue;
+        // a group is 16 (of 128 columns) or 4 (of 32) neighbouring chunks, all of them in the row or none
+        const int c = column<M>(i, 0, tr, threads);
+        float amax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(z[i][j]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        float q[8];
         if (p.quant == MOE_QUANT_FP8_128) {
-            const Fp8Scale q = fp8_scale(top);
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
+            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
+            const Fp8Scale sc = fp8_scale(amax);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) codes[c + 32 * j + lane] = e4m3x2(q.apply(v[j]), 0.0f) & 0xFF;
-            if (lane == 0) static_cast<float *>(p.io.sf)[t * (H / 128) + c / 128] = q.sf;
+            for (int j = 0; j < 8; ++j) q[j] = sc.apply(z[i][j]);
+            if (c < H && (tr & 15) == 0) static_cast<float *>(p.io.sf)[t * (H / 128) + c / 128] = sc.sf;
         } else {
+            const int e = ue8m0_exponent(amax);
+            const float down = pow2(-e);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (c + 32 * j >= H) break;
-                const int e = ue8m0_exponent(amax[j]);
-                codes[c + 32 * j + lane] = e4m3x2(scale_down(v[j], e), 0.0f) & 0xFF;
-                if (lane == 0) static_cast<uint8_t *>(p.io.sf)[t * (H / 32) + c / 32 + j] = (uint8_t)(e + 127);
-            }
+            for (int j = 0; j < 8; ++j) q[j] = z[i][j] * down;
+            if (c < H && (tr & 3) == 0) static_cast<uint8_t *>(p.io.sf)[t * (H / 32) + c / 32] = (uint8_t)(e + 127);
         }
+        if (c < H)
+            *reinterpret_cast<uint2 *>(p.io.codes + t * H + c) =
+                make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
     }
 }
 
 struct NormBwd {
     moe_norm_grad_io io;
-    float *part;   // [parts][3][H]: dw_post, dgate (channel), dw_pre
-    int T, H;
+    float *part;   // [CTAs][3][H]: dw_post, dgate (channel), dw_pre
+    int T, H, gate;
+    bool param_f32;
     float residual_scale;
 };
 
-template <class S, class P, int kGate>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwd p) {
-    extern __shared__ float D[];
-    __shared__ float red[3][kWarps];
-    const int H = p.H, tid = threadIdx.x;
-    float *a_post = p.part + (int64_t)blockIdx.x * 3 * H, *a_gate = a_post + H, *a_pre = a_post + 2 * H;
-    for (int i = tid; i < H; i += kThreads) a_post[i] = a_gate[i] = a_pre[i] = 0.0f;
-    const P *w_post = static_cast<const P *>(p.io.w_post);
-    const P *w_pre = static_cast<const P *>(p.io.w_pre);
-    const P *gate = static_cast<const P *>(p.io.gate);
+// A row of the stream tensors as loaded, so that the next row can be on its way while this one is worked on.
+template <class S, int NV, Map M>
+struct Row {
+    Raw8<S> v[NV];
+    __device__ __forceinline__ void load(const void *base, int64_t ld, int64_t t, int tr, int threads, int H) {
+        if (!base) return;
+        const S *row = static_cast<const S *>(base) + t * ld;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (M == kVec) {
+                const int c = column<M>(i, 0, tr, threads);
+                if (c < H) v[i].load(row + c);
+                else v[i].zero();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int c = column<M>(i, j, tr, threads);
+                    v[i].put(j, c < H ? row[c] : from_f32<S>(0.0f));
+                }
+            }
+        }
+    }
+};
+
+// CTA b takes rows b, b + CTAs, ...; every thread keeps its columns throughout, so the sums over tokens stay with it
+// until the end: in registers, next to the prefetched next row, or for rows of over 8192 columns (kWide) in shared
+// memory with each tensor loaded where it is used.
+template <class S, int NV, Map M, bool kWide, int kMaxThreads, int kMinCtas>
+__global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const __grid_constant__ NormBwd p) {
+    extern __shared__ float wide_acc[];   // kWide: [3][NV][8][threads]
+    __shared__ float red[2][2][32], red2[2][32];
+    const int tr = threadIdx.x, threads = blockDim.x, H = p.H;
     const float inv_h = 1.0f / (float)H;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {   // every thread keeps its own columns throughout
-        const S *h = static_cast<const S *>(p.io.h) + t * p.io.ld_h;
-        const S *dh = p.io.dh ? static_cast<const S *>(p.io.dh) + t * p.io.ld_dh : nullptr;
-        const S *dn = p.io.dn ? static_cast<const S *>(p.io.dn) + t * p.io.ld_dn : nullptr;
-        const S *y = p.io.y ? static_cast<const S *>(p.io.y) + t * p.io.ld_y : nullptr;
-        S *dres = static_cast<S *>(p.io.dresidual) + t * p.io.ld_dresidual;
+    const bool pre = p.io.dn != nullptr, block = p.io.y != nullptr, post = p.io.w_post != nullptr;
+    const bool channel = p.gate == MOE_GATE_CHANNEL;
+    float acc[kWide ? 1 : 3][NV][8];
+    auto sum_at = [&](int which, int i, int j) -> float & {   // 0: dw_post, 1: dgate, 2: dw_pre
+        if (kWide) return wide_acc[((which * NV + i) * 8 + j) * threads + tr];
+        return acc[kWide ? 0 : which][i][j];
+    };
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum_at(k, i, j) = 0.0f;
+    Row<S, NV, M> h, y, dh, dn;
+    auto fetch_h = [&](int64_t t) { if (pre) h.load(p.io.h, p.io.ld_h, t, tr, threads, H); };
+    auto fetch_dn = [&](int64_t t) { dn.load(p.io.dn, p.io.ld_dn, t, tr, threads, H); };
+    auto fetch_dh = [&](int64_t t) { dh.load(p.io.dh, p.io.ld_dh, t, tr, threads, H); };
+    auto fetch_y = [&](int64_t t) { y.load(p.io.y, p.io.ld_y, t, tr, threads, H); };
+    auto fetch = [&](int64_t t) {
+        if (kWide || t >= p.T) return;
+        fetch_h(t), fetch_dn(t), fetch_dh(t), fetch_y(t);
+    };
+    fetch(blockIdx.x);
+    int turn = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
+        float D[NV][8], u[NV][8];
         float r2 = 0.0f, m2 = 0.0f;
-        if (dn) {
+        if (pre) {
             r2 = p.io.rstd_pre[t];
-            for (int i = tid; i < H; i += kThreads) m2 += to_f32(dn[i]) * to_f32(w_pre[i]) * (to_f32(h[i]) * r2);
-            m2 = block_sum<kWarps>(m2, red[0]) * inv_h;
+            if (kWide) fetch_h(t), fetch_dn(t);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float w[8], hv[8];
+                dn.v[i].get(D[i]);
+                h.v[i].get(hv);
+                load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    hv[j] *= r2;
+                    sum_at(2, i, j) = fmaf(D[i][j], hv[j], sum_at(2, i, j));
+                    D[i][j] *= w[j];
+                    m2 = fmaf(D[i][j], hv[j], m2);
+                }
+            }
+            m2 = row_sum<false>(m2, red[0][turn]) * inv_h;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float hv[8];
+                h.v[i].get(hv);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) D[i][j] = r2 * (D[i][j] - hv[j] * r2 * m2);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) D[i][j] = 0.0f;
         }
-        const float r1 = w_post ? p.io.rstd_post[t] : 1.0f;
-        const float gt = kGate == MOE_GATE_TOKEN ? to_f32(gate[t]) : 1.0f;
+        if (p.io.dh) {
+            if (kWide) fetch_dh(t);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float v[8];
+                dh.v[i].get(v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) D[i][j] += v[j];
+            }
+        }
+        if (block) {
+            if (kWide) fetch_y(t);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) y.v[i].get(u[i]);
+        }
+        fetch(t + gridDim.x);
+        const float rs = block ? p.residual_scale : 1.0f;
+        S *dres = static_cast<S *>(p.io.dresidual) + t * p.io.ld_dresidual;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = rs * D[i][j];
+            store8<M>(dres, v, i, tr, threads, H);
+        }
+        if (!block) continue;
+        // D becomes b = D gate w_post, u becomes yh (without a post norm: D gate, y)
+        const float r1 = post ? p.io.rstd_post[t] : 1.0f;
+        const float gt = p.gate == MOE_GATE_TOKEN ? load_param(p.io.gate, p.param_f32, t) : 1.0f;
         float m1 = 0.0f, sg = 0.0f;
-        for (int i = tid; i < H; i += kThreads) {
-            float d = dh ? to_f32(dh[i]) : 0.0f;
-            if (dn) {
-                const float hat = to_f32(h[i]) * r2, g = to_f32(dn[i]);
-                a_pre[i] += g * hat;
-                d += r2 * (g * to_f32(w_pre[i]) - hat * m2);
-            }
-            D[i] = d;
-            if (!y) continue;
-            const float hat = to_f32(y[i]) * r1, w = w_post ? to_f32(w_post[i]) : 1.0f;
-            const float gi = kGate == MOE_GATE_CHANNEL ? to_f32(gate[i]) : gt;
-            const float du = d * hat * w;
-            if (kGate == MOE_GATE_CHANNEL) a_gate[i] += du;
-            sg += du;
-            if (w_post) {
-                a_post[i] += d * gi * hat;
-                m1 += d * gi * w * hat;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[8], g[8];
+            if (post) load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
+            if (channel) load_param8<M>(g, p.io.gate, p.param_f32, i, tr, threads, H);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                u[i][j] *= r1;
+                const float wj = post ? w[j] : 1.0f, gj = channel ? g[j] : gt;
+                const float du = D[i][j] * u[i][j];
+                if (post) sum_at(0, i, j) = fmaf(du, gj, sum_at(0, i, j));
+                if (channel) sum_at(1, i, j) = fmaf(du, wj, sum_at(1, i, j));
+                sg = fmaf(du, wj, sg);
+                D[i][j] *= gj * wj;
+                m1 = fmaf(D[i][j], u[i][j], m1);
             }
         }
-        if (w_post) m1 = block_sum<kWarps>(m1, red[1]) * inv_h;
-        if (kGate == MOE_GATE_TOKEN) {
-            sg = block_sum<kWarps>(sg, red[2]);
-            if (tid == 0) p.io.dgate[t] = sg;
-        }
-        for (int i = tid; i < H; i += kThreads) {
-            const float d = D[i];
-            dres[i] = from_f32<S>(y ? p.residual_scale * d : d);
-            if (!y) continue;
-            const float gi = kGate == MOE_GATE_CHANNEL ? to_f32(gate[i]) : gt;
-            float out = d * gi;
-            if (w_post) {
-                const float hat = to_f32(y[i]) * r1;
-                out = r1 * (out * to_f32(w_post[i]) - hat * m1);
+        if (post || p.gate == MOE_GATE_TOKEN) {
+            // both sums behind one barrier
+            m1 = warp_sum(m1);
+            sg = warp_sum(sg);
+            float *m = red[1][turn], *gs = red2[turn];
+            const int lane = tr & 31;
+            if (lane == 0) m[tr >> 5] = m1, gs[tr >> 5] = sg;
+            __syncthreads();
+            m1 = warp_sum(lane < (threads >> 5) ? m[lane] : 0.0f) * inv_h;
+            if (p.gate == MOE_GATE_TOKEN && tr < 32) {
+                sg = warp_sum(lane < (threads >> 5) ? gs[lane] : 0.0f);
+                if (tr == 0) p.io.dgate[t] = sg;
             }
-            static_cast<S *>(p.io.dy)[t * p.io.ld_dy + i] = from_f32<S>(out);
         }
-        __syncthreads();   // the next row writes `red` again
+        S *dy = static_cast<S *>(p.io.dy) + t * p.io.ld_dy;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (post) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) D[i][j] = r1 * (D[i][j] - u[i][j] * m1);
+            }
+            store8<M>(dy, D[i], i, tr, threads, H);
+        }
+    }
+    float *part = p.part + (int64_t)blockIdx.x * 3 * H;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        if (!(k == 0 ? post : k == 1 ? channel : pre)) continue;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = sum_at(k, i, j);
+            store8<M>(part + k * H, v, i, tr, threads, H);   // kVec: H % 8 == 0, so these rows are 16-byte aligned too
+        }
     }
 }
 
-// Column sums of the partials in row order (the same bits every time).
-__global__ void __launch_bounds__(kThreads) norm_bwd_sum_kernel(const float *part, int parts, int H, float *dw_post,
-                                                                float *dgate, float *dw_pre) {
-    const int i = blockIdx.x * kThreads + threadIdx.x;
+// Column sums of the partials, always in the same order: a thread takes every 32nd row, then the 32 are added in turn.
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *part, int parts, int H, float *dw_post, float *dgate,
+                                                            float *dw_pre) {
+    __shared__ float sum[32][33];
+    const int lane = threadIdx.x & 31, r0 = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
     float *out = blockIdx.y == 0 ? dw_post : blockIdx.y == 1 ? dgate : dw_pre;
-    if (!out || i >= H) return;
+    if (!out) return;
     float s = 0.0f;
-    for (int r = 0; r < parts; ++r) s += part[((int64_t)r * 3 + blockIdx.y) * H + i];
-    out[i] = s;
+    if (col < H)
+#pragma unroll 4
+        for (int r = r0; r < parts; r += 32) s += part[((int64_t)r * 3 + blockIdx.y) * H + col];
+    sum[r0][lane] = s;
+    __syncthreads();
+    s = warp_sum(sum[lane][r0]);   // column r0 of the block, the 32 partial rows across the lanes
+    if (lane == 0 && blockIdx.x * 32 + r0 < H) out[blockIdx.x * 32 + r0] = s;
 }
 
 bool valid(const moe_norm_config *c) {
@@ -197,46 +403,77 @@ bool valid(const moe_norm_config *c) {
     return c->eps > 0.0f && isfinite(c->eps) && isfinite(c->residual_scale);
 }
 
-// `f` is called with the stream's and the parameters' element types and the gate kind.
-template <int kGate, class F>
-cudaError_t by_types(const moe_norm_config *c, F f) {
-    const bool s32 = c->stream_dtype == MOE_DTYPE_F32, p32 = c->param_dtype == MOE_DTYPE_F32;
-    if (s32) return p32 ? f.template run<float, float, kGate>() : f.template run<float, bf16, kGate>();
-    return p32 ? f.template run<bf16, float, kGate>() : f.template run<bf16, bf16, kGate>();
-}
-template <class F>
-cudaError_t by_config(const moe_norm_config *c, F f) {
-    if (c->gate == MOE_GATE_CHANNEL) return by_types<MOE_GATE_CHANNEL>(c, f);
-    if (c->gate == MOE_GATE_TOKEN) return by_types<MOE_GATE_TOKEN>(c, f);
-    return by_types<MOE_GATE_NONE>(c, f);
+bool rows16(const void *p, int64_t ld, size_t es) { return !p || (aligned_to(p, 16) && ld * es % 16 == 0); }
+
+template <class S, int NV, Map M, bool kWarpRow, int kMaxThreads>
+cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
+    const int per_thread = 8 * NV * 32;   // columns of a warp
+    const int threads = kWarpRow ? 128 : (p.H + per_thread - 1) / per_thread * 32;
+    norm_fwd_kernel<S, NV, M, kWarpRow, kMaxThreads><<<kWarpRow ? (p.T + 3) / 4 : p.T, threads, 0, s>>>(p);
+    return cudaGetLastError();
 }
 
-struct RunFwd {
-    const NormFwd &p;
-    cudaStream_t s;
-    template <class S, class P, int kGate>
-    cudaError_t run() const {
-        static std::atomic<uint32_t> done{0};
-        const cudaError_t e = smem_limit_once((const void *)norm_fwd_kernel<S, P, kGate>, 4 * MOE_NORM_MAX_HIDDEN, done);
-        if (e != cudaSuccess) return e;
-        norm_fwd_kernel<S, P, kGate><<<p.T, kThreads, 4 * p.H, s>>>(p);
-        return cudaGetLastError();
-    }
-};
+template <class S, Map M>
+cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
+    // up to 1024 columns a warp holds the row and no barrier is needed
+    if (p.H <= 256) return launch_fwd<S, 1, M, true, 128>(p, s);
+    if (p.H <= 512) return launch_fwd<S, 2, M, true, 128>(p, s);
+    if (p.H <= 1024) return launch_fwd<S, 4, M, true, 128>(p, s);
+    // up to two rows an SM: as many threads a row as it has chunks, for latency; more: fewer and longer threads
+    if (p.H <= 8192) return p.T <= 304 ? launch_fwd<S, 1, M, false, 1024>(p, s) : launch_fwd<S, 2, M, false, 512>(p, s);
+    return launch_fwd<S, 2, M, false, 1024>(p, s);
+}
 
-struct RunBwd {
-    const NormBwd &p;
-    int parts;
-    cudaStream_t s;
-    template <class S, class P, int kGate>
-    cudaError_t run() const {
+template <class S>
+cudaError_t launch_fwd_any(const NormFwd &p, cudaStream_t s) {
+    const moe_norm_io &io = p.io;
+    const size_t es = sizeof(S);
+    const bool vec = p.H % 8 == 0 && rows16(io.residual, io.ld_residual, es) && rows16(io.y, io.ld_y, es) &&
+                     rows16(io.h, io.ld_h, es) && rows16(io.n, io.ld_n, es) && aligned_to(io.w_post, 16) &&
+                     aligned_to(io.w_pre, 16) && (p.gate != MOE_GATE_CHANNEL || aligned_to(io.gate, 16));
+    if (vec) return launch_fwd<S, kVec>(p, s);
+    return p.quant != MOE_QUANT_NONE ? launch_fwd<S, kChunk>(p, s) : launch_fwd<S, kStride>(p, s);
+}
+
+template <class S, int NV, Map M, bool kWide, int kMaxThreads, int kMinCtas>
+cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
+    const int per_thread = 8 * NV * 32;
+    const int threads = (p.H + per_thread - 1) / per_thread * 32;
+    size_t smem = 0;
+    if (kWide) {
+        smem = (size_t)3 * NV * 8 * threads * 4;
         static std::atomic<uint32_t> done{0};
-        const cudaError_t e = smem_limit_once((const void *)norm_bwd_kernel<S, P, kGate>, 4 * MOE_NORM_MAX_HIDDEN, done);
+        const cudaError_t e = smem_limit_once((const void *)norm_bwd_kernel<S, NV, M, kWide, kMaxThreads, kMinCtas>,
+                                              3 * MOE_NORM_MAX_HIDDEN * 4, done);
         if (e != cudaSuccess) return e;
-        norm_bwd_kernel<S, P, kGate><<<parts, kThreads, 4 * p.H, s>>>(p);
-        return cudaGetLastError();
     }
-};
+    norm_bwd_kernel<S, NV, M, kWide, kMaxThreads, kMinCtas><<<parts, threads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <class S, Map M>
+cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
+    if (p.H <= 2048) return launch_bwd<S, 1, M, false, 256, 2>(p, parts, s);
+    if (p.H <= 8192) return launch_bwd<S, 2, M, false, 512, 1>(p, parts, s);
+    return launch_bwd<S, 2, M, true, 1024, 1>(p, parts, s);
+}
+
+// CTAs of the backward pass: as many as an SM holds (registers: 65536 / (threads x 128)), or the rows.
+int bwd_parts(int H, int T) {
+    const int per_sm = H <= 1024 ? 4 : H <= 2048 ? 2 : 1;
+    return std::max(1, std::min(T, 152 * per_sm));
+}
+
+template <class S>
+cudaError_t launch_bwd_any(const NormBwd &p, int parts, cudaStream_t s) {
+    const moe_norm_grad_io &io = p.io;
+    const size_t es = sizeof(S);
+    const bool vec = p.H % 8 == 0 && rows16(io.h, io.ld_h, es) && rows16(io.y, io.ld_y, es) && rows16(io.dh, io.ld_dh, es) &&
+                     rows16(io.dn, io.ld_dn, es) && rows16(io.dresidual, io.ld_dresidual, es) && rows16(io.dy, io.ld_dy, es) &&
+                     aligned_to(io.w_post, 16) && aligned_to(io.w_pre, 16) &&
+                     (p.gate != MOE_GATE_CHANNEL || aligned_to(io.gate, 16));
+    return vec ? launch_bwd<S, kVec>(p, parts, s) : launch_bwd<S, kStride>(p, parts, s);
+}
 
 bool ld_ok(const void *p, int64_t ld, int H) { return !p || ld >= H; }
 
@@ -270,15 +507,16 @@ int moe_norm_forward(const moe_norm_config *cfg, int num_tokens, const moe_norm_
         !aligned_to(io->rstd_post, 4) || !aligned_to(io->rstd_pre, 4) || !aligned_to(io->codes, 16) ||
         !aligned_to(io->sf, 4))
         return MOE_ERR_INVALID_ARG;
-    NormFwd p{*io, num_tokens, H, io->w_pre ? cfg->quant : (int)MOE_QUANT_NONE, cfg->eps, cfg->residual_scale};
-    moe_norm_config c = *cfg;
-    if (!io->y) c.gate = MOE_GATE_NONE;
-    return by_config(&c, RunFwd{p, static_cast<cudaStream_t>(stream)}) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    NormFwd p{*io, num_tokens, H, io->w_pre ? cfg->quant : (int)MOE_QUANT_NONE, io->y ? cfg->gate : (int)MOE_GATE_NONE,
+              cfg->param_dtype == MOE_DTYPE_F32, cfg->eps, cfg->residual_scale};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_fwd_any<float>(p, s) : launch_fwd_any<bf16>(p, s);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 size_t moe_norm_workspace_bytes(const moe_norm_config *cfg, int num_tokens) {
     if (!valid(cfg) || num_tokens < 0) return 0;
-    const size_t b = (size_t)std::max(1, std::min(num_tokens, kMaxParts)) * 3 * cfg->hidden * 4;
+    const size_t b = (size_t)bwd_parts(cfg->hidden, num_tokens) * 3 * cfg->hidden * 4;
     return (b + 255) / 256 * 256;
 }
 
@@ -318,14 +556,14 @@ int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const moe_norm
     const bool channel = io->gate && cfg->gate == MOE_GATE_CHANNEL;
     const bool sums = io->dw_post || io->dw_pre || channel;
     if (!d_workspace) return MOE_ERR_INVALID_ARG;
-    const int parts = std::min(num_tokens, kMaxParts);
-    NormBwd p{*io, static_cast<float *>(d_workspace), num_tokens, H, cfg->residual_scale};
-    moe_norm_config c = *cfg;
-    if (!io->y) c.gate = MOE_GATE_NONE;
-    if (by_config(&c, RunBwd{p, parts, s}) != cudaSuccess) return MOE_ERR_CUDA;
+    const int parts = bwd_parts(H, num_tokens);
+    NormBwd p{*io, static_cast<float *>(d_workspace), num_tokens, H, io->y ? cfg->gate : (int)MOE_GATE_NONE,
+              cfg->param_dtype == MOE_DTYPE_F32, cfg->residual_scale};
+    const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_bwd_any<float>(p, parts, s) : launch_bwd_any<bf16>(p, parts, s);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (sums) {
-        norm_bwd_sum_kernel<<<dim3((H + kThreads - 1) / kThreads, 3), kThreads, 0, s>>>(
-            p.part, parts, H, io->dw_post, channel ? io->dgate : nullptr, io->dw_pre);
+        norm_bwd_sum_kernel<<<dim3((H + 31) / 32, 3), 1024, 0, s>>>(p.part, parts, H, io->dw_post,
+                                                                    channel ? io->dgate : nullptr, io->dw_pre);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;

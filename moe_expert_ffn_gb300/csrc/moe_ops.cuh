@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "moe.h"
+#include "moe_device.cuh"
 #include "moe_internal.h"
 
 namespace moe {
@@ -25,6 +26,58 @@ template <>
 __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat16_rn(v); }
+
+// Eight neighbouring elements as they are in memory (16-byte aligned).
+template <class S>
+struct Raw8;
+template <>
+struct Raw8<bf16> {
+    uint4 r;
+    __device__ __forceinline__ void load(const bf16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = r; }
+    __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+        r = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+    }
+    __device__ __forceinline__ void put(int j, bf16 e) {   // j known at compile time
+        uint32_t &w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
+        const uint32_t b = __bfloat16_as_ushort(e);
+        w = (j & 1) ? (w & 0xFFFFu) | b << 16 : b;
+    }
+};
+template <>
+struct Raw8<float> {
+    float f[8];
+    __device__ __forceinline__ void load(const float *p) {
+        const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+    __device__ __forceinline__ void store(float *p) const {
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+        *(reinterpret_cast<float4 *>(p) + 1) = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = f[j];
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = v[j];
+    }
+    __device__ __forceinline__ void put(int j, float e) { f[j] = e; }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -76,8 +129,7 @@ __device__ __forceinline__ int ue8m0_exponent(float amax) {
     const int e = (fr == 0.5f) ? ex - 1 : ex;
     return min(127, max(-127, e));
 }
-// v / 2^e as v * 2^-e (exact powers of two, the same rounding): 2^-e is a
-// float for every e in [-127, 127].
-__device__ __forceinline__ float scale_down(float v, int e) { return v * ldexpf(1.0f, -e); }
+// 2^e, e in [-127, 127] (2^-127 is a subnormal float).
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(e > -127 ? (uint32_t)(e + 127) << 23 : 0x00400000u); }
 
 }  // namespace moe
