@@ -99,107 +99,6 @@ struct NormFwd {
     float eps, residual_scale;
 };
 
-// One row per CTA, or with kWarpRow per warp.
-template <class S, int NV, Map M, bool kWarpRow, int kMaxThreads>
-__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const __grid_constant__ NormFwd p) {
-    __shared__ float red[2][32];
-    const int64_t t = kWarpRow ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
-    if (kWarpRow && t >= p.T) return;
-    const int tr = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
-    const int H = p.H;
-    const float inv_h = 1.0f / (float)H;
-    const S *res = static_cast<const S *>(p.io.residual) + t * p.io.ld_residual;
-    float z[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) load8<M>(z[i], res, i, tr, threads, H);
-    float s2 = 0.0f;
-    if (p.io.y) {
-        const S *y = static_cast<const S *>(p.io.y) + t * p.io.ld_y;
-        float u[NV][8];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) load8<M>(u[i], y, i, tr, threads, H);
-        float r1 = 1.0f;
-        if (p.io.w_post) {
-            float s1 = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s1 = fmaf(u[i][j], u[i][j], s1);
-            r1 = 1.0f / sqrtf(fmaf(row_sum<kWarpRow>(s1, red[0]), inv_h, p.eps));
-            if (tr == 0 && p.io.rstd_post) p.io.rstd_post[t] = r1;
-        }
-        if (p.gate == MOE_GATE_TOKEN) r1 *= load_param(p.io.gate, p.param_f32, t);
-        S *h = static_cast<S *>(p.io.h) + t * p.io.ld_h;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            float w[8];
-            if (p.io.w_post) {
-                load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
-            }
-            if (p.gate == MOE_GATE_CHANNEL) {
-                load_param8<M>(w, p.io.gate, p.param_f32, i, tr, threads, H);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) z[i][j] = fmaf(u[i][j], r1, p.residual_scale * z[i][j]);
-            store8<M>(h, z[i], i, tr, threads, H);
-        }
-    }
-    if (!p.io.w_pre) return;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s2 = fmaf(z[i][j], z[i][j], s2);
-    const float r2 = 1.0f / sqrtf(fmaf(row_sum<kWarpRow>(s2, red[1]), inv_h, p.eps));
-    if (tr == 0 && p.io.rstd_pre) p.io.rstd_pre[t] = r2;
-    S *n = p.io.n ? static_cast<S *>(p.io.n) + t * p.io.ld_n : nullptr;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float w[8];
-        load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * r2 * w[j];
-        if (n) store8<M>(n, z[i], i, tr, threads, H);
-        if (M == kStride || p.quant == MOE_QUANT_NONE) continue;
-        // a group is 16 (of 128 columns) or 4 (of 32) neighbouring chunks, all of them in the row or none
-        const int c = column<M>(i, 0, tr, threads);
-        float amax = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(z[i][j]));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-        float q[8];
-        if (p.quant == MOE_QUANT_FP8_128) {
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
-            const Fp8Scale sc = fp8_scale(amax);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = sc.apply(z[i][j]);
-            if (c < H && (tr & 15) == 0) static_cast<float *>(p.io.sf)[t * (H / 128) + c / 128] = sc.sf;
-        } else {
-            const int e = ue8m0_exponent(amax);
-            const float down = pow2(-e);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) q[j] = z[i][j] * down;
-            if (c < H && (tr & 3) == 0) static_cast<uint8_t *>(p.io.sf)[t * (H / 32) + c / 32] = (uint8_t)(e + 127);
-        }
-        if (c < H)
-            *reinterpret_cast<uint2 *>(p.io.codes + t * H + c) =
-                make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
-    }
-}
-
-struct NormBwd {
-    moe_norm_grad_io io;
-    float *part;   // [CTAs][3][H]: dw_post, dgate (channel), dw_pre
-    int T, H, gate;
-    bool param_f32;
-    float residual_scale;
-};
-
 // A row of the stream tensors as loaded, so that the next row can be on its way while this one is worked on.
 template <class S, int NV, Map M>
 struct Row {
@@ -211,7 +110,7 @@ struct Row {
         for (int i = 0; i < NV; ++i) {
             if (M == kVec) {
                 const int c = column<M>(i, 0, tr, threads);
-                if (c < H) v[i].load(row + c);
+                if (c < H) v[i].load_once(row + c);
                 else v[i].zero();
             } else {
 #pragma unroll
@@ -222,6 +121,121 @@ struct Row {
             }
         }
     }
+};
+
+// Codes and scale of a thread's chunk at column c.  A group is 16 (of 128 columns) or 4 (of 32) neighbouring chunks,
+// all of them in the row or none; every lane of the warp calls.
+__device__ __forceinline__ void quantise8(const NormFwd &p, const float (&v)[8], int64_t t, int c, int tr) {
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+    float q[8];
+    if (p.quant == MOE_QUANT_FP8_128) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
+        const Fp8Scale sc = fp8_scale(amax);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = sc.apply(v[j]);
+        if (c < p.H && (tr & 15) == 0) static_cast<float *>(p.io.sf)[t * (p.H / 128) + c / 128] = sc.sf;
+    } else {
+        const int e = ue8m0_exponent(amax);
+        const float down = pow2(-e);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = v[j] * down;
+        if (c < p.H && (tr & 3) == 0) static_cast<uint8_t *>(p.io.sf)[t * (p.H / 32) + c / 32] = (uint8_t)(e + 127);
+    }
+    if (c < p.H)
+        *reinterpret_cast<uint2 *>(p.io.codes + t * p.H + c) =
+            make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
+}
+
+// A warp takes one row (kWarpRow), or a CTA rows b, b + CTAs, ..., with the next row on its way from the moment this
+// one is unpacked.
+template <class S, int NV, Map M, bool kWarpRow, int kMaxThreads, int kMinCtas>
+__global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const __grid_constant__ NormFwd p) {
+    __shared__ float red[2][2][32];
+    const int tr = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
+    const int H = p.H;
+    const float inv_h = 1.0f / (float)H;
+    int64_t t = kWarpRow ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
+    Row<S, NV, M> res, y;
+    auto fetch = [&](int64_t t) {
+        if (t >= p.T) return;
+        y.load(p.io.y, p.io.ld_y, t, tr, threads, H);
+        res.load(p.io.residual, p.io.ld_residual, t, tr, threads, H);
+    };
+    fetch(t);
+    int turn = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
+    for (; t < p.T; t += gridDim.x, turn ^= 1) {
+        float z[NV][8], u[NV][8];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            res.v[i].get(z[i]);
+            if (p.io.y) y.v[i].get(u[i]);
+        }
+        if (!kWarpRow) fetch(t + gridDim.x);
+        if (p.io.y) {
+            float r1 = 1.0f;
+            if (p.io.w_post) {
+                float s1 = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s1 = fmaf(u[i][j], u[i][j], s1);
+                r1 = 1.0f / sqrtf(fmaf(row_sum<kWarpRow>(s1, red[0][turn]), inv_h, p.eps));
+                if (tr == 0 && p.io.rstd_post) p.io.rstd_post[t] = r1;
+            }
+            if (p.gate == MOE_GATE_TOKEN) r1 *= load_param(p.io.gate, p.param_f32, t);
+            S *h = static_cast<S *>(p.io.h) + t * p.io.ld_h;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float w[8];
+                if (p.io.w_post) {
+                    load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
+                }
+                if (p.gate == MOE_GATE_CHANNEL) {
+                    load_param8<M>(w, p.io.gate, p.param_f32, i, tr, threads, H);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[i][j] = fmaf(u[i][j], r1, p.residual_scale * z[i][j]);
+                store8<M>(h, z[i], i, tr, threads, H);
+            }
+        }
+        if (p.io.w_pre) {
+            float s2 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s2 = fmaf(z[i][j], z[i][j], s2);
+            const float r2 = 1.0f / sqrtf(fmaf(row_sum<kWarpRow>(s2, red[1][turn]), inv_h, p.eps));
+            if (tr == 0 && p.io.rstd_pre) p.io.rstd_pre[t] = r2;
+            S *n = p.io.n ? static_cast<S *>(p.io.n) + t * p.io.ld_n : nullptr;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float w[8];
+                load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * r2 * w[j];
+                if (n) store8<M>(n, z[i], i, tr, threads, H);
+                if (M != kStride && p.quant != MOE_QUANT_NONE) quantise8(p, z[i], t, column<M>(i, 0, tr, threads), tr);
+            }
+        }
+        if (kWarpRow) break;
+    }
+}
+
+struct NormBwd {
+    moe_norm_grad_io io;
+    float *part;   // [CTAs][3][H]: dw_post, dgate (channel), dw_pre
+    int T, H, gate;
+    bool param_f32;
+    float residual_scale;
 };
 
 // CTA b takes rows b, b + CTAs, ...; every thread keeps its columns throughout, so the sums over tokens stay with it
@@ -405,23 +419,24 @@ bool valid(const moe_norm_config *c) {
 
 bool rows16(const void *p, int64_t ld, size_t es) { return !p || (aligned_to(p, 16) && ld * es % 16 == 0); }
 
-template <class S, int NV, Map M, bool kWarpRow, int kMaxThreads>
+template <class S, int NV, Map M, bool kWarpRow, int kMaxThreads, int kMinCtas>
 cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
     const int per_thread = 8 * NV * 32;   // columns of a warp
     const int threads = kWarpRow ? 128 : (p.H + per_thread - 1) / per_thread * 32;
-    norm_fwd_kernel<S, NV, M, kWarpRow, kMaxThreads><<<kWarpRow ? (p.T + 3) / 4 : p.T, threads, 0, s>>>(p);
+    const int ctas = kWarpRow ? (p.T + 3) / 4 : std::min(p.T, 152 * (1024 / threads > kMinCtas ? 1024 / threads : kMinCtas));
+    norm_fwd_kernel<S, NV, M, kWarpRow, kMaxThreads, kMinCtas><<<ctas, threads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
 template <class S, Map M>
 cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
     // up to 1024 columns a warp holds the row and no barrier is needed
-    if (p.H <= 256) return launch_fwd<S, 1, M, true, 128>(p, s);
-    if (p.H <= 512) return launch_fwd<S, 2, M, true, 128>(p, s);
-    if (p.H <= 1024) return launch_fwd<S, 4, M, true, 128>(p, s);
+    if (p.H <= 256) return launch_fwd<S, 1, M, true, 128, 1>(p, s);
+    if (p.H <= 512) return launch_fwd<S, 2, M, true, 128, 1>(p, s);
+    if (p.H <= 1024) return launch_fwd<S, 4, M, true, 128, 1>(p, s);
     // up to two rows an SM: as many threads a row as it has chunks, for latency; more: fewer and longer threads
-    if (p.H <= 8192) return p.T <= 304 ? launch_fwd<S, 1, M, false, 1024>(p, s) : launch_fwd<S, 2, M, false, 512>(p, s);
-    return launch_fwd<S, 2, M, false, 1024>(p, s);
+    if (p.H <= 8192) return p.T <= 304 ? launch_fwd<S, 1, M, false, 1024, 1>(p, s) : launch_fwd<S, 2, M, false, 512, 2>(p, s);
+    return launch_fwd<S, 2, M, false, 1024, 1>(p, s);
 }
 
 template <class S>

@@ -27,6 +27,16 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ bf16 from_f32<bf16>(float v) { return __float2bfloat16_rn(v); }
 
+// 16 bytes read once, kept out of L1 (which the parameters of every row stay in).
+__device__ __forceinline__ uint4 ld_stream16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // Eight neighbouring elements as they are in memory (16-byte aligned).
 template <class S>
 struct Raw8;
@@ -34,6 +44,7 @@ template <>
 struct Raw8<bf16> {
     uint4 r;
     __device__ __forceinline__ void load(const bf16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void load_once(const bf16 *p) { r = ld_stream16(p); }
     __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = r; }
     __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -59,6 +70,11 @@ struct Raw8<float> {
     __device__ __forceinline__ void load(const float *p) {
         const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+    __device__ __forceinline__ void load_once(const float *p) {
+        const uint4 a = ld_stream16(p), b = ld_stream16(p + 4);
+        f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
+        f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
     }
     __device__ __forceinline__ void store(float *p) const {
         *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
