@@ -8,8 +8,8 @@
 // every input is read once and every output written once whatever the norms in
 // between need.  Sums over a row are f32: 8 terms a chunk in order, then the
 // warp's tree, then the warps'.
-#include <float.h>
 #include <math.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
@@ -232,73 +232,95 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
 
 struct NormBwd {
     moe_norm_grad_io io;
-    float *part;   // [CTAs][3][H]: dw_post, dgate (channel), dw_pre
+    float *part;   // [CTAs][2][H]
     int T, H, gate;
     bool param_f32;
     float residual_scale;
 };
 
+// With t = dn h, S2 = sum t w_pre, du = D yh and S1 = sum du gate w_post (a token's gate g left out of the sum):
+//   D  = dh + r2 dn w_pre - h r2^3 S2 / H
+//   dy = g r1 (D gate w_post - yh S1 / H)
+// and only two sums over tokens are kept per column: P = sum r2 t is dw_pre, and A = sum g du gives dw_post (times a
+// channel gate) and a channel's dgate (times w_post, g = 1) after the last row.
+//
 // CTA b takes rows b, b + CTAs, ...; every thread keeps its columns throughout, so the sums over tokens stay with it
 // until the end: in registers, next to the prefetched next row, or for rows of over 8192 columns (kWide) in shared
 // memory with each tensor loaded where it is used.
 template <class S, int NV, Map M, bool kWide, int kMaxThreads, int kMinCtas>
 __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const __grid_constant__ NormBwd p) {
-    extern __shared__ float wide_acc[];   // kWide: [3][NV][8][threads]
-    __shared__ float red[2][2][32], red2[2][32];
+    extern __shared__ float wide_acc[];   // kWide: [2][NV][8][threads]
+    __shared__ float red[2][2][32];
     const int tr = threadIdx.x, threads = blockDim.x, H = p.H;
     const float inv_h = 1.0f / (float)H;
     const bool pre = p.io.dn != nullptr, block = p.io.y != nullptr, post = p.io.w_post != nullptr;
-    const bool channel = p.gate == MOE_GATE_CHANNEL;
-    float acc[kWide ? 1 : 3][NV][8];
-    auto sum_at = [&](int which, int i, int j) -> float & {   // 0: dw_post, 1: dgate, 2: dw_pre
+    const bool channel = p.gate == MOE_GATE_CHANNEL, token = p.gate == MOE_GATE_TOKEN;
+    float acc[kWide ? 1 : 2][NV][8];
+    auto sum_at = [&](int which, int i, int j) -> float & {   // 0: A, 1: P
         if (kWide) return wide_acc[((which * NV + i) * 8 + j) * threads + tr];
         return acc[kWide ? 0 : which][i][j];
     };
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum_at(k, i, j) = 0.0f;
+    // w_post times a channel's gate (1 where absent)
+    auto load_scale = [&](float (&w)[8], int i) {
+        if (post) {
+            load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+        }
+        if (channel) {
+            float g[8];
+            load_param8<M>(g, p.io.gate, p.param_f32, i, tr, threads, H);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] *= g[j];
+        }
+    };
     Row<S, NV, M> h, y, dh, dn;
-    auto fetch_h = [&](int64_t t) { if (pre) h.load(p.io.h, p.io.ld_h, t, tr, threads, H); };
-    auto fetch_dn = [&](int64_t t) { dn.load(p.io.dn, p.io.ld_dn, t, tr, threads, H); };
+    auto fetch_pre = [&](int64_t t) {
+        if (pre) h.load(p.io.h, p.io.ld_h, t, tr, threads, H);
+        dn.load(p.io.dn, p.io.ld_dn, t, tr, threads, H);
+    };
     auto fetch_dh = [&](int64_t t) { dh.load(p.io.dh, p.io.ld_dh, t, tr, threads, H); };
     auto fetch_y = [&](int64_t t) { y.load(p.io.y, p.io.ld_y, t, tr, threads, H); };
-    auto fetch = [&](int64_t t) {
-        if (kWide || t >= p.T) return;
-        fetch_h(t), fetch_dn(t), fetch_dh(t), fetch_y(t);
-    };
-    fetch(blockIdx.x);
+    if (!kWide && blockIdx.x < p.T) fetch_pre(blockIdx.x), fetch_dh(blockIdx.x), fetch_y(blockIdx.x);
     int turn = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
-        float D[NV][8], u[NV][8];
-        float r2 = 0.0f, m2 = 0.0f;
+        const int64_t next = t + gridDim.x;
+        const bool more = !kWide && next < p.T;
+        float D[NV][8];
         if (pre) {
-            r2 = p.io.rstd_pre[t];
-            if (kWide) fetch_h(t), fetch_dn(t);
+            if (kWide) fetch_pre(t);
+            const float r2 = p.io.rstd_pre[t];
+            float s2 = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float w[8], hv[8];
-                dn.v[i].get(D[i]);
+                float w[8], hv[8], v[8];
+                dn.v[i].get(v);
                 h.v[i].get(hv);
                 load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    hv[j] *= r2;
-                    sum_at(2, i, j) = fmaf(D[i][j], hv[j], sum_at(2, i, j));
-                    D[i][j] *= w[j];
-                    m2 = fmaf(D[i][j], hv[j], m2);
+                    const float th = v[j] * hv[j];
+                    sum_at(1, i, j) = fmaf(th, r2, sum_at(1, i, j));
+                    s2 = fmaf(th, w[j], s2);
+                    D[i][j] = v[j] * r2 * w[j];
                 }
             }
-            m2 = row_sum<false>(m2, red[0][turn]) * inv_h;
+            s2 = row_sum<false>(s2, red[0][turn]) * inv_h * -(r2 * r2 * r2);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float hv[8];
                 h.v[i].get(hv);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) D[i][j] = r2 * (D[i][j] - hv[j] * r2 * m2);
+                for (int j = 0; j < 8; ++j) D[i][j] = fmaf(hv[j], s2, D[i][j]);
             }
+            if (more) fetch_pre(next);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -314,13 +336,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
 #pragma unroll
                 for (int j = 0; j < 8; ++j) D[i][j] += v[j];
             }
+            if (more) fetch_dh(next);
         }
-        if (block) {
-            if (kWide) fetch_y(t);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) y.v[i].get(u[i]);
-        }
-        fetch(t + gridDim.x);
         const float rs = block ? p.residual_scale : 1.0f;
         S *dres = static_cast<S *>(p.io.dresidual) + t * p.io.ld_dresidual;
 #pragma unroll
@@ -331,55 +348,43 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             store8<M>(dres, v, i, tr, threads, H);
         }
         if (!block) continue;
-        // D becomes b = D gate w_post, u becomes yh (without a post norm: D gate, y)
+        if (kWide) fetch_y(t);
         const float r1 = post ? p.io.rstd_post[t] : 1.0f;
-        const float gt = p.gate == MOE_GATE_TOKEN ? load_param(p.io.gate, p.param_f32, t) : 1.0f;
-        float m1 = 0.0f, sg = 0.0f;
+        const float g = token ? load_param(p.io.gate, p.param_f32, t) : 1.0f, gr = g * r1;
+        float s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float w[8], g[8];
-            if (post) load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
-            if (channel) load_param8<M>(g, p.io.gate, p.param_f32, i, tr, threads, H);
+            float w[8], v[8];
+            load_scale(w, i);
+            y.v[i].get(v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                u[i][j] *= r1;
-                const float wj = post ? w[j] : 1.0f, gj = channel ? g[j] : gt;
-                const float du = D[i][j] * u[i][j];
-                if (post) sum_at(0, i, j) = fmaf(du, gj, sum_at(0, i, j));
-                if (channel) sum_at(1, i, j) = fmaf(du, wj, sum_at(1, i, j));
-                sg = fmaf(du, wj, sg);
-                D[i][j] *= gj * wj;
-                m1 = fmaf(D[i][j], u[i][j], m1);
+                const float du = D[i][j] * v[j];   // r1 is applied to the sums
+                sum_at(0, i, j) = fmaf(du, gr, sum_at(0, i, j));
+                D[i][j] *= w[j];
+                s1 = fmaf(du, w[j], s1);
             }
         }
-        if (post || p.gate == MOE_GATE_TOKEN) {
-            // both sums behind one barrier
-            m1 = warp_sum(m1);
-            sg = warp_sum(sg);
-            float *m = red[1][turn], *gs = red2[turn];
-            const int lane = tr & 31;
-            if (lane == 0) m[tr >> 5] = m1, gs[tr >> 5] = sg;
-            __syncthreads();
-            m1 = warp_sum(lane < (threads >> 5) ? m[lane] : 0.0f) * inv_h;
-            if (p.gate == MOE_GATE_TOKEN && tr < 32) {
-                sg = warp_sum(lane < (threads >> 5) ? gs[lane] : 0.0f);
-                if (tr == 0) p.io.dgate[t] = sg;
-            }
+        if (post || token) {
+            s1 = row_sum<false>(s1, red[1][turn]) * r1;
+            if (token && tr == 0) p.io.dgate[t] = s1;
         }
+        const float back = post ? -s1 * inv_h * r1 : 0.0f;
         S *dy = static_cast<S *>(p.io.dy) + t * p.io.ld_dy;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (post) {
+            float v[8];
+            y.v[i].get(v);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) D[i][j] = r1 * (D[i][j] - u[i][j] * m1);
-            }
-            store8<M>(dy, D[i], i, tr, threads, H);
+            for (int j = 0; j < 8; ++j) v[j] = gr * fmaf(v[j], back, D[i][j]);
+            store8<M>(dy, v, i, tr, threads, H);
         }
+        if (more) fetch_y(next);
     }
-    float *part = p.part + (int64_t)blockIdx.x * 3 * H;
+    float *part = p.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        if (!(k == 0 ? post : k == 1 ? channel : pre)) continue;
+    for (int k = 0; k < 2; ++k) {
+        if (!(k == 0 ? post || channel : pre)) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float v[8];
@@ -391,20 +396,27 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
 }
 
 // Column sums of the partials, always in the same order: a thread takes every 32nd row, then the 32 are added in turn.
-__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *part, int parts, int H, float *dw_post, float *dgate,
-                                                            float *dw_pre) {
+// A (blockIdx.y = 0) becomes dw_post and a channel's dgate, P (1) is dw_pre.
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const NormBwd p, int parts) {
     __shared__ float sum[32][33];
-    const int lane = threadIdx.x & 31, r0 = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
-    float *out = blockIdx.y == 0 ? dw_post : blockIdx.y == 1 ? dgate : dw_pre;
-    if (!out) return;
+    const int H = p.H, lane = threadIdx.x & 31, r0 = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    const bool channel = p.gate == MOE_GATE_CHANNEL;
+    if (blockIdx.y == 0 ? !p.io.w_post && !channel : !p.io.dw_pre) return;
     float s = 0.0f;
     if (col < H)
 #pragma unroll 4
-        for (int r = r0; r < parts; r += 32) s += part[((int64_t)r * 3 + blockIdx.y) * H + col];
+        for (int r = r0; r < parts; r += 32) s += p.part[((int64_t)r * 2 + blockIdx.y) * H + col];
     sum[r0][lane] = s;
     __syncthreads();
     s = warp_sum(sum[lane][r0]);   // column r0 of the block, the 32 partial rows across the lanes
-    if (lane == 0 && blockIdx.x * 32 + r0 < H) out[blockIdx.x * 32 + r0] = s;
+    const int out = blockIdx.x * 32 + r0;
+    if (lane != 0 || out >= H) return;
+    if (blockIdx.y == 1) {
+        p.io.dw_pre[out] = s;
+        return;
+    }
+    if (p.io.w_post) p.io.dw_post[out] = channel ? s * load_param(p.io.gate, p.param_f32, out) : s;
+    if (channel) p.io.dgate[out] = p.io.w_post ? s * load_param(p.io.w_post, p.param_f32, out) : s;
 }
 
 bool valid(const moe_norm_config *c) {
@@ -456,10 +468,10 @@ cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
     const int threads = (p.H + per_thread - 1) / per_thread * 32;
     size_t smem = 0;
     if (kWide) {
-        smem = (size_t)3 * NV * 8 * threads * 4;
+        smem = (size_t)2 * NV * 8 * threads * 4;
         static std::atomic<uint32_t> done{0};
         const cudaError_t e = smem_limit_once((const void *)norm_bwd_kernel<S, NV, M, kWide, kMaxThreads, kMinCtas>,
-                                              3 * MOE_NORM_MAX_HIDDEN * 4, done);
+                                              2 * MOE_NORM_MAX_HIDDEN * 4, done);
         if (e != cudaSuccess) return e;
     }
     norm_bwd_kernel<S, NV, M, kWide, kMaxThreads, kMinCtas><<<parts, threads, smem, s>>>(p);
@@ -469,7 +481,7 @@ cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
 template <class S, Map M>
 cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
     if (p.H <= 2048) return launch_bwd<S, 1, M, false, 256, 2>(p, parts, s);
-    if (p.H <= 8192) return launch_bwd<S, 2, M, false, 512, 1>(p, parts, s);
+    if (p.H <= 8192) return getenv("NB2") ? launch_bwd<S, 2, M, false, 512, 1>(p, parts, s) : launch_bwd<S, 1, M, false, 1024, 1>(p, parts, s);
     return launch_bwd<S, 2, M, true, 1024, 1>(p, parts, s);
 }
 
@@ -531,7 +543,7 @@ int moe_norm_forward(const moe_norm_config *cfg, int num_tokens, const moe_norm_
 
 size_t moe_norm_workspace_bytes(const moe_norm_config *cfg, int num_tokens) {
     if (!valid(cfg) || num_tokens < 0) return 0;
-    const size_t b = (size_t)bwd_parts(cfg->hidden, num_tokens) * 3 * cfg->hidden * 4;
+    const size_t b = (size_t)bwd_parts(cfg->hidden, num_tokens) * 2 * cfg->hidden * 4;
     return (b + 255) / 256 * 256;
 }
 
@@ -577,8 +589,7 @@ int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const moe_norm
     const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_bwd_any<float>(p, parts, s) : launch_bwd_any<bf16>(p, parts, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (sums) {
-        norm_bwd_sum_kernel<<<dim3((H + 31) / 32, 3), 1024, 0, s>>>(p.part, parts, H, io->dw_post,
-                                                                    channel ? io->dgate : nullptr, io->dw_pre);
+        norm_bwd_sum_kernel<<<dim3((H + 31) / 32, 2), 1024, 0, s>>>(p, parts);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
