@@ -94,34 +94,64 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
 
 struct NormFwd {
     moe_norm_io io;
-    int T, H, quant, gate;
+    int T, H, quant, gate, slots;
     bool param_f32;
     float eps, residual_scale;
 };
 
-// A row of the stream tensors as loaded, so that the next row can be on its way while this one is worked on.
-template <class S, int NV, Map M>
-struct Row {
-    Raw8<S> v[NV];
-    __device__ __forceinline__ void load(const void *base, int64_t ld, int64_t t, int tr, int threads, int H) {
+// A thread's part of one stream tensor's row, on its way while earlier rows are worked on.  With aligned rows (kRing) it
+// comes through shared memory by asynchronous 16-byte copies, into slots that no other thread touches: the waits are the
+// thread's own, and a slot can be refilled as soon as the thread has read it.  Else it is loaded into registers.
+template <class S, int NV, Map M, bool kRing>
+struct Feed {
+    Raw8<S> v[kRing ? 1 : NV];
+    uint8_t *slots;   // kRing: [slot][NV][threads] 16 (bf16) or 32 (f32) bytes
+    __device__ __forceinline__ uint8_t *at(int slot, int i, int tr, int threads) const {
+        return slots + (size_t)((slot * NV + i) * threads + tr) * (8 * sizeof(S));
+    }
+    __device__ __forceinline__ void fetch(const void *base, int64_t ld, int64_t t, int slot, int tr, int threads, int H) {
         if (!base) return;
         const S *row = static_cast<const S *>(base) + t * ld;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (M == kVec) {
                 const int c = column<M>(i, 0, tr, threads);
-                if (c < H) v[i].load_once(row + c);
-                else v[i].zero();
+                if (kRing) {
+                    if (c < H) copy_async<8 * sizeof(S)>(at(slot, i, tr, threads), row + c);
+                } else if (c < H) {
+                    v[kRing ? 0 : i].load_once(row + c);
+                } else {
+                    v[kRing ? 0 : i].zero();
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int c = column<M>(i, j, tr, threads);
-                    v[i].put(j, c < H ? row[c] : from_f32<S>(0.0f));
+                    v[kRing ? 0 : i].put(j, c < H ? row[c] : from_f32<S>(0.0f));
                 }
             }
         }
     }
+    __device__ __forceinline__ void get(float (&f)[8], int i, int slot, int tr, int threads, int H) const {
+        if (kRing) {
+            Raw8<S> r;
+            r.zero();
+            if (column<M>(i, 0, tr, threads) < H) r.load(reinterpret_cast<const S *>(at(slot, i, tr, threads)));
+            r.get(f);
+        } else {
+            v[kRing ? 0 : i].get(f);
+        }
+    }
 };
+constexpr int kMaxSlots = 4;
+// Waits until at most `slots` - 1 of this thread's groups of copies are under way.
+__device__ __forceinline__ void wait_row(int slots) {
+    if (slots == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (slots == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (slots == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+__device__ __forceinline__ void commit_row() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Codes and scale of a thread's chunk at column c.  A group is 16 (of 128 columns) or 4 (of 32) neighbouring chunks,
 // all of them in the row or none; every lane of the warp calls.
@@ -151,31 +181,61 @@ __device__ __forceinline__ void quantise8(const NormFwd &p, const float (&v)[8],
             make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
 }
 
-// A warp takes one row (kWarpRow), or a CTA rows b, b + CTAs, ..., with the next row on its way from the moment this
-// one is unpacked.
-template <class S, int NV, Map M, bool kWarpRow, int kMaxThreads, int kMinCtas>
+// A warp takes one row (kWarpRow), or a CTA rows b, b + CTAs, ... with the next `slots` rows on their way and (kKeep) its
+// columns' parameters in registers.
+template <class S, int NV, Map M, bool kWarpRow, bool kKeep, int kMaxThreads, int kMinCtas>
 __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const __grid_constant__ NormFwd p) {
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][2][32];
+    constexpr bool kRing = M == kVec && !kWarpRow;
     const int tr = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
-    const int H = p.H;
+    const int H = p.H, slots = kRing ? p.slots : 1;
     const float inv_h = 1.0f / (float)H;
     int64_t t = kWarpRow ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
-    Row<S, NV, M> res, y;
-    auto fetch = [&](int64_t t) {
-        if (t >= p.T) return;
-        y.load(p.io.y, p.io.ld_y, t, tr, threads, H);
-        res.load(p.io.residual, p.io.ld_residual, t, tr, threads, H);
+    Feed<S, NV, M, kRing> res, y;
+    res.slots = ring;
+    y.slots = ring + (size_t)slots * NV * threads * 8 * sizeof(S);
+    auto fetch = [&](int64_t t, int slot) {
+        if (t < p.T) {
+            y.fetch(p.io.y, p.io.ld_y, t, slot, tr, threads, H);
+            res.fetch(p.io.residual, p.io.ld_residual, t, slot, tr, threads, H);
+        }
+        if (kRing) commit_row();
     };
-    fetch(t);
-    int turn = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
-    for (; t < p.T; t += gridDim.x, turn ^= 1) {
+    for (int i = 0; i < slots; ++i) fetch(t + (int64_t)i * gridDim.x, i);
+    // w_post times a channel's gate (1 where absent), w_pre
+    auto load_post = [&](float (&w)[8], int i) {
+        if (p.io.w_post) {
+            load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+        }
+        if (p.gate == MOE_GATE_CHANNEL) {
+            float g[8];
+            load_param8<M>(g, p.io.gate, p.param_f32, i, tr, threads, H);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] *= g[j];
+        }
+    };
+    float k_post[kKeep ? NV : 1][8], k_pre[kKeep ? NV : 1][8];
+    if (kKeep) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (p.io.y) load_post(k_post[kKeep ? i : 0], i);
+            if (p.io.w_pre) load_param8<M>(k_pre[kKeep ? i : 0], p.io.w_pre, p.param_f32, i, tr, threads, H);
+        }
+    }
+    int turn = 0, slot = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
+    for (; t < p.T; t += gridDim.x, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
+        if (kRing) wait_row(slots);
         float z[NV][8], u[NV][8];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            res.v[i].get(z[i]);
-            if (p.io.y) y.v[i].get(u[i]);
+            res.get(z[i], i, slot, tr, threads, H);
+            if (p.io.y) y.get(u[i], i, slot, tr, threads, H);
         }
-        if (!kWarpRow) fetch(t + gridDim.x);
+        if (!kWarpRow) fetch(t + (int64_t)slots * gridDim.x, slot);
         if (p.io.y) {
             float r1 = 1.0f;
             if (p.io.w_post) {
@@ -192,18 +252,10 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float w[8];
-                if (p.io.w_post) {
-                    load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
+                if (!kKeep) load_post(w, i);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
-                }
-                if (p.gate == MOE_GATE_CHANNEL) {
-                    load_param8<M>(w, p.io.gate, p.param_f32, i, tr, threads, H);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) u[i][j] *= w[j];
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[i][j] = fmaf(u[i][j], r1, p.residual_scale * z[i][j]);
+                for (int j = 0; j < 8; ++j)
+                    z[i][j] = fmaf(u[i][j] * (kKeep ? k_post[kKeep ? i : 0][j] : w[j]), r1, p.residual_scale * z[i][j]);
                 store8<M>(h, z[i], i, tr, threads, H);
             }
         }
@@ -219,9 +271,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float w[8];
-                load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+                if (!kKeep) load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * r2 * w[j];
+                for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * r2 * (kKeep ? k_pre[kKeep ? i : 0][j] : w[j]);
                 if (n) store8<M>(n, z[i], i, tr, threads, H);
                 if (M != kStride && p.quant != MOE_QUANT_NONE) quantise8(p, z[i], t, column<M>(i, 0, tr, threads), tr);
             }
@@ -233,7 +285,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
 struct NormBwd {
     moe_norm_grad_io io;
     float *part;   // [CTAs][2][H]
-    int T, H, gate;
+    int T, H, gate, slots;
     bool param_f32;
     float residual_scale;
 };
@@ -245,11 +297,12 @@ struct NormBwd {
 // channel gate) and a channel's dgate (times w_post, g = 1) after the last row.
 //
 // CTA b takes rows b, b + CTAs, ...; every thread keeps its columns throughout, so the sums over tokens stay with it
-// until the end: in registers, next to the prefetched next row, or for rows of over 8192 columns (kWide) in shared
-// memory with each tensor loaded where it is used.
+// until the end: in registers, next to its columns' parameters, or for rows of over 8192 columns (kWide) in shared
+// memory with everything else loaded where it is used.
 template <class S, int NV, Map M, bool kWide, int kMaxThreads, int kMinCtas>
 __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const __grid_constant__ NormBwd p) {
-    extern __shared__ float wide_acc[];   // kWide: [2][NV][8][threads]
+    extern __shared__ __align__(16) uint8_t ring[];
+    float *wide_acc = reinterpret_cast<float *>(ring);   // kWide: [2][NV][8][threads]
     __shared__ float red[2][2][32];
     const int tr = threadIdx.x, threads = blockDim.x, H = p.H;
     const float inv_h = 1.0f / (float)H;
@@ -281,46 +334,70 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             for (int j = 0; j < 8; ++j) w[j] *= g[j];
         }
     };
-    Row<S, NV, M> h, y, dh, dn;
-    auto fetch_pre = [&](int64_t t) {
-        if (pre) h.load(p.io.h, p.io.ld_h, t, tr, threads, H);
-        dn.load(p.io.dn, p.io.ld_dn, t, tr, threads, H);
+    constexpr bool kRing = M == kVec && !kWide;
+    const int slots = kRing ? p.slots : 1;
+    Feed<S, NV, M, kRing> h, y, dh, dn;
+    const size_t tensor = (size_t)slots * NV * threads * 8 * sizeof(S);
+    h.slots = ring, dn.slots = ring + tensor, dh.slots = ring + 2 * tensor, y.slots = ring + 3 * tensor;
+    auto fetch_pre = [&](int64_t t, int slot) {
+        if (t >= p.T || !pre) return;
+        h.fetch(p.io.h, p.io.ld_h, t, slot, tr, threads, H);
+        dn.fetch(p.io.dn, p.io.ld_dn, t, slot, tr, threads, H);
     };
-    auto fetch_dh = [&](int64_t t) { dh.load(p.io.dh, p.io.ld_dh, t, tr, threads, H); };
-    auto fetch_y = [&](int64_t t) { y.load(p.io.y, p.io.ld_y, t, tr, threads, H); };
-    if (!kWide && blockIdx.x < p.T) fetch_pre(blockIdx.x), fetch_dh(blockIdx.x), fetch_y(blockIdx.x);
+    auto fetch_dh = [&](int64_t t, int slot) {
+        if (t < p.T) dh.fetch(p.io.dh, p.io.ld_dh, t, slot, tr, threads, H);
+    };
+    auto fetch_y = [&](int64_t t, int slot) {
+        if (t < p.T) y.fetch(p.io.y, p.io.ld_y, t, slot, tr, threads, H);
+        if (kRing) commit_row();   // the last of a row's copies
+    };
+    if (!kWide)
+        for (int i = 0; i < slots; ++i) {
+            const int64_t t = blockIdx.x + (int64_t)i * gridDim.x;
+            fetch_pre(t, i), fetch_dh(t, i), fetch_y(t, i);
+        }
+    constexpr bool kKeep = !kWide;
+    float k_scale[kKeep ? NV : 1][8], k_pre[kKeep ? NV : 1][8];
+    if (kKeep) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (block) load_scale(k_scale[kKeep ? i : 0], i);
+            if (pre) load_param8<M>(k_pre[kKeep ? i : 0], p.io.w_pre, p.param_f32, i, tr, threads, H);
+        }
+    }
+    int slot = 0;
     int turn = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
-        const int64_t next = t + gridDim.x;
-        const bool more = !kWide && next < p.T;
+    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
+        const int64_t next = kWide ? p.T : t + (int64_t)slots * gridDim.x;
+        if (kRing) wait_row(slots);
         float D[NV][8];
         if (pre) {
-            if (kWide) fetch_pre(t);
+            if (kWide) fetch_pre(t, 0);
             const float r2 = p.io.rstd_pre[t];
             float s2 = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float w[8], hv[8], v[8];
-                dn.v[i].get(v);
-                h.v[i].get(hv);
-                load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+                dn.get(v, i, slot, tr, threads, H);
+                h.get(hv, i, slot, tr, threads, H);
+                if (!kKeep) load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float th = v[j] * hv[j];
+                    const float th = v[j] * hv[j], wj = kKeep ? k_pre[kKeep ? i : 0][j] : w[j];
                     sum_at(1, i, j) = fmaf(th, r2, sum_at(1, i, j));
-                    s2 = fmaf(th, w[j], s2);
-                    D[i][j] = v[j] * r2 * w[j];
+                    s2 = fmaf(th, wj, s2);
+                    D[i][j] = v[j] * r2 * wj;
                 }
             }
             s2 = row_sum<false>(s2, red[0][turn]) * inv_h * -(r2 * r2 * r2);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float hv[8];
-                h.v[i].get(hv);
+                h.get(hv, i, slot, tr, threads, H);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) D[i][j] = fmaf(hv[j], s2, D[i][j]);
             }
-            if (more) fetch_pre(next);
+            fetch_pre(next, slot);
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -328,15 +405,15 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
                 for (int j = 0; j < 8; ++j) D[i][j] = 0.0f;
         }
         if (p.io.dh) {
-            if (kWide) fetch_dh(t);
+            if (kWide) fetch_dh(t, 0);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 float v[8];
-                dh.v[i].get(v);
+                dh.get(v, i, slot, tr, threads, H);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) D[i][j] += v[j];
             }
-            if (more) fetch_dh(next);
+            fetch_dh(next, slot);
         }
         const float rs = block ? p.residual_scale : 1.0f;
         S *dres = static_cast<S *>(p.io.dresidual) + t * p.io.ld_dresidual;
@@ -347,22 +424,25 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             for (int j = 0; j < 8; ++j) v[j] = rs * D[i][j];
             store8<M>(dres, v, i, tr, threads, H);
         }
-        if (!block) continue;
-        if (kWide) fetch_y(t);
+        if (!block) {
+            fetch_y(next, slot);
+            continue;
+        }
+        if (kWide) fetch_y(t, 0);
         const float r1 = post ? p.io.rstd_post[t] : 1.0f;
         const float g = token ? load_param(p.io.gate, p.param_f32, t) : 1.0f, gr = g * r1;
         float s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float w[8], v[8];
-            load_scale(w, i);
-            y.v[i].get(v);
+            if (!kKeep) load_scale(w, i);
+            y.get(v, i, slot, tr, threads, H);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float du = D[i][j] * v[j];   // r1 is applied to the sums
+                const float du = D[i][j] * v[j], wj = kKeep ? k_scale[kKeep ? i : 0][j] : w[j];   // r1 is applied to the sums
                 sum_at(0, i, j) = fmaf(du, gr, sum_at(0, i, j));
-                D[i][j] *= w[j];
-                s1 = fmaf(du, w[j], s1);
+                D[i][j] *= wj;
+                s1 = fmaf(du, wj, s1);
             }
         }
         if (post || token) {
@@ -374,12 +454,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float v[8];
-            y.v[i].get(v);
+            y.get(v, i, slot, tr, threads, H);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = gr * fmaf(v[j], back, D[i][j]);
             store8<M>(dy, v, i, tr, threads, H);
         }
-        if (more) fetch_y(next);
+        fetch_y(next, slot);
     }
     float *part = p.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
@@ -431,24 +511,41 @@ bool valid(const moe_norm_config *c) {
 
 bool rows16(const void *p, int64_t ld, size_t es) { return !p || (aligned_to(p, 16) && ld * es % 16 == 0); }
 
-template <class S, int NV, Map M, bool kWarpRow, int kMaxThreads, int kMinCtas>
-cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
+// Slots of a CTA that shares its SM with ctas - 1 others, `row` bytes each.
+constexpr size_t kRingBytes = 216 * 1024;
+int ring_slots(size_t row, int ctas) { return (int)std::max<size_t>(1, std::min<size_t>(kMaxSlots, kRingBytes / ctas / row)); }
+
+template <class S, int NV, Map M, bool kWarpRow, bool kKeep, int kMaxThreads, int kMinCtas>
+cudaError_t launch_fwd(NormFwd p, cudaStream_t s) {
     const int per_thread = 8 * NV * 32;   // columns of a warp
     const int threads = kWarpRow ? 128 : (p.H + per_thread - 1) / per_thread * 32;
-    const int ctas = kWarpRow ? (p.T + 3) / 4 : std::min(p.T, 152 * (1024 / threads > kMinCtas ? 1024 / threads : kMinCtas));
-    norm_fwd_kernel<S, NV, M, kWarpRow, kMaxThreads, kMinCtas><<<ctas, threads, 0, s>>>(p);
+    const auto kernel = norm_fwd_kernel<S, NV, M, kWarpRow, kKeep, kMaxThreads, kMinCtas>;
+    if (kWarpRow) {
+        kernel<<<(p.T + 3) / 4, threads, 0, s>>>(p);
+        return cudaGetLastError();
+    }
+    const int per_sm = std::max(1, kMaxThreads * kMinCtas / threads);
+    size_t smem = 0;
+    if (M == kVec) {
+        const size_t row = (size_t)2 * NV * threads * 8 * sizeof(S);
+        p.slots = ring_slots(row, per_sm);
+        smem = p.slots * row;
+        static std::atomic<uint32_t> done{0};
+        const cudaError_t e = smem_limit_once((const void *)kernel, kRingBytes, done);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<std::min(p.T, 152 * per_sm), threads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
 template <class S, Map M>
 cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
     // up to 1024 columns a warp holds the row and no barrier is needed
-    if (p.H <= 256) return launch_fwd<S, 1, M, true, 128, 1>(p, s);
-    if (p.H <= 512) return launch_fwd<S, 2, M, true, 128, 1>(p, s);
-    if (p.H <= 1024) return launch_fwd<S, 4, M, true, 128, 1>(p, s);
-    // up to two rows an SM: as many threads a row as it has chunks, for latency; more: fewer and longer threads
-    if (p.H <= 8192) return p.T <= 304 ? launch_fwd<S, 1, M, false, 1024, 1>(p, s) : launch_fwd<S, 2, M, false, 512, 2>(p, s);
-    return launch_fwd<S, 2, M, false, 1024, 1>(p, s);
+    if (p.H <= 256) return launch_fwd<S, 1, M, true, false, 128, 1>(p, s);
+    if (p.H <= 512) return launch_fwd<S, 2, M, true, false, 128, 1>(p, s);
+    if (p.H <= 1024) return launch_fwd<S, 4, M, true, false, 128, 1>(p, s);
+    if (p.H <= 8192) return getenv("NF2") ? launch_fwd<S, 2, M, false, true, 512, 1>(p, s) : launch_fwd<S, 1, M, false, true, 1024, 1>(p, s);
+    return launch_fwd<S, 2, M, false, false, 1024, 1>(p, s);
 }
 
 template <class S>
@@ -463,18 +560,24 @@ cudaError_t launch_fwd_any(const NormFwd &p, cudaStream_t s) {
 }
 
 template <class S, int NV, Map M, bool kWide, int kMaxThreads, int kMinCtas>
-cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
+cudaError_t launch_bwd(NormBwd p, int parts, cudaStream_t s) {
     const int per_thread = 8 * NV * 32;
     const int threads = (p.H + per_thread - 1) / per_thread * 32;
+    const auto kernel = norm_bwd_kernel<S, NV, M, kWide, kMaxThreads, kMinCtas>;
     size_t smem = 0;
     if (kWide) {
         smem = (size_t)2 * NV * 8 * threads * 4;
+    } else if (M == kVec) {
+        const size_t row = (size_t)4 * NV * threads * 8 * sizeof(S);
+        p.slots = ring_slots(row, std::max(1, kMaxThreads * kMinCtas / threads));
+        smem = p.slots * row;
+    }
+    if (smem > 0) {
         static std::atomic<uint32_t> done{0};
-        const cudaError_t e = smem_limit_once((const void *)norm_bwd_kernel<S, NV, M, kWide, kMaxThreads, kMinCtas>,
-                                              2 * MOE_NORM_MAX_HIDDEN * 4, done);
+        const cudaError_t e = smem_limit_once((const void *)kernel, kRingBytes, done);
         if (e != cudaSuccess) return e;
     }
-    norm_bwd_kernel<S, NV, M, kWide, kMaxThreads, kMinCtas><<<parts, threads, smem, s>>>(p);
+    kernel<<<parts, threads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -534,7 +637,7 @@ int moe_norm_forward(const moe_norm_config *cfg, int num_tokens, const moe_norm_
         !aligned_to(io->rstd_post, 4) || !aligned_to(io->rstd_pre, 4) || !aligned_to(io->codes, 16) ||
         !aligned_to(io->sf, 4))
         return MOE_ERR_INVALID_ARG;
-    NormFwd p{*io, num_tokens, H, io->w_pre ? cfg->quant : (int)MOE_QUANT_NONE, io->y ? cfg->gate : (int)MOE_GATE_NONE,
+    NormFwd p{*io, num_tokens, H, io->w_pre ? cfg->quant : (int)MOE_QUANT_NONE, io->y ? cfg->gate : (int)MOE_GATE_NONE, 1,
               cfg->param_dtype == MOE_DTYPE_F32, cfg->eps, cfg->residual_scale};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_fwd_any<float>(p, s) : launch_fwd_any<bf16>(p, s);
@@ -584,7 +687,7 @@ int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const moe_norm
     const bool sums = io->dw_post || io->dw_pre || channel;
     if (!d_workspace) return MOE_ERR_INVALID_ARG;
     const int parts = bwd_parts(H, num_tokens);
-    NormBwd p{*io, static_cast<float *>(d_workspace), num_tokens, H, io->y ? cfg->gate : (int)MOE_GATE_NONE,
+    NormBwd p{*io, static_cast<float *>(d_workspace), num_tokens, H, io->y ? cfg->gate : (int)MOE_GATE_NONE, 1,
               cfg->param_dtype == MOE_DTYPE_F32, cfg->residual_scale};
     const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_bwd_any<float>(p, parts, s) : launch_bwd_any<bf16>(p, parts, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;

@@ -37,6 +37,16 @@ __device__ __forceinline__ uint4 ld_stream16(const void *p) {
     return v;
 }
 
+// Asynchronous copy of `bytes` (16 or 32) to shared memory, past L1.
+template <int bytes>
+__device__ __forceinline__ void copy_async(void *smem, const void *src) {
+    const uint32_t d = smem_u32(smem);
+#pragma unroll
+    for (int i = 0; i < bytes; i += 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i), "l"(static_cast<const uint8_t *>(src) + i)
+                     : "memory");
+}
+
 // Eight neighbouring elements as they are in memory (16-byte aligned).
 template <class S>
 struct Raw8;
