@@ -9,7 +9,6 @@
 // between need.  Sums over a row are f32: 8 terms a chunk in order, then the
 // warp's tree, then the warps'.
 #include <math.h>
-#include <stdlib.h>
 
 #include <algorithm>
 
@@ -33,7 +32,7 @@ __device__ __forceinline__ int column(int i, int j, int tr, int threads) {
 
 // 8 columns of a row as f32 (zero past the row's end).
 template <Map M, class S>
-__device__ __forceinline__ void load8(float (&v)[8], const S *row, int i, int tr, int threads, int H) {
+__device__ __forceinline__ void load8(F8 &v, const S *row, int i, int tr, int threads, int H) {
     if (M == kVec) {
         const int c = column<M>(i, 0, tr, threads);
         if (c < H) {
@@ -41,20 +40,19 @@ __device__ __forceinline__ void load8(float (&v)[8], const S *row, int i, int tr
             r.load(row + c);
             r.get(v);
         } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+            v.fill(0.0f);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = column<M>(i, j, tr, threads);
-            v[j] = c < H ? to_f32(row[c]) : 0.0f;
+            v.put(j, c < H ? to_f32(row[c]) : 0.0f);
         }
     }
 }
 
 template <Map M, class S>
-__device__ __forceinline__ void store8(S *row, const float (&v)[8], int i, int tr, int threads, int H) {
+__device__ __forceinline__ void store8(S *row, const F8 &v, int i, int tr, int threads, int H) {
     if (M == kVec) {
         const int c = column<M>(i, 0, tr, threads);
         if (c < H) {
@@ -66,14 +64,14 @@ __device__ __forceinline__ void store8(S *row, const float (&v)[8], int i, int t
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int c = column<M>(i, j, tr, threads);
-            if (c < H) row[c] = from_f32<S>(v[j]);
+            if (c < H) row[c] = from_f32<S>(v.get(j));
         }
     }
 }
 
 // The same for parameters, whose type is known at run time only (uniform branch).
 template <Map M>
-__device__ __forceinline__ void load_param8(float (&v)[8], const void *w, bool f32, int i, int tr, int threads, int H) {
+__device__ __forceinline__ void load_param8(F8 &v, const void *w, bool f32, int i, int tr, int threads, int H) {
     if (f32) load8<M>(v, static_cast<const float *>(w), i, tr, threads, H);
     else load8<M>(v, static_cast<const bf16 *>(w), i, tr, threads, H);
 }
@@ -132,11 +130,19 @@ struct Feed {
             }
         }
     }
-    __device__ __forceinline__ void get(float (&f)[8], int i, int slot, int tr, int threads, int H) const {
+    // Zeros for the chunks past the row's end, which no copy writes.
+    __device__ __forceinline__ void clear_tail(int n, int tr, int threads, int H) {
+        if (!kRing) return;
+        for (int i = 0; i < NV; ++i)
+            if (column<M>(i, 0, tr, threads) >= H)
+                for (int slot = 0; slot < n; ++slot)
+                    for (int b = 0; b < (int)sizeof(S) / 2; ++b)
+                        reinterpret_cast<uint4 *>(at(slot, i, tr, threads))[b] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(F8 &f, int i, int slot, int tr, int threads) const {
         if (kRing) {
             Raw8<S> r;
-            r.zero();
-            if (column<M>(i, 0, tr, threads) < H) r.load(reinterpret_cast<const S *>(at(slot, i, tr, threads)));
+            r.load(reinterpret_cast<const S *>(at(slot, i, tr, threads)));
             r.get(f);
         } else {
             v[kRing ? 0 : i].get(f);
@@ -155,30 +161,35 @@ __device__ __forceinline__ void commit_row() { asm volatile("cp.async.commit_gro
 
 // Codes and scale of a thread's chunk at column c.  A group is 16 (of 128 columns) or 4 (of 32) neighbouring chunks,
 // all of them in the row or none; every lane of the warp calls.
-__device__ __forceinline__ void quantise8(const NormFwd &p, const float (&v)[8], int64_t t, int c, int tr) {
+__device__ __forceinline__ void quantise8(const NormFwd &p, F8 v, int64_t t, int c, int tr) {
     float amax = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v.get(j)));
     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    float q[8];
+    float inv;
     if (p.quant == MOE_QUANT_FP8_128) {
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
         const Fp8Scale sc = fp8_scale(amax);
+        inv = sc.inv;
+        if (sc.up != 1.0f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = sc.apply(v[j]);
+            for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(v.p[j], pair(sc.up));
+        }
         if (c < p.H && (tr & 15) == 0) static_cast<float *>(p.io.sf)[t * (p.H / 128) + c / 128] = sc.sf;
     } else {
-        const int e = ue8m0_exponent(amax);
-        const float down = pow2(-e);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = v[j] * down;
-        if (c < p.H && (tr & 3) == 0) static_cast<uint8_t *>(p.io.sf)[t * (p.H / 32) + c / 32] = (uint8_t)(e + 127);
+        const int code = ue8m0_code(amax);
+        inv = ue8m0_inverse(code);
+        if (c < p.H && (tr & 3) == 0) static_cast<uint8_t *>(p.io.sf)[t * (p.H / 32) + c / 32] = (uint8_t)code;
     }
-    if (c < p.H)
-        *reinterpret_cast<uint2 *>(p.io.codes + t * p.H + c) =
-            make_uint2(e4m3x2(q[0], q[1]) | e4m3x2(q[2], q[3]) << 16, e4m3x2(q[4], q[5]) | e4m3x2(q[6], q[7]) << 16);
+    uint32_t q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 s = __fmul2_rn(v.p[j], pair(inv));
+        q[j] = e4m3x2(s.x, s.y);
+    }
+    if (c < p.H) *reinterpret_cast<uint2 *>(p.io.codes + t * p.H + c) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
 }
 
 // A warp takes one row (kWarpRow), or a CTA rows b, b + CTAs, ... with the next `slots` rows on their way and (kKeep) its
@@ -203,22 +214,20 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
         if (kRing) commit_row();
     };
     for (int i = 0; i < slots; ++i) fetch(t + (int64_t)i * gridDim.x, i);
-    // w_post times a channel's gate (1 where absent), w_pre
-    auto load_post = [&](float (&w)[8], int i) {
-        if (p.io.w_post) {
-            load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-        }
+    res.clear_tail(slots, tr, threads, H);
+    y.clear_tail(slots, tr, threads, H);
+    // w_post times a channel's gate (1 where absent)
+    auto load_post = [&](F8 &w, int i) {
+        if (p.io.w_post) load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
+        else w.fill(1.0f);
         if (p.gate == MOE_GATE_CHANNEL) {
-            float g[8];
+            F8 g;
             load_param8<M>(g, p.io.gate, p.param_f32, i, tr, threads, H);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] *= g[j];
+            for (int j = 0; j < 4; ++j) w.p[j] = __fmul2_rn(w.p[j], g.p[j]);
         }
     };
-    float k_post[kKeep ? NV : 1][8], k_pre[kKeep ? NV : 1][8];
+    F8 k_post[kKeep ? NV : 1], k_pre[kKeep ? NV : 1];
     if (kKeep) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -229,51 +238,53 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
     int turn = 0, slot = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
     for (; t < p.T; t += gridDim.x, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
         if (kRing) wait_row(slots);
-        float z[NV][8], u[NV][8];
+        F8 z[NV], u[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            res.get(z[i], i, slot, tr, threads, H);
-            if (p.io.y) y.get(u[i], i, slot, tr, threads, H);
+            res.get(z[i], i, slot, tr, threads);
+            if (p.io.y) y.get(u[i], i, slot, tr, threads);
         }
         if (!kWarpRow) fetch(t + (int64_t)slots * gridDim.x, slot);
         if (p.io.y) {
             float r1 = 1.0f;
             if (p.io.w_post) {
-                float s1 = 0.0f;
+                float2 s1 = pair(0.0f);
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) s1 = fmaf(u[i][j], u[i][j], s1);
-                r1 = 1.0f / sqrtf(fmaf(row_sum<kWarpRow>(s1, red[0][turn]), inv_h, p.eps));
+                    for (int j = 0; j < 4; ++j) s1 = __ffma2_rn(u[i].p[j], u[i].p[j], s1);
+                r1 = rsqrtf(fmaf(row_sum<kWarpRow>(s1.x + s1.y, red[0][turn]), inv_h, p.eps));
                 if (tr == 0 && p.io.rstd_post) p.io.rstd_post[t] = r1;
             }
             if (p.gate == MOE_GATE_TOKEN) r1 *= load_param(p.io.gate, p.param_f32, t);
             S *h = static_cast<S *>(p.io.h) + t * p.io.ld_h;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float w[8];
+                F8 w;
                 if (!kKeep) load_post(w, i);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    z[i][j] = fmaf(u[i][j] * (kKeep ? k_post[kKeep ? i : 0][j] : w[j]), r1, p.residual_scale * z[i][j]);
+                for (int j = 0; j < 4; ++j)
+                    z[i].p[j] = __ffma2_rn(__fmul2_rn(u[i].p[j], kKeep ? k_post[kKeep ? i : 0].p[j] : w.p[j]), pair(r1),
+                                           __fmul2_rn(pair(p.residual_scale), z[i].p[j]));
                 store8<M>(h, z[i], i, tr, threads, H);
             }
         }
         if (p.io.w_pre) {
-            float s2 = 0.0f;
+            float2 s2 = pair(0.0f);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s2 = fmaf(z[i][j], z[i][j], s2);
-            const float r2 = 1.0f / sqrtf(fmaf(row_sum<kWarpRow>(s2, red[1][turn]), inv_h, p.eps));
+                for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(z[i].p[j], z[i].p[j], s2);
+            const float r2 = rsqrtf(fmaf(row_sum<kWarpRow>(s2.x + s2.y, red[1][turn]), inv_h, p.eps));
             if (tr == 0 && p.io.rstd_pre) p.io.rstd_pre[t] = r2;
             S *n = p.io.n ? static_cast<S *>(p.io.n) + t * p.io.ld_n : nullptr;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float w[8];
+                F8 w;
                 if (!kKeep) load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z[i][j] = z[i][j] * r2 * (kKeep ? k_pre[kKeep ? i : 0][j] : w[j]);
+                for (int j = 0; j < 4; ++j)
+                    z[i].p[j] = __fmul2_rn(__fmul2_rn(z[i].p[j], pair(r2)), kKeep ? k_pre[kKeep ? i : 0].p[j] : w.p[j]);
                 if (n) store8<M>(n, z[i], i, tr, threads, H);
                 if (M != kStride && p.quant != MOE_QUANT_NONE) quantise8(p, z[i], t, column<M>(i, 0, tr, threads), tr);
             }
@@ -308,30 +319,34 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
     const float inv_h = 1.0f / (float)H;
     const bool pre = p.io.dn != nullptr, block = p.io.y != nullptr, post = p.io.w_post != nullptr;
     const bool channel = p.gate == MOE_GATE_CHANNEL, token = p.gate == MOE_GATE_TOKEN;
-    float acc[kWide ? 1 : 2][NV][8];
-    auto sum_at = [&](int which, int i, int j) -> float & {   // 0: A, 1: P
-        if (kWide) return wide_acc[((which * NV + i) * 8 + j) * threads + tr];
-        return acc[kWide ? 0 : which][i][j];
+    F8 acc[2][kWide ? 1 : NV];   // A, P
+    // adds v * f to sum `which` of chunk i
+    auto add = [&](int which, int i, int j, float2 v, float2 f) {   // pair j
+        if (kWide) {
+            float2 *at = reinterpret_cast<float2 *>(wide_acc) + ((which * NV + i) * 4 + j) * threads + tr;
+            *at = __ffma2_rn(v, f, *at);
+        } else {
+            acc[which][kWide ? 0 : i].p[j] = __ffma2_rn(v, f, acc[which][kWide ? 0 : i].p[j]);
+        }
     };
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum_at(k, i, j) = 0.0f;
-    // w_post times a channel's gate (1 where absent)
-    auto load_scale = [&](float (&w)[8], int i) {
-        if (post) {
-            load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+        for (int i = 0; i < NV; ++i) {
+            if (kWide)
+                for (int j = 0; j < 4; ++j)
+                    reinterpret_cast<float2 *>(wide_acc)[((k * NV + i) * 4 + j) * threads + tr] = pair(0.0f);
+            else acc[k][kWide ? 0 : i].fill(0.0f);
         }
+    // w_post times a channel's gate (1 where absent)
+    auto load_scale = [&](F8 &w, int i) {
+        if (post) load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
+        else w.fill(1.0f);
         if (channel) {
-            float g[8];
+            F8 g;
             load_param8<M>(g, p.io.gate, p.param_f32, i, tr, threads, H);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] *= g[j];
+            for (int j = 0; j < 4; ++j) w.p[j] = __fmul2_rn(w.p[j], g.p[j]);
         }
     };
     constexpr bool kRing = M == kVec && !kWide;
@@ -357,7 +372,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             fetch_pre(t, i), fetch_dh(t, i), fetch_y(t, i);
         }
     constexpr bool kKeep = !kWide;
-    float k_scale[kKeep ? NV : 1][8], k_pre[kKeep ? NV : 1][8];
+    h.clear_tail(slots, tr, threads, H), dn.clear_tail(slots, tr, threads, H);
+    dh.clear_tail(slots, tr, threads, H), y.clear_tail(slots, tr, threads, H);
+    F8 k_scale[kKeep ? NV : 1], k_pre[kKeep ? NV : 1];
     if (kKeep) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -370,48 +387,46 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
         const int64_t next = kWide ? p.T : t + (int64_t)slots * gridDim.x;
         if (kRing) wait_row(slots);
-        float D[NV][8];
+        F8 D[NV];
         if (pre) {
             if (kWide) fetch_pre(t, 0);
             const float r2 = p.io.rstd_pre[t];
-            float s2 = 0.0f;
+            float2 s2 = pair(0.0f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float w[8], hv[8], v[8];
-                dn.get(v, i, slot, tr, threads, H);
-                h.get(hv, i, slot, tr, threads, H);
+                F8 w, hv, v;
+                dn.get(v, i, slot, tr, threads);
+                h.get(hv, i, slot, tr, threads);
                 if (!kKeep) load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float th = v[j] * hv[j], wj = kKeep ? k_pre[kKeep ? i : 0][j] : w[j];
-                    sum_at(1, i, j) = fmaf(th, r2, sum_at(1, i, j));
-                    s2 = fmaf(th, wj, s2);
-                    D[i][j] = v[j] * r2 * wj;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 th = __fmul2_rn(v.p[j], hv.p[j]), wj = kKeep ? k_pre[kKeep ? i : 0].p[j] : w.p[j];
+                    add(1, i, j, th, pair(r2));
+                    s2 = __ffma2_rn(th, wj, s2);
+                    D[i].p[j] = __fmul2_rn(__fmul2_rn(v.p[j], pair(r2)), wj);
                 }
             }
-            s2 = row_sum<false>(s2, red[0][turn]) * inv_h * -(r2 * r2 * r2);
+            const float back = row_sum<false>(s2.x + s2.y, red[0][turn]) * inv_h * -(r2 * r2 * r2);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float hv[8];
-                h.get(hv, i, slot, tr, threads, H);
+                F8 hv;
+                h.get(hv, i, slot, tr, threads);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) D[i][j] = fmaf(hv[j], s2, D[i][j]);
+                for (int j = 0; j < 4; ++j) D[i].p[j] = __ffma2_rn(hv.p[j], pair(back), D[i].p[j]);
             }
             fetch_pre(next, slot);
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) D[i][j] = 0.0f;
+            for (int i = 0; i < NV; ++i) D[i].fill(0.0f);
         }
         if (p.io.dh) {
             if (kWide) fetch_dh(t, 0);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float v[8];
-                dh.get(v, i, slot, tr, threads, H);
+                F8 v;
+                dh.get(v, i, slot, tr, threads);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) D[i][j] += v[j];
+                for (int j = 0; j < 4; ++j) D[i].p[j] = __fadd2_rn(D[i].p[j], v.p[j]);
             }
             fetch_dh(next, slot);
         }
@@ -419,9 +434,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         S *dres = static_cast<S *>(p.io.dresidual) + t * p.io.ld_dresidual;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float v[8];
+            F8 v;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = rs * D[i][j];
+            for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(pair(rs), D[i].p[j]);
             store8<M>(dres, v, i, tr, threads, H);
         }
         if (!block) {
@@ -431,32 +446,33 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         if (kWide) fetch_y(t, 0);
         const float r1 = post ? p.io.rstd_post[t] : 1.0f;
         const float g = token ? load_param(p.io.gate, p.param_f32, t) : 1.0f, gr = g * r1;
-        float s1 = 0.0f;
+        float2 s1 = pair(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float w[8], v[8];
+            F8 w, v;
             if (!kKeep) load_scale(w, i);
-            y.get(v, i, slot, tr, threads, H);
+            y.get(v, i, slot, tr, threads);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float du = D[i][j] * v[j], wj = kKeep ? k_scale[kKeep ? i : 0][j] : w[j];   // r1 is applied to the sums
-                sum_at(0, i, j) = fmaf(du, gr, sum_at(0, i, j));
-                D[i][j] *= wj;
-                s1 = fmaf(du, wj, s1);
+            for (int j = 0; j < 4; ++j) {
+                const float2 du = __fmul2_rn(D[i].p[j], v.p[j]), wj = kKeep ? k_scale[kKeep ? i : 0].p[j] : w.p[j];
+                add(0, i, j, du, pair(gr));   // r1 is applied to the sums
+                s1 = __ffma2_rn(du, wj, s1);
+                D[i].p[j] = __fmul2_rn(D[i].p[j], wj);
             }
         }
+        float back = 0.0f;
         if (post || token) {
-            s1 = row_sum<false>(s1, red[1][turn]) * r1;
-            if (token && tr == 0) p.io.dgate[t] = s1;
+            const float s = row_sum<false>(s1.x + s1.y, red[1][turn]) * r1;
+            if (token && tr == 0) p.io.dgate[t] = s;
+            if (post) back = -s * inv_h * r1;
         }
-        const float back = post ? -s1 * inv_h * r1 : 0.0f;
         S *dy = static_cast<S *>(p.io.dy) + t * p.io.ld_dy;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float v[8];
-            y.get(v, i, slot, tr, threads, H);
+            F8 v;
+            y.get(v, i, slot, tr, threads);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = gr * fmaf(v[j], back, D[i][j]);
+            for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(pair(gr), __ffma2_rn(v.p[j], pair(back), D[i].p[j]));
             store8<M>(dy, v, i, tr, threads, H);
         }
         fetch_y(next, slot);
@@ -467,9 +483,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         if (!(k == 0 ? post || channel : pre)) continue;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = sum_at(k, i, j);
+            F8 v;
+            if (kWide)
+                for (int j = 0; j < 4; ++j)
+                    v.p[j] = reinterpret_cast<float2 *>(wide_acc)[((k * NV + i) * 4 + j) * threads + tr];
+            else v = acc[k][kWide ? 0 : i];
             store8<M>(part + k * H, v, i, tr, threads, H);   // kVec: H % 8 == 0, so these rows are 16-byte aligned too
         }
     }
@@ -544,7 +562,7 @@ cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
     if (p.H <= 256) return launch_fwd<S, 1, M, true, false, 128, 1>(p, s);
     if (p.H <= 512) return launch_fwd<S, 2, M, true, false, 128, 1>(p, s);
     if (p.H <= 1024) return launch_fwd<S, 4, M, true, false, 128, 1>(p, s);
-    if (p.H <= 8192) return getenv("NF2") ? launch_fwd<S, 2, M, false, true, 512, 1>(p, s) : launch_fwd<S, 1, M, false, true, 1024, 1>(p, s);
+    if (p.H <= 8192) return launch_fwd<S, 2, M, false, true, 512, 1>(p, s);
     return launch_fwd<S, 2, M, false, false, 1024, 1>(p, s);
 }
 
@@ -584,7 +602,7 @@ cudaError_t launch_bwd(NormBwd p, int parts, cudaStream_t s) {
 template <class S, Map M>
 cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
     if (p.H <= 2048) return launch_bwd<S, 1, M, false, 256, 2>(p, parts, s);
-    if (p.H <= 8192) return getenv("NB2") ? launch_bwd<S, 2, M, false, 512, 1>(p, parts, s) : launch_bwd<S, 1, M, false, 1024, 1>(p, parts, s);
+    if (p.H <= 8192) return launch_bwd<S, 2, M, false, 512, 1>(p, parts, s);
     return launch_bwd<S, 2, M, true, 1024, 1>(p, parts, s);
 }
 

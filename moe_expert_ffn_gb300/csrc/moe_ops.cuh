@@ -47,6 +47,21 @@ __device__ __forceinline__ void copy_async(void *smem, const void *src) {
                      : "memory");
 }
 
+// Eight f32 values as four pairs: one instruction multiplies or adds a pair.
+struct F8 {
+    float2 p[4];
+    __device__ __forceinline__ float get(int j) const { return (j & 1) ? p[j >> 1].y : p[j >> 1].x; }
+    __device__ __forceinline__ void put(int j, float v) {   // j known at compile time
+        if (j & 1) p[j >> 1].y = v;
+        else p[j >> 1].x = v;
+    }
+    __device__ __forceinline__ void fill(float v) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j] = make_float2(v, v);
+    }
+};
+__device__ __forceinline__ float2 pair(float v) { return make_float2(v, v); }
+
 // Eight neighbouring elements as they are in memory (16-byte aligned).
 template <class S>
 struct Raw8;
@@ -57,16 +72,14 @@ struct Raw8<bf16> {
     __device__ __forceinline__ void load_once(const bf16 *p) { r = ld_stream16(p); }
     __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = r; }
     __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
+    __device__ __forceinline__ void get(F8 &v) const {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
+        for (int j = 0; j < 4; ++j) v.p[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
     }
-    __device__ __forceinline__ void set(const float (&v)[8]) {
-        r = make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+    __device__ __forceinline__ void set(const F8 &v) {
+        r = make_uint4(bf16x2(v.p[0].x, v.p[0].y), bf16x2(v.p[1].x, v.p[1].y), bf16x2(v.p[2].x, v.p[2].y),
+                       bf16x2(v.p[3].x, v.p[3].y));
     }
     __device__ __forceinline__ void put(int j, bf16 e) {   // j known at compile time
         uint32_t &w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
@@ -94,13 +107,13 @@ struct Raw8<float> {
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = 0.0f;
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
+    __device__ __forceinline__ void get(F8 &v) const {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = f[j];
+        for (int j = 0; j < 4; ++j) v.p[j] = make_float2(f[2 * j], f[2 * j + 1]);
     }
-    __device__ __forceinline__ void set(const float (&v)[8]) {
+    __device__ __forceinline__ void set(const F8 &v) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = v[j];
+        for (int j = 0; j < 4; ++j) f[2 * j] = v.p[j].x, f[2 * j + 1] = v.p[j].y;
     }
     __device__ __forceinline__ void put(int j, float e) { f[j] = e; }
 };
@@ -129,33 +142,34 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     return s;
 }
 
-// FP8 group scale sf = amax / 448 and q = v / sf as v times 448/amax (within
-// one f32 rounding of the division, far inside an E4M3 step).  Below 2^-100
-// the reciprocal would pass the f32 range, so v is brought up by 2^64 first;
-// an all-zero group has sf 0 and codes 0.
+// FP8 group scale sf = amax / 448 and q = v / sf as v times 448 / amax (either
+// within 2 units in the last place, far inside an E4M3 step).  Below 2^-100
+// the reciprocal would pass the f32 range, so v is brought up by 2^64 first,
+// and from 2^120 on the fast division is out of its range; an all-zero group
+// has sf 0 and codes 0.
 struct Fp8Scale {
     float sf, up, inv;
-    __device__ __forceinline__ float apply(float v) const { return v * up * inv; }
 };
 __device__ __forceinline__ Fp8Scale fp8_scale(float amax) {
     Fp8Scale q;
-    q.sf = amax / 448.0f;
-    q.up = amax < 0x1p-100f ? 0x1p64f : 1.0f;
-    q.inv = amax > 0.0f ? 448.0f / (amax * q.up) : 0.0f;
+    q.sf = amax * (1.0f / 448.0f);
+    q.up = 1.0f;
+    q.inv = __fdividef(448.0f, amax);
+    if (!(amax >= 0x1p-100f && amax < 0x1p120f)) {
+        if (amax < 1.0f) q.up = 0x1p64f;
+        q.inv = amax > 0.0f ? 448.0f / (amax * q.up) : 0.0f;
+    }
     return q;
 }
 
-// UE8M0 exponent of the smallest power of two 2^e with amax/448 <= 2^e (the
-// ratio in binary32), e in [-127, 127]; -127 for an all-zero group.
-__device__ __forceinline__ int ue8m0_exponent(float amax) {
-    const float r = amax / 448.0f;
-    if (!(r > 0.0f)) return -127;
-    int ex;
-    const float fr = frexpf(r, &ex);
-    const int e = (fr == 0.5f) ? ex - 1 : ex;
-    return min(127, max(-127, e));
+// UE8M0 code e + 127 of the smallest power of two 2^e with amax / 448 <= 2^e:
+// 448 is 1.75 * 2^8, so with amax = m 2^x, e is x - 8 for m <= 1.75 and x - 7
+// above; the addition carries into the exponent exactly for the latter.  At
+// least 0 (all-zero groups among them), for infinities 247.
+__device__ __forceinline__ int ue8m0_code(float amax) {
+    return max(0, (int)((__float_as_uint(amax) + 0x001FFFFFu) >> 23) - 8);
 }
-// 2^e, e in [-127, 127] (2^-127 is a subnormal float).
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(e > -127 ? (uint32_t)(e + 127) << 23 : 0x00400000u); }
+// 2^-e of that code.
+__device__ __forceinline__ float ue8m0_inverse(int code) { return __uint_as_float((uint32_t)(254 - code) << 23); }
 
 }  // namespace moe
