@@ -2,13 +2,20 @@
 // expert counts, and the gradient of the logits (definitions in
 // include/moe.h).
 //
-// One warp per token; lane l holds experts l, l + 32, ...  Every warp walks a
-// contiguous range of tokens and keeps its loss sums in registers until the
-// sequence changes; then it writes them to a row of partial sums of its own.
-// Warp w in sequence s uses row w + s: along the walk either one grows with
-// every new pair, so rows never collide, and the rows of a sequence are those
-// of the consecutive warps that its tokens fall on.  The sums over rows are
-// taken in row order: no atomics, the same bits every time.
+// Large batches are bound by instructions, not by the [T, E] logits: one pass
+// reads them once, and what counts is the choice.  A token belongs to a group
+// of 32 lanes (8 for E <= 64), lane l holding experts l, l + G, ...: coalesced
+// for any E and pitch.  Every lane finds the two largest of its keys in one
+// scan; a round of the choice is then one reduction over the lanes' best, and
+// the winner moves up its second.  Only a lane that won twice scans again.
+//
+// Losses: CTAs walk contiguous token ranges, cut where a sequence ends; within
+// a cut every lane sums its experts' probabilities in registers, the CTA's
+// warps are joined in shared memory, and one row of partial sums is written.
+// CTA b in sequence s uses row b + s: along the walk either one grows with
+// every cut, so rows never collide, and the rows of a sequence are those of
+// the consecutive CTAs that its tokens fall on.  All sums are taken in a fixed
+// order: no float atomics, the same bits every time.
 #include <float.h>
 #include <math.h>
 
@@ -22,18 +29,20 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarpsPerCta = kThreads / 32;
-constexpr int kMaxLossWarps = 2432;   // 16 warps on each of 152 SMs
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxLossCtas = 608;   // four on each of 152 SMs
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr float kLog2e = 1.44269504f;
 
 // Rows of partial sums and what follows them in the workspace.
 struct Partials {
-    float *prob;     // [rows][E]
-    int32_t *count;  // [rows][E]
-    float *z;        // [rows]
-    int32_t *tokens; // [rows]
-    float *seq_bal;  // [S]
-    float *seq_z;    // [S]
+    float *prob;      // [rows][E]
+    int32_t *count;   // [rows][E]
+    float *z;         // [rows]
+    int32_t *tokens;  // [rows]
+    float *seq_bal;   // [S][E / 32]
+    float *seq_z;     // [S]
+    int *ticket;
 };
 
 struct RouterParams {
@@ -44,26 +53,58 @@ struct RouterParams {
     float *topk_weights;
     const int32_t *seq_offsets;
     Partials part;
-    int T, E, k, S, chunk;      // chunk: tokens per warp
+    int T, E, k, S, chunk;      // chunk: tokens per CTA
     int sigmoid, renorm;
     float scale;
 };
 
-// Keys whose order as unsigned integers is the order of the floats; 0 for a
-// closed expert (-inf or NaN).
-__device__ __forceinline__ uint32_t order_key(float v) {
-    if (!(v > -INFINITY)) return 0u;
-    const uint32_t b = __float_as_uint(v + 0.0f);   // -0 and 0 are equal
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+// A logit as it enters choice and scores: NaN and -inf are closed (-inf), +inf is the largest float.
+__device__ __forceinline__ float open_logit(float v) { return fminf(fmaxf(v, -INFINITY), FLT_MAX); }
+
+// e^v: its relative error is that of the rounded exponent, 2^-24 of |v| log2(e), plus 2 units in the last place.
+__device__ __forceinline__ float exp_of(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * kLog2e));
+    return r;
 }
 
-// A logit as it enters the scores: closed ones -inf, +inf the largest float.
-__device__ __forceinline__ float open_logit(float v) { return v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY; }
-
-// Sigmoid times e^-m with m = min(largest logit, 0): the ratios of the scores
-// of a token whose sigmoids all underflow stay right.
+// Sigmoid times e^-m with m = min(largest logit, 0): the ratios of the scores of a token whose sigmoids all underflow
+// stay right.
 __device__ __forceinline__ float sigmoid_scaled(float l, float m) {
-    return l >= 0.0f ? 1.0f / (1.0f + expf(-l)) : expf(l - m) / (1.0f + expf(l));
+    const float u = exp_of(-fabsf(l));
+    const float d = __fdividef(1.0f, 1.0f + u);
+    return l >= 0.0f ? d : (m < 0.0f ? exp_of(l - m) : u) * d;
+}
+// 1 - sigmoid(l)
+__device__ __forceinline__ float sigmoid_slope(float l) {
+    const float u = exp_of(-fabsf(l));
+    return (l >= 0.0f ? u : 1.0f) * __fdividef(1.0f, 1.0f + u);
+}
+
+// Reductions over the G lanes of a token; every lane gets the result.
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+    if (G == 32) {
+        float r;
+        asm("redux.sync.max.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "r"(kAll));
+        return r;
+    }
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+template <int G>
+__device__ __forceinline__ int group_min(int v) {
+    if (G == 32) return __reduce_min_sync(kAll, v);
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) v = min(v, __shfl_xor_sync(kAll, v, o));
+    return v;
 }
 
 __device__ __forceinline__ int find_seq(const int32_t *off, int S, int t) {
@@ -76,138 +117,256 @@ __device__ __forceinline__ int find_seq(const int32_t *off, int S, int t) {
     return lo;
 }
 
-template <class L, int NI, bool kLoss, bool kGiven>
-__global__ void __launch_bounds__(kThreads) router_kernel(const RouterParams p) {
-    const int lane = threadIdx.x & 31;
-    const int w = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
-    const int t0 = (int)min((int64_t)w * p.chunk, (int64_t)p.T), t1 = min(t0 + p.chunk, p.T);
-    if (t0 >= t1) return;
-    float prob[kLoss ? NI : 1];
-    int cnt[kLoss ? NI : 1];
-    float zsum = 0.0f;
-    int tokens = 0, s = 0, s_begin = 0, s_end = p.T;
-    if (kLoss) {
+// The sequence (or the gap before it) that token t is in: its index, whether it counts, and where the cut ends.
+struct Cut {
+    int s, end;
+    bool inside;
+};
+__device__ __forceinline__ Cut cut_at(const int32_t *off, int S, int t, int t1) {
+    Cut c{0, t1, true};
+    if (!off) return c;
+    c.s = find_seq(off, S, t);
+    if (c.s >= S) return Cut{S, t1, false};
+    c.inside = t >= off[c.s];
+    c.end = min(t1, c.inside ? off[c.s + 1] : off[c.s]);
+    return c;
+}
+
+template <class L, int NI, int G>
+__device__ __forceinline__ void load_row(float (&l)[NI], const void *logits, int64_t ld, int t, bool on, int lg, int E) {
+    const L *row = static_cast<const L *>(logits) + (int64_t)t * ld;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) prob[i] = 0.0f, cnt[i] = 0;
-        if (p.seq_offsets) {
-            s = find_seq(p.seq_offsets, p.S, t0);
-            s_begin = s < p.S ? p.seq_offsets[s] : p.T;
-            s_end = s < p.S ? p.seq_offsets[s + 1] : p.T;
+    for (int i = 0; i < NI; ++i) l[i] = on && lg + G * i < E ? open_logit(to_f32(row[lg + G * i])) : -INFINITY;
+}
+
+// The k largest keys of a group's token, ties to the lowest expert.  Slot j goes to lane j % G, place j / G: expert (-1:
+// nothing left) and key.  Returns the lane's chosen experts as bits.
+template <int NI, int G, int NS>
+__device__ __forceinline__ uint32_t choose(const float (&key)[NI], int k, int lg, int (&slot_e)[NS], float (&slot_key)[NS]) {
+    const int base = threadIdx.x & 31 & ~(G - 1);
+    uint32_t mask = 0;
+    float best, second;
+    int bi, si, known;
+    auto scan = [&]() {   // strict comparisons: of equal keys the first stays in front
+        best = second = -INFINITY;
+        bi = si = 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const float v = (mask >> i) & 1 ? -INFINITY : key[i];
+            const bool p1 = v > best, p2 = v > second;
+            second = p1 ? best : p2 ? v : second;
+            si = p1 ? bi : p2 ? i : si;
+            best = p1 ? v : best;
+            bi = p1 ? i : bi;
+        }
+        known = 2;
+    };
+    scan();
+#pragma unroll
+    for (int q = 0; q < NS; ++q) slot_e[q] = -1, slot_key[q] = -INFINITY;
+    for (int j = 0; j < k; ++j) {
+        const float m = group_max<G>(best);
+        const bool mine = best == m && m > -INFINITY;
+        const unsigned all = __ballot_sync(kAll, mine);
+        if (all == 0) break;
+        const unsigned tied = G == 32 ? all : (all >> base) & ((1u << (G & 31)) - 1u);
+        int e;
+        if (__any_sync(kAll, (tied & (tied - 1)) != 0)) {   // equal keys in several lanes
+            e = group_min<G>(mine ? lg + G * bi : 1 << 20);
+        } else {
+            const int w = max(__ffs(tied) - 1, 0);
+            e = w + G * __shfl_sync(kAll, bi, base + w);
+        }
+        if (tied == 0) e = -1;
+        if (e >= 0 && (e & (G - 1)) == lg) {
+            mask |= 1u << (e / G);
+            best = second;
+            bi = si;
+            --known;
+        }
+#pragma unroll
+        for (int q = 0; q < NS; ++q)
+            if (j == q * G + lg) slot_e[q] = e, slot_key[q] = m;
+        if (__any_sync(kAll, known == 0)) {
+            const float b = best;
+            const int i0 = bi, n0 = known;
+            float s2 = second;
+            int s0 = si;
+            scan();
+            if (n0 != 0) best = b, bi = i0, known = n0, second = s2, si = s0;
         }
     }
-    auto flush = [&]() {
-        const int64_t row = (int64_t)w + s;
+    return mask;
+}
+
+// Joins the warps of the CTA: sum of `v` over the groups of every warp, in warp order, for the lanes' experts.
+template <int G>
+__device__ __forceinline__ float over_groups(float v) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            if (e < p.E) {
-                p.part.prob[row * p.E + e] = prob[i];
-                p.part.count[row * p.E + e] = cnt[i];
+    for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+template <class L, int NI, int G, bool kLoss, bool kGiven>
+__global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ RouterParams p) {
+    extern __shared__ float joined[];   // kLoss: [warps][E] probabilities, then counts
+    __shared__ float sz[kWarps];
+    __shared__ int sn[kWarps];
+    constexpr int kGroups = 32 / G;                      // tokens of a warp at a time
+    constexpr int NS = G == 32 ? 1 : 32 / G;             // slots of a lane (k <= 32)
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane & (G - 1), grp = lane / G;
+    const int E = p.E, k = p.k;
+    const int t0 = (int)min((int64_t)blockIdx.x * p.chunk, (int64_t)p.T), t1 = (int)min((int64_t)t0 + p.chunk, (int64_t)p.T);
+    if (kLoss && blockIdx.x == 0 && threadIdx.x == 0) *p.part.ticket = 0;   // for the next kernel
+    float bias[NI];
+    if (!kGiven) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) bias[i] = p.bias && lg + G * i < E ? p.bias[lg + G * i] : 0.0f;
+    }
+    for (int a = t0; a < t1;) {
+        const Cut cut = kLoss ? cut_at(p.seq_offsets, p.S, a, t1) : Cut{0, t1, true};
+        float prob[kLoss ? NI : 1];
+        int cnt[kLoss ? NI : 1];
+        float zsum = 0.0f;
+        int tokens = 0;
+        if (kLoss) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) prob[i] = 0.0f, cnt[i] = 0;
+        }
+        for (int tb = a + warp * kGroups; tb < cut.end; tb += kWarps * kGroups) {
+            const int t = tb + grp;
+            const bool on = t < cut.end;
+            float l[NI];
+            load_row<L, NI, G>(l, p.logits, p.ld, t, on, lg, E);
+            float m = -INFINITY;
+            if (kLoss || !p.renorm) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
+                m = group_max<G>(m);
             }
-            prob[i] = 0.0f;
-            cnt[i] = 0;
-        }
-        if (lane == 0) {
-            p.part.z[row] = zsum;
-            p.part.tokens[row] = tokens;
-        }
-        zsum = 0.0f;
-        tokens = 0;
-    };
-    for (int t = t0; t < t1; ++t) {
-        if (kLoss && p.seq_offsets && t >= s_end) {
-            flush();
-            s = find_seq(p.seq_offsets, p.S, t);
-            s_begin = s < p.S ? p.seq_offsets[s] : p.T;
-            s_end = s < p.S ? p.seq_offsets[s + 1] : p.T;
-        }
-        const L *row = static_cast<const L *>(p.logits) + t * p.ld;
-        float l[NI];
-        uint32_t key[NI];
-        float m = -INFINITY;
+            uint32_t mask = 0;   // bit i: expert lg + G i is chosen
+            if (kGiven) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            l[i] = open_logit(e < p.E ? to_f32(row[e]) : -INFINITY);
-            m = fmaxf(m, l[i]);
-            if (!kGiven) key[i] = e < p.E ? order_key(p.bias ? l[i] + p.bias[e] : l[i]) : 0u;
-            if (!kGiven && !(l[i] > -INFINITY)) key[i] = 0u;
-        }
-        m = warp_max(m);
-        uint32_t mask = 0;   // bit i: expert lane + 32 i is chosen
-        if (kGiven) {
-            const int idx = lane < p.k ? p.topk_idx[(int64_t)t * p.k + lane] : -1;
-            for (int j = 0; j < p.k; ++j) {
-                const int e = __shfl_sync(kAll, idx, j);
-                if (e >= 0 && e < p.E && (e & 31) == lane) mask |= 1u << (e >> 5);
-            }
-        } else {
-            int my_e = -1;          // lane j: slot j
-            float my_l = -INFINITY;
-            for (int j = 0; j < p.k; ++j) {
-                uint32_t best = 0;
-#pragma unroll
-                for (int i = 0; i < NI; ++i) best = max(best, key[i]);
-                const uint32_t top = __reduce_max_sync(kAll, best);
-                if (top == 0) break;
-                int e = 1 << 20;
-                float v = 0.0f;
-#pragma unroll
-                for (int i = NI - 1; i >= 0; --i)
-                    if (key[i] == top) e = lane + 32 * i, v = l[i];
-                const int win = __reduce_min_sync(kAll, (unsigned)e);
-                v = __shfl_sync(kAll, v, win & 31);
-                if (e == win) {
-                    mask |= 1u << (win >> 5);
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if (i == (win >> 5)) key[i] = 0u;
-                }
-                if (lane == j) my_e = win, my_l = v;
-            }
-            // weights of the chosen
-            float wgt = 0.0f;
-            if (p.renorm || p.sigmoid) {
-                const float top_l = warp_max(my_l);
-                if (my_e >= 0)
-                    wgt = !p.sigmoid ? expf(my_l - top_l) : sigmoid_scaled(my_l, p.renorm ? fminf(top_l, 0.0f) : 0.0f);
-                if (p.renorm) {
-                    const float sum = warp_sum(wgt);
-                    wgt = sum > 0.0f ? wgt / sum : 0.0f;
+                for (int q = 0; q < NS; ++q) {
+                    if (q * G >= k) break;
+                    const int j0 = q * G + lg;
+                    const int idx = on && j0 < k ? p.topk_idx[(int64_t)t * k + j0] : -1;
+                    for (int j = 0; j < min(G, k - q * G); ++j) {
+                        const int e = __shfl_sync(kAll, idx, j, G);
+                        if (e >= 0 && e < E && (e & (G - 1)) == lg) mask |= 1u << (e / G);
+                    }
                 }
             } else {
+                int my_e[NS];
+                float my_l[NS], key[NI];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) key[i] = fmaxf(l[i] + bias[i], -INFINITY);   // closed stays -inf, NaN closes
+                if (p.bias) {   // -inf + inf is NaN, closed by the line above; nothing else opens a closed logit
+                    mask = choose<NI, G, NS>(key, k, lg, my_e, my_l);
+#pragma unroll
+                    for (int q = 0; q < NS; ++q)
+                        if (my_e[q] >= 0)
+                            my_l[q] = open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + my_e[q]]));
+                } else {
+                    mask = choose<NI, G, NS>(l, k, lg, my_e, my_l);
+                }
+                // weights of the chosen
+                float wgt[NS], f = p.scale;
+                if (p.renorm) {
+                    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < NS; ++q)
+                        if (my_e[q] >= 0) top = fmaxf(top, my_l[q]);
+                    top = group_max<G>(top);
+#pragma unroll
+                    for (int q = 0; q < NS; ++q) {
+                        wgt[q] = my_e[q] < 0   ? 0.0f
+                                 : p.sigmoid ? sigmoid_scaled(my_l[q], fminf(top, 0.0f))
+                                             : exp_of(my_l[q] - top);
+                        sum += wgt[q];
+                    }
+                    sum = group_sum<G>(sum);
+                    f = sum > 0.0f ? __fdividef(f, sum) : 0.0f;
+                } else if (p.sigmoid) {
+#pragma unroll
+                    for (int q = 0; q < NS; ++q) wgt[q] = my_e[q] < 0 ? 0.0f : sigmoid_scaled(my_l[q], 0.0f);
+                } else {
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) sum += l[i] > -INFINITY ? exp_of(l[i] - m) : 0.0f;
+                    sum = group_sum<G>(sum);
+                    f = sum > 0.0f ? __fdividef(f, sum) : 0.0f;
+#pragma unroll
+                    for (int q = 0; q < NS; ++q) wgt[q] = my_e[q] < 0 ? 0.0f : exp_of(my_l[q] - m);
+                }
+#pragma unroll
+                for (int q = 0; q < NS; ++q) {
+                    const int j = q * G + lg;
+                    if (on && j < k) {
+                        p.topk_idx[(int64_t)t * k + j] = my_e[q];
+                        p.topk_weights[(int64_t)t * k + j] = wgt[q] * f;
+                    }
+                }
+            }
+            if (kLoss && cut.inside) {
+                float q[NI], z = 0.0f;
+                const bool real = m > -INFINITY;
+                const float m0 = real ? m : 0.0f, ms = fminf(m0, 0.0f);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    q[i] = !(l[i] > -INFINITY) ? 0.0f : p.sigmoid ? sigmoid_scaled(l[i], ms) : exp_of(l[i] - m0);
+                    z += q[i];
+                }
+                z = group_sum<G>(z);
+                const float inv = real ? __fdividef(1.0f, z) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    prob[i] = fmaf(q[i], inv, prob[i]);
+                    cnt[i] += real ? (mask >> i) & 1 : 0;
+                }
+                if (real && lg == 0) {
+                    const float lse = m + logf(z);
+                    zsum += p.sigmoid ? 0.0f : lse * lse;
+                    ++tokens;
+                }
+            }
+        }
+        if (kLoss) {
+            int *counts = reinterpret_cast<int *>(joined + kWarps * E);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int e = lg + G * i;
+                const float pr = over_groups<G>(prob[i]);
+                int c = cnt[i];
+#pragma unroll
+                for (int o = G; o < 32; o <<= 1) c += __shfl_xor_sync(kAll, c, o);
+                if (e < E && grp == 0) joined[warp * E + e] = pr, counts[warp * E + e] = c;
+            }
+            zsum = warp_sum(zsum);
+            tokens = __reduce_add_sync(kAll, tokens);
+            if (lane == 0) sz[warp] = zsum, sn[warp] = tokens;
+            __syncthreads();
+            const int64_t row = (int64_t)blockIdx.x + cut.s;
+            for (int e = threadIdx.x; e < E; e += kThreads) {
+                float pr = 0.0f;
+                int c = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) pr += joined[w * E + e], c += counts[w * E + e];
+                p.part.prob[row * E + e] = pr;
+                p.part.count[row * E + e] = c;
+            }
+            if (threadIdx.x == 0) {
                 float z = 0.0f;
+                int n = 0;
 #pragma unroll
-                for (int i = 0; i < NI; ++i) z += l[i] > -INFINITY ? expf(l[i] - m) : 0.0f;
-                z = warp_sum(z);
-                if (my_e >= 0) wgt = expf(my_l - m) / z;
+                for (int w = 0; w < kWarps; ++w) z += sz[w], n += sn[w];
+                p.part.z[row] = z;   // a gap before sequence s writes zeros where s, if it starts in this CTA, writes next
+                p.part.tokens[row] = n;
             }
-            if (lane < p.k) {
-                p.topk_idx[(int64_t)t * p.k + lane] = my_e;
-                p.topk_weights[(int64_t)t * p.k + lane] = wgt * p.scale;
-            }
+            __syncthreads();
         }
-        if (kLoss && m > -INFINITY && t >= s_begin && t < s_end) {
-            float q[NI], z = 0.0f;
-            const float ms = fminf(m, 0.0f);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                q[i] = !(l[i] > -INFINITY) ? 0.0f : p.sigmoid ? sigmoid_scaled(l[i], ms) : expf(l[i] - m);
-                z += q[i];
-            }
-            z = warp_sum(z);
-            const float inv = 1.0f / z;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                prob[i] += q[i] * inv;
-                cnt[i] += (mask >> i) & 1;
-            }
-            const float lse = m + logf(z);
-            zsum += p.sigmoid ? 0.0f : lse * lse;
-            ++tokens;
-        }
+        a = cut.end;
     }
-    if (kLoss) flush();
 }
 
 struct SumParams {
@@ -216,66 +375,83 @@ struct SumParams {
     int32_t *counts;
     float *prob_mean;
     int32_t *seq_tokens;
+    float *loss;
     int T, E, k, S, chunk;
+    float alpha, beta;
 };
 
-// One CTA per sequence: its rows summed in order, then its share of the losses.
-__global__ void __launch_bounds__(kThreads) router_seq_kernel(const SumParams p) {
-    __shared__ float red[kWarpsPerCta];
-    const int s = blockIdx.x;
+// CTA (x, s): 32 experts of sequence s, its rows summed in order (a thread takes every 8th row, then the 8 are added in
+// turn).  The last CTA to finish adds up the losses.
+__global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_constant__ SumParams p) {
+    __shared__ float sp[kWarps][32];
+    __shared__ int sc[kWarps][32];
+    __shared__ float sz[kWarps];
+    __shared__ int sn[kWarps];
+    __shared__ bool last;
+    const int s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
     const int a = p.seq_offsets ? max(0, min(p.seq_offsets[s], p.T)) : 0;
     const int b = p.seq_offsets ? max(0, min(p.seq_offsets[s + 1], p.T)) : p.T;
     const int w0 = a / p.chunk, w1 = b > a ? (b - 1) / p.chunk + 1 : w0;
-    int n = 0;
-    float z = 0.0f;
-    for (int w = w0; w < w1; ++w) {
+    float pr = 0.0f, z = 0.0f;
+    int c = 0, n = 0;
+#pragma unroll 4
+    for (int w = w0 + warp; w < w1; w += kWarps)
+        if (e < p.E) {
+            pr += p.part.prob[(int64_t)(w + s) * p.E + e];
+            c += p.part.count[(int64_t)(w + s) * p.E + e];
+        }
+    for (int w = w0 + threadIdx.x; w < w1; w += kThreads) {
         n += p.part.tokens[w + s];
         z += p.part.z[w + s];
     }
-    const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-    float bal = 0.0f;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-        float ps = 0.0f;
-        int c = 0;
-        for (int w = w0; w < w1; ++w) {
-            ps += p.part.prob[(int64_t)(w + s) * p.E + e];
-            c += p.part.count[(int64_t)(w + s) * p.E + e];
+    sp[warp][lane] = pr;
+    sc[warp][lane] = c;
+    z = warp_sum(z);
+    n = __reduce_add_sync(kAll, n);
+    if (lane == 0) sz[warp] = z, sn[warp] = n;
+    __syncthreads();
+    if (warp == 0) {
+        pr = 0.0f, z = 0.0f, c = 0, n = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) pr += sp[w][lane], c += sc[w][lane], z += sz[w], n += sn[w];
+        const float mean = n > 0 ? pr / (float)n : 0.0f;
+        if (e < p.E) {
+            p.counts[(int64_t)s * p.E + e] = c;
+            p.prob_mean[(int64_t)s * p.E + e] = mean;
         }
-        p.counts[(int64_t)s * p.E + e] = c;
-        p.prob_mean[(int64_t)s * p.E + e] = ps * inv;
-        bal += (float)c * (ps * inv);
+        const float bal = warp_sum(e < p.E ? (float)c * mean : 0.0f);
+        if (lane == 0) {
+            p.part.seq_bal[s * gridDim.x + blockIdx.x] = n > 0 ? bal * (float)p.E / ((float)p.k * (float)n) : 0.0f;
+            if (blockIdx.x == 0) p.seq_tokens[s] = n, p.part.seq_z[s] = z;
+            __threadfence();
+            last = atomicAdd(p.part.ticket, 1) == (int)(gridDim.x * gridDim.y) - 1;
+        }
     }
-    bal = block_sum<kWarpsPerCta>(bal, red);
-    if (threadIdx.x == 0) {
-        p.seq_tokens[s] = n;
-        p.part.seq_bal[s] = bal * ((float)p.E / (float)p.k) * inv;
-        p.part.seq_z[s] = z;
-    }
-}
-
-__global__ void router_loss_kernel(const Partials part, int S, int32_t *seq_tokens, float alpha, float beta, float *loss) {
-    // one warp, sequences in a fixed order
-    const int lane = threadIdx.x;
-    float bal = 0.0f, z = 0.0f;
-    int used = 0, n = 0;
-    for (int s = lane; s < S; s += 32) {
-        bal += part.seq_bal[s];
-        z += part.seq_z[s];
-        used += seq_tokens[s] > 0;
-        n += seq_tokens[s];
+    __syncthreads();
+    if (!last || warp != 0) return;
+    __threadfence();
+    float bal = 0.0f;
+    int used = 0;
+    z = 0.0f, n = 0;
+    for (int i = lane; i < p.S * (int)gridDim.x; i += 32) bal += __ldcg(p.part.seq_bal + i);
+    for (int i = lane; i < p.S; i += 32) {
+        const int ns = __ldcg(p.seq_tokens + i);
+        z += __ldcg(p.part.seq_z + i);
+        used += ns > 0;
+        n += ns;
     }
     bal = warp_sum(bal);
     z = warp_sum(z);
     used = __reduce_add_sync(kAll, used);
     n = __reduce_add_sync(kAll, n);
     if (lane == 0) {
-        bal = used > 0 ? alpha * bal / (float)used : 0.0f;
-        z = n > 0 ? beta * z / (float)n : 0.0f;
-        loss[0] = bal + z;
-        loss[1] = bal;
-        loss[2] = z;
-        seq_tokens[S] = used;
-        seq_tokens[S + 1] = n;
+        bal = used > 0 ? p.alpha * bal / (float)used : 0.0f;
+        z = n > 0 ? p.beta * z / (float)n : 0.0f;
+        p.loss[0] = bal + z;
+        p.loss[1] = bal;
+        p.loss[2] = z;
+        p.seq_tokens[p.S] = used;
+        p.seq_tokens[p.S + 1] = n;
     }
 }
 
@@ -288,103 +464,153 @@ struct RouterBwd {
     const float *d_loss;
     void *d_logits;
     int64_t ld_d;
-    int T, E, k, S, sigmoid, renorm;
+    int T, E, k, S, chunk, sigmoid, renorm;
     float scale, alpha, beta;
 };
 
-template <class L, int NI>
-__global__ void __launch_bounds__(kThreads) router_bwd_kernel(const RouterBwd p) {
-    const int lane = threadIdx.x & 31;
-    const int t = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
-    if (t >= p.T) return;
-    const L *row = static_cast<const L *>(p.logits) + (int64_t)t * p.ld;
-    float l[NI], q[NI], d[NI], m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = open_logit(e < p.E ? to_f32(row[e]) : -INFINITY);
-        m = fmaxf(m, l[i]);
-        d[i] = 0.0f;
-    }
-    m = warp_max(m);
-    const bool real = m > -INFINITY;
-    const float ms = fminf(m, 0.0f);
-    float z = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        q[i] = !(l[i] > -INFINITY) ? 0.0f : p.sigmoid ? sigmoid_scaled(l[i], ms) : expf(l[i] - m);
-        z += q[i];
-    }
-    z = warp_sum(z);
-    const float inv = real ? 1.0f / z : 0.0f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) q[i] *= inv;
-    if (p.d_loss && real) {
-        int s = 0;
-        bool inside = true;
-        if (p.seq_offsets) {
-            s = find_seq(p.seq_offsets, p.S, t);
-            inside = s < p.S && t >= p.seq_offsets[s];
-        }
-        const int n = inside ? p.seq_tokens[s] : 0;
+template <class L, int NI, int G>
+__global__ void __launch_bounds__(kThreads) router_bwd_kernel(const __grid_constant__ RouterBwd p) {
+    extern __shared__ float scatter[];   // [warps][groups][E]: gradients of the chosen logits, zero between tokens
+    constexpr int kGroups = 32 / G;
+    constexpr int NS = G == 32 ? 1 : 32 / G;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane & (G - 1), grp = lane / G;
+    const int E = p.E, k = p.k;
+    float *mine = scatter + (warp * kGroups + grp) * E;
+    if (p.d_weights)
+        for (int e = lg; e < E; e += G) mine[e] = 0.0f;
+    __syncwarp();
+    const int t0 = (int)min((int64_t)blockIdx.x * p.chunk, (int64_t)p.T), t1 = (int)min((int64_t)t0 + p.chunk, (int64_t)p.T);
+    for (int a = t0; a < t1;) {
+        const Cut cut = cut_at(p.seq_offsets, p.S, a, t1);
+        const int n = p.d_loss && cut.inside && cut.s < p.S ? p.seq_tokens[cut.s] : 0;
+        float c[NI], zc = 0.0f;   // the balance loss's pull on each expert's probability, the z loss's on log-sum-exp
         if (n > 0) {
             const float g = *p.d_loss;
-            const float c0 = g * p.alpha * (float)p.E / ((float)p.k * (float)n * (float)n * (float)p.seq_tokens[p.S]);
-            const float zc = p.sigmoid ? 0.0f : g * 2.0f * p.beta / (float)p.seq_tokens[p.S + 1] * (m + logf(z));
-            float dot = 0.0f;
+            const float c0 = g * p.alpha * (float)E / ((float)k * (float)n * (float)n * (float)p.seq_tokens[p.S]);
+            zc = p.sigmoid ? 0.0f : g * 2.0f * p.beta / (float)p.seq_tokens[p.S + 1];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int e = lane + 32 * i;
-                d[i] = e < p.E ? c0 * (float)p.counts[(int64_t)s * p.E + e] : 0.0f;
-                dot += d[i] * q[i];
-            }
-            dot = warp_sum(dot);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                d[i] = q[i] * (d[i] - dot + zc);
-                if (p.sigmoid && l[i] > -INFINITY) d[i] /= 1.0f + expf(l[i]);   // ds/dl = s (1 - s)
-            }
+            for (int i = 0; i < NI; ++i) c[i] = lg + G * i < E ? c0 * (float)p.counts[(int64_t)cut.s * E + lg + G * i] : 0.0f;
         }
-    }
-    if (p.d_weights) {
-        int idx = lane < p.k ? p.topk_idx[(int64_t)t * p.k + lane] : -1;
-        if (idx >= p.E) idx = -1;
-        const float ls = idx >= 0 ? open_logit(to_f32(row[idx])) : -INFINITY;
-        const float dw = idx >= 0 ? p.d_weights[(int64_t)t * p.k + lane] * p.scale : 0.0f;
-        const bool on = ls > -INFINITY;
-        float add = 0.0f, dot = 0.0f;   // gradient of slot `lane`'s logit; what every logit gets times its probability
-        if (p.renorm) {
-            const float top = warp_max(ls);
-            float v = !on ? 0.0f : p.sigmoid ? sigmoid_scaled(ls, fminf(top, 0.0f)) : expf(ls - top);
-            const float sum = warp_sum(v);
-            v = sum > 0.0f ? v / sum : 0.0f;
-            add = v * (dw - warp_sum(v * dw));
-            if (p.sigmoid && on) add /= 1.0f + expf(ls);
-        } else if (p.sigmoid) {
-            if (on) {
-                const float v = sigmoid_scaled(ls, 0.0f);
-                add = v * dw / (1.0f + expf(ls));
-            }
-        } else if (real) {
-            const float v = on ? expf(ls - m) * inv : 0.0f;
-            dot = warp_sum(v * dw);
-            add = v * dw;
-        }
+        const bool dense = n > 0 || (p.d_weights && !p.renorm && !p.sigmoid);   // every probability is needed
+        for (int tb = a + warp * kGroups; tb < cut.end; tb += kWarps * kGroups) {
+            const int t = tb + grp;
+            const bool on = t < cut.end;
+            float l[NI], d[NI], q[NI];
+            load_row<L, NI, G>(l, p.logits, p.ld, t, on, lg, E);
+            // the chosen slots' part
+            float add[NS], ls[NS], dw[NS], dot = 0.0f;
+            int idx[NS];
+            if (p.d_weights) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) d[i] -= q[i] * dot;
-        for (int j = 0; j < p.k; ++j) {
-            const int e = __shfl_sync(kAll, idx, j);
-            const float v = __shfl_sync(kAll, add, j);
+                for (int s = 0; s < NS; ++s) {
+                    const int j = s * G + lg;
+                    idx[s] = on && j < k ? p.topk_idx[(int64_t)t * k + j] : -1;
+                    if (idx[s] >= E) idx[s] = -1;
+                    ls[s] = -INFINITY;
+                    dw[s] = 0.0f;
+                    if (idx[s] >= 0) {
+                        ls[s] = open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + idx[s]]));
+                        dw[s] = p.d_weights[(int64_t)t * k + j] * p.scale;
+                    }
+                }
+            }
+            float m = 0.0f, inv = 0.0f;
+            bool real = false;
+            if (dense) {
+                m = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
+                m = group_max<G>(m);
+                real = m > -INFINITY;
+                m = real ? m : 0.0f;
+                const float ms = fminf(m, 0.0f);
+                float z = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    q[i] = !(l[i] > -INFINITY) ? 0.0f : p.sigmoid ? sigmoid_scaled(l[i], ms) : exp_of(l[i] - m);
+                    z += q[i];
+                }
+                z = group_sum<G>(z);
+                inv = real ? __fdividef(1.0f, z) : 0.0f;
+                const float lse = real ? m + logf(z) : 0.0f;
+                float cq = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    q[i] *= inv;
+                    if (n > 0) cq = fmaf(c[i], q[i], cq);
+                }
+                if (n > 0) {
+                    cq = zc * lse - group_sum<G>(cq);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        d[i] = q[i] * (c[i] + cq);
+                        if (p.sigmoid) d[i] *= sigmoid_slope(l[i]);   // ds/dl = s (1 - s)
+                    }
+                }
+            }
+            if (n == 0) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) d[i] = 0.0f;
+            }
+            if (p.d_weights) {
+                if (p.renorm) {
+                    float top = -INFINITY, sum = 0.0f, mean = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) top = fmaxf(top, ls[s]);
+                    top = group_max<G>(top);
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        add[s] = !(ls[s] > -INFINITY) ? 0.0f
+                                 : p.sigmoid        ? sigmoid_scaled(ls[s], fminf(top, 0.0f))
+                                                    : exp_of(ls[s] - top);
+                        sum += add[s];
+                    }
+                    sum = group_sum<G>(sum);
+                    const float r = sum > 0.0f ? __fdividef(1.0f, sum) : 0.0f;
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        add[s] *= r;
+                        mean = fmaf(add[s], dw[s], mean);
+                    }
+                    mean = group_sum<G>(mean);
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        add[s] *= dw[s] - mean;
+                        if (p.sigmoid && ls[s] > -INFINITY) add[s] *= sigmoid_slope(ls[s]);
+                    }
+                } else if (p.sigmoid) {
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+                        add[s] = ls[s] > -INFINITY ? sigmoid_scaled(ls[s], 0.0f) * sigmoid_slope(ls[s]) * dw[s] : 0.0f;
+                } else {
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        add[s] = real && ls[s] > -INFINITY ? exp_of(ls[s] - m) * inv * dw[s] : 0.0f;
+                        dot += add[s];
+                    }
+                    dot = group_sum<G>(dot);
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) d[i] = fmaf(-q[i], dot, d[i]);
+                }
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+                    if (idx[s] >= 0) mine[idx[s]] = add[s];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (lg + G * i < E) d[i] += mine[lg + G * i];
+                __syncwarp();
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+                    if (idx[s] >= 0) mine[idx[s]] = 0.0f;
+            }
+            L *out = static_cast<L *>(p.d_logits) + (int64_t)t * p.ld_d;
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-                if (e == lane + 32 * i) d[i] += v;
+                if (on && lg + G * i < E) out[lg + G * i] = from_f32<L>(d[i]);
+            __syncwarp();
         }
-    }
-    L *out = static_cast<L *>(p.d_logits) + (int64_t)t * p.ld_d;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 32 * i;
-        if (e < p.E) out[e] = from_f32<L>(d[i]);
+        a = cut.end;
     }
 }
 
@@ -399,11 +625,15 @@ bool valid(const moe_router_config *c) {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-int loss_warps(int T) { return std::min(std::max(T, 1), kMaxLossWarps); }
+// CTAs of a pass over T tokens, `most` at most and no more than give every warp a turn.
+int ctas_for(int T, int E, int most) {
+    const int per_cta = kWarps * (E <= 64 ? 4 : 1);
+    return std::min((std::max(T, 1) + per_cta - 1) / per_cta, most);
+}
 
 // Carves the workspace; returns its size.
 size_t carve(int E, int T, int S, char *base, Partials *out) {
-    const size_t rows = (size_t)loss_warps(T) + S;
+    const size_t rows = (size_t)ctas_for(T, E, kMaxLossCtas) + S;
     size_t o = 0;
     auto take = [&](size_t bytes) {
         char *at = base + o;
@@ -415,52 +645,67 @@ size_t carve(int E, int T, int S, char *base, Partials *out) {
     p.count = reinterpret_cast<int32_t *>(take(rows * E * 4));
     p.z = reinterpret_cast<float *>(take(rows * 4));
     p.tokens = reinterpret_cast<int32_t *>(take(rows * 4));
-    p.seq_bal = reinterpret_cast<float *>(take((size_t)S * 4));
+    p.seq_bal = reinterpret_cast<float *>(take((size_t)S * ((E + 31) / 32) * 4));
     p.seq_z = reinterpret_cast<float *>(take((size_t)S * 4));
+    p.ticket = reinterpret_cast<int *>(take(4));
     if (out) *out = p;
     return o;
 }
 
-template <class L, int NI>
-void launch_router(const RouterParams &p, bool loss, bool given, int warps, cudaStream_t s) {
-    const int ctas = (warps + kWarpsPerCta - 1) / kWarpsPerCta;
-    if (!loss) router_kernel<L, NI, false, false><<<ctas, kThreads, 0, s>>>(p);
-    else if (given) router_kernel<L, NI, true, true><<<ctas, kThreads, 0, s>>>(p);
-    else router_kernel<L, NI, true, false><<<ctas, kThreads, 0, s>>>(p);
+template <class L, int NI, int G>
+cudaError_t launch_router(const RouterParams &p, bool loss, bool given, int ctas, cudaStream_t s) {
+    const size_t smem = (size_t)kWarps * p.E * 8;
+    if (!loss) {
+        router_kernel<L, NI, G, false, false><<<ctas, kThreads, 0, s>>>(p);
+    } else if (given) {
+        static std::atomic<uint32_t> done{0};
+        const cudaError_t e = smem_limit_once((const void *)router_kernel<L, NI, G, true, true>, 65536, done);
+        if (e != cudaSuccess) return e;
+        router_kernel<L, NI, G, true, true><<<ctas, kThreads, smem, s>>>(p);
+    } else {
+        static std::atomic<uint32_t> done{0};
+        const cudaError_t e = smem_limit_once((const void *)router_kernel<L, NI, G, true, false>, 65536, done);
+        if (e != cudaSuccess) return e;
+        router_kernel<L, NI, G, true, false><<<ctas, kThreads, smem, s>>>(p);
+    }
+    return cudaGetLastError();
 }
 
-// Calls f with the number of experts per lane as a template argument.
+// Calls f with the lanes of a token and the experts of a lane as template arguments.
 template <class F>
-void by_experts(int E, F f) {
-    if (E <= 32) f.template run<1>();
-    else if (E <= 64) f.template run<2>();
-    else if (E <= 128) f.template run<4>();
-    else if (E <= 256) f.template run<8>();
-    else if (E <= 512) f.template run<16>();
-    else f.template run<32>();
+cudaError_t by_experts(int E, F f) {
+    if (E <= 8) return f.template run<1, 8>();
+    if (E <= 16) return f.template run<2, 8>();
+    if (E <= 32) return f.template run<4, 8>();
+    if (E <= 64) return f.template run<8, 8>();
+    if (E <= 128) return f.template run<4, 32>();
+    if (E <= 256) return f.template run<8, 32>();
+    if (E <= 512) return f.template run<16, 32>();
+    return f.template run<32, 32>();
 }
 
 struct RunRouter {
     const RouterParams &p;
     bool bf, loss, given;
-    int warps;
+    int ctas;
     cudaStream_t s;
-    template <int NI>
-    void run() const {
-        if (bf) launch_router<bf16, NI>(p, loss, given, warps, s);
-        else launch_router<float, NI>(p, loss, given, warps, s);
+    template <int NI, int G>
+    cudaError_t run() const {
+        return bf ? launch_router<bf16, NI, G>(p, loss, given, ctas, s) : launch_router<float, NI, G>(p, loss, given, ctas, s);
     }
 };
 
 struct RunBwd {
     const RouterBwd &p;
     bool bf;
+    int ctas;
     cudaStream_t s;
-    template <int NI>
-    void run() const {
-        const int ctas = (p.T + kWarpsPerCta - 1) / kWarpsPerCta;
-        if (bf) router_bwd_kernel<bf16, NI><<<ctas, kThreads, 0, s>>>(p);
-        else router_bwd_kernel<float, NI><<<ctas, kThreads, 0, s>>>(p);
+    template <int NI, int G>
+    cudaError_t run() const {
+        const size_t smem = p.d_weights ? (size_t)kWarps * (32 / G) * p.E * 4 : 0;   // at most 32 KB
+        if (bf) router_bwd_kernel<bf16, NI, G><<<ctas, kThreads, smem, s>>>(p);
+        else router_bwd_kernel<float, NI, G><<<ctas, kThreads, smem, s>>>(p);
+        return cudaGetLastError();
     }
 };
 
@@ -486,18 +731,20 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.scale = cfg->weight_scale;
     p.S = loss ? loss->num_seqs : 1;
     p.seq_offsets = loss ? loss->seq_offsets : nullptr;
-    p.chunk = loss ? (T + loss_warps(T) - 1) / loss_warps(T) : 1;
+    const int ctas = ctas_for(T, p.E, loss ? kMaxLossCtas : 1 << 30);
+    p.chunk = std::max(1, (T + ctas - 1) / ctas);
     if (loss) carve(p.E, T, p.S, static_cast<char *>(ws), &p.part);
     if (T > 0) {
-        by_experts(p.E, RunRouter{p, cfg->logits_dtype == MOE_DTYPE_BF16, loss != nullptr, given,
-                                  (T + p.chunk - 1) / p.chunk, s});
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        if (by_experts(p.E, RunRouter{p, cfg->logits_dtype == MOE_DTYPE_BF16, loss != nullptr, given,
+                                      (T + p.chunk - 1) / p.chunk, s}) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    } else if (loss && cudaMemsetAsync(p.part.ticket, 0, sizeof(int), s) != cudaSuccess) {
+        return MOE_ERR_CUDA;
     }
     if (loss) {
-        SumParams q{p.part, p.seq_offsets, loss->counts, loss->prob_mean, loss->seq_tokens, T, p.E, p.k, p.S,
-                    std::max(p.chunk, 1)};
-        router_seq_kernel<<<p.S, kThreads, 0, s>>>(q);
-        router_loss_kernel<<<1, 32, 0, s>>>(p.part, p.S, loss->seq_tokens, cfg->balance_coef, cfg->z_coef, loss->loss);
+        SumParams q{p.part, p.seq_offsets, loss->counts, loss->prob_mean, loss->seq_tokens, loss->loss, T, p.E, p.k, p.S,
+                    p.chunk, cfg->balance_coef, cfg->z_coef};
+        router_seq_kernel<<<dim3((p.E + 31) / 32, p.S), kThreads, 0, s>>>(q);
         if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
@@ -574,8 +821,12 @@ int moe_router_backward(const moe_router_config *cfg, int num_tokens, const void
     p.scale = cfg->weight_scale;
     p.alpha = cfg->balance_coef;
     p.beta = cfg->z_coef;
-    by_experts(p.E, RunBwd{p, cfg->logits_dtype == MOE_DTYPE_BF16, static_cast<cudaStream_t>(stream)});
-    return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    const int ctas = ctas_for(num_tokens, p.E, 152 * 8);
+    p.chunk = (num_tokens + ctas - 1) / ctas;
+    return by_experts(p.E, RunBwd{p, cfg->logits_dtype == MOE_DTYPE_BF16, (num_tokens + p.chunk - 1) / p.chunk,
+                                  static_cast<cudaStream_t>(stream)}) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 }  // extern "C"
