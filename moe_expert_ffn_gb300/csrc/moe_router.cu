@@ -5,9 +5,14 @@
 // Large batches are bound by instructions, not by the [T, E] logits: one pass
 // reads them once, and what counts is the choice.  A token belongs to a group
 // of 32 lanes (8 for E <= 64), lane l holding experts l, l + G, ...: coalesced
-// for any E and pitch.  Every lane finds the two largest of its keys in one
-// scan; a round of the choice is then one reduction over the lanes' best, and
-// the winner moves up its second.  Only a lane that won twice scans again.
+// for any E and pitch.  Keys are made whole numbers: the float's order in the
+// high bits, the expert, inverted, in the low ones.  So no two are equal, a
+// lane sorts its keys with minima and maxima alone, and a round of the choice
+// is one reduction over the lanes' heads, whose winner knows itself.  Whatever
+// f32 bits the expert's number displaced can matter only where two
+// neighbours in the result share all bits above: such a token (1 in some
+// hundreds; none with bf16 logits, which have no such bits) is chosen again
+// from the full keys.
 //
 // Losses: CTAs walk contiguous token ranges, cut where a sequence ends; within
 // a cut every lane sums its experts' probabilities in registers, the CTA's
@@ -139,64 +144,94 @@ __device__ __forceinline__ void load_row(float (&l)[NI], const void *logits, int
     for (int i = 0; i < NI; ++i) l[i] = on && lg + G * i < E ? open_logit(to_f32(row[lg + G * i])) : -INFINITY;
 }
 
-// The k largest keys of a group's token, ties to the lowest expert.  Slot j goes to lane j % G, place j / G: expert (-1:
-// nothing left) and key.  Returns the lane's chosen experts as bits.
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    if (G == 32) return __reduce_max_sync(kAll, v);
+#pragma unroll
+    for (int o = G / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+
+// Sorts in descending order by compare-exchanges (merge-exchange network for NI a power of two).
+template <int NI>
+__device__ __forceinline__ void sort_down(uint32_t (&v)[NI]) {
+#pragma unroll
+    for (int p = NI / 2; p > 0; p /= 2) {
+#pragma unroll
+        for (int q = NI / 2, r = 0, d = p; d > 0; d = q - p, q /= 2, r = p) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (i + d < NI && (i & p) == r) {
+                    const uint32_t a = v[i], b = v[i + d];
+                    v[i] = max(a, b);
+                    v[i + d] = min(a, b);
+                }
+            if (q < p) break;
+        }
+    }
+}
+
+// The k largest keys of a group's token from the full keys, one by one: the exact choice whatever the keys.
 template <int NI, int G, int NS>
-__device__ __forceinline__ uint32_t choose(const float (&key)[NI], int k, int lg, int (&slot_e)[NS], float (&slot_key)[NS]) {
-    const int base = threadIdx.x & 31 & ~(G - 1);
-    uint32_t mask = 0;
-    float best, second;
-    int bi, si, known;
-    auto scan = [&]() {   // strict comparisons: of equal keys the first stays in front
-        best = second = -INFINITY;
-        bi = si = 0;
+__device__ __noinline__ void choose_exact(const float (&key)[NI], int k, int lg, int (&slot_e)[NS]) {
+    uint32_t taken = 0;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const float v = (mask >> i) & 1 ? -INFINITY : key[i];
-            const bool p1 = v > best, p2 = v > second;
-            second = p1 ? best : p2 ? v : second;
-            si = p1 ? bi : p2 ? i : si;
-            best = p1 ? v : best;
-            bi = p1 ? i : bi;
-        }
-        known = 2;
-    };
-    scan();
-#pragma unroll
-    for (int q = 0; q < NS; ++q) slot_e[q] = -1, slot_key[q] = -INFINITY;
+    for (int q = 0; q < NS; ++q) slot_e[q] = -1;
     for (int j = 0; j < k; ++j) {
+        float best = -INFINITY;
+        int bi = 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (!((taken >> i) & 1) && key[i] > best) best = key[i], bi = i;   // of equal keys the first stays
         const float m = group_max<G>(best);
-        const bool mine = best == m && m > -INFINITY;
-        const unsigned all = __ballot_sync(kAll, mine);
-        if (all == 0) break;
-        const unsigned tied = G == 32 ? all : (all >> base) & ((1u << (G & 31)) - 1u);
-        int e;
-        if (__any_sync(kAll, (tied & (tied - 1)) != 0)) {   // equal keys in several lanes
-            e = group_min<G>(mine ? lg + G * bi : 1 << 20);
+        int e = group_min<G>(best == m && m > -INFINITY ? lg + G * bi : 1 << 20);
+        if (e < 1 << 20) {
+            if ((e & (G - 1)) == lg) taken |= 1u << (e / G);
         } else {
-            const int w = max(__ffs(tied) - 1, 0);
-            e = w + G * __shfl_sync(kAll, bi, base + w);
-        }
-        if (tied == 0) e = -1;
-        if (e >= 0 && (e & (G - 1)) == lg) {
-            mask |= 1u << (e / G);
-            best = second;
-            bi = si;
-            --known;
+            e = -1;
         }
 #pragma unroll
         for (int q = 0; q < NS; ++q)
-            if (j == q * G + lg) slot_e[q] = e, slot_key[q] = m;
-        if (__any_sync(kAll, known == 0)) {
-            const float b = best;
-            const int i0 = bi, n0 = known;
-            float s2 = second;
-            int s0 = si;
-            scan();
-            if (n0 != 0) best = b, bi = i0, known = n0, second = s2, si = s0;
+            if (j == q * G + lg) slot_e[q] = e;
+    }
+}
+
+// The k largest keys of a group's token, ties to the lowest expert.  Slot j goes to lane j % G, place j / G: its expert
+// (-1: nothing left).  `exact`: the keys' low bits that the expert's number takes are all zero.
+template <int NI, int G, int NS>
+__device__ __forceinline__ void choose(const float (&key)[NI], int k, int lg, bool exact, int (&slot_e)[NS]) {
+    constexpr uint32_t kLow = (uint32_t)(NI * G - 1);   // bits of an expert's number
+    constexpr uint32_t kOpen = 0x00800000u;             // the order of the smallest finite float
+    uint32_t v[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const uint32_t b = __float_as_uint(key[i] + 0.0f);   // -0 and 0 are equal
+        const uint32_t order = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+        v[i] = (order & ~kLow) | (kLow - (uint32_t)(lg + G * i));
+    }
+    sort_down(v);
+    uint32_t slot[NS];
+#pragma unroll
+    for (int q = 0; q < NS; ++q) slot[q] = 0;
+    uint32_t before = 0;
+    bool near = false;
+    for (int j = 0; j <= k; ++j) {   // the last round is the first one that stays outside
+        const uint32_t m = group_max<G>(v[0]);
+        near |= j > 0 && ((m ^ before) & ~kLow) == 0;
+        before = m < kOpen ? 0xFFFFFFFFu : m;   // closed ones are all alike
+        if (j == k) break;
+#pragma unroll
+        for (int q = 0; q < NS; ++q)
+            if (j == q * G + lg) slot[q] = m;
+        if (v[0] == m) {
+#pragma unroll
+            for (int i = 0; i + 1 < NI; ++i) v[i] = v[i + 1];
+            v[NI - 1] = 0;
         }
     }
-    return mask;
+#pragma unroll
+    for (int q = 0; q < NS; ++q) slot_e[q] = slot[q] < kOpen ? -1 : (int)(kLow - (slot[q] & kLow));
+    if (!exact && __any_sync(kAll, near)) choose_exact<NI, G, NS>(key, k, lg, slot_e);
 }
 
 // Joins the warps of the CTA: sum of `v` over the groups of every warp, in warp order, for the lanes' experts.
@@ -209,29 +244,31 @@ __device__ __forceinline__ float over_groups(float v) {
 
 template <class L, int NI, int G, bool kLoss, bool kGiven>
 __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ RouterParams p) {
-    extern __shared__ float joined[];   // kLoss: [warps][E] probabilities, then counts
+    extern __shared__ float joined[];   // kLoss: [warps][E] probabilities, [E] counts
     __shared__ float sz[kWarps];
     __shared__ int sn[kWarps];
     constexpr int kGroups = 32 / G;                      // tokens of a warp at a time
     constexpr int NS = G == 32 ? 1 : 32 / G;             // slots of a lane (k <= 32)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane & (G - 1), grp = lane / G;
     const int E = p.E, k = p.k;
+    int *counts = reinterpret_cast<int *>(joined + kWarps * E);
     const int t0 = (int)min((int64_t)blockIdx.x * p.chunk, (int64_t)p.T), t1 = (int)min((int64_t)t0 + p.chunk, (int64_t)p.T);
     if (kLoss && blockIdx.x == 0 && threadIdx.x == 0) *p.part.ticket = 0;   // for the next kernel
     float bias[NI];
-    if (!kGiven) {
+    if (!kGiven && p.bias) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) bias[i] = p.bias && lg + G * i < E ? p.bias[lg + G * i] : 0.0f;
+        for (int i = 0; i < NI; ++i) bias[i] = lg + G * i < E ? p.bias[lg + G * i] : 0.0f;
     }
     for (int a = t0; a < t1;) {
         const Cut cut = kLoss ? cut_at(p.seq_offsets, p.S, a, t1) : Cut{0, t1, true};
         float prob[kLoss ? NI : 1];
-        int cnt[kLoss ? NI : 1];
         float zsum = 0.0f;
         int tokens = 0;
         if (kLoss) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) prob[i] = 0.0f, cnt[i] = 0;
+            for (int i = 0; i < NI; ++i) prob[i] = 0.0f;
+            for (int e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
+            __syncthreads();
         }
         for (int tb = a + warp * kGroups; tb < cut.end; tb += kWarps * kGroups) {
             const int t = tb + grp;
@@ -239,50 +276,44 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
             float l[NI];
             load_row<L, NI, G>(l, p.logits, p.ld, t, on, lg, E);
             float m = -INFINITY;
-            if (kLoss || !p.renorm) {
+            if (kLoss || (!p.renorm && !p.sigmoid)) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
                 m = group_max<G>(m);
             }
-            uint32_t mask = 0;   // bit i: expert lg + G i is chosen
+            const bool real = m > -INFINITY;
+            const float m0 = real ? m : 0.0f;
+            int my_e[NS];
             if (kGiven) {
 #pragma unroll
                 for (int q = 0; q < NS; ++q) {
-                    if (q * G >= k) break;
-                    const int j0 = q * G + lg;
-                    const int idx = on && j0 < k ? p.topk_idx[(int64_t)t * k + j0] : -1;
-                    for (int j = 0; j < min(G, k - q * G); ++j) {
-                        const int e = __shfl_sync(kAll, idx, j, G);
-                        if (e >= 0 && e < E && (e & (G - 1)) == lg) mask |= 1u << (e / G);
-                    }
+                    const int j = q * G + lg;
+                    my_e[q] = on && j < k ? p.topk_idx[(int64_t)t * k + j] : -1;
+                    if (my_e[q] >= E) my_e[q] = -1;
                 }
             } else {
-                int my_e[NS];
-                float my_l[NS], key[NI];
+                if (p.bias) {
+                    float key[NI];   // closed stays -inf, NaN (also -inf + inf) closes
 #pragma unroll
-                for (int i = 0; i < NI; ++i) key[i] = fmaxf(l[i] + bias[i], -INFINITY);   // closed stays -inf, NaN closes
-                if (p.bias) {   // -inf + inf is NaN, closed by the line above; nothing else opens a closed logit
-                    mask = choose<NI, G, NS>(key, k, lg, my_e, my_l);
-#pragma unroll
-                    for (int q = 0; q < NS; ++q)
-                        if (my_e[q] >= 0)
-                            my_l[q] = open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + my_e[q]]));
+                    for (int i = 0; i < NI; ++i) key[i] = fmaxf(l[i] + bias[i], -INFINITY);
+                    choose<NI, G, NS>(key, k, lg, false, my_e);
                 } else {
-                    mask = choose<NI, G, NS>(l, k, lg, my_e, my_l);
+                    choose<NI, G, NS>(l, k, lg, sizeof(L) == 2, my_e);
                 }
                 // weights of the chosen
-                float wgt[NS], f = p.scale;
+                float wgt[NS], my_l[NS], f = p.scale;
+#pragma unroll
+                for (int q = 0; q < NS; ++q)
+                    my_l[q] = my_e[q] < 0 ? -INFINITY
+                                          : open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + my_e[q]]));
                 if (p.renorm) {
                     float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-                    for (int q = 0; q < NS; ++q)
-                        if (my_e[q] >= 0) top = fmaxf(top, my_l[q]);
+                    for (int q = 0; q < NS; ++q) top = fmaxf(top, my_l[q]);
                     top = group_max<G>(top);
 #pragma unroll
                     for (int q = 0; q < NS; ++q) {
-                        wgt[q] = my_e[q] < 0   ? 0.0f
-                                 : p.sigmoid ? sigmoid_scaled(my_l[q], fminf(top, 0.0f))
-                                             : exp_of(my_l[q] - top);
+                        wgt[q] = my_e[q] < 0 ? 0.0f : p.sigmoid ? sigmoid_scaled(my_l[q], fminf(top, 0.0f)) : exp_of(my_l[q] - top);
                         sum += wgt[q];
                     }
                     sum = group_sum<G>(sum);
@@ -293,11 +324,11 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
                 } else {
                     float sum = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) sum += l[i] > -INFINITY ? exp_of(l[i] - m) : 0.0f;
+                    for (int i = 0; i < NI; ++i) sum += exp_of(l[i] - m0);
                     sum = group_sum<G>(sum);
                     f = sum > 0.0f ? __fdividef(f, sum) : 0.0f;
 #pragma unroll
-                    for (int q = 0; q < NS; ++q) wgt[q] = my_e[q] < 0 ? 0.0f : exp_of(my_l[q] - m);
+                    for (int q = 0; q < NS; ++q) wgt[q] = my_e[q] < 0 ? 0.0f : exp_of(my_l[q] - m0);
                 }
 #pragma unroll
                 for (int q = 0; q < NS; ++q) {
@@ -310,20 +341,19 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
             }
             if (kLoss && cut.inside) {
                 float q[NI], z = 0.0f;
-                const bool real = m > -INFINITY;
-                const float m0 = real ? m : 0.0f, ms = fminf(m0, 0.0f);
+                const float ms = fminf(m0, 0.0f);
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    q[i] = !(l[i] > -INFINITY) ? 0.0f : p.sigmoid ? sigmoid_scaled(l[i], ms) : exp_of(l[i] - m0);
+                for (int i = 0; i < NI; ++i) {   // a closed logit's score comes out 0
+                    q[i] = p.sigmoid ? sigmoid_scaled(l[i], ms) : exp_of(l[i] - m0);
                     z += q[i];
                 }
                 z = group_sum<G>(z);
                 const float inv = real ? __fdividef(1.0f, z) : 0.0f;
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    prob[i] = fmaf(q[i], inv, prob[i]);
-                    cnt[i] += real ? (mask >> i) & 1 : 0;
-                }
+                for (int i = 0; i < NI; ++i) prob[i] = fmaf(q[i], inv, prob[i]);
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+                    if (real && my_e[s] >= 0) atomicAdd(counts + my_e[s], 1);   // whole numbers: the order does not matter
                 if (real && lg == 0) {
                     const float lse = m + logf(z);
                     zsum += p.sigmoid ? 0.0f : lse * lse;
@@ -332,15 +362,11 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
             }
         }
         if (kLoss) {
-            int *counts = reinterpret_cast<int *>(joined + kWarps * E);
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int e = lg + G * i;
                 const float pr = over_groups<G>(prob[i]);
-                int c = cnt[i];
-#pragma unroll
-                for (int o = G; o < 32; o <<= 1) c += __shfl_xor_sync(kAll, c, o);
-                if (e < E && grp == 0) joined[warp * E + e] = pr, counts[warp * E + e] = c;
+                if (e < E && grp == 0) joined[warp * E + e] = pr;
             }
             zsum = warp_sum(zsum);
             tokens = __reduce_add_sync(kAll, tokens);
@@ -349,11 +375,10 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
             const int64_t row = (int64_t)blockIdx.x + cut.s;
             for (int e = threadIdx.x; e < E; e += kThreads) {
                 float pr = 0.0f;
-                int c = 0;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) pr += joined[w * E + e], c += counts[w * E + e];
+                for (int w = 0; w < kWarps; ++w) pr += joined[w * E + e];
                 p.part.prob[row * E + e] = pr;
-                p.part.count[row * E + e] = c;
+                p.part.count[row * E + e] = counts[e];
             }
             if (threadIdx.x == 0) {
                 float z = 0.0f;
@@ -527,7 +552,7 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const __grid_const
                 float z = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    q[i] = !(l[i] > -INFINITY) ? 0.0f : p.sigmoid ? sigmoid_scaled(l[i], ms) : exp_of(l[i] - m);
+                    q[i] = p.sigmoid ? sigmoid_scaled(l[i], ms) : exp_of(l[i] - m);   // 0 where closed
                     z += q[i];
                 }
                 z = group_sum<G>(z);
@@ -654,18 +679,12 @@ size_t carve(int E, int T, int S, char *base, Partials *out) {
 
 template <class L, int NI, int G>
 cudaError_t launch_router(const RouterParams &p, bool loss, bool given, int ctas, cudaStream_t s) {
-    const size_t smem = (size_t)kWarps * p.E * 8;
+    const size_t smem = (size_t)(kWarps + 1) * p.E * 4;   // at most 36 KB
     if (!loss) {
         router_kernel<L, NI, G, false, false><<<ctas, kThreads, 0, s>>>(p);
     } else if (given) {
-        static std::atomic<uint32_t> done{0};
-        const cudaError_t e = smem_limit_once((const void *)router_kernel<L, NI, G, true, true>, 65536, done);
-        if (e != cudaSuccess) return e;
         router_kernel<L, NI, G, true, true><<<ctas, kThreads, smem, s>>>(p);
     } else {
-        static std::atomic<uint32_t> done{0};
-        const cudaError_t e = smem_limit_once((const void *)router_kernel<L, NI, G, true, false>, 65536, done);
-        if (e != cudaSuccess) return e;
         router_kernel<L, NI, G, true, false><<<ctas, kThreads, smem, s>>>(p);
     }
     return cudaGetLastError();
