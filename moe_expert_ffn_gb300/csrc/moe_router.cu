@@ -137,11 +137,32 @@ __device__ __forceinline__ Cut cut_at(const int32_t *off, int S, int t, int t1) 
     return c;
 }
 
+// A token's logits as loaded (-inf where there is none), so that the next token's can be on their way.
 template <class L, int NI, int G>
-__device__ __forceinline__ void load_row(float (&l)[NI], const void *logits, int64_t ld, int t, bool on, int lg, int E) {
-    const L *row = static_cast<const L *>(logits) + (int64_t)t * ld;
+__device__ __forceinline__ void load_row(L (&l)[NI], const void *logits, int64_t ld, int t, bool on, int lg, int E) {
+    const L *row = static_cast<const L *>(logits) + (int64_t)t * ld + lg;
+    if (E == NI * G) {   // every lane has all its experts
 #pragma unroll
-    for (int i = 0; i < NI; ++i) l[i] = on && lg + G * i < E ? open_logit(to_f32(row[lg + G * i])) : -INFINITY;
+        for (int i = 0; i < NI; ++i) l[i] = on ? row[G * i] : from_f32<L>(-INFINITY);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) l[i] = on && lg + G * i < E ? row[G * i] : from_f32<L>(-INFINITY);
+    }
+}
+
+// Scores of a token's logits times e^-(m or min(m, 0)), 0 where closed, and their sum.
+template <int NI, int G>
+__device__ __forceinline__ float scores(float (&q)[NI], const float (&l)[NI], float m, bool sigmoid) {
+    float z = 0.0f;
+    if (sigmoid) {
+        const float ms = fminf(m, 0.0f);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) z += q[i] = sigmoid_scaled(l[i], ms);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) z += q[i] = exp_of(l[i] - m);
+    }
+    return group_sum<G>(z);
 }
 
 template <int G>
@@ -171,6 +192,40 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[NI]) {
     }
 }
 
+__device__ __forceinline__ void exchange(uint32_t &a, uint32_t &b) {
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+
+// The D largest of v, descending, in v[0..D): all of them, or 4 by sorting fours and merging.
+template <int NI, int D>
+__device__ __forceinline__ void top_down(uint32_t (&v)[NI]) {
+    if (D == NI) {
+        sort_down(v);
+        return;
+    }
+#pragma unroll
+    for (int b = 0; b < NI; b += 4) {
+        exchange(v[b], v[b + 1]);
+        exchange(v[b + 2], v[b + 3]);
+        exchange(v[b], v[b + 2]);
+        exchange(v[b + 1], v[b + 3]);
+        exchange(v[b + 1], v[b + 2]);
+    }
+#pragma unroll
+    for (int w = 4; w < NI; w *= 2)
+#pragma unroll
+        for (int b = 0; b < NI; b += 2 * w) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[b + i] = max(v[b + i], v[b + w + 3 - i]);   // the 4 largest of both, bitonic
+            exchange(v[b], v[b + 2]);
+            exchange(v[b + 1], v[b + 3]);
+            exchange(v[b], v[b + 1]);
+            exchange(v[b + 2], v[b + 3]);
+        }
+}
+
 // The k largest keys of a group's token from the full keys, one by one: the exact choice whatever the keys.
 template <int NI, int G, int NS>
 __device__ __noinline__ void choose_exact(const float (&key)[NI], int k, int lg, int (&slot_e)[NS]) {
@@ -197,8 +252,9 @@ __device__ __noinline__ void choose_exact(const float (&key)[NI], int k, int lg,
 }
 
 // The k largest keys of a group's token, ties to the lowest expert.  Slot j goes to lane j % G, place j / G: its expert
-// (-1: nothing left).  `exact`: the keys' low bits that the expert's number takes are all zero.
-template <int NI, int G, int NS>
+// (-1: nothing left).  `exact`: the keys' low bits that the expert's number takes say nothing.  A lane keeps its D
+// largest; one that wins D < NI times may have had more.
+template <int NI, int G, int NS, int D>
 __device__ __forceinline__ void choose(const float (&key)[NI], int k, int lg, bool exact, int (&slot_e)[NS]) {
     constexpr uint32_t kLow = (uint32_t)(NI * G - 1);   // bits of an expert's number
     constexpr uint32_t kOpen = 0x00800000u;             // the order of the smallest finite float
@@ -209,29 +265,35 @@ __device__ __forceinline__ void choose(const float (&key)[NI], int k, int lg, bo
         const uint32_t order = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
         v[i] = (order & ~kLow) | (kLow - (uint32_t)(lg + G * i));
     }
-    sort_down(v);
-    uint32_t slot[NS];
+    top_down<NI, D>(v);
+    uint32_t slot[NS], out = 0;
 #pragma unroll
     for (int q = 0; q < NS; ++q) slot[q] = 0;
-    uint32_t before = 0;
-    bool near = false;
-    for (int j = 0; j <= k; ++j) {   // the last round is the first one that stays outside
+    for (int j = 0; j < k; ++j) {
         const uint32_t m = group_max<G>(v[0]);
-        near |= j > 0 && ((m ^ before) & ~kLow) == 0;
-        before = m < kOpen ? 0xFFFFFFFFu : m;   // closed ones are all alike
-        if (j == k) break;
 #pragma unroll
         for (int q = 0; q < NS; ++q)
             if (j == q * G + lg) slot[q] = m;
-        if (v[0] == m) {
+        const bool won = v[0] == m;
 #pragma unroll
-            for (int i = 0; i + 1 < NI; ++i) v[i] = v[i + 1];
-            v[NI - 1] = 0;
+        for (int i = 0; i + 1 < D; ++i) v[i] = won ? v[i + 1] : v[i];
+        v[D - 1] = won ? 0u : v[D - 1];
+    }
+    bool again = D < NI && v[0] == 0;
+    if (!exact) {   // open neighbours, the first one left outside among them, that only the displaced bits tell apart
+        out = group_max<G>(v[0]);
+#pragma unroll
+        for (int q = 0; q < NS; ++q) {
+            uint32_t next = __shfl_down_sync(kAll, slot[q], 1, G);
+            const uint32_t wrap = __shfl_sync(kAll, slot[q + 1 < NS ? q + 1 : q], 0, G);
+            if (lg == G - 1) next = q + 1 < NS ? wrap : out;
+            if (q * G + lg == k - 1) next = out;
+            again |= q * G + lg < k && slot[q] >= kOpen && ((slot[q] ^ next) & ~kLow) == 0;
         }
     }
 #pragma unroll
     for (int q = 0; q < NS; ++q) slot_e[q] = slot[q] < kOpen ? -1 : (int)(kLow - (slot[q] & kLow));
-    if (!exact && __any_sync(kAll, near)) choose_exact<NI, G, NS>(key, k, lg, slot_e);
+    if (__any_sync(kAll, again)) choose_exact<NI, G, NS>(key, k, lg, slot_e);
 }
 
 // Joins the warps of the CTA: sum of `v` over the groups of every warp, in warp order, for the lanes' experts.
@@ -242,7 +304,7 @@ __device__ __forceinline__ float over_groups(float v) {
     return v;
 }
 
-template <class L, int NI, int G, bool kLoss, bool kGiven>
+template <class L, int NI, int G, int D, bool kLoss, bool kGiven>
 __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ RouterParams p) {
     extern __shared__ float joined[];   // kLoss: [warps][E] probabilities, [E] counts
     __shared__ float sz[kWarps];
@@ -270,19 +332,23 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
             for (int e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
             __syncthreads();
         }
-        for (int tb = a + warp * kGroups; tb < cut.end; tb += kWarps * kGroups) {
+        L raw[NI];
+        const int tw = a + warp * kGroups;
+        if (tw < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
+        for (int tb = tw; tb < cut.end; tb += kWarps * kGroups) {
             const int t = tb + grp;
             const bool on = t < cut.end;
             float l[NI];
-            load_row<L, NI, G>(l, p.logits, p.ld, t, on, lg, E);
-            float m = -INFINITY;
-            if (kLoss || (!p.renorm && !p.sigmoid)) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) l[i] = open_logit(to_f32(raw[i]));
+            const int tn = tb + kWarps * kGroups;
+            if (tn < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < cut.end, lg, E);
+            float m = -INFINITY, top = -INFINITY;   // the largest logit, and that of the chosen
+            if (kGiven || (kLoss && p.bias) || (!p.renorm && !p.sigmoid)) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
                 m = group_max<G>(m);
             }
-            const bool real = m > -INFINITY;
-            const float m0 = real ? m : 0.0f;
             int my_e[NS];
             if (kGiven) {
 #pragma unroll
@@ -296,9 +362,9 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
                     float key[NI];   // closed stays -inf, NaN (also -inf + inf) closes
 #pragma unroll
                     for (int i = 0; i < NI; ++i) key[i] = fmaxf(l[i] + bias[i], -INFINITY);
-                    choose<NI, G, NS>(key, k, lg, false, my_e);
+                    choose<NI, G, NS, D>(key, k, lg, false, my_e);
                 } else {
-                    choose<NI, G, NS>(l, k, lg, sizeof(L) == 2, my_e);
+                    choose<NI, G, NS, D>(l, k, lg, sizeof(L) == 2, my_e);
                 }
                 // weights of the chosen
                 float wgt[NS], my_l[NS], f = p.scale;
@@ -306,11 +372,14 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
                 for (int q = 0; q < NS; ++q)
                     my_l[q] = my_e[q] < 0 ? -INFINITY
                                           : open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + my_e[q]]));
-                if (p.renorm) {
-                    float top = -INFINITY, sum = 0.0f;
+                if (p.renorm || kLoss) {
 #pragma unroll
                     for (int q = 0; q < NS; ++q) top = fmaxf(top, my_l[q]);
                     top = group_max<G>(top);
+                    if (kLoss && !p.bias) m = top;
+                }
+                if (p.renorm) {
+                    float sum = 0.0f;
 #pragma unroll
                     for (int q = 0; q < NS; ++q) {
                         wgt[q] = my_e[q] < 0 ? 0.0f : p.sigmoid ? sigmoid_scaled(my_l[q], fminf(top, 0.0f)) : exp_of(my_l[q] - top);
@@ -322,10 +391,8 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
 #pragma unroll
                     for (int q = 0; q < NS; ++q) wgt[q] = my_e[q] < 0 ? 0.0f : sigmoid_scaled(my_l[q], 0.0f);
                 } else {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < NI; ++i) sum += exp_of(l[i] - m0);
-                    sum = group_sum<G>(sum);
+                    float all[NI];
+                    const float m0 = m > -INFINITY ? m : 0.0f, sum = scores<NI, G>(all, l, m0, false);
                     f = sum > 0.0f ? __fdividef(f, sum) : 0.0f;
 #pragma unroll
                     for (int q = 0; q < NS; ++q) wgt[q] = my_e[q] < 0 ? 0.0f : exp_of(my_l[q] - m0);
@@ -340,14 +407,9 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
                 }
             }
             if (kLoss && cut.inside) {
-                float q[NI], z = 0.0f;
-                const float ms = fminf(m0, 0.0f);
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {   // a closed logit's score comes out 0
-                    q[i] = p.sigmoid ? sigmoid_scaled(l[i], ms) : exp_of(l[i] - m0);
-                    z += q[i];
-                }
-                z = group_sum<G>(z);
+                const bool real = m > -INFINITY;
+                float q[NI];
+                const float z = scores<NI, G>(q, l, real ? m : 0.0f, p.sigmoid);
                 const float inv = real ? __fdividef(1.0f, z) : 0.0f;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) prob[i] = fmaf(q[i], inv, prob[i]);
@@ -355,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
                 for (int s = 0; s < NS; ++s)
                     if (real && my_e[s] >= 0) atomicAdd(counts + my_e[s], 1);   // whole numbers: the order does not matter
                 if (real && lg == 0) {
-                    const float lse = m + logf(z);
+                    const float lse = m + __logf(z);   // z >= 1
                     zsum += p.sigmoid ? 0.0f : lse * lse;
                     ++tokens;
                 }
@@ -517,11 +579,17 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const __grid_const
             for (int i = 0; i < NI; ++i) c[i] = lg + G * i < E ? c0 * (float)p.counts[(int64_t)cut.s * E + lg + G * i] : 0.0f;
         }
         const bool dense = n > 0 || (p.d_weights && !p.renorm && !p.sigmoid);   // every probability is needed
-        for (int tb = a + warp * kGroups; tb < cut.end; tb += kWarps * kGroups) {
+        L raw[NI];
+        const int tw = a + warp * kGroups;
+        if (tw < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
+        for (int tb = tw; tb < cut.end; tb += kWarps * kGroups) {
             const int t = tb + grp;
             const bool on = t < cut.end;
             float l[NI], d[NI], q[NI];
-            load_row<L, NI, G>(l, p.logits, p.ld, t, on, lg, E);
+#pragma unroll
+            for (int i = 0; i < NI; ++i) l[i] = open_logit(to_f32(raw[i]));
+            const int tn = tb + kWarps * kGroups;
+            if (tn < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < cut.end, lg, E);
             // the chosen slots' part
             float add[NS], ls[NS], dw[NS], dot = 0.0f;
             int idx[NS];
@@ -548,28 +616,21 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const __grid_const
                 m = group_max<G>(m);
                 real = m > -INFINITY;
                 m = real ? m : 0.0f;
-                const float ms = fminf(m, 0.0f);
-                float z = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    q[i] = p.sigmoid ? sigmoid_scaled(l[i], ms) : exp_of(l[i] - m);   // 0 where closed
-                    z += q[i];
-                }
-                z = group_sum<G>(z);
+                const float z = scores<NI, G>(q, l, m, p.sigmoid);
                 inv = real ? __fdividef(1.0f, z) : 0.0f;
-                const float lse = real ? m + logf(z) : 0.0f;
-                float cq = 0.0f;
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    q[i] *= inv;
-                    if (n > 0) cq = fmaf(c[i], q[i], cq);
-                }
+                for (int i = 0; i < NI; ++i) q[i] *= inv;
                 if (n > 0) {
+                    const float lse = real ? m + __logf(z) : 0.0f;   // z >= 1 (sigmoid: unused)
+                    float cq = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) cq = fmaf(c[i], q[i], cq);
                     cq = zc * lse - group_sum<G>(cq);
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        d[i] = q[i] * (c[i] + cq);
-                        if (p.sigmoid) d[i] *= sigmoid_slope(l[i]);   // ds/dl = s (1 - s)
+                    for (int i = 0; i < NI; ++i) d[i] = q[i] * (c[i] + cq);
+                    if (p.sigmoid) {   // ds/dl = s (1 - s)
+#pragma unroll
+                        for (int i = 0; i < NI; ++i) d[i] *= sigmoid_slope(l[i]);
                     }
                 }
             }
@@ -623,16 +684,16 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const __grid_const
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
-                    if (lg + G * i < E) d[i] += mine[lg + G * i];
+                    if (E == NI * G || lg + G * i < E) d[i] += mine[lg + G * i];
                 __syncwarp();
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
                     if (idx[s] >= 0) mine[idx[s]] = 0.0f;
             }
-            L *out = static_cast<L *>(p.d_logits) + (int64_t)t * p.ld_d;
+            L *out = static_cast<L *>(p.d_logits) + (int64_t)t * p.ld_d + lg;
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-                if (on && lg + G * i < E) out[lg + G * i] = from_f32<L>(d[i]);
+                if (on && (E == NI * G || lg + G * i < E)) out[G * i] = from_f32<L>(d[i]);
             __syncwarp();
         }
         a = cut.end;
@@ -677,17 +738,24 @@ size_t carve(int E, int T, int S, char *base, Partials *out) {
     return o;
 }
 
+template <class L, int NI, int G, int D>
+cudaError_t launch_router(const RouterParams &p, bool loss, int ctas, cudaStream_t s) {
+    const size_t smem = (size_t)(kWarps + 1) * p.E * 4;   // at most 36 KB
+    if (loss) router_kernel<L, NI, G, D, true, false><<<ctas, kThreads, smem, s>>>(p);
+    else router_kernel<L, NI, G, D, false, false><<<ctas, kThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
 template <class L, int NI, int G>
 cudaError_t launch_router(const RouterParams &p, bool loss, bool given, int ctas, cudaStream_t s) {
-    const size_t smem = (size_t)(kWarps + 1) * p.E * 4;   // at most 36 KB
-    if (!loss) {
-        router_kernel<L, NI, G, false, false><<<ctas, kThreads, 0, s>>>(p);
-    } else if (given) {
-        router_kernel<L, NI, G, true, true><<<ctas, kThreads, smem, s>>>(p);
-    } else {
-        router_kernel<L, NI, G, true, false><<<ctas, kThreads, smem, s>>>(p);
+    if (given) {
+        router_kernel<L, NI, G, NI, true, true><<<ctas, kThreads, (size_t)(kWarps + 1) * p.E * 4, s>>>(p);
+        return cudaGetLastError();
     }
-    return cudaGetLastError();
+    // up to 12 choices seldom fall four times on one of 32 lanes (1 token in 100 with 12), and four are cheaper to keep
+    // in order than 8 and more
+    constexpr int kFew = G == 32 && NI > 4 ? 4 : NI;
+    if (p.k <= 12) return launch_router<L, NI, G, kFew>(p, loss, ctas, s);
+    return launch_router<L, NI, G, NI>(p, loss, ctas, s);
 }
 
 // Calls f with the lanes of a token and the experts of a lane as template arguments.
@@ -750,7 +818,7 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.scale = cfg->weight_scale;
     p.S = loss ? loss->num_seqs : 1;
     p.seq_offsets = loss ? loss->seq_offsets : nullptr;
-    const int ctas = ctas_for(T, p.E, loss ? kMaxLossCtas : 1 << 30);
+    const int ctas = ctas_for(T, p.E, loss ? kMaxLossCtas : 152 * 6);
     p.chunk = std::max(1, (T + ctas - 1) / ctas);
     if (loss) carve(p.E, T, p.S, static_cast<char *>(ws), &p.part);
     if (T > 0) {
