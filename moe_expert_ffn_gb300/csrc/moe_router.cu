@@ -150,19 +150,34 @@ __device__ __forceinline__ void load_row(L (&l)[NI], const void *logits, int64_t
     }
 }
 
-// Scores of a token's logits times e^-(m or min(m, 0)), 0 where closed, and their sum.
+// Logits as the definitions take them (open_logit): needed only where a NaN or +inf turns up, which the callers see in
+// what they compute.
+template <int NI>
+__device__ __forceinline__ void clean(float (&l)[NI]) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) l[i] = open_logit(l[i]);
+}
+
+// Scores of a token's logits times e^-(m or min(m, 0)), 0 where closed, and their sum.  Cleans l and m if need be.
 template <int NI, int G>
-__device__ __forceinline__ float scores(float (&q)[NI], const float (&l)[NI], float m, bool sigmoid) {
+__device__ __forceinline__ float scores(float (&q)[NI], float (&l)[NI], float &m, bool sigmoid) {
     float z = 0.0f;
-    if (sigmoid) {
-        const float ms = fminf(m, 0.0f);
+    for (int pass = 0; pass < 2; ++pass) {
+        z = 0.0f;
+        if (sigmoid) {
+            const float ms = fminf(m, 0.0f);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) z += q[i] = sigmoid_scaled(l[i], ms);
-    } else {
+            for (int i = 0; i < NI; ++i) z += q[i] = sigmoid_scaled(l[i], ms);
+        } else {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) z += q[i] = exp_of(l[i] - m);
+            for (int i = 0; i < NI; ++i) z += q[i] = exp_of(l[i] - m);
+        }
+        z = group_sum<G>(z);
+        if (!__any_sync(kAll, !(z <= FLT_MAX))) break;
+        clean(l);
+        m = fminf(m, FLT_MAX);
     }
-    return group_sum<G>(z);
+    return z;
 }
 
 template <int G>
@@ -253,9 +268,10 @@ __device__ __noinline__ void choose_exact(const float (&key)[NI], int k, int lg,
 
 // The k largest keys of a group's token, ties to the lowest expert.  Slot j goes to lane j % G, place j / G: its expert
 // (-1: nothing left).  `exact`: the keys' low bits that the expert's number takes say nothing.  A lane keeps its D
-// largest; one that wins D < NI times may have had more.
+// largest; one that wins D < NI times may have had more.  Returns false, with nothing chosen, where a key is +inf or a
+// NaN that sorts above it and `cleaned` does not say that it is meant.
 template <int NI, int G, int NS, int D>
-__device__ __forceinline__ void choose(const float (&key)[NI], int k, int lg, bool exact, int (&slot_e)[NS]) {
+__device__ __forceinline__ bool choose(const float (&key)[NI], int k, int lg, bool exact, bool cleaned, int (&slot_e)[NS]) {
     constexpr uint32_t kLow = (uint32_t)(NI * G - 1);   // bits of an expert's number
     constexpr uint32_t kOpen = 0x00800000u;             // the order of the smallest finite float
     uint32_t v[NI];
@@ -266,6 +282,7 @@ __device__ __forceinline__ void choose(const float (&key)[NI], int k, int lg, bo
         v[i] = (order & ~kLow) | (kLow - (uint32_t)(lg + G * i));
     }
     top_down<NI, D>(v);
+    if (!cleaned && __any_sync(kAll, v[0] >= 0xFF800000u)) return false;   // the order of +inf
     uint32_t slot[NS], out = 0;
 #pragma unroll
     for (int q = 0; q < NS; ++q) slot[q] = 0;
@@ -294,6 +311,7 @@ __device__ __forceinline__ void choose(const float (&key)[NI], int k, int lg, bo
 #pragma unroll
     for (int q = 0; q < NS; ++q) slot_e[q] = slot[q] < kOpen ? -1 : (int)(kLow - (slot[q] & kLow));
     if (__any_sync(kAll, again)) choose_exact<NI, G, NS>(key, k, lg, slot_e);
+    return true;
 }
 
 // Joins the warps of the CTA: sum of `v` over the groups of every warp, in warp order, for the lanes' experts.
@@ -305,7 +323,7 @@ __device__ __forceinline__ float over_groups(float v) {
 }
 
 template <class L, int NI, int G, int D, bool kLoss, bool kGiven>
-__global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ RouterParams p) {
+__global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_kernel(const __grid_constant__ RouterParams p) {
     extern __shared__ float joined[];   // kLoss: [warps][E] probabilities, [E] counts
     __shared__ float sz[kWarps];
     __shared__ int sn[kWarps];
@@ -340,14 +358,14 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
             const bool on = t < cut.end;
             float l[NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) l[i] = open_logit(to_f32(raw[i]));
+            for (int i = 0; i < NI; ++i) l[i] = to_f32(raw[i]);
             const int tn = tb + kWarps * kGroups;
             if (tn < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < cut.end, lg, E);
             float m = -INFINITY, top = -INFINITY;   // the largest logit, and that of the chosen
             if (kGiven || (kLoss && p.bias) || (!p.renorm && !p.sigmoid)) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
-                m = group_max<G>(m);
+                m = fminf(group_max<G>(m), FLT_MAX);
             }
             int my_e[NS];
             if (kGiven) {
@@ -358,13 +376,16 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
                     if (my_e[q] >= E) my_e[q] = -1;
                 }
             } else {
-                if (p.bias) {
-                    float key[NI];   // closed stays -inf, NaN (also -inf + inf) closes
+                for (int pass = 0; pass < 2; ++pass) {
+                    float key[NI];
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) key[i] = fmaxf(l[i] + bias[i], -INFINITY);
-                    choose<NI, G, NS, D>(key, k, lg, false, my_e);
-                } else {
-                    choose<NI, G, NS, D>(l, k, lg, sizeof(L) == 2, my_e);
+                    for (int i = 0; i < NI; ++i) key[i] = p.bias ? l[i] + bias[i] : l[i];
+                    if (pass) {   // -inf + inf closes
+#pragma unroll
+                        for (int i = 0; i < NI; ++i) key[i] = fmaxf(key[i], -INFINITY);
+                    }
+                    if (choose<NI, G, NS, D>(key, k, lg, sizeof(L) == 2 && !p.bias, pass, my_e)) break;
+                    clean(l);
                 }
                 // weights of the chosen
                 float wgt[NS], my_l[NS], f = p.scale;
@@ -392,7 +413,8 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
                     for (int q = 0; q < NS; ++q) wgt[q] = my_e[q] < 0 ? 0.0f : sigmoid_scaled(my_l[q], 0.0f);
                 } else {
                     float all[NI];
-                    const float m0 = m > -INFINITY ? m : 0.0f, sum = scores<NI, G>(all, l, m0, false);
+                    float m0 = m > -INFINITY ? m : 0.0f;
+                    const float sum = scores<NI, G>(all, l, m0, false);
                     f = sum > 0.0f ? __fdividef(f, sum) : 0.0f;
 #pragma unroll
                     for (int q = 0; q < NS; ++q) wgt[q] = my_e[q] < 0 ? 0.0f : exp_of(my_l[q] - m0);
@@ -409,7 +431,8 @@ __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant_
             if (kLoss && cut.inside) {
                 const bool real = m > -INFINITY;
                 float q[NI];
-                const float z = scores<NI, G>(q, l, real ? m : 0.0f, p.sigmoid);
+                m = real ? m : 0.0f;
+                const float z = scores<NI, G>(q, l, m, p.sigmoid);
                 const float inv = real ? __fdividef(1.0f, z) : 0.0f;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) prob[i] = fmaf(q[i], inv, prob[i]);
@@ -556,7 +579,7 @@ struct RouterBwd {
 };
 
 template <class L, int NI, int G>
-__global__ void __launch_bounds__(kThreads) router_bwd_kernel(const __grid_constant__ RouterBwd p) {
+__global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_bwd_kernel(const __grid_constant__ RouterBwd p) {
     extern __shared__ float scatter[];   // [warps][groups][E]: gradients of the chosen logits, zero between tokens
     constexpr int kGroups = 32 / G;
     constexpr int NS = G == 32 ? 1 : 32 / G;
@@ -587,7 +610,7 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const __grid_const
             const bool on = t < cut.end;
             float l[NI], d[NI], q[NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) l[i] = open_logit(to_f32(raw[i]));
+            for (int i = 0; i < NI; ++i) l[i] = to_f32(raw[i]);
             const int tn = tb + kWarps * kGroups;
             if (tn < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < cut.end, lg, E);
             // the chosen slots' part
@@ -613,7 +636,7 @@ __global__ void __launch_bounds__(kThreads) router_bwd_kernel(const __grid_const
                 m = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
-                m = group_max<G>(m);
+                m = fminf(group_max<G>(m), FLT_MAX);
                 real = m > -INFINITY;
                 m = real ? m : 0.0f;
                 const float z = scores<NI, G>(q, l, m, p.sigmoid);
