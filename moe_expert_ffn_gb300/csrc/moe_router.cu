@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxLossCtas = 608;   // four on each of 152 SMs
+constexpr int kMaxCtas = 608;   // four on each of 152 SMs
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.44269504f;
 
@@ -742,7 +742,7 @@ int ctas_for(int T, int E, int most) {
 
 // Carves the workspace; returns its size.
 size_t carve(int E, int T, int S, char *base, Partials *out) {
-    const size_t rows = (size_t)ctas_for(T, E, kMaxLossCtas) + S;
+    const size_t rows = (size_t)ctas_for(T, E, kMaxCtas) + S;
     size_t o = 0;
     auto take = [&](size_t bytes) {
         char *at = base + o;
@@ -841,7 +841,7 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.scale = cfg->weight_scale;
     p.S = loss ? loss->num_seqs : 1;
     p.seq_offsets = loss ? loss->seq_offsets : nullptr;
-    const int ctas = ctas_for(T, p.E, loss ? kMaxLossCtas : 152 * 6);
+    const int ctas = ctas_for(T, p.E, kMaxCtas);
     p.chunk = std::max(1, (T + ctas - 1) / ctas);
     if (loss) carve(p.E, T, p.S, static_cast<char *>(ws), &p.part);
     if (T > 0) {
@@ -931,7 +931,7 @@ int moe_router_backward(const moe_router_config *cfg, int num_tokens, const void
     p.scale = cfg->weight_scale;
     p.alpha = cfg->balance_coef;
     p.beta = cfg->z_coef;
-    const int ctas = ctas_for(num_tokens, p.E, 152 * 8);
+    const int ctas = ctas_for(num_tokens, p.E, kMaxCtas);
     p.chunk = (num_tokens + ctas - 1) / ctas;
     return by_experts(p.E, RunBwd{p, cfg->logits_dtype == MOE_DTYPE_BF16, (num_tokens + p.chunk - 1) / p.chunk,
                                   static_cast<cudaStream_t>(stream)}) == cudaSuccess
