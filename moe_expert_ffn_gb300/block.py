@@ -8,7 +8,6 @@ loop allocates nothing, and allocates them itself when it gets none.
 """
 from __future__ import annotations
 
-import ctypes
 import math
 
 import torch
@@ -35,39 +34,73 @@ def _choice(table, key, name):
     return table[key]
 
 
-def _stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+try:   # the stream's handle without building a Stream object
+    from torch._C import _cuda_getCurrentRawStream as _current_stream
+except ImportError:   # pragma: no cover
+    def _current_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
 
 
-def _rows(t, name, dtype, rows, cols, device):
+def _stream(stream, index):
+    return _current_stream(index) if stream is None else stream.cuda_stream
+
+
+def _index(device):
+    """What Tensor.get_device() gives on `device` (-1: not a GPU)."""
+    return device.index if device.type == "cuda" else -1
+
+
+def _refuse(t, name, dtype, shape, what):
+    raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} {what}, got {t.dtype} {tuple(t.shape)} with "
+                     f"strides {t.stride()} on {t.device}")
+
+
+def _rows(t, name, dtype, shape, index):
     """(pointer, row pitch) of a [rows, cols] tensor whose rows are contiguous."""
-    if t.dtype is not dtype or t.shape != (rows, cols) or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {(rows, cols)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _refuse(t, name, dtype, shape, "on the operator's device")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
     pitch, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if rows < 2:
-        pitch = cols
-    elif pitch < cols:
-        raise ValueError(f"{name} must have rows that do not overlap")
-    return t.data_ptr(), pitch
+    if (step != 1 and shape[1] > 1) or (shape[0] > 1 and pitch < shape[1]):
+        _refuse(t, name, dtype, shape, "with contiguous rows that do not overlap")
+    return t.data_ptr(), pitch if shape[0] > 1 else shape[1]
 
 
-def _flat(t, name, dtype, shape, device):
+def _flat(t, name, dtype, shape, index):
     """Pointer of a contiguous tensor."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, "contiguous on the operator's device")
     return t.data_ptr()
 
 
-class NormOutput:
+class _Outputs:
+    """Output tensors of a call and, once checked against an operator, their native description: a later call with the
+    same ones only asks them for their addresses.  Replacing a tensor has it checked again."""
+    __slots__ = ("_of", "_io", "_own")
+
+    def __init__(self):
+        for n in self.__slots__:
+            object.__setattr__(self, n, None)
+        object.__setattr__(self, "_of", None)
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_of", None)
+
+    def _bind(self, key, io, own):
+        """`own`: (tensor, field of io) pairs."""
+        object.__setattr__(self, "_io", io)
+        object.__setattr__(self, "_own", own)
+        object.__setattr__(self, "_of", key)
+
+
+class NormOutput(_Outputs):
     """What BlockNorm.forward writes: h, n, codes, sf, rstd_post, rstd_pre (None where absent)."""
     __slots__ = ("h", "n", "codes", "sf", "rstd_post", "rstd_pre")
 
 
-class NormGrads:
+class NormGrads(_Outputs):
     """What BlockNorm.backward writes: dresidual, dy, dw_post, dgate, dw_pre (None where absent)."""
     __slots__ = ("dresidual", "dy", "dw_post", "dgate", "dw_pre")
 
@@ -87,7 +120,8 @@ class BlockNorm:
                               _choice(GATES, gate, "gate"), _choice(QUANTS, quant, "quant"), float(eps), float(residual_scale))
         if lib().moe_norm_workspace_bytes(self.cfg, 1) == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "norm config")
-        self._workspace = None
+        self._workspace, self._dev, self._width = None, _index(self.device), (int(hidden),)
+        self._fwd, self._bwd, self._ws_bytes = lib().moe_norm_forward, lib().moe_norm_backward, lib().moe_norm_workspace_bytes
 
     def buffers(self, num_tokens, block=True, post=True, pre=True, normed=True) -> NormOutput:
         """Outputs of a forward of `num_tokens`: with y (`block`), w_post (`post`), w_pre (`pre`), n (`normed`)."""
@@ -115,36 +149,56 @@ class BlockNorm:
                    if block and self.gate else None)
         return g
 
-    def _params(self, T, w_post, gate, w_pre):
-        H, dt, dev = self.hidden, self.param_dtype, self.device
-        return (None if w_post is None else _flat(w_post, "w_post", dt, (H,), dev),
-                None if gate is None else _flat(gate, "gate", dt, (H,) if self.gate == "channel" else (T,), dev),
-                None if w_pre is None else _flat(w_pre, "w_pre", dt, (H,), dev))
+    def _params(self, io, T, w_post, gate, w_pre):
+        dt, dev = self.param_dtype, self._dev
+        io.w_post = None if w_post is None else _flat(w_post, "w_post", dt, self._width, dev)
+        io.gate = None if gate is None else _flat(gate, "gate", dt, self._width if self.gate == "channel" else (T,), dev)
+        io.w_pre = None if w_pre is None else _flat(w_pre, "w_pre", dt, self._width, dev)
+
+    @staticmethod
+    def _check_all(io, wanted, index):
+        """Checks (name, tensor, dtype, shape, pitched) outputs and writes them into io."""
+        own = []
+        for name, t, dtype, shape, pitched in wanted:
+            if t is None:
+                continue
+            if pitched:
+                ptr, pitch = _rows(t, name, dtype, shape, index)
+                setattr(io, "ld_" + name, pitch)
+            else:
+                ptr = _flat(t, name, dtype, shape, index)
+            setattr(io, name, ptr)
+            own.append((t, name))
+        return own
 
     def forward(self, residual, y=None, w_post=None, gate=None, w_pre=None, normed=True, out=None, stream=None) -> NormOutput:
-        T, H, dt, dev, f32 = residual.shape[0], self.hidden, self.dtype, self.device, torch.float32
+        T, H, dt, dev = residual.shape[0], self.hidden, self.dtype, self._dev
         if out is None:
             out = self.buffers(T, y is not None, w_post is not None, w_pre is not None, normed)
-        io = NormIO()
-        io.residual, io.ld_residual = _rows(residual, "residual", dt, T, H, dev)
-        io.w_post, io.gate, io.w_pre = self._params(T, w_post, gate, w_pre)
+        key = (self, T, y is None, w_post is None, w_pre is None)
+        if out._of == key:
+            io = out._io
+            for t, name in out._own:
+                setattr(io, name, t.data_ptr())
+        else:
+            f32, u8, shape, block, pre = torch.float32, torch.uint8, (T, H), y is not None, w_pre is not None
+            io = NormIO()
+            quant = pre and self.quant
+            if block and out.h is None or quant and (out.codes is None or out.sf is None):
+                raise ValueError("out lacks h, codes or sf")
+            own = self._check_all(io, (
+                ("h", out.h if block else None, dt, shape, True), ("n", out.n if pre else None, dt, shape, True),
+                ("codes", out.codes if quant else None, u8, shape, False),
+                ("sf", out.sf if quant else None, f32 if self.quant == "fp8" else u8, (T, H // (128 if self.quant == "fp8" else 32)), False),
+                ("rstd_post", out.rstd_post if block and w_post is not None else None, f32, (T,), False),
+                ("rstd_pre", out.rstd_pre if pre else None, f32, (T,), False)), dev)
+            out._bind(key, io, own)
+        shape = (T, H)
+        io.residual, io.ld_residual = _rows(residual, "residual", dt, shape, dev)
         if y is not None:
-            io.y, io.ld_y = _rows(y, "y", dt, T, H, dev)
-            io.h, io.ld_h = _rows(out.h, "h", dt, T, H, dev)
-            if w_post is not None and out.rstd_post is not None:
-                io.rstd_post = _flat(out.rstd_post, "rstd_post", f32, (T,), dev)
-        if w_pre is not None:
-            if out.n is not None:
-                io.n, io.ld_n = _rows(out.n, "n", dt, T, H, dev)
-            if out.rstd_pre is not None:
-                io.rstd_pre = _flat(out.rstd_pre, "rstd_pre", f32, (T,), dev)
-            if self.quant == "fp8":
-                io.codes = _flat(out.codes, "codes", torch.uint8, (T, H), dev)
-                io.sf = _flat(out.sf, "sf", f32, (T, H // 128), dev)
-            elif self.quant:
-                io.codes = _flat(out.codes, "codes", torch.uint8, (T, H), dev)
-                io.sf = _flat(out.sf, "sf", torch.uint8, (T, H // 32), dev)
-        rc = lib().moe_norm_forward(self.cfg, T, io, _stream(stream, dev))
+            io.y, io.ld_y = _rows(y, "y", dt, shape, dev)
+        self._params(io, T, w_post, gate, w_pre)
+        rc = self._fwd(self.cfg, T, io, _stream(stream, dev))
         if rc:
             _check(rc, "moe_norm_forward")
         return out
@@ -153,38 +207,40 @@ class BlockNorm:
                  out=None, stream=None) -> NormGrads:
         """Gradients from dh (of the stream h) and dn (of the normed n).  Uses a workspace of this object,
         so backward passes of one BlockNorm must not run concurrently."""
-        T, H, dt, dev, f32 = h.shape[0], self.hidden, self.dtype, self.device, torch.float32
+        T, H, dt, dev, f32 = h.shape[0], self.hidden, self.dtype, self._dev, torch.float32
         if out is None:
             out = self.grad_buffers(T, y is not None, w_post is not None, w_pre is not None)
-        io = NormGradIO()
-        io.h, io.ld_h = _rows(h, "h", dt, T, H, dev)
-        io.w_post, io.gate, io.w_pre = self._params(T, w_post, gate, w_pre)
-        if dh is not None:
-            io.dh, io.ld_dh = _rows(dh, "dh", dt, T, H, dev)
-        if dn is not None:
-            io.dn, io.ld_dn = _rows(dn, "dn", dt, T, H, dev)
-        io.dresidual, io.ld_dresidual = _rows(out.dresidual, "dresidual", dt, T, H, dev)
+        key = (self, T, y is None, w_post is None, w_pre is None, gate is None)
+        shape = (T, H)
+        if out._of == key:
+            io = out._io
+            for t, name in out._own:
+                setattr(io, name, t.data_ptr())
+        else:
+            io = NormGradIO()
+            wanted = (("dresidual", out.dresidual, dt, shape, True), ("dy", out.dy if y is not None else None, dt, shape, True),
+                      ("dw_post", out.dw_post if w_post is not None else None, f32, self._width, False),
+                      ("dw_pre", out.dw_pre if w_pre is not None else None, f32, self._width, False),
+                      ("dgate", out.dgate if gate is not None else None, f32, self._width if self.gate == "channel" else (T,), False))
+            out._bind(key, io, self._check_all(io, wanted, dev))
+        io.h, io.ld_h = _rows(h, "h", dt, shape, dev)
+        self._params(io, T, w_post, gate, w_pre)
+        io.dh, io.ld_dh = (None, 0) if dh is None else _rows(dh, "dh", dt, shape, dev)
+        io.dn, io.ld_dn = (None, 0) if dn is None else _rows(dn, "dn", dt, shape, dev)
         if y is not None:
-            io.y, io.ld_y = _rows(y, "y", dt, T, H, dev)
-            io.dy, io.ld_dy = _rows(out.dy, "dy", dt, T, H, dev)
-        if w_post is not None:
-            io.dw_post = _flat(out.dw_post, "dw_post", f32, (H,), dev)
-            io.rstd_post = None if rstd_post is None else _flat(rstd_post, "rstd_post", f32, (T,), dev)
-        if w_pre is not None:
-            io.dw_pre = _flat(out.dw_pre, "dw_pre", f32, (H,), dev)
-            io.rstd_pre = None if rstd_pre is None else _flat(rstd_pre, "rstd_pre", f32, (T,), dev)
-        if gate is not None:
-            io.dgate = _flat(out.dgate, "dgate", f32, (H,) if self.gate == "channel" else (T,), dev)
-        need = lib().moe_norm_workspace_bytes(self.cfg, T)
+            io.y, io.ld_y = _rows(y, "y", dt, shape, dev)
+        io.rstd_post = None if w_post is None or rstd_post is None else _flat(rstd_post, "rstd_post", f32, (T,), dev)
+        io.rstd_pre = None if w_pre is None or rstd_pre is None else _flat(rstd_pre, "rstd_pre", f32, (T,), dev)
+        need = self._ws_bytes(self.cfg, T)
         if self._workspace is None or self._workspace.numel() < need:
-            self._workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        rc = lib().moe_norm_backward(self.cfg, T, io, self._workspace.data_ptr(), _stream(stream, dev))
+            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        rc = self._bwd(self.cfg, T, io, self._workspace.data_ptr(), _stream(stream, dev))
         if rc:
             _check(rc, "moe_norm_backward")
         return out
 
 
-class RouterOutput:
+class RouterOutput(_Outputs):
     """What Router writes: topk_idx, topk_weights and, with the losses, loss ([3]: total, balance, z),
     counts [S, E], prob_mean [S, E], seq_tokens [S] (views of ``tokens`` [S + 2])."""
     __slots__ = ("topk_idx", "topk_weights", "loss", "counts", "prob_mean", "seq_tokens", "tokens")
@@ -206,6 +262,9 @@ class Router:
         need = lib().moe_router_workspace_bytes(self.cfg, 0 if max_tokens is None else int(max_tokens), self.max_seqs)
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "router config")
+        self._dev, self._bias_shape = _index(self.device), (int(num_experts),)
+        L = lib()
+        self._fwd, self._bal, self._bwd = L.moe_router_forward, L.moe_balance_loss, L.moe_router_backward
         # only the loss calls need it: they need to know max_tokens
         self._workspace = None if max_tokens is None else torch.empty(need, dtype=torch.uint8, device=self.device)
 
@@ -226,32 +285,39 @@ class Router:
 
     def _losses(self, T, seq_offsets, out, write=True):
         S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
-        E, dev = self.num_experts, self.device
         if write and (self.max_tokens is None or T > self.max_tokens or S > self.max_seqs):
             raise ValueError(f"{T} tokens in {S} sequences: the router was made for losses of "
                              f"{self.max_tokens} tokens in {self.max_seqs}")
-        io = BalanceIO()
-        io.num_seqs = S
-        if seq_offsets is not None:
-            io.seq_offsets = _flat(seq_offsets, "seq_offsets", torch.int32, (S + 1,), dev)
-        io.loss = _flat(out.loss, "loss", torch.float32, (3,), dev)
-        io.counts = _flat(out.counts, "counts", torch.int32, (S, E), dev)
-        io.prob_mean = _flat(out.prob_mean, "prob_mean", torch.float32, (S, E), dev)
-        io.seq_tokens = _flat(out.tokens, "tokens", torch.int32, (S + 2,), dev)
+        key = (self, S)
+        if out._of == key:
+            io = out._io
+            for t, name in out._own:
+                setattr(io, name, t.data_ptr())
+        else:
+            E, dev, f32, i32 = self.num_experts, self._dev, torch.float32, torch.int32
+            io = BalanceIO()
+            io.num_seqs = S
+            own = BlockNorm._check_all(io, (("loss", out.loss, f32, (3,), False), ("counts", out.counts, i32, (S, E), False),
+                                            ("prob_mean", out.prob_mean, f32, (S, E), False),
+                                            ("seq_tokens", out.tokens, i32, (S + 2,), False)), dev)
+            if len(own) != 4:
+                raise ValueError("out lacks the outputs of the losses")
+            out._bind(key, io, own)
+        io.seq_offsets = None if seq_offsets is None else _flat(seq_offsets, "seq_offsets", torch.int32, (S + 1,), self._dev)
         return io
 
     def _forward(self, logits, bias, loss_seqs, seq_offsets, out, stream):
-        T, E, k, dev = logits.shape[0], self.num_experts, self.topk, self.device
+        T, E, k, dev = logits.shape[0], self.num_experts, self.topk, self._dev
         if out is None:
             out = self.buffers(T, loss_seqs)
-        ptr, ld = _rows(logits, "logits", self.logits_dtype, T, E, dev)
-        b = None if bias is None else _flat(bias, "bias", torch.float32, (E,), dev)
+        ptr, ld = _rows(logits, "logits", self.logits_dtype, (T, E), dev)
+        b = None if bias is None else _flat(bias, "bias", torch.float32, self._bias_shape, dev)
         idx = _flat(out.topk_idx, "topk_idx", torch.int32, (T, k), dev)
         wts = _flat(out.topk_weights, "topk_weights", torch.float32, (T, k), dev)
         io = ws = None
         if loss_seqs is not None:
             io, ws = self._losses(T, seq_offsets, out), self._workspace.data_ptr()
-        rc = lib().moe_router_forward(self.cfg, T, ptr, ld, b, idx, wts, io, ws, _stream(stream, dev))
+        rc = self._fwd(self.cfg, T, ptr, ld, b, idx, wts, io, ws, _stream(stream, dev))
         if rc:
             _check(rc, "moe_router_forward")
         return out
@@ -267,13 +333,13 @@ class Router:
 
     def balance_loss(self, logits, topk_idx, seq_offsets=None, out=None, stream=None) -> RouterOutput:
         """The losses of a choice made elsewhere."""
-        T, E, dev = logits.shape[0], self.num_experts, self.device
+        T, E, dev = logits.shape[0], self.num_experts, self._dev
         if out is None:
             out = self.buffers(T, 1 if seq_offsets is None else seq_offsets.shape[0] - 1)
-        ptr, ld = _rows(logits, "logits", self.logits_dtype, T, E, dev)
+        ptr, ld = _rows(logits, "logits", self.logits_dtype, (T, E), dev)
         idx = _flat(topk_idx, "topk_idx", torch.int32, (T, self.topk), dev)
         io = self._losses(T, seq_offsets, out)
-        rc = lib().moe_balance_loss(self.cfg, T, ptr, ld, idx, io, self._workspace.data_ptr(), _stream(stream, dev))
+        rc = self._bal(self.cfg, T, ptr, ld, idx, io, self._workspace.data_ptr(), _stream(stream, dev))
         if rc:
             _check(rc, "moe_balance_loss")
         return out
@@ -281,20 +347,20 @@ class Router:
     def backward(self, logits, fwd, d_weights=None, d_loss=None, seq_offsets=None, out=None, stream=None):
         """d_logits through topk_weights (`d_weights` [T, k]) and through loss[0] (`d_loss`, an f32 scalar on the
         device); `fwd` is what the forward call returned."""
-        T, E, k, dev = logits.shape[0], self.num_experts, self.topk, self.device
+        T, E, k, dev = logits.shape[0], self.num_experts, self.topk, self._dev
         if out is None:
-            out = torch.empty(T, E, dtype=self.logits_dtype, device=dev)
-        ptr, ld = _rows(logits, "logits", self.logits_dtype, T, E, dev)
-        dptr, dld = _rows(out, "d_logits", self.logits_dtype, T, E, dev)
+            out = torch.empty(T, E, dtype=self.logits_dtype, device=self.device)
+        ptr, ld = _rows(logits, "logits", self.logits_dtype, (T, E), dev)
+        dptr, dld = _rows(out, "d_logits", self.logits_dtype, (T, E), dev)
         idx = dw = io = dl = None
         if d_weights is not None:
             idx = _flat(fwd.topk_idx, "topk_idx", torch.int32, (T, k), dev)
             dw = _flat(d_weights, "d_weights", torch.float32, (T, k), dev)
         if d_loss is not None:
-            io, dl = self._losses(T, seq_offsets, fwd, write=False), _flat(d_loss, "d_loss", torch.float32, d_loss.shape, dev)
             if d_loss.numel() != 1:
                 raise ValueError("d_loss must hold one value")
-        rc = lib().moe_router_backward(self.cfg, T, ptr, ld, idx, dw, io, dl, dptr, dld, _stream(stream, dev))
+            io, dl = self._losses(T, seq_offsets, fwd, write=False), _flat(d_loss, "d_loss", torch.float32, d_loss.shape, dev)
+        rc = self._bwd(self.cfg, T, ptr, ld, idx, dw, io, dl, dptr, dld, _stream(stream, dev))
         if rc:
             _check(rc, "moe_router_backward")
         return out
@@ -314,10 +380,10 @@ class Fp4Linear:
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "fp4 linear config")
         self.weights = torch.empty(need, dtype=torch.uint8, device=self.device)
-        self._ready = False
+        self._ready, self._dev, self._fwd = False, _index(self.device), lib().moe_fp4_linear_forward
 
     def transform_weights(self, w, w_sf, stream=None):
-        N, K, dev = self.out_features, self.in_features, self.device
+        N, K, dev = self.out_features, self.in_features, self._dev
         wp = _flat(w, "w", torch.uint8, (N, K // 2), dev)
         sp = _flat(w_sf, "w_sf", torch.uint8, (N, K // 32), dev)
         _check(lib().moe_fp4_linear_transform_weights(self.cfg, wp, sp, self.weights.data_ptr(), _stream(stream, dev)),
@@ -330,13 +396,13 @@ class Fp4Linear:
     def forward(self, x, add=None, out=None, stream=None):
         if not self._ready:
             raise MoEError(-6, "moe_fp4_linear_forward")
-        T, n, dev = x.shape[0], self.out_columns, self.device
+        T, n, dev = x.shape[0], self.out_columns, self._dev
         if out is None:
             out = self.buffers(T)
-        xp, ldx = _rows(x, "x", torch.bfloat16, T, self.in_features, dev)
-        yp, ldy = _rows(out, "y", self.out_dtype, T, n, dev)
-        ap, lda = (None, 0) if add is None else _rows(add, "add", self.out_dtype, T, n, dev)
-        rc = lib().moe_fp4_linear_forward(self.cfg, T, xp, ldx, self.weights.data_ptr(), ap, lda, yp, ldy, _stream(stream, dev))
+        xp, ldx = _rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
+        yp, ldy = _rows(out, "y", self.out_dtype, (T, n), dev)
+        ap, lda = (None, 0) if add is None else _rows(add, "add", self.out_dtype, (T, n), dev)
+        rc = self._fwd(self.cfg, T, xp, ldx, self.weights.data_ptr(), ap, lda, yp, ldy, _stream(stream, dev))
         if rc:
             _check(rc, "moe_fp4_linear_forward")
         return out
