@@ -44,7 +44,8 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxM = MOE_FP4_LINEAR_MAX_TOKENS;
-constexpr int kDepth = 4;          // 128-column blocks in flight per warp
+constexpr int kMaxDepth = 8;       // 128-column blocks in flight per warp
+constexpr int kSlotBytes = 1280;   // of one block in shared memory: codes, and every lane's own copy of its scales
 constexpr int kBlockCodes = 1024;  // bytes of a tile's 128-column block
 constexpr int kBlockScales = 64;
 constexpr int kSumShift = 18;      // partial sums are held times 2^-18: |x| up to the bf16 maximum cannot overflow them
@@ -78,19 +79,18 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
         : "r"(w));
 }
 
+// c = A B (the first of a scale group's two), c += A B
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 ld_once(const uint4 *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
 }
 
 // 2^(byte q of s - 127)
@@ -101,13 +101,14 @@ __device__ __forceinline__ float group_scale(uint32_t s) {
 
 __device__ __forceinline__ void add4(float4 &a, const float4 &b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
-struct Block {
-    uint4 lo, hi;   // codes of rows g and g + 8
-    uint2 sc;       // their four scales
-};
+// Waits until at most kDepth - 1 of this thread's groups of copies are under way.
+template <int kDepth>
+__device__ __forceinline__ void wait_block() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+}
 
-template <class O, bool kSwiglu, int NT, bool kCluster>
-__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams p) {
+template <class O, bool kSwiglu, int NT, bool kCluster, int kDepth>
+__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -117,9 +118,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
     const int cta_b0 = kCluster ? p.blocks * rank / p.split : 0;
     const int cta_blocks = (kCluster ? p.blocks * (rank + 1) / p.split : p.blocks) - cta_b0;
     const int max_blocks = kCluster ? (p.blocks + p.split - 1) / p.split : p.blocks;   // the same layout in every CTA
-    // smem: x as halves [block][group][token][t] 16 bytes, the blocks' powers of two [block][16], partial sums
-    uint4 *xs = reinterpret_cast<uint4 *>(smem);
-    float *xe = reinterpret_cast<float *>(smem + (size_t)max_blocks * 4 * M * 64);
+    // smem: the warps' slots, x as halves [block][group][token][t] 16 bytes, the blocks' powers of two [block][16], sums
+    uint8_t *slots = smem + warp * (kDepth * kSlotBytes);
+    uint4 *xs = reinterpret_cast<uint4 *>(smem + kWarps * kDepth * kSlotBytes);
+    float *xe = reinterpret_cast<float *>(xs + max_blocks * 16 * M);
     float4 *red = reinterpret_cast<float4 *>(xe + max_blocks * kMaxM);
     float4 *joined = red + kThreads * NT;   // [other rank][tile][NT][32], in the cluster's first CTA
 
@@ -128,52 +130,79 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
     const int rounds = (my_tiles + tiles_at_once - 1) / tiles_at_once;
     const int kb0 = cta_blocks * wk / p.wk, nkb = cta_blocks * (wk + 1) / p.wk - kb0;   // within the CTA's part
 
-    auto load = [&](int round, int j, Block &b) {
-        const int i = round * tiles_at_once + wn;
-        if (i >= my_tiles || j >= nkb) return;
-        const int64_t at = (int64_t)(group + i * p.groups) * p.blocks + cta_b0 + kb0 + j;
-        const uint4 *c = reinterpret_cast<const uint4 *>(p.codes + at * kBlockCodes);
-        b.lo = ld_once(c + lane);
-        b.hi = ld_once(c + 32 + lane);
-        b.sc = __ldg(reinterpret_cast<const uint2 *>(p.scales + at * kBlockScales) + g);
+    // The warp's blocks, round by round, run through its slots by asynchronous copies: a lane copies what it will read
+    // itself, so that its own wait is all that is needed.
+    const int64_t tile_blocks = (int64_t)p.groups * tiles_at_once * p.blocks;   // from a warp's tile to its next one
+    int64_t in_at = ((int64_t)(group + wn * p.groups)) * p.blocks + cta_b0 + kb0;   // block of the next copy
+    int in_left = nkb, in_i = wn;
+    const uint32_t slot0 = smem_u32(slots), slot_end = slot0 + kDepth * kSlotBytes;
+    uint32_t in_slot = slot0;
+    const uint8_t *codes = p.codes + lane * 16, *scales = p.scales + g * 8;
+    auto copy_next = [&]() {
+        if (in_left > 0 && in_i < my_tiles) {
+            const uint8_t *c = codes + in_at * kBlockCodes;
+            asm volatile(
+                "cp.async.cg.shared.global [%0], [%1], 16;\n\tcp.async.cg.shared.global [%0 + 512], [%1 + 512], 16;" ::"r"(
+                    in_slot + lane * 16),
+                "l"(c)
+                : "memory");
+            asm volatile("cp.async.ca.shared.global [%0 + 1024], [%1], 8;" ::"r"(in_slot + lane * 8),
+                         "l"(scales + in_at * kBlockScales)
+                         : "memory");
+            ++in_at;
+            if (--in_left == 0) in_at += tile_blocks - nkb, in_left = nkb, in_i += tiles_at_once;
+            in_slot += kSlotBytes;
+            if (in_slot == slot_end) in_slot = slot0;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    Block buf[kDepth];
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(0, d, buf[d]);
+#pragma unroll 1
+    for (int d = 0; d < kDepth; ++d) copy_next();
 
-    // x -> halves: a half-warp takes one token's 128-column block at a time
+    // x -> halves: a half-warp takes one block of every token, four tokens' loads at a time
     {
         const int sub = lane & 15;
-        const unsigned half = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;   // the halves may end at different items
-        for (int i = warp * 2 + (lane >> 4); i < cta_blocks * M; i += kWarps * 2) {
-            const int b = i / M, m = i - b * M, k = (cta_b0 + b) * 128 + sub * 8;
-            const bf16 *src = p.x + m * p.ld_x + k;
-            uint32_t v[4] = {0, 0, 0, 0};
-            if (k < p.K) {   // K is a multiple of 32: all eight columns are there
-                if (p.x_vec) {
-                    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src));
-                    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
-                } else {
-                    const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
+        const unsigned half = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;   // the halves may end at different blocks
+        for (int b = warp * 2 + (lane >> 4); b < cta_blocks; b += kWarps * 2) {
+            const int k = (cta_b0 + b) * 128 + sub * 8;
+            for (int m0 = 0; m0 < M; m0 += 4) {
+                uint32_t v[4][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j] = (uint32_t)e[2 * j] | (uint32_t)e[2 * j + 1] << 16;
+                for (int i = 0; i < 4; ++i) {
+                    if (m0 + i >= M) break;
+                    const bf16 *src = p.x + (m0 + i) * p.ld_x + k;
+                    v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;
+                    if (k >= p.K) continue;   // K is a multiple of 32: all eight columns are there or none
+                    if (p.x_vec) {
+                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src));
+                        v[i][0] = q.x, v[i][1] = q.y, v[i][2] = q.z, v[i][3] = q.w;
+                    } else {
+                        const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[i][j] = (uint32_t)e[2 * j] | (uint32_t)e[2 * j + 1] << 16;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = m0 + i;
+                    if (m >= M) break;
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) top = max(top, max(v[i][j] & 0x7FFFu, (v[i][j] >> 16) & 0x7FFFu));
+#pragma unroll
+                    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
+                    const int e = max((int)(top >> 7), 33);   // the largest exponent; 33 keeps 2^(e-141-18) a normal float
+                    const float down = __uint_as_float((uint32_t)(268 - e) << 23);   // 2^(141 - e)
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a = __uint_as_float(v[i][j] << 16) * down, c = __uint_as_float(v[i][j] & 0xFFFF0000u) * down;
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(c), "f"(a));
+                    }
+                    xs[((b * 4 + (sub >> 2)) * M + m) * 4 + (sub & 3)] = make_uint4(h[0], h[1], h[2], h[3]);
+                    if (sub == 0) xe[b * kMaxM + m] = __uint_as_float((uint32_t)(e - 14 - kSumShift) << 23);
                 }
             }
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) top = max(top, max(v[j] & 0x7FFFu, (v[j] >> 16) & 0x7FFFu));
-#pragma unroll
-            for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
-            const int e = max((int)(top >> 7), 33);   // the largest exponent; 33 keeps 2^(e-141-18) a normal float
-            const float down = __uint_as_float((uint32_t)(268 - e) << 23);   // 2^(141 - e)
-            uint32_t h[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float a = __uint_as_float(v[j] << 16) * down, c = __uint_as_float(v[j] & 0xFFFF0000u) * down;
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(c), "f"(a));
-            }
-            xs[((b * 4 + (sub >> 2)) * M + m) * 4 + (sub & 3)] = make_uint4(h[0], h[1], h[2], h[3]);
-            if (sub == 0) xe[b * kMaxM + m] = __uint_as_float((uint32_t)(e - 14 - kSumShift) << 23);
         }
     }
     // every CTA of a cluster has started before another one writes to its shared memory
@@ -184,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
 #pragma unroll
     for (int n = 0; n < NT; ++n) row[n] = min(g + 8 * n, M - 1) * 4 + t;
 
+    int out_slot = 0;
     for (int r = 0; r < rounds; ++r) {
         float acc[NT][4];
 #pragma unroll
@@ -192,15 +222,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
             for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
         const int i_tile = r * tiles_at_once + wn;
         if (i_tile < my_tiles) {
-            for (int j0 = 0; j0 < nkb; j0 += kDepth) {
-#pragma unroll
-                for (int d = 0; d < kDepth; ++d) {
-                    const int j = j0 + d;
-                    if (j >= nkb) break;
-                    const Block b = buf[d];
-                    if (j + kDepth < nkb) load(r, j + kDepth, buf[d]);
-                    else load(r + 1, d, buf[d]);
-                    const uint32_t wl[4] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w}, wh[4] = {b.hi.x, b.hi.y, b.hi.z, b.hi.w};
+            {
+#pragma unroll 1
+                for (int j = 0; j < nkb; ++j) {
+                    wait_block<kDepth>();
+                    const uint8_t *slot = slots + out_slot;
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(slot + lane * 16);
+                    const uint4 hi = *reinterpret_cast<const uint4 *>(slot + 512 + lane * 16);
+                    const uint2 sc = *reinterpret_cast<const uint2 *>(slot + 1024 + lane * 8);
+                    out_slot = out_slot + kSlotBytes == kDepth * kSlotBytes ? 0 : out_slot + kSlotBytes;
+                    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
                     float sum[NT][4];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -212,19 +243,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
                         uint32_t a[4], c[4];
                         e2m1x8(wl[q], a);
                         e2m1x8(wh[q], c);
-                        const float s0 = q == 0   ? group_scale<0>(b.sc.x)
-                                         : q == 1 ? group_scale<1>(b.sc.x)
-                                         : q == 2 ? group_scale<2>(b.sc.x)
-                                                  : group_scale<3>(b.sc.x);
-                        const float s1 = q == 0   ? group_scale<0>(b.sc.y)
-                                         : q == 1 ? group_scale<1>(b.sc.y)
-                                         : q == 2 ? group_scale<2>(b.sc.y)
-                                                  : group_scale<3>(b.sc.y);
+                        const float s0 = q == 0   ? group_scale<0>(sc.x)
+                                         : q == 1 ? group_scale<1>(sc.x)
+                                         : q == 2 ? group_scale<2>(sc.x)
+                                                  : group_scale<3>(sc.x);
+                        const float s1 = q == 0   ? group_scale<0>(sc.y)
+                                         : q == 1 ? group_scale<1>(sc.y)
+                                         : q == 2 ? group_scale<2>(sc.y)
+                                                  : group_scale<3>(sc.y);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const uint4 xv = xb[q * M * 4 + row[n]];
-                            float f[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            mma_f16(f, a[0], c[0], a[1], c[1], xv.x, xv.y);
+                            float f[4];
+                            mma_f16_first(f, a[0], c[0], a[1], c[1], xv.x, xv.y);
                             mma_f16(f, a[2], c[2], a[3], c[3], xv.z, xv.w);
                             sum[n][0] = fmaf(s0, f[0], sum[n][0]);
                             sum[n][1] = fmaf(s0, f[1], sum[n][1]);
@@ -240,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const LinearParams 
                         acc[n][2] = fmaf(e.x, sum[n][2], acc[n][2]);
                         acc[n][3] = fmaf(e.y, sum[n][3], acc[n][3]);
                     }
+                    copy_next();   // into the slot just read
                 }
             }
         }
@@ -370,15 +402,16 @@ Layout layout(const moe_fp4_linear_config *c) {
 }
 
 // Shared memory of a CTA that holds `blocks` blocks of x.
-size_t smem_bytes(int blocks, int M, int split, int tiles_at_once) {
+size_t smem_bytes(int blocks, int M, int split, int tiles_at_once, int depth) {
     const int nt = M > 8 ? 2 : 1;
-    return (size_t)blocks * (256 * M + 4 * kMaxM) + (size_t)(kThreads + (split - 1) * tiles_at_once * 32) * nt * 16;
+    return (size_t)kWarps * depth * kSlotBytes + (size_t)blocks * (256 * M + 4 * kMaxM) +
+           (size_t)(kThreads + (split - 1) * tiles_at_once * 32) * nt * 16;
 }
 
-template <class O, bool kSwiglu, int NT, bool kCluster>
+template <class O, bool kSwiglu, int NT, bool kCluster, int kDepth>
 cudaError_t launch(const LinearParams &p, size_t smem, cudaStream_t s) {
     static std::atomic<uint32_t> done{0};
-    const cudaError_t e = smem_limit_once((const void *)linear_kernel<O, kSwiglu, NT, kCluster>, kMaxSmem, done);
+    const cudaError_t e = smem_limit_once((const void *)linear_kernel<O, kSwiglu, NT, kCluster, kDepth>, kMaxSmem, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(p.groups * p.split);
@@ -391,12 +424,18 @@ cudaError_t launch(const LinearParams &p, size_t smem, cudaStream_t s) {
     a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
     c.attrs = a;
     c.numAttrs = kCluster ? 1 : 0;
-    return cudaLaunchKernelEx(&c, linear_kernel<O, kSwiglu, NT, kCluster>, p);
+    return cudaLaunchKernelEx(&c, linear_kernel<O, kSwiglu, NT, kCluster, kDepth>, p);
+}
+template <class O, bool kSwiglu, int NT, bool kCluster>
+cudaError_t launch(const LinearParams &p, size_t smem, int depth, cudaStream_t s) {
+    return depth == kMaxDepth ? launch<O, kSwiglu, NT, kCluster, kMaxDepth>(p, smem, s)
+                              : launch<O, kSwiglu, NT, kCluster, kMaxDepth / 2>(p, smem, s);
 }
 template <class O, bool kSwiglu>
-cudaError_t launch(const LinearParams &p, size_t smem, cudaStream_t s) {
-    if (p.M > 8) return p.split > 1 ? launch<O, kSwiglu, 2, true>(p, smem, s) : launch<O, kSwiglu, 2, false>(p, smem, s);
-    return p.split > 1 ? launch<O, kSwiglu, 1, true>(p, smem, s) : launch<O, kSwiglu, 1, false>(p, smem, s);
+cudaError_t launch(const LinearParams &p, size_t smem, int depth, cudaStream_t s) {
+    if (p.M > 8)
+        return p.split > 1 ? launch<O, kSwiglu, 2, true>(p, smem, depth, s) : launch<O, kSwiglu, 2, false>(p, smem, depth, s);
+    return p.split > 1 ? launch<O, kSwiglu, 1, true>(p, smem, depth, s) : launch<O, kSwiglu, 1, false>(p, smem, depth, s);
 }
 
 }  // namespace
@@ -457,16 +496,23 @@ int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tokens, con
     // K is split over a cluster where the tokens' x does not fit one CTA's shared memory, or where there are so few
     // tiles that half the SMs would idle and each part keeps 8 blocks
     size_t smem = 0;
+    int depth = kMaxDepth;
     for (p.split = 1;; p.split *= 2) {
         if (p.split > 8) return MOE_ERR_UNSUPPORTED;
         p.groups = std::min(std::max(1, sms / p.split), l.tiles);
-        // one tile per group of wk warps at a time: as many groups as a CTA has tiles
-        const int per_cta = (l.tiles + p.groups - 1) / p.groups;
-        p.wk = kWarps;
-        while (p.wk > 1 && kWarps / p.wk < per_cta) p.wk /= 2;
-        if (p.wk == 1 && num_tokens > 8) p.wk = 2;   // two warps finish the two token groups
-        smem = smem_bytes((l.blocks + p.split - 1) / p.split, num_tokens, p.split, kWarps / p.wk);
-        if (smem > kMaxSmem) continue;
+        const int per_cta = (l.tiles + p.groups - 1) / p.groups, blocks = (l.blocks + p.split - 1) / p.split;
+        // a tile's K over wk warps: the fewest blocks one after the other on a warp, a join counted as one more, among
+        // what fits (two warps at least where there are two token groups to finish)
+        int best = 1 << 30;
+        for (int wk = num_tokens > 8 ? 2 : 1; wk <= kWarps; wk *= 2) {
+            const int rounds = (per_cta * wk + kWarps - 1) / kWarps;
+            const int cost = rounds * ((blocks + wk - 1) / wk + (wk > 1));
+            int d = kMaxDepth;
+            size_t need = smem_bytes(blocks, num_tokens, p.split, kWarps / wk, d);
+            if (need > kMaxSmem) need = smem_bytes(blocks, num_tokens, p.split, kWarps / wk, d /= 2);
+            if (need <= kMaxSmem && cost < best) best = cost, p.wk = wk, depth = d, smem = need;
+        }
+        if (best == 1 << 30) continue;
         if (p.split < 8 && l.tiles * p.split * 2 <= sms && l.blocks / (p.split * 2) >= 8) continue;
         break;
     }
@@ -474,8 +520,8 @@ int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tokens, con
     p.x_vec = aligned_to(x, 16) && ld_x % 8 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f32 = cfg->out_dtype == MOE_DTYPE_F32;
-    const cudaError_t e = swiglu ? (f32 ? launch<float, true>(p, smem, s) : launch<bf16, true>(p, smem, s))
-                                 : (f32 ? launch<float, false>(p, smem, s) : launch<bf16, false>(p, smem, s));
+    const cudaError_t e = swiglu ? (f32 ? launch<float, true>(p, smem, depth, s) : launch<bf16, true>(p, smem, depth, s))
+                                 : (f32 ? launch<float, false>(p, smem, depth, s) : launch<bf16, false>(p, smem, depth, s));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -142,23 +142,18 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     return s;
 }
 
-// FP8 group scale sf = amax / 448 and q = v / sf as v times 448 / amax (either
-// within 2 units in the last place, far inside an E4M3 step).  Below 2^-100
-// the reciprocal would pass the f32 range, so v is brought up by 2^64 first,
-// and from 2^120 on the fast division is out of its range; an all-zero group
-// has sf 0 and codes 0.
+// FP8 group scale sf = amax / 448 and q = v / sf as v times the rounded
+// 448 / amax (within one more rounding of the division: a code differs where v
+// is that near a tie).  Below 2^-100 the reciprocal would pass the f32 range,
+// so v is brought up by 2^64 first; an all-zero group has sf 0 and codes 0.
 struct Fp8Scale {
     float sf, up, inv;
 };
 __device__ __forceinline__ Fp8Scale fp8_scale(float amax) {
     Fp8Scale q;
     q.sf = amax * (1.0f / 448.0f);
-    q.up = 1.0f;
-    q.inv = __fdividef(448.0f, amax);
-    if (!(amax >= 0x1p-100f && amax < 0x1p120f)) {
-        if (amax < 1.0f) q.up = 0x1p64f;
-        q.inv = amax > 0.0f ? 448.0f / (amax * q.up) : 0.0f;
-    }
+    q.up = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+    q.inv = amax > 0.0f ? 448.0f / (amax * q.up) : 0.0f;
     return q;
 }
 
