@@ -409,7 +409,7 @@ MOE_API int moe_router_backward(const moe_router_config *cfg, int num_tokens, co
 typedef enum { MOE_ACT_NONE = 0, MOE_ACT_SWIGLU = 1 } moe_act;
 
 #define MOE_FP4_LINEAR_MAX_TOKENS 16
-#define MOE_FP4_LINEAR_MAX_IN 28672
+#define MOE_FP4_LINEAR_MAX_IN 24576
 
 typedef struct {
     int in_features;   /* K, a multiple of 32, at most MOE_FP4_LINEAR_MAX_IN */

@@ -21,13 +21,16 @@
 // that no partial sum leaves the f32 range that the result stays in; the
 // row's exponent multiplies the finished sum.
 //
-// Layout (written once by moe_fp4_linear_transform_weights): tiles of 16 rows
-// (SWIGLU: 8 gate rows and their 8 up rows), per tile and 128-column block 1 KB
-// of codes in fragment order -- lane (g, t) of a warp loads for row g, then
-// for row g + 8, 16 bytes: word t of each of the block's four scale groups --
-// and 64 bytes of scales.  A word holds 8 consecutive columns, so the
-// fragments of a group use columns in an order of their own, the same for
-// codes and x.
+// Layout (written once by moe_fp4_linear_transform_weights): tiles of 32 rows
+// in two halves of 16 (SWIGLU: 8 gate rows and their 8 up rows each), per tile
+// and 128-column block 2 KB of codes in fragment order -- lane (g, t) of a
+// warp reads for row g, then for row g + 8 of a half, 16 bytes: word t of each
+// of the block's four scale groups -- and 128 bytes of scales.  A word holds 8
+// consecutive columns, so the fragments of a group use columns in an order of
+// their own, the same for codes and x.  Codes and scales of a block lie
+// together (2176 bytes): one stream per warp, and tiles of a power of two of
+// columns do not start on the same few memory partitions (with 64 KB between
+// tiles the 28672 x 4096 product read at 3.5 TB/s).
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
@@ -44,17 +47,17 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxM = MOE_FP4_LINEAR_MAX_TOKENS;
-constexpr int kMaxDepth = 8;       // 128-column blocks in flight per warp
-constexpr int kSlotBytes = 1280;   // of one block in shared memory: codes, and every lane's own copy of its scales
-constexpr int kBlockCodes = 1024;  // bytes of a tile's 128-column block
-constexpr int kBlockScales = 64;
+constexpr int kTileRows = 32;
+constexpr int kBlockCodes = 2048;               // bytes of a tile's 128-column block: codes,
+constexpr int kBlockBytes = kBlockCodes + 128;  // then scales
+constexpr int kMaxDepth = 6;                    // blocks in flight per warp
 constexpr int kSumShift = 18;      // partial sums are held times 2^-18: |x| up to the bf16 maximum cannot overflow them
 constexpr size_t kMaxSmem = 227 * 1024;
 
 struct LinearParams {
     const bf16 *x;
     int64_t ld_x;
-    const uint8_t *codes, *scales;
+    const uint8_t *blocks_at;
     const int32_t *row_exp;
     const void *add;
     int64_t ld_add;
@@ -63,6 +66,8 @@ struct LinearParams {
     int M, K, n_out, tiles, blocks;   // blocks: 128-column blocks of a row
     int split, groups;                // CTAs of a cluster that split K; clusters, which share the tiles
     int wk;                           // warps of a CTA that split its part of K for one tile
+    bool one_round;                   // every warp has one tile at most
+    int depth;                        // blocks in flight per warp: 2, 3, 4 or 6
     float clamp;
     bool x_vec;
 };
@@ -93,25 +98,28 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 2^(byte q of s - 127)
-template <int q>
-__device__ __forceinline__ float group_scale(uint32_t s) {
+// 2^(byte q of s - 127), q known at compile time
+__device__ __forceinline__ float group_scale(uint32_t s, int q) {
     return __uint_as_float((q < 3 ? s << (23 - 8 * q) : s >> 1) & 0x7F800000u);
 }
 
 __device__ __forceinline__ void add4(float4 &a, const float4 &b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
-// Waits until at most kDepth - 1 of this thread's groups of copies are under way.
-template <int kDepth>
-__device__ __forceinline__ void wait_block() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+// Waits until at most depth - 1 of the warp's groups of copies are under way.
+__device__ __forceinline__ void wait_block(int depth) {
+    if (depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (depth == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (depth == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else asm volatile("cp.async.wait_group 5;" ::: "memory");
+    __syncwarp();   // the scales were copied by other lanes
 }
 
-template <class O, bool kSwiglu, int NT, bool kCluster, int kDepth>
+template <class O, bool kSwiglu, int NT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
+    constexpr int kParts = 2 * NT;   // accumulator fragments of a tile: row half u, token group n at 2 n + u
     const int M = p.M;
     const int rank = kCluster ? (int)(blockIdx.x % p.split) : 0;   // clusters are consecutive CTAs
     const int group = kCluster ? (int)(blockIdx.x / p.split) : (int)blockIdx.x;
@@ -119,15 +127,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const int cta_blocks = (kCluster ? p.blocks * (rank + 1) / p.split : p.blocks) - cta_b0;
     const int max_blocks = kCluster ? (p.blocks + p.split - 1) / p.split : p.blocks;   // the same layout in every CTA
     // smem: the warps' slots, x as halves [block][group][token][t] 16 bytes, the blocks' powers of two [block][16], sums
-    uint8_t *slots = smem + warp * (kDepth * kSlotBytes);
-    uint4 *xs = reinterpret_cast<uint4 *>(smem + kWarps * kDepth * kSlotBytes);
+    const int ring = p.depth * kBlockBytes;
+    uint8_t *slots = smem + warp * ring;
+    uint4 *xs = reinterpret_cast<uint4 *>(smem + kWarps * ring);
     float *xe = reinterpret_cast<float *>(xs + max_blocks * 16 * M);
-    float4 *red = reinterpret_cast<float4 *>(xe + max_blocks * kMaxM);
-    float4 *joined = red + kThreads * NT;   // [other rank][tile][NT][32], in the cluster's first CTA
+    float4 *joined = reinterpret_cast<float4 *>(xe + max_blocks * kMaxM);   // [other rank][tile][part][32], in the first CTA
+    float4 *red = joined + (p.split - 1) * (kWarps / p.wk) * kParts * 32;
 
     const int wn = warp / p.wk, wk = warp % p.wk, tiles_at_once = kWarps / p.wk;
     const int my_tiles = (p.tiles - group + p.groups - 1) / p.groups;
     const int rounds = (my_tiles + tiles_at_once - 1) / tiles_at_once;
+    // a lone round leaves the slots free for the join
+    const int red_step = p.one_round ? ring / 16 : kParts * 32;
+    if (p.one_round) red = reinterpret_cast<float4 *>(smem);
     const int kb0 = cta_blocks * wk / p.wk, nkb = cta_blocks * (wk + 1) / p.wk - kb0;   // within the CTA's part
 
     // The warp's blocks, round by round, run through its slots by asynchronous copies: a lane copies what it will read
@@ -135,29 +147,30 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     const int64_t tile_blocks = (int64_t)p.groups * tiles_at_once * p.blocks;   // from a warp's tile to its next one
     int64_t in_at = ((int64_t)(group + wn * p.groups)) * p.blocks + cta_b0 + kb0;   // block of the next copy
     int in_left = nkb, in_i = wn;
-    const uint32_t slot0 = smem_u32(slots), slot_end = slot0 + kDepth * kSlotBytes;
+    const uint32_t slot0 = smem_u32(slots), slot_end = slot0 + ring;
     uint32_t in_slot = slot0;
-    const uint8_t *codes = p.codes + lane * 16, *scales = p.scales + g * 8;
+    const uint8_t *source = p.blocks_at + lane * 16;
     auto copy_next = [&]() {
         if (in_left > 0 && in_i < my_tiles) {
-            const uint8_t *c = codes + in_at * kBlockCodes;
+            const uint8_t *c = source + in_at * kBlockBytes;
             asm volatile(
-                "cp.async.cg.shared.global [%0], [%1], 16;\n\tcp.async.cg.shared.global [%0 + 512], [%1 + 512], 16;" ::"r"(
-                    in_slot + lane * 16),
+                "cp.async.cg.shared.global [%0], [%1], 16;\n\tcp.async.cg.shared.global [%0 + 512], [%1 + 512], 16;\n\t"
+                "cp.async.cg.shared.global [%0 + 1024], [%1 + 1024], 16;\n\t"
+                "cp.async.cg.shared.global [%0 + 1536], [%1 + 1536], 16;" ::"r"(in_slot + lane * 16),
                 "l"(c)
                 : "memory");
-            asm volatile("cp.async.ca.shared.global [%0 + 1024], [%1], 8;" ::"r"(in_slot + lane * 8),
-                         "l"(scales + in_at * kBlockScales)
-                         : "memory");
+            if (lane < 8)
+                asm volatile("cp.async.cg.shared.global [%0 + 2048], [%1 + 2048], 16;" ::"r"(in_slot + lane * 16), "l"(c)
+                             : "memory");
             ++in_at;
             if (--in_left == 0) in_at += tile_blocks - nkb, in_left = nkb, in_i += tiles_at_once;
-            in_slot += kSlotBytes;
+            in_slot += kBlockBytes;
             if (in_slot == slot_end) in_slot = slot0;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
-    for (int d = 0; d < kDepth; ++d) copy_next();
+    for (int d = 0; d < p.depth; ++d) copy_next();
 
     // x -> halves: a half-warp takes one block of every token, four tokens' loads at a time
     {
@@ -186,9 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                 for (int i = 0; i < 4; ++i) {
                     const int m = m0 + i;
                     if (m >= M) break;
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) top = max(top, max(v[i][j] & 0x7FFFu, (v[i][j] >> 16) & 0x7FFFu));
+                    uint32_t top = __vmaxu2(__vmaxu2(v[i][0] & 0x7FFF7FFFu, v[i][1] & 0x7FFF7FFFu),
+                                            __vmaxu2(v[i][2] & 0x7FFF7FFFu, v[i][3] & 0x7FFF7FFFu));
+                    top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
                     for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
                     const int e = max((int)(top >> 7), 33);   // the largest exponent; 33 keeps 2^(e-141-18) a normal float
@@ -215,80 +228,77 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 
     int out_slot = 0;
     for (int r = 0; r < rounds; ++r) {
-        float acc[NT][4];
+        float4 acc[kParts];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+        for (int i = 0; i < kParts; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const int i_tile = r * tiles_at_once + wn;
         if (i_tile < my_tiles) {
-            {
 #pragma unroll 1
-                for (int j = 0; j < nkb; ++j) {
-                    wait_block<kDepth>();
-                    const uint8_t *slot = slots + out_slot;
-                    const uint4 lo = *reinterpret_cast<const uint4 *>(slot + lane * 16);
-                    const uint4 hi = *reinterpret_cast<const uint4 *>(slot + 512 + lane * 16);
-                    const uint2 sc = *reinterpret_cast<const uint2 *>(slot + 1024 + lane * 8);
-                    out_slot = out_slot + kSlotBytes == kDepth * kSlotBytes ? 0 : out_slot + kSlotBytes;
-                    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-                    float sum[NT][4];
+            for (int j = 0; j < nkb; ++j) {
+                wait_block(p.depth);
+                const uint8_t *slot = slots + out_slot;
+                out_slot = out_slot + kBlockBytes == ring ? 0 : out_slot + kBlockBytes;
+                uint32_t w[4][4];   // rows g, g + 8 of the halves; their words of the four groups
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(slot + 512 * i + lane * 16);
+                    w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+                }
+                const uint4 scv = *reinterpret_cast<const uint4 *>(slot + kBlockCodes + g * 16);
+                const uint32_t sc[4] = {scv.x, scv.y, scv.z, scv.w};
+                float2 sum[kParts][2];   // rows g and g + 8, two tokens each
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) sum[n][i] = 0.0f;
-                    const uint4 *xb = xs + (kb0 + j) * 16 * M;
+                for (int i = 0; i < kParts; ++i) sum[i][0] = sum[i][1] = make_float2(0.0f, 0.0f);
+                const uint4 *xb = xs + (kb0 + j) * 16 * M;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 4; ++q) {
+                    uint4 xv[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) xv[n] = xb[q * M * 4 + row[n]];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
                         uint32_t a[4], c[4];
-                        e2m1x8(wl[q], a);
-                        e2m1x8(wh[q], c);
-                        const float s0 = q == 0   ? group_scale<0>(sc.x)
-                                         : q == 1 ? group_scale<1>(sc.x)
-                                         : q == 2 ? group_scale<2>(sc.x)
-                                                  : group_scale<3>(sc.x);
-                        const float s1 = q == 0   ? group_scale<0>(sc.y)
-                                         : q == 1 ? group_scale<1>(sc.y)
-                                         : q == 2 ? group_scale<2>(sc.y)
-                                                  : group_scale<3>(sc.y);
+                        e2m1x8(w[2 * u][q], a);
+                        e2m1x8(w[2 * u + 1][q], c);
+                        const float s0 = group_scale(sc[2 * u], q), s1 = group_scale(sc[2 * u + 1], q);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            const uint4 xv = xb[q * M * 4 + row[n]];
                             float f[4];
-                            mma_f16_first(f, a[0], c[0], a[1], c[1], xv.x, xv.y);
-                            mma_f16(f, a[2], c[2], a[3], c[3], xv.z, xv.w);
-                            sum[n][0] = fmaf(s0, f[0], sum[n][0]);
-                            sum[n][1] = fmaf(s0, f[1], sum[n][1]);
-                            sum[n][2] = fmaf(s1, f[2], sum[n][2]);
-                            sum[n][3] = fmaf(s1, f[3], sum[n][3]);
+                            mma_f16_first(f, a[0], c[0], a[1], c[1], xv[n].x, xv[n].y);
+                            mma_f16(f, a[2], c[2], a[3], c[3], xv[n].z, xv[n].w);
+                            float2(&sm)[2] = sum[2 * n + u];
+                            sm[0] = __ffma2_rn(pair(s0), make_float2(f[0], f[1]), sm[0]);
+                            sm[1] = __ffma2_rn(pair(s1), make_float2(f[2], f[3]), sm[1]);
                         }
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float2 e = *reinterpret_cast<const float2 *>(xe + (kb0 + j) * kMaxM + 8 * n + 2 * t);
-                        acc[n][0] = fmaf(e.x, sum[n][0], acc[n][0]);
-                        acc[n][1] = fmaf(e.y, sum[n][1], acc[n][1]);
-                        acc[n][2] = fmaf(e.x, sum[n][2], acc[n][2]);
-                        acc[n][3] = fmaf(e.y, sum[n][3], acc[n][3]);
-                    }
-                    copy_next();   // into the slot just read
                 }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float2 e = *reinterpret_cast<const float2 *>(xe + (kb0 + j) * kMaxM + 8 * n + 2 * t);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float4 &v = acc[2 * n + u];
+                        const float2 lo = __ffma2_rn(e, sum[2 * n + u][0], make_float2(v.x, v.y));
+                        const float2 hi = __ffma2_rn(e, sum[2 * n + u][1], make_float2(v.z, v.w));
+                        v = make_float4(lo.x, lo.y, hi.x, hi.y);
+                    }
+                }
+                __syncwarp();   // every lane has read the scales
+                copy_next();    // into the slot just read
             }
         }
         if (p.wk > 1) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                red[(warp * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            for (int i = 0; i < kParts; ++i) red[warp * red_step + i * 32 + lane] = acc[i];
             __syncthreads();
         }
-        // warp n of the tile finishes the tokens of column group n (a lone warp all of them)
+        // part i of a tile is finished by the tile's warp i % wk
         if (p.wk > 1 && i_tile < my_tiles) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (wk != n) continue;
-                float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int w = 0; w < p.wk; ++w) add4(s, red[((wn * p.wk + w) * NT + n) * 32 + lane]);
-                acc[n][0] = s.x, acc[n][1] = s.y, acc[n][2] = s.z, acc[n][3] = s.w;
+            for (int i = 0; i < kParts; ++i) {
+                if (i % p.wk != wk) continue;
+                acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int w = 0; w < p.wk; ++w) add4(acc[i], red[(wn * p.wk + w) * red_step + i * 32 + lane]);
             }
         }
         if (kCluster) {
@@ -297,43 +307,41 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (rank > 0 && i_tile < my_tiles) {
                 float4 *dst = cluster.map_shared_rank(joined, 0);
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    if (p.wk == 1 || wk == n)
-                        dst[(((rank - 1) * tiles_at_once + wn) * NT + n) * 32 + lane] =
-                            make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+                for (int i = 0; i < kParts; ++i)
+                    if (i % p.wk == wk) dst[(((rank - 1) * tiles_at_once + wn) * kParts + i) * 32 + lane] = acc[i];
             }
             cluster.sync();
             if (rank == 0 && i_tile < my_tiles) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if (p.wk > 1 && wk != n) continue;
-                    float4 s = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-                    for (int o = 0; o < p.split - 1; ++o) add4(s, joined[((o * tiles_at_once + wn) * NT + n) * 32 + lane]);
-                    acc[n][0] = s.x, acc[n][1] = s.y, acc[n][2] = s.z, acc[n][3] = s.w;
+                for (int i = 0; i < kParts; ++i) {
+                    if (i % p.wk != wk) continue;
+                    for (int o = 0; o < p.split - 1; ++o) add4(acc[i], joined[((o * tiles_at_once + wn) * kParts + i) * 32 + lane]);
                 }
             }
         }
         if (i_tile < my_tiles && rank == 0) {
             const int tile = group + i_tile * p.groups;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (p.wk > 1 && wk != n) continue;
-                const int e0 = p.row_exp[tile * 16 + g], e1 = p.row_exp[tile * 16 + g + 8];
+            for (int part = 0; part < kParts; ++part) {
+                if (part % p.wk != wk) continue;
+                const int u = part & 1, n = part >> 1, first = tile * kTileRows + 16 * u;
+                const int e0 = p.row_exp[first + g], e1 = p.row_exp[first + g + 8];
+                float v[4] = {acc[part].x, acc[part].y, acc[part].z, acc[part].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][i] = ldexpf(acc[n][i], (i < 2 ? e0 : e1) + kSumShift);
+                for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], (i < 2 ? e0 : e1) + kSumShift);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int m = 8 * n + 2 * t + (i & 1);
-                    const int col = kSwiglu ? tile * 8 + g : tile * 16 + g + 8 * (i >> 1);
+                    const int col = kSwiglu ? first / 2 + g : first + g + 8 * (i >> 1);
                     if (m >= M || col >= p.n_out || (kSwiglu && i > 1)) continue;
-                    float v = acc[n][i];
+                    float o = v[i];
                     if (kSwiglu) {
-                        const float gt = fminf(fmaxf(v, -p.clamp), p.clamp);
-                        const float up = fminf(fmaxf(acc[n][(i + 2) & 3], -p.clamp), p.clamp);
-                        v = gt / (1.0f + expf(-gt)) * up;
+                        const float gt = fminf(fmaxf(o, -p.clamp), p.clamp);
+                        const float up = fminf(fmaxf(v[(i + 2) & 3], -p.clamp), p.clamp);
+                        o = gt / (1.0f + expf(-gt)) * up;
                     }
-                    if (p.add) v += to_f32(static_cast<const O *>(p.add)[m * p.ld_add + col]);
-                    static_cast<O *>(p.y)[m * p.ld_y + col] = from_f32<O>(v);
+                    if (p.add) o += to_f32(static_cast<const O *>(p.add)[m * p.ld_add + col]);
+                    static_cast<O *>(p.y)[m * p.ld_y + col] = from_f32<O>(o);
                 }
             }
         }
@@ -343,20 +351,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     }
 }
 
-// Row that slot r (0..15) of a tile holds, or -1.
+// Row that slot r (0..31) of a tile holds, or -1.
 __device__ __forceinline__ int row_of(int tile, int r, int N, bool swiglu) {
     const int n = swiglu ? N / 2 : N;
-    const int i = swiglu ? tile * 8 + (r & 7) : tile * 16 + r;
+    const int i = swiglu ? tile * (kTileRows / 2) + (r >> 4) * 8 + (r & 7) : tile * kTileRows + r;
     if (i >= n) return -1;
-    return swiglu && r >= 8 ? n + i : i;
+    return swiglu && (r & 8) ? n + i : i;
 }
 
 // One warp per (tile, slot): the row's largest scale, its scales relative to that one, its codes in fragment order.
 __global__ void linear_transform_kernel(const uint8_t *w, const uint8_t *w_sf, int N, int K, bool swiglu, int tiles, int blocks,
-                                        uint8_t *codes, uint8_t *scales, int32_t *row_exp) {
+                                        uint8_t *out, int32_t *row_exp) {
     const int lane = threadIdx.x & 31;
     const int slot = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int tile = slot >> 4, r = slot & 15;
+    const int tile = slot / kTileRows, r = slot % kTileRows;
     if (tile >= tiles) return;
     const int row = row_of(tile, r, N, swiglu), groups = K / 32;
     int top = 0;
@@ -367,11 +375,11 @@ __global__ void linear_transform_kernel(const uint8_t *w, const uint8_t *w_sf, i
     for (int i = lane; i < blocks * 4; i += 32) {   // group i of the row
         const int64_t at = (int64_t)tile * blocks + (i >> 2);
         const bool in = row >= 0 && i < groups;
-        // [block][g][row half][4 groups]; a scale 2^-127 or less of the largest one counts as 0
-        scales[at * kBlockScales + (r & 7) * 8 + (r >> 3) * 4 + (i & 3)] =
+        // [block][g][rows g, g + 8, g + 16, g + 24][4 groups]; a scale 2^-127 or less of the largest one counts as 0
+        out[at * kBlockBytes + kBlockCodes + (r & 7) * 16 + (r >> 3) * 4 + (i & 3)] =
             in ? (uint8_t)max(0, 127 + (int)w_sf[(int64_t)row * groups + i] - top) : 0;
         const uint32_t *src = reinterpret_cast<const uint32_t *>(w + (int64_t)row * (K / 2)) + i * 4;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(codes + at * kBlockCodes + (r >> 3) * 512 + (r & 7) * 64);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(out + at * kBlockBytes + (r >> 3) * 512 + (r & 7) * 64);
         for (int t = 0; t < 4; ++t) dst[t * 4 + (i & 3)] = in ? src[t] : 0u;
     }
 }
@@ -388,30 +396,28 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct Layout {
     int tiles, blocks;
-    size_t scales, row_exp, total;   // offsets; codes are at 0
+    size_t row_exp, total;   // offset; the blocks are at 0
 };
 Layout layout(const moe_fp4_linear_config *c) {
     Layout l;
-    l.tiles = c->act == MOE_ACT_SWIGLU ? (c->out_features / 2 + 7) / 8 : (c->out_features + 15) / 16;
+    l.tiles = (c->out_features + kTileRows - 1) / kTileRows;   // of gate and up rows alike
     l.blocks = (c->in_features + 127) / 128;
-    const size_t n = (size_t)l.tiles * l.blocks;
-    l.scales = n * kBlockCodes;
-    l.row_exp = l.scales + up256(n * kBlockScales);
-    l.total = l.row_exp + up256((size_t)l.tiles * 16 * 4);
+    l.row_exp = up256((size_t)l.tiles * l.blocks * kBlockBytes);
+    l.total = l.row_exp + up256((size_t)l.tiles * kTileRows * 4);
     return l;
 }
 
 // Shared memory of a CTA that holds `blocks` blocks of x.
-size_t smem_bytes(int blocks, int M, int split, int tiles_at_once, int depth) {
-    const int nt = M > 8 ? 2 : 1;
-    return (size_t)kWarps * depth * kSlotBytes + (size_t)blocks * (256 * M + 4 * kMaxM) +
-           (size_t)(kThreads + (split - 1) * tiles_at_once * 32) * nt * 16;
+size_t smem_bytes(int blocks, int M, int split, int tiles_at_once, int depth, bool join) {
+    const int parts = M > 8 ? 4 : 2;
+    return (size_t)kWarps * depth * kBlockBytes + (size_t)blocks * (256 * M + 4 * kMaxM) +
+           (size_t)((join ? kThreads : 0) + (split - 1) * tiles_at_once * 32) * parts * 16;
 }
 
-template <class O, bool kSwiglu, int NT, bool kCluster, int kDepth>
+template <class O, bool kSwiglu, int NT, bool kCluster>
 cudaError_t launch(const LinearParams &p, size_t smem, cudaStream_t s) {
     static std::atomic<uint32_t> done{0};
-    const cudaError_t e = smem_limit_once((const void *)linear_kernel<O, kSwiglu, NT, kCluster, kDepth>, kMaxSmem, done);
+    const cudaError_t e = smem_limit_once((const void *)linear_kernel<O, kSwiglu, NT, kCluster>, kMaxSmem, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c = {};
     c.gridDim = dim3(p.groups * p.split);
@@ -424,18 +430,12 @@ cudaError_t launch(const LinearParams &p, size_t smem, cudaStream_t s) {
     a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
     c.attrs = a;
     c.numAttrs = kCluster ? 1 : 0;
-    return cudaLaunchKernelEx(&c, linear_kernel<O, kSwiglu, NT, kCluster, kDepth>, p);
-}
-template <class O, bool kSwiglu, int NT, bool kCluster>
-cudaError_t launch(const LinearParams &p, size_t smem, int depth, cudaStream_t s) {
-    return depth == kMaxDepth ? launch<O, kSwiglu, NT, kCluster, kMaxDepth>(p, smem, s)
-                              : launch<O, kSwiglu, NT, kCluster, kMaxDepth / 2>(p, smem, s);
+    return cudaLaunchKernelEx(&c, linear_kernel<O, kSwiglu, NT, kCluster>, p);
 }
 template <class O, bool kSwiglu>
-cudaError_t launch(const LinearParams &p, size_t smem, int depth, cudaStream_t s) {
-    if (p.M > 8)
-        return p.split > 1 ? launch<O, kSwiglu, 2, true>(p, smem, depth, s) : launch<O, kSwiglu, 2, false>(p, smem, depth, s);
-    return p.split > 1 ? launch<O, kSwiglu, 1, true>(p, smem, depth, s) : launch<O, kSwiglu, 1, false>(p, smem, depth, s);
+cudaError_t launch(const LinearParams &p, size_t smem, cudaStream_t s) {
+    if (p.M > 8) return p.split > 1 ? launch<O, kSwiglu, 2, true>(p, smem, s) : launch<O, kSwiglu, 2, false>(p, smem, s);
+    return p.split > 1 ? launch<O, kSwiglu, 1, true>(p, smem, s) : launch<O, kSwiglu, 1, false>(p, smem, s);
 }
 
 }  // namespace
@@ -453,9 +453,9 @@ int moe_fp4_linear_transform_weights(const moe_fp4_linear_config *cfg, const voi
         return MOE_ERR_INVALID_ARG;
     const Layout l = layout(cfg);
     uint8_t *d = static_cast<uint8_t *>(d_weights);
-    linear_transform_kernel<<<(l.tiles * 16 + 7) / 8, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+    linear_transform_kernel<<<l.tiles * kTileRows / 8, 256, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<const uint8_t *>(w), static_cast<const uint8_t *>(w_sf), cfg->out_features, cfg->in_features,
-        cfg->act == MOE_ACT_SWIGLU, l.tiles, l.blocks, d, d + l.scales, reinterpret_cast<int32_t *>(d + l.row_exp));
+        cfg->act == MOE_ACT_SWIGLU, l.tiles, l.blocks, d, reinterpret_cast<int32_t *>(d + l.row_exp));
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -481,8 +481,7 @@ int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tokens, con
     LinearParams p;
     p.x = static_cast<const bf16 *>(x);
     p.ld_x = ld_x;
-    p.codes = wt;
-    p.scales = wt + l.scales;
+    p.blocks_at = wt;
     p.row_exp = reinterpret_cast<const int32_t *>(wt + l.row_exp);
     p.add = add;
     p.ld_add = ld_add;
@@ -493,35 +492,34 @@ int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tokens, con
     p.n_out = n_out;
     p.tiles = l.tiles;
     p.blocks = l.blocks;
-    // K is split over a cluster where the tokens' x does not fit one CTA's shared memory, or where there are so few
-    // tiles that half the SMs would idle and each part keeps 8 blocks
+    // K over the CTAs of a cluster (split) and the warps of a CTA (wk): the fewest blocks one after the other on a warp,
+    // among what fits in shared memory.  A join of warps counts as one block more, one of CTAs as two.
     size_t smem = 0;
-    int depth = kMaxDepth;
-    for (p.split = 1;; p.split *= 2) {
-        if (p.split > 8) return MOE_ERR_UNSUPPORTED;
-        p.groups = std::min(std::max(1, sms / p.split), l.tiles);
-        const int per_cta = (l.tiles + p.groups - 1) / p.groups, blocks = (l.blocks + p.split - 1) / p.split;
-        // a tile's K over wk warps: the fewest blocks one after the other on a warp, a join counted as one more, among
-        // what fits (two warps at least where there are two token groups to finish)
-        int best = 1 << 30;
-        for (int wk = num_tokens > 8 ? 2 : 1; wk <= kWarps; wk *= 2) {
+    int best = 1 << 30;
+    p.depth = 0;
+    for (int split = 1; split <= 8; split *= 2) {
+        const int groups = std::min(std::max(1, sms / split), l.tiles);
+        const int per_cta = (l.tiles + groups - 1) / groups, blocks = (l.blocks + split - 1) / split;
+        for (int wk = 1; wk <= kWarps; wk *= 2) {
             const int rounds = (per_cta * wk + kWarps - 1) / kWarps;
-            const int cost = rounds * ((blocks + wk - 1) / wk + (wk > 1));
-            int d = kMaxDepth;
-            size_t need = smem_bytes(blocks, num_tokens, p.split, kWarps / wk, d);
-            if (need > kMaxSmem) need = smem_bytes(blocks, num_tokens, p.split, kWarps / wk, d /= 2);
-            if (need <= kMaxSmem && cost < best) best = cost, p.wk = wk, depth = d, smem = need;
+            const int cost = rounds * ((blocks + wk - 1) / wk + (wk > 1) + 2 * (split > 1));
+            if (cost >= best) continue;
+            for (int d : {kMaxDepth, 4, 3, 2}) {
+                const size_t need = smem_bytes(blocks, num_tokens, split, kWarps / wk, d, wk > 1 && rounds > 1);
+                if (need > kMaxSmem) continue;
+                best = cost, smem = need;
+                p.split = split, p.groups = groups, p.wk = wk, p.one_round = rounds == 1, p.depth = d;
+                break;
+            }
         }
-        if (best == 1 << 30) continue;
-        if (p.split < 8 && l.tiles * p.split * 2 <= sms && l.blocks / (p.split * 2) >= 8) continue;
-        break;
     }
+    if (p.depth == 0) return MOE_ERR_UNSUPPORTED;   // no such size within MOE_FP4_LINEAR_MAX_IN
     p.clamp = cfg->act_clamp;
     p.x_vec = aligned_to(x, 16) && ld_x % 8 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f32 = cfg->out_dtype == MOE_DTYPE_F32;
-    const cudaError_t e = swiglu ? (f32 ? launch<float, true>(p, smem, depth, s) : launch<bf16, true>(p, smem, depth, s))
-                                 : (f32 ? launch<float, false>(p, smem, depth, s) : launch<bf16, false>(p, smem, depth, s));
+    const cudaError_t e = swiglu ? (f32 ? launch<float, true>(p, smem, s) : launch<bf16, true>(p, smem, s))
+                                 : (f32 ? launch<float, false>(p, smem, s) : launch<bf16, false>(p, smem, s));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
