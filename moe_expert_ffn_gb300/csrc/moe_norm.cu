@@ -235,8 +235,14 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
             if (p.io.w_pre) load_param8<M>(k_pre[kKeep ? i : 0], p.io.w_pre, p.param_f32, i, tr, threads, H);
         }
     }
+    auto token_gate = [&](int64_t t) {
+        return p.gate == MOE_GATE_TOKEN && t < p.T ? load_param(p.io.gate, p.param_f32, t) : 1.0f;
+    };
+    float gate_ahead = token_gate(t);   // asked for one row ahead
     int turn = 0, slot = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
     for (; t < p.T; t += gridDim.x, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
+        const float gate = gate_ahead;
+        if (!kWarpRow) gate_ahead = token_gate(t + gridDim.x);
         if (kRing) wait_row(slots);
         F8 z[NV], u[NV];
 #pragma unroll
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
                 r1 = rsqrtf(fmaf(row_sum<kWarpRow>(s1.x + s1.y, red[0][turn]), inv_h, p.eps));
                 if (tr == 0 && p.io.rstd_post) p.io.rstd_post[t] = r1;
             }
-            if (p.gate == MOE_GATE_TOKEN) r1 *= load_param(p.io.gate, p.param_f32, t);
+            r1 *= gate;
             S *h = static_cast<S *>(p.io.h) + t * p.io.ld_h;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -382,15 +388,31 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             if (pre) load_param8<M>(k_pre[kKeep ? i : 0], p.io.w_pre, p.param_f32, i, tr, threads, H);
         }
     }
+    // the row's scalars, asked for one row ahead
+    struct Scalars {
+        float r1, r2, g;
+    };
+    auto scalars = [&](int64_t t) {
+        Scalars s{1.0f, 0.0f, 1.0f};
+        if (t < p.T) {
+            if (post) s.r1 = p.io.rstd_post[t];
+            if (pre) s.r2 = p.io.rstd_pre[t];
+            if (token) s.g = load_param(p.io.gate, p.param_f32, t);
+        }
+        return s;
+    };
+    Scalars ahead = scalars(blockIdx.x);
     int slot = 0;
     int turn = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
     for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
         const int64_t next = kWide ? p.T : t + (int64_t)slots * gridDim.x;
+        const Scalars now = ahead;
+        ahead = scalars(t + gridDim.x);
         if (kRing) wait_row(slots);
         F8 D[NV];
         if (pre) {
             if (kWide) fetch_pre(t, 0);
-            const float r2 = p.io.rstd_pre[t];
+            const float r2 = now.r2;
             float2 s2 = pair(0.0f);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -444,8 +466,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             continue;
         }
         if (kWide) fetch_y(t, 0);
-        const float r1 = post ? p.io.rstd_post[t] : 1.0f;
-        const float g = token ? load_param(p.io.gate, p.param_f32, t) : 1.0f, gr = g * r1;
+        const float r1 = now.r1, gr = now.g * r1;
         float2 s1 = pair(0.0f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
