@@ -103,9 +103,9 @@ struct NormFwd {
 template <class S, int NV, Map M, bool kRing>
 struct Feed {
     Raw8<S> v[kRing ? 1 : NV];
-    uint8_t *slots;   // kRing: [slot][NV][threads] 16 (bf16) or 32 (f32) bytes
-    __device__ __forceinline__ uint8_t *at(int slot, int i, int tr, int threads) const {
-        return slots + (size_t)((slot * NV + i) * threads + tr) * (8 * sizeof(S));
+    uint32_t slots;   // kRing: shared address of [slot][NV][threads] 16 (bf16) or 32 (f32) bytes
+    __device__ __forceinline__ uint32_t at(int slot, int i, int tr, int threads) const {
+        return slots + ((slot * NV + i) * threads + tr) * (uint32_t)(8 * sizeof(S));
     }
     __device__ __forceinline__ void fetch(const void *base, int64_t ld, int64_t t, int slot, int tr, int threads, int H) {
         if (!base) return;
@@ -137,12 +137,13 @@ struct Feed {
             if (column<M>(i, 0, tr, threads) >= H)
                 for (int slot = 0; slot < n; ++slot)
                     for (int b = 0; b < (int)sizeof(S) / 2; ++b)
-                        reinterpret_cast<uint4 *>(at(slot, i, tr, threads))[b] = make_uint4(0, 0, 0, 0);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(slot, i, tr, threads) + 16 * b), "r"(0)
+                                     : "memory");
     }
     __device__ __forceinline__ void get(F8 &f, int i, int slot, int tr, int threads) const {
         if (kRing) {
             Raw8<S> r;
-            r.load(reinterpret_cast<const S *>(at(slot, i, tr, threads)));
+            r.load_shared(at(slot, i, tr, threads));
             r.get(f);
         } else {
             v[kRing ? 0 : i].get(f);
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
     const float inv_h = 1.0f / (float)H;
     int64_t t = kWarpRow ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5) : (int64_t)blockIdx.x;
     Feed<S, NV, M, kRing> res, y;
-    res.slots = ring;
-    y.slots = ring + (size_t)slots * NV * threads * 8 * sizeof(S);
+    res.slots = smem_u32(ring);
+    y.slots = res.slots + (uint32_t)(slots * NV * threads * 8 * sizeof(S));
     auto fetch = [&](int64_t t, int slot) {
         if (t < p.T) {
             y.fetch(p.io.y, p.io.ld_y, t, slot, tr, threads, H);
@@ -358,8 +359,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
     constexpr bool kRing = M == kVec && !kWide;
     const int slots = kRing ? p.slots : 1;
     Feed<S, NV, M, kRing> h, y, dh, dn;
-    const size_t tensor = (size_t)slots * NV * threads * 8 * sizeof(S);
-    h.slots = ring, dn.slots = ring + tensor, dh.slots = ring + 2 * tensor, y.slots = ring + 3 * tensor;
+    const uint32_t tensor = (uint32_t)(slots * NV * threads * 8 * sizeof(S));
+    h.slots = smem_u32(ring), dn.slots = h.slots + tensor, dh.slots = dn.slots + tensor, y.slots = dh.slots + tensor;
     auto fetch_pre = [&](int64_t t, int slot) {
         if (t >= p.T || !pre) return;
         h.fetch(p.io.h, p.io.ld_h, t, slot, tr, threads, H);

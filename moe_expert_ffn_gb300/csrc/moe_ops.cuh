@@ -37,10 +37,15 @@ __device__ __forceinline__ uint4 ld_stream16(const void *p) {
     return v;
 }
 
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
 // Asynchronous copy of `bytes` (16 or 32) to shared memory, past L1.
 template <int bytes>
-__device__ __forceinline__ void copy_async(void *smem, const void *src) {
-    const uint32_t d = smem_u32(smem);
+__device__ __forceinline__ void copy_async(uint32_t d, const void *src) {
 #pragma unroll
     for (int i = 0; i < bytes; i += 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d + i), "l"(static_cast<const uint8_t *>(src) + i)
@@ -70,6 +75,7 @@ struct Raw8<bf16> {
     uint4 r;
     __device__ __forceinline__ void load(const bf16 *p) { r = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void load_once(const bf16 *p) { r = ld_stream16(p); }
+    __device__ __forceinline__ void load_shared(uint32_t at) { r = ld_shared16(at); }
     __device__ __forceinline__ void store(bf16 *p) const { *reinterpret_cast<uint4 *>(p) = r; }
     __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(F8 &v) const {
@@ -94,8 +100,9 @@ struct Raw8<float> {
         const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
     }
-    __device__ __forceinline__ void load_once(const float *p) {
-        const uint4 a = ld_stream16(p), b = ld_stream16(p + 4);
+    __device__ __forceinline__ void load_once(const float *p) { put(ld_stream16(p), ld_stream16(p + 4)); }
+    __device__ __forceinline__ void load_shared(uint32_t at) { put(ld_shared16(at), ld_shared16(at + 16)); }
+    __device__ __forceinline__ void put(const uint4 &a, const uint4 &b) {
         f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
         f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
     }
