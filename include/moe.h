@@ -364,6 +364,8 @@ typedef struct {
  * (moe_forward's inactive slot).  +inf counts as the largest finite f32.  The
  * bias takes no part in the scores. */
 
+#define MOE_MAX_SEQS (1 << 20)
+
 /* Losses of a batch of S sequences (token ranges), over the tokens that have
  * an open logit (n_s of sequence s, S' sequences with n_s > 0, N in all), with
  * p the scores scaled to sum 1 and c the chosen slots of each expert:
@@ -371,7 +373,7 @@ typedef struct {
  *   z       = beta / N sum_t logsumexp(logits_t)^2
  * c is a constant for the gradient. */
 typedef struct {
-    int num_seqs;                  /* S >= 1 */
+    int num_seqs;                  /* S, 1..MOE_MAX_SEQS */
     const int32_t *seq_offsets;    /* [S+1] nondecreasing token offsets within [0, T], or NULL: S = 1, all tokens.
                                       Tokens outside every range are routed but enter no loss */
     float *loss;                   /* [3]: total, balance, z */

@@ -90,6 +90,20 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return warp_sum(lane < (int)(blockDim.x >> 5) ? red[lane] : 0.0f);
 }
 
+// The same for R rows of the CTA behind one barrier (`red` R floats per warp).
+template <int R>
+__device__ __forceinline__ void row_sums(float (&v)[R], float *red) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = warp_sum(v[r]);
+    if (lane == 0)
+#pragma unroll
+        for (int r = 0; r < R; ++r) red[r * 32 + (threadIdx.x >> 5)] = v[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = warp_sum(lane < (int)(blockDim.x >> 5) ? red[r * 32 + lane] : 0.0f);
+}
+
 struct NormFwd {
     moe_norm_io io;
     int T, H, quant, gate, slots;
@@ -130,15 +144,19 @@ struct Feed {
             }
         }
     }
-    // Zeros for the chunks past the row's end, which no copy writes.
-    __device__ __forceinline__ void clear_tail(int n, int tr, int threads, int H) {
-        if (!kRing) return;
-        for (int i = 0; i < NV; ++i)
-            if (column<M>(i, 0, tr, threads) >= H)
-                for (int slot = 0; slot < n; ++slot)
+    // Zeros where no copy will write: the chunks past the row's end, and rows past the last one.
+    __device__ __forceinline__ void clear(int n, int tr, int threads, int H) {
+        if (kRing) {
+            for (int slot = 0; slot < n; ++slot)
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
                     for (int b = 0; b < (int)sizeof(S) / 2; ++b)
                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(slot, i, tr, threads) + 16 * b), "r"(0)
                                      : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) v[kRing ? 0 : i].zero();
+        }
     }
     __device__ __forceinline__ void get(F8 &f, int i, int slot, int tr, int threads) const {
         if (kRing) {
@@ -150,6 +168,38 @@ struct Feed {
         }
     }
 };
+// Where a CTA that walks rows keeps its columns' parameters: in registers, in shared memory (each thread its own), or
+// nowhere (loaded for every row).
+enum Keep { kNone, kRegs, kShared };
+template <int NV, Keep K>
+struct Params {
+    F8 reg[K == kRegs ? NV : 1];
+    uint32_t base;   // kShared: shared address of [NV][2][threads] 16 bytes
+    static constexpr int kBytes = K == kShared ? NV * 32 : 0;   // a thread's
+    __device__ __forceinline__ uint32_t at(int i, int half, int tr, int threads) const {
+        return base + ((i * 2 + half) * threads + tr) * 16;
+    }
+    __device__ __forceinline__ void set(int i, const F8 &v, int tr, int threads) {
+        if (K == kRegs) reg[K == kRegs ? i : 0] = v;
+        if (K == kShared)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at(i, h, tr, threads)), "f"(v.p[2 * h].x),
+                             "f"(v.p[2 * h].y), "f"(v.p[2 * h + 1].x), "f"(v.p[2 * h + 1].y)
+                             : "memory");
+    }
+    __device__ __forceinline__ void get(F8 &v, int i, int tr, int threads) const {
+        if (K == kRegs) v = reg[K == kRegs ? i : 0];
+        if (K == kShared)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint4 q = ld_shared16(at(i, h, tr, threads));
+                v.p[2 * h] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+                v.p[2 * h + 1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+            }
+    }
+};
+
 constexpr int kMaxSlots = 4;
 // Waits until at most `slots` - 1 of this thread's groups of copies are under way.
 __device__ __forceinline__ void wait_row(int slots) {
@@ -195,7 +245,7 @@ __device__ __forceinline__ void quantise8(const NormFwd &p, F8 v, int64_t t, int
 
 // A warp takes one row (kWarpRow), or a CTA rows b, b + CTAs, ... with the next `slots` rows on their way and (kKeep) its
 // columns' parameters in registers.
-template <class S, int NV, Map M, bool kWarpRow, bool kKeep, int kMaxThreads, int kMinCtas>
+template <class S, int NV, Map M, bool kWarpRow, Keep kKeep, int kMaxThreads, int kMinCtas>
 __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const __grid_constant__ NormFwd p) {
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][2][32];
@@ -207,6 +257,10 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
     Feed<S, NV, M, kRing> res, y;
     res.slots = smem_u32(ring);
     y.slots = res.slots + (uint32_t)(slots * NV * threads * 8 * sizeof(S));
+    if (kRing && H < NV * 8 * threads) {
+        res.clear(slots, tr, threads, H);
+        y.clear(slots, tr, threads, H);
+    }
     auto fetch = [&](int64_t t, int slot) {
         if (t < p.T) {
             y.fetch(p.io.y, p.io.ld_y, t, slot, tr, threads, H);
@@ -215,8 +269,6 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
         if (kRing) commit_row();
     };
     for (int i = 0; i < slots; ++i) fetch(t + (int64_t)i * gridDim.x, i);
-    res.clear_tail(slots, tr, threads, H);
-    y.clear_tail(slots, tr, threads, H);
     // w_post times a channel's gate (1 where absent)
     auto load_post = [&](F8 &w, int i) {
         if (p.io.w_post) load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
@@ -228,12 +280,21 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
             for (int j = 0; j < 4; ++j) w.p[j] = __fmul2_rn(w.p[j], g.p[j]);
         }
     };
-    F8 k_post[kKeep ? NV : 1], k_pre[kKeep ? NV : 1];
-    if (kKeep) {
+    Params<NV, kKeep> k_post, k_pre;
+    k_post.base = res.slots + (uint32_t)(2 * slots * NV * threads * 8 * sizeof(S));
+    k_pre.base = k_post.base + k_post.kBytes * threads;
+    if (kKeep != kNone) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (p.io.y) load_post(k_post[kKeep ? i : 0], i);
-            if (p.io.w_pre) load_param8<M>(k_pre[kKeep ? i : 0], p.io.w_pre, p.param_f32, i, tr, threads, H);
+            F8 w;
+            if (p.io.y) {
+                load_post(w, i);
+                k_post.set(i, w, tr, threads);
+            }
+            if (p.io.w_pre) {
+                load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+                k_pre.set(i, w, tr, threads);
+            }
         }
     }
     auto token_gate = [&](int64_t t) {
@@ -268,10 +329,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 F8 w;
-                if (!kKeep) load_post(w, i);
+                if (kKeep == kNone) load_post(w, i);
+                else k_post.get(w, i, tr, threads);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    z[i].p[j] = __ffma2_rn(__fmul2_rn(u[i].p[j], kKeep ? k_post[kKeep ? i : 0].p[j] : w.p[j]), pair(r1),
+                    z[i].p[j] = __ffma2_rn(__fmul2_rn(u[i].p[j], w.p[j]), pair(r1),
                                            __fmul2_rn(pair(p.residual_scale), z[i].p[j]));
                 store8<M>(h, z[i], i, tr, threads, H);
             }
@@ -288,10 +350,10 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 F8 w;
-                if (!kKeep) load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+                if (kKeep == kNone) load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+                else k_pre.get(w, i, tr, threads);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    z[i].p[j] = __fmul2_rn(__fmul2_rn(z[i].p[j], pair(r2)), kKeep ? k_pre[kKeep ? i : 0].p[j] : w.p[j]);
+                for (int j = 0; j < 4; ++j) z[i].p[j] = __fmul2_rn(__fmul2_rn(z[i].p[j], pair(r2)), w.p[j]);
                 if (n) store8<M>(n, z[i], i, tr, threads, H);
                 if (M != kStride && p.quant != MOE_QUANT_NONE) quantise8(p, z[i], t, column<M>(i, 0, tr, threads), tr);
             }
@@ -317,12 +379,13 @@ struct NormBwd {
 // CTA b takes rows b, b + CTAs, ...; every thread keeps its columns throughout, so the sums over tokens stay with it
 // until the end: in registers, next to its columns' parameters, or for rows of over 8192 columns (kWide) in shared
 // memory with everything else loaded where it is used.
-template <class S, int NV, Map M, bool kWide, int kMaxThreads, int kMinCtas>
+template <class S, int NV, int R, Map M, bool kWide, int kMaxThreads, int kMinCtas>
 __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const __grid_constant__ NormBwd p) {
     extern __shared__ __align__(16) uint8_t ring[];
     float *wide_acc = reinterpret_cast<float *>(ring);   // kWide: [2][NV][8][threads]
-    __shared__ float red[2][2][32];
+    __shared__ float red[2][2][R * 32];
     const int tr = threadIdx.x, threads = blockDim.x, H = p.H;
+    launch_next();
     const float inv_h = 1.0f / (float)H;
     const bool pre = p.io.dn != nullptr, block = p.io.y != nullptr, post = p.io.w_post != nullptr;
     const bool channel = p.gate == MOE_GATE_CHANNEL, token = p.gate == MOE_GATE_TOKEN;
@@ -358,35 +421,53 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
     };
     constexpr bool kRing = M == kVec && !kWide;
     const int slots = kRing ? p.slots : 1;
-    Feed<S, NV, M, kRing> h, y, dh, dn;
+    Feed<S, NV, M, kRing> h[R], y[R], dh[R], dn[R];
     const uint32_t tensor = (uint32_t)(slots * NV * threads * 8 * sizeof(S));
-    h.slots = smem_u32(ring), dn.slots = h.slots + tensor, dh.slots = dn.slots + tensor, y.slots = dh.slots + tensor;
-    auto fetch_pre = [&](int64_t t, int slot) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        h[r].slots = smem_u32(ring) + 4 * r * tensor;
+        dn[r].slots = h[r].slots + tensor, dh[r].slots = dn[r].slots + tensor, y[r].slots = dh[r].slots + tensor;
+        h[r].clear(slots, tr, threads, H), dn[r].clear(slots, tr, threads, H);
+        dh[r].clear(slots, tr, threads, H), y[r].clear(slots, tr, threads, H);
+    }
+    // row r of the pass that begins at row t
+    auto fetch_pre = [&](int64_t t, int slot, int r) {
+        t += r * (int64_t)gridDim.x;
         if (t >= p.T || !pre) return;
-        h.fetch(p.io.h, p.io.ld_h, t, slot, tr, threads, H);
-        dn.fetch(p.io.dn, p.io.ld_dn, t, slot, tr, threads, H);
+        h[r].fetch(p.io.h, p.io.ld_h, t, slot, tr, threads, H);
+        dn[r].fetch(p.io.dn, p.io.ld_dn, t, slot, tr, threads, H);
     };
-    auto fetch_dh = [&](int64_t t, int slot) {
-        if (t < p.T) dh.fetch(p.io.dh, p.io.ld_dh, t, slot, tr, threads, H);
+    auto fetch_dh = [&](int64_t t, int slot, int r) {
+        t += r * (int64_t)gridDim.x;
+        if (t < p.T) dh[r].fetch(p.io.dh, p.io.ld_dh, t, slot, tr, threads, H);
     };
-    auto fetch_y = [&](int64_t t, int slot) {
-        if (t < p.T) y.fetch(p.io.y, p.io.ld_y, t, slot, tr, threads, H);
-        if (kRing) commit_row();   // the last of a row's copies
+    auto fetch_y = [&](int64_t t, int slot, int r) {
+        t += r * (int64_t)gridDim.x;
+        if (t < p.T) y[r].fetch(p.io.y, p.io.ld_y, t, slot, tr, threads, H);
     };
     if (!kWide)
         for (int i = 0; i < slots; ++i) {
-            const int64_t t = blockIdx.x + (int64_t)i * gridDim.x;
-            fetch_pre(t, i), fetch_dh(t, i), fetch_y(t, i);
+            const int64_t t = blockIdx.x + (int64_t)i * R * gridDim.x;
+#pragma unroll
+            for (int r = 0; r < R; ++r) fetch_pre(t, i, r), fetch_dh(t, i, r), fetch_y(t, i, r);
+            if (kRing) commit_row();
         }
-    constexpr bool kKeep = !kWide;
-    h.clear_tail(slots, tr, threads, H), dn.clear_tail(slots, tr, threads, H);
-    dh.clear_tail(slots, tr, threads, H), y.clear_tail(slots, tr, threads, H);
-    F8 k_scale[kKeep ? NV : 1], k_pre[kKeep ? NV : 1];
-    if (kKeep) {
+    constexpr Keep kKeep = kWide ? kNone : R == 1 ? kRegs : kShared;
+    Params<NV, kKeep> k_scale, k_pre;
+    k_scale.base = h[0].slots + 4 * R * tensor;
+    k_pre.base = k_scale.base + k_scale.kBytes * threads;
+    if (kKeep != kNone) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (block) load_scale(k_scale[kKeep ? i : 0], i);
-            if (pre) load_param8<M>(k_pre[kKeep ? i : 0], p.io.w_pre, p.param_f32, i, tr, threads, H);
+            F8 w;
+            if (block) {
+                load_scale(w, i);
+                k_scale.set(i, w, tr, threads);
+            }
+            if (pre) {
+                load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+                k_pre.set(i, w, tr, threads);
+            }
         }
     }
     // the row's scalars, asked for one row ahead
@@ -402,102 +483,151 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         }
         return s;
     };
-    Scalars ahead = scalars(blockIdx.x);
+    Scalars ahead[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) ahead[r] = scalars(blockIdx.x + r * (int64_t)gridDim.x);
     int slot = 0;
-    int turn = 0;   // the reductions of consecutive rows use different words: one barrier each is enough
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
-        const int64_t next = kWide ? p.T : t + (int64_t)slots * gridDim.x;
-        const Scalars now = ahead;
-        ahead = scalars(t + gridDim.x);
+    int turn = 0;   // the reductions of consecutive passes use different words: one barrier each is enough
+    const int64_t step = (int64_t)R * gridDim.x;
+    for (int64_t t = blockIdx.x; t < p.T; t += step, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
+        const int64_t next = kWide ? p.T : t + slots * step;
+        const bool pair_of_rows = R == 2 && t + gridDim.x < p.T;   // the second row is there
+        Scalars now[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            now[r] = ahead[r];
+            ahead[r] = scalars(t + step + r * (int64_t)gridDim.x);
+        }
         if (kRing) wait_row(slots);
-        F8 D[NV];
+        F8 D[R][NV];   // of a second row that is not there: whatever it holds, nothing is summed or written
         if (pre) {
-            if (kWide) fetch_pre(t, 0);
-            const float r2 = now.r2;
-            float2 s2 = pair(0.0f);
+            float2 s2[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                s2[r] = pair(0.0f);
+                if (kWide) fetch_pre(t, 0, 0);
+            }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                F8 w, hv, v;
-                dn.get(v, i, slot, tr, threads);
-                h.get(hv, i, slot, tr, threads);
-                if (!kKeep) load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
+                F8 w;
+                if (kKeep != kNone) k_pre.get(w, i, tr, threads);
+                else load_param8<M>(w, p.io.w_pre, p.param_f32, i, tr, threads, H);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 th = __fmul2_rn(v.p[j], hv.p[j]), wj = kKeep ? k_pre[kKeep ? i : 0].p[j] : w.p[j];
-                    add(1, i, j, th, pair(r2));
-                    s2 = __ffma2_rn(th, wj, s2);
-                    D[i].p[j] = __fmul2_rn(__fmul2_rn(v.p[j], pair(r2)), wj);
+                for (int r = 0; r < R; ++r) {
+                    if (r == 1 && !pair_of_rows) continue;
+                    F8 hv, v;
+                    dn[r].get(v, i, slot, tr, threads);
+                    h[r].get(hv, i, slot, tr, threads);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 th = __fmul2_rn(v.p[j], hv.p[j]);
+                        add(1, i, j, th, pair(now[r].r2));
+                        s2[r] = __ffma2_rn(th, w.p[j], s2[r]);
+                        D[r][i].p[j] = __fmul2_rn(__fmul2_rn(v.p[j], pair(now[r].r2)), w.p[j]);
+                    }
                 }
             }
-            const float back = row_sum<false>(s2.x + s2.y, red[0][turn]) * inv_h * -(r2 * r2 * r2);
+            float back[R];
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                F8 hv;
-                h.get(hv, i, slot, tr, threads);
+            for (int r = 0; r < R; ++r) back[r] = s2[r].x + s2[r].y;
+            row_sums<R>(back, red[0][turn]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) D[i].p[j] = __ffma2_rn(hv.p[j], pair(back), D[i].p[j]);
+            for (int r = 0; r < R; ++r) {
+                back[r] *= inv_h * -(now[r].r2 * now[r].r2 * now[r].r2);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    F8 hv;
+                    h[r].get(hv, i, slot, tr, threads);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) D[r][i].p[j] = __ffma2_rn(hv.p[j], pair(back[r]), D[r][i].p[j]);
+                }
+                fetch_pre(next, slot, r);
             }
-            fetch_pre(next, slot);
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) D[i].fill(0.0f);
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) D[r][i].fill(0.0f);
         }
-        if (p.io.dh) {
-            if (kWide) fetch_dh(t, 0);
+        const float rs = block ? p.residual_scale : 1.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t tt = t + r * (int64_t)gridDim.x;
+            if (p.io.dh) {
+                if (kWide) fetch_dh(t, 0, 0);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    F8 v;
+                    dh[r].get(v, i, slot, tr, threads);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) D[r][i].p[j] = __fadd2_rn(D[r][i].p[j], v.p[j]);
+                }
+                fetch_dh(next, slot, r);
+            }
+            if (r == 1 && !pair_of_rows) continue;
+            S *dres = static_cast<S *>(p.io.dresidual) + tt * p.io.ld_dresidual;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 F8 v;
-                dh.get(v, i, slot, tr, threads);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) D[i].p[j] = __fadd2_rn(D[i].p[j], v.p[j]);
+                for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(pair(rs), D[r][i].p[j]);
+                store8<M>(dres, v, i, tr, threads, H);
             }
-            fetch_dh(next, slot);
-        }
-        const float rs = block ? p.residual_scale : 1.0f;
-        S *dres = static_cast<S *>(p.io.dresidual) + t * p.io.ld_dresidual;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            F8 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(pair(rs), D[i].p[j]);
-            store8<M>(dres, v, i, tr, threads, H);
         }
         if (!block) {
-            fetch_y(next, slot);
+            if (kRing) commit_row();
             continue;
         }
-        if (kWide) fetch_y(t, 0);
-        const float r1 = now.r1, gr = now.g * r1;
-        float2 s1 = pair(0.0f);
+        float2 s1[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s1[r] = pair(0.0f);
+            if (kWide) fetch_y(t, 0, 0);
+        }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            F8 w, v;
-            if (!kKeep) load_scale(w, i);
-            y.get(v, i, slot, tr, threads);
+            F8 w;
+            if (kKeep != kNone) k_scale.get(w, i, tr, threads);
+            else load_scale(w, i);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 du = __fmul2_rn(D[i].p[j], v.p[j]), wj = kKeep ? k_scale[kKeep ? i : 0].p[j] : w.p[j];
-                add(0, i, j, du, pair(gr));   // r1 is applied to the sums
-                s1 = __ffma2_rn(du, wj, s1);
-                D[i].p[j] = __fmul2_rn(D[i].p[j], wj);
+            for (int r = 0; r < R; ++r) {
+                if (r == 1 && !pair_of_rows) continue;
+                F8 v;
+                y[r].get(v, i, slot, tr, threads);
+                const float gr = now[r].g * now[r].r1;   // r1 is applied to the sums
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 du = __fmul2_rn(D[r][i].p[j], v.p[j]);
+                    add(0, i, j, du, pair(gr));
+                    s1[r] = __ffma2_rn(du, w.p[j], s1[r]);
+                    D[r][i].p[j] = __fmul2_rn(D[r][i].p[j], w.p[j]);
+                }
             }
         }
-        float back = 0.0f;
-        if (post || token) {
-            const float s = row_sum<false>(s1.x + s1.y, red[1][turn]) * r1;
-            if (token && tr == 0) p.io.dgate[t] = s;
-            if (post) back = -s * inv_h * r1;
-        }
-        S *dy = static_cast<S *>(p.io.dy) + t * p.io.ld_dy;
+        float sum[R];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            F8 v;
-            y.get(v, i, slot, tr, threads);
+        for (int r = 0; r < R; ++r) sum[r] = s1[r].x + s1[r].y;
+        if (post || token) row_sums<R>(sum, red[1][turn]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(pair(gr), __ffma2_rn(v.p[j], pair(back), D[i].p[j]));
-            store8<M>(dy, v, i, tr, threads, H);
+        for (int r = 0; r < R; ++r) {
+            const int64_t tt = t + r * (int64_t)gridDim.x;
+            if (r == 0 || pair_of_rows) {
+                const float s = sum[r] * now[r].r1, gr = now[r].g * now[r].r1;
+                if (token && tr == 0) p.io.dgate[tt] = s;
+                const float back = post ? -s * inv_h * now[r].r1 : 0.0f;
+                S *dy = static_cast<S *>(p.io.dy) + tt * p.io.ld_dy;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    F8 v;
+                    y[r].get(v, i, slot, tr, threads);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(pair(gr), __ffma2_rn(v.p[j], pair(back), D[r][i].p[j]));
+                    store8<M>(dy, v, i, tr, threads, H);
+                }
+            }
+            fetch_y(next, slot, r);
         }
-        fetch_y(next, slot);
+        if (kRing) commit_row();   // a pass's copies are one group
     }
     float *part = p.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
@@ -521,10 +651,11 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const NormBwd p, int
     __shared__ float sum[32][33];
     const int H = p.H, lane = threadIdx.x & 31, r0 = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
     const bool channel = p.gate == MOE_GATE_CHANNEL;
+    wait_for_previous();
     if (blockIdx.y == 0 ? !p.io.w_post && !channel : !p.io.dw_pre) return;
     float s = 0.0f;
     if (col < H)
-#pragma unroll 4
+#pragma unroll 8
         for (int r = r0; r < parts; r += 32) s += p.part[((int64_t)r * 2 + blockIdx.y) * H + col];
     sum[r0][lane] = s;
     __syncthreads();
@@ -553,9 +684,12 @@ bool rows16(const void *p, int64_t ld, size_t es) { return !p || (aligned_to(p, 
 
 // Slots of a CTA that shares its SM with ctas - 1 others, `row` bytes each.
 constexpr size_t kRingBytes = 216 * 1024;
-int ring_slots(size_t row, int ctas) { return (int)std::max<size_t>(1, std::min<size_t>(kMaxSlots, kRingBytes / ctas / row)); }
+int ring_slots(size_t row, int ctas, size_t params) {
+    const size_t room = kRingBytes / ctas > params ? kRingBytes / ctas - params : 0;
+    return (int)std::max<size_t>(1, std::min<size_t>(kMaxSlots, room / row));
+}
 
-template <class S, int NV, Map M, bool kWarpRow, bool kKeep, int kMaxThreads, int kMinCtas>
+template <class S, int NV, Map M, bool kWarpRow, Keep kKeep, int kMaxThreads, int kMinCtas>
 cudaError_t launch_fwd(NormFwd p, cudaStream_t s) {
     const int per_thread = 8 * NV * 32;   // columns of a warp
     const int threads = kWarpRow ? 128 : (p.H + per_thread - 1) / per_thread * 32;
@@ -568,8 +702,9 @@ cudaError_t launch_fwd(NormFwd p, cudaStream_t s) {
     size_t smem = 0;
     if (M == kVec) {
         const size_t row = (size_t)2 * NV * threads * 8 * sizeof(S);
-        p.slots = ring_slots(row, per_sm);
-        smem = p.slots * row;
+        const size_t params = (size_t)2 * Params<NV, kKeep>::kBytes * threads;
+        p.slots = ring_slots(row, per_sm, params);
+        smem = p.slots * row + params;
         static std::atomic<uint32_t> done{0};
         const cudaError_t e = smem_limit_once((const void *)kernel, kRingBytes, done);
         if (e != cudaSuccess) return e;
@@ -581,11 +716,13 @@ cudaError_t launch_fwd(NormFwd p, cudaStream_t s) {
 template <class S, Map M>
 cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
     // up to 1024 columns a warp holds the row and no barrier is needed
-    if (p.H <= 256) return launch_fwd<S, 1, M, true, false, 128, 1>(p, s);
-    if (p.H <= 512) return launch_fwd<S, 2, M, true, false, 128, 1>(p, s);
-    if (p.H <= 1024) return launch_fwd<S, 4, M, true, false, 128, 1>(p, s);
-    if (p.H <= 8192) return launch_fwd<S, 2, M, false, true, 512, 1>(p, s);
-    return launch_fwd<S, 2, M, false, false, 1024, 1>(p, s);
+    if (p.H <= 256) return launch_fwd<S, 1, M, true, kNone, 128, 1>(p, s);
+    if (p.H <= 512) return launch_fwd<S, 2, M, true, kNone, 128, 1>(p, s);
+    if (p.H <= 1024) return launch_fwd<S, 4, M, true, kNone, 128, 1>(p, s);
+    // more rows than SMs: two CTAs an SM, so that one works while the other waits at its barrier
+    if (p.H <= 8192 && M == kVec && p.T > 152) return launch_fwd<S, 2, M, false, kShared, 512, 2>(p, s);
+    if (p.H <= 8192) return launch_fwd<S, 2, M, false, kRegs, 512, 1>(p, s);
+    return launch_fwd<S, 2, M, false, kNone, 1024, 1>(p, s);
 }
 
 template <class S>
@@ -599,18 +736,19 @@ cudaError_t launch_fwd_any(const NormFwd &p, cudaStream_t s) {
     return p.quant != MOE_QUANT_NONE ? launch_fwd<S, kChunk>(p, s) : launch_fwd<S, kStride>(p, s);
 }
 
-template <class S, int NV, Map M, bool kWide, int kMaxThreads, int kMinCtas>
+template <class S, int NV, int R, Map M, bool kWide, int kMaxThreads, int kMinCtas>
 cudaError_t launch_bwd(NormBwd p, int parts, cudaStream_t s) {
     const int per_thread = 8 * NV * 32;
     const int threads = (p.H + per_thread - 1) / per_thread * 32;
-    const auto kernel = norm_bwd_kernel<S, NV, M, kWide, kMaxThreads, kMinCtas>;
+    const auto kernel = norm_bwd_kernel<S, NV, R, M, kWide, kMaxThreads, kMinCtas>;
     size_t smem = 0;
     if (kWide) {
         smem = (size_t)2 * NV * 8 * threads * 4;
     } else if (M == kVec) {
-        const size_t row = (size_t)4 * NV * threads * 8 * sizeof(S);
-        p.slots = ring_slots(row, std::max(1, kMaxThreads * kMinCtas / threads));
-        smem = p.slots * row;
+        const size_t row = (size_t)4 * R * NV * threads * 8 * sizeof(S);
+        const size_t params = R == 2 ? (size_t)2 * Params<NV, kShared>::kBytes * threads : 0;
+        p.slots = ring_slots(row, std::max(1, kMaxThreads * kMinCtas / threads), params);
+        smem = p.slots * row + params;
     }
     if (smem > 0) {
         static std::atomic<uint32_t> done{0};
@@ -623,9 +761,13 @@ cudaError_t launch_bwd(NormBwd p, int parts, cudaStream_t s) {
 
 template <class S, Map M>
 cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
-    if (p.H <= 2048) return launch_bwd<S, 1, M, false, 256, 2>(p, parts, s);
-    if (p.H <= 8192) return launch_bwd<S, 2, M, false, 512, 1>(p, parts, s);
-    return launch_bwd<S, 2, M, true, 1024, 1>(p, parts, s);
+    if (p.H <= 2048) return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts, s);
+    if (p.H <= 8192) {
+        // two rows a pass where both fit the CTA's shared memory: half the barriers, and the parameters read once for two
+        if (M == kVec && sizeof(S) == 2) return launch_bwd<S, 2, 2, M, false, 512, 1>(p, parts, s);
+        return launch_bwd<S, 2, 1, M, false, 512, 1>(p, parts, s);
+    }
+    return launch_bwd<S, 2, 1, M, true, 1024, 1>(p, parts, s);
 }
 
 // CTAs of the backward pass: as many as an SM holds (registers: 65536 / (threads x 128)), or the rows.
@@ -732,8 +874,7 @@ int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const moe_norm
     const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_bwd_any<float>(p, parts, s) : launch_bwd_any<bf16>(p, parts, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (sums) {
-        norm_bwd_sum_kernel<<<dim3((H + 31) / 32, 2), 1024, 0, s>>>(p, parts);
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch_after(norm_bwd_sum_kernel, dim3((H + 31) / 32, 2), 1024, s, p, parts) != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
 }

@@ -333,7 +333,10 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_kernel(const
     const int E = p.E, k = p.k;
     int *counts = reinterpret_cast<int *>(joined + kWarps * E);
     const int t0 = (int)min((int64_t)blockIdx.x * p.chunk, (int64_t)p.T), t1 = (int)min((int64_t)t0 + p.chunk, (int64_t)p.T);
-    if (kLoss && blockIdx.x == 0 && threadIdx.x == 0) *p.part.ticket = 0;   // for the next kernel
+    if (kLoss) {
+        launch_next();
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.part.ticket = 0;   // for that kernel
+    }
     float bias[NI];
     if (!kGiven && p.bias) {
 #pragma unroll
@@ -490,7 +493,7 @@ struct SumParams {
     float alpha, beta;
 };
 
-// CTA (x, s): 32 experts of sequence s, its rows summed in order (a thread takes every 8th row, then the 8 are added in
+// CTA (s, x): 32 experts of sequence s, its rows summed in order (a thread takes every 8th row, then the 8 are added in
 // turn).  The last CTA to finish adds up the losses.
 __global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_constant__ SumParams p) {
     __shared__ float sp[kWarps][32];
@@ -498,7 +501,9 @@ __global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_const
     __shared__ float sz[kWarps];
     __shared__ int sn[kWarps];
     __shared__ bool last;
-    const int s = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const int slabs = (p.E + 31) / 32, s = blockIdx.x / slabs, slab = blockIdx.x - s * slabs;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = slab * 32 + lane;
+    wait_for_previous();
     const int a = p.seq_offsets ? max(0, min(p.seq_offsets[s], p.T)) : 0;
     const int b = p.seq_offsets ? max(0, min(p.seq_offsets[s + 1], p.T)) : p.T;
     const int w0 = a / p.chunk, w1 = b > a ? (b - 1) / p.chunk + 1 : w0;
@@ -531,10 +536,10 @@ __global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_const
         }
         const float bal = warp_sum(e < p.E ? (float)c * mean : 0.0f);
         if (lane == 0) {
-            p.part.seq_bal[s * gridDim.x + blockIdx.x] = n > 0 ? bal * (float)p.E / ((float)p.k * (float)n) : 0.0f;
-            if (blockIdx.x == 0) p.seq_tokens[s] = n, p.part.seq_z[s] = z;
+            p.part.seq_bal[blockIdx.x] = n > 0 ? bal * (float)p.E / ((float)p.k * (float)n) : 0.0f;
+            if (slab == 0) p.seq_tokens[s] = n, p.part.seq_z[s] = z;
             __threadfence();
-            last = atomicAdd(p.part.ticket, 1) == (int)(gridDim.x * gridDim.y) - 1;
+            last = atomicAdd(p.part.ticket, 1) == (int)gridDim.x - 1;
         }
     }
     __syncthreads();
@@ -543,7 +548,7 @@ __global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_const
     float bal = 0.0f;
     int used = 0;
     z = 0.0f, n = 0;
-    for (int i = lane; i < p.S * (int)gridDim.x; i += 32) bal += __ldcg(p.part.seq_bal + i);
+    for (int i = lane; i < (int)gridDim.x; i += 32) bal += __ldcg(p.part.seq_bal + i);
     for (int i = lane; i < p.S; i += 32) {
         const int ns = __ldcg(p.seq_tokens + i);
         z += __ldcg(p.part.seq_z + i);
@@ -820,7 +825,7 @@ struct RunBwd {
 };
 
 bool loss_ok(const moe_balance_io *l, const void *ws) {
-    return l->num_seqs >= 1 && (l->seq_offsets || l->num_seqs == 1) && l->loss && l->counts && l->prob_mean &&
+    return l->num_seqs >= 1 && l->num_seqs <= MOE_MAX_SEQS && (l->seq_offsets || l->num_seqs == 1) && l->loss && l->counts && l->prob_mean &&
            l->seq_tokens && ws && aligned_to(ws, 256) && aligned_to(l->seq_offsets, 4) && aligned_to(l->loss, 4) &&
            aligned_to(l->counts, 4) && aligned_to(l->prob_mean, 4) && aligned_to(l->seq_tokens, 4);
 }
@@ -854,8 +859,7 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     if (loss) {
         SumParams q{p.part, p.seq_offsets, loss->counts, loss->prob_mean, loss->seq_tokens, loss->loss, T, p.E, p.k, p.S,
                     p.chunk, cfg->balance_coef, cfg->z_coef};
-        router_seq_kernel<<<dim3((p.E + 31) / 32, p.S), kThreads, 0, s>>>(q);
-        if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch_after(router_seq_kernel, dim3((unsigned)((p.E + 31) / 32) * p.S), kThreads, s, q) != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
 }
@@ -868,7 +872,7 @@ using namespace moe;
 extern "C" {
 
 size_t moe_router_workspace_bytes(const moe_router_config *cfg, int max_tokens, int max_seqs) {
-    if (!valid(cfg) || max_tokens < 0 || max_seqs < 1) return 0;
+    if (!valid(cfg) || max_tokens < 0 || max_seqs < 1 || max_seqs > MOE_MAX_SEQS) return 0;
     return carve(cfg->num_experts, max_tokens, max_seqs, nullptr, nullptr);
 }
 
