@@ -66,12 +66,13 @@ struct RouterParams {
 // A logit as it enters choice and scores: NaN and -inf are closed (-inf), +inf is the largest float.
 __device__ __forceinline__ float open_logit(float v) { return fminf(fmaxf(v, -INFINITY), FLT_MAX); }
 
-// e^v: its relative error is that of the rounded exponent, 2^-24 of |v| log2(e), plus 2 units in the last place.
-__device__ __forceinline__ float exp_of(float v) {
+__device__ __forceinline__ float exp2_of(float v) {
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * kLog2e));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// e^v: its relative error is that of the rounded exponent, 2^-24 of |v| log2(e), plus 2 units in the last place.
+__device__ __forceinline__ float exp_of(float v) { return exp2_of(v * kLog2e); }
 
 // Sigmoid times e^-m with m = min(largest logit, 0): the ratios of the scores of a token whose sigmoids all underflow
 // stay right.
@@ -169,8 +170,19 @@ __device__ __forceinline__ float scores(float (&q)[NI], float (&l)[NI], float &m
 #pragma unroll
             for (int i = 0; i < NI; ++i) z += q[i] = sigmoid_scaled(l[i], ms);
         } else {
+            if (NI % 2 == 0) {
+                float2 zz = pair(0.0f);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) z += q[i] = exp_of(l[i] - m);
+                for (int i = 0; i + 1 < NI; i += 2) {
+                    const float2 v = __fmul2_rn(__fadd2_rn(make_float2(l[i], l[i + 1]), pair(-m)), pair(kLog2e));
+                    q[i] = exp2_of(v.x), q[i + 1] = exp2_of(v.y);
+                    zz = __fadd2_rn(zz, make_float2(q[i], q[i + 1]));
+                }
+                z = zz.x + zz.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) z += q[i] = exp_of(l[i] - m);
+            }
         }
         z = group_sum<G>(z);
         if (!__any_sync(kAll, !(z <= FLT_MAX))) break;
@@ -608,8 +620,21 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_bwd_kernel(c
         }
         const bool dense = n > 0 || (p.d_weights && !p.renorm && !p.sigmoid);   // every probability is needed
         L raw[NI];
+        int next_idx[NS];
+        float next_dw[NS];
+        auto load_slots = [&](int t, bool on) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const int j = s * G + lg;
+                next_idx[s] = on && j < k ? p.topk_idx[(int64_t)t * k + j] : -1;
+                next_dw[s] = on && j < k ? p.d_weights[(int64_t)t * k + j] : 0.0f;
+            }
+        };
         const int tw = a + warp * kGroups;
-        if (tw < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
+        if (tw < cut.end) {
+            load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
+            if (p.d_weights) load_slots(tw + grp, tw + grp < cut.end);
+        }
         for (int tb = tw; tb < cut.end; tb += kWarps * kGroups) {
             const int t = tb + grp;
             const bool on = t < cut.end;
@@ -624,16 +649,12 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_bwd_kernel(c
             if (p.d_weights) {
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
-                    const int j = s * G + lg;
-                    idx[s] = on && j < k ? p.topk_idx[(int64_t)t * k + j] : -1;
-                    if (idx[s] >= E) idx[s] = -1;
-                    ls[s] = -INFINITY;
-                    dw[s] = 0.0f;
-                    if (idx[s] >= 0) {
-                        ls[s] = open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + idx[s]]));
-                        dw[s] = p.d_weights[(int64_t)t * k + j] * p.scale;
-                    }
+                    idx[s] = next_idx[s] < E ? next_idx[s] : -1;
+                    dw[s] = idx[s] >= 0 ? next_dw[s] * p.scale : 0.0f;
+                    ls[s] = idx[s] < 0 ? -INFINITY
+                                       : open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + idx[s]]));
                 }
+                if (tn < cut.end) load_slots(tn + grp, tn + grp < cut.end);
             }
             float m = 0.0f, inv = 0.0f;
             bool real = false;
