@@ -172,49 +172,52 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll 1
     for (int d = 0; d < p.depth; ++d) copy_next();
 
-    // x -> halves: a half-warp takes one block of every token, four tokens' loads at a time
+    // x -> halves: a half-warp takes one token's block at a time, four items' loads together
     {
-        const int sub = lane & 15;
-        const unsigned half = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;   // the halves may end at different blocks
-        for (int b = warp * 2 + (lane >> 4); b < cta_blocks; b += kWarps * 2) {
-            const int k = (cta_b0 + b) * 128 + sub * 8;
-            for (int m0 = 0; m0 < M; m0 += 4) {
-                uint32_t v[4][4];
+        const int sub = lane & 15, items = cta_blocks * M;
+        const unsigned half = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;   // the halves may end at different items
+        const float inv_m = 1.0f / (float)M;
+        for (int i0 = warp * 2 + (lane >> 4); i0 < items; i0 += 4 * 2 * kWarps) {
+            uint32_t v[4][4];
+            int bs[4], ms[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (m0 + i >= M) break;
-                    const bf16 *src = p.x + (m0 + i) * p.ld_x + k;
-                    v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;
-                    if (k >= p.K) continue;   // K is a multiple of 32: all eight columns are there or none
-                    if (p.x_vec) {
-                        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src));
-                        v[i][0] = q.x, v[i][1] = q.y, v[i][2] = q.z, v[i][3] = q.w;
-                    } else {
-                        const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
+            for (int i = 0; i < 4; ++i) {
+                const int item = i0 + i * 2 * kWarps;
+                if (item >= items) break;
+                bs[i] = (int)(((float)item + 0.5f) * inv_m);   // item / M: far from rounding for items < 2^18
+                ms[i] = item - bs[i] * M;
+                const int k = (cta_b0 + bs[i]) * 128 + sub * 8;
+                const bf16 *src = p.x + ms[i] * p.ld_x + k;
+                v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;
+                if (k >= p.K) continue;   // K is a multiple of 32: all eight columns are there or none
+                if (p.x_vec) {
+                    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src));
+                    v[i][0] = q.x, v[i][1] = q.y, v[i][2] = q.z, v[i][3] = q.w;
+                } else {
+                    const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[i][j] = (uint32_t)e[2 * j] | (uint32_t)e[2 * j + 1] << 16;
-                    }
+                    for (int j = 0; j < 4; ++j) v[i][j] = (uint32_t)e[2 * j] | (uint32_t)e[2 * j + 1] << 16;
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int m = m0 + i;
-                    if (m >= M) break;
-                    uint32_t top = __vmaxu2(__vmaxu2(v[i][0] & 0x7FFF7FFFu, v[i][1] & 0x7FFF7FFFu),
-                                            __vmaxu2(v[i][2] & 0x7FFF7FFFu, v[i][3] & 0x7FFF7FFFu));
-                    top = max(top & 0xFFFFu, top >> 16);
+            for (int i = 0; i < 4; ++i) {
+                if (i0 + i * 2 * kWarps >= items) break;
+                uint32_t top = __vmaxu2(__vmaxu2(v[i][0] & 0x7FFF7FFFu, v[i][1] & 0x7FFF7FFFu),
+                                        __vmaxu2(v[i][2] & 0x7FFF7FFFu, v[i][3] & 0x7FFF7FFFu));
+                top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
-                    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
-                    const int e = max((int)(top >> 7), 33);   // the largest exponent; 33 keeps 2^(e-141-18) a normal float
-                    const float down = __uint_as_float((uint32_t)(268 - e) << 23);   // 2^(141 - e)
-                    uint32_t h[4];
+                for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
+                const int e = max((int)(top >> 7), 33);   // the largest exponent; 33 keeps 2^(e-141-18) a normal float
+                const float down = __uint_as_float((uint32_t)(268 - e) << 23);   // 2^(141 - e)
+                uint32_t h[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float a = __uint_as_float(v[i][j] << 16) * down, c = __uint_as_float(v[i][j] & 0xFFFF0000u) * down;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(c), "f"(a));
-                    }
-                    xs[((b * 4 + (sub >> 2)) * M + m) * 4 + (sub & 3)] = make_uint4(h[0], h[1], h[2], h[3]);
-                    if (sub == 0) xe[b * kMaxM + m] = __uint_as_float((uint32_t)(e - 14 - kSumShift) << 23);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = __fmul2_rn(make_float2(__uint_as_float(v[i][j] << 16), __uint_as_float(v[i][j] & 0xFFFF0000u)),
+                                                pair(down));
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(f.y), "f"(f.x));
                 }
+                xs[((bs[i] * 4 + (sub >> 2)) * M + ms[i]) * 4 + (sub & 3)] = make_uint4(h[0], h[1], h[2], h[3]);
+                if (sub == 0) xe[bs[i] * kMaxM + ms[i]] = __uint_as_float((uint32_t)(e - 14 - kSumShift) << 23);
             }
         }
     }
@@ -232,7 +235,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < kParts; ++i) acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         const int i_tile = r * tiles_at_once + wn;
+        int row_e[2][2] = {};   // exponents of rows g, g + 8 of the halves, for the end of the round
         if (i_tile < my_tiles) {
+            const int32_t *e = p.row_exp + (group + i_tile * p.groups) * kTileRows + g;
+            row_e[0][0] = e[0], row_e[0][1] = e[8], row_e[1][0] = e[16], row_e[1][1] = e[24];
 #pragma unroll 1
             for (int j = 0; j < nkb; ++j) {
                 wait_block(p.depth);
@@ -325,10 +331,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             for (int part = 0; part < kParts; ++part) {
                 if (part % p.wk != wk) continue;
                 const int u = part & 1, n = part >> 1, first = tile * kTileRows + 16 * u;
-                const int e0 = p.row_exp[first + g], e1 = p.row_exp[first + g + 8];
                 float v[4] = {acc[part].x, acc[part].y, acc[part].z, acc[part].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = ldexpf(v[i], (i < 2 ? e0 : e1) + kSumShift);
+                for (int i = 0; i < 4; ++i) {   // times 2^(exponent + kSumShift), in two steps that are floats
+                    const int e = row_e[u][i >> 1] + kSumShift, e1 = e >> 1;
+                    v[i] = v[i] * pow2(e1) * pow2(e - e1);
+                }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int m = 8 * n + 2 * t + (i & 1);

@@ -168,6 +168,9 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     return s;
 }
 
+// 2^e, e in [-126, 127].
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
 // FP8 group scale sf = amax / 448 and q = v / sf as v times the rounded
 // 448 / amax (within one more rounding of the division: a code differs where v
 // is that near a tie).  Below 2^-100 the reciprocal would pass the f32 range,
