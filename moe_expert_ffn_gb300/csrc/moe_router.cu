@@ -10,9 +10,11 @@
 // lane sorts its keys with minima and maxima alone, and a round of the choice
 // is one reduction over the lanes' heads, whose winner knows itself.  Whatever
 // f32 bits the expert's number displaced can matter only where two
-// neighbours in the result share all bits above: such a token (1 in some
-// hundreds; none with bf16 logits, which have no such bits) is chosen again
-// from the full keys.
+// neighbours in the result share all bits above (1 token in some hundreds;
+// none with bf16 logits, which have no such bits): those are ranked anew by
+// their full keys, or, at the edge of the chosen, the token is chosen again.
+// (When every such token was chosen again, the few warps that met two of them
+// held up the rest: 17 us for 32767 tokens whose average warp took 11.)
 //
 // Losses: CTAs walk contiguous token ranges, cut where a sequence ends; within
 // a cut every lane sums its experts' probabilities in registers, the CTA's
@@ -286,42 +288,74 @@ template <int NI, int G, int NS, int D>
 __device__ __forceinline__ bool choose(const float (&key)[NI], int k, int lg, bool exact, bool cleaned, int (&slot_e)[NS]) {
     constexpr uint32_t kLow = (uint32_t)(NI * G - 1);   // bits of an expert's number
     constexpr uint32_t kOpen = 0x00800000u;             // the order of the smallest finite float
-    uint32_t v[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
+    auto packed = [&](int i) {
         const uint32_t b = __float_as_uint(key[i] + 0.0f);   // -0 and 0 are equal
         const uint32_t order = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-        v[i] = (order & ~kLow) | (kLow - (uint32_t)(lg + G * i));
-    }
+        return (order & ~kLow) | (kLow - (uint32_t)(lg + G * i));
+    };
+    uint32_t v[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) v[i] = packed(i);
     top_down<NI, D>(v);
     if (!cleaned && __any_sync(kAll, v[0] >= 0xFF800000u)) return false;   // the order of +inf
-    uint32_t slot[NS], out = 0;
+    uint32_t slot[NS], last = 0;
 #pragma unroll
     for (int q = 0; q < NS; ++q) slot[q] = 0;
     for (int j = 0; j < k; ++j) {
-        const uint32_t m = group_max<G>(v[0]);
+        last = group_max<G>(v[0]);
 #pragma unroll
         for (int q = 0; q < NS; ++q)
-            if (j == q * G + lg) slot[q] = m;
-        const bool won = v[0] == m;
+            if (j == q * G + lg) slot[q] = last;
+        const bool won = v[0] == last;
 #pragma unroll
         for (int i = 0; i + 1 < D; ++i) v[i] = won ? v[i + 1] : v[i];
         v[D - 1] = won ? 0u : v[D - 1];
     }
-    bool again = D < NI && v[0] == 0;
-    if (!exact) {   // open neighbours, the first one left outside among them, that only the displaced bits tell apart
-        out = group_max<G>(v[0]);
+    bool again = false;
+    if (D < NI && __any_sync(kAll, v[0] == 0)) {   // a lane gave all it kept: had it more that belong?
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) n += packed(i) >= last;
+        again = n > D;
+    }
+#pragma unroll
+    for (int q = 0; q < NS; ++q) slot_e[q] = slot[q] < kOpen ? -1 : (int)(kLow - (slot[q] & kLow));
+    if (!exact) {   // open neighbours that only the displaced bits tell apart, among the chosen and at their edge
+        const uint32_t out = group_max<G>(v[0]);
+        bool near = false;
 #pragma unroll
         for (int q = 0; q < NS; ++q) {
             uint32_t next = __shfl_down_sync(kAll, slot[q], 1, G);
             const uint32_t wrap = __shfl_sync(kAll, slot[q + 1 < NS ? q + 1 : q], 0, G);
             if (lg == G - 1) next = q + 1 < NS ? wrap : out;
-            if (q * G + lg == k - 1) next = out;
-            again |= q * G + lg < k && slot[q] >= kOpen && ((slot[q] ^ next) & ~kLow) == 0;
+            const bool edge = q * G + lg == k - 1;
+            if (edge) next = out;
+            const bool same = q * G + lg < k && slot[q] >= kOpen && ((slot[q] ^ next) & ~kLow) == 0;
+            near |= same && !edge;
+            again |= same && (edge || NS > 1);
+        }
+        if (NS == 1 && __any_sync(kAll, near) && !__any_sync(kAll, again)) {
+            // the right ones in a wrong order: ranked anew by their full keys
+            const int e = lg < k ? slot_e[0] : -1;
+            float mine = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const float f = __shfl_sync(kAll, key[i], e & (G - 1), G);
+                if (e >= 0 && e / G == i) mine = f;
+            }
+            int rank = 0;   // empty slots (e = -1) stay behind all others
+            for (int j = 0; j < k; ++j) {
+                const float f = __shfl_sync(kAll, mine, j, G);
+                const int fe = __shfl_sync(kAll, e, j, G);
+                rank += f > mine || (f == mine && fe >= 0 && fe < e);
+            }
+            const int held = e;
+            for (int j = 0; j < k; ++j) {
+                const int r = __shfl_sync(kAll, rank, j, G), fe = __shfl_sync(kAll, held, j, G);
+                if (fe >= 0 && r == lg) slot_e[0] = fe;
+            }
         }
     }
-#pragma unroll
-    for (int q = 0; q < NS; ++q) slot_e[q] = slot[q] < kOpen ? -1 : (int)(kLow - (slot[q] & kLow));
     if (__any_sync(kAll, again)) choose_exact<NI, G, NS>(key, k, lg, slot_e);
     return true;
 }
