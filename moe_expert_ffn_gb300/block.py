@@ -8,6 +8,7 @@ loop allocates nothing, and allocates them itself when it gets none.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 
 import torch
@@ -77,10 +78,10 @@ def _flat(t, name, dtype, shape, index):
 class _Outputs:
     """Output tensors of a call and, once checked against an operator, their native description: a later call with the
     same ones only asks them for their addresses.  Replacing a tensor has it checked again."""
-    __slots__ = ("_of", "_io", "_own")
+    __slots__ = ("_of", "_key", "_io", "_own")
 
     def __init__(self):
-        for n in self.__slots__:
+        for n in type(self).__slots__:
             object.__setattr__(self, n, None)
         object.__setattr__(self, "_of", None)
 
@@ -88,11 +89,10 @@ class _Outputs:
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_of", None)
 
-    def _bind(self, key, io, own):
-        """`own`: (tensor, field of io) pairs."""
-        object.__setattr__(self, "_io", io)
-        object.__setattr__(self, "_own", own)
-        object.__setattr__(self, "_of", key)
+    def _bind(self, op, key, io, own):
+        """Checked for calls of `op` described by `key`; `own`: (tensor, field of io) pairs."""
+        for n, v in (("_io", io), ("_own", own), ("_key", key), ("_of", op)):
+            object.__setattr__(self, n, v)
 
 
 class NormOutput(_Outputs):
@@ -120,7 +120,8 @@ class BlockNorm:
                               _choice(GATES, gate, "gate"), _choice(QUANTS, quant, "quant"), float(eps), float(residual_scale))
         if lib().moe_norm_workspace_bytes(self.cfg, 1) == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "norm config")
-        self._workspace, self._dev, self._width = None, _index(self.device), (int(hidden),)
+        self._workspace, self._dev, self._width, self._channel = None, _index(self.device), (int(hidden),), gate == "channel"
+        self._cfg = ctypes.byref(self.cfg)
         self._fwd, self._bwd, self._ws_bytes = lib().moe_norm_forward, lib().moe_norm_backward, lib().moe_norm_workspace_bytes
 
     def buffers(self, num_tokens, block=True, post=True, pre=True, normed=True) -> NormOutput:
@@ -150,10 +151,10 @@ class BlockNorm:
         return g
 
     def _params(self, io, T, w_post, gate, w_pre):
-        dt, dev = self.param_dtype, self._dev
-        io.w_post = None if w_post is None else _flat(w_post, "w_post", dt, self._width, dev)
-        io.gate = None if gate is None else _flat(gate, "gate", dt, self._width if self.gate == "channel" else (T,), dev)
-        io.w_pre = None if w_pre is None else _flat(w_pre, "w_pre", dt, self._width, dev)
+        dt, dev, width = self.param_dtype, self._dev, self._width
+        io.w_post = None if w_post is None else _flat(w_post, "w_post", dt, width, dev)
+        io.gate = None if gate is None else _flat(gate, "gate", dt, width if self._channel else (T,), dev)
+        io.w_pre = None if w_pre is None else _flat(w_pre, "w_pre", dt, width, dev)
 
     @staticmethod
     def _check_all(io, wanted, index):
@@ -175,8 +176,8 @@ class BlockNorm:
         T, H, dt, dev = residual.shape[0], self.hidden, self.dtype, self._dev
         if out is None:
             out = self.buffers(T, y is not None, w_post is not None, w_pre is not None, normed)
-        key = (self, T, y is None, w_post is None, w_pre is None)
-        if out._of == key:
+        key = (T, y is None, w_post is None, w_pre is None)
+        if out._of is self and out._key == key:
             io = out._io
             for t, name in out._own:
                 setattr(io, name, t.data_ptr())
@@ -192,13 +193,13 @@ class BlockNorm:
                 ("sf", out.sf if quant else None, f32 if self.quant == "fp8" else u8, (T, H // (128 if self.quant == "fp8" else 32)), False),
                 ("rstd_post", out.rstd_post if block and w_post is not None else None, f32, (T,), False),
                 ("rstd_pre", out.rstd_pre if pre else None, f32, (T,), False)), dev)
-            out._bind(key, io, own)
+            out._bind(self, key, io, own)
         shape = (T, H)
         io.residual, io.ld_residual = _rows(residual, "residual", dt, shape, dev)
         if y is not None:
             io.y, io.ld_y = _rows(y, "y", dt, shape, dev)
         self._params(io, T, w_post, gate, w_pre)
-        rc = self._fwd(self.cfg, T, io, _stream(stream, dev))
+        rc = self._fwd(self._cfg, T, io, _current_stream(dev) if stream is None else stream.cuda_stream)
         if rc:
             _check(rc, "moe_norm_forward")
         return out
@@ -210,9 +211,9 @@ class BlockNorm:
         T, H, dt, dev, f32 = h.shape[0], self.hidden, self.dtype, self._dev, torch.float32
         if out is None:
             out = self.grad_buffers(T, y is not None, w_post is not None, w_pre is not None)
-        key = (self, T, y is None, w_post is None, w_pre is None, gate is None)
+        key = (T, y is None, w_post is None, w_pre is None, gate is None)
         shape = (T, H)
-        if out._of == key:
+        if out._of is self and out._key == key:
             io = out._io
             for t, name in out._own:
                 setattr(io, name, t.data_ptr())
@@ -222,7 +223,7 @@ class BlockNorm:
                       ("dw_post", out.dw_post if w_post is not None else None, f32, self._width, False),
                       ("dw_pre", out.dw_pre if w_pre is not None else None, f32, self._width, False),
                       ("dgate", out.dgate if gate is not None else None, f32, self._width if self.gate == "channel" else (T,), False))
-            out._bind(key, io, self._check_all(io, wanted, dev))
+            out._bind(self, key, io, self._check_all(io, wanted, dev))
         io.h, io.ld_h = _rows(h, "h", dt, shape, dev)
         self._params(io, T, w_post, gate, w_pre)
         io.dh, io.ld_dh = (None, 0) if dh is None else _rows(dh, "dh", dt, shape, dev)
@@ -231,10 +232,10 @@ class BlockNorm:
             io.y, io.ld_y = _rows(y, "y", dt, shape, dev)
         io.rstd_post = None if w_post is None or rstd_post is None else _flat(rstd_post, "rstd_post", f32, (T,), dev)
         io.rstd_pre = None if w_pre is None or rstd_pre is None else _flat(rstd_pre, "rstd_pre", f32, (T,), dev)
-        need = self._ws_bytes(self.cfg, T)
+        need = self._ws_bytes(self._cfg, T)
         if self._workspace is None or self._workspace.numel() < need:
             self._workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        rc = self._bwd(self.cfg, T, io, self._workspace.data_ptr(), _stream(stream, dev))
+        rc = self._bwd(self._cfg, T, io, self._workspace.data_ptr(), _stream(stream, dev))
         if rc:
             _check(rc, "moe_norm_backward")
         return out
@@ -263,6 +264,7 @@ class Router:
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "router config")
         self._dev, self._bias_shape = _index(self.device), (int(num_experts),)
+        self._cfg = ctypes.byref(self.cfg)
         L = lib()
         self._fwd, self._bal, self._bwd = L.moe_router_forward, L.moe_balance_loss, L.moe_router_backward
         # only the loss calls need it: they need to know max_tokens
@@ -288,8 +290,7 @@ class Router:
         if write and (self.max_tokens is None or T > self.max_tokens or S > self.max_seqs):
             raise ValueError(f"{T} tokens in {S} sequences: the router was made for losses of "
                              f"{self.max_tokens} tokens in {self.max_seqs}")
-        key = (self, S)
-        if out._of == key:
+        if out._of is self and out._key == S:
             io = out._io
             for t, name in out._own:
                 setattr(io, name, t.data_ptr())
@@ -302,7 +303,7 @@ class Router:
                                             ("seq_tokens", out.tokens, i32, (S + 2,), False)), dev)
             if len(own) != 4:
                 raise ValueError("out lacks the outputs of the losses")
-            out._bind(key, io, own)
+            out._bind(self, S, io, own)
         io.seq_offsets = None if seq_offsets is None else _flat(seq_offsets, "seq_offsets", torch.int32, (S + 1,), self._dev)
         return io
 
@@ -317,7 +318,7 @@ class Router:
         io = ws = None
         if loss_seqs is not None:
             io, ws = self._losses(T, seq_offsets, out), self._workspace.data_ptr()
-        rc = self._fwd(self.cfg, T, ptr, ld, b, idx, wts, io, ws, _stream(stream, dev))
+        rc = self._fwd(self._cfg, T, ptr, ld, b, idx, wts, io, ws, _stream(stream, dev))
         if rc:
             _check(rc, "moe_router_forward")
         return out
@@ -339,7 +340,7 @@ class Router:
         ptr, ld = _rows(logits, "logits", self.logits_dtype, (T, E), dev)
         idx = _flat(topk_idx, "topk_idx", torch.int32, (T, self.topk), dev)
         io = self._losses(T, seq_offsets, out)
-        rc = self._bal(self.cfg, T, ptr, ld, idx, io, self._workspace.data_ptr(), _stream(stream, dev))
+        rc = self._bal(self._cfg, T, ptr, ld, idx, io, self._workspace.data_ptr(), _stream(stream, dev))
         if rc:
             _check(rc, "moe_balance_loss")
         return out
@@ -360,7 +361,7 @@ class Router:
             if d_loss.numel() != 1:
                 raise ValueError("d_loss must hold one value")
             io, dl = self._losses(T, seq_offsets, fwd, write=False), _flat(d_loss, "d_loss", torch.float32, d_loss.shape, dev)
-        rc = self._bwd(self.cfg, T, ptr, ld, idx, dw, io, dl, dptr, dld, _stream(stream, dev))
+        rc = self._bwd(self._cfg, T, ptr, ld, idx, dw, io, dl, dptr, dld, _stream(stream, dev))
         if rc:
             _check(rc, "moe_router_backward")
         return out
@@ -380,7 +381,7 @@ class Fp4Linear:
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "fp4 linear config")
         self.weights = torch.empty(need, dtype=torch.uint8, device=self.device)
-        self._ready, self._dev, self._fwd = False, _index(self.device), lib().moe_fp4_linear_forward
+        self._cfg, self._ready, self._dev, self._fwd = ctypes.byref(self.cfg), False, _index(self.device), lib().moe_fp4_linear_forward
 
     def transform_weights(self, w, w_sf, stream=None):
         N, K, dev = self.out_features, self.in_features, self._dev
@@ -402,7 +403,7 @@ class Fp4Linear:
         xp, ldx = _rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
         yp, ldy = _rows(out, "y", self.out_dtype, (T, n), dev)
         ap, lda = (None, 0) if add is None else _rows(add, "add", self.out_dtype, (T, n), dev)
-        rc = self._fwd(self.cfg, T, xp, ldx, self.weights.data_ptr(), ap, lda, yp, ldy, _stream(stream, dev))
+        rc = self._fwd(self._cfg, T, xp, ldx, self.weights.data_ptr(), ap, lda, yp, ldy, _stream(stream, dev))
         if rc:
             _check(rc, "moe_fp4_linear_forward")
         return out
