@@ -318,4 +318,5 @@ class MoELayer:
             pass
 
 
-from .block import BlockNorm, Fp4Linear, NormGrads, NormOutput, Router, RouterOutput  # noqa: E402,F401
+from .block import (FP4_LINEAR_MAX_TOKENS, BlockNorm, Fp4Linear, NormGrads, NormOutput, Router,  # noqa: E402,F401
+                    RouterOutput)
