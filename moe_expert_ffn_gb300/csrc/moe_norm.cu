@@ -201,14 +201,18 @@ struct Params {
 };
 
 constexpr int kMaxSlots = 4;
-// Waits until at most `slots` - 1 of this thread's groups of copies are under way.
-__device__ __forceinline__ void wait_row(int slots) {
-    if (slots == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
-    else if (slots == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-    else if (slots == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+// Waits until at most n of this thread's groups of copies are under way.
+__device__ __forceinline__ void wait_groups(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;   // 2 kMaxSlots - 1
+    }
 }
-__device__ __forceinline__ void commit_row() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 // Codes and scale of a thread's chunk at column c.  A group is 16 (of 128 columns) or 4 (of 32) neighbouring chunks,
 // all of them in the row or none; every lane of the warp calls.
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
             y.fetch(p.io.y, p.io.ld_y, t, slot, tr, threads, H);
             res.fetch(p.io.residual, p.io.ld_residual, t, slot, tr, threads, H);
         }
-        if (kRing) commit_row();
+        if (kRing) commit_group();
     };
     for (int i = 0; i < slots; ++i) fetch(t + (int64_t)i * gridDim.x, i);
     // w_post times a channel's gate (1 where absent)
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
     for (; t < p.T; t += gridDim.x, turn ^= 1, slot = slot + 1 == slots ? 0 : slot + 1) {
         const float gate = gate_ahead;
         if (!kWarpRow) gate_ahead = token_gate(t + gridDim.x);
-        if (kRing) wait_row(slots);
+        if (kRing) wait_groups(slots - 1);
         F8 z[NV], u[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -449,8 +453,11 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         for (int i = 0; i < slots; ++i) {
             const int64_t t = blockIdx.x + (int64_t)i * R * gridDim.x;
 #pragma unroll
-            for (int r = 0; r < R; ++r) fetch_pre(t, i, r), fetch_dh(t, i, r), fetch_y(t, i, r);
-            if (kRing) commit_row();
+            for (int r = 0; r < R; ++r) fetch_pre(t, i, r), fetch_dh(t, i, r);
+            if (kRing) commit_group();
+#pragma unroll
+            for (int r = 0; r < R; ++r) fetch_y(t, i, r);
+            if (kRing) commit_group();
         }
     constexpr Keep kKeep = kWide ? kNone : R == 1 ? kRegs : kShared;
     Params<NV, kKeep> k_scale, k_pre;
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             now[r] = ahead[r];
             ahead[r] = scalars(t + step + r * (int64_t)gridDim.x);
         }
-        if (kRing) wait_row(slots);
+        if (kRing) wait_groups(2 * slots - 1);   // all but y: a pass's copies are two groups
         F8 D[R][NV];   // of a second row that is not there: whatever it holds, nothing is summed or written
         if (pre) {
             float2 s2[R];
@@ -574,10 +581,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
                 store8<M>(dres, v, i, tr, threads, H);
             }
         }
+        if (kRing) commit_group();
         if (!block) {
-            if (kRing) commit_row();
+            if (kRing) commit_group();
             continue;
         }
+        if (kRing) wait_groups(2 * slots - 1);   // y, which was asked for last
         float2 s1[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -627,7 +636,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             }
             fetch_y(next, slot, r);
         }
-        if (kRing) commit_row();   // a pass's copies are one group
+        if (kRing) commit_group();
     }
     float *part = p.part + (int64_t)blockIdx.x * 2 * H;
 #pragma unroll
