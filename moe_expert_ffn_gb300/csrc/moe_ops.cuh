@@ -56,10 +56,9 @@ __device__ __forceinline__ uint4 ld_stream16(const void *p) {
     return v;
 }
 
+// 16 bytes at a shared address, by an ordinary load that the compiler may move among others.
 __device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-    return v;
+    return *reinterpret_cast<const uint4 *>(__cvta_shared_to_generic(at));
 }
 
 // Asynchronous copy of `bytes` (16 or 32) to shared memory, past L1.
