@@ -169,57 +169,62 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll 1
-    for (int d = 0; d < p.depth; ++d) copy_next();
-
-    // x -> halves: a half-warp takes one token's block at a time, four items' loads together
-    {
-        const int sub = lane & 15, items = cta_blocks * M;
-        const unsigned half = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;   // the halves may end at different items
-        const float inv_m = 1.0f / (float)M;
-        for (int i0 = warp * 2 + (lane >> 4); i0 < items; i0 += 4 * 2 * kWarps) {
-            uint32_t v[4][4];
-            int bs[4], ms[4];
+    // x -> halves: a half-warp takes one token's block at a time, kBatch items' loads together.  The first ones are asked
+    // for before the weights, which would otherwise keep them waiting (a microsecond of a one-token call).
+    constexpr int kBatch = NT == 2 ? 8 : 4;
+    const int sub = lane & 15, items = cta_blocks * M, item0 = warp * 2 + (lane >> 4);
+    const unsigned half = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;   // the halves may end at different items
+    const float inv_m = 1.0f / (float)M;
+    uint4 v[kBatch];
+    auto block_of = [&](int item) { return (int)(((float)item + 0.5f) * inv_m); };   // item / M: far from rounding
+    auto load_x = [&](int i0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int item = i0 + i * 2 * kWarps;
-                if (item >= items) break;
-                bs[i] = (int)(((float)item + 0.5f) * inv_m);   // item / M: far from rounding for items < 2^18
-                ms[i] = item - bs[i] * M;
-                const int k = (cta_b0 + bs[i]) * 128 + sub * 8;
-                const bf16 *src = p.x + ms[i] * p.ld_x + k;
-                v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0;
-                if (k >= p.K) continue;   // K is a multiple of 32: all eight columns are there or none
-                if (p.x_vec) {
-                    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src));
-                    v[i][0] = q.x, v[i][1] = q.y, v[i][2] = q.z, v[i][3] = q.w;
-                } else {
-                    const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[i][j] = (uint32_t)e[2 * j] | (uint32_t)e[2 * j + 1] << 16;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i0 + i * 2 * kWarps >= items) break;
-                uint32_t top = __vmaxu2(__vmaxu2(v[i][0] & 0x7FFF7FFFu, v[i][1] & 0x7FFF7FFFu),
-                                        __vmaxu2(v[i][2] & 0x7FFF7FFFu, v[i][3] & 0x7FFF7FFFu));
-                top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-                for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
-                const int e = max((int)(top >> 7), 33);   // the largest exponent; 33 keeps 2^(e-141-18) a normal float
-                const float down = __uint_as_float((uint32_t)(268 - e) << 23);   // 2^(141 - e)
-                uint32_t h[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = __fmul2_rn(make_float2(__uint_as_float(v[i][j] << 16), __uint_as_float(v[i][j] & 0xFFFF0000u)),
-                                                pair(down));
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(f.y), "f"(f.x));
-                }
-                xs[((bs[i] * 4 + (sub >> 2)) * M + ms[i]) * 4 + (sub & 3)] = make_uint4(h[0], h[1], h[2], h[3]);
-                if (sub == 0) xe[bs[i] * kMaxM + ms[i]] = __uint_as_float((uint32_t)(e - 14 - kSumShift) << 23);
+        for (int i = 0; i < kBatch; ++i) {
+            const int item = i0 + i * 2 * kWarps;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (item >= items) continue;
+            const int b = block_of(item), k = (cta_b0 + b) * 128 + sub * 8;
+            if (k >= p.K) continue;   // K is a multiple of 32: all eight columns are there or none
+            const bf16 *src = p.x + (item - b * M) * p.ld_x + k;
+            if (p.x_vec) {
+                v[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+            } else {
+                const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
+                v[i] = make_uint4((uint32_t)e[0] | (uint32_t)e[1] << 16, (uint32_t)e[2] | (uint32_t)e[3] << 16,
+                                  (uint32_t)e[4] | (uint32_t)e[5] << 16, (uint32_t)e[6] | (uint32_t)e[7] << 16);
             }
         }
+    };
+    auto convert_x = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int item = i0 + i * 2 * kWarps;
+            if (item >= items) break;
+            const int b = block_of(item), m = item - b * M;
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+            top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(half, top, o));
+            const int e = max((int)(top >> 7), 33);   // the largest exponent; 33 keeps 2^(e-141-18) a normal float
+            const float down = __uint_as_float((uint32_t)(268 - e) << 23);   // 2^(141 - e)
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = __fmul2_rn(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), pair(down));
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(f.y), "f"(f.x));
+            }
+            xs[((b * 4 + (sub >> 2)) * M + m) * 4 + (sub & 3)] = make_uint4(h[0], h[1], h[2], h[3]);
+            if (sub == 0) xe[b * kMaxM + m] = __uint_as_float((uint32_t)(e - 14 - kSumShift) << 23);
+        }
+    };
+    load_x(item0);
+#pragma unroll 1
+    for (int d = 0; d < p.depth; ++d) copy_next();
+    convert_x(item0);
+    for (int i0 = item0 + kBatch * 2 * kWarps; i0 < items; i0 += kBatch * 2 * kWarps) {
+        load_x(i0);
+        convert_x(i0);
     }
     // every CTA of a cluster has started before another one writes to its shared memory
     if (kCluster) cooperative_groups::this_cluster().sync();
@@ -304,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             for (int i = 0; i < kParts; ++i) {
                 if (i % p.wk != wk) continue;
                 acc[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
                 for (int w = 0; w < p.wk; ++w) add4(acc[i], red[(wn * p.wk + w) * red_step + i * 32 + lane]);
             }
         }
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         }
         // the next round writes `red` and `joined` again, and no CTA leaves while another may still write to it
         if (kCluster) cooperative_groups::this_cluster().sync();
-        else if (p.wk > 1) __syncthreads();
+        else if (p.wk > 1 && !p.one_round) __syncthreads();
     }
 }
 
