@@ -117,6 +117,7 @@ __device__ __forceinline__ void wait_block(int depth) {
 template <class O, bool kSwiglu, int NT, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
+    launch_next();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     constexpr int kParts = 2 * NT;   // accumulator fragments of a tile: row half u, token group n at 2 n + u
@@ -218,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (sub == 0) xe[b * kMaxM + m] = __uint_as_float((uint32_t)(e - 14 - kSumShift) << 23);
         }
     };
+    wait_for_previous();
     load_x(item0);
 #pragma unroll 1
     for (int d = 0; d < p.depth; ++d) copy_next();
@@ -429,27 +431,16 @@ size_t smem_bytes(int blocks, int M, int split, int tiles_at_once, int depth, bo
 }
 
 template <class O, bool kSwiglu, int NT, bool kCluster>
-cudaError_t launch(const LinearParams &p, size_t smem, cudaStream_t s) {
+cudaError_t launch_linear(const LinearParams &p, size_t smem, cudaStream_t s) {
     static std::atomic<uint32_t> done{0};
     const cudaError_t e = smem_limit_once((const void *)linear_kernel<O, kSwiglu, NT, kCluster>, kMaxSmem, done);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(p.groups * p.split);
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    cudaLaunchAttribute a[1];
-    a[0].id = cudaLaunchAttributeClusterDimension;
-    a[0].val.clusterDim.x = p.split;
-    a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
-    c.attrs = a;
-    c.numAttrs = kCluster ? 1 : 0;
-    return cudaLaunchKernelEx(&c, linear_kernel<O, kSwiglu, NT, kCluster>, p);
+    return launch(linear_kernel<O, kSwiglu, NT, kCluster>, p.groups * p.split, kThreads, smem, kCluster ? p.split : 1, s, p);
 }
 template <class O, bool kSwiglu>
-cudaError_t launch(const LinearParams &p, size_t smem, cudaStream_t s) {
-    if (p.M > 8) return p.split > 1 ? launch<O, kSwiglu, 2, true>(p, smem, s) : launch<O, kSwiglu, 2, false>(p, smem, s);
-    return p.split > 1 ? launch<O, kSwiglu, 1, true>(p, smem, s) : launch<O, kSwiglu, 1, false>(p, smem, s);
+cudaError_t launch_linear(const LinearParams &p, size_t smem, cudaStream_t s) {
+    if (p.M > 8) return p.split > 1 ? launch_linear<O, kSwiglu, 2, true>(p, smem, s) : launch_linear<O, kSwiglu, 2, false>(p, smem, s);
+    return p.split > 1 ? launch_linear<O, kSwiglu, 1, true>(p, smem, s) : launch_linear<O, kSwiglu, 1, false>(p, smem, s);
 }
 
 }  // namespace
@@ -529,8 +520,8 @@ int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tokens, con
     p.x_vec = aligned_to(x, 16) && ld_x % 8 == 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool f32 = cfg->out_dtype == MOE_DTYPE_F32;
-    const cudaError_t e = swiglu ? (f32 ? launch<float, true>(p, smem, s) : launch<bf16, true>(p, smem, s))
-                                 : (f32 ? launch<float, false>(p, smem, s) : launch<bf16, false>(p, smem, s));
+    const cudaError_t e = swiglu ? (f32 ? launch_linear<float, true>(p, smem, s) : launch_linear<bf16, true>(p, smem, s))
+                                 : (f32 ? launch_linear<float, false>(p, smem, s) : launch_linear<bf16, false>(p, smem, s));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

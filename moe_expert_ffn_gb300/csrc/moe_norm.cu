@@ -254,6 +254,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][2][32];
     constexpr bool kRing = M == kVec && !kWarpRow;
+    launch_next();
+    wait_for_previous();
     const int tr = kWarpRow ? threadIdx.x & 31 : threadIdx.x, threads = kWarpRow ? 32 : blockDim.x;
     const int H = p.H, slots = kRing ? p.slots : 1;
     const float inv_h = 1.0f / (float)H;
@@ -390,6 +392,7 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
     __shared__ float red[2][2][R * 32];
     const int tr = threadIdx.x, threads = blockDim.x, H = p.H;
     launch_next();
+    wait_for_previous();
     const float inv_h = 1.0f / (float)H;
     const bool pre = p.io.dn != nullptr, block = p.io.y != nullptr, post = p.io.w_post != nullptr;
     const bool channel = p.gate == MOE_GATE_CHANNEL, token = p.gate == MOE_GATE_TOKEN;
@@ -655,23 +658,24 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
 }
 
 // Column sums of the partials, always in the same order: a thread takes every 32nd row, then the 32 are added in turn.
-// A (blockIdx.y = 0) becomes dw_post and a channel's dgate, P (1) is dw_pre.
+// A (even CTAs) becomes dw_post and a channel's dgate, P (odd) is dw_pre.
 __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const NormBwd p, int parts) {
     __shared__ float sum[32][33];
-    const int H = p.H, lane = threadIdx.x & 31, r0 = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    const int H = p.H, lane = threadIdx.x & 31, r0 = threadIdx.x >> 5, which = blockIdx.x & 1, col0 = (blockIdx.x >> 1) * 32;
     const bool channel = p.gate == MOE_GATE_CHANNEL;
+    launch_next();
     wait_for_previous();
-    if (blockIdx.y == 0 ? !p.io.w_post && !channel : !p.io.dw_pre) return;
+    if (which == 0 ? !p.io.w_post && !channel : !p.io.dw_pre) return;
     float s = 0.0f;
-    if (col < H)
+    if (col0 + lane < H)
 #pragma unroll 8
-        for (int r = r0; r < parts; r += 32) s += p.part[((int64_t)r * 2 + blockIdx.y) * H + col];
+        for (int r = r0; r < parts; r += 32) s += p.part[((int64_t)r * 2 + which) * H + col0 + lane];
     sum[r0][lane] = s;
     __syncthreads();
     s = warp_sum(sum[lane][r0]);   // column r0 of the block, the 32 partial rows across the lanes
-    const int out = blockIdx.x * 32 + r0;
+    const int out = col0 + r0;
     if (lane != 0 || out >= H) return;
-    if (blockIdx.y == 1) {
+    if (which == 1) {
         p.io.dw_pre[out] = s;
         return;
     }
@@ -703,10 +707,7 @@ cudaError_t launch_fwd(NormFwd p, cudaStream_t s) {
     const int per_thread = 8 * NV * 32;   // columns of a warp
     const int threads = kWarpRow ? 128 : (p.H + per_thread - 1) / per_thread * 32;
     const auto kernel = norm_fwd_kernel<S, NV, M, kWarpRow, kKeep, kMaxThreads, kMinCtas>;
-    if (kWarpRow) {
-        kernel<<<(p.T + 3) / 4, threads, 0, s>>>(p);
-        return cudaGetLastError();
-    }
+    if (kWarpRow) return launch(kernel, (p.T + 3) / 4, threads, 0, 1, s, p);
     const int per_sm = std::max(1, kMaxThreads * kMinCtas / threads);
     size_t smem = 0;
     if (M == kVec) {
@@ -718,8 +719,7 @@ cudaError_t launch_fwd(NormFwd p, cudaStream_t s) {
         const cudaError_t e = smem_limit_once((const void *)kernel, kRingBytes, done);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<std::min(p.T, 152 * per_sm), threads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch(kernel, std::min(p.T, 152 * per_sm), threads, smem, 1, s, p);
 }
 
 template <class S, Map M>
@@ -764,8 +764,7 @@ cudaError_t launch_bwd(NormBwd p, int parts, cudaStream_t s) {
         const cudaError_t e = smem_limit_once((const void *)kernel, kRingBytes, done);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<parts, threads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch(kernel, parts, threads, smem, 1, s, p);
 }
 
 template <class S, Map M>
@@ -883,7 +882,7 @@ int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const moe_norm
     const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_bwd_any<float>(p, parts, s) : launch_bwd_any<bf16>(p, parts, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (sums) {
-        if (launch_after(norm_bwd_sum_kernel, dim3((H + 31) / 32, 2), 1024, s, p, parts) != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch(norm_bwd_sum_kernel, 2 * ((H + 31) / 32), 1024, 0, 1, s, p, parts) != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
 }

@@ -18,22 +18,28 @@ inline bool valid_dtype(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F3
 inline size_t dtype_bytes(int d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
 inline bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// A kernel that only follows the call's previous one can be set up while that one runs: launch_after() launches it so,
-// the previous one calls launch_next(), and it calls wait_for_previous() (which waits for all of the previous kernel and
-// its stores) before it reads anything.
+// Every kernel here may be set up while the one before it in the stream still runs, which hides most of the 2 to 3 us
+// between two launches: it is launched with launch(), calls launch_next() first of all, and in every thread
+// wait_for_previous() -- which waits until all kernels before it are done and their stores visible -- before it reads what
+// an earlier kernel may have written or writes anything.  A kernel that does not call launch_next() (anybody else's) is
+// waited for as always.
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <class... P, class... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, const A &...args) {
+cudaError_t launch(void (*kernel)(P...), unsigned grid, int threads, size_t smem, int cluster, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t c = {};
-    c.gridDim = grid;
+    c.gridDim = dim3(grid);
     c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
     c.stream = s;
-    cudaLaunchAttribute a[1];
+    cudaLaunchAttribute a[2];
     a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     a[0].val.programmaticStreamSerializationAllowed = 1;
+    a[1].id = cudaLaunchAttributeClusterDimension;
+    a[1].val.clusterDim.x = cluster;
+    a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
     c.attrs = a;
-    c.numAttrs = 1;
+    c.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&c, kernel, args...);
 }
 

@@ -379,10 +379,9 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_kernel(const
     const int E = p.E, k = p.k;
     int *counts = reinterpret_cast<int *>(joined + kWarps * E);
     const int t0 = (int)min((int64_t)blockIdx.x * p.chunk, (int64_t)p.T), t1 = (int)min((int64_t)t0 + p.chunk, (int64_t)p.T);
-    if (kLoss) {
-        launch_next();
-        if (blockIdx.x == 0 && threadIdx.x == 0) *p.part.ticket = 0;   // for that kernel
-    }
+    launch_next();
+    wait_for_previous();
+    if (kLoss && blockIdx.x == 0 && threadIdx.x == 0) *p.part.ticket = 0;   // for the next kernel
     float bias[NI];
     if (!kGiven && p.bias) {
 #pragma unroll
@@ -547,6 +546,7 @@ __global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_const
     __shared__ float sz[kWarps];
     __shared__ int sn[kWarps];
     __shared__ bool last;
+    launch_next();
     const int slabs = (p.E + 31) / 32, s = blockIdx.x / slabs, slab = blockIdx.x - s * slabs;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = slab * 32 + lane;
     wait_for_previous();
@@ -637,6 +637,8 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_bwd_kernel(c
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane & (G - 1), grp = lane / G;
     const int E = p.E, k = p.k;
     float *mine = scatter + (warp * kGroups + grp) * E;
+    launch_next();
+    wait_for_previous();
     if (p.d_weights)
         for (int e = lg; e < E; e += G) mine[e] = 0.0f;
     __syncwarp();
@@ -824,16 +826,13 @@ size_t carve(int E, int T, int S, char *base, Partials *out) {
 template <class L, int NI, int G, int D>
 cudaError_t launch_router(const RouterParams &p, bool loss, int ctas, cudaStream_t s) {
     const size_t smem = (size_t)(kWarps + 1) * p.E * 4;   // at most 36 KB
-    if (loss) router_kernel<L, NI, G, D, true, false><<<ctas, kThreads, smem, s>>>(p);
-    else router_kernel<L, NI, G, D, false, false><<<ctas, kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    if (loss) return launch(router_kernel<L, NI, G, D, true, false>, ctas, kThreads, smem, 1, s, p);
+    return launch(router_kernel<L, NI, G, D, false, false>, ctas, kThreads, 0, 1, s, p);
 }
 template <class L, int NI, int G>
 cudaError_t launch_router(const RouterParams &p, bool loss, bool given, int ctas, cudaStream_t s) {
-    if (given) {
-        router_kernel<L, NI, G, NI, true, true><<<ctas, kThreads, (size_t)(kWarps + 1) * p.E * 4, s>>>(p);
-        return cudaGetLastError();
-    }
+    if (given)
+        return launch(router_kernel<L, NI, G, NI, true, true>, ctas, kThreads, (size_t)(kWarps + 1) * p.E * 4, 1, s, p);
     // up to 12 choices seldom fall four times on one of 32 lanes (1 token in 100 with 12), and four are cheaper to keep
     // in order than 8 and more
     constexpr int kFew = G == 32 && NI > 4 ? 4 : NI;
@@ -873,9 +872,8 @@ struct RunBwd {
     template <int NI, int G>
     cudaError_t run() const {
         const size_t smem = p.d_weights ? (size_t)kWarps * (32 / G) * p.E * 4 : 0;   // at most 32 KB
-        if (bf) router_bwd_kernel<bf16, NI, G><<<ctas, kThreads, smem, s>>>(p);
-        else router_bwd_kernel<float, NI, G><<<ctas, kThreads, smem, s>>>(p);
-        return cudaGetLastError();
+        if (bf) return launch(router_bwd_kernel<bf16, NI, G>, ctas, kThreads, smem, 1, s, p);
+        return launch(router_bwd_kernel<float, NI, G>, ctas, kThreads, smem, 1, s, p);
     }
 };
 
@@ -914,7 +912,7 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     if (loss) {
         SumParams q{p.part, p.seq_offsets, loss->counts, loss->prob_mean, loss->seq_tokens, loss->loss, T, p.E, p.k, p.S,
                     p.chunk, cfg->balance_coef, cfg->z_coef};
-        if (launch_after(router_seq_kernel, dim3((unsigned)((p.E + 31) / 32) * p.S), kThreads, s, q) != cudaSuccess) return MOE_ERR_CUDA;
+        if (launch(router_seq_kernel, (unsigned)((p.E + 31) / 32) * p.S, kThreads, 0, 1, s, q) != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
 }
