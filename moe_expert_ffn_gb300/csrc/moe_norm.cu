@@ -368,9 +368,12 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
     }
 }
 
+// Columns between the rows of partial sums.
+__host__ __device__ __forceinline__ int64_t part_pitch(int H) { return (H + 31) / 32 * 32; }
+
 struct NormBwd {
     moe_norm_grad_io io;
-    float *part;   // [CTAs][2][H]
+    float *part;   // [CTAs][2][part_pitch(H)]
     int T, H, gate, slots;
     bool param_f32;
     float residual_scale;
@@ -641,7 +644,8 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
         }
         if (kRing) commit_group();
     }
-    float *part = p.part + (int64_t)blockIdx.x * 2 * H;
+    const int64_t pitch = part_pitch(H);
+    float *part = p.part + (int64_t)blockIdx.x * 2 * pitch;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         if (!(k == 0 ? post || channel : pre)) continue;
@@ -652,35 +656,49 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
                 for (int j = 0; j < 4; ++j)
                     v.p[j] = reinterpret_cast<float2 *>(wide_acc)[((k * NV + i) * 4 + j) * threads + tr];
             else v = acc[k][kWide ? 0 : i];
-            store8<M>(part + k * H, v, i, tr, threads, H);   // kVec: H % 8 == 0, so these rows are 16-byte aligned too
+            store8<M>(part + k * pitch, v, i, tr, threads, H);
         }
     }
 }
 
-// Column sums of the partials, always in the same order: a thread takes every 32nd row, then the 32 are added in turn.
-// A (even CTAs) becomes dw_post and a channel's dgate, P (odd) is dw_pre.
-__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const NormBwd p, int parts) {
-    __shared__ float sum[32][33];
-    const int H = p.H, lane = threadIdx.x & 31, r0 = threadIdx.x >> 5, which = blockIdx.x & 1, col0 = (blockIdx.x >> 1) * 32;
+// Column sums of the partials, always in the same order: 32 columns a CTA, 8 lanes of 4 columns to a row; a thread takes
+// every kRows-th row, then those are added in turn.  With 32 rows at a time the CTAs are small enough for the first ones
+// to be in place beside the main kernel's.
+template <int kRows>
+__global__ void __launch_bounds__(kRows * 8) norm_bwd_sum_kernel(const __grid_constant__ NormBwd p, int parts) {
+    __shared__ float sum[kRows][33];
+    const int H = p.H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.x & 1, col0 = (blockIdx.x >> 1) * 32;
     const bool channel = p.gate == MOE_GATE_CHANNEL;
     launch_next();
     wait_for_previous();
     if (which == 0 ? !p.io.w_post && !channel : !p.io.dw_pre) return;
-    float s = 0.0f;
-    if (col0 + lane < H)
-#pragma unroll 8
-        for (int r = r0; r < parts; r += 32) s += p.part[((int64_t)r * 2 + which) * H + col0 + lane];
-    sum[r0][lane] = s;
-    __syncthreads();
-    s = warp_sum(sum[lane][r0]);   // column r0 of the block, the 32 partial rows across the lanes
-    const int out = col0 + r0;
-    if (lane != 0 || out >= H) return;
-    if (which == 1) {
-        p.io.dw_pre[out] = s;
-        return;
+    const int r0 = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+    const int64_t pitch = part_pitch(H);
+    const float *at = p.part + which * pitch + col0 + c;   // the padding's columns are read and not used
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 5
+    for (int r = r0; r < parts; r += kRows) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(at + r * 2 * pitch));
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
-    if (p.io.w_post) p.io.dw_post[out] = channel ? s * load_param(p.io.gate, p.param_f32, out) : s;
-    if (channel) p.io.dgate[out] = p.io.w_post ? s * load_param(p.io.w_post, p.param_f32, out) : s;
+    sum[r0][c] = s.x, sum[r0][c + 1] = s.y, sum[r0][c + 2] = s.z, sum[r0][c + 3] = s.w;
+    __syncthreads();
+    constexpr int kWarps = kRows / 4;
+#pragma unroll
+    for (int k = warp; k < 32; k += kWarps) {
+        float v = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kRows; r += 32) v += sum[r + lane][k];
+        v = warp_sum(v);
+        const int out = col0 + k;
+        if (lane != 0 || out >= H) continue;
+        if (which == 1) {
+            p.io.dw_pre[out] = v;
+            continue;
+        }
+        if (p.io.w_post) p.io.dw_post[out] = channel ? v * load_param(p.io.gate, p.param_f32, out) : v;
+        if (channel) p.io.dgate[out] = p.io.w_post ? v * load_param(p.io.w_post, p.param_f32, out) : v;
+    }
 }
 
 bool valid(const moe_norm_config *c) {
@@ -729,7 +747,8 @@ cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
     if (p.H <= 512) return launch_fwd<S, 2, M, true, kNone, 128, 1>(p, s);
     if (p.H <= 1024) return launch_fwd<S, 4, M, true, kNone, 128, 1>(p, s);
     // more rows than SMs: two CTAs an SM, so that one works while the other waits at its barrier
-    if (p.H <= 8192 && M == kVec && p.T > 152) return launch_fwd<S, 2, M, false, kShared, 512, 2>(p, s);
+    if constexpr (M == kVec)
+        if (p.H <= 8192 && p.T > 152) return launch_fwd<S, 2, M, false, kShared, 512, 2>(p, s);
     if (p.H <= 8192) return launch_fwd<S, 2, M, false, kRegs, 512, 1>(p, s);
     return launch_fwd<S, 2, M, false, kNone, 1024, 1>(p, s);
 }
@@ -772,8 +791,8 @@ cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
     if (p.H <= 2048) return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts, s);
     if (p.H <= 8192) {
         // two rows a pass where both fit the CTA's shared memory: half the barriers, and the parameters read once for two
-        if (M == kVec && sizeof(S) == 2) return launch_bwd<S, 2, 2, M, false, 512, 1>(p, parts, s);
-        return launch_bwd<S, 2, 1, M, false, 512, 1>(p, parts, s);
+        if constexpr (M == kVec && sizeof(S) == 2) return launch_bwd<S, 2, 2, M, false, 512, 1>(p, parts, s);
+        else return launch_bwd<S, 2, 1, M, false, 512, 1>(p, parts, s);
     }
     return launch_bwd<S, 2, 1, M, true, 1024, 1>(p, parts, s);
 }
@@ -836,7 +855,7 @@ int moe_norm_forward(const moe_norm_config *cfg, int num_tokens, const moe_norm_
 
 size_t moe_norm_workspace_bytes(const moe_norm_config *cfg, int num_tokens) {
     if (!valid(cfg) || num_tokens < 0) return 0;
-    const size_t b = (size_t)bwd_parts(cfg->hidden, num_tokens) * 2 * cfg->hidden * 4;
+    const size_t b = (size_t)bwd_parts(cfg->hidden, num_tokens) * 2 * part_pitch(cfg->hidden) * 4;
     return (b + 255) / 256 * 256;
 }
 
@@ -882,7 +901,10 @@ int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const moe_norm
     const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_bwd_any<float>(p, parts, s) : launch_bwd_any<bf16>(p, parts, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (sums) {
-        if (launch(norm_bwd_sum_kernel, 2 * ((H + 31) / 32), 1024, 0, 1, s, p, parts) != cudaSuccess) return MOE_ERR_CUDA;
+        const int ctas = 2 * ((H + 31) / 32);
+        const cudaError_t e = parts > 256 ? launch(norm_bwd_sum_kernel<128>, ctas, 1024, 0, 1, s, p, parts)
+                                          : launch(norm_bwd_sum_kernel<32>, ctas, 256, 0, 1, s, p, parts);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
 }
