@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     };
     // x -> halves: a half-warp takes one token's block at a time, kBatch items' loads together.  The first ones are asked
     // for before the weights, which would otherwise keep them waiting (a microsecond of a one-token call).
-    constexpr int kBatch = NT == 2 ? 8 : 4;
+    constexpr int kBatch = NT == 2 ? 16 : 4;
     const int sub = lane & 15, items = cta_blocks * M, item0 = warp * 2 + (lane >> 4);
     const unsigned half = lane < 16 ? 0x0000FFFFu : 0xFFFF0000u;   // the halves may end at different items
     const float inv_m = 1.0f / (float)M;
