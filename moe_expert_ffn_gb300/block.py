@@ -1,10 +1,11 @@
 """The MoE block around the expert layer: BlockNorm, Router and Fp4Linear.
 
-Like MoELayer these allocate device memory through PyTorch, check shapes and
-types, marshal pointers and turn error codes into exceptions; everything they
-compute runs in the CUDA library (include/moe.h).  Every call takes ``out``
-buffers made once with ``buffers()`` / ``grad_buffers()``, so that a decode
-loop allocates nothing, and allocates them itself when it gets none.
+Like MoELayer these allocate device memory through PyTorch and turn error
+codes into exceptions; shapes, types, devices and pitches are checked, and
+pointers marshalled, in _bind (csrc/bind.cpp); everything they compute runs in
+the CUDA library (include/moe.h).  Every call takes ``out`` buffers made once
+with ``buffers()`` / ``grad_buffers()``, so that a decode loop allocates
+nothing, and allocates them itself when it gets none.
 """
 from __future__ import annotations
 
@@ -13,8 +14,7 @@ import math
 
 import torch
 
-from . import (MOE_ERR_INVALID_ARG, Fp4LinearConfig, MoEError, NormConfig, NormGradIO, NormIO, RouterConfig,
-               BalanceIO, _check, lib)
+from . import MOE_ERR_INVALID_ARG, Fp4LinearConfig, MoEError, NormConfig, RouterConfig, _check, lib
 
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 GATES = {None: 0, "channel": 1, "token": 2}
@@ -43,7 +43,9 @@ except ImportError:   # pragma: no cover
 
 
 def _stream(stream, index):
-    return _current_stream(index) if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return _current_stream(index) if index >= 0 else 0
 
 
 def _index(device):
@@ -51,56 +53,28 @@ def _index(device):
     return device.index if device.type == "cuda" else -1
 
 
-def _refuse(t, name, dtype, shape, what):
-    raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} {what}, got {t.dtype} {tuple(t.shape)} with "
-                     f"strides {t.stride()} on {t.device}")
+def _bind():
+    """The module that takes tensors to the library (raises if it was not built)."""
+    try:
+        from . import _bind as b
+    except ImportError as e:
+        raise RuntimeError("moe_expert_ffn_gb300/_bind.so is missing or was built against another PyTorch: build it with "
+                           "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    if b.torch_version != torch.__version__.split("+")[0]:
+        raise RuntimeError(f"moe_expert_ffn_gb300/_bind.so was built against PyTorch {b.torch_version}: build it again")
+    return b
 
 
-def _rows(t, name, dtype, shape, index):
-    """(pointer, row pitch) of a [rows, cols] tensor whose rows are contiguous."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
-        _refuse(t, name, dtype, shape, "on the operator's device")
-    if t.is_contiguous():
-        return t.data_ptr(), shape[1]
-    pitch, step = t.stride()
-    if (step != 1 and shape[1] > 1) or (shape[0] > 1 and pitch < shape[1]):
-        _refuse(t, name, dtype, shape, "with contiguous rows that do not overlap")
-    return t.data_ptr(), pitch if shape[0] > 1 else shape[1]
+def _address(fn):
+    return ctypes.cast(fn, ctypes.c_void_p).value
 
 
-def _flat(t, name, dtype, shape, index):
-    """Pointer of a contiguous tensor."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-        _refuse(t, name, dtype, shape, "contiguous on the operator's device")
-    return t.data_ptr()
-
-
-class _Outputs:
-    """Output tensors of a call and, once checked against an operator, their native description: a later call with the
-    same ones only asks them for their addresses.  Replacing a tensor has it checked again."""
-    __slots__ = ("_of", "_key", "_io", "_own")
-
-    def __init__(self):
-        for n in type(self).__slots__:
-            object.__setattr__(self, n, None)
-        object.__setattr__(self, "_of", None)
-
-    def __setattr__(self, name, value):
-        object.__setattr__(self, name, value)
-        object.__setattr__(self, "_of", None)
-
-    def _bind(self, op, key, io, own):
-        """Checked for calls of `op` described by `key`; `own`: (tensor, field of io) pairs."""
-        for n, v in (("_io", io), ("_own", own), ("_key", key), ("_of", op)):
-            object.__setattr__(self, n, v)
-
-
-class NormOutput(_Outputs):
+class NormOutput:
     """What BlockNorm.forward writes: h, n, codes, sf, rstd_post, rstd_pre (None where absent)."""
     __slots__ = ("h", "n", "codes", "sf", "rstd_post", "rstd_pre")
 
 
-class NormGrads(_Outputs):
+class NormGrads:
     """What BlockNorm.backward writes: dresidual, dy, dw_post, dgate, dw_pre (None where absent)."""
     __slots__ = ("dresidual", "dy", "dw_post", "dgate", "dw_pre")
 
@@ -120,9 +94,9 @@ class BlockNorm:
                               _choice(GATES, gate, "gate"), _choice(QUANTS, quant, "quant"), float(eps), float(residual_scale))
         if lib().moe_norm_workspace_bytes(self.cfg, 1) == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "norm config")
-        self._workspace, self._dev, self._width, self._channel = None, _index(self.device), (int(hidden),), gate == "channel"
-        self._cfg = ctypes.byref(self.cfg)
-        self._fwd, self._bwd, self._ws_bytes = lib().moe_norm_forward, lib().moe_norm_backward, lib().moe_norm_workspace_bytes
+        self._workspace, self._ws_tokens, self._dev, b = None, -1, _index(self.device), _bind()
+        self._cfg, self._fwd, self._bwd = ctypes.addressof(self.cfg), b.norm_forward, b.norm_backward
+        self._fwd_at, self._bwd_at = _address(lib().moe_norm_forward), _address(lib().moe_norm_backward)
 
     def buffers(self, num_tokens, block=True, post=True, pre=True, normed=True) -> NormOutput:
         """Outputs of a forward of `num_tokens`: with y (`block`), w_post (`post`), w_pre (`pre`), n (`normed`)."""
@@ -150,56 +124,11 @@ class BlockNorm:
                    if block and self.gate else None)
         return g
 
-    def _params(self, io, T, w_post, gate, w_pre):
-        dt, dev, width = self.param_dtype, self._dev, self._width
-        io.w_post = None if w_post is None else _flat(w_post, "w_post", dt, width, dev)
-        io.gate = None if gate is None else _flat(gate, "gate", dt, width if self._channel else (T,), dev)
-        io.w_pre = None if w_pre is None else _flat(w_pre, "w_pre", dt, width, dev)
-
-    @staticmethod
-    def _check_all(io, wanted, index):
-        """Checks (name, tensor, dtype, shape, pitched) outputs and writes them into io."""
-        own = []
-        for name, t, dtype, shape, pitched in wanted:
-            if t is None:
-                continue
-            if pitched:
-                ptr, pitch = _rows(t, name, dtype, shape, index)
-                setattr(io, "ld_" + name, pitch)
-            else:
-                ptr = _flat(t, name, dtype, shape, index)
-            setattr(io, name, ptr)
-            own.append((t, name))
-        return own
-
     def forward(self, residual, y=None, w_post=None, gate=None, w_pre=None, normed=True, out=None, stream=None) -> NormOutput:
-        T, H, dt, dev = residual.shape[0], self.hidden, self.dtype, self._dev
         if out is None:
-            out = self.buffers(T, y is not None, w_post is not None, w_pre is not None, normed)
-        key = (T, y is None, w_post is None, w_pre is None)
-        if out._of is self and out._key == key:
-            io = out._io
-            for t, name in out._own:
-                setattr(io, name, t.data_ptr())
-        else:
-            f32, u8, shape, block, pre = torch.float32, torch.uint8, (T, H), y is not None, w_pre is not None
-            io = NormIO()
-            quant = pre and self.quant
-            if block and out.h is None or quant and (out.codes is None or out.sf is None):
-                raise ValueError("out lacks h, codes or sf")
-            own = self._check_all(io, (
-                ("h", out.h if block else None, dt, shape, True), ("n", out.n if pre else None, dt, shape, True),
-                ("codes", out.codes if quant else None, u8, shape, False),
-                ("sf", out.sf if quant else None, f32 if self.quant == "fp8" else u8, (T, H // (128 if self.quant == "fp8" else 32)), False),
-                ("rstd_post", out.rstd_post if block and w_post is not None else None, f32, (T,), False),
-                ("rstd_pre", out.rstd_pre if pre else None, f32, (T,), False)), dev)
-            out._bind(self, key, io, own)
-        shape = (T, H)
-        io.residual, io.ld_residual = _rows(residual, "residual", dt, shape, dev)
-        if y is not None:
-            io.y, io.ld_y = _rows(y, "y", dt, shape, dev)
-        self._params(io, T, w_post, gate, w_pre)
-        rc = self._fwd(self._cfg, T, io, _current_stream(dev) if stream is None else stream.cuda_stream)
+            out = self.buffers(residual.shape[0], y is not None, w_post is not None, w_pre is not None, normed)
+        rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev),
+                       residual, y, w_post, gate, w_pre, out.h, out.n, out.codes, out.sf, out.rstd_post, out.rstd_pre)
         if rc:
             _check(rc, "moe_norm_forward")
         return out
@@ -208,40 +137,21 @@ class BlockNorm:
                  out=None, stream=None) -> NormGrads:
         """Gradients from dh (of the stream h) and dn (of the normed n).  Uses a workspace of this object,
         so backward passes of one BlockNorm must not run concurrently."""
-        T, H, dt, dev, f32 = h.shape[0], self.hidden, self.dtype, self._dev, torch.float32
+        T = h.shape[0]
         if out is None:
             out = self.grad_buffers(T, y is not None, w_post is not None, w_pre is not None)
-        key = (T, y is None, w_post is None, w_pre is None, gate is None)
-        shape = (T, H)
-        if out._of is self and out._key == key:
-            io = out._io
-            for t, name in out._own:
-                setattr(io, name, t.data_ptr())
-        else:
-            io = NormGradIO()
-            wanted = (("dresidual", out.dresidual, dt, shape, True), ("dy", out.dy if y is not None else None, dt, shape, True),
-                      ("dw_post", out.dw_post if w_post is not None else None, f32, self._width, False),
-                      ("dw_pre", out.dw_pre if w_pre is not None else None, f32, self._width, False),
-                      ("dgate", out.dgate if gate is not None else None, f32, self._width if self.gate == "channel" else (T,), False))
-            out._bind(self, key, io, self._check_all(io, wanted, dev))
-        io.h, io.ld_h = _rows(h, "h", dt, shape, dev)
-        self._params(io, T, w_post, gate, w_pre)
-        io.dh, io.ld_dh = (None, 0) if dh is None else _rows(dh, "dh", dt, shape, dev)
-        io.dn, io.ld_dn = (None, 0) if dn is None else _rows(dn, "dn", dt, shape, dev)
-        if y is not None:
-            io.y, io.ld_y = _rows(y, "y", dt, shape, dev)
-        io.rstd_post = None if w_post is None or rstd_post is None else _flat(rstd_post, "rstd_post", f32, (T,), dev)
-        io.rstd_pre = None if w_pre is None or rstd_pre is None else _flat(rstd_pre, "rstd_pre", f32, (T,), dev)
-        need = self._ws_bytes(self._cfg, T)
-        if self._workspace is None or self._workspace.numel() < need:
-            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        rc = self._bwd(self._cfg, T, io, self._workspace.data_ptr(), _stream(stream, dev))
+        if T > self._ws_tokens:   # larger batches need no less
+            self._workspace = torch.empty(lib().moe_norm_workspace_bytes(self.cfg, T), dtype=torch.uint8, device=self.device)
+            self._ws_tokens = T
+        rc = self._bwd(self._bwd_at, self._cfg, self._dev, _stream(stream, self._dev), h, dh, dn, y, w_post, gate, w_pre,
+                       rstd_post, rstd_pre, out.dresidual, out.dy, out.dw_post, out.dgate, out.dw_pre,
+                       self._workspace.data_ptr())
         if rc:
             _check(rc, "moe_norm_backward")
         return out
 
 
-class RouterOutput(_Outputs):
+class RouterOutput:
     """What Router writes: topk_idx, topk_weights and, with the losses, loss ([3]: total, balance, z),
     counts [S, E], prob_mean [S, E], seq_tokens [S] (views of ``tokens`` [S + 2])."""
     __slots__ = ("topk_idx", "topk_weights", "loss", "counts", "prob_mean", "seq_tokens", "tokens")
@@ -263,12 +173,14 @@ class Router:
         need = lib().moe_router_workspace_bytes(self.cfg, 0 if max_tokens is None else int(max_tokens), self.max_seqs)
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "router config")
-        self._dev, self._bias_shape = _index(self.device), (int(num_experts),)
-        self._cfg = ctypes.byref(self.cfg)
-        L = lib()
-        self._fwd, self._bal, self._bwd = L.moe_router_forward, L.moe_balance_loss, L.moe_router_backward
+        self._dev, self._cfg, L, b = _index(self.device), ctypes.addressof(self.cfg), lib(), _bind()
+        self._fwd, self._bal, self._bwd = b.router_forward, b.balance_loss, b.router_backward
+        self._fwd_at, self._bal_at, self._bwd_at = (_address(L.moe_router_forward), _address(L.moe_balance_loss),
+                                                    _address(L.moe_router_backward))
         # only the loss calls need it: they need to know max_tokens
         self._workspace = None if max_tokens is None else torch.empty(need, dtype=torch.uint8, device=self.device)
+        self._limits = (-1 if max_tokens is None else int(max_tokens), self.max_seqs,
+                        None if max_tokens is None else self._workspace.data_ptr())
 
     def buffers(self, num_tokens, num_seqs=None) -> RouterOutput:
         """Outputs of a call on `num_tokens`, with those of the losses for `num_seqs` sequences."""
@@ -285,62 +197,31 @@ class Router:
             o.seq_tokens = o.tokens[:num_seqs]
         return o
 
-    def _losses(self, T, seq_offsets, out, write=True):
-        S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
-        if write and (self.max_tokens is None or T > self.max_tokens or S > self.max_seqs):
-            raise ValueError(f"{T} tokens in {S} sequences: the router was made for losses of "
-                             f"{self.max_tokens} tokens in {self.max_seqs}")
-        if out._of is self and out._key == S:
-            io = out._io
-            for t, name in out._own:
-                setattr(io, name, t.data_ptr())
-        else:
-            E, dev, f32, i32 = self.num_experts, self._dev, torch.float32, torch.int32
-            io = BalanceIO()
-            io.num_seqs = S
-            own = BlockNorm._check_all(io, (("loss", out.loss, f32, (3,), False), ("counts", out.counts, i32, (S, E), False),
-                                            ("prob_mean", out.prob_mean, f32, (S, E), False),
-                                            ("seq_tokens", out.tokens, i32, (S + 2,), False)), dev)
-            if len(own) != 4:
-                raise ValueError("out lacks the outputs of the losses")
-            out._bind(self, S, io, own)
-        io.seq_offsets = None if seq_offsets is None else _flat(seq_offsets, "seq_offsets", torch.int32, (S + 1,), self._dev)
-        return io
-
-    def _forward(self, logits, bias, loss_seqs, seq_offsets, out, stream):
-        T, E, k, dev = logits.shape[0], self.num_experts, self.topk, self._dev
+    def forward(self, logits, bias=None, out=None, stream=None) -> RouterOutput:
+        """topk_idx and topk_weights of logits [T, E] (bias f32 [E]: for the choice alone)."""
         if out is None:
-            out = self.buffers(T, loss_seqs)
-        ptr, ld = _rows(logits, "logits", self.logits_dtype, (T, E), dev)
-        b = None if bias is None else _flat(bias, "bias", torch.float32, self._bias_shape, dev)
-        idx = _flat(out.topk_idx, "topk_idx", torch.int32, (T, k), dev)
-        wts = _flat(out.topk_weights, "topk_weights", torch.float32, (T, k), dev)
-        io = ws = None
-        if loss_seqs is not None:
-            io, ws = self._losses(T, seq_offsets, out), self._workspace.data_ptr()
-        rc = self._fwd(self._cfg, T, ptr, ld, b, idx, wts, io, ws, _stream(stream, dev))
+            out = self.buffers(logits.shape[0])
+        rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), logits, bias, out.topk_idx, out.topk_weights)
         if rc:
             _check(rc, "moe_router_forward")
         return out
 
-    def forward(self, logits, bias=None, out=None, stream=None) -> RouterOutput:
-        """topk_idx and topk_weights of logits [T, E] (bias f32 [E]: for the choice alone)."""
-        return self._forward(logits, bias, None, None, out, stream)
-
     def forward_train(self, logits, bias=None, seq_offsets=None, out=None, stream=None) -> RouterOutput:
         """The same with the losses, in one pass; seq_offsets int32 [S + 1], or None for one sequence."""
-        S = 1 if seq_offsets is None else seq_offsets.shape[0] - 1
-        return self._forward(logits, bias, S, seq_offsets, out, stream)
+        if out is None:
+            out = self.buffers(logits.shape[0], 1 if seq_offsets is None else seq_offsets.shape[0] - 1)
+        rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), logits, bias, out.topk_idx, out.topk_weights,
+                       seq_offsets, out.loss, out.counts, out.prob_mean, out.tokens, *self._limits)
+        if rc:
+            _check(rc, "moe_router_forward")
+        return out
 
     def balance_loss(self, logits, topk_idx, seq_offsets=None, out=None, stream=None) -> RouterOutput:
         """The losses of a choice made elsewhere."""
-        T, E, dev = logits.shape[0], self.num_experts, self._dev
         if out is None:
-            out = self.buffers(T, 1 if seq_offsets is None else seq_offsets.shape[0] - 1)
-        ptr, ld = _rows(logits, "logits", self.logits_dtype, (T, E), dev)
-        idx = _flat(topk_idx, "topk_idx", torch.int32, (T, self.topk), dev)
-        io = self._losses(T, seq_offsets, out)
-        rc = self._bal(self._cfg, T, ptr, ld, idx, io, self._workspace.data_ptr(), _stream(stream, dev))
+            out = self.buffers(logits.shape[0], 1 if seq_offsets is None else seq_offsets.shape[0] - 1)
+        rc = self._bal(self._bal_at, self._cfg, self._dev, _stream(stream, self._dev), logits, topk_idx,
+                       seq_offsets, out.loss, out.counts, out.prob_mean, out.tokens, *self._limits)
         if rc:
             _check(rc, "moe_balance_loss")
         return out
@@ -348,20 +229,13 @@ class Router:
     def backward(self, logits, fwd, d_weights=None, d_loss=None, seq_offsets=None, out=None, stream=None):
         """d_logits through topk_weights (`d_weights` [T, k]) and through loss[0] (`d_loss`, an f32 scalar on the
         device); `fwd` is what the forward call returned."""
-        T, E, k, dev = logits.shape[0], self.num_experts, self.topk, self._dev
         if out is None:
-            out = torch.empty(T, E, dtype=self.logits_dtype, device=self.device)
-        ptr, ld = _rows(logits, "logits", self.logits_dtype, (T, E), dev)
-        dptr, dld = _rows(out, "d_logits", self.logits_dtype, (T, E), dev)
-        idx = dw = io = dl = None
-        if d_weights is not None:
-            idx = _flat(fwd.topk_idx, "topk_idx", torch.int32, (T, k), dev)
-            dw = _flat(d_weights, "d_weights", torch.float32, (T, k), dev)
+            out = torch.empty(logits.shape[0], self.num_experts, dtype=self.logits_dtype, device=self.device)
+        args = (self._bwd_at, self._cfg, self._dev, _stream(stream, self._dev), logits,
+                fwd.topk_idx if d_weights is not None else None, d_weights, out)
         if d_loss is not None:
-            if d_loss.numel() != 1:
-                raise ValueError("d_loss must hold one value")
-            io, dl = self._losses(T, seq_offsets, fwd, write=False), _flat(d_loss, "d_loss", torch.float32, d_loss.shape, dev)
-        rc = self._bwd(self._cfg, T, ptr, ld, idx, dw, io, dl, dptr, dld, _stream(stream, dev))
+            args += (d_loss, seq_offsets, fwd.loss, fwd.counts, fwd.prob_mean, fwd.tokens, *self._limits)
+        rc = self._bwd(*args)
         if rc:
             _check(rc, "moe_router_backward")
         return out
@@ -381,14 +255,12 @@ class Fp4Linear:
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "fp4 linear config")
         self.weights = torch.empty(need, dtype=torch.uint8, device=self.device)
-        self._cfg, self._ready, self._dev, self._fwd = ctypes.byref(self.cfg), False, _index(self.device), lib().moe_fp4_linear_forward
+        self._cfg, self._ready, self._dev, b = ctypes.addressof(self.cfg), False, _index(self.device), _bind()
+        self._fwd, self._fwd_at = b.linear_forward, _address(lib().moe_fp4_linear_forward)
 
     def transform_weights(self, w, w_sf, stream=None):
-        N, K, dev = self.out_features, self.in_features, self._dev
-        wp = _flat(w, "w", torch.uint8, (N, K // 2), dev)
-        sp = _flat(w_sf, "w_sf", torch.uint8, (N, K // 32), dev)
-        _check(lib().moe_fp4_linear_transform_weights(self.cfg, wp, sp, self.weights.data_ptr(), _stream(stream, dev)),
-               "moe_fp4_linear_transform_weights")
+        _check(_bind().linear_transform(_address(lib().moe_fp4_linear_transform_weights), self._cfg, self._dev,
+                                        _stream(stream, self._dev), w, w_sf, self.weights.data_ptr()), "moe_fp4_linear_transform_weights")
         self._ready = True
 
     def buffers(self, num_tokens):
@@ -397,13 +269,9 @@ class Fp4Linear:
     def forward(self, x, add=None, out=None, stream=None):
         if not self._ready:
             raise MoEError(-6, "moe_fp4_linear_forward")
-        T, n, dev = x.shape[0], self.out_columns, self._dev
         if out is None:
-            out = self.buffers(T)
-        xp, ldx = _rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
-        yp, ldy = _rows(out, "y", self.out_dtype, (T, n), dev)
-        ap, lda = (None, 0) if add is None else _rows(add, "add", self.out_dtype, (T, n), dev)
-        rc = self._fwd(self._cfg, T, xp, ldx, self.weights.data_ptr(), ap, lda, yp, ldy, _stream(stream, dev))
+            out = self.buffers(x.shape[0])
+        rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), x, add, out, self.weights.data_ptr())
         if rc:
             _check(rc, "moe_fp4_linear_forward")
         return out

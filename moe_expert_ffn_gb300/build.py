@@ -3,6 +3,8 @@
 Every translation unit in csrc/ is compiled for sm_103a in parallel, then
 linked into moe_expert_ffn_gb300/libmoe_gb300.so.  No cmake, no torch
 extension machinery: the library has a plain C ABI (include/moe.h).
+csrc/bind.cpp, which takes the block operators' tensors to that ABI, is built
+beside it against the installed PyTorch (_bind.so).
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -48,7 +52,43 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_bind(force: bool = False) -> str:
+    import torch
+    src, root = os.path.join(CSRC, "bind.cpp"), os.path.dirname(torch.__file__)
+    stamp = os.path.join(BUILD, f"bind-{torch.__version__}.stamp")   # of the PyTorch that it was built against
+    os.makedirs(BUILD, exist_ok=True)
+    if not force and os.path.exists(stamp) and not _stale(BIND, [src, os.path.join(INCLUDE, "moe.h"), __file__]):
+        return BIND
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("g++ not found")
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stderr}")
+    os.replace(tmp, BIND)
+    for old in glob.glob(os.path.join(BUILD, "bind-*.stamp")):
+        os.remove(old)
+    with open(stamp, "w"):
+        pass
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        bind = ex.submit(build_bind, force)
+        path = _build_library(force, verbose, ptxas_info)
+        bind.result()
+    return path
+
+
+def _build_library(force, verbose, ptxas_info) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
     hdrs = _headers()

@@ -197,3 +197,50 @@ def test_binding_refuses(m):
     with pytest.raises(m.MoEError):
         lin.forward(torch.zeros(1, 64, dtype=torch.bfloat16))
     assert ctypes.sizeof(m.NormIO) == 8 * 15 and ctypes.sizeof(m.BalanceIO) == 8 * 6
+
+
+def test_binding_checks_outputs(m):
+    """Outputs are checked like inputs, at every call: types, shapes, pitches, what is missing, what is no tensor."""
+    cpu, bf = torch.device("cpu"), torch.bfloat16
+    op = m.BlockNorm(256, gate="token", quant="ue8m0", device=cpu)
+    x, w, g = torch.zeros(3, 256, dtype=bf), torch.ones(256), torch.ones(3)
+
+    def call(**change):
+        o = op.buffers(3)
+        for n, v in change.items():
+            setattr(o, n, v)
+        op.forward(x, x, w_post=w, gate=g, w_pre=w, out=o)
+
+    for change in (dict(h=None), dict(codes=None), dict(sf=None), dict(h=torch.zeros(3, 256)), dict(h=torch.zeros(2, 256, dtype=bf)),
+                   dict(n=torch.zeros(3, 128, dtype=bf)), dict(codes=torch.zeros(3, 256, dtype=bf)), dict(sf=torch.zeros(3, 2)),
+                   dict(codes=torch.zeros(256, 3, dtype=torch.uint8).t()), dict(rstd_post=torch.zeros(4)),
+                   dict(rstd_pre=torch.zeros(3, 1)), dict(h=torch.zeros(1, 256, dtype=bf).expand(3, 256))):
+        with pytest.raises(ValueError):
+            call(**change)
+    with pytest.raises(RuntimeError):   # all is well, but nothing is launched on CPU tensors
+        call()
+    for bad in (3, "x", [x]):
+        with pytest.raises(TypeError):
+            op.forward(bad if isinstance(bad, list) else x, x, w_post=bad, gate=g, w_pre=w, out=op.buffers(3))
+    with pytest.raises(ValueError):
+        op.forward(x, x, w_post=w, gate=torch.ones(256), w_pre=w, out=op.buffers(3))
+    with pytest.raises(ValueError):
+        op.backward(x, x, x, y=x, w_post=w, gate=g, w_pre=w, rstd_post=torch.ones(3), rstd_pre=torch.ones(2))
+    r = m.Router(8, 2, balance_coef=1.0, max_tokens=4, max_seqs=2, device=cpu)
+    l = torch.zeros(3, 8)
+    o = r.buffers(3, 1)
+    for n, v in (("counts", torch.zeros(1, 8)), ("counts", None), ("loss", torch.zeros(2)), ("tokens", torch.zeros(2, dtype=torch.int32)),
+                 ("topk_idx", torch.zeros(3, 2, dtype=torch.int64))):
+        keep = getattr(o, n)
+        setattr(o, n, v)
+        with pytest.raises(ValueError):
+            r.forward_train(l, out=o)
+        setattr(o, n, keep)
+    for off in (torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.int64), torch.zeros(2, 2, dtype=torch.int32),
+                torch.zeros(0, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            r.forward_train(l, None, off, out=r.buffers(3, 2))
+    with pytest.raises(ValueError):
+        r.backward(l, o, d_loss=torch.ones(2))
+    with pytest.raises(ValueError):
+        r.backward(l, o, d_weights=torch.ones(3, 2, dtype=bf))
