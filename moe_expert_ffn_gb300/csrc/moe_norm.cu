@@ -8,6 +8,22 @@
 // every input is read once and every output written once whatever the norms in
 // between need.  Sums over a row are f32: 8 terms a chunk in order, then the
 // warp's tree, then the warps'.
+//
+// Forward: a row's time is two reductions one after the other, each a barrier,
+// so what counts is that memory is busy meanwhile: the next rows come through
+// private slots of shared memory by asynchronous copies, and two CTAs share an
+// SM.  4096 rows of 7168 bf16 with codes and normed output: 44.3 us, 6.0 TB/s
+// (a simple kernel with a CTA a row 135); 1023 rows of 4096 to UE8M0 codes
+// 10.5 us; one row 3.9 us, which is the latency of a launch, three dependent
+// trips to memory and shared memory and two barriers.
+//
+// Backward: four tensors come in and two go out, with one reduction after two
+// of them have arrived and one after the fourth; the column sums stay in
+// registers (two per column are enough: the gradients of w_post and of a
+// channel's gate are the same sum times the other one) and are joined by a
+// second kernel in a fixed order.  4096 rows of 7168 bf16: 75.1 us, 4.7 TB/s,
+// 66 of them in the main kernel (a simple kernel 719); 1777 rows of 1001 f32
+// by element: 15.0 us.
 #include <math.h>
 
 #include <algorithm>
@@ -742,13 +758,20 @@ cudaError_t launch_fwd(NormFwd p, cudaStream_t s) {
 
 template <class S, Map M>
 cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
-    // up to 1024 columns a warp holds the row and no barrier is needed
+    // A warp holds a short row without barriers (4096 x 512 bf16: 6.1 us, as CTAs of a warp that walk rows 9.6).  From 513
+    // columns on, aligned rows are faster in CTAs that walk (32768 x 1024: 57.5 us, a row a warp 65.5; at 600 rows 5.3 and
+    // 5.0); by element, where nothing is copied ahead, a warp still wins (4096 x 1001: 15.4 us against 40.8).
     if (p.H <= 256) return launch_fwd<S, 1, M, true, kNone, 128, 1>(p, s);
     if (p.H <= 512) return launch_fwd<S, 2, M, true, kNone, 128, 1>(p, s);
-    if (p.H <= 1024) return launch_fwd<S, 4, M, true, kNone, 128, 1>(p, s);
-    // more rows than SMs: two CTAs an SM, so that one works while the other waits at its barrier
-    if constexpr (M == kVec)
+    if constexpr (M == kVec) {
+        // More rows than SMs: two CTAs an SM, so that one works while the other waits at its barrier, with the parameters
+        // in shared memory because no registers are left for them (4096 x 7168 bf16: 44.5 us, one CTA with registers 53.8;
+        // 160 rows 6.2 and 6.1).  Fewer rows: each has an SM to itself, and registers save the trip (1 row 3.9 us against
+        // 4.2, 128 rows 4.1 against 5.8).
         if (p.H <= 8192 && p.T > 152) return launch_fwd<S, 2, M, false, kShared, 512, 2>(p, s);
+    } else {
+        if (p.H <= 1024) return launch_fwd<S, 4, M, true, kNone, 128, 1>(p, s);
+    }
     if (p.H <= 8192) return launch_fwd<S, 2, M, false, kRegs, 512, 1>(p, s);
     return launch_fwd<S, 2, M, false, kNone, 1024, 1>(p, s);
 }
@@ -786,25 +809,35 @@ cudaError_t launch_bwd(NormBwd p, int parts, cudaStream_t s) {
     return launch(kernel, parts, threads, smem, 1, s, p);
 }
 
+// CTAs of the backward pass, `per_sm` on each SM, or the rows.
+int ctas_of(int T, int per_sm) { return std::max(1, std::min(T, 152 * per_sm)); }
+
+// `parts`: the CTAs, each of which leaves a row of partial sums.
 template <class S, Map M>
-cudaError_t launch_bwd(const NormBwd &p, int parts, cudaStream_t s) {
-    if (p.H <= 2048) return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts, s);
-    if (p.H <= 8192) {
-        // two rows a pass where both fit the CTA's shared memory: half the barriers, and the parameters read once for two
-        if constexpr (M == kVec && sizeof(S) == 2) return launch_bwd<S, 2, 2, M, false, 512, 1>(p, parts, s);
-        else return launch_bwd<S, 2, 1, M, false, 512, 1>(p, parts, s);
+cudaError_t launch_bwd(const NormBwd &p, int &parts, cudaStream_t s) {
+    // Two rows a pass where both fit the CTA's shared memory: half the barriers, and the parameters read once for two
+    // (4096 x 7168 bf16: 75 us, one row a pass 86).
+    constexpr int kRows = M == kVec && sizeof(S) == 2 ? 2 : 1;
+    if (p.H <= 2048) {
+        // Short aligned rows, two or more passes a CTA: as the longer ones, several CTAs an SM (32768 x 1024 bf16 71 us, one
+        // chunk a thread and a row a pass 92; 4096 x 2048 f32 43, 47).  Fewer rows (300 x 1024: 7.8 us against 10.3), or
+        // rows read by element into registers (1777 x 1001 f32: 15 against 27): one chunk a thread.
+        const int many = p.H <= 1024 ? 8 : 4;
+        if constexpr (M == kVec) {
+            if (p.T >= 2 * 152 * many) return launch_bwd<S, 2, kRows, M, false, 512, 1>(p, parts = ctas_of(p.T, many), s);
+        }
+        return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts = ctas_of(p.T, many / 2), s);
     }
+    parts = ctas_of(p.T, 1);
+    if (p.H <= 8192) return launch_bwd<S, 2, kRows, M, false, 512, 1>(p, parts, s);
     return launch_bwd<S, 2, 1, M, true, 1024, 1>(p, parts, s);
 }
 
-// CTAs of the backward pass: as many as an SM holds (registers: 65536 / (threads x 128)), or the rows.
-int bwd_parts(int H, int T) {
-    const int per_sm = H <= 1024 ? 4 : H <= 2048 ? 2 : 1;
-    return std::max(1, std::min(T, 152 * per_sm));
-}
+// The most that launch_bwd takes.
+int bwd_parts(int H, int T) { return ctas_of(T, H <= 1024 ? 8 : H <= 2048 ? 4 : 1); }
 
 template <class S>
-cudaError_t launch_bwd_any(const NormBwd &p, int parts, cudaStream_t s) {
+cudaError_t launch_bwd_any(const NormBwd &p, int &parts, cudaStream_t s) {
     const moe_norm_grad_io &io = p.io;
     const size_t es = sizeof(S);
     const bool vec = p.H % 8 == 0 && rows16(io.h, io.ld_h, es) && rows16(io.y, io.ld_y, es) && rows16(io.dh, io.ld_dh, es) &&
@@ -895,7 +928,7 @@ int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const moe_norm
     const bool channel = io->gate && cfg->gate == MOE_GATE_CHANNEL;
     const bool sums = io->dw_post || io->dw_pre || channel;
     if (!d_workspace) return MOE_ERR_INVALID_ARG;
-    const int parts = bwd_parts(H, num_tokens);
+    int parts = 0;
     NormBwd p{*io, static_cast<float *>(d_workspace), num_tokens, H, io->y ? cfg->gate : (int)MOE_GATE_NONE, 1,
               cfg->param_dtype == MOE_DTYPE_F32, cfg->residual_scale};
     const cudaError_t e = cfg->stream_dtype == MOE_DTYPE_F32 ? launch_bwd_any<float>(p, parts, s) : launch_bwd_any<bf16>(p, parts, s);

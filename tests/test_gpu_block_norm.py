@@ -440,3 +440,31 @@ def test_offsets_past_32_bits(m):
     close(out.h, ref["h"], "h", ref["mag"])
     close(out.n, ref["n"], "n", ref["nmag"])
     assert torch.equal(out.rstd_post, want.rstd_post) or torch.allclose(out.rstd_post, want.rstd_post, rtol=1e-6)
+
+
+@pytest.mark.parametrize("T,H", [(161, 1024), (400, 776), (310, 520), (700, 5000)])
+@pytest.mark.parametrize("dtype,pdtype", [(BF, F32), (F32, BF)], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_forward_of_many_rows(m, T, H, dtype, pdtype, gate):
+    """More rows than SMs: CTAs that walk rows."""
+    test_forward_matches_formula(m, T, H, dtype, pdtype, gate)
+
+
+@pytest.mark.parametrize("quant,H", [("fp8", 640), ("fp8", 1024), ("ue8m0", 544), ("ue8m0", 992), ("fp8", 2048)])
+@pytest.mark.parametrize("T", [1, 200])
+def test_quantised_outputs_of_short_rows(m, quant, H, T):
+    d = make(T, H, BF, F32, "token", seed=T + H)
+    op = m.BlockNorm(H, EPS, gate="token", quant=quant, device=DEV)
+    out = op.forward(d["residual"], d["y"], d["w_post"], d["gate"], d["w_pre"])
+    ref = ref_forward(d, 1.0, "token")
+    close(out.h, ref["h"], "h", ref["mag"])
+    close(out.n, ref["n"], "n", ref["nmag"])
+    check_codes(out.codes, out.sf, ref["n"], quant)
+
+
+@pytest.mark.parametrize("T,H", [(2432, 1024), (2701, 264), (4870, 8), (1217, 1288), (1900, 2048)])
+@pytest.mark.parametrize("dtype,pdtype", [(BF, F32), (F32, F32), (F32, BF)], ids=["bf16", "f32", "f32_bf16"])
+@pytest.mark.parametrize("gate", [None, "channel", "token"])
+def test_backward_of_many_short_rows(m, T, H, dtype, pdtype, gate):
+    """Several CTAs an SM, each with rows for two passes and more."""
+    test_backward_matches_formula(m, T, H, dtype, pdtype, gate)
