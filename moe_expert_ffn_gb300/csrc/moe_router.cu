@@ -115,28 +115,41 @@ __device__ __forceinline__ int group_min(int v) {
     return v;
 }
 
-__device__ __forceinline__ int find_seq(const int32_t *off, int S, int t) {
-    int lo = 0, hi = S;   // first s with off[s + 1] > t
+// The first s in [s0, S) with off[s + 1] > t, else S; every lane of a warp calls and gets it.  One load asks for 32
+// offsets: the next ones, where a walk's sequences are, then those that cut the rest into 32.  (A search by halves, anew
+// for every cut, made most of the time of small batches: 19 tokens in 20 sequences 56 us for losses and gradient.)
+__device__ __forceinline__ int find_seq(const int32_t *off, int S, int t, int s0) {
+    const int lane = threadIdx.x & 31;
+    int lo = s0, hi = S, step = 1;   // the answer is in [lo, hi]; hi is S or was seen to end past t
     while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (off[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
+        const int m = lo + (lane + 1) * step - 1;
+        const unsigned past = __ballot_sync(kAll, m < hi && off[m + 1] > t);
+        if (past) {
+            const int f = __ffs(past) - 1;
+            hi = lo + (f + 1) * step - 1;
+            lo += f * step;
+        } else {
+            lo += min(32, (hi - lo) / step) * step;
+        }
+        step = (hi - lo + 31) / 32;
     }
-    return lo;
+    return hi;
 }
 
-// The sequence (or the gap before it) that token t is in: its index, whether it counts, and where the cut ends.
+// The sequence (or the gap before it) that token t is in, from sequence s0 on: its index, whether it counts, and where
+// the cut ends.
 struct Cut {
     int s, end;
     bool inside;
 };
-__device__ __forceinline__ Cut cut_at(const int32_t *off, int S, int t, int t1) {
+__device__ __forceinline__ Cut cut_at(const int32_t *off, int S, int t, int t1, int s0) {
     Cut c{0, t1, true};
     if (!off) return c;
-    c.s = find_seq(off, S, t);
+    c.s = find_seq(off, S, t, s0);
     if (c.s >= S) return Cut{S, t1, false};
-    c.inside = t >= off[c.s];
-    c.end = min(t1, c.inside ? off[c.s + 1] : off[c.s]);
+    const int begin = off[c.s], end = off[c.s + 1];
+    c.inside = t >= begin;
+    c.end = min(t1, c.inside ? end : begin);
     return c;
 }
 
@@ -387,8 +400,13 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_kernel(const
 #pragma unroll
         for (int i = 0; i < NI; ++i) bias[i] = lg + G * i < E ? p.bias[lg + G * i] : 0.0f;
     }
+    int s_at = 0;
     for (int a = t0; a < t1;) {
-        const Cut cut = kLoss ? cut_at(p.seq_offsets, p.S, a, t1) : Cut{0, t1, true};
+        const Cut cut = kLoss ? cut_at(p.seq_offsets, p.S, a, t1, s_at) : Cut{0, t1, true};
+        s_at = cut.s;
+        L raw[NI];
+        const int tw = a + warp * kGroups;
+        if (tw < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
         float prob[kLoss ? NI : 1];
         float zsum = 0.0f;
         int tokens = 0;
@@ -398,9 +416,6 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_kernel(const
             for (int e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
             __syncthreads();
         }
-        L raw[NI];
-        const int tw = a + warp * kGroups;
-        if (tw < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
         for (int tb = tw; tb < cut.end; tb += kWarps * kGroups) {
             const int t = tb + grp;
             const bool on = t < cut.end;
@@ -643,18 +658,10 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_bwd_kernel(c
         for (int e = lg; e < E; e += G) mine[e] = 0.0f;
     __syncwarp();
     const int t0 = (int)min((int64_t)blockIdx.x * p.chunk, (int64_t)p.T), t1 = (int)min((int64_t)t0 + p.chunk, (int64_t)p.T);
+    int s_at = 0;
     for (int a = t0; a < t1;) {
-        const Cut cut = cut_at(p.seq_offsets, p.S, a, t1);
-        const int n = p.d_loss && cut.inside && cut.s < p.S ? p.seq_tokens[cut.s] : 0;
-        float c[NI], zc = 0.0f;   // the balance loss's pull on each expert's probability, the z loss's on log-sum-exp
-        if (n > 0) {
-            const float g = *p.d_loss;
-            const float c0 = g * p.alpha * (float)E / ((float)k * (float)n * (float)n * (float)p.seq_tokens[p.S]);
-            zc = p.sigmoid ? 0.0f : g * 2.0f * p.beta / (float)p.seq_tokens[p.S + 1];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) c[i] = lg + G * i < E ? c0 * (float)p.counts[(int64_t)cut.s * E + lg + G * i] : 0.0f;
-        }
-        const bool dense = n > 0 || (p.d_weights && !p.renorm && !p.sigmoid);   // every probability is needed
+        const Cut cut = cut_at(p.seq_offsets, p.S, a, t1, s_at);
+        s_at = cut.s;
         L raw[NI];
         int next_idx[NS];
         float next_dw[NS];
@@ -671,6 +678,20 @@ __global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_bwd_kernel(c
             load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
             if (p.d_weights) load_slots(tw + grp, tw + grp < cut.end);
         }
+        int n = 0;
+        float c[NI], zc = 0.0f;   // the balance loss's pull on each expert's probability, the z loss's on log-sum-exp
+        if (p.d_loss && cut.inside && cut.s < p.S) {
+            int count[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) count[i] = lg + G * i < E ? p.counts[(int64_t)cut.s * E + lg + G * i] : 0;
+            const float g = *p.d_loss, seqs = (float)p.seq_tokens[p.S], all = (float)p.seq_tokens[p.S + 1];
+            n = p.seq_tokens[cut.s];
+            const float c0 = n > 0 ? g * p.alpha * (float)E / ((float)k * (float)n * (float)n * seqs) : 0.0f;
+            zc = p.sigmoid || n == 0 ? 0.0f : g * 2.0f * p.beta / all;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) c[i] = c0 * (float)count[i];
+        }
+        const bool dense = n > 0 || (p.d_weights && !p.renorm && !p.sigmoid);   // every probability is needed
         for (int tb = tw; tb < cut.end; tb += kWarps * kGroups) {
             const int t = tb + grp;
             const bool on = t < cut.end;
@@ -796,15 +817,17 @@ bool valid(const moe_router_config *c) {
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-// CTAs of a pass over T tokens, `most` at most and no more than give every warp a turn.
-int ctas_for(int T, int E, int most) {
+// CTAs of a pass over T tokens in S sequences, each with a contiguous part: no more than give every warp a turn, but two
+// to a sequence, because a CTA takes its sequences' parts one after the other.
+int ctas_for(int T, int E, int S) {
     const int per_cta = kWarps * (E <= 64 ? 4 : 1);
-    return std::min((std::max(T, 1) + per_cta - 1) / per_cta, most);
+    const int even = (std::max(T, 1) + per_cta - 1) / per_cta;
+    return std::min(std::max(even, S > 1 ? (int)std::min<int64_t>(T, (int64_t)8 * S) : 1), kMaxCtas);
 }
 
 // Carves the workspace; returns its size.
 size_t carve(int E, int T, int S, char *base, Partials *out) {
-    const size_t rows = (size_t)ctas_for(T, E, kMaxCtas) + S;
+    const size_t rows = (size_t)ctas_for(T, E, S) + S;
     size_t o = 0;
     auto take = [&](size_t bytes) {
         char *at = base + o;
@@ -899,7 +922,7 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.scale = cfg->weight_scale;
     p.S = loss ? loss->num_seqs : 1;
     p.seq_offsets = loss ? loss->seq_offsets : nullptr;
-    const int ctas = ctas_for(T, p.E, kMaxCtas);
+    const int ctas = ctas_for(T, p.E, p.S);
     p.chunk = std::max(1, (T + ctas - 1) / ctas);
     if (loss) carve(p.E, T, p.S, static_cast<char *>(ws), &p.part);
     if (T > 0) {
@@ -988,7 +1011,7 @@ int moe_router_backward(const moe_router_config *cfg, int num_tokens, const void
     p.scale = cfg->weight_scale;
     p.alpha = cfg->balance_coef;
     p.beta = cfg->z_coef;
-    const int ctas = ctas_for(num_tokens, p.E, kMaxCtas);
+    const int ctas = ctas_for(num_tokens, p.E, p.S);
     p.chunk = (num_tokens + ctas - 1) / ctas;
     return by_experts(p.E, RunBwd{p, cfg->logits_dtype == MOE_DTYPE_BF16, (num_tokens + p.chunk - 1) / p.chunk,
                                   static_cast<cudaStream_t>(stream)}) == cudaSuccess
