@@ -599,8 +599,11 @@ __global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_const
         if (lane == 0) {
             p.part.seq_bal[blockIdx.x] = n > 0 ? bal * (float)p.E / ((float)p.k * (float)n) : 0.0f;
             if (slab == 0) p.seq_tokens[s] = n, p.part.seq_z[s] = z;
-            __threadfence();
-            last = atomicAdd(p.part.ticket, 1) == (int)gridDim.x - 1;
+            last = gridDim.x == 1;   // alone, it reads what this thread wrote
+            if (!last) {
+                __threadfence();
+                last = atomicAdd(p.part.ticket, 1) == (int)gridDim.x - 1;
+            }
         }
     }
     __syncthreads();
