@@ -31,6 +31,13 @@
 // together (2176 bytes): one stream per warp, and tiles of a power of two of
 // columns do not start on the same few memory partitions (with 64 KB between
 // tiles the 28672 x 4096 product read at 3.5 TB/s).
+//
+// Measured: 4096 x 7168 with SwiGLU for one token 5.7 us (2.7 TB/s; the bytes
+// alone 2.3 us, a product of 75 x 96 takes 3.3), 7168 x 2048 for 5 tokens
+// 4.8 us, 28672 x 4096 for 16 tokens 20.9 us (3.1 TB/s; bytes 9.7): there every
+// CTA reads and converts all of x (5 to 6 us), and half of the issue slots of
+// the rest go to conversions, MMAs and scale products, which wait on one
+// another with 4 warps to a scheduler.  Simple kernels: 165, 160 and 3093 us.
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
@@ -495,7 +502,8 @@ int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tokens, con
     p.tiles = l.tiles;
     p.blocks = l.blocks;
     // K over the CTAs of a cluster (split) and the warps of a CTA (wk): the fewest blocks one after the other on a warp,
-    // among what fits in shared memory.  A join of warps counts as one block more, one of CTAs as two.
+    // among what fits in shared memory.  A join of warps counts as one block more, one of CTAs as two (2048 x 16384 for 4
+    // tokens: 9.8 us over clusters, 13.6 without; 4096 x 7168 for one token: 5.7 without, 8.5 over pairs).
     size_t smem = 0;
     int best = 1 << 30;
     p.depth = 0;

@@ -379,3 +379,26 @@ def test_graph_capture(m):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.loss, want.loss) and torch.equal(out.counts, want.counts)
+
+
+@pytest.mark.parametrize("T,S", [(19, 20), (700, 33), (700, 70), (5000, 1500), (60, 2100)])
+def test_ragged_sequences_with_runs_of_empty_ones(m, T, S):
+    """Sequences are found 32 offsets at a time: runs of empty ones longer than that, gaps at both ends."""
+    E, k = 24, 3
+    g = torch.Generator().manual_seed(T + S)
+    cut = torch.randint(1, T, (S + 1,), generator=g)
+    cut[S // 4: S // 2] = T // 3
+    cut[-S // 5:] = T - 1
+    off = sorted(cut.tolist())
+    x = make(T, E, seed=S)
+    offs = torch.tensor(off, dtype=torch.int32, device=DEV)
+    dw, one = torch.randn(T, k, generator=g).to(DEV), torch.full((), 2.0, device=DEV)
+    op = m.Router(E, k, balance_coef=0.5, z_coef=0.25, max_tokens=T, max_seqs=S, device=DEV)
+    out = op.forward_train(x, None, offs)
+    idx = ref_choice(x, None, k)
+    ref = ref_all(x, idx, "softmax", True, 1.0, k, off, 0.5, 0.25, dw.double().cpu().numpy(), 2.0)
+    assert np.array_equal(out.topk_idx.cpu().numpy(), idx)
+    assert np.array_equal(out.counts.cpu().numpy(), ref["counts"]) and np.array_equal(out.seq_tokens.cpu().numpy(), ref["n"])
+    close(out.prob_mean, ref["prob"], "prob_mean")
+    close(out.loss, ref["loss"], "loss")
+    close(op.backward(x, out, dw, one, offs), ref["grad"], "d_logits", mag=ref["grad_mag"])
