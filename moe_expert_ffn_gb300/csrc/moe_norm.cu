@@ -23,7 +23,7 @@
 // channel's gate are the same sum times the other one) and are joined by a
 // second kernel in a fixed order.  4096 rows of 7168 bf16: 75.1 us, 4.7 TB/s,
 // 66 of them in the main kernel (a simple kernel 719); 1777 rows of 1001 f32
-// by element: 15.0 us.
+// by element: 13.8 us.
 #include <math.h>
 
 #include <algorithm>
@@ -69,7 +69,12 @@ __device__ __forceinline__ void load8(F8 &v, const S *row, int i, int tr, int th
 
 template <Map M, class S>
 __device__ __forceinline__ void store8(S *row, const F8 &v, int i, int tr, int threads, int H) {
-    if (M == kVec) {
+    if (M == kStride) {
+        S *at = row + column<M>(i, 0, tr, threads);
+#pragma unroll
+        for (int j = 0; j < 8; ++j, at += threads)
+            if (column<M>(i, j, tr, threads) < H) *at = from_f32<S>(v.get(j));
+    } else if (M == kVec) {
         const int c = column<M>(i, 0, tr, threads);
         if (c < H) {
             Raw8<S> r;
@@ -129,10 +134,13 @@ struct NormFwd {
 
 // A thread's part of one stream tensor's row, on its way while earlier rows are worked on.  With aligned rows (kRing) it
 // comes through shared memory by asynchronous 16-byte copies, into slots that no other thread touches: the waits are the
-// thread's own, and a slot can be refilled as soon as the thread has read it.  Else it is loaded into registers.
+// thread's own, and a slot can be refilled as soon as the thread has read it.  Else it is loaded into registers: by
+// element one to an element, because packing two at once would wait for them there and then (4096 x 5001 bf16 forward:
+// 270 us against 79).
 template <class S, int NV, Map M, bool kRing>
 struct Feed {
-    Raw8<S> v[kRing ? 1 : NV];
+    Raw8<S> v[kRing || M != kVec ? 1 : NV];
+    S e[M != kVec ? NV * 8 : 1];
     uint32_t slots;   // kRing: shared address of [slot][NV][threads] 16 (bf16) or 32 (f32) bytes
     __device__ __forceinline__ uint32_t at(int slot, int i, int tr, int threads) const {
         return slots + ((slot * NV + i) * threads + tr) * (uint32_t)(8 * sizeof(S));
@@ -140,6 +148,7 @@ struct Feed {
     __device__ __forceinline__ void fetch(const void *base, int64_t ld, int64_t t, int slot, int tr, int threads, int H) {
         if (!base) return;
         const S *row = static_cast<const S *>(base) + t * ld;
+        const S *at_c = row + column<M>(0, 0, tr, threads);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (M == kVec) {
@@ -147,15 +156,20 @@ struct Feed {
                 if (kRing) {
                     if (c < H) copy_async<8 * sizeof(S)>(at(slot, i, tr, threads), row + c);
                 } else if (c < H) {
-                    v[kRing ? 0 : i].load_once(row + c);
+                    v[kRing || M != kVec ? 0 : i].load_once(row + c);
                 } else {
-                    v[kRing ? 0 : i].zero();
+                    v[kRing || M != kVec ? 0 : i].zero();
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const int c = column<M>(i, j, tr, threads);
-                    v[kRing ? 0 : i].put(j, c < H ? row[c] : from_f32<S>(0.0f));
+                    if (M == kStride) {
+                        e[M != kVec ? i * 8 + j : 0] = c < H ? *at_c : from_f32<S>(0.0f);
+                        at_c += threads;
+                    } else {
+                        e[M != kVec ? i * 8 + j : 0] = c < H ? row[c] : from_f32<S>(0.0f);
+                    }
                 }
             }
         }
@@ -171,7 +185,12 @@ struct Feed {
                                      : "memory");
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) v[kRing ? 0 : i].zero();
+            for (int i = 0; i < NV; ++i) {
+                if (M == kVec) v[kRing || M != kVec ? 0 : i].zero();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (M != kVec) e[M != kVec ? i * 8 + j : 0] = from_f32<S>(0.0f);
+            }
         }
     }
     __device__ __forceinline__ void get(F8 &f, int i, int slot, int tr, int threads) const {
@@ -179,8 +198,11 @@ struct Feed {
             Raw8<S> r;
             r.load_shared(at(slot, i, tr, threads));
             r.get(f);
+        } else if (M == kVec) {
+            v[kRing || M != kVec ? 0 : i].get(f);
         } else {
-            v[kRing ? 0 : i].get(f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f.put(j, to_f32(e[M != kVec ? i * 8 + j : 0]));
         }
     }
 };
@@ -290,7 +312,10 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
         }
         if (kRing) commit_group();
     };
-    for (int i = 0; i < slots; ++i) fetch(t + (int64_t)i * gridDim.x, i);
+    // By element over 8192 columns no registers are left for a row ahead (4096 x 9001 bf16: 398 us, ahead and spilled 413).
+    constexpr bool kAhead = !(M != kVec && !kWarpRow && kKeep == kNone);
+    if (kAhead)
+        for (int i = 0; i < slots; ++i) fetch(t + (int64_t)i * gridDim.x, i);
     // w_post times a channel's gate (1 where absent)
     auto load_post = [&](F8 &w, int i) {
         if (p.io.w_post) load_param8<M>(w, p.io.w_post, p.param_f32, i, tr, threads, H);
@@ -328,13 +353,14 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
         const float gate = gate_ahead;
         if (!kWarpRow) gate_ahead = token_gate(t + gridDim.x);
         if (kRing) wait_groups(slots - 1);
+        if (!kAhead) fetch(t, 0);
         F8 z[NV], u[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             res.get(z[i], i, slot, tr, threads);
             if (p.io.y) y.get(u[i], i, slot, tr, threads);
         }
-        if (!kWarpRow) fetch(t + (int64_t)slots * gridDim.x, slot);
+        if (!kWarpRow && kAhead) fetch(t + (int64_t)slots * gridDim.x, slot);
         if (p.io.y) {
             float r1 = 1.0f;
             if (p.io.w_post) {
@@ -384,6 +410,10 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_fwd_kernel(const _
     }
 }
 
+// Where the backward pass keeps its parameters: in registers where a thread's rows and sums leave some.
+constexpr Keep bwd_keep(int R, bool wide) {
+    return wide ? kNone : R == 1 ? kRegs : kShared;
+}
 // Columns between the rows of partial sums.
 __host__ __device__ __forceinline__ int64_t part_pitch(int H) { return (H + 31) / 32 * 32; }
 
@@ -481,9 +511,9 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             for (int r = 0; r < R; ++r) fetch_y(t, i, r);
             if (kRing) commit_group();
         }
-    constexpr Keep kKeep = kWide ? kNone : R == 1 ? kRegs : kShared;
+    constexpr Keep kKeep = bwd_keep(R, kWide);
     Params<NV, kKeep> k_scale, k_pre;
-    k_scale.base = h[0].slots + 4 * R * tensor;
+    k_scale.base = smem_u32(ring) + (kRing ? 4 * R * tensor : 0);
     k_pre.base = k_scale.base + k_scale.kBytes * threads;
     if (kKeep != kNone) {
 #pragma unroll
@@ -760,7 +790,7 @@ template <class S, Map M>
 cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
     // A warp holds a short row without barriers (4096 x 512 bf16: 6.1 us, as CTAs of a warp that walk rows 9.6).  From 513
     // columns on, aligned rows are faster in CTAs that walk (32768 x 1024: 57.5 us, a row a warp 65.5; at 600 rows 5.3 and
-    // 5.0); by element, where nothing is copied ahead, a warp still wins (4096 x 1001: 15.4 us against 40.8).
+    // 5.0); by element, where nothing is copied ahead, a warp still wins (4096 x 1001: 14.8 us against 35).
     if (p.H <= 256) return launch_fwd<S, 1, M, true, kNone, 128, 1>(p, s);
     if (p.H <= 512) return launch_fwd<S, 2, M, true, kNone, 128, 1>(p, s);
     if constexpr (M == kVec) {
@@ -792,12 +822,12 @@ cudaError_t launch_bwd(NormBwd p, int parts, cudaStream_t s) {
     const int per_thread = 8 * NV * 32;
     const int threads = (p.H + per_thread - 1) / per_thread * 32;
     const auto kernel = norm_bwd_kernel<S, NV, R, M, kWide, kMaxThreads, kMinCtas>;
+    const size_t params = (size_t)2 * Params<NV, bwd_keep(R, kWide)>::kBytes * threads;
     size_t smem = 0;
     if (kWide) {
         smem = (size_t)2 * NV * 8 * threads * 4;
     } else if (M == kVec) {
         const size_t row = (size_t)4 * R * NV * threads * 8 * sizeof(S);
-        const size_t params = R == 2 ? (size_t)2 * Params<NV, kShared>::kBytes * threads : 0;
         p.slots = ring_slots(row, std::max(1, kMaxThreads * kMinCtas / threads), params);
         smem = p.slots * row + params;
     }
@@ -812,29 +842,34 @@ cudaError_t launch_bwd(NormBwd p, int parts, cudaStream_t s) {
 // CTAs of the backward pass, `per_sm` on each SM, or the rows.
 int ctas_of(int T, int per_sm) { return std::max(1, std::min(T, 152 * per_sm)); }
 
+// CTAs an SM holds with two chunks a thread and 128 registers, or 64 (kWide).
+int bwd_per_sm(int H, bool wide) { return std::max(1, std::min(8, (wide ? 1024 : 512) / ((H + 511) / 512 * 32))); }
+
 // `parts`: the CTAs, each of which leaves a row of partial sums.
 template <class S, Map M>
 cudaError_t launch_bwd(const NormBwd &p, int &parts, cudaStream_t s) {
-    // Two rows a pass where both fit the CTA's shared memory: half the barriers, and the parameters read once for two
-    // (4096 x 7168 bf16: 75 us, one row a pass 86).
-    constexpr int kRows = M == kVec && sizeof(S) == 2 ? 2 : 1;
-    if (p.H <= 2048) {
-        // Short aligned rows, two or more passes a CTA: as the longer ones, several CTAs an SM (32768 x 1024 bf16 71 us, one
-        // chunk a thread and a row a pass 92; 4096 x 2048 f32 43, 47).  Fewer rows (300 x 1024: 7.8 us against 10.3), or
-        // rows read by element into registers (1777 x 1001 f32: 15 against 27): one chunk a thread.
-        const int many = p.H <= 1024 ? 8 : 4;
-        if constexpr (M == kVec) {
-            if (p.T >= 2 * 152 * many) return launch_bwd<S, 2, kRows, M, false, 512, 1>(p, parts = ctas_of(p.T, many), s);
-        }
-        return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts = ctas_of(p.T, many / 2), s);
+    if constexpr (M == kVec) {
+        // Two rows a pass where both fit the CTA's shared memory: half the barriers, and the parameters read once for two
+        // (4096 x 7168 bf16: 75 us, one row a pass 86).
+        constexpr int kRows = sizeof(S) == 2 ? 2 : 1;
+        const int per_sm = bwd_per_sm(p.H, false);
+        // Few short rows, less than two passes a CTA: one chunk a thread and a row a pass (300 x 1024 bf16: 7.8 us against
+        // 10.3; 32768 x 1024: 92 against 71).
+        if (p.H <= 2048 && p.T < 2 * 152 * per_sm)
+            return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts = ctas_of(p.T, p.H <= 1024 ? 4 : 2), s);
+        if (p.H <= 8192) return launch_bwd<S, 2, kRows, M, false, 512, 1>(p, parts = ctas_of(p.T, per_sm), s);
+        return launch_bwd<S, 2, 1, M, true, 1024, 1>(p, parts = ctas_of(p.T, 1), s);
+    } else {
+        // By element into registers a row ahead: one chunk a thread, for which they last.  Wider rows come in as they are
+        // needed, behind other CTAs' (4096 x 5001 bf16: 196 us, two chunks a thread ahead, spilled, 281).
+        if (p.H <= 2048) return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts = ctas_of(p.T, p.H <= 1024 ? 4 : 2), s);
+        if (p.H <= 4096) return launch_bwd<S, 1, 1, M, false, 512, 1>(p, parts = ctas_of(p.T, 1), s);
+        return launch_bwd<S, 2, 1, M, true, 1024, 1>(p, parts = ctas_of(p.T, bwd_per_sm(p.H, true)), s);
     }
-    parts = ctas_of(p.T, 1);
-    if (p.H <= 8192) return launch_bwd<S, 2, kRows, M, false, 512, 1>(p, parts, s);
-    return launch_bwd<S, 2, 1, M, true, 1024, 1>(p, parts, s);
 }
 
 // The most that launch_bwd takes.
-int bwd_parts(int H, int T) { return ctas_of(T, H <= 1024 ? 8 : H <= 2048 ? 4 : 1); }
+int bwd_parts(int H, int T) { return ctas_of(T, bwd_per_sm(H, H > 4096)); }
 
 template <class S>
 cudaError_t launch_bwd_any(const NormBwd &p, int &parts, cudaStream_t s) {

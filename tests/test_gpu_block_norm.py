@@ -468,3 +468,11 @@ def test_quantised_outputs_of_short_rows(m, quant, H, T):
 def test_backward_of_many_short_rows(m, T, H, dtype, pdtype, gate):
     """Several CTAs an SM, each with rows for two passes and more."""
     test_backward_matches_formula(m, T, H, dtype, pdtype, gate)
+
+
+@pytest.mark.parametrize("T,H", [(5, 2501), (161, 4001), (310, 4097), (4, 8191), (3, 9001), (700, 4096), (460, 2560), (301, 8200)])
+@pytest.mark.parametrize("dtype,pdtype", [(BF, F32), (F32, BF)], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+def test_wide_rows_by_element_and_several_ctas_an_sm(m, T, H, dtype, pdtype, gate):
+    test_forward_matches_formula(m, T, H, dtype, pdtype, gate)
+    test_backward_matches_formula(m, T, H, dtype, pdtype, gate)
