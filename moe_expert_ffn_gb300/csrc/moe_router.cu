@@ -28,9 +28,9 @@
 // 18.7 us, 380 warp instructions a token, two thirds of the issue slots taken
 // and the integer pipe the busiest (reading the logits alone would take 2.8; a
 // simple kernel 38.9).  65536 tokens of 256 f32 logits in 17 sequences with
-// losses and the whole gradient: 80.7 us (forward 40, sums 6, backward 34;
+// losses and the whole gradient: 79.2 us (forward 40, sums 5, backward 34;
 // bytes alone 21.1; simple kernels 339).  128 tokens: 2.0 us.  2048 tokens of
-// 8 experts, losses of a given choice and gradient: 8.4 us, three launches,
+// 8 experts, losses of a given choice and gradient: 8.0 us, three launches,
 // each a chain of a few trips to memory.
 #include <float.h>
 #include <math.h>
@@ -390,8 +390,12 @@ __device__ __forceinline__ float over_groups(float v) {
     return v;
 }
 
+// CTAs an SM by the experts of a lane: what registers allow without spills that cost (32767 x 256: four 18.7 us, five or
+// six 20.6 to 22; 28219 x 259: two 20.4, one 29.2).
+constexpr int ctas_an_sm(int NI) { return NI <= 8 ? 4 : NI == 16 ? 2 : 1; }
+
 template <class L, int NI, int G, int D, bool kLoss, bool kGiven>
-__global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_kernel(const __grid_constant__ RouterParams p) {
+__global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const __grid_constant__ RouterParams p) {
     extern __shared__ float joined[];   // kLoss: [warps][E] probabilities, [E] counts
     __shared__ float sz[kWarps];
     __shared__ int sn[kWarps];
@@ -562,13 +566,14 @@ struct SumParams {
     float alpha, beta;
 };
 
-// CTA (s, x): 32 experts of sequence s, its rows summed in order (a thread takes every 8th row, then the 8 are added in
+// CTA (s, x): 32 experts of sequence s, its rows summed in order (a thread takes every W-th row, then the W are added in
 // turn).  The last CTA to finish adds up the losses.
-__global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_constant__ SumParams p) {
-    __shared__ float sp[kWarps][32];
-    __shared__ int sc[kWarps][32];
-    __shared__ float sz[kWarps];
-    __shared__ int sn[kWarps];
+template <int W>
+__global__ void __launch_bounds__(W * 32) router_seq_kernel(const __grid_constant__ SumParams p) {
+    __shared__ float sp[W][32];
+    __shared__ int sc[W][32];
+    __shared__ float sz[W];
+    __shared__ int sn[W];
     __shared__ bool last;
     launch_next();
     const int slabs = (p.E + 31) / 32, s = blockIdx.x / slabs, slab = blockIdx.x - s * slabs;
@@ -580,12 +585,12 @@ __global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_const
     float pr = 0.0f, z = 0.0f;
     int c = 0, n = 0;
 #pragma unroll 4
-    for (int w = w0 + warp; w < w1; w += kWarps)
+    for (int w = w0 + warp; w < w1; w += W)
         if (e < p.E) {
             pr += p.part.prob[(int64_t)(w + s) * p.E + e];
             c += p.part.count[(int64_t)(w + s) * p.E + e];
         }
-    for (int w = w0 + threadIdx.x; w < w1; w += kThreads) {
+    for (int w = w0 + threadIdx.x; w < w1; w += W * 32) {
         n += p.part.tokens[w + s];
         z += p.part.z[w + s];
     }
@@ -598,7 +603,7 @@ __global__ void __launch_bounds__(kThreads) router_seq_kernel(const __grid_const
     if (warp == 0) {
         pr = 0.0f, z = 0.0f, c = 0, n = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) pr += sp[w][lane], c += sc[w][lane], z += sz[w], n += sn[w];
+        for (int w = 0; w < W; ++w) pr += sp[w][lane], c += sc[w][lane], z += sz[w], n += sn[w];
         const float mean = n > 0 ? pr / (float)n : 0.0f;
         if (e < p.E) {
             p.counts[(int64_t)s * p.E + e] = c;
@@ -657,7 +662,7 @@ struct RouterBwd {
 };
 
 template <class L, int NI, int G>
-__global__ void __launch_bounds__(kThreads, NI <= 8 ? 4 : 1) router_bwd_kernel(const __grid_constant__ RouterBwd p) {
+__global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(const __grid_constant__ RouterBwd p) {
     extern __shared__ float scatter[];   // [warps][groups][E]: gradients of the chosen logits, zero between tokens
     constexpr int kGroups = 32 / G;
     constexpr int NS = G == 32 ? 1 : 32 / G;
@@ -949,7 +954,12 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     if (loss) {
         SumParams q{p.part, p.seq_offsets, loss->counts, loss->prob_mean, loss->seq_tokens, loss->loss, T, p.E, p.k, p.S,
                     p.chunk, cfg->balance_coef, cfg->z_coef};
-        if (launch(router_seq_kernel, (unsigned)((p.E + 31) / 32) * p.S, kThreads, 0, 1, s, q) != cudaSuccess) return MOE_ERR_CUDA;
+        // 32 warps where a sequence has more rows than 8 can take in two turns (40397 tokens of 59 experts in one
+        // sequence, losses and gradient: 47.8 us, with 8 warps 61.5)
+        const unsigned sums = (unsigned)((p.E + 31) / 32) * p.S;
+        const cudaError_t e = ctas > 16 * p.S ? launch(router_seq_kernel<32>, sums, 1024, 0, 1, s, q)
+                                              : launch(router_seq_kernel<8>, sums, 256, 0, 1, s, q);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
 }
