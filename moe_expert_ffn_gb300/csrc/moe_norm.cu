@@ -798,8 +798,10 @@ cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
         // More rows than SMs: two CTAs an SM, so that one works while the other waits at its barrier, with the parameters
         // in shared memory because no registers are left for them (4096 x 7168 bf16: 44.5 us, one CTA with registers 53.8;
         // 160 rows 6.2 and 6.1).  Fewer rows: each has an SM to itself, and registers save the trip (1 row 3.9 us against
-        // 4.2, 128 rows 4.1 against 5.8).
-        if (p.H <= 8192 && p.T > 152) return launch_fwd<S, 2, M, false, kShared, 512, 2>(p, s);
+        // 4.2, 128 rows 4.1 against 5.8).  f32 rows are twice as long, which leaves two CTAs' shared memory no second slot
+        // beside the parameters: registers (1767 x 4096: 24.8 us against 29.1, 2000 x 7168 42.7 and 42.3).
+        if constexpr (sizeof(S) == 2)
+            if (p.H <= 8192 && p.T > 152) return launch_fwd<S, 2, M, false, kShared, 512, 2>(p, s);
     } else {
         if (p.H <= 1024) return launch_fwd<S, 4, M, true, kNone, 128, 1>(p, s);
     }
