@@ -335,9 +335,11 @@ __device__ __forceinline__ bool choose(const float (&key)[NI], int k, int lg, bo
     }
     bool again = false;
     if (D < NI && __any_sync(kAll, v[0] == 0)) {   // a lane gave all it kept: had it more that belong?
+        // one that it did not keep may share the last one's high bits and have the larger full key; closed ones do not count
+        const uint32_t least = max(exact ? last : last & ~kLow, kOpen);
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) n += packed(i) >= last;
+        for (int i = 0; i < NI; ++i) n += packed(i) >= least;
         again = n > D;
     }
 #pragma unroll
