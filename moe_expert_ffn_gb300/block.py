@@ -65,6 +65,14 @@ def _bind():
     return b
 
 
+def _made(stream, make, *args):
+    """What a call allocates itself: memory of the stream it runs on, so that it goes back to that one."""
+    if stream is None:
+        return make(*args)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
 def _address(fn):
     return ctypes.cast(fn, ctypes.c_void_p).value
 
@@ -75,8 +83,9 @@ class NormOutput:
 
 
 class NormGrads:
-    """What BlockNorm.backward writes: dresidual, dy, dw_post, dgate, dw_pre (None where absent)."""
-    __slots__ = ("dresidual", "dy", "dw_post", "dgate", "dw_pre")
+    """What BlockNorm.backward writes: dresidual, dy, dw_post, dgate, dw_pre (None where absent), and the workspace of
+    partial sums that it writes on the way (None or unset: every call allocates one)."""
+    __slots__ = ("dresidual", "dy", "dw_post", "dgate", "dw_pre", "workspace")
 
 
 class BlockNorm:
@@ -94,9 +103,10 @@ class BlockNorm:
                               _choice(GATES, gate, "gate"), _choice(QUANTS, quant, "quant"), float(eps), float(residual_scale))
         if lib().moe_norm_workspace_bytes(self.cfg, 1) == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "norm config")
-        self._workspace, self._ws_tokens, self._dev, b = None, -1, _index(self.device), _bind()
+        self._dev, b = _index(self.device), _bind()
         self._cfg, self._fwd, self._bwd = ctypes.addressof(self.cfg), b.norm_forward, b.norm_backward
         self._fwd_at, self._bwd_at = _address(lib().moe_norm_forward), _address(lib().moe_norm_backward)
+        self._ws_at = _address(lib().moe_norm_workspace_bytes)
 
     def buffers(self, num_tokens, block=True, post=True, pre=True, normed=True) -> NormOutput:
         """Outputs of a forward of `num_tokens`: with y (`block`), w_post (`post`), w_pre (`pre`), n (`normed`)."""
@@ -113,7 +123,11 @@ class BlockNorm:
                     else torch.empty(T, H // 32, dtype=torch.uint8, device=dev))
         return o
 
+    def _workspace(self, num_tokens):
+        return torch.empty(lib().moe_norm_workspace_bytes(self.cfg, num_tokens), dtype=torch.uint8, device=self.device)
+
     def grad_buffers(self, num_tokens, block=True, post=True, pre=True) -> NormGrads:
+        """Outputs and workspace of a backward pass of `num_tokens`; passes with buffers of their own may run concurrently."""
         T, H, dev = num_tokens, self.hidden, self.device
         g = NormGrads()
         g.dresidual = torch.empty(T, H, dtype=self.dtype, device=dev)
@@ -122,6 +136,7 @@ class BlockNorm:
         g.dw_pre = torch.empty(H, dtype=torch.float32, device=dev) if pre else None
         g.dgate = (torch.empty(H if self.gate == "channel" else T, dtype=torch.float32, device=dev)
                    if block and self.gate else None)
+        g.workspace = self._workspace(T)
         return g
 
     def forward(self, residual, y=None, w_post=None, gate=None, w_pre=None, normed=True, out=None, stream=None) -> NormOutput:
@@ -135,17 +150,15 @@ class BlockNorm:
 
     def backward(self, h, dh=None, dn=None, y=None, w_post=None, gate=None, w_pre=None, rstd_post=None, rstd_pre=None,
                  out=None, stream=None) -> NormGrads:
-        """Gradients from dh (of the stream h) and dn (of the normed n).  Uses a workspace of this object,
-        so backward passes of one BlockNorm must not run concurrently."""
+        """Gradients from dh (of the stream h) and dn (of the normed n)."""
         T = h.shape[0]
         if out is None:
-            out = self.grad_buffers(T, y is not None, w_post is not None, w_pre is not None)
-        if T > self._ws_tokens:   # larger batches need no less
-            self._workspace = torch.empty(lib().moe_norm_workspace_bytes(self.cfg, T), dtype=torch.uint8, device=self.device)
-            self._ws_tokens = T
+            out = _made(stream, self.grad_buffers, T, y is not None, w_post is not None, w_pre is not None)
+        ws = getattr(out, "workspace", None)
+        if ws is None:
+            ws = _made(stream, self._workspace, T)
         rc = self._bwd(self._bwd_at, self._cfg, self._dev, _stream(stream, self._dev), h, dh, dn, y, w_post, gate, w_pre,
-                       rstd_post, rstd_pre, out.dresidual, out.dy, out.dw_post, out.dgate, out.dw_pre,
-                       self._workspace.data_ptr())
+                       rstd_post, rstd_pre, out.dresidual, out.dy, out.dw_post, out.dgate, out.dw_pre, ws, self._ws_at)
         if rc:
             _check(rc, "moe_norm_backward")
         return out

@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
+#include <algorithm>
 #include <limits>
 #include <sstream>
 
@@ -181,7 +182,8 @@ int norm_forward(Args &a) {
     return unlocked(a, [&] { return c.fn(c.cfg, T, &io, c.stream); });
 }
 
-// ..., h, dh, dn, y, w_post, gate, w_pre, rstd_post, rstd_pre, dresidual, dy, dw_post, dgate, dw_pre, workspace address
+// ..., h, dh, dn, y, w_post, gate, w_pre, rstd_post, rstd_pre, dresidual, dy, dw_post, dgate, dw_pre, workspace, address of its
+// size's function
 int norm_backward(Args &a) {
     const Head<decltype(&moe_norm_backward), moe_norm_config> c(a);
     const int64_t H = c.cfg->hidden;
@@ -191,9 +193,12 @@ int norm_backward(Args &a) {
                      *gate = a.tensor("gate"), *w_pre = a.tensor("w_pre"), *rstd_post = a.tensor("rstd_post"),
                      *rstd_pre = a.tensor("rstd_pre"), *dresidual = a.tensor("dresidual"), *dy = a.tensor("dy"),
                      *dw_post = a.tensor("dw_post"), *dgate = a.tensor("dgate"), *dw_pre = a.tensor("dw_pre");
-    void *ws = address<void *>(a.next());
+    const at::Tensor *work = needed(a.tensor("workspace"), "workspace");
+    const auto ws_bytes = address<decltype(&moe_norm_workspace_bytes)>(a.next());
     a.done();
     const int T = tokens(h, "h");
+    void *ws;
+    a.flat(work, "workspace", at::kByte, -1, std::max<int64_t>(work->numel(), (int64_t)ws_bytes(c.cfg, T)), ws, true);
     const int64_t gates = c.cfg->gate == MOE_GATE_CHANNEL ? H : T;
     a.rows(h, "h", s, T, H, io.h, io.ld_h, false);
     a.rows(dh, "dh", s, T, H, io.dh, io.ld_dh, false);
