@@ -195,12 +195,13 @@ class Router:
         self._limits = (-1 if max_tokens is None else int(max_tokens), self.max_seqs,
                         None if max_tokens is None else self._workspace.data_ptr())
 
-    def buffers(self, num_tokens, num_seqs=None) -> RouterOutput:
-        """Outputs of a call on `num_tokens`, with those of the losses for `num_seqs` sequences."""
+    def buffers(self, num_tokens, num_seqs=None, choice=True) -> RouterOutput:
+        """Outputs of a call on `num_tokens`, with those of the losses for `num_seqs` sequences, and without those of the
+        choice where it is made elsewhere."""
         T, k, E, dev = num_tokens, self.topk, self.num_experts, self.device
         o = RouterOutput()
-        o.topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
-        o.topk_weights = torch.empty(T, k, dtype=torch.float32, device=dev)
+        o.topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev) if choice else None
+        o.topk_weights = torch.empty(T, k, dtype=torch.float32, device=dev) if choice else None
         o.loss = o.counts = o.prob_mean = o.seq_tokens = o.tokens = None
         if num_seqs is not None:
             o.loss = torch.empty(3, dtype=torch.float32, device=dev)
@@ -230,14 +231,18 @@ class Router:
         return out
 
     def balance_loss(self, logits, topk_idx, seq_offsets=None, out=None, stream=None) -> RouterOutput:
-        """The losses of a choice made elsewhere."""
+        """The losses of a choice made elsewhere.  The result has that choice as its topk_idx, for backward, and no
+        weights; of `out` the loss tensors are used, and its own choice stays what it is."""
         if out is None:
-            out = self.buffers(logits.shape[0], 1 if seq_offsets is None else seq_offsets.shape[0] - 1)
+            out = self.buffers(logits.shape[0], 1 if seq_offsets is None else seq_offsets.shape[0] - 1, choice=False)
         rc = self._bal(self._bal_at, self._cfg, self._dev, _stream(stream, self._dev), logits, topk_idx,
                        seq_offsets, out.loss, out.counts, out.prob_mean, out.tokens, *self._limits)
         if rc:
             _check(rc, "moe_balance_loss")
-        return out
+        o = RouterOutput()
+        o.topk_idx, o.topk_weights = topk_idx, None
+        o.loss, o.counts, o.prob_mean, o.seq_tokens, o.tokens = out.loss, out.counts, out.prob_mean, out.seq_tokens, out.tokens
+        return o
 
     def backward(self, logits, fwd, d_weights=None, d_loss=None, seq_offsets=None, out=None, stream=None):
         """d_logits through topk_weights (`d_weights` [T, k]) and through loss[0] (`d_loss`, an f32 scalar on the
