@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             if (k >= p.K) continue;   // K is a multiple of 32: all eight columns are there or none
             const bf16 *src = p.x + (item - b * M) * p.ld_x + k;
             if (p.x_vec) {
-                v[i] = __ldg(reinterpret_cast<const uint4 *>(src));
+                v[i] = ld_stream16(src);
             } else {
                 const uint16_t *e = reinterpret_cast<const uint16_t *>(src);
                 v[i] = make_uint4((uint32_t)e[0] | (uint32_t)e[1] << 16, (uint32_t)e[2] | (uint32_t)e[3] << 16,
