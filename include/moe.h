@@ -260,10 +260,12 @@ MOE_API void moe_destroy(moe_ctx *ctx);
  * device memory (workspaces, laid-out weights, outputs) is the caller's,
  * calls are stream-ordered and asynchronous, and argument errors are found
  * on the host before anything is launched.  They may be captured into CUDA
- * graphs.  Row pitches `ld_*` are in elements; rows themselves are
- * contiguous, and any pitch >= the row length and any element-aligned base
- * works (16-byte aligned rows are the fast case).  num_tokens = 0 launches
- * nothing that reads tokens: sums over tokens come out zero.
+ * graphs.  They launch on the calling thread's current device, which must be
+ * the one of the stream and the memory.  Row pitches `ld_*` are in elements;
+ * rows themselves are contiguous, and any pitch >= the row length and any
+ * element-aligned base works (16-byte aligned rows are the fast case).
+ * num_tokens = 0 launches nothing that reads tokens: sums over tokens come
+ * out zero.
  * ------------------------------------------------------------------------ */
 
 typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;

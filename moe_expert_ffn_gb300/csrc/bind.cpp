@@ -10,6 +10,7 @@
 // device index (-1: CPU) and the stream's handle, then tensors (None where
 // absent), and return the library's code.  They keep nothing between calls.
 #include <Python.h>
+#include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
 
@@ -150,6 +151,14 @@ struct Head {
         a.index = (int)number(a.next());
         stream = address<void *>(a.next());
         if (!fn || !cfg) fail(PyExc_TypeError, "no function or config");
+        // The library launches on the current device, and every device's default stream has the handle 0.
+        if (a.index < 0) return;
+        const int now = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA)->getDevice().index();
+        if (now == a.index) return;
+        std::ostringstream s;
+        s << "the operator is on cuda:" << a.index << " and the current device is cuda:" << now << ": call it under torch.cuda.device("
+          << a.index << ")";
+        fail(PyExc_RuntimeError, s.str());
     }
 };
 
