@@ -593,13 +593,15 @@ __global__ void __launch_bounds__(kMaxThreads, kMinCtas) norm_bwd_kernel(const _
             row_sums<R>(back, red[0][turn]);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                back[r] *= inv_h * -(now[r].r2 * now[r].r2 * now[r].r2);
+                // r2^3 may leave the f32 range (rows beyond 2^42, rows of zeros under a tiny eps): h r2 and the rest do not
+                back[r] = back[r] * -now[r].r2 * inv_h * now[r].r2;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     F8 hv;
                     h[r].get(hv, i, slot, tr, threads);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) D[r][i].p[j] = __ffma2_rn(hv.p[j], pair(back[r]), D[r][i].p[j]);
+                    for (int j = 0; j < 4; ++j)
+                        D[r][i].p[j] = __ffma2_rn(__fmul2_rn(hv.p[j], pair(now[r].r2)), pair(back[r]), D[r][i].p[j]);
                 }
                 fetch_pre(next, slot, r);
             }
