@@ -774,7 +774,7 @@ cudaError_t launch_fwd(NormFwd p, cudaStream_t s) {
     const int per_thread = 8 * NV * 32;   // columns of a warp
     const int threads = kWarpRow ? 128 : (p.H + per_thread - 1) / per_thread * 32;
     const auto kernel = norm_fwd_kernel<S, NV, M, kWarpRow, kKeep, kMaxThreads, kMinCtas>;
-    if (kWarpRow) return launch(kernel, (p.T + 3) / 4, threads, 0, 1, s, p);
+    if (kWarpRow) return launch(kernel, ((unsigned)p.T + 3) / 4, threads, 0, 1, s, p);
     const int per_sm = std::max(1, kMaxThreads * kMinCtas / threads);
     size_t smem = 0;
     if (M == kVec) {

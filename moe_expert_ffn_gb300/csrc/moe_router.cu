@@ -164,7 +164,7 @@ __device__ __forceinline__ Cut cut_at(const int32_t *off, int S, int t, int t1, 
 
 // A token's logits as loaded (-inf where there is none), so that the next token's can be on their way.
 template <class L, int NI, int G>
-__device__ __forceinline__ void load_row(L (&l)[NI], const void *logits, int64_t ld, int t, bool on, int lg, int E) {
+__device__ __forceinline__ void load_row(L (&l)[NI], const void *logits, int64_t ld, uint32_t t, bool on, int lg, int E) {
     const L *row = static_cast<const L *>(logits) + (int64_t)t * ld + lg;
     if (E == NI * G) {   // every lane has all its experts
 #pragma unroll
@@ -420,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
         const Cut cut = kLoss ? cut_at(p.seq_offsets, p.S, a, t1, s_at) : Cut{0, t1, true};
         s_at = cut.s;
         L raw[NI];
-        const int tw = a + warp * kGroups;
-        if (tw < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
+        const uint32_t end = cut.end, tw = (uint32_t)a + warp * kGroups;   // a step past the last token may pass 2^31
+        if (tw < end) load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < end, lg, E);
         float prob[kLoss ? NI : 1];
         float zsum = 0.0f;
         int tokens = 0;
@@ -431,14 +431,14 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
             for (int e = threadIdx.x; e < E; e += kThreads) counts[e] = 0;
             __syncthreads();
         }
-        for (int tb = tw; tb < cut.end; tb += kWarps * kGroups) {
-            const int t = tb + grp;
-            const bool on = t < cut.end;
+        for (uint32_t tb = tw; tb < end; tb += kWarps * kGroups) {
+            const uint32_t t = tb + grp;
+            const bool on = t < end;
             float l[NI];
 #pragma unroll
             for (int i = 0; i < NI; ++i) l[i] = to_f32(raw[i]);
-            const int tn = tb + kWarps * kGroups;
-            if (tn < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < cut.end, lg, E);
+            const uint32_t tn = tb + kWarps * kGroups;
+            if (tn < end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < end, lg, E);
             float m = -INFINITY, top = -INFINITY;   // the largest logit, and that of the chosen
             if (kGiven || (kLoss && p.bias) || (!p.renorm && !p.sigmoid)) {
 #pragma unroll
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(co
         L raw[NI];
         int next_idx[NS];
         float next_dw[NS];
-        auto load_slots = [&](int t, bool on) {
+        auto load_slots = [&](uint32_t t, bool on) {
 #pragma unroll
             for (int s = 0; s < NS; ++s) {
                 const int j = s * G + lg;
@@ -692,10 +692,10 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(co
                 next_dw[s] = on && j < k ? p.d_weights[(int64_t)t * k + j] : 0.0f;
             }
         };
-        const int tw = a + warp * kGroups;
-        if (tw < cut.end) {
-            load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < cut.end, lg, E);
-            if (p.d_weights) load_slots(tw + grp, tw + grp < cut.end);
+        const uint32_t end = cut.end, tw = (uint32_t)a + warp * kGroups;   // a step past the last token may pass 2^31
+        if (tw < end) {
+            load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < end, lg, E);
+            if (p.d_weights) load_slots(tw + grp, tw + grp < end);
         }
         int n = 0;
         float c[NI], zc = 0.0f;   // the balance loss's pull on each expert's probability, the z loss's on log-sum-exp
@@ -711,14 +711,14 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(co
             for (int i = 0; i < NI; ++i) c[i] = c0 * (float)count[i];
         }
         const bool dense = n > 0 || (p.d_weights && !p.renorm && !p.sigmoid);   // every probability is needed
-        for (int tb = tw; tb < cut.end; tb += kWarps * kGroups) {
-            const int t = tb + grp;
-            const bool on = t < cut.end;
+        for (uint32_t tb = tw; tb < end; tb += kWarps * kGroups) {
+            const uint32_t t = tb + grp;
+            const bool on = t < end;
             float l[NI], d[NI], q[NI];
 #pragma unroll
             for (int i = 0; i < NI; ++i) l[i] = to_f32(raw[i]);
-            const int tn = tb + kWarps * kGroups;
-            if (tn < cut.end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < cut.end, lg, E);
+            const uint32_t tn = tb + kWarps * kGroups;
+            if (tn < end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < end, lg, E);
             // the chosen slots' part
             float add[NS], ls[NS], dw[NS], dot = 0.0f;
             int idx[NS];
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(co
                     ls[s] = idx[s] < 0 ? -INFINITY
                                        : open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + idx[s]]));
                 }
-                if (tn < cut.end) load_slots(tn + grp, tn + grp < cut.end);
+                if (tn < end) load_slots(tn + grp, tn + grp < end);
             }
             float m = 0.0f, inv = 0.0f;
             bool real = false;
@@ -841,7 +841,7 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 // gradient: 8.6 us, with two to a sequence 10.8).
 int ctas_for(int T, int E, int S) {
     const int per_cta = kWarps * (E <= 64 ? 4 : 1);
-    const int even = (std::max(T, 1) + per_cta - 1) / per_cta;
+    const int even = (std::max(T, 1) - 1) / per_cta + 1;
     return std::min(std::max(even, S > 1 ? (int)std::min<int64_t>(T, (int64_t)8 * S) : 1), kMaxCtas);
 }
 
@@ -944,11 +944,11 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.S = loss ? loss->num_seqs : 1;
     p.seq_offsets = loss ? loss->seq_offsets : nullptr;
     const int ctas = ctas_for(T, p.E, p.S);
-    p.chunk = std::max(1, (T + ctas - 1) / ctas);
+    p.chunk = T > 0 ? (T - 1) / ctas + 1 : 1;
     if (loss) carve(p.E, T, p.S, static_cast<char *>(ws), &p.part);
     if (T > 0) {
         if (by_experts(p.E, RunRouter{p, cfg->logits_dtype == MOE_DTYPE_BF16, loss != nullptr, given,
-                                      (T + p.chunk - 1) / p.chunk, s}) != cudaSuccess)
+                                      (T - 1) / p.chunk + 1, s}) != cudaSuccess)
             return MOE_ERR_CUDA;
     } else if (loss && cudaMemsetAsync(p.part.ticket, 0, sizeof(int), s) != cudaSuccess) {
         return MOE_ERR_CUDA;
@@ -1038,8 +1038,8 @@ int moe_router_backward(const moe_router_config *cfg, int num_tokens, const void
     p.alpha = cfg->balance_coef;
     p.beta = cfg->z_coef;
     const int ctas = ctas_for(num_tokens, p.E, p.S);
-    p.chunk = (num_tokens + ctas - 1) / ctas;
-    return by_experts(p.E, RunBwd{p, cfg->logits_dtype == MOE_DTYPE_BF16, (num_tokens + p.chunk - 1) / p.chunk,
+    p.chunk = (num_tokens - 1) / ctas + 1;
+    return by_experts(p.E, RunBwd{p, cfg->logits_dtype == MOE_DTYPE_BF16, (num_tokens - 1) / p.chunk + 1,
                                   static_cast<cudaStream_t>(stream)}) == cudaSuccess
                ? MOE_OK
                : MOE_ERR_CUDA;
