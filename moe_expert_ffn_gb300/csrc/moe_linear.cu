@@ -423,7 +423,7 @@ struct Layout {
 };
 Layout layout(const moe_fp4_linear_config *c) {
     Layout l;
-    l.tiles = (c->out_features + kTileRows - 1) / kTileRows;   // of gate and up rows alike
+    l.tiles = (c->out_features - 1) / kTileRows + 1;   // of gate and up rows alike
     l.blocks = (c->in_features + 127) / 128;
     l.row_exp = up256((size_t)l.tiles * l.blocks * kBlockBytes);
     l.total = l.row_exp + up256((size_t)l.tiles * kTileRows * 4);
@@ -465,7 +465,7 @@ int moe_fp4_linear_transform_weights(const moe_fp4_linear_config *cfg, const voi
         return MOE_ERR_INVALID_ARG;
     const Layout l = layout(cfg);
     uint8_t *d = static_cast<uint8_t *>(d_weights);
-    linear_transform_kernel<<<l.tiles * kTileRows / 8, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+    linear_transform_kernel<<<l.tiles * (kTileRows / 8), 256, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<const uint8_t *>(w), static_cast<const uint8_t *>(w_sf), cfg->out_features, cfg->in_features,
         cfg->act == MOE_ACT_SWIGLU, l.tiles, l.blocks, d, reinterpret_cast<int32_t *>(d + l.row_exp));
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
