@@ -420,7 +420,7 @@ typedef struct {
     int out_features;  /* N rows of the weight; even with MOE_ACT_SWIGLU */
     int act;           /* moe_act; SWIGLU: rows [0, N/2) gate, [N/2, N) up, output silu(gate) * up of N/2 columns */
     int out_dtype;     /* moe_dtype of add and y */
-    float act_clamp;   /* symmetric clamp of gate and up before SWIGLU; +INFINITY = off */
+    float act_clamp;   /* symmetric clamp of gate and up before SWIGLU; +INFINITY = off; a NaN stays one */
 } moe_fp4_linear_config;
 
 /* Weights in the layer's FP4 format (MOE_W_FP4_E2M1_UE8M0_32): w u8 [N, K/2]

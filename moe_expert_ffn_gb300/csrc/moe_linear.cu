@@ -110,6 +110,9 @@ __device__ __forceinline__ float group_scale(uint32_t s, int q) {
     return __uint_as_float((q < 3 ? s << (23 - 8 * q) : s >> 1) & 0x7F800000u);
 }
 
+// v in [-c, c]; a NaN stays one (minimum and maximum would make it a bound)
+__device__ __forceinline__ float clamped(float v, float c) { return v > c ? c : v < -c ? -c : v; }
+
 __device__ __forceinline__ void add4(float4 &a, const float4 &b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
 // Waits until at most depth - 1 of the warp's groups of copies are under way.
@@ -359,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
                     if (m >= M || col >= p.n_out || (kSwiglu && i > 1)) continue;
                     float o = v[i];
                     if (kSwiglu) {
-                        const float gt = fminf(fmaxf(o, -p.clamp), p.clamp);
-                        const float up = fminf(fmaxf(v[(i + 2) & 3], -p.clamp), p.clamp);
+                        const float gt = clamped(o, p.clamp), up = clamped(v[(i + 2) & 3], p.clamp);
                         o = gt / (1.0f + expf(-gt)) * up;
                     }
                     if (p.add) o += to_f32(static_cast<const O *>(p.add)[m * p.ld_add + col]);
