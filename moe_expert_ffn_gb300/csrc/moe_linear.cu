@@ -10,10 +10,11 @@
 // into the A fragments of m16n8k16 MMAs whose N is the tokens: the products
 // of up to 8 tokens cost the issue slots of one.  E2M1 is exact in f16.
 //
-// x is exact too: every 128-column block of a token is scaled by the power of
-// two that brings its largest element into [2^14, 2^15), where f16 keeps all 8
-// bits of a bf16 down to 2^-33 of that element (below, the error is under
-// 2^-39 of it, far under the f32 sum's own).  Each CTA converts its x once
+// x is nearly always exact too: every 128-column block of a token is scaled by
+// the power of two that brings its largest element into [2^14, 2^15), where f16
+// keeps all 8 bits of a bf16 down to 2^-31 of that power of two (2^-17; below,
+// the error is at most 2^-39 of it, half of f16's smallest step, far under the
+// f32 sum's own unless the large element meets a zero weight).  Each CTA converts its x once
 // into shared memory, in the order of the B fragments.
 //
 // Every scale group is summed by itself (two MMAs from zero) and joined in
