@@ -14,8 +14,8 @@
 // the power of two that brings its largest element into [2^14, 2^15), where f16
 // keeps all 8 bits of a bf16 down to 2^-31 of that power of two (2^-17; below,
 // the error is at most 2^-39 of it, half of f16's smallest step, far under the
-// f32 sum's own unless the large element meets a zero weight).  Each CTA converts its x once
-// into shared memory, in the order of the B fragments.
+// f32 sum's own unless the large element meets a zero weight).  Each CTA
+// converts its x once into shared memory, in the order of the B fragments.
 //
 // Every scale group is summed by itself (two MMAs from zero) and joined in
 // f32 under its scale.  Scales are held relative to their row's largest, so

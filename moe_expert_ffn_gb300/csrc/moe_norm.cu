@@ -264,12 +264,8 @@ __device__ __forceinline__ void quantise8(const NormFwd &p, F8 v, int64_t t, int
     if (p.quant == MOE_QUANT_FP8_128) {
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 4));
         amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 8));
-        const Fp8Scale sc = fp8_scale(amax);
+        const Fp8Scale sc = fp8_scale(amax, v);
         inv = sc.inv;
-        if (sc.up != 1.0f) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(v.p[j], pair(sc.up));
-        }
         if (c < p.H && (tr & 15) == 0) static_cast<float *>(p.io.sf)[t * (p.H / 128) + c / 128] = sc.sf;
     } else {
         const int code = ue8m0_code(amax);

@@ -176,18 +176,29 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
 // 2^e, e in [-126, 127].
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// FP8 group scale sf = amax / 448 and q = v / sf as v times the rounded
-// 448 / amax (within one more rounding of the division: a code differs where v
-// is that near a tie).  Below 2^-100 the reciprocal would pass the f32 range,
-// so v is brought up by 2^64 first; an all-zero group has sf 0 and codes 0.
+// FP8 group scale sf = amax / 448, the rounded quotient, and inv, by which v
+// becomes q = v / sf: the rounded 448 / amax (within one more rounding of the
+// division: a code differs where v is that near a tie).  The quotient by a
+// constant is its product with the rounded reciprocal and one correction by
+// the exact remainder (Brisebarre, Muller and Raina 2004; for 448 right for
+// every mantissa; with a division 4096 x 7168 takes 45.5 us instead of 44.0).
+// Below 2^-100, where the remainder would not stay normal and inv would pass
+// the f32 range, v is brought up by 2^64; an all-zero group has sf 0 and codes
+// 0, one with an infinity sf infinity.
 struct Fp8Scale {
-    float sf, up, inv;
+    float sf, inv;
 };
-__device__ __forceinline__ Fp8Scale fp8_scale(float amax) {
-    Fp8Scale q;
-    q.sf = amax * (1.0f / 448.0f);
-    q.up = amax < 0x1p-100f ? 0x1p64f : 1.0f;
-    q.inv = amax > 0.0f ? 448.0f / (amax * q.up) : 0.0f;
+__device__ __forceinline__ Fp8Scale fp8_scale(float amax, F8 &v) {
+    const float near = amax * (1.0f / 448.0f);
+    Fp8Scale q{fmaf(fmaf(-448.0f, near, amax), 1.0f / 448.0f, near), 448.0f / amax};
+    const uint32_t lo = 0x0D800000u, inf = 0x7F800000u;   // 2^-100
+    if (__float_as_uint(amax) - lo >= inf - lo) {
+        const float up = amax < 1.0f ? 0x1p64f : 1.0f;
+        q.sf = amax / 448.0f;
+        q.inv = amax > 0.0f ? 448.0f / (amax * up) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v.p[j] = __fmul2_rn(v.p[j], pair(up));
+    }
     return q;
 }
 
