@@ -726,9 +726,9 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(co
 #pragma unroll
                 for (int s = 0; s < NS; ++s) {
                     idx[s] = next_idx[s] < E ? next_idx[s] : -1;
-                    dw[s] = idx[s] >= 0 ? next_dw[s] * p.scale : 0.0f;
                     ls[s] = idx[s] < 0 ? -INFINITY
                                        : open_logit(to_f32(static_cast<const L *>(p.logits)[(int64_t)t * p.ld + idx[s]]));
+                    dw[s] = ls[s] > -INFINITY ? next_dw[s] * p.scale : 0.0f;   // a closed expert's may be anything
                 }
                 if (tn < end) load_slots(tn + grp, tn + grp < end);
             }
