@@ -166,8 +166,8 @@ class BlockNorm:
 
 class RouterOutput:
     """What Router writes: topk_idx, topk_weights and, with the losses, loss ([3]: total, balance, z),
-    counts [S, E], prob_mean [S, E], seq_tokens [S] (views of ``tokens`` [S + 2])."""
-    __slots__ = ("topk_idx", "topk_weights", "loss", "counts", "prob_mean", "seq_tokens", "tokens")
+    counts [S, E], prob_mean [S, E], seq_tokens [S] (views of ``tokens`` [S + 2]) and the seq_offsets they go by."""
+    __slots__ = ("topk_idx", "topk_weights", "loss", "counts", "prob_mean", "seq_tokens", "tokens", "seq_offsets")
 
 
 class Router:
@@ -202,7 +202,7 @@ class Router:
         o = RouterOutput()
         o.topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev) if choice else None
         o.topk_weights = torch.empty(T, k, dtype=torch.float32, device=dev) if choice else None
-        o.loss = o.counts = o.prob_mean = o.seq_tokens = o.tokens = None
+        o.loss = o.counts = o.prob_mean = o.seq_tokens = o.tokens = o.seq_offsets = None
         if num_seqs is not None:
             o.loss = torch.empty(3, dtype=torch.float32, device=dev)
             o.counts = torch.empty(num_seqs, E, dtype=torch.int32, device=dev)
@@ -228,6 +228,7 @@ class Router:
                        seq_offsets, out.loss, out.counts, out.prob_mean, out.tokens, *self._limits)
         if rc:
             _check(rc, "moe_router_forward")
+        out.seq_offsets = seq_offsets
         return out
 
     def balance_loss(self, logits, topk_idx, seq_offsets=None, out=None, stream=None) -> RouterOutput:
@@ -241,17 +242,20 @@ class Router:
             _check(rc, "moe_balance_loss")
         o = RouterOutput()
         o.topk_idx, o.topk_weights = topk_idx, None
+        o.seq_offsets = out.seq_offsets = seq_offsets
         o.loss, o.counts, o.prob_mean, o.seq_tokens, o.tokens = out.loss, out.counts, out.prob_mean, out.seq_tokens, out.tokens
         return o
 
     def backward(self, logits, fwd, d_weights=None, d_loss=None, seq_offsets=None, out=None, stream=None):
         """d_logits through topk_weights (`d_weights` [T, k]) and through loss[0] (`d_loss`, an f32 scalar on the
-        device); `fwd` is what the forward call returned."""
+        device); `fwd` is what the forward call returned, and seq_offsets need not be given again."""
         if out is None:
             out = torch.empty(logits.shape[0], self.num_experts, dtype=self.logits_dtype, device=self.device)
         args = (self._bwd_at, self._cfg, self._dev, _stream(stream, self._dev), logits,
                 fwd.topk_idx if d_weights is not None else None, d_weights, out)
         if d_loss is not None:
+            if seq_offsets is None:
+                seq_offsets = getattr(fwd, "seq_offsets", None)
             args += (d_loss, seq_offsets, fwd.loss, fwd.counts, fwd.prob_mean, fwd.tokens, *self._limits)
         rc = self._bwd(*args)
         if rc:
