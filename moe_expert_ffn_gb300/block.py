@@ -5,7 +5,8 @@ codes into exceptions; shapes, types, devices and pitches are checked, and
 pointers marshalled, in _bind (csrc/bind.cpp); everything they compute runs in
 the CUDA library (include/moe.h).  Every call takes ``out`` buffers made once
 with ``buffers()`` / ``grad_buffers()``, so that a decode loop allocates
-nothing, and allocates them itself when it gets none.
+nothing, and allocates them itself, as memory of the stream it runs on, when
+it gets none.
 """
 from __future__ import annotations
 
@@ -141,7 +142,7 @@ class BlockNorm:
 
     def forward(self, residual, y=None, w_post=None, gate=None, w_pre=None, normed=True, out=None, stream=None) -> NormOutput:
         if out is None:
-            out = self.buffers(residual.shape[0], y is not None, w_post is not None, w_pre is not None, normed)
+            out = _made(stream, self.buffers, residual.shape[0], y is not None, w_post is not None, w_pre is not None, normed)
         rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev),
                        residual, y, w_post, gate, w_pre, out.h, out.n, out.codes, out.sf, out.rstd_post, out.rstd_pre)
         if rc:
@@ -211,10 +212,13 @@ class Router:
             o.seq_tokens = o.tokens[:num_seqs]
         return o
 
+    def _grad_buffer(self, num_tokens):
+        return torch.empty(num_tokens, self.num_experts, dtype=self.logits_dtype, device=self.device)
+
     def forward(self, logits, bias=None, out=None, stream=None) -> RouterOutput:
         """topk_idx and topk_weights of logits [T, E] (bias f32 [E]: for the choice alone)."""
         if out is None:
-            out = self.buffers(logits.shape[0])
+            out = _made(stream, self.buffers, logits.shape[0])
         rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), logits, bias, out.topk_idx, out.topk_weights)
         if rc:
             _check(rc, "moe_router_forward")
@@ -223,7 +227,7 @@ class Router:
     def forward_train(self, logits, bias=None, seq_offsets=None, out=None, stream=None) -> RouterOutput:
         """The same with the losses, in one pass; seq_offsets int32 [S + 1], or None for one sequence."""
         if out is None:
-            out = self.buffers(logits.shape[0], 1 if seq_offsets is None else seq_offsets.shape[0] - 1)
+            out = _made(stream, self.buffers, logits.shape[0], 1 if seq_offsets is None else seq_offsets.shape[0] - 1)
         rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), logits, bias, out.topk_idx, out.topk_weights,
                        seq_offsets, out.loss, out.counts, out.prob_mean, out.tokens, *self._limits)
         if rc:
@@ -235,7 +239,7 @@ class Router:
         """The losses of a choice made elsewhere.  The result has that choice as its topk_idx, for backward, and no
         weights; of `out` the loss tensors are used, and its own choice stays what it is."""
         if out is None:
-            out = self.buffers(logits.shape[0], 1 if seq_offsets is None else seq_offsets.shape[0] - 1, choice=False)
+            out = _made(stream, self.buffers, logits.shape[0], 1 if seq_offsets is None else seq_offsets.shape[0] - 1, False)
         rc = self._bal(self._bal_at, self._cfg, self._dev, _stream(stream, self._dev), logits, topk_idx,
                        seq_offsets, out.loss, out.counts, out.prob_mean, out.tokens, *self._limits)
         if rc:
@@ -250,7 +254,7 @@ class Router:
         """d_logits through topk_weights (`d_weights` [T, k]) and through loss[0] (`d_loss`, an f32 scalar on the
         device); `fwd` is what the forward call returned, and seq_offsets need not be given again."""
         if out is None:
-            out = torch.empty(logits.shape[0], self.num_experts, dtype=self.logits_dtype, device=self.device)
+            out = _made(stream, self._grad_buffer, logits.shape[0])
         args = (self._bwd_at, self._cfg, self._dev, _stream(stream, self._dev), logits,
                 fwd.topk_idx if d_weights is not None else None, d_weights, out)
         if d_loss is not None:
@@ -292,7 +296,7 @@ class Fp4Linear:
         if not self._ready:
             raise MoEError(-6, "moe_fp4_linear_forward")
         if out is None:
-            out = self.buffers(x.shape[0])
+            out = _made(stream, self.buffers, x.shape[0])
         rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), x, add, out, self.weights.data_ptr())
         if rc:
             _check(rc, "moe_fp4_linear_forward")
