@@ -7,6 +7,10 @@ the CUDA library (include/moe.h).  Every call takes ``out`` buffers made once
 with ``buffers()`` / ``grad_buffers()``, so that a decode loop allocates
 nothing, and allocates them itself, as memory of the stream it runs on, when
 it gets none.
+
+They take no part in autograd: outputs have no graph, gradients come from the
+backward() calls, and a forward call whose inputs require gradients (outside
+torch.no_grad()) warns of that.
 """
 from __future__ import annotations
 

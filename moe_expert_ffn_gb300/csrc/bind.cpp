@@ -10,6 +10,7 @@
 // device index (-1: CPU) and the stream's handle, then tensors (None where
 // absent), and return the library's code.  They keep nothing between calls.
 #include <Python.h>
+#include <c10/core/GradMode.h>
 #include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <torch/version.h>
@@ -48,6 +49,7 @@ at::ScalarType type_of(int dtype) { return dtype == MOE_DTYPE_F32 ? at::kFloat :
 struct Args {
     PyObject *const *at, *const *end;
     int index = -1;
+    bool grad = false;   // an input requires a gradient
 
     Args(PyObject *const *args, Py_ssize_t n) : at(args), end(args + n) {}
     PyObject *next() {
@@ -76,7 +78,17 @@ struct Args {
         const bool shape = rows < 0 ? t.dim() == 1 && t.size(0) == cols : t.dim() == 2 && t.size(0) == rows && t.size(1) == cols;
         if (!shape || t.scalar_type() != dt || t.get_device() != index) refuse(t, name, dt, rows, cols, "on the operator's device");
     }
-    static void *pointer(const at::Tensor &t, bool out) { return out ? t.mutable_data_ptr() : const_cast<void *>(t.const_data_ptr()); }
+    void *pointer(const at::Tensor &t, bool out) {
+        grad |= !out && t.requires_grad();
+        return out ? t.mutable_data_ptr() : const_cast<void *>(t.const_data_ptr());
+    }
+    // Called by the forward passes, whose outputs know nothing of their inputs' graph.
+    void tell_of_graph(const char *what) const {
+        if (!grad || !c10::GradMode::is_enabled()) return;
+        const std::string s = std::string(what) + " got an input that requires a gradient, but takes no part in autograd: its outputs "
+                              "are cut from the graph. Call it under torch.no_grad(), and the operator's backward() for gradients.";
+        if (PyErr_WarnEx(PyExc_UserWarning, s.c_str(), 1) < 0) throw PythonError{};
+    }
 
     // A [rows, cols] tensor whose rows are contiguous.
     template <class P>
@@ -188,6 +200,7 @@ int norm_forward(Args &a) {
     }
     if (y && w_post) a.flat(rstd_post, "rstd_post", at::kFloat, -1, T, io.rstd_post, true);
     if (w_pre) a.flat(rstd_pre, "rstd_pre", at::kFloat, -1, T, io.rstd_pre, true);
+    a.tell_of_graph("BlockNorm.forward");
     return unlocked(a, [&] { return c.fn(c.cfg, T, &io, c.stream); });
 }
 
@@ -269,6 +282,7 @@ int router_forward(Args &a) {
     const bool with_loss = a.at != a.end;
     if (with_loss) losses(a, T, E, true, io, ws);
     a.done();
+    a.tell_of_graph("Router.forward");
     return unlocked(a, [&] { return c.fn(c.cfg, T, l, ld, b, i, w, with_loss ? &io : nullptr, ws, c.stream); });
 }
 
@@ -287,6 +301,7 @@ int balance_loss(Args &a) {
     void *ws;
     losses(a, T, E, true, io, ws);
     a.done();
+    a.tell_of_graph("Router.balance_loss");
     return unlocked(a, [&] { return c.fn(c.cfg, T, l, ld, i, &io, ws, c.stream); });
 }
 
@@ -348,6 +363,7 @@ int linear_forward(Args &a) {
     a.rows(x, "x", at::kBFloat16, T, c.cfg->in_features, xp, ldx, false);
     a.rows(add, "add", o, T, n, ap, lda, false);
     a.rows(needed(y, "y"), "y", o, T, n, yp, ldy, true);
+    a.tell_of_graph("Fp4Linear.forward");
     return unlocked(a, [&] { return c.fn(c.cfg, T, xp, ldx, store, ap, lda, yp, ldy, c.stream); });
 }
 
