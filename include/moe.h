@@ -349,6 +349,12 @@ MOE_API int moe_norm_backward(const moe_norm_config *cfg, int num_tokens, const 
 
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
+/* What a bias is added to for the choice: the logit, or (MOE_SCORE_SIGMOID
+ * only) the score, as routers are trained that balance their experts by such
+ * biases.  The two choose differently: of logits 4 and 0 with biases 0 and
+ * 0.6, the first by logits, the second by scores. */
+typedef enum { MOE_BIAS_LOGIT = 0, MOE_BIAS_SCORE = 1 } moe_bias;
+
 typedef struct {
     int num_experts;      /* E, 1..1024 */
     int topk;             /* k, 1..min(32, E) */
@@ -358,13 +364,16 @@ typedef struct {
     float weight_scale;   /* finite */
     float balance_coef;   /* alpha of the balance loss, finite */
     float z_coef;         /* beta of the z loss, finite; 0 with MOE_SCORE_SIGMOID */
+    int bias_on;          /* moe_bias */
 } moe_router_config;
 
-/* The choice: the k largest logit + bias (f32 sums), ties to the lowest
- * expert.  A logit of -inf or NaN, or a sum that is, closes its expert for
- * the token; a slot with no open expert left gets topk_idx -1 and weight 0
- * (moe_forward's inactive slot).  +inf counts as the largest finite f32.  The
- * bias takes no part in the scores. */
+/* The choice: the k largest logit + bias, or score + bias (f32 sums, the
+ * score within 2^-19 of itself or 2^-40), ties to the lowest expert; without a
+ * bias the k largest logits.  A logit of -inf or NaN, or a sum that is, closes
+ * its expert for the token; a slot with no open expert left gets topk_idx -1
+ * and weight 0 (moe_forward's inactive slot).  +inf counts as the largest
+ * finite f32.  The bias takes no part in the weights.  Experts are not limited
+ * to groups. */
 
 #define MOE_MAX_SEQS (1 << 20)
 

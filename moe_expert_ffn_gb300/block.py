@@ -25,6 +25,7 @@ DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 GATES = {None: 0, "channel": 1, "token": 2}
 QUANTS = {None: 0, "fp8": 1, "ue8m0": 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
+BIASES = {"logit": 0, "score": 1}
 ACTS = {None: 0, "swiglu": 1}
 FP4_LINEAR_MAX_TOKENS = 16
 
@@ -177,17 +178,18 @@ class RouterOutput:
 
 class Router:
     """Top-k router: topk_idx and topk_weights for MoELayer.forward from logits, the balance and z losses
-    with per-sequence expert counts, and the gradient of the logits.  Losses use a workspace of this
+    with per-sequence expert counts, and the gradient of the logits.  A bias, which takes part in the choice alone, is
+    added to the logits or (``bias_on`` "score", with sigmoid scores) to the scores.  Losses use a workspace of this
     object: two loss calls of one Router must not run concurrently."""
 
     def __init__(self, num_experts, topk, score="softmax", renormalize=True, weight_scale=1.0, balance_coef=0.0, z_coef=0.0,
-                 logits_dtype=torch.float32, max_tokens=None, max_seqs=1, device=None):
+                 logits_dtype=torch.float32, max_tokens=None, max_seqs=1, device=None, bias_on="logit"):
         self.num_experts, self.topk, self.logits_dtype = int(num_experts), int(topk), logits_dtype
         self.max_tokens, self.max_seqs = max_tokens, int(max_seqs)
         self.device = _device(device)
         self.cfg = RouterConfig(int(num_experts), int(topk), _choice(SCORES, score, "score"), int(bool(renormalize)),
                                 _choice(DTYPES, logits_dtype, "logits_dtype"), float(weight_scale), float(balance_coef),
-                                float(z_coef))
+                                float(z_coef), _choice(BIASES, bias_on, "bias_on"))
         need = lib().moe_router_workspace_bytes(self.cfg, 0 if max_tokens is None else int(max_tokens), self.max_seqs)
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "router config")

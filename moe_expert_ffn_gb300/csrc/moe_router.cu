@@ -70,7 +70,7 @@ struct RouterParams {
     const int32_t *seq_offsets;
     Partials part;
     int T, E, k, S, chunk;      // chunk: tokens per CTA
-    int sigmoid, renorm;
+    int sigmoid, renorm, score_bias;
     float scale;
 };
 
@@ -458,6 +458,10 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
                     float key[NI];
 #pragma unroll
                     for (int i = 0; i < NI; ++i) key[i] = p.bias ? l[i] + bias[i] : l[i];
+                    if (p.score_bias) {   // 32767 x 256 bf16 20.5 us, on the logits 18.2
+#pragma unroll
+                        for (int i = 0; i < NI; ++i) key[i] = l[i] > -INFINITY ? sigmoid_scaled(l[i], 0.0f) + bias[i] : -INFINITY;
+                    }
                     if (pass) {   // -inf + inf closes
 #pragma unroll
                         for (int i = 0; i < NI; ++i) key[i] = fmaxf(key[i], -INFINITY);
@@ -831,6 +835,7 @@ bool valid(const moe_router_config *c) {
     if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return false;
     if (!valid_dtype(c->logits_dtype)) return false;
     if (!isfinite(c->weight_scale) || !isfinite(c->balance_coef) || !isfinite(c->z_coef)) return false;
+    if (c->bias_on != MOE_BIAS_LOGIT && (c->bias_on != MOE_BIAS_SCORE || c->score != MOE_SCORE_SIGMOID)) return false;
     return c->score == MOE_SCORE_SOFTMAX || c->z_coef == 0.0f;
 }
 
@@ -940,6 +945,7 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.k = cfg->topk;
     p.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
     p.renorm = cfg->renormalize != 0;
+    p.score_bias = bias && cfg->bias_on == MOE_BIAS_SCORE;
     p.scale = cfg->weight_scale;
     p.S = loss ? loss->num_seqs : 1;
     p.seq_offsets = loss ? loss->seq_offsets : nullptr;
