@@ -1010,8 +1010,9 @@ int moe_router_backward(const moe_router_config *cfg, int num_tokens, const void
                         const int32_t *topk_idx, const float *d_weights, const moe_balance_io *loss,
                         const float *d_loss, void *d_logits, int64_t ld_d_logits, void *stream) {
     if (!valid(cfg) || num_tokens < 0 || (!d_weights && !d_loss)) return MOE_ERR_INVALID_ARG;
-    if (d_loss && (!loss || loss->num_seqs < 1 || (!loss->seq_offsets && loss->num_seqs != 1) || !loss->counts ||
-                   !loss->seq_tokens))
+    if (d_loss && (!loss || loss->num_seqs < 1 || loss->num_seqs > MOE_MAX_SEQS || (!loss->seq_offsets && loss->num_seqs != 1) ||
+                   !loss->counts || !loss->seq_tokens || !aligned_to(loss->seq_offsets, 4) || !aligned_to(loss->counts, 4) ||
+                   !aligned_to(loss->seq_tokens, 4)))
         return MOE_ERR_INVALID_ARG;
     if (num_tokens == 0) return MOE_OK;
     const size_t es = dtype_bytes(cfg->logits_dtype);
