@@ -111,11 +111,6 @@ struct Raw8<bf16> {
         r = make_uint4(bf16x2(v.p[0].x, v.p[0].y), bf16x2(v.p[1].x, v.p[1].y), bf16x2(v.p[2].x, v.p[2].y),
                        bf16x2(v.p[3].x, v.p[3].y));
     }
-    __device__ __forceinline__ void put(int j, bf16 e) {   // j known at compile time
-        uint32_t &w = j < 2 ? r.x : j < 4 ? r.y : j < 6 ? r.z : r.w;
-        const uint32_t b = __bfloat16_as_ushort(e);
-        w = (j & 1) ? (w & 0xFFFFu) | b << 16 : b;
-    }
 };
 template <>
 struct Raw8<float> {
@@ -146,31 +141,12 @@ struct Raw8<float> {
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[2 * j] = v.p[j].x, f[2 * j + 1] = v.p[j].y;
     }
-    __device__ __forceinline__ void put(int j, float e) { f[j] = e; }
 };
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-    return v;
-}
-
-// Sum over the CTA in a fixed order; `red` holds one float per warp and must
-// not be used again before the next barrier of the CTA.
-template <int kWarps>
-__device__ __forceinline__ float block_sum(float v, float *red) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += red[w];
-    return s;
 }
 
 // 2^e, e in [-126, 127].
