@@ -309,8 +309,8 @@ typedef struct {
     const void *w_pre;                          /* [H] or NULL */
     void *h; int64_t ld_h;                      /* [T, H] out, with y */
     void *n; int64_t ld_n;                      /* [T, H] out or NULL, with w_pre */
-    uint8_t *codes;                             /* [T, H] out, with cfg->quant */
-    void *sf;                                   /* f32 [T, H/128] or u8 [T, H/32] out, with cfg->quant */
+    uint8_t *codes;                             /* [T, H] out, with cfg->quant; 16-byte aligned */
+    void *sf;                                   /* f32 [T, H/128] or u8 [T, H/32] out, with cfg->quant; 4-byte aligned */
     float *rstd_post, *rstd_pre;                /* [T] out or NULL: r1, r2 for the backward pass */
 } moe_norm_io;
 
@@ -433,8 +433,9 @@ typedef struct {
 } moe_fp4_linear_config;
 
 /* Weights in the layer's FP4 format (MOE_W_FP4_E2M1_UE8M0_32): w u8 [N, K/2]
- * (low nibble = even k), w_sf u8 UE8M0 [N, K/32] (code 255 is not a number
- * and must not occur).  They are laid out once into a store of
+ * (low nibble = even k; 16-byte aligned), w_sf u8 UE8M0 [N, K/32] (code 255
+ * is not a number and must not occur; a code 127 or more below its row's
+ * largest counts as a scale of 0).  They are laid out once into a store of
  * moe_fp4_linear_weight_bytes() bytes (0 if `cfg` is invalid; 256-byte
  * aligned) and may be freed once the stream has passed that call. */
 MOE_API size_t moe_fp4_linear_weight_bytes(const moe_fp4_linear_config *cfg);

@@ -12,7 +12,7 @@
 // Forward: a row's time is two reductions one after the other, each a barrier,
 // so what counts is that memory is busy meanwhile: the next rows come through
 // private slots of shared memory by asynchronous copies, and two CTAs share an
-// SM.  4096 rows of 7168 bf16 with codes and normed output: 44.3 us, 6.0 TB/s
+// SM.  4096 rows of 7168 bf16 with codes and normed output: 44.2 us, 6.0 TB/s
 // (a simple kernel with a CTA a row 135); 1023 rows of 4096 to UE8M0 codes
 // 10.5 us; one row 3.9 us, which is the latency of a launch, three dependent
 // trips to memory and shared memory and two barriers.
@@ -21,9 +21,9 @@
 // of them have arrived and one after the fourth; the column sums stay in
 // registers (two per column are enough: the gradients of w_post and of a
 // channel's gate are the same sum times the other one) and are joined by a
-// second kernel in a fixed order.  4096 rows of 7168 bf16: 75.1 us, 4.7 TB/s,
+// second kernel in a fixed order.  4096 rows of 7168 bf16: 76.0 us, 4.6 TB/s,
 // 66 of them in the main kernel (a simple kernel 719); 1777 rows of 1001 f32
-// by element: 13.8 us.
+// by element: 13.9 us.
 #include <math.h>
 
 #include <algorithm>
@@ -794,7 +794,7 @@ cudaError_t launch_fwd(const NormFwd &p, cudaStream_t s) {
     if (p.H <= 512) return launch_fwd<S, 2, M, true, kNone, 128, 1>(p, s);
     if constexpr (M == kVec) {
         // More rows than SMs: two CTAs an SM, so that one works while the other waits at its barrier, with the parameters
-        // in shared memory because no registers are left for them (4096 x 7168 bf16: 44.5 us, one CTA with registers 53.8;
+        // in shared memory because no registers are left for them (4096 x 7168 bf16: 44.2 us, one CTA with registers 53.8;
         // 160 rows 6.2 and 6.1).  Fewer rows: each has an SM to itself, and registers save the trip (1 row 3.9 us against
         // 4.2, 128 rows 4.1 against 5.8).  f32 rows are twice as long, which leaves two CTAs' shared memory no second slot
         // beside the parameters: registers (1767 x 4096: 24.8 us against 29.1, 2000 x 7168 42.7 and 42.3).
@@ -851,21 +851,21 @@ template <class S, Map M>
 cudaError_t launch_bwd(const NormBwd &p, int &parts, cudaStream_t s) {
     if constexpr (M == kVec) {
         // Two rows a pass where both fit the CTA's shared memory: half the barriers, and the parameters read once for two
-        // (4096 x 7168 bf16: 75 us, one row a pass 86).
+        // (4096 x 7168 bf16: 76 us, one row a pass 86).
         constexpr int kRows = sizeof(S) == 2 ? 2 : 1;
         const int per_sm = bwd_per_sm(p.H, false);
         // Few short rows, less than two passes a CTA: one chunk a thread and a row a pass (300 x 1024 bf16: 7.8 us against
         // 10.3; 32768 x 1024: 92 against 71).
         if (p.H <= 2048 && p.T < 2 * 152 * per_sm)
             return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts = ctas_of(p.T, p.H <= 1024 ? 4 : 2), s);
-        // A row to a CTA: no second one (152 x 7168 bf16: 13.5 us, against 14.9; 1 x 4096: 8.0 and 9.2).
+        // A row to a CTA: no second one (152 x 7168 bf16: 13.1 us, against 14.9; 1 x 4096: 7.5 and 9.2).
         if (p.H <= 8192 && (kRows == 1 || p.T <= 152 * per_sm))
             return launch_bwd<S, 2, 1, M, false, 512, 1>(p, parts = ctas_of(p.T, per_sm), s);
         if (p.H <= 8192) return launch_bwd<S, 2, kRows, M, false, 512, 1>(p, parts = ctas_of(p.T, per_sm), s);
         return launch_bwd<S, 2, 1, M, true, 1024, 1>(p, parts = ctas_of(p.T, 1), s);
     } else {
         // By element into registers a row ahead: one chunk a thread, for which they last.  Wider rows come in as they are
-        // needed, behind other CTAs' (4096 x 5001 bf16: 196 us, two chunks a thread ahead, spilled, 281).
+        // needed, behind other CTAs' (4096 x 5001 bf16: 193 us, two chunks a thread ahead, spilled, 281).
         if (p.H <= 2048) return launch_bwd<S, 1, 1, M, false, 256, 2>(p, parts = ctas_of(p.T, p.H <= 1024 ? 4 : 2), s);
         if (p.H <= 4096) return launch_bwd<S, 1, 1, M, false, 512, 1>(p, parts = ctas_of(p.T, 1), s);
         return launch_bwd<S, 2, 1, M, true, 1024, 1>(p, parts = ctas_of(p.T, bwd_per_sm(p.H, true)), s);

@@ -25,12 +25,12 @@
 // order: no float atomics, the same bits every time.
 //
 // Measured: 32767 tokens of 256 bf16 logits, 8 chosen, sigmoid with a bias:
-// 18.7 us, 380 warp instructions a token, two thirds of the issue slots taken
+// 18.5 us, 380 warp instructions a token, two thirds of the issue slots taken
 // and the integer pipe the busiest (reading the logits alone would take 2.8; a
 // simple kernel 38.9).  65536 tokens of 256 f32 logits in 17 sequences with
-// losses and the whole gradient: 79.2 us (forward 40, sums 5, backward 34;
-// bytes alone 21.1; simple kernels 339).  128 tokens: 2.0 us.  2048 tokens of
-// 8 experts, losses of a given choice and gradient: 8.0 us, three launches,
+// losses and the whole gradient: 77 us (forward 40, sums 5, backward 32; bytes
+// alone 21.1; simple kernels 339).  128 tokens: 2.0 us.  2048 tokens of 8
+// experts, losses of a given choice and gradient: 8.0 us, three launches,
 // each a chain of a few trips to memory.
 #include <float.h>
 #include <math.h>
@@ -396,7 +396,7 @@ __device__ __forceinline__ float over_groups(float v) {
     return v;
 }
 
-// CTAs an SM by the experts of a lane: what registers allow without spills that cost (32767 x 256: four 18.7 us, five or
+// CTAs an SM by the experts of a lane: what registers allow without spills that cost (32767 x 256: four 18.5 us, five or
 // six 20.6 to 22; 28219 x 259: two 20.4, one 29.2).
 constexpr int ctas_an_sm(int NI) { return NI <= 8 ? 4 : NI == 16 ? 2 : 1; }
 
