@@ -36,6 +36,7 @@ def reference(h, dn, w, eps):
 
 def check(m, h, dn, w, eps, dtype):
     r, ref, mag = reference(h, dn, w, eps)
+    assert max(r.max(), mag.max()) < 2.0 ** 126
     op = m.BlockNorm(h.shape[1], float(eps), dtype=dtype, device=DEV)
     fwd = op.forward(h, w_pre=w)
     got = op.backward(h, dn=dn, w_pre=w, rstd_pre=fwd.rstd_pre).dresidual.double().cpu()
