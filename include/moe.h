@@ -448,6 +448,51 @@ MOE_API int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tok
                                    const void *d_weights, const void *add, int64_t ld_add, void *y, int64_t ld_y,
                                    void *stream);
 
+/* ---- FP8 linear ---- */
+
+/* Dense products with weights in the layer's FP8 format (MOE_W_FP8_BLK128)
+ * for any number of tokens, and their gradients.  A matrix is E4M3 codes and
+ * f32 scales, one for each 128 elements along the contracted axis (the last
+ * ones may be fewer), and of weights one for each 128 x 128:
+ *   x  [T, K]: x_sf  [T, ceil(K/128)]           forward (BlockNorm's codes and sf, moe_fp8_quant's)
+ *   w  [N, K]: w_sf  [ceil(N/128), ceil(K/128)]
+ *   dy [T, N]: dy_sf [T, ceil(N/128)]           the input's gradient
+ *   dy [T, N]: dy_sf [ceil(T/128), N], x [T, K]: x_sf [ceil(T/128), K]    the weight's gradient
+ * Codes lie in their natural order in all of them; nothing is laid out anew.
+ * Code matrices and outputs are 16-byte aligned with pitches of a multiple of
+ * 16 bytes; w and the scales are contiguous. */
+typedef struct {
+    int in_features;   /* K, a multiple of 16, 16..2^20 */
+    int out_features;  /* N rows of the weight, a multiple of 16, 16..2^20; of 256 with MOE_ACT_SWIGLU */
+    int act;           /* moe_act; SWIGLU: rows [0, N/2) gate, [N/2, N) up, output silu(gate) * up of N/2 columns */
+    int quant;         /* moe_quant of the forward output: NONE, or with SWIGLU also FP8_128 */
+    int out_dtype;     /* moe_dtype of add, y and dx (without quant) */
+    float act_clamp;   /* symmetric clamp of gate and up before SWIGLU; +INFINITY = off; a NaN stays one */
+} moe_fp8_linear_config;
+
+/* y [T, N or N/2] = act(x W^T) (+ add), sums in f32, one rounding.  With
+ * quant: y u8 [T, N/2] codes of act(x W^T) in f32 and y_sf f32 [T, N/256]
+ * (contiguous), the x and x_sf of a next product; add NULL.  add may be y. */
+MOE_API int moe_fp8_linear_forward(const moe_fp8_linear_config *cfg, int num_tokens, const void *x, int64_t ld_x,
+                                   const float *x_sf, const void *w, const float *w_sf, const void *add, int64_t ld_add,
+                                   void *y, int64_t ld_y, float *y_sf, void *stream);
+
+/* dx [T, K] = dy W (+ add); dy is the gradient of x W^T (before act). */
+MOE_API int moe_fp8_linear_backward_input(const moe_fp8_linear_config *cfg, int num_tokens, const void *dy, int64_t ld_dy,
+                                          const float *dy_sf, const void *w, const float *w_sf, const void *add,
+                                          int64_t ld_add, void *dx, int64_t ld_dx, void *stream);
+
+/* dw f32 [N, K] = dy^T x (+ add): the same call gives the same bits.  add may
+ * be dw (a sum over micro-batches).  Without tokens dw is add, or zero. */
+MOE_API int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int num_tokens, const void *dy, int64_t ld_dy,
+                                           const float *dy_sf, const void *x, int64_t ld_x, const float *x_sf,
+                                           const float *add, int64_t ld_add, float *dw, int64_t ld_dw, void *stream);
+
+/* Synchronises the current device; MOE_ERR_DEVICE_TIMEOUT if a bounded wait of
+ * an FP8 linear kernel gave up there since the last call (its output is
+ * undefined then), else MOE_OK. */
+MOE_API int moe_fp8_linear_status(void);
+
 #ifdef __cplusplus
 }
 #endif

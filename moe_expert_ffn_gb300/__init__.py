@@ -38,6 +38,7 @@ ABI_SYMBOLS = (
     "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward",
     "moe_router_workspace_bytes", "moe_router_forward", "moe_balance_loss", "moe_router_backward",
     "moe_fp4_linear_weight_bytes", "moe_fp4_linear_transform_weights", "moe_fp4_linear_forward",
+    "moe_fp8_linear_forward", "moe_fp8_linear_backward_input", "moe_fp8_linear_backward_weight", "moe_fp8_linear_status",
 )
 
 
@@ -78,6 +79,8 @@ RouterConfig = _struct("RouterConfig", _ints("num_experts", "topk", "score", "re
                        _floats("weight_scale", "balance_coef", "z_coef"), _ints("bias_on"))
 BalanceIO = _struct("BalanceIO", _ints("num_seqs"), _ptrs("seq_offsets", "loss", "counts", "prob_mean", "seq_tokens"))
 Fp4LinearConfig = _struct("Fp4LinearConfig", _ints("in_features", "out_features", "act", "out_dtype"),
+                          _floats("act_clamp"))
+Fp8LinearConfig = _struct("Fp8LinearConfig", _ints("in_features", "out_features", "act", "quant", "out_dtype"),
                           _floats("act_clamp"))
 
 
@@ -132,6 +135,7 @@ def lib():
             L.moe_destroy.argtypes = [vp]
             i64, ncfg, rcfg, fcfg, bio = (ctypes.c_int64, ctypes.POINTER(NormConfig), ctypes.POINTER(RouterConfig),
                                           ctypes.POINTER(Fp4LinearConfig), ctypes.POINTER(BalanceIO))
+            ecfg = ctypes.POINTER(Fp8LinearConfig)
             for name, res, args in (
                     ("moe_norm_forward", i32, [ncfg, i32, ctypes.POINTER(NormIO), vp]),
                     ("moe_norm_workspace_bytes", sz, [ncfg, i32]),
@@ -142,7 +146,11 @@ def lib():
                     ("moe_router_backward", i32, [rcfg, i32, vp, i64, vp, vp, bio, vp, vp, i64, vp]),
                     ("moe_fp4_linear_weight_bytes", sz, [fcfg]),
                     ("moe_fp4_linear_transform_weights", i32, [fcfg, vp, vp, vp, vp]),
-                    ("moe_fp4_linear_forward", i32, [fcfg, i32, vp, i64, vp, vp, i64, vp, i64, vp])):
+                    ("moe_fp4_linear_forward", i32, [fcfg, i32, vp, i64, vp, vp, i64, vp, i64, vp]),
+                    ("moe_fp8_linear_forward", i32, [ecfg, i32, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp]),
+                    ("moe_fp8_linear_backward_input", i32, [ecfg, i32, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp]),
+                    ("moe_fp8_linear_backward_weight", i32, [ecfg, i32, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp]),
+                    ("moe_fp8_linear_status", i32, [])):
                 fn = getattr(L, name)
                 fn.restype, fn.argtypes = res, args
             _lib = L
@@ -318,5 +326,5 @@ class MoELayer:
             pass
 
 
-from .block import (FP4_LINEAR_MAX_TOKENS, BlockNorm, Fp4Linear, NormGrads, NormOutput, Router,  # noqa: E402,F401
+from .block import (FP4_LINEAR_MAX_TOKENS, BlockNorm, Fp4Linear, Fp8Codes, Fp8Linear, NormGrads, NormOutput, Router,  # noqa: E402,F401
                     RouterOutput)

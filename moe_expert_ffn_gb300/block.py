@@ -19,7 +19,7 @@ import math
 
 import torch
 
-from . import MOE_ERR_INVALID_ARG, Fp4LinearConfig, MoEError, NormConfig, RouterConfig, _check, lib
+from . import MOE_ERR_INVALID_ARG, Fp4LinearConfig, Fp8LinearConfig, MoEError, NormConfig, RouterConfig, _check, lib
 
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 GATES = {None: 0, "channel": 1, "token": 2}
@@ -306,4 +306,80 @@ class Fp4Linear:
         rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), x, add, out, self.weights.data_ptr())
         if rc:
             _check(rc, "moe_fp4_linear_forward")
+        return out
+
+
+class Fp8Codes:
+    """A matrix in the layer's FP8 format: codes (u8 [rows, columns]) with sf, f32 scales for each 128 columns of a row (of
+    weights for each 128 x 128), and col_codes with col_sf, scales for each 128 rows of a column (None where absent)."""
+    __slots__ = ("codes", "sf", "col_codes", "col_sf")
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+class Fp8Linear:
+    """y = act(x W^T) (+ add) with E4M3 codes and f32 scales: x per 1 x 128, W per 128 x 128 (the layer's FP8 format), any
+    number of tokens, and its gradients.  act "swiglu": rows [0, N/2) gate, [N/2, N) up, N/2 outputs; with quant "fp8" these
+    come as the codes and scales of a next product's input.  Weights go with every call and may change between calls."""
+
+    def __init__(self, in_features, out_features, act=None, quant=None, out_dtype=torch.bfloat16, act_clamp=math.inf, device=None):
+        self.device, self.out_dtype, self.quant = _device(device), out_dtype, quant
+        self.in_features, self.out_features = int(in_features), int(out_features)
+        self.out_columns = self.out_features // 2 if act == "swiglu" else self.out_features
+        self.cfg = Fp8LinearConfig(int(in_features), int(out_features), _choice(ACTS, act, "act"), _choice(QUANTS, quant, "quant"),
+                                   _choice(DTYPES, out_dtype, "out_dtype"), float(act_clamp))
+        L, b = lib(), _bind()
+        # a call without tokens checks the config alone
+        if L.moe_fp8_linear_backward_input(self.cfg, 0, None, 0, None, None, None, None, 0, None, 0, None):
+            raise MoEError(MOE_ERR_INVALID_ARG, "fp8 linear config")
+        self._cfg, self._dev = ctypes.addressof(self.cfg), _index(self.device)
+        self._fwd, self._dx, self._dw = b.fp8_forward, b.fp8_backward_input, b.fp8_backward_weight
+        self._fwd_at, self._dx_at, self._dw_at = (_address(L.moe_fp8_linear_forward), _address(L.moe_fp8_linear_backward_input),
+                                                  _address(L.moe_fp8_linear_backward_weight))
+
+    def buffers(self, num_tokens):
+        """The output of a forward of `num_tokens`: a tensor, or Fp8Codes with quant."""
+        if not self.quant:
+            return torch.empty(num_tokens, self.out_columns, dtype=self.out_dtype, device=self.device)
+        o = Fp8Codes()
+        o.codes = torch.empty(num_tokens, self.out_columns, dtype=torch.uint8, device=self.device)
+        o.sf = torch.empty(num_tokens, self.out_columns // 128, dtype=torch.float32, device=self.device)
+        o.col_codes = o.col_sf = None
+        return o
+
+    def input_grad_buffer(self, num_tokens):
+        return torch.empty(num_tokens, self.in_features, dtype=self.out_dtype, device=self.device)
+
+    def weight_grad_buffer(self):
+        return torch.empty(self.out_features, self.in_features, dtype=torch.float32, device=self.device)
+
+    def forward(self, x, x_sf, w, w_sf, add=None, out=None, stream=None):
+        """x u8 [T, K] with x_sf [T, ceil(K/128)], w u8 [N, K] with w_sf [ceil(N/128), ceil(K/128)]."""
+        if out is None:
+            out = _made(stream, self.buffers, x.shape[0])
+        y, y_sf = (out.codes, out.sf) if self.quant else (out, None)
+        rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), x, x_sf, w, w_sf, add, y, y_sf)
+        if rc:
+            _check(rc, "moe_fp8_linear_forward")
+        return out
+
+    def backward_input(self, dy, dy_sf, w, w_sf, add=None, out=None, stream=None):
+        """dx [T, K] = dy W (+ add): dy u8 [T, N] with dy_sf [T, ceil(N/128)], the gradient of x W^T (before act)."""
+        if out is None:
+            out = _made(stream, self.input_grad_buffer, dy.shape[0])
+        rc = self._dx(self._dx_at, self._cfg, self._dev, _stream(stream, self._dev), dy, dy_sf, w, w_sf, add, out)
+        if rc:
+            _check(rc, "moe_fp8_linear_backward_input")
+        return out
+
+    def backward_weight(self, dy, dy_sf, x, x_sf, add=None, out=None, stream=None):
+        """dw f32 [N, K] = dy^T x (+ add, which may be `out`): codes with scales along the tokens, dy_sf [ceil(T/128), N] and
+        x_sf [ceil(T/128), K]."""
+        if out is None:
+            out = _made(stream, self.weight_grad_buffer)
+        rc = self._dw(self._dw_at, self._cfg, self._dev, _stream(stream, self._dev), dy, dy_sf, x, x_sf, add, out)
+        if rc:
+            _check(rc, "moe_fp8_linear_backward_weight")
         return out

@@ -367,6 +367,78 @@ int linear_forward(Args &a) {
     return unlocked(a, [&] { return c.fn(c.cfg, T, xp, ldx, store, ap, lda, yp, ldy, c.stream); });
 }
 
+int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+// ..., x, x_sf, w, w_sf, add, y, y_sf
+int fp8_forward(Args &a) {
+    const Head<decltype(&moe_fp8_linear_forward), moe_fp8_linear_config> c(a);
+    const int64_t K = c.cfg->in_features, N = c.cfg->out_features, n = c.cfg->act == MOE_ACT_SWIGLU ? N / 2 : N;
+    const bool quant = c.cfg->quant != MOE_QUANT_NONE;
+    const at::ScalarType o = quant ? at::kByte : type_of(c.cfg->out_dtype);
+    const at::Tensor *x = a.tensor("x"), *x_sf = a.tensor("x_sf"), *w = a.tensor("w"), *w_sf = a.tensor("w_sf"), *add = a.tensor("add"),
+                     *y = a.tensor("y"), *y_sf = a.tensor("y_sf");
+    a.done();
+    const int T = tokens(x, "x");
+    const void *xp, *wp, *ap;
+    void *yp;
+    const float *xs, *ws;
+    float *ys = nullptr;
+    int64_t ldx, lda, ldy;
+    if (quant && add) fail(PyExc_ValueError, "add is not for a quantised output");
+    a.rows(x, "x", at::kByte, T, K, xp, ldx, false);
+    a.flat(needed(x_sf, "x_sf"), "x_sf", at::kFloat, T, blocks(K), xs, false);
+    a.flat(needed(w, "w"), "w", at::kByte, N, K, wp, false);
+    a.flat(needed(w_sf, "w_sf"), "w_sf", at::kFloat, blocks(N), blocks(K), ws, false);
+    a.rows(add, "add", o, T, n, ap, lda, false);
+    a.rows(needed(y, quant ? "codes" : "y"), quant ? "codes" : "y", o, T, n, yp, ldy, true);
+    if (quant) a.flat(needed(y_sf, "sf"), "sf", at::kFloat, T, n / 128, ys, true);
+    a.tell_of_graph("Fp8Linear.forward");
+    return unlocked(a, [&] { return c.fn(c.cfg, T, xp, ldx, xs, wp, ws, ap, lda, yp, ldy, ys, c.stream); });
+}
+
+// ..., dy, dy_sf, w, w_sf, add, dx
+int fp8_backward_input(Args &a) {
+    const Head<decltype(&moe_fp8_linear_backward_input), moe_fp8_linear_config> c(a);
+    const int64_t K = c.cfg->in_features, N = c.cfg->out_features;
+    const at::ScalarType o = type_of(c.cfg->out_dtype);
+    const at::Tensor *dy = a.tensor("dy"), *dy_sf = a.tensor("dy_sf"), *w = a.tensor("w"), *w_sf = a.tensor("w_sf"),
+                     *add = a.tensor("add"), *dx = a.tensor("dx");
+    a.done();
+    const int T = tokens(dy, "dy");
+    const void *dp, *wp, *ap;
+    void *xp;
+    const float *ds, *ws;
+    int64_t ldd, lda, ldx;
+    a.rows(dy, "dy", at::kByte, T, N, dp, ldd, false);
+    a.flat(needed(dy_sf, "dy_sf"), "dy_sf", at::kFloat, T, blocks(N), ds, false);
+    a.flat(needed(w, "w"), "w", at::kByte, N, K, wp, false);
+    a.flat(needed(w_sf, "w_sf"), "w_sf", at::kFloat, blocks(N), blocks(K), ws, false);
+    a.rows(add, "add", o, T, K, ap, lda, false);
+    a.rows(needed(dx, "dx"), "dx", o, T, K, xp, ldx, true);
+    return unlocked(a, [&] { return c.fn(c.cfg, T, dp, ldd, ds, wp, ws, ap, lda, xp, ldx, c.stream); });
+}
+
+// ..., dy, dy_sf, x, x_sf, add, dw
+int fp8_backward_weight(Args &a) {
+    const Head<decltype(&moe_fp8_linear_backward_weight), moe_fp8_linear_config> c(a);
+    const int64_t K = c.cfg->in_features, N = c.cfg->out_features;
+    const at::Tensor *dy = a.tensor("dy"), *dy_sf = a.tensor("dy_sf"), *x = a.tensor("x"), *x_sf = a.tensor("x_sf"),
+                     *add = a.tensor("add"), *dw = a.tensor("dw");
+    a.done();
+    const int T = tokens(dy, "dy");
+    const void *dp, *xp;
+    const float *ds, *xs, *ap;
+    float *wp;
+    int64_t ldd, ldx, lda, ldw;
+    a.rows(dy, "dy", at::kByte, T, N, dp, ldd, false);
+    a.flat(needed(dy_sf, "dy_sf"), "dy_sf", at::kFloat, blocks(T), N, ds, false);
+    a.rows(needed(x, "x"), "x", at::kByte, T, K, xp, ldx, false);
+    a.flat(needed(x_sf, "x_sf"), "x_sf", at::kFloat, blocks(T), K, xs, false);
+    a.rows(add, "add", at::kFloat, N, K, ap, lda, false);
+    a.rows(needed(dw, "dw"), "dw", at::kFloat, N, K, wp, ldw, true);
+    return unlocked(a, [&] { return c.fn(c.cfg, T, dp, ldd, ds, xp, ldx, xs, ap, lda, wp, ldw, c.stream); });
+}
+
 template <int (*F)(Args &)>
 PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F>)), METH_FASTCALL, nullptr};
@@ -375,7 +447,9 @@ PyMethodDef method(const char *name) {
 PyMethodDef methods[] = {method<norm_forward>("norm_forward"),         method<norm_backward>("norm_backward"),
                          method<router_forward>("router_forward"),     method<balance_loss>("balance_loss"),
                          method<router_backward>("router_backward"),   method<linear_transform>("linear_transform"),
-                         method<linear_forward>("linear_forward"),     {nullptr, nullptr, 0, nullptr}};
+                         method<linear_forward>("linear_forward"),     method<fp8_forward>("fp8_forward"),
+                         method<fp8_backward_input>("fp8_backward_input"), method<fp8_backward_weight>("fp8_backward_weight"),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", "Tensors to the C ABI of the block operators.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 

@@ -172,6 +172,13 @@ size_t x_sf_bytes(const moe_config &g, int T) {
 
 }  // namespace
 
+namespace moe {
+bool encode_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
+                uint32_t box_outer) {
+    return make_map(m, base, inner, outer, stride, box_inner, box_outer);
+}
+}  // namespace moe
+
 struct moe_ctx {
     moe_config cfg;
     Layout L;

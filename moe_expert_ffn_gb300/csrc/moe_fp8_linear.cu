@@ -1,0 +1,936 @@
+// moe_fp8_linear.cu -- dense products in E4M3 with f32 scales per 128 (definitions in include/moe.h): the forward product, its
+// input's gradient and its weight's gradient.
+//
+// All three are one product of rows and columns over a contracted axis D, cut into blocks of 128:
+//     out[r, c] = sum_b sr(r, b) sc(c, b) sum_{d in b} rows[r, d] cols[c, d]
+//   forward        rows = x  [T, K], cols = W [N, K]:  sr per token, sc per 128 columns
+//   input's        rows = dy [T, N], cols = W^T:       sr per token, sc per 128 columns
+//   weight's       rows = dy^T,      cols = x^T (D = T): sr and sc per row and column
+// The transposed operands are not copied: the tensor core reads a tile whose contracted axis is the slower one in shared
+// memory as it is ("MN-major"), so every operand is loaded from the layout in which its maker wrote it.
+//
+// The scales are floats, which the tensor core cannot apply, so each block of 128 has an accumulator of its own in TMEM, read
+// and folded into f32 registers while the next ones are computed.
+#include <math.h>
+
+#include <algorithm>
+
+#include "moe.h"
+#include "moe_device.cuh"
+#include "moe_gemm_common.cuh"
+#include "moe_ops.cuh"
+
+namespace moe {
+namespace {
+
+enum Mode { kForward, kSwiglu, kInput, kWeight };
+constexpr bool rows_mn(int m) { return m == kWeight; }                  // whether an operand's contracted axis is the slower one
+constexpr bool cols_mn(int m) { return m == kInput || m == kWeight; }
+
+// The status block of every launch: moe_device.cuh's error words.
+__device__ int g_status[kErrWords];
+
+struct Fp8Params {
+    const float *row_sf, *col_sf;
+    int64_t rs_row, rs_blk;       // row_sf[row * rs_row + block * rs_blk]
+    int64_t cs_col, cs_blk;       // col_sf[col / 128 (weight's: col) * cs_col + block * cs_blk]
+    const void *add;
+    int64_t ld_add;
+    void *out;                    // f32 or bf16 by `f32`, or codes with `sf`
+    int64_t ld_out;
+    float *sf;
+    int R, C, DB;                 // rows and columns of the output, blocks of the contracted axis
+    int tiles_r, tiles_c, split;
+    int f32;
+    int wide;                     // out and add in 32-byte pieces
+    float clamp;
+};
+
+constexpr uint32_t kPanel = 128 * 128;   // 128 rows or columns of one block
+constexpr int kChunk = 8;                // blocks whose scales are brought to shared memory together
+
+// Shared-memory descriptor of 128 rows or columns of a block, 128-byte swizzled: contracted axis the faster one, or the slower
+// one (groups of eight contracted elements 1024 bytes apart).  `step`: what 32 contracted elements add to it.
+template <bool kMN>
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
+    return sw128_kmajor_desc(saddr);   // the same fields: one 128-byte atom across, eight-row groups 1024 bytes apart
+}
+template <bool kMN>
+__device__ constexpr uint32_t operand_step() { return kMN ? 32 * 128 / 16 : 2; }
+
+constexpr uint32_t idesc_major(bool a_mn, bool b_mn) { return (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u); }
+
+__device__ __forceinline__ float clamp_of(float v, float c) { return v < -c ? -c : v > c ? c : v; }   // a NaN stays one
+__device__ __forceinline__ float swiglu_of(float g, float u, float c) {
+    g = clamp_of(g, c);
+    return __fdividef(g, 1.0f + expf(-g)) * clamp_of(u, c);
+}
+
+__device__ __forceinline__ void store_once(void *p, const uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                     "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+__device__ __forceinline__ void load_once(const void *p, uint32_t (&v)[8], bool wide) {
+    if (wide) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        const uint4 a = static_cast<const uint4 *>(p)[0], b = static_cast<const uint4 *>(p)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+}
+// 16 consecutive outputs of a row: out = v (+ add).
+__device__ __forceinline__ void put16(const Fp8Params &p, float (&v)[16], int64_t row, int col) {
+    uint32_t w[8];
+    if (p.f32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (p.add) {
+                load_once(static_cast<const float *>(p.add) + row * p.ld_add + col + 8 * h, w, p.wide);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[8 * h + i] += __uint_as_float(w[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 * h + i]);
+            store_once(static_cast<float *>(p.out) + row * p.ld_out + col + 8 * h, w, p.wide);
+        }
+        return;
+    }
+    if (p.add) {
+        load_once(static_cast<const bf16 *>(p.add) + row * p.ld_add + col, w, p.wide);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[2 * i] += __uint_as_float(w[i] << 16);
+            v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+    store_once(static_cast<bf16 *>(p.out) + row * p.ld_out + col, w, p.wide);
+}
+
+// ============================================================================
+// Many rows: 256 x 256 tiles on CTA pairs
+// ============================================================================
+constexpr int kWideWarps = 12;           // 0 copies, 1 MMA, 2 scales, 4..11 fold and store
+constexpr int kWideThreads = 32 * kWideWarps;
+constexpr int kFoldWarp0 = 4;
+constexpr int kFoldWarps = 8;
+constexpr int kWideStages = 3;
+constexpr uint32_t kWideStage = 4 * kPanel;   // two blocks of this CTA's 128 rows and of its half of the columns
+constexpr int kRowPitch = 132;           // floats between two blocks of row scales: writers of 4 rows x 8 blocks meet no bank twice
+constexpr int kRowGroup = 16;            // row tiles that the walk takes together
+
+struct alignas(8) WideCtrl {
+    uint64_t full[kWideStages], empty[kWideStages];
+    uint64_t tfull[2], tempty[2];
+    uint64_t sfull[2], sempty[2];
+    uint64_t halves[4];              // a row's two fold warps have written their maxima
+    uint32_t tmem_base;
+    int abort;
+    float amax[2][kFoldWarps][32];
+};
+
+template <int kMode>
+struct WideScales {
+    float row[2][kChunk * kRowPitch];
+    float col[2][kMode == kWeight ? kChunk * 256 : kChunk * 2];
+};
+
+template <int kMode>
+constexpr size_t wide_smem() {
+    return 1024 + (size_t)kWideStages * kWideStage + sizeof(WideScales<kMode>) + sizeof(WideCtrl);
+}
+
+struct WideTile {
+    int tr, tc;
+};
+// Row tiles in groups of 16, in a group all of them for a column tile before the next one: what a wave of tiles reads stays in L2.
+__device__ __forceinline__ WideTile wide_tile(int64_t tile, const Fp8Params &p) {
+    const int64_t per = (int64_t)kRowGroup * p.tiles_c;
+    const int g = (int)(tile / per), first = g * kRowGroup, n = min(kRowGroup, p.tiles_r - first);
+    const int local = (int)(tile - g * per);
+    return {first + local % n, local / n};
+}
+
+// acc += the warp's 2 x 64 TMEM columns times their scales; `release` once the last ones are in registers.
+template <bool kCol, class F>
+__device__ __forceinline__ void fold_wide(float2 (&acc)[64], uint32_t t0, uint32_t t1, float s0, float s1, const float *cs,
+                                          F release) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        float v[32], w[32];
+        tmem_ld32(c ? t1 : t0, v);
+        tmem_ld32((c ? t1 : t0) + 32, w);
+        tmem_ld_wait();
+        if (c == 1) release();
+        const float2 s = pair(c ? s1 : s0);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float *from = i < 16 ? v + 2 * i : w + 2 * i - 32;
+            float2 f = s;
+            if (kCol) f = __fmul2_rn(s, *reinterpret_cast<const float2 *>(cs + 64 * c + 2 * i));
+            acc[32 * c + i] = __ffma2_rn(make_float2(from[0], from[1]), f, acc[32 * c + i]);
+        }
+    }
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_cols,
+                    const __grid_constant__ Fp8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    launch_next();
+    const uint32_t raw = smem_u32(smem_raw), base = align1024(raw);
+    uint8_t *after = smem_raw + (base - raw) + kWideStages * kWideStage;
+    WideScales<kMode> &sc = *reinterpret_cast<WideScales<kMode> *>(after);
+    WideCtrl *ctrl = reinterpret_cast<WideCtrl *>(after + sizeof(WideScales<kMode>));
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31, rank = cluster_ctarank();
+    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    const int DB = p.DB, stages = (DB + 1) / 2;
+    const int64_t total = (int64_t)p.tiles_r * p.tiles_c;
+    int *err = g_status;
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tm_rows);
+        tma_prefetch_desc(&tm_cols);
+        for (int s = 0; s < kWideStages; ++s) {
+            mbar_init(smem_u32(&ctrl->full[s]), 1);
+            mbar_init(smem_u32(&ctrl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&ctrl->tfull[b]), 1);
+            mbar_init(smem_u32(&ctrl->tempty[b]), 2 * kFoldWarps);
+            mbar_init(smem_u32(&ctrl->sfull[b]), 1);
+            mbar_init(smem_u32(&ctrl->sempty[b]), kFoldWarps);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ctrl->halves[i]), 2);
+        ctrl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(&ctrl->tmem_base), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = ctrl->tmem_base;
+    volatile int *abort_flag = &ctrl->abort;
+    const uint32_t full_c = mapa_shared(smem_u32(&ctrl->full[0]), 0), tempty_c = mapa_shared(smem_u32(&ctrl->tempty[0]), 0);
+    wait_for_previous();
+
+    if (warp == 0) {
+        // ---- copies: each CTA its 128 rows and its half of the columns (SwiGLU: gate rows of W in the even CTA, up rows in the odd)
+        const uint64_t pol = policy_evict_normal();
+        int it = 0;
+        bool ok = true;
+        for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
+            const WideTile t = wide_tile(tile, p);
+            const int r0 = t.tr * 256 + (int)rank * 128;
+            const int c0 = kMode == kSwiglu ? t.tc * 128 + (int)rank * p.C : t.tc * 256 + (int)rank * 128;
+            for (int ks = 0; ks < stages; ++ks, ++it) {
+                const int s = it % kWideStages, n = min(2, DB - 2 * ks);
+                if (!mbar_wait(smem_u32(&ctrl->empty[s]), ((it / kWideStages) & 1) ^ 1, abort_flag, err)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&ctrl->full[s]), (uint32_t)n * 4 * kPanel);
+                    const uint32_t dst = base + s * kWideStage, full = full_c + 8u * s;
+                    for (int j = 0; j < n; ++j) {
+                        const int d = (2 * ks + j) * 128;
+                        tma_load_2d_pair(dst + j * kPanel, &tm_rows, rows_mn(kMode) ? r0 : d, rows_mn(kMode) ? d : r0, full, pol);
+                        tma_load_2d_pair(dst + (2 + j) * kPanel, &tm_cols, cols_mn(kMode) ? c0 : d, cols_mn(kMode) ? d : c0, full,
+                                         pol);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        for (int i = max(0, it - kWideStages); i < it; ++i)   // the last copies land before the pair ends
+            drain_wait(smem_u32(&ctrl->empty[i % kWideStages]), (i / kWideStages) & 1, err);
+    } else if (warp == 1) {
+        // ---- MMA (even CTA): one block, one accumulator
+        if (rank == 0) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(256, 256) | idesc_major(rows_mn(kMode), cols_mn(kMode));
+            int it = 0, kt = 0;
+            bool ok = true;
+            for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
+                for (int ks = 0; ok && ks < stages; ++ks, ++it) {
+                    const int s = it % kWideStages, n = min(2, DB - 2 * ks);
+                    if (!mbar_wait(smem_u32(&ctrl->full[s]), (it / kWideStages) & 1, abort_flag, err)) {
+                        ok = false;
+                        break;
+                    }
+                    for (int j = 0; j < n; ++j, ++kt) {
+                        const int b = kt & 1;
+                        if (!mbar_wait(smem_u32(&ctrl->tempty[b]), ((kt >> 1) & 1) ^ 1, abort_flag, err)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint64_t a = operand_desc<rows_mn(kMode)>(base + s * kWideStage + j * kPanel);
+                            const uint64_t w = operand_desc<cols_mn(kMode)>(base + s * kWideStage + (2 + j) * kPanel);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_pair_e4m3(tmem + b * 256, a + kk * operand_step<rows_mn(kMode)>(),
+                                               w + kk * operand_step<cols_mn(kMode)>(), idesc, kk > 0);
+                            umma_pair_commit(smem_u32(&ctrl->tfull[b]), 3);
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && lane == 0) umma_pair_commit(smem_u32(&ctrl->empty[s]), 3);
+                    __syncwarp();
+                }
+            }
+            if (it > 0) drain_wait(smem_u32(&ctrl->empty[(it - 1) % kWideStages]), ((it - 1) / kWideStages) & 1, err);
+        }
+    } else if (warp == 2) {
+        // ---- scales of eight blocks at a time to shared memory
+        int ch = 0;
+        bool ok = true;
+        for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
+            const WideTile t = wide_tile(tile, p);
+            const int r0 = t.tr * 256 + (int)rank * 128;
+            for (int k0 = 0; k0 < DB; k0 += kChunk, ++ch) {
+                const int slot = ch & 1;
+                if (!mbar_wait(smem_u32(&ctrl->sempty[slot]), ((ch >> 1) & 1) ^ 1, abort_flag, err)) {
+                    ok = false;
+                    break;
+                }
+                if (kMode == kWeight) {   // neighbouring rows and columns lie together
+                    for (int j = 0; j < kChunk; ++j) {
+                        const int b = k0 + j;
+                        if (b >= DB) break;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = r0 + (int)lane + 32 * i;
+                            sc.row[slot][j * kRowPitch + lane + 32 * i] = r < p.R ? p.row_sf[(int64_t)b * p.rs_blk + r] : 0.0f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int c = t.tc * 256 + (int)lane + 32 * i;
+                            sc.col[slot][j * 256 + lane + 32 * i] = c < p.C ? p.col_sf[(int64_t)b * p.cs_blk + c] : 0.0f;
+                        }
+                    }
+                } else {   // eight blocks of a row lie together: a load takes them of four rows
+                    const int j = lane & 7, b = k0 + j;
+#pragma unroll 8
+                    for (int i = 0; i < 32; ++i) {
+                        const int r = r0 + (int)(lane >> 3) + 4 * i;
+                        sc.row[slot][j * kRowPitch + (lane >> 3) + 4 * i] =
+                            b < DB && r < p.R ? p.row_sf[(int64_t)r * p.rs_row + b] : 0.0f;
+                    }
+                    if (lane < 16) {
+                        const int h = lane >> 3;
+                        const int cb = kMode == kSwiglu ? t.tc + h * (p.C / 128) : t.tc * 2 + h;
+                        const bool on = b < DB && (kMode == kSwiglu || cb * 128 < p.C);
+                        sc.col[slot][j * 2 + h] = on ? p.col_sf[cb * p.cs_col + b * p.cs_blk] : 0.0f;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctrl->sfull[slot]));
+            }
+        }
+    } else if (warp >= kFoldWarp0) {
+        // ---- fold the blocks' accumulators, own 128 rows; warp: 32 rows, half of the columns
+        const int q = warp & 3, h = (warp - kFoldWarp0) >> 2;
+        const int lrow = q * 32 + (int)lane;
+        // SwiGLU: 64 gate columns and the 64 up columns that belong to them
+        const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + (kMode == kSwiglu ? 64 * h : 128 * h);
+        const uint32_t t1 = t0 + (kMode == kSwiglu ? 128 : 64);
+        int kt = 0, ch = 0, done = 0;
+        bool ok = true;
+        for (int64_t tile = cluster; ok && tile < total; tile += clusters, ++done) {
+            const WideTile t = wide_tile(tile, p);
+            float2 acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
+            for (int k0 = 0; ok && k0 < DB; k0 += kChunk, ++ch) {
+                const int slot = ch & 1;
+                if (!mbar_wait(smem_u32(&ctrl->sfull[slot]), (ch >> 1) & 1, abort_flag, err)) {
+                    ok = false;
+                    break;
+                }
+                const int n = min(kChunk, DB - k0);
+                for (int j = 0; j < n; ++j, ++kt) {
+                    const int b = kt & 1;
+                    const float sr = sc.row[slot][j * kRowPitch + lrow];
+                    float s0 = sr, s1 = sr;
+                    const float *cs = nullptr;
+                    if (kMode == kWeight) {
+                        cs = &sc.col[slot][j * 256 + h * 128];
+                    } else if (kMode == kSwiglu) {
+                        s0 = sr * sc.col[slot][2 * j], s1 = sr * sc.col[slot][2 * j + 1];
+                    } else {
+                        s0 = s1 = sr * sc.col[slot][2 * j + h];
+                    }
+                    if (!mbar_wait(smem_u32(&ctrl->tfull[b]), (kt >> 1) & 1, abort_flag, err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    fold_wide<kMode == kWeight>(acc, t0 + b * 256, t1 + b * 256, s0, s1, cs, [&] {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(tempty_c + 8u * b);
+                    });
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctrl->sempty[slot]));
+            }
+            if (!ok) break;
+            const int64_t row = (int64_t)t.tr * 256 + rank * 128 + lrow;
+            if (kMode == kSwiglu) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    acc[i].x = swiglu_of(acc[i].x, acc[32 + i].x, p.clamp);
+                    acc[i].y = swiglu_of(acc[i].y, acc[32 + i].y, p.clamp);
+                    amax = fmaxf(amax, fmaxf(fabsf(acc[i].x), fabsf(acc[i].y)));
+                }
+                const int col = t.tc * 128 + h * 64;
+                if (p.sf) {
+                    // the other 64 columns of the group of 128 are another warp's
+                    float (&all)[kFoldWarps][32] = ctrl->amax[done & 1];
+                    all[warp - kFoldWarp0][lane] = amax;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&ctrl->halves[q]));
+                    if (!mbar_wait(smem_u32(&ctrl->halves[q]), done & 1, abort_flag, err)) break;
+                    amax = fmaxf(amax, all[(warp - kFoldWarp0) ^ 4][lane]);
+                    const GroupScale g = group_scale(amax);
+                    if (row < p.R) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = g.codes(acc[2 * i].x, acc[2 * i].y) | g.codes(acc[2 * i + 1].x, acc[2 * i + 1].y) << 16;
+                        uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row * p.ld_out + col);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                        if (h == 0) p.sf[row * (p.C / 128) + t.tc] = g.sf;
+                    }
+                } else if (row < p.R) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[2 * i] = acc[8 * c + i].x, v[2 * i + 1] = acc[8 * c + i].y;
+                        put16(p, v, row, col + 16 * c);
+                    }
+                }
+            } else if (row < p.R) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const int col = t.tc * 256 + h * 128 + 16 * c;
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[2 * i] = acc[8 * c + i].x, v[2 * i + 1] = acc[8 * c + i].y;
+                    if (col < p.C) put16(p, v, row, col);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    // neither CTA leaves or frees TMEM while the pair's MMA may still touch it
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ============================================================================
+// Few rows: tiles of 128 columns x BT rows, the contracted axis split over a cluster
+// ============================================================================
+constexpr int kSmallThreads = 32 * 11;   // 0 copies, 1 MMA, 2 scales, 3..10 fold
+constexpr int kSmallFold0 = 3;
+
+template <int BT>
+constexpr int small_stages() { return BT == 16 ? 3 : BT == 32 ? 5 : BT == 64 ? 4 : 3; }
+template <int BT>
+constexpr int small_bufs() { return BT <= 64 ? 4 : 2; }
+template <int kMode, int BT>
+constexpr uint32_t small_stage() { return 2 * kPanel + (kMode == kSwiglu ? 1 : 2) * BT * 128; }
+
+template <int kMode, int BT>
+struct SmallCtrl {
+    uint64_t full[small_stages<BT>()], empty[small_stages<BT>()];
+    uint64_t tfull[2][small_bufs<BT>()], tempty[2][small_bufs<BT>()];
+    uint64_t sfull[2], sempty[2];
+    uint32_t tmem_base;
+    int abort;
+    alignas(16) float sc[2][kChunk * (BT + 4)];
+    float lane_sc[2][kMode == kWeight ? kChunk * 128 : 1];
+};
+template <int kMode, int BT>
+constexpr size_t small_smem() {
+    return 1024 + (size_t)small_stages<BT>() * small_stage<kMode, BT>() + sizeof(SmallCtrl<kMode, BT>);
+}
+
+__device__ __forceinline__ float4 ld_cluster16(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 plus(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
+// Two panels of 128 columns a stage: two neighbouring blocks (SwiGLU: gate and up rows of one), each with accumulators and four
+// fold warps of its own.  TMEM lanes are the output's columns, its columns the rows.
+template <int kMode, int BT>
+__global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
+    fp8_small_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_cols,
+                     const __grid_constant__ Fp8Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    launch_next();
+    using Ctrl = SmallCtrl<kMode, BT>;
+    constexpr int kStages = small_stages<BT>(), kBufs = small_bufs<BT>();
+    constexpr uint32_t kStage = small_stage<kMode, BT>(), kRows = BT * 128;
+    constexpr uint32_t kTmem = 2 * kBufs * BT;
+    constexpr bool kGlu = kMode == kSwiglu;
+    const uint32_t raw = smem_u32(smem_raw), base = align1024(raw);
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem_raw + (base - raw) + kStages * kStage);
+    const int warp = threadIdx.x >> 5;
+    const uint32_t lane = threadIdx.x & 31, rank = cluster_ctarank();
+    const int split = p.split, tile = blockIdx.x / split, tr = tile % p.tiles_r, tc = tile / p.tiles_r;
+    const int r0 = tr * BT;
+    const int DB = p.DB, all = kGlu ? DB : (DB + 1) / 2;                   // stages of the whole axis
+    const int s0 = (int)((int64_t)all * rank / split), s1 = (int)((int64_t)all * (rank + 1) / split);   // this CTA's
+    int *err = g_status;
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tm_rows);
+        tma_prefetch_desc(&tm_cols);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&ctrl->full[s]), 1);
+            mbar_init(smem_u32(&ctrl->empty[s]), 1);
+        }
+        for (int j = 0; j < 2; ++j) {
+            for (int b = 0; b < kBufs; ++b) {
+                mbar_init(smem_u32(&ctrl->tfull[j][b]), 1);
+                mbar_init(smem_u32(&ctrl->tempty[j][b]), 4);
+            }
+            mbar_init(smem_u32(&ctrl->sfull[j]), 1);
+            mbar_init(smem_u32(&ctrl->sempty[j]), 8);
+        }
+        ctrl->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&ctrl->tmem_base), kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctrl->tmem_base;
+    volatile int *abort_flag = &ctrl->abort;
+    wait_for_previous();
+
+    if (warp == 0) {
+        const uint64_t pol_w = p.tiles_r > 1 ? policy_evict_normal() : policy_evict_first(), pol_x = policy_evict_last();
+        int it = 0;
+        for (int st = s0; st < s1; ++st, ++it) {
+            const int s = it % kStages, n = kGlu ? 2 : min(2, DB - 2 * st);
+            if (!mbar_wait(smem_u32(&ctrl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, err)) break;
+            if (lane == 0) {
+                const uint32_t full = smem_u32(&ctrl->full[s]), dst = base + s * kStage;
+                mbar_arrive_expect_tx(full, (uint32_t)n * kPanel + (kGlu ? 1 : n) * kRows);
+                for (int j = 0; j < n; ++j) {
+                    const int d = (kGlu ? st : 2 * st + j) * 128, c0 = tc * 128 + (kGlu ? j * p.C : 0);
+                    tma_load_2d(dst + j * kPanel, &tm_cols, cols_mn(kMode) ? c0 : d, cols_mn(kMode) ? d : c0, full, pol_w);
+                    if (!kGlu || j == 0)
+                        tma_load_2d(dst + 2 * kPanel + j * kRows, &tm_rows, rows_mn(kMode) ? r0 : d, rows_mn(kMode) ? d : r0, full,
+                                    pol_x);
+                }
+            }
+            __syncwarp();
+        }
+        for (int i = max(0, it - kStages); i < it; ++i) drain_wait(smem_u32(&ctrl->full[i % kStages]), (i / kStages) & 1, err);
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(128, BT) | idesc_major(cols_mn(kMode), rows_mn(kMode));
+        int it = 0;
+        bool ok = true;
+        for (int st = s0; ok && st < s1; ++st, ++it) {
+            const int s = it % kStages, b = it % kBufs, n = kGlu ? 2 : min(2, DB - 2 * st);
+            if (!mbar_wait(smem_u32(&ctrl->full[s]), (it / kStages) & 1, abort_flag, err)) break;
+            for (int j = 0; j < n; ++j) {
+                if (!mbar_wait(smem_u32(&ctrl->tempty[j][b]), ((it / kBufs) & 1) ^ 1, abort_flag, err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t a = operand_desc<cols_mn(kMode)>(base + s * kStage + j * kPanel);
+                    const uint64_t x = operand_desc<rows_mn(kMode)>(base + s * kStage + 2 * kPanel + (kGlu ? 0 : j) * kRows);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_e4m3(tmem + (j * kBufs + b) * BT, a + kk * operand_step<cols_mn(kMode)>(),
+                                  x + kk * operand_step<rows_mn(kMode)>(), idesc, kk > 0);
+                    umma_commit(smem_u32(&ctrl->tfull[j][b]));
+                }
+                __syncwarp();
+            }
+            if (ok && lane == 0) umma_commit(smem_u32(&ctrl->empty[s]));
+            __syncwarp();
+        }
+        if (it > 0) drain_wait(smem_u32(&ctrl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1, err);
+    } else if (warp == 2) {
+        // the product of both scales for each row of each panel (weight's: the row's, and the column's apart)
+        for (int st = s0, ch = 0; st < s1; st += kChunk / 2, ++ch) {
+            const int slot = ch & 1;
+            if (!mbar_wait(smem_u32(&ctrl->sempty[slot]), ((ch >> 1) & 1) ^ 1, abort_flag, err)) break;
+            float *sc = ctrl->sc[slot];
+            if (kMode == kWeight) {
+                for (int j = 0; j < kChunk && 2 * st + j < DB; ++j) {
+                    const int64_t b = 2 * st + j;
+#pragma unroll
+                    for (int i = 0; i < BT / 32; ++i) {
+                        const int r = r0 + (int)lane + 32 * i;
+                        sc[j * (BT + 4) + lane + 32 * i] = r < p.R ? p.row_sf[b * p.rs_blk + r] : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = tc * 128 + (int)lane + 32 * i;
+                        ctrl->lane_sc[slot][j * 128 + lane + 32 * i] = c < p.C ? p.col_sf[b * p.cs_blk + c] : 0.0f;
+                    }
+                }
+            } else {
+                constexpr int kBlocks = kGlu ? kChunk / 2 : kChunk, kEach = 32 / kBlocks;   // blocks of a chunk, rows of a load
+                const int j = lane % kBlocks, b = (kGlu ? st : 2 * st) + j, sub = lane / kBlocks;
+                float g = 0.0f, u = 0.0f;
+                if (b < DB) {
+                    g = p.col_sf[tc * p.cs_col + b * p.cs_blk];
+                    if (kGlu) u = p.col_sf[(tc + p.C / 128) * p.cs_col + b * p.cs_blk];
+                }
+#pragma unroll 8
+                for (int i = 0; i < BT / kEach; ++i) {
+                    const int r = r0 + sub + kEach * i;
+                    const float v = b < DB && r < p.R ? p.row_sf[(int64_t)r * p.rs_row + b] : 0.0f;
+                    sc[(kGlu ? 2 * j : j) * (BT + 4) + sub + kEach * i] = v * g;
+                    if (kGlu) sc[(2 * j + 1) * (BT + 4) + sub + kEach * i] = v * u;
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctrl->sfull[slot]));
+        }
+    } else {
+        const int set = (warp - kSmallFold0) >> 2, q = warp & 3;
+        const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + set * kBufs * BT;
+        constexpr int kStep = BT < 32 ? BT : 32;
+        float acc[BT];
+#pragma unroll
+        for (int i = 0; i < BT; ++i) acc[i] = 0.0f;
+        bool ok = true;
+        for (int it = 0, st = s0; ok && st < s1; ++st, ++it) {
+            const int slot = (it >> 2) & 1, b = it % kBufs;
+            if ((it & 3) == 0 && !mbar_wait(smem_u32(&ctrl->sfull[slot]), (it >> 3) & 1, abort_flag, err)) break;
+            if (kGlu || 2 * st + set < DB) {
+                const int j = 2 * (it & 3) + set;
+                const float *sc = ctrl->sc[slot] + j * (BT + 4);
+                const float mine = kMode == kWeight ? ctrl->lane_sc[slot][j * 128 + q * 32 + lane] : 1.0f;
+                if (!mbar_wait(smem_u32(&ctrl->tfull[set][b]), (it / kBufs) & 1, abort_flag, err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < BT; c += kStep) {
+                    float v[kStep];
+                    if constexpr (kStep == 32) tmem_ld32(t + b * BT + c, v);
+                    else tmem_ld16(t + b * BT + c, v);
+                    tmem_ld_wait();
+                    if (c + kStep == BT) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&ctrl->tempty[set][b]));
+                    }
+#pragma unroll
+                    for (int i = 0; i < kStep; i += 4) {
+                        float4 s = *reinterpret_cast<const float4 *>(sc + c + i);
+                        if (kMode == kWeight) s.x *= mine, s.y *= mine, s.z *= mine, s.w *= mine;
+                        acc[c + i] = fmaf(v[i], s.x, acc[c + i]);
+                        acc[c + i + 1] = fmaf(v[i + 1], s.y, acc[c + i + 1]);
+                        acc[c + i + 2] = fmaf(v[i + 2], s.z, acc[c + i + 2]);
+                        acc[c + i + 3] = fmaf(v[i + 3], s.w, acc[c + i + 3]);
+                    }
+                }
+            }
+            if ((it & 3) == 3) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctrl->sempty[slot]));
+            }
+        }
+        // every MMA of the CTA is done (both sets have seen theirs): the stages' memory takes the partial sums [set][row][128]
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        float *part = reinterpret_cast<float *>(smem_raw + (base - raw)) + (size_t)set * BT * 128 + q * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < BT; ++i) part[i * 128] = acc[i];
+    }
+    __syncwarp();
+    cluster_sync();
+    if (warp >= kSmallFold0) {
+        // join the cluster's partial sums, in rank order: a warp takes a row of the tile, a lane four columns
+        const int col = tc * 128 + 4 * (int)lane;
+        for (int i = (warp - kSmallFold0) * split + (int)rank; i < BT; i += 8 * split) {
+            const int64_t row = (int64_t)r0 + i;
+            if (row >= p.R) break;
+            const uint32_t at = base + (uint32_t)((i * 128 + 4 * lane) * 4);
+            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = a;
+#pragma unroll 8
+            for (int r = 0; r < split; ++r) {
+                const uint32_t from = mapa_shared(at, r);
+                a = plus(a, ld_cluster16(from));
+                u = plus(u, ld_cluster16(from + BT * 512));
+            }
+            if (kGlu) {
+                a.x = swiglu_of(a.x, u.x, p.clamp), a.y = swiglu_of(a.y, u.y, p.clamp);
+                a.z = swiglu_of(a.z, u.z, p.clamp), a.w = swiglu_of(a.w, u.w, p.clamp);
+                if (p.sf) {
+                    float amax = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w)));
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+                    const GroupScale g = group_scale(amax);
+                    *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.out) + row * p.ld_out + col) =
+                        g.codes(a.x, a.y) | g.codes(a.z, a.w) << 16;
+                    if (lane == 0) p.sf[row * (p.C / 128) + tc] = g.sf;
+                    continue;
+                }
+            } else {
+                a = plus(a, u);
+            }
+            if (col >= p.C) continue;
+            if (p.f32) {
+                if (p.add) a = plus(a, *reinterpret_cast<const float4 *>(static_cast<const float *>(p.add) + row * p.ld_add + col));
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * p.ld_out + col) = a;
+            } else {
+                if (p.add) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const bf16 *>(p.add) + row * p.ld_add + col);
+                    a = plus(a, make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)));
+                }
+                *reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + row * p.ld_out + col) =
+                    make_uint2(bf16x2(a.x, a.y), bf16x2(a.z, a.w));
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();   // no CTA leaves while another reads its partial sums
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmem);
+    }
+}
+
+// ---- host ------------------------------------------------------------------
+constexpr int kMaxFeatures = 1 << 20;
+
+int up_to(int64_t n, int m) { return (int)((n + m - 1) / m); }
+
+bool valid(const moe_fp8_linear_config *c) {
+    if (!c || c->in_features < 16 || c->in_features % 16 || c->in_features > kMaxFeatures) return false;
+    if (c->out_features < 16 || c->out_features % 16 || c->out_features > kMaxFeatures) return false;
+    if (c->act != MOE_ACT_NONE && c->act != MOE_ACT_SWIGLU) return false;
+    if (c->act == MOE_ACT_SWIGLU && c->out_features % 256) return false;
+    if (c->quant != MOE_QUANT_NONE && (c->quant != MOE_QUANT_FP8_128 || c->act != MOE_ACT_SWIGLU)) return false;
+    return valid_dtype(c->out_dtype) && c->act_clamp > 0.0f;
+}
+
+// Rows of a 16-byte aligned matrix, with a pitch that keeps them so.
+bool rows_ok(const void *p, int64_t ld, int64_t cols, size_t es) {
+    return p && aligned_to(p, 16) && ld >= cols && ld * (int64_t)es % 16 == 0;
+}
+
+int this_device() {
+    int d = -1;
+    return cudaGetDevice(&d) == cudaSuccess && d >= 0 && d < 32 ? d : -1;
+}
+int sm_count(int dev) {
+    static std::atomic<int> known[32];
+    int n = known[dev].load(std::memory_order_acquire);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        known[dev].store(n, std::memory_order_release);
+    }
+    return n;
+}
+
+template <int kMode>
+cudaError_t launch_wide(const CUtensorMap &rows, const CUtensorMap &cols, const Fp8Params &p, int dev, cudaStream_t s) {
+    static std::atomic<int> resident[32];   // CTA pairs that the device holds at once
+    static std::atomic<uint32_t> smem_set{0};
+    cudaError_t e = smem_limit_once(reinterpret_cast<const void *>(fp8_wide_kernel<kMode>), wide_smem<kMode>(), smem_set);
+    if (e != cudaSuccess) return e;
+    int pairs = resident[dev].load(std::memory_order_acquire);
+    if (!pairs) {
+        cudaLaunchConfig_t c = {};
+        cudaLaunchAttribute a[1];
+        a[0].id = cudaLaunchAttributeClusterDimension;
+        a[0].val.clusterDim.x = 2, a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+        c.gridDim = dim3(sm_count(dev) & ~1);
+        c.blockDim = dim3(kWideThreads);
+        c.dynamicSmemBytes = wide_smem<kMode>();
+        c.attrs = a, c.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&pairs, fp8_wide_kernel<kMode>, &c);
+        if (e != cudaSuccess) return e;
+        if (pairs < 1) return cudaErrorLaunchOutOfResources;
+        resident[dev].store(pairs, std::memory_order_release);
+    }
+    const int64_t tiles = (int64_t)p.tiles_r * p.tiles_c;
+    return launch(fp8_wide_kernel<kMode>, 2u * (unsigned)std::min<int64_t>(pairs, tiles), kWideThreads, wide_smem<kMode>(), 2, s,
+                  rows, cols, p);
+}
+
+template <int kMode, int BT>
+cudaError_t launch_small(const CUtensorMap &rows, const CUtensorMap &cols, const Fp8Params &p, cudaStream_t s) {
+    static std::atomic<uint32_t> smem_set{0};
+    cudaError_t e = smem_limit_once(reinterpret_cast<const void *>(fp8_small_kernel<kMode, BT>), small_smem<kMode, BT>(), smem_set);
+    if (e != cudaSuccess) return e;
+    return launch(fp8_small_kernel<kMode, BT>, (unsigned)(p.tiles_r * p.tiles_c * p.split), kSmallThreads, small_smem<kMode, BT>(),
+                  p.split, s, rows, cols, p);
+}
+
+// rows [R x D] and cols [C' x D] codes; *_ld: pitch of the matrix as stored.
+template <int kMode>
+int run(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_cols, int64_t D, Fp8Params p, cudaStream_t s) {
+    const int dev = this_device();
+    const int sms = dev < 0 ? 0 : sm_count(dev);
+    if (!sms) return MOE_ERR_CUDA;
+    p.DB = up_to(D, 128);
+    const int wt = kMode == kSwiglu ? 2 * p.C : p.C;   // rows of W
+    p.tiles_r = up_to(p.R, 256);
+    p.tiles_c = up_to(p.C, kMode == kSwiglu ? 128 : 256);
+    int bt = 0;
+    if (p.R <= 16 && kMode != kWeight) bt = 16;
+    else if (p.R <= 32 && kMode != kWeight) bt = 32;
+    else if (p.R <= 64 && kMode != kWeight) bt = 64;
+    else if ((int64_t)p.tiles_r * p.tiles_c < sms / 4) bt = 128;
+    CUtensorMap mr, mc;
+    const uint32_t box = bt ? bt : 128;
+    if (!(rows_mn(kMode) ? encode_map(&mr, rows, p.R, D, ld_rows, 128, 128) : encode_map(&mr, rows, D, p.R, ld_rows, 128, box)) ||
+        !(cols_mn(kMode) ? encode_map(&mc, cols, wt, D, ld_cols, 128, 128) : encode_map(&mc, cols, D, wt, ld_cols, 128, 128)))
+        return MOE_ERR_CUDA;
+    cudaError_t e;
+    if (!bt) {
+        e = launch_wide<kMode>(mr, mc, p, dev, s);
+    } else {
+        p.tiles_r = up_to(p.R, bt);
+        p.tiles_c = up_to(p.C, 128);
+        const int stages = kMode == kSwiglu ? p.DB : (p.DB + 1) / 2;
+        const int64_t room = (int64_t)sms * (bt == 16 ? 2 : 1) / ((int64_t)p.tiles_r * p.tiles_c);
+        p.split = (int)std::max<int64_t>(1, std::min<int64_t>({room, 8, std::max(1, stages / 2)}));
+        if constexpr (kMode == kWeight)
+            e = launch_small<kMode, 128>(mr, mc, p, s);
+        else
+            e = bt == 16   ? launch_small<kMode, 16>(mr, mc, p, s)
+                : bt == 32 ? launch_small<kMode, 32>(mr, mc, p, s)
+                : bt == 64 ? launch_small<kMode, 64>(mr, mc, p, s)
+                           : launch_small<kMode, 128>(mr, mc, p, s);
+    }
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+bool wide_pieces(const Fp8Params &p) {
+    const int es = p.f32 ? 4 : 2;
+    return aligned_to(p.out, 32) && p.ld_out * es % 32 == 0 && (!p.add || (aligned_to(p.add, 32) && p.ld_add * es % 32 == 0));
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_fp8_linear_forward(const moe_fp8_linear_config *cfg, int num_tokens, const void *x, int64_t ld_x, const float *x_sf,
+                           const void *w, const float *w_sf, const void *add, int64_t ld_add, void *y, int64_t ld_y, float *y_sf,
+                           void *stream) {
+    if (!valid(cfg) || num_tokens < 0) return MOE_ERR_INVALID_ARG;
+    const bool glu = cfg->act == MOE_ACT_SWIGLU, quant = cfg->quant != MOE_QUANT_NONE;
+    if (quant ? !y_sf || add : y_sf != nullptr) return MOE_ERR_INVALID_ARG;
+    if (num_tokens == 0) return MOE_OK;
+    const int64_t K = cfg->in_features, N = cfg->out_features, n = glu ? N / 2 : N;
+    const size_t es = quant ? 1 : dtype_bytes(cfg->out_dtype);
+    if (!rows_ok(x, ld_x, K, 1) || !rows_ok(w, K, K, 1) || !rows_ok(y, ld_y, n, es) || (add && !rows_ok(add, ld_add, n, es)))
+        return MOE_ERR_INVALID_ARG;
+    if (!x_sf || !w_sf || !aligned_to(x_sf, 4) || !aligned_to(w_sf, 4) || !aligned_to(y_sf, 4)) return MOE_ERR_INVALID_ARG;
+    Fp8Params p{};
+    p.row_sf = x_sf, p.col_sf = w_sf;
+    p.rs_row = p.cs_col = up_to(K, 128);
+    p.rs_blk = p.cs_blk = 1;
+    p.add = add, p.ld_add = ld_add, p.out = y, p.ld_out = ld_y, p.sf = y_sf;
+    p.R = num_tokens, p.C = (int)n, p.f32 = cfg->out_dtype == MOE_DTYPE_F32, p.clamp = cfg->act_clamp;
+    p.wide = wide_pieces(p);
+    const uint8_t *a = static_cast<const uint8_t *>(x), *b = static_cast<const uint8_t *>(w);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return glu ? run<kSwiglu>(a, ld_x, b, K, K, p, s) : run<kForward>(a, ld_x, b, K, K, p, s);
+}
+
+int moe_fp8_linear_backward_input(const moe_fp8_linear_config *cfg, int num_tokens, const void *dy, int64_t ld_dy,
+                                  const float *dy_sf, const void *w, const float *w_sf, const void *add, int64_t ld_add, void *dx,
+                                  int64_t ld_dx, void *stream) {
+    if (!valid(cfg) || num_tokens < 0) return MOE_ERR_INVALID_ARG;
+    if (num_tokens == 0) return MOE_OK;
+    const int64_t K = cfg->in_features, N = cfg->out_features;
+    const size_t es = dtype_bytes(cfg->out_dtype);
+    if (!rows_ok(dy, ld_dy, N, 1) || !rows_ok(w, K, K, 1) || !rows_ok(dx, ld_dx, K, es) || (add && !rows_ok(add, ld_add, K, es)))
+        return MOE_ERR_INVALID_ARG;
+    if (!dy_sf || !w_sf || !aligned_to(dy_sf, 4) || !aligned_to(w_sf, 4)) return MOE_ERR_INVALID_ARG;
+    Fp8Params p{};
+    p.row_sf = dy_sf, p.col_sf = w_sf;
+    p.rs_row = up_to(N, 128), p.rs_blk = 1;
+    p.cs_col = 1, p.cs_blk = up_to(K, 128);
+    p.add = add, p.ld_add = ld_add, p.out = dx, p.ld_out = ld_dx;
+    p.R = num_tokens, p.C = (int)K, p.f32 = cfg->out_dtype == MOE_DTYPE_F32;
+    p.wide = wide_pieces(p);
+    return run<kInput>(static_cast<const uint8_t *>(dy), ld_dy, static_cast<const uint8_t *>(w), K, N, p,
+                       static_cast<cudaStream_t>(stream));
+}
+
+int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int num_tokens, const void *dy, int64_t ld_dy,
+                                   const float *dy_sf, const void *x, int64_t ld_x, const float *x_sf, const float *add,
+                                   int64_t ld_add, float *dw, int64_t ld_dw, void *stream) {
+    if (!valid(cfg) || num_tokens < 0) return MOE_ERR_INVALID_ARG;
+    const int64_t K = cfg->in_features, N = cfg->out_features;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!rows_ok(dw, ld_dw, K, 4) || (add && !rows_ok(add, ld_add, K, 4))) return MOE_ERR_INVALID_ARG;
+    if (num_tokens == 0) {   // nothing is summed
+        const cudaError_t e = !add       ? cudaMemset2DAsync(dw, ld_dw * 4, 0, K * 4, N, s)
+                              : add != dw ? cudaMemcpy2DAsync(dw, ld_dw * 4, add, ld_add * 4, K * 4, N, cudaMemcpyDeviceToDevice, s)
+                                          : cudaSuccess;
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    if (!rows_ok(dy, ld_dy, N, 1) || !rows_ok(x, ld_x, K, 1)) return MOE_ERR_INVALID_ARG;
+    if (!dy_sf || !x_sf || !aligned_to(dy_sf, 4) || !aligned_to(x_sf, 4)) return MOE_ERR_INVALID_ARG;
+    Fp8Params p{};
+    p.row_sf = dy_sf, p.col_sf = x_sf;
+    p.rs_row = p.cs_col = 1;
+    p.rs_blk = N, p.cs_blk = K;
+    p.add = add, p.ld_add = ld_add, p.out = dw, p.ld_out = ld_dw;
+    p.R = (int)N, p.C = (int)K, p.f32 = 1;
+    p.wide = wide_pieces(p);
+    return run<kWeight>(static_cast<const uint8_t *>(dy), ld_dy, static_cast<const uint8_t *>(x), ld_x, num_tokens, p, s);
+}
+
+int moe_fp8_linear_status(void) {
+    int w[kErrWords] = {};
+    if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpyFromSymbol(w, g_status, sizeof w) != cudaSuccess) return MOE_ERR_CUDA;
+    if (!w[0]) return MOE_OK;
+    const int zero[kErrWords] = {};
+    if (cudaMemcpyToSymbol(g_status, zero, sizeof zero) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_ERR_DEVICE_TIMEOUT;
+}
+
+}  // extern "C"

@@ -23,6 +23,10 @@ inline cudaError_t smem_limit_once(const void *func, size_t bytes, std::atomic<u
     return e;
 }
 
+// Tensor map of a 2-D byte matrix [outer, inner] with row pitch `stride`, boxes of box_inner x box_outer bytes, 128-byte swizzle.
+bool encode_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
+                uint32_t box_outer);
+
 constexpr int kBM = 128;   // pool rows (routed pairs) per M block
 constexpr int kBK = 128;   // K bytes per pipeline stage (one scale block)
 constexpr int kNMajorMinRows = 256;  // experts with at least this many pairs walk N-major

@@ -190,4 +190,18 @@ __device__ __forceinline__ int ue8m0_code(float amax) {
 // 2^-e of that code.
 __device__ __forceinline__ float ue8m0_inverse(int code) { return __uint_as_float((uint32_t)(254 - code) << 23); }
 
+// Scale of a group of E4M3 codes as the layer's requantisation has it: sf = amax / 448, codes of v times the rounded 1 / sf.
+// Where amax is below 2^-100 (1 / sf would pass the f32 range at its end) v is brought up by 2^64 first.  An all-zero group has
+// sf 0 and codes 0, one with an infinity sf infinity.
+struct GroupScale {
+    float sf, inv, up;
+    __device__ __forceinline__ uint32_t codes(float a, float b) const { return e4m3x2(a * up * inv, b * up * inv); }
+};
+__device__ __forceinline__ GroupScale group_scale(float amax) {
+    GroupScale g{amax / 448.0f, 0.0f, 1.0f};
+    if (amax > 0.0f && amax < 0x1p-100f) g.up = 0x1p64f;
+    g.inv = amax > 0.0f ? __frcp_rn(g.sf * g.up) : 1.0f;
+    return g;
+}
+
 }  // namespace moe
