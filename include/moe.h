@@ -493,6 +493,47 @@ MOE_API int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int
  * undefined then), else MOE_OK. */
 MOE_API int moe_fp8_linear_status(void);
 
+/* ---- FP8 quantiser ---- */
+
+/* Codes and scales of a matrix in the forms that the FP8 linear takes, in one
+ * pass: scales sf per 128 columns of a row (the last ones may be fewer), with
+ * codes of their own; and col_sf per 128 rows of a column, with theirs.
+ * sf = amax / 448 of the group, a code is the E4M3 of the value times the
+ * rounded 1 / sf.  An all-zero group has scale 0 and codes 0; a NaN takes no
+ * part in its group's scale and is a NaN's code; an infinity makes its
+ * group's scale infinity and its values NaN. */
+typedef struct {
+    int columns;       /* H, a multiple of 16, 16..2^20; of 128 with MOE_ACT_SWIGLU */
+    int act;           /* moe_act: what is quantised is v, or silu(g) * u of v [T, 2H], g its columns [0, H), u [H, 2H) */
+    int dtype;         /* moe_dtype of v and d */
+    float act_clamp;   /* symmetric clamp of g and u before SWIGLU; +INFINITY = off; a NaN stays one */
+} moe_fp8_quant_config;
+
+/* W = H, in the backward pass 2H.  Codes are 16-byte aligned and contiguous,
+ * col_sf is 16-byte aligned; codes and sf, or col_codes and col_sf, may be
+ * NULL. */
+typedef struct {
+    uint8_t *codes;      /* [T, W] */
+    float *sf;           /* [T, ceil(W/128)] */
+    uint8_t *col_codes;  /* [T, W] */
+    float *col_sf;       /* [ceil(T/128), W] */
+} moe_fp8_quant_io;
+
+/* v [T, H], with SWIGLU [T, 2H]: 16-byte aligned rows. */
+MOE_API int moe_fp8_quant(const moe_fp8_quant_config *cfg, int num_tokens, const void *v, int64_t ld_v,
+                          const moe_fp8_quant_io *out, void *stream);
+
+/* SWIGLU's gradient, quantised: from d [T, H], the gradient of silu(g) * u,
+ * and v [T, 2H], with s = sigmoid(g): dg = d u s (1 + g (1 - s)) in columns
+ * [0, H), du = d g s in [H, 2H); 0 for a g or u beyond the clamp. */
+MOE_API int moe_fp8_quant_backward(const moe_fp8_quant_config *cfg, int num_tokens, const void *d, int64_t ld_d, const void *v,
+                                   int64_t ld_v, const moe_fp8_quant_io *out, void *stream);
+
+/* Weights w [N, H]: codes u8 [N, H], sf f32 [ceil(N/128), ceil(H/128)] of
+ * each 128 x 128 (act MOE_ACT_NONE). */
+MOE_API int moe_fp8_quant_weights(const moe_fp8_quant_config *cfg, int num_rows, const void *w, int64_t ld_w, uint8_t *codes,
+                                  float *sf, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -39,6 +39,7 @@ ABI_SYMBOLS = (
     "moe_router_workspace_bytes", "moe_router_forward", "moe_balance_loss", "moe_router_backward",
     "moe_fp4_linear_weight_bytes", "moe_fp4_linear_transform_weights", "moe_fp4_linear_forward",
     "moe_fp8_linear_forward", "moe_fp8_linear_backward_input", "moe_fp8_linear_backward_weight", "moe_fp8_linear_status",
+    "moe_fp8_quant", "moe_fp8_quant_backward", "moe_fp8_quant_weights",
 )
 
 
@@ -82,6 +83,9 @@ Fp4LinearConfig = _struct("Fp4LinearConfig", _ints("in_features", "out_features"
                           _floats("act_clamp"))
 Fp8LinearConfig = _struct("Fp8LinearConfig", _ints("in_features", "out_features", "act", "quant", "out_dtype"),
                           _floats("act_clamp"))
+
+Fp8QuantConfig = _struct("Fp8QuantConfig", _ints("columns", "act", "dtype"), _floats("act_clamp"))
+Fp8QuantIO = _struct("Fp8QuantIO", _ptrs("codes", "sf", "col_codes", "col_sf"))
 
 
 class MoEError(RuntimeError):
@@ -135,7 +139,7 @@ def lib():
             L.moe_destroy.argtypes = [vp]
             i64, ncfg, rcfg, fcfg, bio = (ctypes.c_int64, ctypes.POINTER(NormConfig), ctypes.POINTER(RouterConfig),
                                           ctypes.POINTER(Fp4LinearConfig), ctypes.POINTER(BalanceIO))
-            ecfg = ctypes.POINTER(Fp8LinearConfig)
+            ecfg, qcfg, qio = (ctypes.POINTER(Fp8LinearConfig), ctypes.POINTER(Fp8QuantConfig), ctypes.POINTER(Fp8QuantIO))
             for name, res, args in (
                     ("moe_norm_forward", i32, [ncfg, i32, ctypes.POINTER(NormIO), vp]),
                     ("moe_norm_workspace_bytes", sz, [ncfg, i32]),
@@ -150,7 +154,10 @@ def lib():
                     ("moe_fp8_linear_forward", i32, [ecfg, i32, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp]),
                     ("moe_fp8_linear_backward_input", i32, [ecfg, i32, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp]),
                     ("moe_fp8_linear_backward_weight", i32, [ecfg, i32, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp]),
-                    ("moe_fp8_linear_status", i32, [])):
+                    ("moe_fp8_linear_status", i32, []),
+                    ("moe_fp8_quant", i32, [qcfg, i32, vp, i64, qio, vp]),
+                    ("moe_fp8_quant_backward", i32, [qcfg, i32, vp, i64, vp, i64, qio, vp]),
+                    ("moe_fp8_quant_weights", i32, [qcfg, i32, vp, i64, vp, vp, vp])):
                 fn = getattr(L, name)
                 fn.restype, fn.argtypes = res, args
             _lib = L
@@ -326,5 +333,5 @@ class MoELayer:
             pass
 
 
-from .block import (FP4_LINEAR_MAX_TOKENS, BlockNorm, Fp4Linear, Fp8Codes, Fp8Linear, NormGrads, NormOutput, Router,  # noqa: E402,F401
-                    RouterOutput)
+from .block import (FP4_LINEAR_MAX_TOKENS, BlockNorm, Fp4Linear, Fp8Codes, Fp8Linear, Fp8Quant, NormGrads,  # noqa: E402,F401
+                    NormOutput, Router, RouterOutput)

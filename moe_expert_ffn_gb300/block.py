@@ -19,7 +19,8 @@ import math
 
 import torch
 
-from . import MOE_ERR_INVALID_ARG, Fp4LinearConfig, Fp8LinearConfig, MoEError, NormConfig, RouterConfig, _check, lib
+from . import (MOE_ERR_INVALID_ARG, Fp4LinearConfig, Fp8LinearConfig, Fp8QuantConfig, Fp8QuantIO, MoEError, NormConfig, RouterConfig,
+               _check, lib)
 
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 GATES = {None: 0, "channel": 1, "token": 2}
@@ -382,4 +383,66 @@ class Fp8Linear:
         rc = self._dw(self._dw_at, self._cfg, self._dev, _stream(stream, self._dev), dy, dy_sf, x, x_sf, add, out)
         if rc:
             _check(rc, "moe_fp8_linear_backward_weight")
+        return out
+
+
+class Fp8Quant:
+    """Codes and scales of a matrix in the forms that Fp8Linear takes, in one pass: per 128 columns of a row (``rows``: the
+    forward product's and the input's gradient's), per 128 rows of a column (``cols``: the weight's gradient's).  act "swiglu":
+    of silu(g) * u, g and u the halves of v [T, 2 columns], and with backward() of its gradient."""
+
+    def __init__(self, columns, act=None, dtype=torch.bfloat16, act_clamp=math.inf, device=None):
+        self.columns, self.act, self.dtype, self.device = int(columns), act, dtype, _device(device)
+        self.cfg = Fp8QuantConfig(int(columns), _choice(ACTS, act, "act"), _choice(DTYPES, dtype, "dtype"), float(act_clamp))
+        L, b = lib(), _bind()
+        # a call without rows checks the config alone
+        if L.moe_fp8_quant(self.cfg, 0, None, 0, Fp8QuantIO(codes=16, sf=16), None):
+            raise MoEError(MOE_ERR_INVALID_ARG, "fp8 quantiser config")
+        self._cfg, self._dev = ctypes.addressof(self.cfg), _index(self.device)
+        self._fwd, self._bwd, self._wts = b.fp8_quant, b.fp8_quant_backward, b.fp8_quant_weights
+        self._fwd_at, self._bwd_at, self._wts_at = (_address(L.moe_fp8_quant), _address(L.moe_fp8_quant_backward),
+                                                    _address(L.moe_fp8_quant_weights))
+
+    def buffers(self, num_tokens, rows=True, cols=False, grad=False) -> Fp8Codes:
+        """Outputs for `num_tokens`: with scales along `rows`, along `cols`; `grad`: of backward (two times the columns)."""
+        T, W, dev = num_tokens, self.columns * (2 if grad else 1), self.device
+        o = Fp8Codes()
+        o.codes = torch.empty(T, W, dtype=torch.uint8, device=dev) if rows else None
+        o.sf = torch.empty(T, _blocks(W), dtype=torch.float32, device=dev) if rows else None
+        o.col_codes = torch.empty(T, W, dtype=torch.uint8, device=dev) if cols else None
+        o.col_sf = torch.empty(_blocks(T), W, dtype=torch.float32, device=dev) if cols else None
+        return o
+
+    def weight_buffers(self, num_rows) -> Fp8Codes:
+        o = Fp8Codes()
+        o.codes = torch.empty(num_rows, self.columns, dtype=torch.uint8, device=self.device)
+        o.sf = torch.empty(_blocks(num_rows), _blocks(self.columns), dtype=torch.float32, device=self.device)
+        o.col_codes = o.col_sf = None
+        return o
+
+    def forward(self, v, rows=True, cols=False, out=None, stream=None) -> Fp8Codes:
+        """Of v [T, columns] (swiglu: [T, 2 columns]); what `out` holds goes before `rows` and `cols`."""
+        if out is None:
+            out = _made(stream, self.buffers, v.shape[0], rows, cols)
+        rc = self._fwd(self._fwd_at, self._cfg, self._dev, _stream(stream, self._dev), v, out.codes, out.sf, out.col_codes, out.col_sf)
+        if rc:
+            _check(rc, "moe_fp8_quant")
+        return out
+
+    def backward(self, d, v, rows=True, cols=True, out=None, stream=None) -> Fp8Codes:
+        """The gradient of v [T, 2 columns] from d [T, columns], that of silu(g) * u."""
+        if out is None:
+            out = _made(stream, self.buffers, v.shape[0], rows, cols, True)
+        rc = self._bwd(self._bwd_at, self._cfg, self._dev, _stream(stream, self._dev), d, v, out.codes, out.sf, out.col_codes, out.col_sf)
+        if rc:
+            _check(rc, "moe_fp8_quant_backward")
+        return out
+
+    def weights(self, w, out=None, stream=None) -> Fp8Codes:
+        """Of weights w [N, columns], a scale for each 128 x 128."""
+        if out is None:
+            out = _made(stream, self.weight_buffers, w.shape[0])
+        rc = self._wts(self._wts_at, self._cfg, self._dev, _stream(stream, self._dev), w, out.codes, out.sf)
+        if rc:
+            _check(rc, "moe_fp8_quant_weights")
         return out

@@ -439,6 +439,65 @@ int fp8_backward_weight(Args &a) {
     return unlocked(a, [&] { return c.fn(c.cfg, T, dp, ldd, ds, xp, ldx, xs, ap, lda, wp, ldw, c.stream); });
 }
 
+// The forms of output of a matrix [T, W]; codes, sf, col_codes, col_sf
+void fp8_codes(Args &a, int T, int64_t W, moe_fp8_quant_io &io) {
+    const at::Tensor *codes = a.tensor("codes"), *sf = a.tensor("sf"), *col_codes = a.tensor("col_codes"), *col_sf = a.tensor("col_sf");
+    a.flat(codes, "codes", at::kByte, T, W, io.codes, true);
+    a.flat(sf, "sf", at::kFloat, T, blocks(W), io.sf, true);
+    a.flat(col_codes, "col_codes", at::kByte, T, W, io.col_codes, true);
+    a.flat(col_sf, "col_sf", at::kFloat, blocks(T), W, io.col_sf, true);
+}
+
+// ..., v, codes, sf, col_codes, col_sf
+int fp8_quant(Args &a) {
+    const Head<decltype(&moe_fp8_quant), moe_fp8_quant_config> c(a);
+    const at::Tensor *v = a.tensor("v");
+    const int T = tokens(v, "v");
+    const int64_t H = c.cfg->columns;
+    const void *p;
+    int64_t ld;
+    moe_fp8_quant_io io{};
+    a.rows(v, "v", type_of(c.cfg->dtype), T, c.cfg->act == MOE_ACT_SWIGLU ? 2 * H : H, p, ld, false);
+    fp8_codes(a, T, H, io);
+    a.done();
+    a.tell_of_graph("Fp8Quant.forward");
+    return unlocked(a, [&] { return c.fn(c.cfg, T, p, ld, &io, c.stream); });
+}
+
+// ..., d, v, codes, sf, col_codes, col_sf
+int fp8_quant_backward(Args &a) {
+    const Head<decltype(&moe_fp8_quant_backward), moe_fp8_quant_config> c(a);
+    const at::Tensor *d = a.tensor("d"), *v = a.tensor("v");
+    const int T = tokens(v, "v");
+    const int64_t H = c.cfg->columns;
+    const void *dp, *vp;
+    int64_t ldd, ldv;
+    moe_fp8_quant_io io{};
+    a.rows(needed(d, "d"), "d", type_of(c.cfg->dtype), T, H, dp, ldd, false);
+    a.rows(v, "v", type_of(c.cfg->dtype), T, 2 * H, vp, ldv, false);
+    fp8_codes(a, T, 2 * H, io);
+    a.done();
+    return unlocked(a, [&] { return c.fn(c.cfg, T, dp, ldd, vp, ldv, &io, c.stream); });
+}
+
+// ..., w, codes, sf
+int fp8_quant_weights(Args &a) {
+    const Head<decltype(&moe_fp8_quant_weights), moe_fp8_quant_config> c(a);
+    const at::Tensor *w = a.tensor("w"), *codes = a.tensor("codes"), *sf = a.tensor("sf");
+    a.done();
+    const int N = tokens(w, "w");
+    const int64_t H = c.cfg->columns;
+    const void *p;
+    uint8_t *q;
+    float *s;
+    int64_t ld;
+    a.rows(w, "w", type_of(c.cfg->dtype), N, H, p, ld, false);
+    a.flat(needed(codes, "codes"), "codes", at::kByte, N, H, q, true);
+    a.flat(needed(sf, "sf"), "sf", at::kFloat, blocks(N), blocks(H), s, true);
+    a.tell_of_graph("Fp8Quant.weights");
+    return unlocked(a, [&] { return c.fn(c.cfg, N, p, ld, q, s, c.stream); });
+}
+
 template <int (*F)(Args &)>
 PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<F>)), METH_FASTCALL, nullptr};
@@ -449,7 +508,8 @@ PyMethodDef methods[] = {method<norm_forward>("norm_forward"),         method<no
                          method<router_backward>("router_backward"),   method<linear_transform>("linear_transform"),
                          method<linear_forward>("linear_forward"),     method<fp8_forward>("fp8_forward"),
                          method<fp8_backward_input>("fp8_backward_input"), method<fp8_backward_weight>("fp8_backward_weight"),
-                         {nullptr, nullptr, 0, nullptr}};
+                         method<fp8_quant>("fp8_quant"),               method<fp8_quant_backward>("fp8_quant_backward"),
+                         method<fp8_quant_weights>("fp8_quant_weights"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", "Tensors to the C ABI of the block operators.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
