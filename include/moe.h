@@ -355,6 +355,10 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
  * 0.6, the first by logits, the second by scores. */
 typedef enum { MOE_BIAS_LOGIT = 0, MOE_BIAS_SCORE = 1 } moe_bias;
 
+/* By what groups of experts are ranked: by their largest key, or by the sum
+ * of their two largest (f32; of one open expert's, that alone). */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+
 typedef struct {
     int num_experts;      /* E, 1..1024 */
     int topk;             /* k, 1..min(32, E) */
@@ -365,6 +369,10 @@ typedef struct {
     float balance_coef;   /* alpha of the balance loss, finite */
     float z_coef;         /* beta of the z loss, finite; 0 with MOE_SCORE_SIGMOID */
     int bias_on;          /* moe_bias */
+    int num_groups;       /* 0: the choice is not limited to groups; else 2..32 groups of E / num_groups neighbouring experts,
+                             num_groups * ceil(E / num_groups / 32) <= 32 */
+    int topk_groups;      /* with groups: of how many the experts are, 1..num_groups; k <= topk_groups * E / num_groups */
+    int group_score;      /* moe_group_score */
 } moe_router_config;
 
 /* The choice: the k largest logit + bias, or score + bias (f32 sums, the
@@ -372,8 +380,13 @@ typedef struct {
  * bias the k largest logits.  A logit of -inf or NaN, or a sum that is, closes
  * its expert for the token; a slot with no open expert left gets topk_idx -1
  * and weight 0 (moe_forward's inactive slot).  +inf counts as the largest
- * finite f32.  The bias takes no part in the weights.  Experts are not limited
- * to groups. */
+ * finite f32.  The bias takes no part in the weights.
+ * With groups a token's experts are of its topk_groups best groups (ties to
+ * the lowest group) by these keys, and of no others.  Its scores, where the
+ * bias is on them or would be (bias_on SCORE; a group's sum is of scores then
+ * even without a bias), are the f32 next to the exact sigmoid: the choice is
+ * that of these keys, bit for bit.  Everything else -- weights, losses,
+ * gradient -- is as without groups. */
 
 #define MOE_MAX_SEQS (1 << 20)
 

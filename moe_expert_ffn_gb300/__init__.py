@@ -77,7 +77,7 @@ NormIO = _struct("NormIO", _pitched("residual", "y"), _ptrs("w_post", "gate", "w
 NormGradIO = _struct("NormGradIO", _pitched("h", "y"), _ptrs("w_post", "gate", "w_pre", "rstd_post", "rstd_pre"),
                      _pitched("dh", "dn", "dresidual", "dy"), _ptrs("dw_post", "dgate", "dw_pre"))
 RouterConfig = _struct("RouterConfig", _ints("num_experts", "topk", "score", "renormalize", "logits_dtype"),
-                       _floats("weight_scale", "balance_coef", "z_coef"), _ints("bias_on"))
+                       _floats("weight_scale", "balance_coef", "z_coef"), _ints("bias_on", "num_groups", "topk_groups", "group_score"))
 BalanceIO = _struct("BalanceIO", _ints("num_seqs"), _ptrs("seq_offsets", "loss", "counts", "prob_mean", "seq_tokens"))
 Fp4LinearConfig = _struct("Fp4LinearConfig", _ints("in_features", "out_features", "act", "out_dtype"),
                           _floats("act_clamp"))

@@ -27,6 +27,7 @@ GATES = {None: 0, "channel": 1, "token": 2}
 QUANTS = {None: 0, "fp8": 1, "ue8m0": 2}
 SCORES = {"softmax": 0, "sigmoid": 1}
 BIASES = {"logit": 0, "score": 1}
+GROUP_SCORES = {"max": 0, "top2": 1}
 ACTS = {None: 0, "swiglu": 1}
 FP4_LINEAR_MAX_TOKENS = 16
 
@@ -180,17 +181,21 @@ class RouterOutput:
 class Router:
     """Top-k router: topk_idx and topk_weights for MoELayer.forward from logits, the balance and z losses
     with per-sequence expert counts, and the gradient of the logits.  A bias, which takes part in the choice alone, is
-    added to the logits or (``bias_on`` "score", with sigmoid scores) to the scores.  Losses use a workspace of this
+    added to the logits or (``bias_on`` "score", with sigmoid scores) to the scores.  With ``groups`` of neighbouring experts a
+    token's are chosen of its ``topk_groups`` best groups, ranked by their largest key or (``group_score`` "top2") the sum of
+    their two largest.  Losses use a workspace of this
     object: two loss calls of one Router must not run concurrently."""
 
     def __init__(self, num_experts, topk, score="softmax", renormalize=True, weight_scale=1.0, balance_coef=0.0, z_coef=0.0,
-                 logits_dtype=torch.float32, max_tokens=None, max_seqs=1, device=None, bias_on="logit"):
+                 logits_dtype=torch.float32, max_tokens=None, max_seqs=1, device=None, bias_on="logit", groups=None,
+                 topk_groups=None, group_score="max"):
         self.num_experts, self.topk, self.logits_dtype = int(num_experts), int(topk), logits_dtype
         self.max_tokens, self.max_seqs = max_tokens, int(max_seqs)
         self.device = _device(device)
         self.cfg = RouterConfig(int(num_experts), int(topk), _choice(SCORES, score, "score"), int(bool(renormalize)),
                                 _choice(DTYPES, logits_dtype, "logits_dtype"), float(weight_scale), float(balance_coef),
-                                float(z_coef), _choice(BIASES, bias_on, "bias_on"))
+                                float(z_coef), _choice(BIASES, bias_on, "bias_on"), *self._groups(groups, topk_groups),
+                                _choice(GROUP_SCORES, group_score, "group_score"))
         need = lib().moe_router_workspace_bytes(self.cfg, 0 if max_tokens is None else int(max_tokens), self.max_seqs)
         if need == 0:
             raise MoEError(MOE_ERR_INVALID_ARG, "router config")
@@ -202,6 +207,16 @@ class Router:
         self._workspace = None if max_tokens is None else torch.empty(need, dtype=torch.uint8, device=self.device)
         self._limits = (-1 if max_tokens is None else int(max_tokens), self.max_seqs,
                         None if max_tokens is None else self._workspace.data_ptr())
+
+    @staticmethod
+    def _groups(groups, topk_groups):
+        if groups is None:
+            if topk_groups is not None:
+                raise ValueError("topk_groups without groups")
+            return 0, 0
+        if topk_groups is None or int(groups) < 1:
+            raise ValueError("groups must be positive, with topk_groups")
+        return int(groups), int(topk_groups)
 
     def buffers(self, num_tokens, num_seqs=None, choice=True) -> RouterOutput:
         """Outputs of a call on `num_tokens`, with those of the losses for `num_seqs` sequences, and without those of the

@@ -71,6 +71,8 @@ struct RouterParams {
     Partials part;
     int T, E, k, S, chunk;      // chunk: tokens per CTA
     int sigmoid, renorm, score_bias;
+    int groups, group_size, use_groups, top2;   // groups > 1: the choice is limited to the best use_groups groups
+    int each;                                   // registers of a lane for a group
     float scale;
 };
 
@@ -166,16 +168,43 @@ __device__ __forceinline__ Cut cut_at(const int32_t *off, int S, int t, int t1, 
     return c;
 }
 
+// Which experts a lane holds: lg, lg + G, ...; with groups (kGrouped) a group takes `each` registers of every lane, so that a
+// group's experts are in registers of their own: register i holds place lg + G (i % each) of group i / each.
+template <int NI, int G, bool kGrouped>
+struct Experts {
+    int off[kGrouped ? NI : 1];
+    uint32_t has_bits = 0;
+    __device__ __forceinline__ Experts(const RouterParams &p, int lg) {
+        if constexpr (kGrouped) {
+#pragma unroll
+            for (int i = 0, g = 0, j = 0; i < NI; ++i) {
+                off[i] = g * p.group_size + j * G;
+                if (g < p.groups && j * G + lg < p.group_size) has_bits |= 1u << i;
+                if (++j == p.each) j = 0, ++g;
+            }
+        }
+    }
+    __device__ __forceinline__ int at(int i, int lg) const {
+        if constexpr (kGrouped) return off[i] + lg;
+        return lg + G * i;
+    }
+    __device__ __forceinline__ bool has(int i, int lg, int E) const {
+        if constexpr (kGrouped) return (has_bits >> i) & 1;
+        return lg + G * i < E;
+    }
+};
+
 // A token's logits as loaded (-inf where there is none), so that the next token's can be on their way.
-template <class L, int NI, int G>
-__device__ __forceinline__ void load_row(L (&l)[NI], const void *logits, int64_t ld, uint32_t t, bool on, int lg, int E) {
+template <class L, int NI, int G, bool kGrouped = false>
+__device__ __forceinline__ void load_row(L (&l)[NI], const void *logits, int64_t ld, uint32_t t, bool on, int lg, int E,
+                                         const Experts<NI, G, kGrouped> &x) {
     const L *row = static_cast<const L *>(logits) + (int64_t)t * ld + lg;
     if (E == NI * G) {   // every lane has all its experts
 #pragma unroll
         for (int i = 0; i < NI; ++i) l[i] = on ? row[G * i] : from_f32<L>(-INFINITY);
     } else {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) l[i] = on && lg + G * i < E ? row[G * i] : from_f32<L>(-INFINITY);
+        for (int i = 0; i < NI; ++i) l[i] = on && x.has(i, lg, E) ? row[x.at(i, 0)] : from_f32<L>(-INFINITY);
     }
 }
 
@@ -281,19 +310,26 @@ __device__ __forceinline__ void top_down(uint32_t (&v)[NI]) {
         }
 }
 
-// The k largest keys of a group's token from the full keys, one by one: the exact choice whatever the keys.
+// The k largest keys of a group's token from the full keys, one by one: the exact choice whatever the keys.  Returns whether
+// two neighbours among them, or the last one and the first left out, are no further apart than `margin` (of use where it is
+// not negative).
 template <int NI, int G, int NS>
-__device__ __noinline__ void choose_exact(const float (&key)[NI], int k, int lg, int (&slot_e)[NS]) {
+__device__ __noinline__ bool choose_exact(const float (&key)[NI], int k, int lg, float margin, int (&slot_e)[NS]) {
     uint32_t taken = 0;
+    bool close = false;
+    float above = INFINITY;
+    const int rounds = margin >= 0.0f ? k + 1 : k;
 #pragma unroll
     for (int q = 0; q < NS; ++q) slot_e[q] = -1;
-    for (int j = 0; j < k; ++j) {
+    for (int j = 0; j < rounds; ++j) {
         float best = -INFINITY;
         int bi = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i)
             if (!((taken >> i) & 1) && key[i] > best) best = key[i], bi = i;   // of equal keys the first stays
         const float m = group_max<G>(best);
+        close |= above - m <= margin;   // -inf: nothing is left, no neighbour
+        above = m > -INFINITY ? m : INFINITY;
         int e = group_min<G>(best == m && m > -INFINITY ? lg + G * bi : 1 << 20);
         if (e < 1 << 20) {
             if ((e & (G - 1)) == lg) taken |= 1u << (e / G);
@@ -302,23 +338,31 @@ __device__ __noinline__ void choose_exact(const float (&key)[NI], int k, int lg,
         }
 #pragma unroll
         for (int q = 0; q < NS; ++q)
-            if (j == q * G + lg) slot_e[q] = e;
+            if (j == q * G + lg && j < k) slot_e[q] = e;
     }
+    return close;
+}
+
+// A float as a whole number of the same order, and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t b = __float_as_uint(v + 0.0f);   // -0 and 0 are equal
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+    return __uint_as_float(o ^ ((uint32_t)((int32_t)~o >> 31) | 0x80000000u));
 }
 
 // The k largest keys of a group's token, ties to the lowest expert.  Slot j goes to lane j % G, place j / G: its expert
 // (-1: nothing left).  `exact`: the keys' low bits that the expert's number takes say nothing.  A lane keeps its D
 // largest; one that wins D < NI times may have had more.  Returns false, with nothing chosen, where a key is +inf or a
-// NaN that sorts above it and `cleaned` does not say that it is meant.
-template <int NI, int G, int NS, int D>
-__device__ __forceinline__ bool choose(const float (&key)[NI], int k, int lg, bool exact, bool cleaned, int (&slot_e)[NS]) {
+// NaN that sorts above it and `cleaned` does not say that it is meant.  kMargin: keys are right within margin / 2 (their order is
+// known where they are further apart than that); `close` says whether two that matter are not.
+template <int NI, int G, int NS, int D, bool kMargin = false>
+__device__ __forceinline__ bool choose(const float (&key)[NI], int k, int lg, bool exact, bool cleaned, int (&slot_e)[NS],
+                                       float margin = -1.0f, bool *close = nullptr) {
     constexpr uint32_t kLow = (uint32_t)(NI * G - 1);   // bits of an expert's number
     constexpr uint32_t kOpen = 0x00800000u;             // the order of the smallest finite float
-    auto packed = [&](int i) {
-        const uint32_t b = __float_as_uint(key[i] + 0.0f);   // -0 and 0 are equal
-        const uint32_t order = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-        return (order & ~kLow) | (kLow - (uint32_t)(lg + G * i));
-    };
+    auto packed = [&](int i) { return (ordered(key[i]) & ~kLow) | (kLow - (uint32_t)(lg + G * i)); };
     uint32_t v[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) v[i] = packed(i);
@@ -340,7 +384,8 @@ __device__ __forceinline__ bool choose(const float (&key)[NI], int k, int lg, bo
     bool again = false;
     if (D < NI && __any_sync(kAll, v[0] == 0)) {   // a lane gave all it kept: had it more that belong?
         // one that it did not keep may share the last one's high bits and have the larger full key; closed ones do not count
-        const uint32_t least = max(exact ? last : last & ~kLow, kOpen);
+        uint32_t least = max(exact ? last : last & ~kLow, kOpen);
+        if (kMargin) least = max(ordered(from_ordered(least) - margin) & ~kLow, kOpen);
         int n = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) n += packed(i) >= least;
@@ -358,6 +403,11 @@ __device__ __forceinline__ bool choose(const float (&key)[NI], int k, int lg, bo
             if (lg == G - 1) next = q + 1 < NS ? wrap : out;
             const bool edge = q * G + lg == k - 1;
             if (edge) next = out;
+            if (kMargin) {   // by the high bits and the margin together: what is near is chosen anew by the full keys
+                const float hi = from_ordered(slot[q] & ~kLow), lo = from_ordered(next | kLow);
+                again |= q * G + lg < k && slot[q] >= kOpen && next >= kOpen && hi - lo <= margin;
+                continue;
+            }
             const bool same = q * G + lg < k && slot[q] >= kOpen && ((slot[q] ^ next) & ~kLow) == 0;
             near |= same && !edge;
             again |= same && (edge || NS > 1);
@@ -384,7 +434,10 @@ __device__ __forceinline__ bool choose(const float (&key)[NI], int k, int lg, bo
             }
         }
     }
-    if (__any_sync(kAll, again)) choose_exact<NI, G, NS>(key, k, lg, slot_e);
+    if (__any_sync(kAll, again)) {
+        const bool c = choose_exact<NI, G, NS>(key, k, lg, kMargin ? margin : -1.0f, slot_e);
+        if (kMargin) *close = c;
+    }
     return true;
 }
 
@@ -400,7 +453,98 @@ __device__ __forceinline__ float over_groups(float v) {
 // six 20.6 to 22; 28219 x 259: two 20.4, one 29.2).
 constexpr int ctas_an_sm(int NI) { return NI <= 8 ? 4 : NI == 16 ? 2 : 1; }
 
-template <class L, int NI, int G, int D, bool kLoss, bool kGiven>
+// Closes the experts outside the best use_groups groups of a token: a group's score is its largest key, or the sum of its two
+// largest (of one open expert's, that alone), ties go to the lowest group.  Returns whether the scores of the last group taken
+// and the best one left out are within `margin`.
+template <int NI, int G>
+__device__ __forceinline__ bool keep_groups(float (&key)[NI], const RouterParams &p, int lg, float margin) {
+    float first = -INFINITY, second = -INFINITY, score = -INFINITY;
+#pragma unroll
+    for (int i = 0, g = 0, j = 0; i < NI; ++i) {
+        second = fmaxf(second, fminf(first, key[i]));
+        first = fmaxf(first, key[i]);
+        if (++j == p.each) {
+            float s = group_max<G>(first);
+            if (p.top2) {
+                const unsigned best = __ballot_sync(kAll, first == s) >> (threadIdx.x & 31 & ~(G - 1)) & (G == 32 ? kAll : (1u << G) - 1);
+                float t = group_max<G>(first == s ? second : first);
+                if (__popc(best) > 1) t = s;
+                s += t > -INFINITY ? t : 0.0f;
+            }
+            if (lg == g) score = s;   // groups <= G
+            first = second = -INFINITY;
+            j = 0, ++g;
+        }
+    }
+    int rank = 0;
+#pragma unroll 8
+    for (int g = 0; g < p.groups; ++g) {
+        const float s = __shfl_sync(kAll, score, g, G);
+        rank += s > score || (s == score && g < lg);
+    }
+    const bool taken = rank < p.use_groups && lg < p.groups;
+    const unsigned mask = __ballot_sync(kAll, taken) >> (threadIdx.x & 31 & ~(G - 1));
+#pragma unroll
+    for (int i = 0, g = 0, j = 0; i < NI; ++i) {
+        if (!((mask >> g) & 1)) key[i] = -INFINITY;
+        if (++j == p.each) j = 0, ++g;
+    }
+    if (margin < 0.0f) return false;
+    const float left = group_max<G>(taken ? -INFINITY : score);
+    return __any_sync(kAll, taken && score > -INFINITY && score - left <= margin);
+}
+
+// sigmoid(l) rounded from 64 bits: the order of scores that f32 arithmetic leaves open.
+__device__ __noinline__ float score_exact(float l) { return l > -INFINITY ? (float)(1.0 / (1.0 + exp(-(double)l))) : -INFINITY; }
+
+// How far apart two keys (scores plus bias), or two sums of two keys, must be for their f32 order to be that of the exact ones:
+// a score is within 2^-21 of the exact one (score_of: its exponential within 2^-22 + 1.7 |l| 2^-24 of itself, the quotient within
+// 2^-22; either error shrinks with the score), so the difference of two sums is within 2^-19; and each of the up to six sums
+// that enter it, approximate and exact, rounds to 2^-24 of the largest key or twice that: under 2^-20 of it in all.
+constexpr float kScoreMargin = 0x1p-19f;
+
+// The choice limited to groups.  Cleans l.
+template <int NI, int G, int NS, int D, bool kLoss>
+__device__ __forceinline__ void choose_grouped(float (&l)[NI], const float (&bias)[NI], const RouterParams &p, int lg, bool exact,
+                                               int (&slot_e)[NS]) {
+    clean(l);
+    bool close = false;
+    {
+        float key[NI];
+        float largest = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            key[i] = p.score_bias ? score_of_call(l[i]) : l[i];
+            if (p.bias) key[i] = fmaxf(key[i] + bias[i], -INFINITY);
+            if (p.score_bias) largest = fmaxf(largest, key[i] > -INFINITY ? fabsf(key[i]) : 0.0f);
+        }
+        if (p.score_bias) {
+            const float margin = fmaf(group_max<G>(largest), 0x1p-20f, kScoreMargin);
+            close = keep_groups<NI, G>(key, p, lg, margin);
+            bool c = false;
+            choose<NI, G, NS, D, true>(key, p.k, lg, false, true, slot_e, margin, &c);
+            close |= c;
+        } else {
+            keep_groups<NI, G>(key, p, lg, -1.0f);
+            choose<NI, G, NS, D>(key, p.k, lg, exact, true, slot_e);
+        }
+    }
+    if (__any_sync(kAll, close)) {
+        float key[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            key[i] = score_exact(l[i]);
+            if (p.bias) key[i] = fmaxf(key[i] + bias[i], -INFINITY);
+        }
+        keep_groups<NI, G>(key, p, lg, -1.0f);
+        choose_exact<NI, G, NS>(key, p.k, lg, -1.0f, slot_e);
+    }
+#pragma unroll
+    for (int q = 0; q < NS; ++q)
+        if (slot_e[q] >= 0 && p.E != NI * G) slot_e[q] = slot_e[q] / (p.each * G) * p.group_size + slot_e[q] % (p.each * G);
+}
+
+template <class L, int NI, int G, int D, bool kLoss, bool kGiven, bool kGrouped = false>
 __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const __grid_constant__ RouterParams p) {
     extern __shared__ float joined[];   // kLoss: [warps][E] probabilities, [E] counts
     __shared__ float sz[kWarps];
@@ -414,10 +558,11 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
     launch_next();
     wait_for_previous();
     if (kLoss && blockIdx.x == 0 && threadIdx.x == 0) *p.part.ticket = 0;   // for the next kernel
+    const Experts<NI, G, kGrouped> x(p, lg);
     float bias[NI];
     if (!kGiven && p.bias) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) bias[i] = lg + G * i < E ? p.bias[lg + G * i] : 0.0f;
+        for (int i = 0; i < NI; ++i) bias[i] = x.has(i, lg, E) ? p.bias[x.at(i, lg)] : 0.0f;
     }
     int s_at = 0;
     for (int a = t0; a < t1;) {
@@ -425,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
         s_at = cut.s;
         L raw[NI];
         const uint32_t end = cut.end, tw = (uint32_t)a + warp * kGroups;   // a step past the last token may pass 2^31
-        if (tw < end) load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < end, lg, E);
+        if (tw < end) load_row(raw, p.logits, p.ld, tw + grp, tw + grp < end, lg, E, x);
         float prob[kLoss ? NI : 1];
         float zsum = 0.0f;
         int tokens = 0;
@@ -442,9 +587,9 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
 #pragma unroll
             for (int i = 0; i < NI; ++i) l[i] = to_f32(raw[i]);
             const uint32_t tn = tb + kWarps * kGroups;
-            if (tn < end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < end, lg, E);
+            if (tn < end) load_row(raw, p.logits, p.ld, tn + grp, tn + grp < end, lg, E, x);
             float m = -INFINITY, top = -INFINITY;   // the largest logit, and that of the chosen
-            if (kGiven || (kLoss && p.bias) || (!p.renorm && !p.sigmoid)) {
+            if (kGiven || (kLoss && (p.bias || kGrouped)) || (!p.renorm && !p.sigmoid)) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i) m = fmaxf(m, l[i]);
                 m = fminf(group_max<G>(m), FLT_MAX);
@@ -458,7 +603,9 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
                     if (my_e[q] >= E) my_e[q] = -1;
                 }
             } else {
-                for (int pass = 0; pass < 2; ++pass) {
+                if constexpr (kGrouped) {
+                    choose_grouped<NI, G, NS, D, kLoss>(l, bias, p, lg, sizeof(L) == 2 && !p.bias, my_e);
+                } else for (int pass = 0; pass < 2; ++pass) {
                     float key[NI];
 #pragma unroll
                     for (int i = 0; i < NI; ++i) key[i] = l[i];
@@ -487,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
 #pragma unroll
                     for (int q = 0; q < NS; ++q) top = fmaxf(top, my_l[q]);
                     top = group_max<G>(top);
-                    if (kLoss && !p.bias) m = top;
+                    if (kLoss && !kGrouped && !p.bias) m = top;
                 }
                 if (p.renorm) {
                     float sum = 0.0f;
@@ -539,9 +686,8 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
         if (kLoss) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int e = lg + G * i;
                 const float pr = over_groups<G>(prob[i]);
-                if (e < E && grp == 0) joined[warp * E + e] = pr;
+                if (x.has(i, lg, E) && grp == 0) joined[warp * E + x.at(i, lg)] = pr;
             }
             zsum = warp_sum(zsum);
             tokens = __reduce_add_sync(kAll, tokens);
@@ -683,6 +829,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(co
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lg = lane & (G - 1), grp = lane / G;
     const int E = p.E, k = p.k;
     float *mine = scatter + (warp * kGroups + grp) * E;
+    const Experts<NI, G, false> x(RouterParams{}, lg);
     launch_next();
     wait_for_previous();
     if (p.d_weights)
@@ -706,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(co
         };
         const uint32_t end = cut.end, tw = (uint32_t)a + warp * kGroups;   // a step past the last token may pass 2^31
         if (tw < end) {
-            load_row<L, NI, G>(raw, p.logits, p.ld, tw + grp, tw + grp < end, lg, E);
+            load_row(raw, p.logits, p.ld, tw + grp, tw + grp < end, lg, E, x);
             if (p.d_weights) load_slots(tw + grp, tw + grp < end);
         }
         int n = 0;
@@ -730,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_bwd_kernel(co
 #pragma unroll
             for (int i = 0; i < NI; ++i) l[i] = to_f32(raw[i]);
             const uint32_t tn = tb + kWarps * kGroups;
-            if (tn < end) load_row<L, NI, G>(raw, p.logits, p.ld, tn + grp, tn + grp < end, lg, E);
+            if (tn < end) load_row(raw, p.logits, p.ld, tn + grp, tn + grp < end, lg, E, x);
             // the chosen slots' part
             float add[NS], ls[NS], dw[NS], dot = 0.0f;
             int idx[NS];
@@ -843,6 +990,13 @@ bool valid(const moe_router_config *c) {
     if (c->score != MOE_SCORE_SOFTMAX && c->score != MOE_SCORE_SIGMOID) return false;
     if (!valid_dtype(c->logits_dtype)) return false;
     if (!isfinite(c->weight_scale) || !isfinite(c->balance_coef) || !isfinite(c->z_coef)) return false;
+    if (c->num_groups != 0) {
+        if (c->num_groups < 2 || c->num_groups > 32 || c->num_experts % c->num_groups) return false;
+        const int size = c->num_experts / c->num_groups;
+        if (c->num_groups * ((size + 31) / 32) > 32) return false;
+        if (c->topk_groups < 1 || c->topk_groups > c->num_groups || c->topk > c->topk_groups * size) return false;
+        if (c->group_score != MOE_GROUP_MAX && c->group_score != MOE_GROUP_TOP2) return false;
+    }
     if (c->bias_on != MOE_BIAS_LOGIT && (c->bias_on != MOE_BIAS_SCORE || c->score != MOE_SCORE_SIGMOID)) return false;
     return c->score == MOE_SCORE_SOFTMAX || c->z_coef == 0.0f;
 }
@@ -921,6 +1075,30 @@ struct RunRouter {
     }
 };
 
+// The same for groups of experts, whose registers are their own: eight lanes have a token where no more than eight registers
+// hold it so, else 32.
+struct RunGrouped {
+    const RouterParams &p;
+    bool bf, loss;
+    int ctas;
+    cudaStream_t s;
+    template <class L, int NI, int G>
+    cudaError_t run() const {
+        constexpr int kFew = G == 32 && NI > 4 ? 4 : NI;
+        if (loss) return launch(router_kernel<L, NI, G, kFew, true, false, true>, ctas, kThreads, (size_t)(kWarps + 1) * p.E * 4, 1, s, p);
+        return launch(router_kernel<L, NI, G, kFew, false, false, true>, ctas, kThreads, 0, 1, s, p);
+    }
+    template <int NI, int G>
+    cudaError_t run() const {
+        return bf ? run<bf16, NI, G>() : run<float, NI, G>();
+    }
+    cudaError_t run() const {
+        const int n = p.groups * p.each;
+        if (p.each * 8 >= p.group_size && n <= 8) return n <= 2 ? run<2, 8>() : n <= 4 ? run<4, 8>() : run<8, 8>();
+        return n <= 2 ? run<2, 32>() : n <= 4 ? run<4, 32>() : n <= 8 ? run<8, 32>() : n <= 16 ? run<16, 32>() : run<32, 32>();
+    }
+};
+
 struct RunBwd {
     const RouterBwd &p;
     bool bf;
@@ -954,13 +1132,25 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
     p.renorm = cfg->renormalize != 0;
     p.score_bias = bias && cfg->bias_on == MOE_BIAS_SCORE;
+    if (cfg->num_groups && !given && cfg->topk_groups < cfg->num_groups) {   // all groups: no limit
+        p.groups = cfg->num_groups;
+        p.group_size = p.E / p.groups;
+        p.use_groups = cfg->topk_groups;
+        p.top2 = cfg->group_score == MOE_GROUP_TOP2 && p.group_size > 1;
+        const int by8 = (p.group_size + 7) / 8;
+        p.each = p.groups * by8 <= 8 ? by8 : (p.group_size + 31) / 32;
+        p.score_bias = cfg->bias_on == MOE_BIAS_SCORE;   // without a bias too: a group's sum is of scores
+    }
     p.scale = cfg->weight_scale;
     p.S = loss ? loss->num_seqs : 1;
     p.seq_offsets = loss ? loss->seq_offsets : nullptr;
     const int ctas = ctas_for(T, p.E, p.S);
     p.chunk = T > 0 ? (T - 1) / ctas + 1 : 1;
     if (loss) carve(p.E, T, p.S, static_cast<char *>(ws), &p.part);
-    if (T > 0) {
+    if (T > 0 && p.groups > 1) {
+        if (RunGrouped{p, cfg->logits_dtype == MOE_DTYPE_BF16, loss != nullptr, (T - 1) / p.chunk + 1, s}.run() != cudaSuccess)
+            return MOE_ERR_CUDA;
+    } else if (T > 0) {
         if (by_experts(p.E, RunRouter{p, cfg->logits_dtype == MOE_DTYPE_BF16, loss != nullptr, given,
                                       (T - 1) / p.chunk + 1, s}) != cudaSuccess)
             return MOE_ERR_CUDA;
