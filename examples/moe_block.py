@@ -8,7 +8,7 @@ A block takes the residual stream h and the previous block's output y:
     h, n, codes, sf = BlockNorm(h, y)                 gate, residual sum, both norms, quantised input of the experts
     idx, weights    = Router(n W_r^T)                 top-k choice of the experts
     out             = MoELayer(codes, sf, idx, weights)
-    out            += W_down . swiglu(W_gate_up . n)  the shared expert, FP4 weights (up to 16 tokens)
+    out            += W_down . swiglu(W_gate_up . n)  the shared expert: FP4 weights up to 16 tokens, FP8 above
 
 and hands (h, out) to the next block.  Every buffer of a step is made once, so
 a step allocates nothing and can be captured into a CUDA graph.
@@ -23,27 +23,33 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import moe_expert_ffn_gb300 as moe  # noqa: E402
 import moe_synth  # noqa: E402
+from examples.shared_expert import SharedExpert  # noqa: E402
 
 
 class MoEBlock:
     """One block for up to `tokens` tokens, with random weights; FP4 weights in the routed experts too."""
 
-    def __init__(self, tokens, hidden, inter, experts, topk, seed=0, device="cuda"):
+    def __init__(self, tokens, hidden, inter, experts, topk, seed=0, device="cuda", groups=None, topk_groups=None):
         dev = torch.device(device)
         wl = moe_synth.custom(tokens, hidden, inter, experts, topk, seed=seed, wfmt=moe.MOE_W_FP4_E2M1_UE8M0_32)
         g = torch.Generator(device=dev).manual_seed(seed)
         rand = lambda *s: torch.randn(*s, generator=g, device=dev)  # noqa: E731
         self.T, self.H, self.E = tokens, hidden, experts
         self.norm = moe.BlockNorm(hidden, gate="channel", quant="ue8m0", device=dev)
-        self.router = moe.Router(experts, topk, balance_coef=1e-2, z_coef=1e-4, max_tokens=tokens, device=dev)
+        self.router = moe.Router(experts, topk, balance_coef=1e-2, z_coef=1e-4, max_tokens=tokens, device=dev, groups=groups,
+                                 topk_groups=topk_groups)
         self.experts = moe.MoELayer(tokens, hidden, inter, experts, topk, wfmt=wl.wfmt, device=torch.device("cuda", torch.cuda.current_device()))
         self.experts.transform_weights(*moe_synth.make_weights(wl, device=dev))
-        self.gate_up = moe.Fp4Linear(hidden, 2 * inter, act="swiglu", device=dev)
-        self.down = moe.Fp4Linear(inter, hidden, device=dev)
-        self.shared = {"gate_up": moe_synth.pack_e2m1_rows(rand(2 * inter, hidden) / hidden ** 0.5),
-                       "down": moe_synth.pack_e2m1_rows(rand(hidden, inter) / inter ** 0.5)}
-        self.gate_up.transform_weights(*self.shared["gate_up"])
-        self.down.transform_weights(*self.shared["down"])
+        w_gate_up, w_down = rand(2 * inter, hidden) / hidden ** 0.5, rand(hidden, inter) / inter ** 0.5
+        self.few = tokens <= moe.FP4_LINEAR_MAX_TOKENS
+        if self.few:
+            self.gate_up = moe.Fp4Linear(hidden, 2 * inter, act="swiglu", device=dev)
+            self.down = moe.Fp4Linear(inter, hidden, device=dev)
+            self.shared = {"gate_up": moe_synth.pack_e2m1_rows(w_gate_up), "down": moe_synth.pack_e2m1_rows(w_down)}
+            self.gate_up.transform_weights(*self.shared["gate_up"])
+            self.down.transform_weights(*self.shared["down"])
+        else:
+            self.shared = SharedExpert(w_gate_up, w_down)
         self.w_post, self.w_pre = 1 + 0.1 * rand(hidden), 1 + 0.1 * rand(hidden)
         self.gate = 0.5 + 0.1 * rand(hidden)
         self.w_router = rand(experts, hidden) / hidden ** 0.5
@@ -52,7 +58,7 @@ class MoEBlock:
         self.routed = self.router.buffers(tokens, num_seqs=1)
         self.logits = torch.empty(tokens, experts, device=dev)
         self.n32 = torch.empty(tokens, hidden, device=dev)
-        self.mid = self.gate_up.buffers(tokens)
+        self.mid = self.gate_up.buffers(tokens) if self.few else self.shared.buffers(tokens)
         self.out = torch.empty(tokens, hidden, dtype=torch.bfloat16, device=dev)
 
     def _route_input(self, h, y):
@@ -67,9 +73,11 @@ class MoEBlock:
         o = self._route_input(h, y)
         r = self.router.forward(self.logits, out=self.routed)
         self.experts.forward(o.codes, o.sf, r.topk_idx, r.topk_weights, y=self.out)
-        if self.T <= moe.FP4_LINEAR_MAX_TOKENS:
+        if self.few:
             self.gate_up.forward(o.n, out=self.mid)
             self.down.forward(self.mid, add=self.out, out=self.out)
+        else:
+            self.shared.forward(o.n, add=self.out, out=self.out, buffers=self.mid)
         return o.h, self.out
 
     def train_router(self, h, y, lr):

@@ -19,7 +19,7 @@ import math
 
 import torch
 
-from . import (MOE_ERR_INVALID_ARG, Fp4LinearConfig, Fp8LinearConfig, Fp8QuantConfig, Fp8QuantIO, MoEError, NormConfig, RouterConfig,
+from . import (MOE_ERR_INVALID_ARG, Fp4LinearConfig, Fp8LinearConfig, Fp8QuantConfig, MoEError, NormConfig, RouterConfig,
                _check, lib)
 
 DTYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -411,7 +411,7 @@ class Fp8Quant:
         self.cfg = Fp8QuantConfig(int(columns), _choice(ACTS, act, "act"), _choice(DTYPES, dtype, "dtype"), float(act_clamp))
         L, b = lib(), _bind()
         # a call without rows checks the config alone
-        if L.moe_fp8_quant(self.cfg, 0, None, 0, Fp8QuantIO(codes=16, sf=16), None):
+        if L.moe_fp8_quant(self.cfg, 0, None, 0, None, None):
             raise MoEError(MOE_ERR_INVALID_ARG, "fp8 quantiser config")
         self._cfg, self._dev = ctypes.addressof(self.cfg), _index(self.device)
         self._fwd, self._bwd, self._wts = b.fp8_quant, b.fp8_quant_backward, b.fp8_quant_weights

@@ -60,10 +60,9 @@ __device__ constexpr uint32_t operand_step() { return kMN ? 32 * 128 / 16 : 2; }
 
 constexpr uint32_t idesc_major(bool a_mn, bool b_mn) { return (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u); }
 
-__device__ __forceinline__ float clamp_of(float v, float c) { return v < -c ? -c : v > c ? c : v; }   // a NaN stays one
 __device__ __forceinline__ float swiglu_of(float g, float u, float c) {
     g = clamp_of(g, c);
-    return __fdividef(g, 1.0f + expf(-g)) * clamp_of(u, c);
+    return g * sigmoid_of(g) * clamp_of(u, c);
 }
 
 __device__ __forceinline__ void store_once(void *p, const uint32_t (&v)[8], bool wide) {
@@ -859,8 +858,8 @@ int moe_fp8_linear_forward(const moe_fp8_linear_config *cfg, int num_tokens, con
                            void *stream) {
     if (!valid(cfg) || num_tokens < 0) return MOE_ERR_INVALID_ARG;
     const bool glu = cfg->act == MOE_ACT_SWIGLU, quant = cfg->quant != MOE_QUANT_NONE;
-    if (quant ? !y_sf || add : y_sf != nullptr) return MOE_ERR_INVALID_ARG;
     if (num_tokens == 0) return MOE_OK;
+    if (quant ? !y_sf || add : y_sf != nullptr) return MOE_ERR_INVALID_ARG;
     const int64_t K = cfg->in_features, N = cfg->out_features, n = glu ? N / 2 : N;
     const size_t es = quant ? 1 : dtype_bytes(cfg->out_dtype);
     if (!rows_ok(x, ld_x, K, 1) || !rows_ok(w, K, K, 1) || !rows_ok(y, ld_y, n, es) || (add && !rows_ok(add, ld_add, n, es)))

@@ -40,9 +40,6 @@ __device__ __forceinline__ void load4(const bf16 *p, float (&v)[4]) {
     v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xFFFF0000u);
 }
 
-__device__ __forceinline__ float clamped(float v, float c) { return v < -c ? -c : v > c ? c : v; }   // a NaN stays one
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + expf(-g)); }
-
 // A tile's values (RW rows of four columns) with the scales of their groups.
 template <int RW, int kWarps>
 __device__ __forceinline__ void write_tile(const float (&v)[RW][4], const QuantParams &p, int W, int64_t r0, int c0, bool on, bool blocks,
@@ -139,17 +136,17 @@ __global__ void __launch_bounds__(kWarps * 32) quant_kernel(const __grid_constan
         for (int r = 0; r < RW; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float g = clamped(a[r][i], p.clamp);
-                a[r][i] = g * sigmoid(g) * clamped(u[r][i], p.clamp);
+                const float g = clamp_of(a[r][i], p.clamp);
+                a[r][i] = g * sigmoid_of(g) * clamp_of(u[r][i], p.clamp);
             }
     }
     if constexpr (kKind == kGrad) {
-        // with s = sigmoid(g): da = d u s (1 + g (1 - s)), du = d g s, none through a clamp
+        // with s = sigmoid_of(g): da = d u s (1 + g (1 - s)), du = d g s, none through a clamp
 #pragma unroll
         for (int r = 0; r < RW; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float g0 = a[r][i], u0 = u[r][i], g = clamped(g0, p.clamp), up = clamped(u0, p.clamp), s = sigmoid(g);
+                const float g0 = a[r][i], u0 = u[r][i], g = clamp_of(g0, p.clamp), up = clamp_of(u0, p.clamp), s = sigmoid_of(g);
                 a[r][i] = fabsf(g0) > p.clamp ? 0.0f : e[r][i] * up * (s * fmaf(g, 1.0f - s, 1.0f));
                 u[r][i] = fabsf(u0) > p.clamp ? 0.0f : e[r][i] * (g * s);
             }
@@ -207,8 +204,9 @@ using namespace moe;
 extern "C" {
 
 int moe_fp8_quant(const moe_fp8_quant_config *cfg, int num_tokens, const void *v, int64_t ld_v, const moe_fp8_quant_io *out, void *stream) {
-    if (!valid(cfg) || num_tokens < 0 || !out_ok(out)) return MOE_ERR_INVALID_ARG;
+    if (!valid(cfg) || num_tokens < 0) return MOE_ERR_INVALID_ARG;
     if (num_tokens == 0) return MOE_OK;
+    if (!out_ok(out)) return MOE_ERR_INVALID_ARG;
     const bool glu = cfg->act == MOE_ACT_SWIGLU;
     if (!rows_ok(v, ld_v, (int64_t)cfg->columns * (glu ? 2 : 1), dtype_bytes(cfg->dtype))) return MOE_ERR_INVALID_ARG;
     const QuantParams p{v, nullptr, ld_v, 0, out->codes, out->col_codes, out->sf, out->col_sf, num_tokens, cfg->columns, cfg->act_clamp};
@@ -217,8 +215,9 @@ int moe_fp8_quant(const moe_fp8_quant_config *cfg, int num_tokens, const void *v
 
 int moe_fp8_quant_backward(const moe_fp8_quant_config *cfg, int num_tokens, const void *d, int64_t ld_d, const void *v, int64_t ld_v,
                            const moe_fp8_quant_io *out, void *stream) {
-    if (!valid(cfg) || cfg->act != MOE_ACT_SWIGLU || num_tokens < 0 || !out_ok(out)) return MOE_ERR_INVALID_ARG;
+    if (!valid(cfg) || cfg->act != MOE_ACT_SWIGLU || num_tokens < 0) return MOE_ERR_INVALID_ARG;
     if (num_tokens == 0) return MOE_OK;
+    if (!out_ok(out)) return MOE_ERR_INVALID_ARG;
     const size_t es = dtype_bytes(cfg->dtype);
     if (!rows_ok(v, ld_v, 2 * (int64_t)cfg->columns, es) || !rows_ok(d, ld_d, cfg->columns, es)) return MOE_ERR_INVALID_ARG;
     const QuantParams p{v, d, ld_v, ld_d, out->codes, out->col_codes, out->sf, out->col_sf, num_tokens, cfg->columns, cfg->act_clamp};

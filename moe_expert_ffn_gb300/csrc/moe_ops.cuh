@@ -190,6 +190,15 @@ __device__ __forceinline__ int ue8m0_code(float amax) {
 // 2^-e of that code.
 __device__ __forceinline__ float ue8m0_inverse(int code) { return __uint_as_float((uint32_t)(254 - code) << 23); }
 
+// Symmetric clamp; a NaN stays one.
+__device__ __forceinline__ float clamp_of(float v, float c) { return v < -c ? -c : v > c ? c : v; }
+
+// 1 / (1 + e^-g) by the exponential that cannot overflow: within 2^-21 of itself, or 2^-149 where that is no normal number.
+__device__ __forceinline__ float sigmoid_of(float g) {
+    const float t = expf(-fabsf(g));
+    return __fdividef(g >= 0.0f ? 1.0f : t, 1.0f + t);
+}
+
 // Scale of a group of E4M3 codes as the layer's requantisation has it: sf = amax / 448, codes of v times the rounded 1 / sf.
 // Where amax is below 2^-100 (1 / sf would pass the f32 range at its end) v is brought up by 2^64 first.  An all-zero group has
 // sf 0 and codes 0, one with an infinity sf infinity.
