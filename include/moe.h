@@ -473,7 +473,8 @@ MOE_API int moe_fp4_linear_forward(const moe_fp4_linear_config *cfg, int num_tok
  *   dy [T, N]: dy_sf [ceil(T/128), N], x [T, K]: x_sf [ceil(T/128), K]    the weight's gradient
  * Codes lie in their natural order in all of them; nothing is laid out anew.
  * Code matrices and outputs are 16-byte aligned with pitches of a multiple of
- * 16 bytes; w and the scales are contiguous. */
+ * 16 bytes; w and the scales are contiguous, those along the tokens 16-byte
+ * aligned. */
 typedef struct {
     int in_features;   /* K, a multiple of 16, 16..2^20 */
     int out_features;  /* N rows of the weight, a multiple of 16, 16..2^20; of 256 with MOE_ACT_SWIGLU */
@@ -500,6 +501,12 @@ MOE_API int moe_fp8_linear_backward_input(const moe_fp8_linear_config *cfg, int 
 MOE_API int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int num_tokens, const void *dy, int64_t ld_dy,
                                            const float *dy_sf, const void *x, int64_t ld_x, const float *x_sf,
                                            const float *add, int64_t ld_add, float *dw, int64_t ld_dw, void *stream);
+
+/* Test of the timeout path: every wait of the next FP8 linear launch of the
+ * process gives up after `wait_limit_us` microseconds instead of two seconds,
+ * and CTA 0 withholds its copies, so that waits run out.  That call returns
+ * MOE_OK; later ones run normally. */
+MOE_API int moe_fp8_linear_test_arm_timeout(int wait_limit_us);
 
 /* Synchronises the current device; MOE_ERR_DEVICE_TIMEOUT if a bounded wait of
  * an FP8 linear kernel gave up there since the last call (its output is

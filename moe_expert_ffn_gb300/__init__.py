@@ -39,6 +39,7 @@ ABI_SYMBOLS = (
     "moe_router_workspace_bytes", "moe_router_forward", "moe_balance_loss", "moe_router_backward",
     "moe_fp4_linear_weight_bytes", "moe_fp4_linear_transform_weights", "moe_fp4_linear_forward",
     "moe_fp8_linear_forward", "moe_fp8_linear_backward_input", "moe_fp8_linear_backward_weight", "moe_fp8_linear_status",
+    "moe_fp8_linear_test_arm_timeout",
     "moe_fp8_quant", "moe_fp8_quant_backward", "moe_fp8_quant_weights",
 )
 
@@ -155,6 +156,7 @@ def lib():
                     ("moe_fp8_linear_backward_input", i32, [ecfg, i32, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp]),
                     ("moe_fp8_linear_backward_weight", i32, [ecfg, i32, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp]),
                     ("moe_fp8_linear_status", i32, []),
+                    ("moe_fp8_linear_test_arm_timeout", i32, [i32]),
                     ("moe_fp8_quant", i32, [qcfg, i32, vp, i64, qio, vp]),
                     ("moe_fp8_quant_backward", i32, [qcfg, i32, vp, i64, vp, i64, qio, vp]),
                     ("moe_fp8_quant_weights", i32, [qcfg, i32, vp, i64, vp, vp, vp])):

@@ -43,8 +43,38 @@ struct Fp8Params {
     int tiles_r, tiles_c, split;
     int f32;
     int wide;                     // out and add in 32-byte pieces
+    int wait_us;                  // 0, or (a test of the timeout) the limit of every wait, with CTA 0's first copies withheld
     float clamp;
 };
+
+// Waits for a barrier's phase, at most two seconds (or wait_us); false when it or another wait of the CTA gave up.  The clock, the
+// limit and the abort flag are looked at every 256 polls, and none of them before.
+__device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, volatile int *abort_flag, const Fp8Params &p) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 255) == 0) {
+            if (*abort_flag) return false;
+            const uint64_t now = globaltimer_ns(), limit = p.wait_us ? 1000ull * (uint64_t)p.wait_us : kWaitTimeoutNs;
+            if (!t0) {
+                t0 = now;
+            } else if (now - t0 > limit) {
+                *abort_flag = 1;
+                raise_timeout(g_status);
+                return false;
+            }
+        }
+    }
+}
+// The same whatever the abort flag says: for what is in flight when a CTA ends.
+__device__ __forceinline__ void await_end(uint32_t bar, uint32_t parity, const Fp8Params &p) {
+    const uint64_t limit = p.wait_us ? 1000ull * (uint64_t)p.wait_us : kWaitTimeoutNs;
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (globaltimer_ns() - t0 > limit) return;
+}
 
 constexpr uint32_t kPanel = 128 * 128;   // 128 rows or columns of one block
 constexpr int kChunk = 8;                // blocks whose scales are brought to shared memory together
@@ -126,6 +156,9 @@ constexpr int kFoldWarps = 8;
 constexpr int kWideStages = 3;
 constexpr uint32_t kWideStage = 4 * kPanel;   // two blocks of this CTA's 128 rows and of its half of the columns
 constexpr int kRowPitch = 132;           // floats between two blocks of row scales: writers of 4 rows x 8 blocks meet no bank twice
+// Registers of the four other warps and of the fold warps: 128 x 72 + 256 x 216 threads' are the 384 x 168 of the launch.
+constexpr int kOtherRegs = 72, kFoldRegs = 216;
+static_assert(128 * kOtherRegs + 256 * kFoldRegs <= kWideThreads * 168, "registers of the launch");
 constexpr int kRowGroup = 16;            // row tiles that the walk takes together
 
 struct alignas(8) WideCtrl {
@@ -162,24 +195,35 @@ __device__ __forceinline__ WideTile wide_tile(int64_t tile, const Fp8Params &p) 
 
 // acc += the warp's 2 x 64 TMEM columns times their scales; `release` once the last ones are in registers.
 template <bool kCol, class F>
-__device__ __forceinline__ void fold_wide(float2 (&acc)[64], uint32_t t0, uint32_t t1, float s0, float s1, const float *cs,
-                                          F release) {
+__device__ __forceinline__ void fold_wide(float2 (&acc)[64], uint32_t t0, uint32_t t1, float s0, float s1, uint32_t cs, F release) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        float v[32], w[32];
-        tmem_ld32(c ? t1 : t0, v);
-        tmem_ld32((c ? t1 : t0) + 32, w);
+    for (int c = 0; c < 8; ++c) {
+        float v[16];
+        tmem_ld16((c < 4 ? t0 : t1) + 16 * (c & 3), v);
         tmem_ld_wait();
-        if (c == 1) release();
-        const float2 s = pair(c ? s1 : s0);
+        if (c == 7) release();
+        const float2 s = pair(c < 4 ? s0 : s1);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float *from = i < 16 ? v + 2 * i : w + 2 * i - 32;
-            float2 f = s;
-            if (kCol) f = __fmul2_rn(s, *reinterpret_cast<const float2 *>(cs + 64 * c + 2 * i));
-            acc[32 * c + i] = __ffma2_rn(make_float2(from[0], from[1]), f, acc[32 * c + i]);
+        for (int i = 0; i < 4; ++i) {
+            float2 f = s, g = s;
+            if (kCol) {
+                const uint4 k = ld_shared16(cs + 64 * c + 16 * i);
+                f = __fmul2_rn(s, make_float2(__uint_as_float(k.x), __uint_as_float(k.y)));
+                g = __fmul2_rn(s, make_float2(__uint_as_float(k.z), __uint_as_float(k.w)));
+            }
+            acc[8 * c + 2 * i] = __ffma2_rn(make_float2(v[4 * i], v[4 * i + 1]), f, acc[8 * c + 2 * i]);
+            acc[8 * c + 2 * i + 1] = __ffma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), g, acc[8 * c + 2 * i + 1]);
         }
     }
+}
+
+// 16 bytes of scales to shared memory, zeros where there are none.
+__device__ __forceinline__ void copy_scales(float *to, const float *from, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+// An arrival (one of the barrier's count) when this thread's copies have landed.
+__device__ __forceinline__ void arrive_when_copied(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 template <int kMode>
@@ -197,7 +241,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
     const int DB = p.DB, stages = (DB + 1) / 2;
     const int64_t total = (int64_t)p.tiles_r * p.tiles_c;
-    int *err = g_status;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_rows);
@@ -209,7 +252,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctrl->tfull[b]), 1);
             mbar_init(smem_u32(&ctrl->tempty[b]), 2 * kFoldWarps);
-            mbar_init(smem_u32(&ctrl->sfull[b]), 1);
+            mbar_init(smem_u32(&ctrl->sfull[b]), kMode == kWeight ? 32 : 1);
             mbar_init(smem_u32(&ctrl->sempty[b]), kFoldWarps);
         }
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ctrl->halves[i]), 2);
@@ -228,128 +271,129 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     const uint32_t full_c = mapa_shared(smem_u32(&ctrl->full[0]), 0), tempty_c = mapa_shared(smem_u32(&ctrl->tempty[0]), 0);
     wait_for_previous();
 
-    if (warp == 0) {
-        // ---- copies: each CTA its 128 rows and its half of the columns (SwiGLU: gate rows of W in the even CTA, up rows in the odd)
-        const uint64_t pol = policy_evict_normal();
-        int it = 0;
-        bool ok = true;
-        for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
-            const WideTile t = wide_tile(tile, p);
-            const int r0 = t.tr * 256 + (int)rank * 128;
-            const int c0 = kMode == kSwiglu ? t.tc * 128 + (int)rank * p.C : t.tc * 256 + (int)rank * 128;
-            for (int ks = 0; ks < stages; ++ks, ++it) {
-                const int s = it % kWideStages, n = min(2, DB - 2 * ks);
-                if (!mbar_wait(smem_u32(&ctrl->empty[s]), ((it / kWideStages) & 1) ^ 1, abort_flag, err)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&ctrl->full[s]), (uint32_t)n * 4 * kPanel);
-                    const uint32_t dst = base + s * kWideStage, full = full_c + 8u * s;
-                    for (int j = 0; j < n; ++j) {
-                        const int d = (2 * ks + j) * 128;
-                        tma_load_2d_pair(dst + j * kPanel, &tm_rows, rows_mn(kMode) ? r0 : d, rows_mn(kMode) ? d : r0, full, pol);
-                        tma_load_2d_pair(dst + (2 + j) * kPanel, &tm_cols, cols_mn(kMode) ? c0 : d, cols_mn(kMode) ? d : c0, full,
-                                         pol);
-                    }
-                }
-                __syncwarp();
-            }
-        }
-        for (int i = max(0, it - kWideStages); i < it; ++i)   // the last copies land before the pair ends
-            drain_wait(smem_u32(&ctrl->empty[i % kWideStages]), (i / kWideStages) & 1, err);
-    } else if (warp == 1) {
-        // ---- MMA (even CTA): one block, one accumulator
-        if (rank == 0) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(256, 256) | idesc_major(rows_mn(kMode), cols_mn(kMode));
-            int it = 0, kt = 0;
+    if (warp < kFoldWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 0) {
+            // ---- copies: each CTA its 128 rows and its half of the columns (SwiGLU: gate rows of W in the even CTA, up rows in the odd)
+            const uint64_t pol = policy_evict_normal();
+            int it = 0;
             bool ok = true;
             for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
-                for (int ks = 0; ok && ks < stages; ++ks, ++it) {
+                const WideTile t = wide_tile(tile, p);
+                const int r0 = t.tr * 256 + (int)rank * 128;
+                const int c0 = kMode == kSwiglu ? t.tc * 128 + (int)rank * p.C : t.tc * 256 + (int)rank * 128;
+                for (int ks = 0; ks < stages; ++ks, ++it) {
                     const int s = it % kWideStages, n = min(2, DB - 2 * ks);
-                    if (!mbar_wait(smem_u32(&ctrl->full[s]), (it / kWideStages) & 1, abort_flag, err)) {
+                    if (!await(smem_u32(&ctrl->empty[s]), ((it / kWideStages) & 1) ^ 1, abort_flag, p)) {
                         ok = false;
                         break;
                     }
-                    for (int j = 0; j < n; ++j, ++kt) {
-                        const int b = kt & 1;
-                        if (!mbar_wait(smem_u32(&ctrl->tempty[b]), ((kt >> 1) & 1) ^ 1, abort_flag, err)) {
-                            ok = false;
-                            break;
+                    if (lane == 0) {
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&ctrl->full[s]), (uint32_t)n * 4 * kPanel);
+                        const uint32_t dst = base + s * kWideStage, full = full_c + 8u * s;
+                        for (int j = 0; j < n; ++j) {
+                            if (p.wait_us && blockIdx.x == 0) break;
+                            const int d = (2 * ks + j) * 128;
+                            tma_load_2d_pair(dst + j * kPanel, &tm_rows, rows_mn(kMode) ? r0 : d, rows_mn(kMode) ? d : r0, full, pol);
+                            tma_load_2d_pair(dst + (2 + j) * kPanel, &tm_cols, cols_mn(kMode) ? c0 : d, cols_mn(kMode) ? d : c0, full,
+                                             pol);
                         }
-                        tc_fence_after();
-                        if (lane == 0) {
-                            const uint64_t a = operand_desc<rows_mn(kMode)>(base + s * kWideStage + j * kPanel);
-                            const uint64_t w = operand_desc<cols_mn(kMode)>(base + s * kWideStage + (2 + j) * kPanel);
-#pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                umma_pair_e4m3(tmem + b * 256, a + kk * operand_step<rows_mn(kMode)>(),
-                                               w + kk * operand_step<cols_mn(kMode)>(), idesc, kk > 0);
-                            umma_pair_commit(smem_u32(&ctrl->tfull[b]), 3);
-                        }
-                        __syncwarp();
                     }
-                    if (ok && lane == 0) umma_pair_commit(smem_u32(&ctrl->empty[s]), 3);
                     __syncwarp();
                 }
             }
-            if (it > 0) drain_wait(smem_u32(&ctrl->empty[(it - 1) % kWideStages]), ((it - 1) / kWideStages) & 1, err);
-        }
-    } else if (warp == 2) {
-        // ---- scales of eight blocks at a time to shared memory
-        int ch = 0;
-        bool ok = true;
-        for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
-            const WideTile t = wide_tile(tile, p);
-            const int r0 = t.tr * 256 + (int)rank * 128;
-            for (int k0 = 0; k0 < DB; k0 += kChunk, ++ch) {
-                const int slot = ch & 1;
-                if (!mbar_wait(smem_u32(&ctrl->sempty[slot]), ((ch >> 1) & 1) ^ 1, abort_flag, err)) {
-                    ok = false;
-                    break;
-                }
-                if (kMode == kWeight) {   // neighbouring rows and columns lie together
-                    for (int j = 0; j < kChunk; ++j) {
-                        const int b = k0 + j;
-                        if (b >= DB) break;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = r0 + (int)lane + 32 * i;
-                            sc.row[slot][j * kRowPitch + lane + 32 * i] = r < p.R ? p.row_sf[(int64_t)b * p.rs_blk + r] : 0.0f;
+            for (int i = max(0, it - kWideStages); i < it; ++i)   // the last copies land before the pair ends
+                await_end(smem_u32(&ctrl->empty[i % kWideStages]), (i / kWideStages) & 1, p);
+        } else if (warp == 1) {
+            // ---- MMA (one thread of the even CTA): a stage's first block into accumulator 0, its second into 1
+            if (rank == 0 && lane == 0) {
+                constexpr uint32_t idesc = idesc_e4m3_f32(256, 256) | idesc_major(rows_mn(kMode), cols_mn(kMode));
+                const uint64_t a0 = operand_desc<rows_mn(kMode)>(base), w0 = operand_desc<cols_mn(kMode)>(base + 2 * kPanel);
+                int s = 0, it = 0;
+                uint32_t ph = 0, tph[2] = {1, 1};
+                bool ok = true;
+                for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
+                    for (int ks = 0; ok && ks < stages; ++ks, ++it) {
+                        const int n = min(2, DB - 2 * ks);
+                        if (!await(smem_u32(&ctrl->full[s]), ph, abort_flag, p)) {
+                            ok = false;
+                            break;
                         }
+                        const uint64_t a = a0 + s * (kWideStage / 16), w = w0 + s * (kWideStage / 16);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int c = t.tc * 256 + (int)lane + 32 * i;
-                            sc.col[slot][j * 256 + lane + 32 * i] = c < p.C ? p.col_sf[(int64_t)b * p.cs_blk + c] : 0.0f;
+                        for (int j = 0; j < 2; ++j) {
+                            if (j >= n) break;
+                            if (!await(smem_u32(&ctrl->tempty[j]), tph[j], abort_flag, p)) {
+                                ok = false;
+                                break;
+                            }
+                            tph[j] ^= 1;
+                            tc_fence_after();
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                umma_pair_e4m3(tmem + j * 256, a + j * (kPanel / 16) + kk * operand_step<rows_mn(kMode)>(),
+                                               w + j * (kPanel / 16) + kk * operand_step<cols_mn(kMode)>(), idesc, kk > 0);
+                            umma_pair_commit(smem_u32(&ctrl->tfull[j]), 3);
                         }
+                        if (ok) umma_pair_commit(smem_u32(&ctrl->empty[s]), 3);
+                        if (++s == kWideStages) s = 0, ph ^= 1;
                     }
-                } else {   // eight blocks of a row lie together: a load takes them of four rows
-                    const int j = lane & 7, b = k0 + j;
+                }
+                if (it > 0) await_end(smem_u32(&ctrl->empty[(it - 1) % kWideStages]), ((it - 1) / kWideStages) & 1, p);
+            }
+        } else if (warp == 2) {
+            // ---- scales of eight blocks at a time to shared memory
+            int ch = 0;
+            bool ok = true;
+            for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
+                const WideTile t = wide_tile(tile, p);
+                const int r0 = t.tr * 256 + (int)rank * 128;
+                for (int k0 = 0; k0 < DB; k0 += kChunk, ++ch) {
+                    const int slot = ch & 1;
+                    if (!await(smem_u32(&ctrl->sempty[slot]), ((ch >> 1) & 1) ^ 1, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    if (kMode == kWeight) {   // neighbouring rows and columns lie together, sizes are multiples of 16
+                        const int r = r0 + 4 * (int)lane, c = t.tc * 256 + 4 * (int)lane;
+                        const int n = min(kChunk, DB - k0);
+                        for (int j = 0; j < n; ++j) {
+                            const int64_t b = k0 + j;
+                            copy_scales(&sc.row[slot][j * kRowPitch + 4 * lane], p.row_sf + b * p.rs_blk + r, r < p.R);
+                            copy_scales(&sc.col[slot][j * 256 + 4 * lane], p.col_sf + b * p.cs_blk + c, c < p.C);
+                            copy_scales(&sc.col[slot][j * 256 + 128 + 4 * lane], p.col_sf + b * p.cs_blk + c + 128, c + 128 < p.C);
+                        }
+                        arrive_when_copied(smem_u32(&ctrl->sfull[slot]));
+                    } else {   // eight blocks of a row lie together: a load takes them of four rows
+                        const int j = lane & 7, b = k0 + j;
 #pragma unroll 8
-                    for (int i = 0; i < 32; ++i) {
-                        const int r = r0 + (int)(lane >> 3) + 4 * i;
-                        sc.row[slot][j * kRowPitch + (lane >> 3) + 4 * i] =
-                            b < DB && r < p.R ? p.row_sf[(int64_t)r * p.rs_row + b] : 0.0f;
-                    }
-                    if (lane < 16) {
-                        const int h = lane >> 3;
-                        const int cb = kMode == kSwiglu ? t.tc + h * (p.C / 128) : t.tc * 2 + h;
-                        const bool on = b < DB && (kMode == kSwiglu || cb * 128 < p.C);
-                        sc.col[slot][j * 2 + h] = on ? p.col_sf[cb * p.cs_col + b * p.cs_blk] : 0.0f;
+                        for (int i = 0; i < 32; ++i) {
+                            const int r = r0 + (int)(lane >> 3) + 4 * i;
+                            sc.row[slot][j * kRowPitch + (lane >> 3) + 4 * i] =
+                                b < DB && r < p.R ? p.row_sf[(int64_t)r * p.rs_row + b] : 0.0f;
+                        }
+                        if (lane < 16) {
+                            const int h = lane >> 3;
+                            const int cb = kMode == kSwiglu ? t.tc + h * (p.C / 128) : t.tc * 2 + h;
+                            const bool on = b < DB && (kMode == kSwiglu || cb * 128 < p.C);
+                            sc.col[slot][j * 2 + h] = on ? p.col_sf[cb * p.cs_col + b * p.cs_blk] : 0.0f;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&ctrl->sfull[slot]));
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctrl->sfull[slot]));
             }
         }
-    } else if (warp >= kFoldWarp0) {
+    } else {
         // ---- fold the blocks' accumulators, own 128 rows; warp: 32 rows, half of the columns
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFoldRegs));
         const int q = warp & 3, h = (warp - kFoldWarp0) >> 2;
         const int lrow = q * 32 + (int)lane;
         // SwiGLU: 64 gate columns and the 64 up columns that belong to them
         const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + (kMode == kSwiglu ? 64 * h : 128 * h);
         const uint32_t t1 = t0 + (kMode == kSwiglu ? 128 : 64);
-        int kt = 0, ch = 0, done = 0;
+        int ch = 0, done = 0;
+        uint32_t phases = 0;
         bool ok = true;
         for (int64_t tile = cluster; ok && tile < total; tile += clusters, ++done) {
             const WideTile t = wide_tile(tile, p);
@@ -358,27 +402,28 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
             for (int k0 = 0; ok && k0 < DB; k0 += kChunk, ++ch) {
                 const int slot = ch & 1;
-                if (!mbar_wait(smem_u32(&ctrl->sfull[slot]), (ch >> 1) & 1, abort_flag, err)) {
+                if (!await(smem_u32(&ctrl->sfull[slot]), (ch >> 1) & 1, abort_flag, p)) {
                     ok = false;
                     break;
                 }
                 const int n = min(kChunk, DB - k0);
-                for (int j = 0; j < n; ++j, ++kt) {
-                    const int b = kt & 1;
+                for (int j = 0; j < n; ++j) {
+                    const int b = j & 1;
                     const float sr = sc.row[slot][j * kRowPitch + lrow];
                     float s0 = sr, s1 = sr;
-                    const float *cs = nullptr;
+                    uint32_t cs = 0;
                     if (kMode == kWeight) {
-                        cs = &sc.col[slot][j * 256 + h * 128];
+                        cs = smem_u32(&sc.col[slot][j * 256 + h * 128]);
                     } else if (kMode == kSwiglu) {
                         s0 = sr * sc.col[slot][2 * j], s1 = sr * sc.col[slot][2 * j + 1];
                     } else {
                         s0 = s1 = sr * sc.col[slot][2 * j + h];
                     }
-                    if (!mbar_wait(smem_u32(&ctrl->tfull[b]), (kt >> 1) & 1, abort_flag, err)) {
+                    if (!await(smem_u32(&ctrl->tfull[b]), (phases >> b) & 1, abort_flag, p)) {
                         ok = false;
                         break;
                     }
+                    phases ^= 1u << b;
                     tc_fence_after();
                     fold_wide<kMode == kWeight>(acc, t0 + b * 256, t1 + b * 256, s0, s1, cs, [&] {
                         tc_fence_before();
@@ -406,7 +451,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     all[warp - kFoldWarp0][lane] = amax;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&ctrl->halves[q]));
-                    if (!mbar_wait(smem_u32(&ctrl->halves[q]), done & 1, abort_flag, err)) break;
+                    if (!await(smem_u32(&ctrl->halves[q]), done & 1, abort_flag, p)) break;
                     amax = fmaxf(amax, all[(warp - kFoldWarp0) ^ 4][lane]);
                     const GroupScale g = group_scale(amax);
                     if (row < p.R) {
@@ -506,7 +551,6 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
     const int r0 = tr * BT;
     const int DB = p.DB, all = kGlu ? DB : (DB + 1) / 2;                   // stages of the whole axis
     const int s0 = (int)((int64_t)all * rank / split), s1 = (int)((int64_t)all * (rank + 1) / split);   // this CTA's
-    int *err = g_status;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tm_rows);
@@ -542,11 +586,12 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
         int it = 0;
         for (int st = s0; st < s1; ++st, ++it) {
             const int s = it % kStages, n = kGlu ? 2 : min(2, DB - 2 * st);
-            if (!mbar_wait(smem_u32(&ctrl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, err)) break;
+            if (!await(smem_u32(&ctrl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, p)) break;
             if (lane == 0) {
                 const uint32_t full = smem_u32(&ctrl->full[s]), dst = base + s * kStage;
                 mbar_arrive_expect_tx(full, (uint32_t)n * kPanel + (kGlu ? 1 : n) * kRows);
                 for (int j = 0; j < n; ++j) {
+                    if (p.wait_us && blockIdx.x == 0) break;
                     const int d = (kGlu ? st : 2 * st + j) * 128, c0 = tc * 128 + (kGlu ? j * p.C : 0);
                     tma_load_2d(dst + j * kPanel, &tm_cols, cols_mn(kMode) ? c0 : d, cols_mn(kMode) ? d : c0, full, pol_w);
                     if (!kGlu || j == 0)
@@ -556,16 +601,16 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
             }
             __syncwarp();
         }
-        for (int i = max(0, it - kStages); i < it; ++i) drain_wait(smem_u32(&ctrl->full[i % kStages]), (i / kStages) & 1, err);
+        for (int i = max(0, it - kStages); i < it; ++i) await_end(smem_u32(&ctrl->full[i % kStages]), (i / kStages) & 1, p);
     } else if (warp == 1) {
         constexpr uint32_t idesc = idesc_e4m3_f32(128, BT) | idesc_major(cols_mn(kMode), rows_mn(kMode));
         int it = 0;
         bool ok = true;
         for (int st = s0; ok && st < s1; ++st, ++it) {
             const int s = it % kStages, b = it % kBufs, n = kGlu ? 2 : min(2, DB - 2 * st);
-            if (!mbar_wait(smem_u32(&ctrl->full[s]), (it / kStages) & 1, abort_flag, err)) break;
+            if (!await(smem_u32(&ctrl->full[s]), (it / kStages) & 1, abort_flag, p)) break;
             for (int j = 0; j < n; ++j) {
-                if (!mbar_wait(smem_u32(&ctrl->tempty[j][b]), ((it / kBufs) & 1) ^ 1, abort_flag, err)) {
+                if (!await(smem_u32(&ctrl->tempty[j][b]), ((it / kBufs) & 1) ^ 1, abort_flag, p)) {
                     ok = false;
                     break;
                 }
@@ -584,12 +629,12 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
             if (ok && lane == 0) umma_commit(smem_u32(&ctrl->empty[s]));
             __syncwarp();
         }
-        if (it > 0) drain_wait(smem_u32(&ctrl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1, err);
+        if (it > 0) await_end(smem_u32(&ctrl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1, p);
     } else if (warp == 2) {
         // the product of both scales for each row of each panel (weight's: the row's, and the column's apart)
         for (int st = s0, ch = 0; st < s1; st += kChunk / 2, ++ch) {
             const int slot = ch & 1;
-            if (!mbar_wait(smem_u32(&ctrl->sempty[slot]), ((ch >> 1) & 1) ^ 1, abort_flag, err)) break;
+            if (!await(smem_u32(&ctrl->sempty[slot]), ((ch >> 1) & 1) ^ 1, abort_flag, p)) break;
             float *sc = ctrl->sc[slot];
             if (kMode == kWeight) {
                 for (int j = 0; j < kChunk && 2 * st + j < DB; ++j) {
@@ -634,12 +679,12 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
         bool ok = true;
         for (int it = 0, st = s0; ok && st < s1; ++st, ++it) {
             const int slot = (it >> 2) & 1, b = it % kBufs;
-            if ((it & 3) == 0 && !mbar_wait(smem_u32(&ctrl->sfull[slot]), (it >> 3) & 1, abort_flag, err)) break;
+            if ((it & 3) == 0 && !await(smem_u32(&ctrl->sfull[slot]), (it >> 3) & 1, abort_flag, p)) break;
             if (kGlu || 2 * st + set < DB) {
                 const int j = 2 * (it & 3) + set;
                 const float *sc = ctrl->sc[slot] + j * (BT + 4);
                 const float mine = kMode == kWeight ? ctrl->lane_sc[slot][j * 128 + q * 32 + lane] : 1.0f;
-                if (!mbar_wait(smem_u32(&ctrl->tfull[set][b]), (it / kBufs) & 1, abort_flag, err)) {
+                if (!await(smem_u32(&ctrl->tfull[set][b]), (it / kBufs) & 1, abort_flag, p)) {
                     ok = false;
                     break;
                 }
@@ -736,6 +781,8 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
 // ---- host ------------------------------------------------------------------
 constexpr int kMaxFeatures = 1 << 20;
 
+std::atomic<int> armed_us{0};   // a test's wait limit for the next launch
+
 int up_to(int64_t n, int m) { return (int)((n + m - 1) / m); }
 
 bool valid(const moe_fp8_linear_config *c) {
@@ -808,6 +855,7 @@ int run(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_co
     const int sms = dev < 0 ? 0 : sm_count(dev);
     if (!sms) return MOE_ERR_CUDA;
     p.DB = up_to(D, 128);
+    p.wait_us = armed_us.exchange(0, std::memory_order_relaxed);
     const int wt = kMode == kSwiglu ? 2 * p.C : p.C;   // rows of W
     p.tiles_r = up_to(p.R, 256);
     p.tiles_c = up_to(p.C, kMode == kSwiglu ? 128 : 256);
@@ -912,7 +960,7 @@ int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int num_tok
         return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
     if (!rows_ok(dy, ld_dy, N, 1) || !rows_ok(x, ld_x, K, 1)) return MOE_ERR_INVALID_ARG;
-    if (!dy_sf || !x_sf || !aligned_to(dy_sf, 4) || !aligned_to(x_sf, 4)) return MOE_ERR_INVALID_ARG;
+    if (!dy_sf || !x_sf || !aligned_to(dy_sf, 16) || !aligned_to(x_sf, 16)) return MOE_ERR_INVALID_ARG;
     Fp8Params p{};
     p.row_sf = dy_sf, p.col_sf = x_sf;
     p.rs_row = p.cs_col = 1;
@@ -921,6 +969,12 @@ int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int num_tok
     p.R = (int)N, p.C = (int)K, p.f32 = 1;
     p.wide = wide_pieces(p);
     return run<kWeight>(static_cast<const uint8_t *>(dy), ld_dy, static_cast<const uint8_t *>(x), ld_x, num_tokens, p, s);
+}
+
+int moe_fp8_linear_test_arm_timeout(int wait_limit_us) {
+    if (wait_limit_us < 1) return MOE_ERR_INVALID_ARG;
+    armed_us.store(wait_limit_us);
+    return MOE_OK;
 }
 
 int moe_fp8_linear_status(void) {

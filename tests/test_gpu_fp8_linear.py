@@ -276,3 +276,20 @@ def test_repeats_streams_and_capture(m, T):
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(first, flat(out)))
+
+
+@pytest.mark.parametrize("T,N,K", [(20, 272, 400), (300, 272, 400), (2500, 1040, 400)])
+def test_a_wait_that_runs_out(m, T, N, K):
+    """CTA 0 withholds its copies for one call: its waits give up, the status says so once, the next call is as before."""
+    a = forward_inputs(T, N, K, 13)
+    op = m.Fp8Linear(K, N, device=DEV)
+    before = op.forward(*a)
+    torch.cuda.synchronize()
+    assert m.lib().moe_fp8_linear_status() == m.MOE_OK
+    assert m.lib().moe_fp8_linear_test_arm_timeout(0) == m.MOE_ERR_INVALID_ARG
+    assert m.lib().moe_fp8_linear_test_arm_timeout(20000) == m.MOE_OK
+    op.forward(*a)
+    assert m.lib().moe_fp8_linear_status() == m.MOE_ERR_DEVICE_TIMEOUT
+    assert m.lib().moe_fp8_linear_status() == m.MOE_OK
+    assert torch.equal(op.forward(*a), before)
+    assert m.lib().moe_fp8_linear_status() == m.MOE_OK
