@@ -40,7 +40,7 @@ struct Fp8Params {
     int64_t ld_out;
     float *sf;
     int R, C, DB;                 // rows and columns of the output, blocks of the contracted axis
-    int tiles_r, tiles_c, split;
+    int tiles_r, tiles_c, split, stages;
     int f32;
     int wide;                     // out and add in 32-byte pieces
     int wait_us;                  // 0, or (a test of the timeout) the limit of every wait, with CTA 0's first copies withheld
@@ -229,6 +229,11 @@ __device__ __forceinline__ void ask_for_add(const Fp8Params &p, int r0, int c0, 
         const char *from = static_cast<const char *>(p.add) + (row * p.ld_add + c0) * es;
         for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + o));
     }
+}
+
+// Asks for a box of a tensor to be brought to L2, where every later write of it shows: for what an earlier kernel may still write.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap *tm, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tm), "r"(x), "r"(y) : "memory");
 }
 
 // 16 bytes of scales to shared memory, zeros where there are none.
@@ -513,29 +518,41 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // ============================================================================
 // Few rows: tiles of 128 columns x BT rows, the contracted axis split over a cluster
 // ============================================================================
-constexpr int kSmallThreads = 32 * 11;   // 0 copies, 1 MMA, 2 scales, 3..10 fold
-constexpr int kSmallFold0 = 3;
+constexpr int kSmallThreads = 32 * 12;   // 0 copies, 1 and 2 MMA, 3 scales, 4..11 fold
+constexpr int kSmallFold0 = 4;
+constexpr int kAhead = 16;               // panels of the weight that a CTA asks for before the kernel before it has ended
 
-template <int BT>
-constexpr int small_stages() { return BT == 16 ? 3 : BT == 32 ? 5 : BT == 64 ? 4 : 3; }
+constexpr int kMaxStages = 5;
+constexpr size_t kSmHalf = 115712, kSmAll = 232448;   // shared memory of a CTA, two and one of them an SM
+
 template <int BT>
 constexpr int small_bufs() { return BT <= 64 ? 4 : 2; }
 template <int kMode, int BT>
 constexpr uint32_t small_stage() { return 2 * kPanel + (kMode == kSwiglu ? 1 : 2) * BT * 128; }
+// Whether the cluster's CTAs send one another their sums; those of 128 rows have no room but the stages', and are fetched.
+template <int BT, bool kSplit>
+constexpr bool small_sends() { return kSplit && BT <= 64; }
 
 template <int kMode, int BT>
 struct SmallCtrl {
-    uint64_t full[small_stages<BT>()], empty[small_stages<BT>()];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t tfull[2][small_bufs<BT>()], tempty[2][small_bufs<BT>()];
     uint64_t sfull[2], sempty[2];
+    uint64_t sums;
     uint32_t tmem_base;
     int abort;
     alignas(16) float sc[2][kChunk * (BT + 4)];
-    float lane_sc[2][kMode == kWeight ? kChunk * 128 : 1];
+    float lane_sc[2][kMode == kWeight ? kChunk * 128 : 4];
 };
-template <int kMode, int BT>
-constexpr size_t small_smem() {
-    return 1024 + (size_t)small_stages<BT>() * small_stage<kMode, BT>() + sizeof(SmallCtrl<kMode, BT>);
+// Bytes of the sums that a CTA is sent for `rows` rows of a tile: [rank][row of its][set][128].
+constexpr size_t sent_bytes(int rows, int split) { return (size_t)((rows + split - 1) / split) * split * 1024; }
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Four bytes to a CTA of the cluster, counted by a barrier of its.
+__device__ __forceinline__ void send(uint32_t to, float v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to), "r"(__float_as_uint(v)), "r"(bar)
+                 : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster16(uint32_t addr) {
@@ -545,25 +562,61 @@ __device__ __forceinline__ float4 ld_cluster16(uint32_t addr) {
 }
 __device__ __forceinline__ float4 plus(float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
 
-// Two panels of 128 columns a stage: two neighbouring blocks (SwiGLU: gate and up rows of one), each with accumulators and four
-// fold warps of its own.  TMEM lanes are the output's columns, its columns the rows.
-template <int kMode, int BT>
+// Four consecutive outputs, and of add.
+__device__ __forceinline__ float4 load4(const Fp8Params &p, int64_t row, int col) {
+    if (p.f32) return *reinterpret_cast<const float4 *>(static_cast<const float *>(p.add) + row * p.ld_add + col);
+    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const bf16 *>(p.add) + row * p.ld_add + col);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(const Fp8Params &p, float4 a, int64_t row, int col) {
+    if (p.f32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * p.ld_out + col) = a;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + row * p.ld_out + col) = make_uint2(bf16x2(a.x, a.y), bf16x2(a.z, a.w));
+}
+
+// act, quantisation, add and store of four columns of a row; a lane has them, a warp 128.
+template <bool kGlu>
+__device__ __forceinline__ void finish4(const Fp8Params &p, float4 a, float4 u, float4 add, int64_t row, int tc) {
+    const int lane = threadIdx.x & 31, col = tc * 128 + 4 * lane;
+    if (kGlu) {
+        a.x = swiglu_of(a.x, u.x, p.clamp), a.y = swiglu_of(a.y, u.y, p.clamp);
+        a.z = swiglu_of(a.z, u.z, p.clamp), a.w = swiglu_of(a.w, u.w, p.clamp);
+        if (p.sf) {
+            const float mine = fmaxf(fmaxf(fmaxf(fmaxf(0.0f, fabsf(a.x)), fabsf(a.y)), fabsf(a.z)), fabsf(a.w));
+            const GroupScale g = group_scale(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mine))));
+            *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.out) + row * p.ld_out + col) = g.codes(a.x, a.y) | g.codes(a.z, a.w) << 16;
+            if (lane == 0) p.sf[row * (p.C / 128) + tc] = g.sf;
+            return;
+        }
+    } else {
+        a = plus(a, u);
+    }
+    if (col < p.C) store4(p, plus(a, add), row, col);
+}
+
+// Two panels of 128 columns a stage: two neighbouring blocks (SwiGLU: gate and up rows of one), each with an MMA thread,
+// accumulators and four fold warps of its own.  TMEM lanes are the output's columns, its columns the rows.
+template <int kMode, int BT, bool kSplit>
 __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
     fp8_small_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_cols,
                      const __grid_constant__ Fp8Params p) {
     extern __shared__ uint8_t smem_raw[];
     launch_next();
     using Ctrl = SmallCtrl<kMode, BT>;
-    constexpr int kStages = small_stages<BT>(), kBufs = small_bufs<BT>();
+    constexpr int kBufs = small_bufs<BT>();
+    const int kStages = p.stages;
     constexpr uint32_t kStage = small_stage<kMode, BT>(), kRows = BT * 128;
     constexpr uint32_t kTmem = 2 * kBufs * BT;
-    constexpr bool kGlu = kMode == kSwiglu;
+    constexpr bool kGlu = kMode == kSwiglu, kSend = small_sends<BT, kSplit>();
     const uint32_t raw = smem_u32(smem_raw), base = align1024(raw);
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(smem_raw + (base - raw) + kStages * kStage);
+    float *sent = reinterpret_cast<float *>(ctrl + 1);
     const int warp = threadIdx.x >> 5;
-    const uint32_t lane = threadIdx.x & 31, rank = cluster_ctarank();
-    const int split = p.split, tile = blockIdx.x / split, tr = tile % p.tiles_r, tc = tile / p.tiles_r;
-    const int r0 = tr * BT;
+    const uint32_t lane = threadIdx.x & 31, rank = kSplit ? cluster_ctarank() : 0;
+    const int split = kSplit ? p.split : 1, tile = blockIdx.x / split, tr = tile % p.tiles_r, tc = tile / p.tiles_r;
+    const int r0 = tr * BT, rows = min(BT, p.R - r0);
     const int DB = p.DB, all = kGlu ? DB : (DB + 1) / 2;                   // stages of the whole axis
     const int s0 = (int)((int64_t)all * rank / split), s1 = (int)((int64_t)all * (rank + 1) / split);   // this CTA's
 
@@ -572,18 +625,21 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
         tma_prefetch_desc(&tm_cols);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_u32(&ctrl->full[s]), 1);
-            mbar_init(smem_u32(&ctrl->empty[s]), 1);
+            mbar_init(smem_u32(&ctrl->empty[s]), 2);
         }
         for (int j = 0; j < 2; ++j) {
             for (int b = 0; b < kBufs; ++b) {
                 mbar_init(smem_u32(&ctrl->tfull[j][b]), 1);
                 mbar_init(smem_u32(&ctrl->tempty[j][b]), 4);
             }
-            mbar_init(smem_u32(&ctrl->sfull[j]), 1);
+            mbar_init(smem_u32(&ctrl->sfull[j]), kMode == kWeight ? 32 : 1);
             mbar_init(smem_u32(&ctrl->sempty[j]), 8);
         }
+        mbar_init(smem_u32(&ctrl->sums), 1);
         ctrl->abort = 0;
         fence_mbar_init();
+        // rows rank, rank + split, ... are this CTA's to join: every CTA of the cluster sends it 128 sums of both sets for each
+        if (kSend) mbar_arrive_expect_tx(smem_u32(&ctrl->sums), (uint32_t)((max(rows - (int)rank, 0) + split - 1) / split * split * 1024));
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(&ctrl->tmem_base), kTmem);
@@ -592,16 +648,26 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (kSend) cluster_arrive();   // the others may send from here on
     const uint32_t tmem = ctrl->tmem_base;
     volatile int *abort_flag = &ctrl->abort;
+    // the weight's part in L2 while the kernel before this one ends
+    if (kMode != kWeight && warp == 3) {
+        const int panel = 2 * s0 + (int)lane;
+        if (lane < kAhead && panel < (kGlu ? 2 * s1 : min(2 * s1, DB))) {
+            const int d = (kGlu ? panel >> 1 : panel) * 128, c0 = tc * 128 + (kGlu ? (panel & 1) * p.C : 0);
+            prefetch_box(&tm_cols, cols_mn(kMode) ? c0 : d, cols_mn(kMode) ? d : c0);
+        }
+    }
     wait_for_previous();
 
     if (warp == 0) {
         const uint64_t pol_w = p.tiles_r > 1 ? policy_evict_normal() : policy_evict_first(), pol_x = policy_evict_last();
-        int it = 0;
-        for (int st = s0; st < s1; ++st, ++it) {
-            const int s = it % kStages, n = kGlu ? 2 : min(2, DB - 2 * st);
-            if (!await(smem_u32(&ctrl->empty[s]), ((it / kStages) & 1) ^ 1, abort_flag, p)) break;
+        int s = 0;
+        uint32_t ph = 1;
+        for (int st = s0; st < s1; ++st) {
+            const int n = kGlu ? 2 : min(2, DB - 2 * st);
+            if (!await(smem_u32(&ctrl->empty[s]), ph, abort_flag, p)) break;
             if (lane == 0) {
                 const uint32_t full = smem_u32(&ctrl->full[s]), dst = base + s * kStage;
                 mbar_arrive_expect_tx(full, (uint32_t)n * kPanel + (kGlu ? 1 : n) * kRows);
@@ -615,71 +681,71 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
                 }
             }
             __syncwarp();
+            if (++s == kStages) s = 0, ph ^= 1;
         }
-        for (int i = max(0, it - kStages); i < it; ++i) await_end(smem_u32(&ctrl->full[i % kStages]), (i / kStages) & 1, p);
-    } else if (warp == 1) {
-        constexpr uint32_t idesc = idesc_e4m3_f32(128, BT) | idesc_major(cols_mn(kMode), rows_mn(kMode));
-        int it = 0;
-        bool ok = true;
-        for (int st = s0; ok && st < s1; ++st, ++it) {
-            const int s = it % kStages, b = it % kBufs, n = kGlu ? 2 : min(2, DB - 2 * st);
-            if (!await(smem_u32(&ctrl->full[s]), (it / kStages) & 1, abort_flag, p)) break;
-            for (int j = 0; j < n; ++j) {
-                if (!await(smem_u32(&ctrl->tempty[j][b]), ((it / kBufs) & 1) ^ 1, abort_flag, p)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t a = operand_desc<cols_mn(kMode)>(base + s * kStage + j * kPanel);
-                    const uint64_t x = operand_desc<rows_mn(kMode)>(base + s * kStage + 2 * kPanel + (kGlu ? 0 : j) * kRows);
+        for (int i = 0; i < min(kStages, s1 - s0); ++i) {   // the last copies land before the CTA ends
+            if (--s < 0) s = kStages - 1, ph ^= 1;
+            await_end(smem_u32(&ctrl->full[s]), ph ^ 1, p);
+        }
+    } else if (warp <= 2) {
+        // one thread for each panel of a stage
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(128, BT) | idesc_major(cols_mn(kMode), rows_mn(kMode));
+            const int j = warp - 1;
+            const uint64_t a0 = operand_desc<cols_mn(kMode)>(base + j * kPanel);
+            const uint64_t x0 = operand_desc<rows_mn(kMode)>(base + 2 * kPanel + (kGlu ? 0 : j) * kRows);
+            int s = 0, b = 0;
+            uint32_t ph = 0, tph = 1;
+            for (int st = s0; st < s1; ++st) {
+                if (!await(smem_u32(&ctrl->full[s]), ph, abort_flag, p)) break;
+                if (kGlu || 2 * st + j < DB) {
+                    if (!await(smem_u32(&ctrl->tempty[j][b]), tph, abort_flag, p)) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        umma_e4m3(tmem + (j * kBufs + b) * BT, a + kk * operand_step<cols_mn(kMode)>(),
-                                  x + kk * operand_step<rows_mn(kMode)>(), idesc, kk > 0);
+                        umma_e4m3(tmem + (j * kBufs + b) * BT, a0 + s * (kStage / 16) + kk * operand_step<cols_mn(kMode)>(),
+                                  x0 + s * (kStage / 16) + kk * operand_step<rows_mn(kMode)>(), idesc, kk > 0);
                     umma_commit(smem_u32(&ctrl->tfull[j][b]));
                 }
-                __syncwarp();
+                umma_commit(smem_u32(&ctrl->empty[s]));
+                if (++s == kStages) s = 0, ph ^= 1;
+                if (++b == kBufs) b = 0, tph ^= 1;
             }
-            if (ok && lane == 0) umma_commit(smem_u32(&ctrl->empty[s]));
-            __syncwarp();
+            if (s1 > s0) await_end(smem_u32(&ctrl->empty[s ? s - 1 : kStages - 1]), s ? ph : ph ^ 1, p);
         }
-        if (it > 0) await_end(smem_u32(&ctrl->empty[(it - 1) % kStages]), ((it - 1) / kStages) & 1, p);
-    } else if (warp == 2) {
+    } else if (warp == 3) {
         // the product of both scales for each row of each panel (weight's: the row's, and the column's apart)
         for (int st = s0, ch = 0; st < s1; st += kChunk / 2, ++ch) {
             const int slot = ch & 1;
             if (!await(smem_u32(&ctrl->sempty[slot]), ((ch >> 1) & 1) ^ 1, abort_flag, p)) break;
             float *sc = ctrl->sc[slot];
             if (kMode == kWeight) {
-                for (int j = 0; j < kChunk && 2 * st + j < DB; ++j) {
+                const int r = r0 + 4 * (int)lane, c = tc * 128 + 4 * (int)lane, n = min(kChunk, DB - 2 * st);
+                for (int j = 0; j < n; ++j) {
                     const int64_t b = 2 * st + j;
+                    copy_scales(sc + j * (BT + 4) + 4 * lane, p.row_sf + b * p.rs_blk + r, r < p.R);
+                    copy_scales(&ctrl->lane_sc[slot][j * 128 + 4 * lane], p.col_sf + b * p.cs_blk + c, c < p.C);
+                }
+                arrive_when_copied(smem_u32(&ctrl->sfull[slot]));
+                continue;
+            }
+            constexpr int kBlocks = kGlu ? kChunk / 2 : kChunk, kEach = 32 / kBlocks;   // blocks of a chunk, rows of a load
+            const int j = lane % kBlocks, b = (kGlu ? st : 2 * st) + j, sub = lane / kBlocks;
+            float g = 0.0f, u = 0.0f;
+            if (b < DB) {
+                g = p.col_sf[tc * p.cs_col + b * p.cs_blk];
+                if (kGlu) u = p.col_sf[(tc + p.C / 128) * p.cs_col + b * p.cs_blk];
+            }
+            float v[BT / kEach];
 #pragma unroll
-                    for (int i = 0; i < BT / 32; ++i) {
-                        const int r = r0 + (int)lane + 32 * i;
-                        sc[j * (BT + 4) + lane + 32 * i] = r < p.R ? p.row_sf[b * p.rs_blk + r] : 0.0f;
-                    }
+            for (int i = 0; i < BT / kEach; ++i) {
+                const int r = r0 + sub + kEach * i;
+                v[i] = b < DB && r < p.R ? p.row_sf[(int64_t)r * p.rs_row + b] : 0.0f;
+            }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = tc * 128 + (int)lane + 32 * i;
-                        ctrl->lane_sc[slot][j * 128 + lane + 32 * i] = c < p.C ? p.col_sf[b * p.cs_blk + c] : 0.0f;
-                    }
-                }
-            } else {
-                constexpr int kBlocks = kGlu ? kChunk / 2 : kChunk, kEach = 32 / kBlocks;   // blocks of a chunk, rows of a load
-                const int j = lane % kBlocks, b = (kGlu ? st : 2 * st) + j, sub = lane / kBlocks;
-                float g = 0.0f, u = 0.0f;
-                if (b < DB) {
-                    g = p.col_sf[tc * p.cs_col + b * p.cs_blk];
-                    if (kGlu) u = p.col_sf[(tc + p.C / 128) * p.cs_col + b * p.cs_blk];
-                }
-#pragma unroll 8
-                for (int i = 0; i < BT / kEach; ++i) {
-                    const int r = r0 + sub + kEach * i;
-                    const float v = b < DB && r < p.R ? p.row_sf[(int64_t)r * p.rs_row + b] : 0.0f;
-                    sc[(kGlu ? 2 * j : j) * (BT + 4) + sub + kEach * i] = v * g;
-                    if (kGlu) sc[(2 * j + 1) * (BT + 4) + sub + kEach * i] = v * u;
-                }
+            for (int i = 0; i < BT / kEach; ++i) {
+                sc[(kGlu ? 2 * j : j) * (BT + 4) + sub + kEach * i] = v[i] * g;
+                if (kGlu) sc[(2 * j + 1) * (BT + 4) + sub + kEach * i] = v[i] * u;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctrl->sfull[slot]));
@@ -691,18 +757,14 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
         float acc[BT];
 #pragma unroll
         for (int i = 0; i < BT; ++i) acc[i] = 0.0f;
-        bool ok = true;
-        for (int it = 0, st = s0; ok && st < s1; ++st, ++it) {
+        for (int it = 0, st = s0; st < s1; ++st, ++it) {
             const int slot = (it >> 2) & 1, b = it % kBufs;
             if ((it & 3) == 0 && !await(smem_u32(&ctrl->sfull[slot]), (it >> 3) & 1, abort_flag, p)) break;
             if (kGlu || 2 * st + set < DB) {
                 const int j = 2 * (it & 3) + set;
-                const float *sc = ctrl->sc[slot] + j * (BT + 4);
+                const uint32_t sc = smem_u32(ctrl->sc[slot] + j * (BT + 4));
                 const float mine = kMode == kWeight ? ctrl->lane_sc[slot][j * 128 + q * 32 + lane] : 1.0f;
-                if (!await(smem_u32(&ctrl->tfull[set][b]), (it / kBufs) & 1, abort_flag, p)) {
-                    ok = false;
-                    break;
-                }
+                if (!await(smem_u32(&ctrl->tfull[set][b]), (it / kBufs) & 1, abort_flag, p)) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < BT; c += kStep) {
@@ -717,12 +779,13 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
                     }
 #pragma unroll
                     for (int i = 0; i < kStep; i += 4) {
-                        float4 s = *reinterpret_cast<const float4 *>(sc + c + i);
-                        if (kMode == kWeight) s.x *= mine, s.y *= mine, s.z *= mine, s.w *= mine;
-                        acc[c + i] = fmaf(v[i], s.x, acc[c + i]);
-                        acc[c + i + 1] = fmaf(v[i + 1], s.y, acc[c + i + 1]);
-                        acc[c + i + 2] = fmaf(v[i + 2], s.z, acc[c + i + 2]);
-                        acc[c + i + 3] = fmaf(v[i + 3], s.w, acc[c + i + 3]);
+                        const uint4 k = ld_shared16(sc + 4 * (c + i));
+                        float4 f = make_float4(__uint_as_float(k.x), __uint_as_float(k.y), __uint_as_float(k.z), __uint_as_float(k.w));
+                        if (kMode == kWeight) f.x *= mine, f.y *= mine, f.z *= mine, f.w *= mine;
+                        acc[c + i] = fmaf(v[i], f.x, acc[c + i]);
+                        acc[c + i + 1] = fmaf(v[i + 1], f.y, acc[c + i + 1]);
+                        acc[c + i + 2] = fmaf(v[i + 2], f.z, acc[c + i + 2]);
+                        acc[c + i + 3] = fmaf(v[i + 3], f.w, acc[c + i + 3]);
                     }
                 }
             }
@@ -731,62 +794,88 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
                 if (lane == 0) mbar_arrive(smem_u32(&ctrl->sempty[slot]));
             }
         }
-        // every MMA of the CTA is done (both sets have seen theirs): the stages' memory takes the partial sums [set][row][128]
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        float *part = reinterpret_cast<float *>(smem_raw + (base - raw)) + (size_t)set * BT * 128 + q * 32 + lane;
+        if (kSend) {
+            // row i's sums to the CTA that joins it: i % split, where it is row i / split
+            cluster_wait();
+            const uint32_t bar = smem_u32(&ctrl->sums), per = (rows + split - 1) / split;
+            const uint32_t to = smem_u32(sent) + (rank * per * 256 + set * 128 + q * 32 + lane) * 4;
 #pragma unroll
-        for (int i = 0; i < BT; ++i) part[i * 128] = acc[i];
+            for (int i = 0; i < BT; ++i)
+                if (i < rows) {
+                    const uint32_t who = i & (split - 1);
+                    send(mapa_shared(to + (i / split) * 1024, who), acc[i], mapa_shared(bar, who));
+                }
+            cluster_arrive();
+        } else {
+            // every MMA of the CTA is done (both sets have seen theirs): the stages' memory takes the sums [set][row][128]
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            float *part = reinterpret_cast<float *>(smem_raw + (base - raw)) + (size_t)set * BT * 128 + q * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < BT; ++i)
+                if (i < rows) part[i * 128] = acc[i];
+            if (!kSplit) asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
     }
     __syncwarp();
-    cluster_sync();
-    if (warp >= kSmallFold0) {
-        // join the cluster's partial sums, in rank order: a warp takes a row of the tile, a lane four columns
-        const int col = tc * 128 + 4 * (int)lane;
-        for (int i = (warp - kSmallFold0) * split + (int)rank; i < BT; i += 8 * split) {
-            const int64_t row = (int64_t)r0 + i;
-            if (row >= p.R) break;
-            const uint32_t at = base + (uint32_t)((i * 128 + 4 * lane) * 4);
-            float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f), u = a;
-#pragma unroll 8
-            for (int r = 0; r < split; ++r) {
-                const uint32_t from = mapa_shared(at, r);
-                a = plus(a, ld_cluster16(from));
-                u = plus(u, ld_cluster16(from + BT * 512));
+    if (kSend) {
+        if (warp < kSmallFold0) cluster_wait(), cluster_arrive();
+    } else if (kSplit) {
+        cluster_sync();
+    }
+    // join the sums, in rank order: a warp takes rows of the tile, a lane four columns
+    const float4 none = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (warp >= kSmallFold0 && kSend) {
+        if ((int)rank < rows && await(smem_u32(&ctrl->sums), 0, abort_flag, p)) {
+            for (int k = warp - kSmallFold0; k * split + (int)rank < rows; k += 8) {
+                const int64_t row = (int64_t)r0 + k * split + rank;
+                float4 a = none, u = none, add = none;
+                if (p.add && tc * 128 + 4 * (int)lane < p.C) add = load4(p, row, tc * 128 + 4 * (int)lane);
+                for (int r = 0; r < split; ++r) {
+                    const float *from = sent + (r * ((rows + split - 1) / split) + k) * 256 + 4 * lane;
+                    a = plus(a, *reinterpret_cast<const float4 *>(from));
+                    u = plus(u, *reinterpret_cast<const float4 *>(from + 128));
+                }
+                finish4<kGlu>(p, a, u, add, row, tc);
             }
-            if (kGlu) {
-                a.x = swiglu_of(a.x, u.x, p.clamp), a.y = swiglu_of(a.y, u.y, p.clamp);
-                a.z = swiglu_of(a.z, u.z, p.clamp), a.w = swiglu_of(a.w, u.w, p.clamp);
-                if (p.sf) {
-                    float amax = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w)));
+        }
+    } else if (warp >= kSmallFold0) {
+        constexpr int kTogether = BT >= 64 ? 4 : 1;   // rows on their way together
+        const int step = 8 * split;
+        for (int i0 = (warp - kSmallFold0) * split + (int)rank; i0 < rows; i0 += kTogether * step) {
+            float4 sum[kTogether][2], add[kTogether];
 #pragma unroll
-                    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-                    const GroupScale g = group_scale(amax);
-                    *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.out) + row * p.ld_out + col) =
-                        g.codes(a.x, a.y) | g.codes(a.z, a.w) << 16;
-                    if (lane == 0) p.sf[row * (p.C / 128) + tc] = g.sf;
-                    continue;
-                }
-            } else {
-                a = plus(a, u);
+            for (int k = 0; k < kTogether; ++k) {
+                sum[k][0] = sum[k][1] = add[k] = none;
+                if (p.add && tc * 128 + 4 * (int)lane < p.C && i0 + k * step < rows) add[k] = load4(p, (int64_t)r0 + i0 + k * step, tc * 128 + 4 * (int)lane);
             }
-            if (col >= p.C) continue;
-            if (p.f32) {
-                if (p.add) a = plus(a, *reinterpret_cast<const float4 *>(static_cast<const float *>(p.add) + row * p.ld_add + col));
-                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * p.ld_out + col) = a;
-            } else {
-                if (p.add) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const bf16 *>(p.add) + row * p.ld_add + col);
-                    a = plus(a, make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u)));
+            for (int r = 0; r < split; ++r) {
+                float4 v[kTogether][2];
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) {
+                    const uint32_t at = base + (uint32_t)((min(i0 + k * step, BT - 1) * 128 + 4 * lane) * 4);   // a row past the last is not stored
+                    const uint32_t from = kSplit ? mapa_shared(at, r) : at;
+                    v[k][0] = ld_cluster16(from);
+                    v[k][1] = ld_cluster16(from + BT * 512);
                 }
-                *reinterpret_cast<uint2 *>(static_cast<bf16 *>(p.out) + row * p.ld_out + col) =
-                    make_uint2(bf16x2(a.x, a.y), bf16x2(a.z, a.w));
+#pragma unroll
+                for (int k = 0; k < kTogether; ++k) sum[k][0] = plus(sum[k][0], v[k][0]), sum[k][1] = plus(sum[k][1], v[k][1]);
             }
+#pragma unroll
+            for (int k = 0; k < kTogether; ++k)
+                if (i0 + k * step < rows) finish4<kGlu>(p, sum[k][0], sum[k][1], add[k], (int64_t)r0 + i0 + k * step, tc);
         }
     }
     __syncwarp();
     tc_fence_before();
-    cluster_sync();   // no CTA leaves while another reads its partial sums
+    // no CTA leaves while another sends to it or reads from it
+    if (kSend) {
+        cluster_wait();
+        __syncthreads();
+    } else if (kSplit) {
+        cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmem);
@@ -854,13 +943,22 @@ cudaError_t launch_wide(const CUtensorMap &rows, const CUtensorMap &cols, const 
                   rows, cols, p);
 }
 
+template <int kMode, int BT, bool kSplit>
+cudaError_t launch_small(const CUtensorMap &rows, const CUtensorMap &cols, Fp8Params p, cudaStream_t s) {
+    static std::atomic<uint32_t> smem_set{0};
+    constexpr size_t kFixed = 1024 + sizeof(SmallCtrl<kMode, BT>), kStage = small_stage<kMode, BT>(), kRoom = BT == 16 ? kSmHalf : kSmAll;
+    constexpr size_t kSent = small_sends<BT, kSplit>() ? sent_bytes(BT, 8) : 0;
+    static_assert(kFixed + kSent + 2 * kStage <= kRoom, "shared memory");
+    cudaError_t e = smem_limit_once(reinterpret_cast<const void *>(fp8_small_kernel<kMode, BT, kSplit>), kRoom, smem_set);
+    if (e != cudaSuccess) return e;
+    const size_t sent = kSent ? sent_bytes(std::min(p.R, BT), p.split) : 0;
+    p.stages = (int)std::min<size_t>(kMaxStages, (kRoom - kFixed - sent) / kStage);
+    return launch(fp8_small_kernel<kMode, BT, kSplit>, (unsigned)(p.tiles_r * p.tiles_c * p.split), kSmallThreads,
+                  kFixed + p.stages * kStage + sent, p.split, s, rows, cols, p);
+}
 template <int kMode, int BT>
 cudaError_t launch_small(const CUtensorMap &rows, const CUtensorMap &cols, const Fp8Params &p, cudaStream_t s) {
-    static std::atomic<uint32_t> smem_set{0};
-    cudaError_t e = smem_limit_once(reinterpret_cast<const void *>(fp8_small_kernel<kMode, BT>), small_smem<kMode, BT>(), smem_set);
-    if (e != cudaSuccess) return e;
-    return launch(fp8_small_kernel<kMode, BT>, (unsigned)(p.tiles_r * p.tiles_c * p.split), kSmallThreads, small_smem<kMode, BT>(),
-                  p.split, s, rows, cols, p);
+    return p.split > 1 ? launch_small<kMode, BT, true>(rows, cols, p, s) : launch_small<kMode, BT, false>(rows, cols, p, s);
 }
 
 // rows [R x D] and cols [C' x D] codes; *_ld: pitch of the matrix as stored.
@@ -891,8 +989,9 @@ int run(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_co
         p.tiles_r = up_to(p.R, bt);
         p.tiles_c = up_to(p.C, 128);
         const int stages = kMode == kSwiglu ? p.DB : (p.DB + 1) / 2;
-        const int64_t room = (int64_t)sms * (bt == 16 ? 2 : 1) / ((int64_t)p.tiles_r * p.tiles_c);
-        p.split = (int)std::max<int64_t>(1, std::min<int64_t>({room, 8, std::max(1, stages / 2)}));
+        // a power of two of CTAs to a tile, as many as there are SMs for, each with two stages at least
+        p.split = 1;
+        while (p.split < 8 && (int64_t)p.tiles_r * p.tiles_c * p.split * 2 <= sms && stages >= 4 * p.split) p.split *= 2;
         if constexpr (kMode == kWeight)
             e = launch_small<kMode, 128>(mr, mc, p, s);
         else
@@ -921,6 +1020,7 @@ int moe_fp8_linear_forward(const moe_fp8_linear_config *cfg, int num_tokens, con
                            void *stream) {
     if (!valid(cfg) || num_tokens < 0) return MOE_ERR_INVALID_ARG;
     const bool glu = cfg->act == MOE_ACT_SWIGLU, quant = cfg->quant != MOE_QUANT_NONE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (num_tokens == 0) return MOE_OK;
     if (quant ? !y_sf || add : y_sf != nullptr) return MOE_ERR_INVALID_ARG;
     const int64_t K = cfg->in_features, N = cfg->out_features, n = glu ? N / 2 : N;
@@ -936,7 +1036,6 @@ int moe_fp8_linear_forward(const moe_fp8_linear_config *cfg, int num_tokens, con
     p.R = num_tokens, p.C = (int)n, p.f32 = cfg->out_dtype == MOE_DTYPE_F32, p.clamp = cfg->act_clamp;
     p.wide = wide_pieces(p);
     const uint8_t *a = static_cast<const uint8_t *>(x), *b = static_cast<const uint8_t *>(w);
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
     return glu ? run<kSwiglu>(a, ld_x, b, K, K, p, s) : run<kForward>(a, ld_x, b, K, K, p, s);
 }
 
