@@ -961,7 +961,64 @@ cudaError_t launch_small(const CUtensorMap &rows, const CUtensorMap &cols, const
     return p.split > 1 ? launch_small<kMode, BT, true>(rows, cols, p, s) : launch_small<kMode, BT, false>(rows, cols, p, s);
 }
 
-// rows [R x D] and cols [C' x D] codes; *_ld: pitch of the matrix as stored.
+// Clusters of `split` CTAs, one an SM, that the device holds at once.
+int resident_clusters(int dev, int split) {
+    static std::atomic<int> known[32][4];
+    if (split == 1) return sm_count(dev);
+    std::atomic<int> &slot = known[dev][split == 2 ? 1 : split == 4 ? 2 : 3];
+    int n = slot.load(std::memory_order_acquire);
+    if (!n) {
+        static std::atomic<uint32_t> smem_set{0};
+        const auto kernel = fp8_small_kernel<kForward, 64, true>;
+        if (smem_limit_once(reinterpret_cast<const void *>(kernel), kSmAll, smem_set) != cudaSuccess) return 0;
+        cudaLaunchConfig_t c = {};
+        cudaLaunchAttribute a[1];
+        a[0].id = cudaLaunchAttributeClusterDimension;
+        a[0].val.clusterDim.x = split, a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+        c.gridDim = dim3(sm_count(dev) / split * split);
+        c.blockDim = dim3(kSmallThreads);
+        c.dynamicSmemBytes = kSmAll;
+        c.attrs = a, c.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess || n < 1) return 0;
+        slot.store(n, std::memory_order_release);
+    }
+    return n;
+}
+
+// Which kernel, and how: rows of a tile (0: the wide kernel) and CTAs to a tile, by what they are estimated to take, in ns, from
+// what was measured: a panel of 128 x 128 weights with 32 rows 200, with 64 245 (each wave of CTAs 2000 more, joining a cluster's
+// sums 1300 and 50 a row); of a weight's gradient 500; a block of a wide tile 430, of a weight's gradient 600 (each wave of
+// CTA pairs 2500, the launch 1500).  Sides of it: 128 x 7168 x 2048 11.8 us wide, 8.5 in 64s; 129 rows 13.0 wide, 14.5 in 64s;
+// 512 x 576 x 7168 25.7 wide, 16.4 in 64s, 14.2 with two CTAs to a tile; 999 x 2064 x 4176 25 us in 128s, 19 wide.
+struct Plan {
+    int bt, split;
+};
+Plan plan_for(int mode, int64_t R, int64_t C, int DB, int sms, int dev) {
+    const int panels = mode == kSwiglu ? 2 * DB : DB, stages = (panels + 1) / 2;
+    const int64_t cols = up_to(C, 128);
+    if (mode != kWeight && R <= 16) {   // two CTAs an SM; as many to a tile as fill the SMs once, the next call's beside them
+        int split = 1;
+        while (split < 8 && cols * split * 2 <= sms && stages >= 4 * split) split *= 2;
+        return {16, split};
+    }
+    const int64_t pairs = sms / 2, tiles = up_to(R, 256) * (int64_t)up_to(C, mode == kSwiglu ? 128 : 256);
+    int64_t best = (tiles + pairs - 1) / pairs * (DB * (mode == kWeight ? 600 : 430) + 2500) + 1500;
+    Plan plan{0, 1};
+    for (int bt = mode == kWeight ? 128 : 32; bt <= (mode == kWeight ? 128 : 64); bt *= 2) {
+        const int64_t each = mode == kWeight ? 500 : bt == 32 ? 200 : 245, n = up_to(R, bt) * cols;
+        for (int split = 1; split <= (mode == kWeight ? 4 : 8); split *= 2) {
+            if (split > 1 && stages < 2 * split) break;
+            const int64_t room = resident_clusters(dev, split);
+            if (!room || (split > 1 && n > room)) break;
+            const int64_t cost = (n + room - 1) / room * ((panels + split - 1) / split * each + 2000) +
+                                 (split > 1 ? 1300 + 50 * std::min<int64_t>(R, bt) : 0);
+            if (cost < best) best = cost, plan = {bt, split};
+        }
+    }
+    return plan;
+}
+
+// rows [R x D] and cols [C' x D] codes; ld: pitch of the matrix as stored.
 template <int kMode>
 int run(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_cols, int64_t D, Fp8Params p, cudaStream_t s) {
     const int dev = this_device();
@@ -970,35 +1027,27 @@ int run(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_co
     p.DB = up_to(D, 128);
     p.wait_us = armed_us.exchange(0, std::memory_order_relaxed);
     const int wt = kMode == kSwiglu ? 2 * p.C : p.C;   // rows of W
-    p.tiles_r = up_to(p.R, 256);
-    p.tiles_c = up_to(p.C, kMode == kSwiglu ? 128 : 256);
-    int bt = 0;
-    if (p.R <= 16 && kMode != kWeight) bt = 16;
-    else if (p.R <= 32 && kMode != kWeight) bt = 32;
-    else if (p.R <= 64 && kMode != kWeight) bt = 64;
-    else if ((int64_t)p.tiles_r * p.tiles_c < sms / 4) bt = 128;
+    const Plan plan = plan_for(kMode, p.R, p.C, p.DB, sms, dev);
+    const uint32_t box = plan.bt ? plan.bt : 128;
     CUtensorMap mr, mc;
-    const uint32_t box = bt ? bt : 128;
     if (!(rows_mn(kMode) ? encode_map(&mr, rows, p.R, D, ld_rows, 128, 128) : encode_map(&mr, rows, D, p.R, ld_rows, 128, box)) ||
         !(cols_mn(kMode) ? encode_map(&mc, cols, wt, D, ld_cols, 128, 128) : encode_map(&mc, cols, D, wt, ld_cols, 128, 128)))
         return MOE_ERR_CUDA;
     cudaError_t e;
-    if (!bt) {
+    if (!plan.bt) {
+        p.tiles_r = up_to(p.R, 256);
+        p.tiles_c = up_to(p.C, kMode == kSwiglu ? 128 : 256);
         e = launch_wide<kMode>(mr, mc, p, dev, s);
     } else {
-        p.tiles_r = up_to(p.R, bt);
+        p.tiles_r = up_to(p.R, plan.bt);
         p.tiles_c = up_to(p.C, 128);
-        const int stages = kMode == kSwiglu ? p.DB : (p.DB + 1) / 2;
-        // a power of two of CTAs to a tile, as many as there are SMs for, each with two stages at least
-        p.split = 1;
-        while (p.split < 8 && (int64_t)p.tiles_r * p.tiles_c * p.split * 2 <= sms && stages >= 4 * p.split) p.split *= 2;
+        p.split = plan.split;
         if constexpr (kMode == kWeight)
             e = launch_small<kMode, 128>(mr, mc, p, s);
         else
-            e = bt == 16   ? launch_small<kMode, 16>(mr, mc, p, s)
-                : bt == 32 ? launch_small<kMode, 32>(mr, mc, p, s)
-                : bt == 64 ? launch_small<kMode, 64>(mr, mc, p, s)
-                           : launch_small<kMode, 128>(mr, mc, p, s);
+            e = plan.bt == 16   ? launch_small<kMode, 16>(mr, mc, p, s)
+                : plan.bt == 32 ? launch_small<kMode, 32>(mr, mc, p, s)
+                                : launch_small<kMode, 64>(mr, mc, p, s);
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
