@@ -207,9 +207,14 @@ struct GroupScale {
     __device__ __forceinline__ uint32_t codes(float a, float b) const { return e4m3x2(a * up * inv, b * up * inv); }
 };
 __device__ __forceinline__ GroupScale group_scale(float amax) {
-    GroupScale g{amax / 448.0f, 0.0f, 1.0f};
-    if (amax > 0.0f && amax < 0x1p-100f) g.up = 0x1p64f;
-    g.inv = amax > 0.0f ? __frcp_rn(g.sf * g.up) : 1.0f;
+    // the rounded quotient by fp8_scale's correction, by division where that is not exact (and for zeros, which need no care then)
+    const float near = amax * (1.0f / 448.0f);
+    GroupScale g{fmaf(fminf(fmaf(-448.0f, near, amax), FLT_MAX), 1.0f / 448.0f, near), 1.0f, 1.0f};
+    if (amax < 0x1p-100f) {
+        g.sf = amax / 448.0f;
+        g.up = amax > 0.0f ? 0x1p64f : 1.0f;
+    }
+    if (amax > 0.0f) g.inv = __frcp_rn(g.sf * g.up);
     return g;
 }
 
