@@ -1,0 +1,39 @@
+// moe_router_groups.cu -- routing limited to groups of experts (definitions in include/moe.h), by the router's kernel
+// (moe_router.cuh): a group has registers of its own, so its score is a reduction or two over the lanes.
+#include "moe_router.cuh"
+
+namespace moe {
+namespace {
+
+// The same for groups of experts, whose registers are their own: eight lanes have a token where no more than eight registers
+// hold it so, else 32.
+struct RunGrouped {
+    const RouterParams &p;
+    bool bf, loss;
+    int ctas;
+    cudaStream_t s;
+    template <class L, int NI, int G, int kOne>
+    cudaError_t run() const {
+        constexpr int kFew = G == 32 && NI > 4 ? 4 : NI;
+        if (loss) return launch(router_kernel<L, NI, G, kFew, true, false, kOne>, ctas, kThreads, (size_t)(kWarps + 1) * p.E * 4, 1, s, p);
+        return launch(router_kernel<L, NI, G, kFew, false, false, kOne>, ctas, kThreads, 0, 1, s, p);
+    }
+    template <int NI, int G>
+    cudaError_t run() const {
+        if (NI > 2 && p.each == 1) return bf ? run<bf16, NI, G, 2>() : run<float, NI, G, 2>();
+        return bf ? run<bf16, NI, G, 1>() : run<float, NI, G, 1>();
+    }
+    cudaError_t run() const {
+        const int n = p.groups * p.each;
+        if (p.each * 8 >= p.group_size && n <= 8) return n <= 2 ? run<2, 8>() : n <= 4 ? run<4, 8>() : run<8, 8>();
+        return n <= 2 ? run<2, 32>() : n <= 4 ? run<4, 32>() : n <= 8 ? run<8, 32>() : n <= 16 ? run<16, 32>() : run<32, 32>();
+    }
+};
+
+}  // namespace
+
+cudaError_t launch_router_groups(const RouterParams &p, bool bf, bool loss, int ctas, cudaStream_t s) {
+    return RunGrouped{p, bf, loss, ctas, s}.run();
+}
+
+}  // namespace moe
