@@ -529,6 +529,9 @@ template <int BT>
 constexpr int small_bufs() { return BT <= 64 ? 4 : 2; }
 template <int kMode, int BT>
 constexpr uint32_t small_stage() { return 2 * kPanel + (kMode == kSwiglu ? 1 : 2) * BT * 128; }
+// The next call's CTAs come while this one's still start, so CTAs of both that an SM's shared memory holds must find TMEM there
+// together, or each waits for the other: beside a tile of 16 rows, which has a quarter, is room for nothing larger.
+static_assert(2 * small_stage<kSwiglu, 16>() + std::min<size_t>(wide_smem<kForward>(), 5 * small_stage<kSwiglu, 32>()) > kSmAll, "TMEM");
 // Whether the cluster's CTAs send one another their sums; those of 128 rows have no room but the stages', and are fetched.
 template <int BT, bool kSplit>
 constexpr bool small_sends() { return kSplit && BT <= 64; }
@@ -796,6 +799,7 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
         }
         if (kSend) {
             // row i's sums to the CTA that joins it: i % split, where it is row i / split
+            __syncwarp();
             cluster_wait();
             const uint32_t bar = smem_u32(&ctrl->sums), per = (rows + split - 1) / split;
             const uint32_t to = smem_u32(sent) + (rank * per * 256 + set * 128 + q * 32 + lane) * 4;
@@ -902,6 +906,10 @@ bool valid(const moe_fp8_linear_config *c) {
 bool rows_ok(const void *p, int64_t ld, int64_t cols, size_t es) {
     return p && aligned_to(p, 16) && ld >= cols && ld * (int64_t)es % 16 == 0;
 }
+// An added matrix: absent, apart from the output, or the output itself, row by row.
+bool add_ok(const void *add, int64_t ld, const void *out, int64_t ld_out, int64_t rows, int64_t cols, size_t es) {
+    return !add || (rows_ok(add, ld, cols, es) && (add != out || ld == ld_out || rows == 1));
+}
 
 int this_device() {
     int d = -1;
@@ -994,15 +1002,14 @@ struct Plan {
     int bt, split;
 };
 Plan plan_for(int mode, int64_t R, int64_t C, int DB, int sms, int dev) {
-    const int panels = mode == kSwiglu ? 2 * DB : DB, stages = (panels + 1) / 2;
-    const int64_t cols = up_to(C, 128);
+    const int64_t panels = mode == kSwiglu ? 2 * (int64_t)DB : DB, stages = (panels + 1) / 2, cols = up_to(C, 128);
     if (mode != kWeight && R <= 16) {   // two CTAs an SM; as many to a tile as fill the SMs once, the next call's beside them
         int split = 1;
         while (split < 8 && cols * split * 2 <= sms && stages >= 4 * split) split *= 2;
         return {16, split};
     }
     const int64_t pairs = sms / 2, tiles = up_to(R, 256) * (int64_t)up_to(C, mode == kSwiglu ? 128 : 256);
-    int64_t best = (tiles + pairs - 1) / pairs * (DB * (mode == kWeight ? 600 : 430) + 2500) + 1500;
+    int64_t best = (tiles + pairs - 1) / pairs * ((int64_t)DB * (mode == kWeight ? 600 : 430) + 2500) + 1500;
     Plan plan{0, 1};
     for (int bt = mode == kWeight ? 128 : 32; bt <= (mode == kWeight ? 128 : 64); bt *= 2) {
         const int64_t each = mode == kWeight ? 500 : bt == 32 ? 200 : 245, n = up_to(R, bt) * cols;
@@ -1074,7 +1081,7 @@ int moe_fp8_linear_forward(const moe_fp8_linear_config *cfg, int num_tokens, con
     if (quant ? !y_sf || add : y_sf != nullptr) return MOE_ERR_INVALID_ARG;
     const int64_t K = cfg->in_features, N = cfg->out_features, n = glu ? N / 2 : N;
     const size_t es = quant ? 1 : dtype_bytes(cfg->out_dtype);
-    if (!rows_ok(x, ld_x, K, 1) || !rows_ok(w, K, K, 1) || !rows_ok(y, ld_y, n, es) || (add && !rows_ok(add, ld_add, n, es)))
+    if (!rows_ok(x, ld_x, K, 1) || !rows_ok(w, K, K, 1) || !rows_ok(y, ld_y, n, es) || !add_ok(add, ld_add, y, ld_y, num_tokens, n, es))
         return MOE_ERR_INVALID_ARG;
     if (!x_sf || !w_sf || !aligned_to(x_sf, 4) || !aligned_to(w_sf, 4) || !aligned_to(y_sf, 4)) return MOE_ERR_INVALID_ARG;
     Fp8Params p{};
@@ -1095,7 +1102,7 @@ int moe_fp8_linear_backward_input(const moe_fp8_linear_config *cfg, int num_toke
     if (num_tokens == 0) return MOE_OK;
     const int64_t K = cfg->in_features, N = cfg->out_features;
     const size_t es = dtype_bytes(cfg->out_dtype);
-    if (!rows_ok(dy, ld_dy, N, 1) || !rows_ok(w, K, K, 1) || !rows_ok(dx, ld_dx, K, es) || (add && !rows_ok(add, ld_add, K, es)))
+    if (!rows_ok(dy, ld_dy, N, 1) || !rows_ok(w, K, K, 1) || !rows_ok(dx, ld_dx, K, es) || !add_ok(add, ld_add, dx, ld_dx, num_tokens, K, es))
         return MOE_ERR_INVALID_ARG;
     if (!dy_sf || !w_sf || !aligned_to(dy_sf, 4) || !aligned_to(w_sf, 4)) return MOE_ERR_INVALID_ARG;
     Fp8Params p{};
@@ -1115,7 +1122,7 @@ int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int num_tok
     if (!valid(cfg) || num_tokens < 0) return MOE_ERR_INVALID_ARG;
     const int64_t K = cfg->in_features, N = cfg->out_features;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!rows_ok(dw, ld_dw, K, 4) || (add && !rows_ok(add, ld_add, K, 4))) return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(dw, ld_dw, K, 4) || !add_ok(add, ld_add, dw, ld_dw, N, K, 4)) return MOE_ERR_INVALID_ARG;
     if (num_tokens == 0) {   // nothing is summed
         const cudaError_t e = !add       ? cudaMemset2DAsync(dw, ld_dw * 4, 0, K * 4, N, s)
                               : add != dw ? cudaMemcpy2DAsync(dw, ld_dw * 4, add, ld_add * 4, K * 4, N, cudaMemcpyDeviceToDevice, s)
