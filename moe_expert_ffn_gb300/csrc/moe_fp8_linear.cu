@@ -42,7 +42,7 @@ struct Fp8Params {
     int R, C, DB;                 // rows and columns of the output, blocks of the contracted axis
     int tiles_r, tiles_c, split, stages;
     int f32;
-    int wide;                     // out and add in 32-byte pieces
+    int out_stages;               // stages that a wide tile's output passes through, 0: written directly (codes)
     int wait_us;                  // 0, or (a test of the timeout) the limit of every wait, with CTA 0's first copies withheld
     float clamp;
 };
@@ -95,59 +95,6 @@ __device__ __forceinline__ float swiglu_of(float g, float u, float c) {
     return g * sigmoid_of(g) * clamp_of(u, c);
 }
 
-__device__ __forceinline__ void store_once(void *p, const uint32_t (&v)[8], bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-                     "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                     : "memory");
-    } else {
-        static_cast<uint4 *>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-        static_cast<uint4 *>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    }
-}
-__device__ __forceinline__ void load_once(const void *p, uint32_t (&v)[8], bool wide) {
-    if (wide) {
-        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                     : "l"(p)
-                     : "memory");
-    } else {
-        const uint4 a = static_cast<const uint4 *>(p)[0], b = static_cast<const uint4 *>(p)[1];
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-}
-// 16 consecutive outputs of a row: out = v (+ add).  (With more of add asked for at once the fold loop's registers are laid out
-// worse: 32 columns at a time 207 us for the listed weight gradient, 16 174.)
-__device__ __forceinline__ void put16(const Fp8Params &p, float (&v)[16], int64_t row, int col) {
-    uint32_t w[8], x[8];
-    if (p.f32) {
-        if (p.add) {
-            const float *add = static_cast<const float *>(p.add) + row * p.ld_add + col;
-            load_once(add, w, p.wide);
-            load_once(add + 8, x, p.wide);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += __uint_as_float(w[i]), v[8 + i] += __uint_as_float(x[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]), x[i] = __float_as_uint(v[8 + i]);
-        float *out = static_cast<float *>(p.out) + row * p.ld_out + col;
-        store_once(out, w, p.wide);
-        store_once(out + 8, x, p.wide);
-        return;
-    }
-    if (p.add) {
-        load_once(static_cast<const bf16 *>(p.add) + row * p.ld_add + col, w, p.wide);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[2 * i] += __uint_as_float(w[i] << 16);
-            v[2 * i + 1] += __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
-    store_once(static_cast<bf16 *>(p.out) + row * p.ld_out + col, w, p.wide);
-}
-
 // ============================================================================
 // Many rows: 256 x 256 tiles on CTA pairs
 // ============================================================================
@@ -167,8 +114,12 @@ struct alignas(8) WideCtrl {
     uint64_t full[kWideStages], empty[kWideStages];
     uint64_t tfull[2], tempty[2];
     uint64_t sfull[2], sempty[2];
+    // a stage is the output's (with what is added to it), and holds it; of four tiles in turn, because the three stages may all be
+    // granted before the first is written
+    uint64_t granted[4][2], written[4][2];
     uint64_t halves[4];              // a row's two fold warps have written their maxima
     uint32_t tmem_base;
+    uint32_t where[4][2];            // the granted stage's address (the fold warps have no register for what says it)
     int abort;
     float amax[2][kFoldWarps][32];
 };
@@ -219,15 +170,48 @@ __device__ __forceinline__ void fold_wide(float2 (&acc)[64], uint32_t t0, uint32
     }
 }
 
-// Brings a tile's part of add to L2 while the tile is computed: 128 rows from r0, `cols` columns from c0.
-__device__ __forceinline__ void ask_for_add(const Fp8Params &p, int r0, int c0, int cols) {
-    const int lane = threadIdx.x & 31, es = p.f32 ? 4 : 2;
-    const int bytes = min(cols, p.C - c0) * es;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t row = (int64_t)r0 + lane + 32 * i;
-        if (row >= p.R) break;
-        const char *from = static_cast<const char *>(p.add) + (row * p.ld_add + c0) * es;
-        for (int o = 0; o < bytes; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + o));
+// A tile's output, as 128 rows of 128 bytes ("panels", 128-byte swizzled): its first byte in a row, and how many panels there are.
+struct OutTile {
+    int x, panels;
+};
+template <int kMode>
+__device__ __forceinline__ OutTile out_tile(const Fp8Params &p, int tc) {
+    const int es = p.f32 ? 4 : 2, width = (kMode == kSwiglu ? 128 : 256) * es;
+    return {tc * width, min(width, p.C * es - tc * width + 127) / 128};
+}
+
+// A thread's outputs to its row of the panels from `panel` on, added to what is there with `add`.
+template <int kPairs>
+__device__ __forceinline__ void put_row(const float2 (&acc)[64], uint32_t panel, int row, bool f32, bool add) {
+    const uint32_t at = panel + row * 128, swz = row & 7;
+    if (f32) {
+#pragma unroll
+        for (int k = 0; k < kPairs / 2; ++k) {
+            const uint32_t a = at + (k / 8) * kPanel + (((k & 7) ^ swz) << 4);
+            float4 v = make_float4(acc[2 * k].x, acc[2 * k].y, acc[2 * k + 1].x, acc[2 * k + 1].y);
+            if (add) {
+                const uint4 w = ld_shared16(a);
+                v.x += __uint_as_float(w.x), v.y += __uint_as_float(w.y), v.z += __uint_as_float(w.z), v.w += __uint_as_float(w.w);
+            }
+            st_shared_v4(a, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kPairs / 4; ++k) {
+        const uint32_t a = at + (k / 8) * kPanel + (((k & 7) ^ swz) << 4);
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (add) {
+            const uint4 u = ld_shared16(a);
+            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 v = acc[4 * k + i];
+            if (add) v.x += __uint_as_float(w[i] << 16), v.y += __uint_as_float(w[i] & 0xFFFF0000u);
+            w[i] = bf16x2(v.x, v.y);
+        }
+        st_shared_v4(a, w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -248,7 +232,7 @@ __device__ __forceinline__ void arrive_when_copied(uint32_t bar) {
 template <int kMode>
 __global__ void __launch_bounds__(kWideThreads, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_cols,
-                    const __grid_constant__ Fp8Params p) {
+                    const __grid_constant__ CUtensorMap tm_add, const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Fp8Params p) {
     extern __shared__ uint8_t smem_raw[];
     launch_next();
     const uint32_t raw = smem_u32(smem_raw), base = align1024(raw);
@@ -274,6 +258,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             mbar_init(smem_u32(&ctrl->sfull[b]), kMode == kWeight ? 32 : 1);
             mbar_init(smem_u32(&ctrl->sempty[b]), kFoldWarps);
         }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(smem_u32(&ctrl->granted[i >> 1][i & 1]), 1);
+            mbar_init(smem_u32(&ctrl->written[i >> 1][i & 1]), p.out_stages == 2 ? kFoldWarps / 2 : kFoldWarps);
+        }
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&ctrl->halves[i]), 2);
         ctrl->abort = 0;
         fence_mbar_init();
@@ -295,9 +283,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         if (warp == 0) {
             // ---- copies: each CTA its 128 rows and its half of the columns (SwiGLU: gate rows of W in the even CTA, up rows in the odd)
             const uint64_t pol = policy_evict_normal();
-            int it = 0;
+            int it = 0, done = 0;
             bool ok = true;
-            for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
+            for (int64_t tile = cluster; ok && tile < total; tile += clusters, ++done) {
                 const WideTile t = wide_tile(tile, p);
                 const int r0 = t.tr * 256 + (int)rank * 128;
                 const int c0 = kMode == kSwiglu ? t.tc * 128 + (int)rank * p.C : t.tc * 256 + (int)rank * 128;
@@ -320,6 +308,24 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     }
                     __syncwarp();
                 }
+                for (int e = 0; ok && e < p.out_stages; ++e, ++it) {   // and the stages of its output
+                    const int s = it % kWideStages;
+                    if (!await(smem_u32(&ctrl->empty[s]), ((it / kWideStages) & 1) ^ 1, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        const OutTile o = out_tile<kMode>(p, t.tc);
+                        const int n = p.add ? min(4, o.panels - 4 * e) : 0;
+                        const uint32_t granted = smem_u32(&ctrl->granted[done & 3][e]);
+                        ctrl->where[done & 3][e] = base + s * kWideStage;
+                        if (n > 0) mbar_arrive_expect_tx(granted, (uint32_t)n * kPanel);
+                        else mbar_arrive(granted);
+                        for (int i = 0; i < n; ++i)
+                            tma_load_2d(base + s * kWideStage + i * kPanel, &tm_add, o.x + (4 * e + i) * 128, r0, granted, pol);
+                    }
+                    __syncwarp();
+                }
             }
             for (int i = max(0, it - kWideStages); i < it; ++i)   // the last copies land before the pair ends
                 await_end(smem_u32(&ctrl->empty[i % kWideStages]), (i / kWideStages) & 1, p);
@@ -328,16 +334,18 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (rank == 0 && lane == 0) {
                 constexpr uint32_t idesc = idesc_e4m3_f32(256, 256) | idesc_major(rows_mn(kMode), cols_mn(kMode));
                 const uint64_t a0 = operand_desc<rows_mn(kMode)>(base), w0 = operand_desc<cols_mn(kMode)>(base + 2 * kPanel);
-                int s = 0, it = 0;
-                uint32_t ph = 0, tph[2] = {1, 1};
+                int it = 0, last = -1;
+                uint32_t ph = 0, tph[2] = {1, 1};   // ph: of each stage
                 bool ok = true;
-                for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
+                for (int64_t tile = cluster; ok && tile < total; tile += clusters, it += p.out_stages) {
+                    int s = it % kWideStages;
                     for (int ks = 0; ok && ks < stages; ++ks, ++it) {
                         const int n = min(2, DB - 2 * ks);
-                        if (!await(smem_u32(&ctrl->full[s]), ph, abort_flag, p)) {
+                        if (!await(smem_u32(&ctrl->full[s]), (ph >> s) & 1, abort_flag, p)) {
                             ok = false;
                             break;
                         }
+                        ph ^= 1u << s;
                         const uint64_t a = a0 + s * (kWideStage / 16), w = w0 + s * (kWideStage / 16);
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -355,10 +363,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                             umma_pair_commit(smem_u32(&ctrl->tfull[j]), 3);
                         }
                         if (ok) umma_pair_commit(smem_u32(&ctrl->empty[s]), 3);
-                        if (++s == kWideStages) s = 0, ph ^= 1;
+                        last = it;
+                        if (++s == kWideStages) s = 0;
                     }
                 }
-                if (it > 0) await_end(smem_u32(&ctrl->empty[(it - 1) % kWideStages]), ((it - 1) / kWideStages) & 1, p);
+                if (last >= 0) await_end(smem_u32(&ctrl->empty[last % kWideStages]), (last / kWideStages) & 1, p);
             }
         } else if (warp == 2) {
             // ---- scales of eight blocks at a time to shared memory
@@ -367,7 +376,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             for (int64_t tile = cluster; ok && tile < total; tile += clusters) {
                 const WideTile t = wide_tile(tile, p);
                 const int r0 = t.tr * 256 + (int)rank * 128;
-                if (p.add) ask_for_add(p, r0, t.tc * (kMode == kSwiglu ? 128 : 256), kMode == kSwiglu ? 128 : 256);
                 for (int k0 = 0; k0 < DB; k0 += kChunk, ++ch) {
                     const int slot = ch & 1;
                     if (!await(smem_u32(&ctrl->sempty[slot]), ((ch >> 1) & 1) ^ 1, abort_flag, p)) {
@@ -403,6 +411,33 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     }
                 }
             }
+        } else if (p.out_stages && lane == 0) {
+            // ---- stores: the output's stages as the fold warps have written them, given back when they are read
+            int it = stages, done = 0;
+            bool ok = true;
+            for (int64_t tile = cluster; ok && tile < total; tile += clusters, it += stages + p.out_stages, ++done) {
+                const WideTile t = wide_tile(tile, p);
+                const int r0 = t.tr * 256 + (int)rank * 128;
+                const OutTile o = out_tile<kMode>(p, t.tc);
+                for (int e = 0; e < p.out_stages; ++e) {
+                    const int s = (it + e) % kWideStages;
+                    if (!await(smem_u32(&ctrl->written[done & 3][e]), (done >> 2) & 1, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    for (int i = 4 * e; r0 < p.R && i < min(4 * e + 4, o.panels); ++i)
+                        tma_store_2d(&tm_out, o.x + i * 128, r0, base + s * kWideStage + (i - 4 * e) * kPanel);
+                    tma_store_commit();
+                }
+                if (!ok) break;
+                if (p.out_stages == 2) {
+                    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    mbar_arrive(smem_u32(&ctrl->empty[it % kWideStages]));
+                }
+                tma_store_wait_read();
+                mbar_arrive(smem_u32(&ctrl->empty[(it + p.out_stages - 1) % kWideStages]));
+            }
+            tma_store_wait_all();
         }
     } else {
         // ---- fold the blocks' accumulators, own 128 rows; warp: 32 rows, half of the columns
@@ -484,25 +519,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         for (int i = 0; i < 4; ++i) to[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                         if (h == 0) p.sf[row * (p.C / 128) + t.tc] = g.sf;
                     }
-                } else if (row < p.R) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[16];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[2 * i] = acc[8 * c + i].x, v[2 * i + 1] = acc[8 * c + i].y;
-                        put16(p, v, row, col + 16 * c);
-                    }
-                }
-            } else if (row < p.R) {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const int col = t.tc * 256 + h * 128 + 16 * c;
-                    float v[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[2 * i] = acc[8 * c + i].x, v[2 * i + 1] = acc[8 * c + i].y;
-                    if (col < p.C) put16(p, v, row, col);
+                    continue;
                 }
             }
+            // through a stage of the ring and a copy from there: the stores, all CTAs' at once, do not hold up the next tile
+            const int e = kMode != kSwiglu && p.out_stages == 2 ? h : 0;
+            if (!await(smem_u32(&ctrl->granted[done & 3][e]), (done >> 2) & 1, abort_flag, p)) break;
+            const uint32_t stage = ctrl->where[done & 3][e];
+            const bool f32 = kMode == kWeight || p.f32;
+            const int before = kMode == kSwiglu ? (f32 ? 2 : 1) : f32 ? 0 : 2;   // panels of the other half before this one's
+            put_row<kMode == kSwiglu ? 32 : 64>(acc, stage + h * before * kPanel, lrow, f32, p.add != nullptr);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctrl->written[done & 3][e]));
         }
     }
     __syncwarp();
@@ -926,7 +955,7 @@ int sm_count(int dev) {
 }
 
 template <int kMode>
-cudaError_t launch_wide(const CUtensorMap &rows, const CUtensorMap &cols, const Fp8Params &p, int dev, cudaStream_t s) {
+cudaError_t launch_wide(const CUtensorMap &rows, const CUtensorMap &cols, const CUtensorMap &add, const CUtensorMap &out, const Fp8Params &p, int dev, cudaStream_t s) {
     static std::atomic<int> resident[32];   // CTA pairs that the device holds at once
     static std::atomic<uint32_t> smem_set{0};
     cudaError_t e = smem_limit_once(reinterpret_cast<const void *>(fp8_wide_kernel<kMode>), wide_smem<kMode>(), smem_set);
@@ -948,7 +977,7 @@ cudaError_t launch_wide(const CUtensorMap &rows, const CUtensorMap &cols, const 
     }
     const int64_t tiles = (int64_t)p.tiles_r * p.tiles_c;
     return launch(fp8_wide_kernel<kMode>, 2u * (unsigned)std::min<int64_t>(pairs, tiles), kWideThreads, wide_smem<kMode>(), 2, s,
-                  rows, cols, p);
+                  rows, cols, add, out, p);
 }
 
 template <int kMode, int BT, bool kSplit>
@@ -1044,7 +1073,13 @@ int run(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_co
     if (!plan.bt) {
         p.tiles_r = up_to(p.R, 256);
         p.tiles_c = up_to(p.C, kMode == kSwiglu ? 128 : 256);
-        e = launch_wide<kMode>(mr, mc, p, dev, s);
+        const int es = p.f32 ? 4 : 2;
+        p.out_stages = p.sf ? 0 : kMode != kSwiglu && p.f32 ? 2 : 1;
+        CUtensorMap mo = mr, ma = mr;
+        if (p.out_stages && (!encode_map(&mo, p.out, (uint64_t)p.C * es, p.R, p.ld_out * es, 128, 128) ||
+                             (p.add && !encode_map(&ma, p.add, (uint64_t)p.C * es, p.R, p.ld_add * es, 128, 128))))
+            return MOE_ERR_CUDA;
+        e = launch_wide<kMode>(mr, mc, ma, mo, p, dev, s);
     } else {
         p.tiles_r = up_to(p.R, plan.bt);
         p.tiles_c = up_to(p.C, 128);
@@ -1057,11 +1092,6 @@ int run(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_co
                                 : launch_small<kMode, 64>(mr, mc, p, s);
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-}
-
-bool wide_pieces(const Fp8Params &p) {
-    const int es = p.f32 ? 4 : 2;
-    return aligned_to(p.out, 32) && p.ld_out * es % 32 == 0 && (!p.add || (aligned_to(p.add, 32) && p.ld_add * es % 32 == 0));
 }
 
 }  // namespace
@@ -1090,7 +1120,6 @@ int moe_fp8_linear_forward(const moe_fp8_linear_config *cfg, int num_tokens, con
     p.rs_blk = p.cs_blk = 1;
     p.add = add, p.ld_add = ld_add, p.out = y, p.ld_out = ld_y, p.sf = y_sf;
     p.R = num_tokens, p.C = (int)n, p.f32 = cfg->out_dtype == MOE_DTYPE_F32, p.clamp = cfg->act_clamp;
-    p.wide = wide_pieces(p);
     const uint8_t *a = static_cast<const uint8_t *>(x), *b = static_cast<const uint8_t *>(w);
     return glu ? run<kSwiglu>(a, ld_x, b, K, K, p, s) : run<kForward>(a, ld_x, b, K, K, p, s);
 }
@@ -1111,7 +1140,6 @@ int moe_fp8_linear_backward_input(const moe_fp8_linear_config *cfg, int num_toke
     p.cs_col = 1, p.cs_blk = up_to(K, 128);
     p.add = add, p.ld_add = ld_add, p.out = dx, p.ld_out = ld_dx;
     p.R = num_tokens, p.C = (int)K, p.f32 = cfg->out_dtype == MOE_DTYPE_F32;
-    p.wide = wide_pieces(p);
     return run<kInput>(static_cast<const uint8_t *>(dy), ld_dy, static_cast<const uint8_t *>(w), K, N, p,
                        static_cast<cudaStream_t>(stream));
 }
@@ -1137,7 +1165,6 @@ int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int num_tok
     p.rs_blk = N, p.cs_blk = K;
     p.add = add, p.ld_add = ld_add, p.out = dw, p.ld_out = ld_dw;
     p.R = (int)N, p.C = (int)K, p.f32 = 1;
-    p.wide = wide_pieces(p);
     return run<kWeight>(static_cast<const uint8_t *>(dy), ld_dy, static_cast<const uint8_t *>(x), ld_x, num_tokens, p, s);
 }
 
