@@ -442,7 +442,8 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.scale = cfg->weight_scale;
     p.S = loss ? loss->num_seqs : 1;
     p.seq_offsets = loss ? loss->seq_offsets : nullptr;
-    const int ctas = ctas_for(T, p.E, p.S);
+    const int held = p.groups * p.each;   // with groups, registers of a lane
+    const int ctas = std::min(ctas_for(T, p.E, p.S), loss && held > 4 && held <= 8 ? kMaxCtas / 4 * ctas_an_sm(8, true) : kMaxCtas);
     p.chunk = T > 0 ? (T - 1) / ctas + 1 : 1;
     if (loss) carve(p.E, T, p.S, static_cast<char *>(ws), &p.part);
     if (T > 0 && p.groups > 1) {

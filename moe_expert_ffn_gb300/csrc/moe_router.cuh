@@ -454,8 +454,9 @@ __device__ __forceinline__ float over_groups(float v) {
 }
 
 // CTAs an SM by the experts of a lane: what registers allow without spills that cost (32767 x 256: four 18.5 us, five or
-// six 20.6 to 22; 28219 x 259: two 20.4, one 29.2).
-constexpr int ctas_an_sm(int NI) { return NI <= 8 ? 4 : NI == 16 ? 2 : 1; }
+// six 20.6 to 22; 28219 x 259: two 20.4, one 29.2).  With both groups and losses (`both`) three: 32768 x 256 bf16 in 4 groups,
+// losses and gradient 51 us, with four 58; of scores in 8 groups 77, with four and the scores by a call 83.
+constexpr int ctas_an_sm(int NI, bool both = false) { return NI == 8 && both ? 3 : NI <= 8 ? 4 : NI == 16 ? 2 : 1; }
 
 // A group's score from what its lanes hold of it, their largest key and (top2) their second.
 template <int G>
@@ -472,15 +473,22 @@ __device__ __forceinline__ float group_score(float first, float second, bool top
 
 // Closes the experts outside the best use_groups groups of a token: a group's score is its largest key, or the sum of its two
 // largest (of one open expert's, that alone), ties go to the lowest group.  Returns whether the scores of the last group taken
-// and the best one left out are within `margin`.  kOne: a group is one register of every lane.
-template <int NI, int G, bool kOne>
+// and the best one left out are within `margin`.  kEach: registers that a group is of every lane, 0 where p.each says.
+template <int NI, int G, int kEach>
 __device__ __forceinline__ bool keep_groups(float (&key)[NI], const RouterParams &p, int lg, float margin) {
     float score = -INFINITY;   // of group lg, groups <= G
-    if (kOne) {
+    if (kEach) {
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const float s = group_score<G>(key[i], -INFINITY, p.top2);
-            if (lg == i) score = s;
+        for (int g = 0; g < NI / (kEach ? kEach : 1); ++g) {
+            float first = key[g * kEach], second = -INFINITY;
+#pragma unroll
+            for (int j = 1; j < kEach; ++j) {
+                const float v = key[g * kEach + j];
+                second = fmaxf(second, fminf(first, v));
+                first = fmaxf(first, v);
+            }
+            const float s = group_score<G>(first, second, p.top2);
+            if (lg == g) score = s;
         }
     } else {
         float first = -INFINITY, second = -INFINITY;
@@ -497,7 +505,7 @@ __device__ __forceinline__ bool keep_groups(float (&key)[NI], const RouterParams
         }
     }
     int rank = 0;
-    if (kOne && G == 32 && NI == 8) {
+    if (kEach == 1 && G == 32 && NI == 8) {
         // four lanes to a group, each comparing it with two others
         const int g = lg & 7;
         const float own = __shfl_sync(kAll, score, g);
@@ -506,6 +514,12 @@ __device__ __forceinline__ bool keep_groups(float (&key)[NI], const RouterParams
             const int h = (lg >> 3) + q;
             const float s = __shfl_sync(kAll, score, h);
             rank += __popc(__ballot_sync(kAll, s > own || (s == own && h < g)) & (0x01010101u << g));
+        }
+    } else if (kEach) {   // groups that are not there have no better score
+#pragma unroll
+        for (int g = 0; g < NI / (kEach ? kEach : 1); ++g) {
+            const float s = __shfl_sync(kAll, score, g, G);
+            rank += s > score || (s == score && g < lg);
         }
     } else {
 #pragma unroll 8
@@ -518,8 +532,8 @@ __device__ __forceinline__ bool keep_groups(float (&key)[NI], const RouterParams
     const unsigned mask = __ballot_sync(kAll, taken) >> (threadIdx.x & 31 & ~(G - 1));
 #pragma unroll
     for (int i = 0, g = 0, j = 0; i < NI; ++i) {
-        if (!((mask >> (kOne ? i : g)) & 1)) key[i] = -INFINITY;
-        if (!kOne && ++j == p.each) j = 0, ++g;
+        if (!((mask >> (kEach ? i / (kEach ? kEach : 1) : g)) & 1)) key[i] = -INFINITY;
+        if (!kEach && ++j == p.each) j = 0, ++g;
     }
     if (margin < 0.0f) return false;
     const float left = group_max<G>(taken ? -INFINITY : score);
@@ -592,7 +606,7 @@ __device__ __noinline__ float score_exact(float l) {
 __device__ __forceinline__ float score_margin(float bias) { return fmaf(1.0f + bias, 0x1p-20f, 0x1p-19f); }
 
 // The choice limited to groups.
-template <class L, int NI, int G, int NS, int D, bool kLoss, bool kOne>
+template <class L, int NI, int G, int NS, int D, bool kLoss, int kEach>
 __device__ __forceinline__ void choose_grouped(float (&l)[NI], const float (&bias)[NI], float margin, const RouterParams &p, uint32_t t, int lg,
                                                bool exact, int (&slot_e)[NS]) {
     auto expert_of = [&](int place) { return p.E == NI * G ? place : place / (p.each * G) * p.group_size + place % (p.each * G); };
@@ -607,14 +621,14 @@ __device__ __forceinline__ void choose_grouped(float (&l)[NI], const float (&bia
     // a score of a NaN is closed, of +inf 1, as of the largest logit
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        key[i] = p.score_bias ? (kLoss ? score_of_call(l[i]) : score_of(l[i])) : open_logit(l[i]);
+        key[i] = p.score_bias ? score_of(l[i]) : open_logit(l[i]);
         if (p.bias) key[i] = fmaxf(key[i] + bias[i], -INFINITY);
     }
     if (p.score_bias) {
-        close = keep_groups<NI, G, kOne>(key, p, lg, margin);
+        close = keep_groups<NI, G, kEach>(key, p, lg, margin);
         choose<NI, G, NS, D, true>(key, p.k, lg, false, true, slot_e, margin, &edge, exact_of);
     } else {
-        keep_groups<NI, G, kOne>(key, p, lg, -1.0f);
+        keep_groups<NI, G, kEach>(key, p, lg, -1.0f);
         choose<NI, G, NS, D>(key, p.k, lg, exact, true, slot_e);
     }
     if (__any_sync(kAll, close || edge)) {
@@ -632,9 +646,10 @@ __device__ __forceinline__ void choose_grouped(float (&l)[NI], const float (&bia
         if (slot_e[q] >= 0) slot_e[q] = expert_of(slot_e[q]);
 }
 
-// kGrouped: 0, or with groups of any size 1, of one register a lane 2.
+// kGrouped: 0, or with groups of any size 1, of one register a lane 2, of two 3 (32768 x 256 bf16 in 4 groups, losses and gradient
+// 64 us by the form for any size, 58).
 template <class L, int NI, int G, int D, bool kLoss, bool kGiven, int kGrouped = 0>
-__global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const __grid_constant__ RouterParams p) {
+__global__ void __launch_bounds__(kThreads, ctas_an_sm(NI, kGrouped && kLoss)) router_kernel(const __grid_constant__ RouterParams p) {
     extern __shared__ float joined[];   // kLoss: [warps][E] probabilities, [E] counts
     __shared__ float sz[kWarps];
     __shared__ int sn[kWarps];
@@ -702,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI)) router_kernel(const 
                 }
             } else {
                 if constexpr (kGrouped) {
-                    choose_grouped<L, NI, G, NS, D, kLoss, kGrouped == 2>(l, bias, margin, p, t, lg, sizeof(L) == 2 && !p.bias && !p.score_bias, my_e);
+                    choose_grouped<L, NI, G, NS, D, kLoss, kGrouped - 1>(l, bias, margin, p, t, lg, sizeof(L) == 2 && !p.bias && !p.score_bias, my_e);
                 } else for (int pass = 0; pass < 2; ++pass) {
                     float key[NI];
 #pragma unroll

@@ -12,15 +12,16 @@ struct RunGrouped {
     bool bf, loss;
     int ctas;
     cudaStream_t s;
-    template <class L, int NI, int G, int kOne>
+    template <class L, int NI, int G, int kGrouped>
     cudaError_t run() const {
         constexpr int kFew = G == 32 && NI > 4 ? 4 : NI;
-        if (loss) return launch(router_kernel<L, NI, G, kFew, true, false, kOne>, ctas, kThreads, (size_t)(kWarps + 1) * p.E * 4, 1, s, p);
-        return launch(router_kernel<L, NI, G, kFew, false, false, kOne>, ctas, kThreads, 0, 1, s, p);
+        if (loss) return launch(router_kernel<L, NI, G, kFew, true, false, kGrouped>, ctas, kThreads, (size_t)(kWarps + 1) * p.E * 4, 1, s, p);
+        return launch(router_kernel<L, NI, G, kFew, false, false, kGrouped>, ctas, kThreads, 0, 1, s, p);
     }
     template <int NI, int G>
     cudaError_t run() const {
         if (NI > 2 && p.each == 1) return bf ? run<bf16, NI, G, 2>() : run<float, NI, G, 2>();
+        if (NI > 4 && p.each == 2) return bf ? run<bf16, NI, G, 3>() : run<float, NI, G, 3>();
         return bf ? run<bf16, NI, G, 1>() : run<float, NI, G, 1>();
     }
     cudaError_t run() const {
