@@ -10,7 +10,15 @@
 // memory as it is ("MN-major"), so every operand is loaded from the layout in which its maker wrote it.
 //
 // The scales are floats, which the tensor core cannot apply, so each block of 128 has an accumulator of its own in TMEM, read
-// and folded into f32 registers while the next ones are computed.
+// and folded into f32 registers while the next ones are computed: out += TMEM * (sr sc), in block order, so the same call gives
+// the same bits.
+//
+// Two kernels.  With many rows, 256 x 256 tiles on CTA pairs (fp8_wide_kernel), bound by the fold: a 256 x 256 x 128 block
+// takes the fold warps of an SM some 800 cycles (TMEM reads and their latency, 128 x 256 multiply-adds, the hand-over), the
+// tensor cores 512, so they are busy 57% of 2048 x 28672 x 4096 (182 us, 2.6 PFLOP/s).  With few, tiles of 128 columns by 16 to 64
+// rows with the contracted axis split over clusters (fp8_small_kernel), bound by the weights' way through one wave of CTAs and
+// what lies around it: launch, first copies, the join (4096 x 7168 for one token 8.6 us, of them 4.3 for the weights' bytes).
+// plan_for() chooses by what each is estimated to take.
 #include <math.h>
 
 #include <algorithm>
@@ -98,6 +106,12 @@ __device__ __forceinline__ float swiglu_of(float g, float u, float c) {
 // ============================================================================
 // Many rows: 256 x 256 tiles on CTA pairs
 // ============================================================================
+// A pair's MMA reads 128 rows and 128 columns of each CTA's, half of what two single CTAs would read, so the ring's three stages
+// hold two blocks each, one barrier for both.  The stores and what is added go through a stage too, by bulk copies beside the
+// next tile's blocks (2048 x 28672 x 4096 182 us, weight's gradient with add 140; written and read directly, by all CTAs at once
+// at a tile's end, 187 and 174).  Measured besides: 4096 x 4096 x 7168 with SwiGLU and codes 108 us (256 tiles on 76 pairs: 3.4 waves take 4), input's
+// gradient 4096 x 7168 x 2048 54 (1.7 waves take 2), weight's 4096 x 4096 x 7168 with add 140 (a scale a column more to multiply
+// by, 235 MB of sums read and written).
 constexpr int kWideWarps = 12;           // 0 copies, 1 MMA, 2 scales, 4..11 fold and store
 constexpr int kWideThreads = 32 * kWideWarps;
 constexpr int kFoldWarp0 = 4;
@@ -629,7 +643,11 @@ __device__ __forceinline__ void finish4(const Fp8Params &p, float4 a, float4 u, 
 }
 
 // Two panels of 128 columns a stage: two neighbouring blocks (SwiGLU: gate and up rows of one), each with an MMA thread,
-// accumulators and four fold warps of its own.  TMEM lanes are the output's columns, its columns the rows.
+// accumulators and four fold warps of its own.  TMEM lanes are the output's columns, its columns the rows: the weight is the MMA's
+// 128-row operand, so that 16 rows cost 16 columns.  The cluster's CTAs have a part of the contracted axis each and send their
+// sums, row by row, to the CTA that joins that row.  Measured: one token's 4096 x 7168 with SwiGLU and codes 8.6 us (with one MMA
+// thread for both panels, no weights asked for before the kernel before has ended and sums fetched by who joins them 10.0);
+// 128 x 7168 x 2048 8.6 us (2.7 at the copy rate); 16 x 28672 x 4096 21.5 us (5.5 TB/s).
 template <int kMode, int BT, bool kSplit>
 __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
     fp8_small_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_cols,
@@ -1026,13 +1044,15 @@ int resident_clusters(int dev, int split) {
 // what was measured: a panel of 128 x 128 weights with 32 rows 200, with 64 245 (each wave of CTAs 2000 more, joining a cluster's
 // sums 1300 and 50 a row); of a weight's gradient 500; a block of a wide tile 430, of a weight's gradient 600 (each wave of
 // CTA pairs 2500, the launch 1500).  Sides of it: 128 x 7168 x 2048 11.8 us wide, 8.5 in 64s; 129 rows 13.0 wide, 14.5 in 64s;
-// 512 x 576 x 7168 25.7 wide, 16.4 in 64s, 14.2 with two CTAs to a tile; 999 x 2064 x 4176 25 us in 128s, 19 wide.
+// 512 x 576 x 7168 25.7 wide, 16.4 in 64s, 14.2 with two CTAs to a tile; 999 x 2064 x 4176 25 us in 128s, 22 wide.
 struct Plan {
     int bt, split;
 };
 Plan plan_for(int mode, int64_t R, int64_t C, int DB, int sms, int dev) {
     const int64_t panels = mode == kSwiglu ? 2 * (int64_t)DB : DB, stages = (panels + 1) / 2, cols = up_to(C, 128);
-    if (mode != kWeight && R <= 16) {   // two CTAs an SM; as many to a tile as fill the SMs once, the next call's beside them
+    // two CTAs an SM (one, with more stages or registers, 13 to 15 us for one token's 4096 x 7168, two 8.6); as many to a tile as
+    // fill the SMs once, the next call's beside them
+    if (mode != kWeight && R <= 16) {
         int split = 1;
         while (split < 8 && cols * split * 2 <= sms && stages >= 4 * split) split *= 2;
         return {16, split};
