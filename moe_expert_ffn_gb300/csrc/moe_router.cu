@@ -447,7 +447,8 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.chunk = T > 0 ? (T - 1) / ctas + 1 : 1;
     if (loss) carve(p.E, T, p.S, static_cast<char *>(ws), &p.part);
     if (T > 0 && p.groups > 1) {
-        if (launch_router_groups(p, cfg->logits_dtype == MOE_DTYPE_BF16, loss != nullptr, (T - 1) / p.chunk + 1, s) != cudaSuccess)
+        const auto run = cfg->logits_dtype == MOE_DTYPE_BF16 ? launch_router_groups_bf16 : launch_router_groups_f32;
+        if (run(p, loss != nullptr, (T - 1) / p.chunk + 1, s) != cudaSuccess)
             return MOE_ERR_CUDA;
     } else if (T > 0) {
         if (by_experts(p.E, RunRouter{p, cfg->logits_dtype == MOE_DTYPE_BF16, loss != nullptr, given,

@@ -1,5 +1,5 @@
 // moe_router.cuh -- the router's forward kernel (choice, weights, partial sums of the losses), instantiated without groups in
-// moe_router.cu and with them in moe_router_groups.cu.
+// moe_router.cu and with them in moe_router_groups*.cu.
 #pragma once
 
 #include <float.h>
@@ -39,8 +39,9 @@ struct RouterParams {
     float scale;
 };
 
-// moe_router_groups.cu: a forward pass whose choice is limited to groups.
-cudaError_t launch_router_groups(const RouterParams &p, bool bf, bool loss, int ctas, cudaStream_t s);
+// moe_router_groups*.cu: a forward pass whose choice is limited to groups.
+cudaError_t launch_router_groups_f32(const RouterParams &p, bool loss, int ctas, cudaStream_t s);
+cudaError_t launch_router_groups_bf16(const RouterParams &p, bool loss, int ctas, cudaStream_t s);
 
 namespace {
 
