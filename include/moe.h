@@ -520,7 +520,8 @@ MOE_API int moe_fp8_linear_status(void);
  * pass: scales sf per 128 columns of a row (the last ones may be fewer), with
  * codes of their own; and col_sf per 128 rows of a column, with theirs.
  * sf = amax / 448 of the group, a code is the E4M3 of the value times the
- * rounded 1 / sf.  An all-zero group has scale 0 and codes 0; a NaN takes no
+ * rounded 1 / sf.  A group of zeros, or one whose amax / 448 rounds to zero
+ * (magnitudes up to 448 * 2^-150), has scale 0 and codes 0; a NaN takes no
  * part in its group's scale and is a NaN's code; an infinity makes its
  * group's scale infinity and its values NaN. */
 typedef struct {

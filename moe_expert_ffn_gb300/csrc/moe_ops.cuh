@@ -200,8 +200,9 @@ __device__ __forceinline__ float sigmoid_of(float g) {
 }
 
 // Scale of a group of E4M3 codes as the layer's requantisation has it: sf = amax / 448, codes of v times the rounded 1 / sf.
-// Where amax is below 2^-100 (1 / sf would pass the f32 range at its end) v is brought up by 2^64 first.  An all-zero group has
-// sf 0 and codes 0, one with an infinity sf infinity.
+// Where amax is below 2^-100 (1 / sf would pass the f32 range at its end) v is brought up by 2^64 first.  A group of zeros, or one
+// whose amax / 448 rounds to zero (at most 448 2^-150), has sf 0 and codes 0 (inv 1 of
+// 2^64 v, which is below 2^-77).  One with an infinity has sf infinity.
 struct GroupScale {
     float sf, inv, up;
     __device__ __forceinline__ uint32_t codes(float a, float b) const { return e4m3x2(a * up * inv, b * up * inv); }
@@ -214,7 +215,7 @@ __device__ __forceinline__ GroupScale group_scale(float amax) {
         g.sf = amax / 448.0f;
         g.up = amax > 0.0f ? 0x1p64f : 1.0f;
     }
-    if (amax > 0.0f) g.inv = __frcp_rn(g.sf * g.up);
+    if (g.sf > 0.0f) g.inv = __frcp_rn(g.sf * g.up);   // by 0 it were infinity, and a zero times that no number
     return g;
 }
 
