@@ -84,10 +84,11 @@ __device__ __forceinline__ float most(const float (&v)[4]) {
     return fmaxf(fmaxf(fmaxf(fmaxf(0.0f, fabsf(v[0])), fabsf(v[1])), fabsf(v[2])), fabsf(v[3]));
 }
 
-// Codes of a warp's rows to `to` (its first row's four columns of this lane), W bytes apart, `rows` of them.
+// Codes of a warp's rows to `tile` + `at` (its first row's four columns of this lane), W bytes apart, `rows` of them (lanes past the
+// last column none).  `factor` may ask other lanes, so the whole warp takes the same way and only the stores are a lane's own.
 template <int RW, class F>
 __device__ __forceinline__ void put_codes(uint8_t *tile, uint32_t at, uint32_t W, const float (&v)[RW][4], int rows, bool plain, F factor) {
-    if (rows == RW && plain) {   // almost always: no question asked for a row
+    if (plain && __all_sync(kAll, rows == RW)) {   // almost always: no question asked for a row
 #pragma unroll
         for (int r = 0; r < RW; ++r, at += W) *reinterpret_cast<uint32_t *>(tile + at) = codes4(v[r], factor(r), true);
         return;
