@@ -430,7 +430,8 @@ int route(const moe_router_config *cfg, int T, const void *logits, int64_t ld, c
     p.sigmoid = cfg->score == MOE_SCORE_SIGMOID;
     p.renorm = cfg->renormalize != 0;
     p.score_bias = bias && cfg->bias_on == MOE_BIAS_SCORE;
-    if (cfg->num_groups && !given && cfg->topk_groups < cfg->num_groups) {   // all groups: no limit
+    // all groups: by logits the choice is that without groups; by scores it is not, whose keys without groups are approximate
+    if (cfg->num_groups && !given && (cfg->topk_groups < cfg->num_groups || cfg->bias_on == MOE_BIAS_SCORE)) {
         p.groups = cfg->num_groups;
         p.group_size = p.E / p.groups;
         p.use_groups = cfg->topk_groups;
