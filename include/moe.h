@@ -384,7 +384,8 @@ typedef struct {
  * With groups a token's experts are of its topk_groups best groups (ties to
  * the lowest group) by these keys, and of no others.  Its scores, where the
  * bias is on them or would be (bias_on SCORE; a group's sum is of scores then
- * even without a bias), are the f32 next to the exact sigmoid: the choice is
+ * even without a bias), are the f32 next to the exact sigmoid, or, where that
+ * is within 2^-43 of itself of the middle of two, one of these: the choice is
  * that of these keys, bit for bit.  Everything else -- weights, losses,
  * gradient -- is as without groups. */
 

@@ -569,10 +569,11 @@ __device__ __noinline__ void keep_groups_again(float (&key)[NI], const RouterPar
         if (!((mask >> (i / p.each)) & 1)) key[i] = -INFINITY;
 }
 
-// sigmoid(l) with an error of about 2^-44 before it is rounded: the order of scores that f32 arithmetic leaves open, in pairs of floats
-// whose sum is the number (sums and products with their exact errors by the methods of Dekker and Knuth; in 64 bits, whose units
-// are few, a token that needs them held up the rest: 32767 x 256 44 us, in pairs 40).  With y = |l| - n ln 2, e^-|l| is 2^-n
-// times e^-y, and that the 64th power of e^(-y / 64), by its series; powers by w -> 2 w + w^2 on what they are above 1.
+// sigmoid(l) as a pair of floats within 2^-44 of itself, and rounded once: the order of scores that f32 arithmetic leaves open (sums and
+// products with their exact errors by the methods of Dekker and Knuth; in 64 bits, whose units are few, a token that needs them held
+// up the rest: 32767 x 256 44 us, in pairs 40).  With y = |l| - n ln 2 (ln 2 in parts, the first short enough for n times it to be
+// exact, by Cody and Waite), e^-|l| is 2^-n times e^-y, and that the 256th power of e^(-y / 256), by its series; powers by w -> 2 w +
+// w^2 on what they are above 1.  (The 64th power of e^(-y / 64) is within 2^-40.6: the series' last terms, rounded, 64 times.)
 __device__ __noinline__ float score_exact(float l) {
     if (!(l > -INFINITY)) return -INFINITY;
     if (l >= 32.0f) return 1.0f;
@@ -581,11 +582,11 @@ __device__ __noinline__ float score_exact(float l) {
     constexpr float kLn2Low = (float)(0.693359375 - 0.69314718055994530942 - (double)kLn2Mid);
     const float r = fmaf(-n, 0.693359375f, a), p = __fmul_rn(n, kLn2Mid), e = fmaf(n, kLn2Low, fmaf(n, kLn2Mid, -p));
     const float yh = r + p, z = yh - r, yl = (r - (yh - z)) + (p - z) + e;
-    const float xh = yh * -0x1p-6f, xl = yl * -0x1p-6f, sq = __fmul_rn(xh, xh), sl = fmaf(xh, xh, -sq) + 2.0f * xh * xl;
+    const float xh = yh * -0x1p-8f, xl = yl * -0x1p-8f, sq = __fmul_rn(xh, xh), sl = fmaf(xh, xh, -sq) + 2.0f * xh * xl;
     const float tail = sq * xh * fmaf(xh, fmaf(xh, fmaf(xh, 1.0f / 720, 1.0f / 120), 1.0f / 24), 1.0f / 6);
     float wh = xh + 0.5f * sq, wl = (xh - wh) + 0.5f * sq + (xl + 0.5f * sl + tail);
 #pragma unroll 1
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const float ph = __fmul_rn(wh, wh), pl = fmaf(wh, wh, -ph) + 2.0f * wh * wl;
         const float h = 2.0f * wh + ph, low = (2.0f * wh - h) + ph + (2.0f * wl + pl);
         wh = h + low;
@@ -596,7 +597,11 @@ __device__ __noinline__ float score_exact(float l) {
     const float q = __frcp_rn(dh), ql = q * fmaf(-q, dl, fmaf(-q, dh, 1.0f));   // 1 / (1 + e^-|l|)
     if (l >= 0.0f) return q + ql;
     const float ph = __fmul_rn(gh, q), pl = fmaf(gh, q, -ph) + (gh * ql + gl * q);
-    return ldexpf(ph + pl, -(int)n);
+    if (n < 126.0f) return ldexpf(ph + pl, -(int)n);
+    // below the normal numbers, or next to them: in units of 2^-149 from 46 bits behind the point, so that it is rounded once
+    const int drop = (int)n - 103;
+    const long long v = (long long)(ph * 0x1p46f) + (long long)(pl * 0x1p46f);
+    return __int_as_float((int)((v + (1ll << (drop - 1))) >> drop));
 }
 
 // How far apart two keys (scores plus bias), or two sums of two keys, must be for their f32 order to be that of the exact ones:
