@@ -488,7 +488,9 @@ typedef struct {
 /* y [T, N or N/2] = act(x W^T) (+ add), sums in f32, one rounding.  With
  * quant: y u8 [T, N/2] codes of act(x W^T) in f32 and y_sf f32 [T, N/256]
  * (contiguous), the x and x_sf of a next product; add NULL.  add may be the
- * output itself, here as in the gradients (same pitch). */
+ * output itself, here as in the gradients (same pitch); one that overlaps the
+ * output in another way is refused (of another pitch, where their ranges of
+ * memory meet). */
 MOE_API int moe_fp8_linear_forward(const moe_fp8_linear_config *cfg, int num_tokens, const void *x, int64_t ld_x,
                                    const float *x_sf, const void *w, const float *w_sf, const void *add, int64_t ld_add,
                                    void *y, int64_t ld_y, float *y_sf, void *stream);

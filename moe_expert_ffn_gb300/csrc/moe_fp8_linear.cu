@@ -953,9 +953,21 @@ bool valid(const moe_fp8_linear_config *c) {
 bool rows_ok(const void *p, int64_t ld, int64_t cols, size_t es) {
     return p && aligned_to(p, 16) && ld >= cols && ld * (int64_t)es % 16 == 0;
 }
-// An added matrix: absent, apart from the output, or the output itself, row by row.
+// Whether two matrices of `rows` x `cols` elements share an element or may: apart in memory, or columns of the same rows that do not
+// meet, they do not.
+bool overlap(const void *p, int64_t ld_p, const void *q, int64_t ld_q, int64_t rows, int64_t cols, size_t es) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q), row = (uintptr_t)cols * es;
+    const uintptr_t pitch_a = (uintptr_t)ld_p * es, pitch_b = (uintptr_t)ld_q * es, last = (uintptr_t)rows - 1;
+    if (a + last * pitch_a + row <= b || b + last * pitch_b + row <= a) return false;
+    if (rows == 1 || pitch_a != pitch_b) return true;
+    const uintptr_t off = a < b ? (b - a) % pitch_a : (a - b) % pitch_a;   // from a row of the one to the next of the other
+    return off < row || pitch_a - off < row;
+}
+// An added matrix: absent, the output itself, row by row, or apart from it (tiles are read and stored in no fixed order).
 bool add_ok(const void *add, int64_t ld, const void *out, int64_t ld_out, int64_t rows, int64_t cols, size_t es) {
-    return !add || (rows_ok(add, ld, cols, es) && (add != out || ld == ld_out || rows == 1));
+    if (!add) return true;
+    if (!rows_ok(add, ld, cols, es)) return false;
+    return add == out ? ld == ld_out || rows == 1 : !overlap(add, ld, out, ld_out, rows, cols, es);
 }
 
 int this_device() {
