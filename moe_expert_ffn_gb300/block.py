@@ -338,7 +338,8 @@ def _blocks(n):
 class Fp8Linear:
     """y = act(x W^T) (+ add) with E4M3 codes and f32 scales: x per 1 x 128, W per 128 x 128 (the layer's FP8 format), any
     number of tokens, and its gradients.  act "swiglu": rows [0, N/2) gate, [N/2, N) up, N/2 outputs; with quant "fp8" these
-    come as the codes and scales of a next product's input.  Weights go with every call and may change between calls."""
+    come as the codes and scales of a next product's input.  Weights go with every call and may change between calls.
+    A kernel's waits end after two seconds: should one have given up, outputs since the last device_status() are undefined."""
 
     def __init__(self, in_features, out_features, act=None, quant=None, out_dtype=torch.bfloat16, act_clamp=math.inf, device=None):
         self.device, self.out_dtype, self.quant = _device(device), out_dtype, quant
@@ -354,6 +355,14 @@ class Fp8Linear:
         self._fwd, self._dx, self._dw = b.fp8_forward, b.fp8_backward_input, b.fp8_backward_weight
         self._fwd_at, self._dx_at, self._dw_at = (_address(L.moe_fp8_linear_forward), _address(L.moe_fp8_linear_backward_input),
                                                   _address(L.moe_fp8_linear_backward_weight))
+
+    def device_status(self) -> int:
+        """MOE_ERR_DEVICE_TIMEOUT if a wait of any FP8 linear's call on this device gave up since it was last asked (their outputs
+        are undefined then), else MOE_OK.  Waits for the device."""
+        if self._dev < 0:
+            raise RuntimeError("the operator was made for the CPU: it only checks its arguments")
+        with torch.cuda.device(self._dev):
+            return int(lib().moe_fp8_linear_status())
 
     def buffers(self, num_tokens):
         """The output of a forward of `num_tokens`: a tensor, or Fp8Codes with quant."""
