@@ -916,6 +916,9 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
                 if (i0 + k * step < rows) finish4<kGlu>(p, sum[k][0], sum[k][1], add[k], (int64_t)r0 + i0 + k * step, tc);
         }
     }
+    // where a wait gave up too, the sums on their way to this CTA land before it ends: every CTA sends them, and a barrier of the
+    // cluster orders their start alone
+    if (kSend && threadIdx.x == 0) await_end(smem_u32(&ctrl->sums), 0, p);
     __syncwarp();
     tc_fence_before();
     // no CTA leaves while another sends to it or reads from it
