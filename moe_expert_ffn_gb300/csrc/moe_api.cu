@@ -117,15 +117,21 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 
 EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    }
+    if (!fn) fn = driver_fn<EncodeTiledFn>("cuTensorMapEncodeTiled", 12000);
     return fn;
+}
+
+// Encodes a map.  The driver wants a current context, which a thread has from
+// its first runtime call that needs one: where it has none yet (a call of the
+// library may be its first) the current device's is bound.
+template <class... A>
+bool encode(EncodeTiledFn fn, A... args) {
+    if (fn(args...) == CUDA_SUCCESS) return true;
+    static const auto get = driver_fn<CUresult (*)(CUcontext *)>("cuCtxGetCurrent", 4000);
+    CUcontext ctx = nullptr;
+    int dev = 0;
+    if (!get || get(&ctx) != CUDA_SUCCESS || ctx) return false;   // refused for another reason
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && fn(args...) == CUDA_SUCCESS;
 }
 
 // 2-D tensor [outer, inner] with row stride `stride` bytes, boxes of
@@ -142,9 +148,9 @@ bool make_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, 
     cuuint64_t strides[1] = {stride};
     cuuint32_t box[2] = {box_inner, box_outer};
     cuuint32_t es[2] = {1, 1};
-    return fn(m, dtype, 2, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(fn, m, dtype, 2u, const_cast<void *>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // The same rows as a 3-D tensor [inner/128 panels][outer rows][128 bytes], so
@@ -158,9 +164,9 @@ bool make_map_panels(CUtensorMap *m, const void *base, uint64_t inner, uint64_t 
     cuuint64_t strides[2] = {stride, 128};
     cuuint32_t box[3] = {128, box_outer, box_panels};
     cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode(fn, m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3u, const_cast<void *>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

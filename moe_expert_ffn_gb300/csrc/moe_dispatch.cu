@@ -389,21 +389,11 @@ NoallocSlot g_noalloc_slot[kNaMaxDevices];
 typedef CUresult (*CtxGetCurrentFn)(CUcontext *);
 typedef CUresult (*CtxGetIdFn)(CUcontext, unsigned long long *);
 
-template <class Fn>
-Fn driver_fn(const char *name, int version) {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-        return nullptr;
-    return reinterpret_cast<Fn>(p);
-}
-
 // ID of the calling thread's current context, 0 when there is none yet (the
 // runtime binds the primary context on its first call that needs one).
 unsigned long long current_ctx_id() {
-    static const CtxGetCurrentFn get_ctx = driver_fn<CtxGetCurrentFn>("cuCtxGetCurrent", 4000);
-    static const CtxGetIdFn get_id = driver_fn<CtxGetIdFn>("cuCtxGetId", 12000);
+    static const CtxGetCurrentFn get_ctx = moe::driver_fn<CtxGetCurrentFn>("cuCtxGetCurrent", 4000);
+    static const CtxGetIdFn get_id = moe::driver_fn<CtxGetIdFn>("cuCtxGetId", 12000);
     CUcontext ctx = nullptr;
     unsigned long long id = 0;
     if (!get_ctx || !get_id || get_ctx(&ctx) != CUDA_SUCCESS || !ctx || get_id(ctx, &id) != CUDA_SUCCESS) return 0;

@@ -23,6 +23,17 @@ inline cudaError_t smem_limit_once(const void *func, size_t bytes, std::atomic<u
     return e;
 }
 
+// A driver function, nullptr where there is none.
+template <class Fn>
+inline Fn driver_fn(const char *name, int version) {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return reinterpret_cast<Fn>(p);
+}
+
 // Tensor map of a 2-D byte matrix [outer, inner] with row pitch `stride`, boxes of box_inner x box_outer bytes, 128-byte swizzle.
 bool encode_map(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
                 uint32_t box_outer);
