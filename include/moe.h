@@ -506,8 +506,8 @@ MOE_API int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int
                                            const float *dy_sf, const void *x, int64_t ld_x, const float *x_sf,
                                            const float *add, int64_t ld_add, float *dw, int64_t ld_dw, void *stream);
 
-/* Test of the timeout path: every wait of the next FP8 linear launch of the
- * process gives up after `wait_limit_us` microseconds instead of two seconds,
+/* Test of the timeout path: every wait of the calling thread's next FP8 linear
+ * launch gives up after `wait_limit_us` microseconds instead of two seconds,
  * and CTA 0 withholds its copies, so that waits run out.  That call returns
  * MOE_OK; later ones run normally. */
 MOE_API int moe_fp8_linear_test_arm_timeout(int wait_limit_us);

@@ -939,7 +939,7 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
 // ---- host ------------------------------------------------------------------
 constexpr int kMaxFeatures = 1 << 20;
 
-std::atomic<int> armed_us{0};   // a test's wait limit for the next launch
+thread_local int armed_us = 0;   // a test's wait limit for this thread's next launch
 
 int up_to(int64_t n, int m) { return (int)((n + m - 1) / m); }
 
@@ -1096,7 +1096,7 @@ int run(const uint8_t *rows, int64_t ld_rows, const uint8_t *cols, int64_t ld_co
     const int sms = dev < 0 ? 0 : sm_count(dev);
     if (!sms) return MOE_ERR_CUDA;
     p.DB = up_to(D, 128);
-    p.wait_us = armed_us.exchange(0, std::memory_order_relaxed);
+    p.wait_us = armed_us, armed_us = 0;
     const int wt = kMode == kSwiglu ? 2 * p.C : p.C;   // rows of W
     const Plan plan = plan_for(kMode, p.R, p.C, p.DB, sms, dev);
     const uint32_t box = plan.bt ? plan.bt : 128;
@@ -1205,7 +1205,7 @@ int moe_fp8_linear_backward_weight(const moe_fp8_linear_config *cfg, int num_tok
 
 int moe_fp8_linear_test_arm_timeout(int wait_limit_us) {
     if (wait_limit_us < 1) return MOE_ERR_INVALID_ARG;
-    armed_us.store(wait_limit_us);
+    armed_us = wait_limit_us;
     return MOE_OK;
 }
 
