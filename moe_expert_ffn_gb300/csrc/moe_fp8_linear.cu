@@ -248,7 +248,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     fp8_wide_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_cols,
                     const __grid_constant__ CUtensorMap tm_add, const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Fp8Params p) {
     extern __shared__ uint8_t smem_raw[];
-    launch_next();
     const uint32_t raw = smem_u32(smem_raw), base = align1024(raw);
     uint8_t *after = smem_raw + (base - raw) + kWideStages * kWideStage;
     WideScales<kMode> &sc = *reinterpret_cast<WideScales<kMode> *>(after);
@@ -287,6 +286,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
+    launch_next();
     const uint32_t tmem = ctrl->tmem_base;
     volatile int *abort_flag = &ctrl->abort;
     const uint32_t full_c = mapa_shared(smem_u32(&ctrl->full[0]), 0), tempty_c = mapa_shared(smem_u32(&ctrl->tempty[0]), 0);
@@ -572,9 +572,6 @@ template <int BT>
 constexpr int small_bufs() { return BT <= 64 ? 4 : 2; }
 template <int kMode, int BT>
 constexpr uint32_t small_stage() { return 2 * kPanel + (kMode == kSwiglu ? 1 : 2) * BT * 128; }
-// The next call's CTAs come while this one's still start, so CTAs of both that an SM's shared memory holds must find TMEM there
-// together, or each waits for the other: beside a tile of 16 rows, which has a quarter, is room for nothing larger.
-static_assert(2 * small_stage<kSwiglu, 16>() + std::min<size_t>(wide_smem<kForward>(), 5 * small_stage<kSwiglu, 32>()) > kSmAll, "TMEM");
 // Whether the cluster's CTAs send one another their sums; those of 128 rows have no room but the stages', and are fetched.
 template <int BT, bool kSplit>
 constexpr bool small_sends() { return kSplit && BT <= 64; }
@@ -653,7 +650,6 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
     fp8_small_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_cols,
                      const __grid_constant__ Fp8Params p) {
     extern __shared__ uint8_t smem_raw[];
-    launch_next();
     using Ctrl = SmallCtrl<kMode, BT>;
     constexpr int kBufs = small_bufs<BT>();
     const int kStages = p.stages;
@@ -698,6 +694,7 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    launch_next();
     if (kSend) cluster_arrive();   // the others may send from here on
     const uint32_t tmem = ctrl->tmem_base;
     volatile int *abort_flag = &ctrl->abort;

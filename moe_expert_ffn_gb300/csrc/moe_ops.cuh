@@ -20,7 +20,8 @@ inline size_t dtype_bytes(int d) { return d == MOE_DTYPE_F32 ? 4 : 2; }
 inline bool aligned_to(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // Every kernel here may be set up while the one before it in the stream still runs, which hides most of the 2 to 3 us
-// between two launches: it is launched with launch(), calls launch_next() first of all, and in every thread
+// between two launches: it is launched with launch(), calls launch_next() first of all (one that takes TMEM, once it has it: the next
+// kernel's CTAs hold theirs while they wait for this one, which must not wait for it in turn), and in every thread
 // wait_for_previous() -- which waits until all kernels before it are done and their stores visible -- before it reads what
 // an earlier kernel may have written or writes anything.  A kernel that does not call launch_next() (anybody else's) is
 // waited for as always.
