@@ -36,6 +36,10 @@
  * detected on the host before anything is launched.  Faults found on the
  * device (an expert id outside [-1, E), a pipeline wait that timed out) are
  * recorded in a device error word that moe_device_status() reads.
+ *
+ * Structures carry no size: a program is compiled with the header of the
+ * library that it runs with.  Fields are added at the ends of configs
+ * (moe_router_config's bias_on to group_score), where 0 means as before.
  */
 #ifndef MOE_GB300_H
 #define MOE_GB300_H

@@ -214,8 +214,8 @@ class Router:
             if topk_groups is not None:
                 raise ValueError("topk_groups without groups")
             return 0, 0
-        if topk_groups is None or int(groups) < 1:
-            raise ValueError("groups must be positive, with topk_groups")
+        if topk_groups is None or int(groups) < 2:
+            raise ValueError("groups must be 2 or more, with topk_groups (one group is no limit: leave both out)")
         return int(groups), int(topk_groups)
 
     def buffers(self, num_tokens, num_seqs=None, choice=True) -> RouterOutput:

@@ -87,12 +87,10 @@ __device__ __forceinline__ void await_end(uint32_t bar, uint32_t parity, const F
 constexpr uint32_t kPanel = 128 * 128;   // 128 rows or columns of one block
 constexpr int kChunk = 8;                // blocks whose scales are brought to shared memory together
 
-// Shared-memory descriptor of 128 rows or columns of a block, 128-byte swizzled: contracted axis the faster one, or the slower
-// one (groups of eight contracted elements 1024 bytes apart).  `step`: what 32 contracted elements add to it.
-template <bool kMN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
-    return sw128_kmajor_desc(saddr);   // the same fields: one 128-byte atom across, eight-row groups 1024 bytes apart
-}
+// Shared-memory descriptor of 128 rows or columns of a block, 128-byte swizzled, whether the contracted axis is the faster one or the
+// slower one: one 128-byte atom across, groups of eight (rows, or contracted elements) 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) { return sw128_kmajor_desc(saddr); }
+// What 32 contracted elements add to it.
 template <bool kMN>
 __device__ constexpr uint32_t operand_step() { return kMN ? 32 * 128 / 16 : 2; }
 
@@ -347,7 +345,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             // ---- MMA (one thread of the even CTA): a stage's first block into accumulator 0, its second into 1
             if (rank == 0 && lane == 0) {
                 constexpr uint32_t idesc = idesc_e4m3_f32(256, 256) | idesc_major(rows_mn(kMode), cols_mn(kMode));
-                const uint64_t a0 = operand_desc<rows_mn(kMode)>(base), w0 = operand_desc<cols_mn(kMode)>(base + 2 * kPanel);
+                const uint64_t a0 = operand_desc(base), w0 = operand_desc(base + 2 * kPanel);
                 int it = 0, last = -1;
                 uint32_t ph = 0, tph[2] = {1, 1};   // ph: of each stage
                 bool ok = true;
@@ -739,8 +737,8 @@ __global__ void __launch_bounds__(kSmallThreads, BT == 16 ? 2 : 1)
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_e4m3_f32(128, BT) | idesc_major(cols_mn(kMode), rows_mn(kMode));
             const int j = warp - 1;
-            const uint64_t a0 = operand_desc<cols_mn(kMode)>(base + j * kPanel);
-            const uint64_t x0 = operand_desc<rows_mn(kMode)>(base + 2 * kPanel + (kGlu ? 0 : j) * kRows);
+            const uint64_t a0 = operand_desc(base + j * kPanel);
+            const uint64_t x0 = operand_desc(base + 2 * kPanel + (kGlu ? 0 : j) * kRows);
             int s = 0, b = 0;
             uint32_t ph = 0, tph = 1;
             for (int st = s0; st < s1; ++st) {
@@ -968,20 +966,6 @@ bool add_ok(const void *add, int64_t ld, const void *out, int64_t ld_out, int64_
     if (!add) return true;
     if (!rows_ok(add, ld, cols, es)) return false;
     return add == out ? ld == ld_out || rows == 1 : !overlap(add, ld, out, ld_out, rows, cols, es);
-}
-
-int this_device() {
-    int d = -1;
-    return cudaGetDevice(&d) == cudaSuccess && d >= 0 && d < 32 ? d : -1;
-}
-int sm_count(int dev) {
-    static std::atomic<int> known[32];
-    int n = known[dev].load(std::memory_order_acquire);
-    if (!n) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-        known[dev].store(n, std::memory_order_release);
-    }
-    return n;
 }
 
 template <int kMode>

@@ -4,8 +4,9 @@
 // One pass: a CTA takes tiles of 128 columns by 128 rows (32 where only rows of few tokens are scaled), every value is read once,
 // held in registers in f32, and written with the scale of its row's group, of its column's group, or of both.  A warp has whole
 // rows of the tile, so a row's largest value is one reduction over the warp; a column's are joined over the warps in shared
-// memory.  What bounds it is the integer pipe (maxima, conversions, one reduction a row), not memory: 4096 x 7168 bf16 both ways
-// 26.3 us, 4.5 TB/s (17.3 at the copy rate); the columns alone, without the reductions, 16.7.
+// memory.  What bounds it is latency, of loads, reductions and barriers on 15 warps an SM (128 registers each), not a unit: 4096 x 7168
+// bf16 both ways 26.3 us, 4.5 TB/s (17.3 at the copy rate), with 58% of the issue slots, 41% of the integer pipe and 36% of the
+// memory's rate in use; the columns alone, without the reductions, 16.7.
 #include <math.h>
 
 #include <algorithm>
@@ -250,15 +251,19 @@ int launch_quant(QuantParams p, cudaStream_t s) {
     const int64_t tiles = ((int64_t)p.T + RW * kWarps - 1) / (RW * kWarps) * ((p.H + 127) / 128);
     if (tiles > 0x3FFFFFFF) return MOE_ERR_UNSUPPORTED;
     p.tiles = (uint32_t)tiles;
+    const int dev = this_device(), sms = dev < 0 ? 0 : sm_count(dev);
+    if (!sms) return MOE_ERR_CUDA;
     // what the SMs hold at once; each walks on, its next tile on the way
-    const unsigned ctas = (unsigned)std::min<int64_t>(tiles, (int64_t)kCtas * 152);
+    const unsigned ctas = (unsigned)std::min<int64_t>(tiles, (int64_t)kCtas * sms);
     return launch(quant_kernel<S, kKind, RW, kWarps, kCtas>, ctas, kWarps * 32, 0, 1, s, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 template <class S>
 int run(const QuantParams &p, int kind, cudaStream_t s) {
     // Rows and warps of a tile, CTAs an SM.  bf16 tiles of 128 rows in eight warps leave registers for the next tile's rows (4096 x
     // 7168 both ways 26.3 us, columns alone 16.7, rows alone 18.5; without them 29.0, 22.5, 21.8); f32 ones do not (29 both ways,
-    // spilled 79).  Rows alone of few tokens in tiles of 32, so that more SMs have one (128 x 7168 2.4 us, 3.6 in tiles of 128).
+    // spilled 79).  Rows alone of few tokens in tiles of 32, so that more SMs have one; 1024 rows and more in whole warps' tiles (bf16,
+    // in tiles of 32 / of 128 rows: 256 x 7168 3.0 / 3.1 us, 512 x 7168 4.8 / 4.1, 1024 x 2048 3.1 / 3.4, 1024 x 7168 7.0 / 6.7, 2048 x
+    // 2048 5.0 / 4.2, 2048 x 7168 12.3 / 10.0; f32, 32 / 64 rows: 256 x 7168 3.4 / 3.6, 2048 x 7168 14.4 / 13.2).
     // SwiGLU's gradient holds three inputs: 32 warps of four rows (1777 x 2048 16.9 us, 16 of eight 22).
     constexpr int RW = sizeof(S) == 2 ? 16 : 8, kWarps = 128 / RW;
     if (kind == kBlocks) return launch_quant<S, kBlocks, RW, kWarps, 2>(p, s);

@@ -23,6 +23,21 @@ inline cudaError_t smem_limit_once(const void *func, size_t bytes, std::atomic<u
     return e;
 }
 
+// The current device, -1 where there is none or it is past the 32 that tables here hold; and a device's SMs (0: not known).
+inline int this_device() {
+    int d = -1;
+    return cudaGetDevice(&d) == cudaSuccess && d >= 0 && d < 32 ? d : -1;
+}
+inline int sm_count(int dev) {
+    static std::atomic<int> known[32];
+    int n = known[dev].load(std::memory_order_acquire);
+    if (!n) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        known[dev].store(n, std::memory_order_release);
+    }
+    return n;
+}
+
 // A driver function, nullptr where there is none.
 template <class Fn>
 inline Fn driver_fn(const char *name, int version) {

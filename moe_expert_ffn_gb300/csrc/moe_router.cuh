@@ -612,7 +612,7 @@ __device__ __noinline__ float score_exact(float l) {
 __device__ __forceinline__ float score_margin(float bias) { return fmaf(1.0f + bias, 0x1p-20f, 0x1p-19f); }
 
 // The choice limited to groups.
-template <class L, int NI, int G, int NS, int D, bool kLoss, int kEach>
+template <class L, int NI, int G, int NS, int D, int kEach>
 __device__ __forceinline__ void choose_grouped(float (&l)[NI], const float (&bias)[NI], float margin, const RouterParams &p, uint32_t t, int lg,
                                                bool exact, int (&slot_e)[NS]) {
     auto expert_of = [&](int place) { return p.E == NI * G ? place : place / (p.each * G) * p.group_size + place % (p.each * G); };
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, ctas_an_sm(NI, kGrouped && kLoss)) r
                 }
             } else {
                 if constexpr (kGrouped) {
-                    choose_grouped<L, NI, G, NS, D, kLoss, kGrouped - 1>(l, bias, margin, p, t, lg, sizeof(L) == 2 && !p.bias && !p.score_bias, my_e);
+                    choose_grouped<L, NI, G, NS, D, kGrouped - 1>(l, bias, margin, p, t, lg, sizeof(L) == 2 && !p.bias && !p.score_bias, my_e);
                 } else for (int pass = 0; pass < 2; ++pass) {
                     float key[NI];
 #pragma unroll
