@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // one f32 ulp of the quotient, so an E4M3 code can differ only
             // for a quotient within an ulp of a rounding midpoint
             const float sf = amax / 448.0f;
-            const float rsf = (sf == 0.0f) ? 0.0f : __frcp_rn(sf);
+            // (0 where 1/sf is past the f32 range, values below 2^-119: a zero times infinity were a NaN's code)
+            const float rsf = sf > 0x1p-128f ? __frcp_rn(sf) : 0.0f;
             uint32_t pk[16];
 #pragma unroll
             for (int w4 = 0; w4 < 16; ++w4) {
