@@ -15,9 +15,10 @@
 //
 // Two kernels.  With many rows, 256 x 256 tiles on CTA pairs (fp8_wide_kernel), bound by the fold: a 256 x 256 x 128 block
 // takes the fold warps of an SM some 800 cycles (TMEM reads and their latency, 128 x 256 multiply-adds, the hand-over), the
-// tensor cores 512, so they are busy 57% of 2048 x 28672 x 4096 (182 us, 2.6 PFLOP/s).  With few, tiles of 128 columns by 16 to 64
-// rows with the contracted axis split over clusters (fp8_small_kernel), bound by the weights' way through one wave of CTAs and
-// what lies around it: launch, first copies, the join (4096 x 7168 for one token 8.6 us, of them 4.3 for the weights' bytes).
+// tensor cores 512, so they are busy 57% of 2048 x 28672 x 4096 (178 to 190 us, 2.5 to 2.7 PFLOP/s; called for seconds, at the lower
+// clock of that load, 196 to 205).  With few, tiles of 128 columns by 16 to 64 rows with the contracted axis split over clusters
+// (fp8_small_kernel), bound by the weights' way through one wave of CTAs and what lies around it: launch, first copies, the join
+// (4096 x 7168 for one token 8.6 us, of them 4.3 for the weights' bytes).
 // plan_for() chooses by what each is estimated to take.
 #include <math.h>
 

@@ -261,7 +261,7 @@ template <class S>
 int run(const QuantParams &p, int kind, cudaStream_t s) {
     // Rows and warps of a tile, CTAs an SM.  bf16 tiles of 128 rows in eight warps leave registers for the next tile's rows (4096 x
     // 7168 both ways 26.3 us, columns alone 16.7, rows alone 18.5; without them 29.0, 22.5, 21.8); f32 ones do not (29 both ways,
-    // spilled 79).  Rows alone of few tokens in tiles of 32, so that more SMs have one; 1024 rows and more in whole warps' tiles (bf16,
+    // spilled 79).  Rows alone of few tokens in tiles of 32, so that more SMs have one; 1024 rows and more in larger ones (bf16,
     // in tiles of 32 / of 128 rows: 256 x 7168 3.0 / 3.1 us, 512 x 7168 4.8 / 4.1, 1024 x 2048 3.1 / 3.4, 1024 x 7168 7.0 / 6.7, 2048 x
     // 2048 5.0 / 4.2, 2048 x 7168 12.3 / 10.0; f32, 32 / 64 rows: 256 x 7168 3.4 / 3.6, 2048 x 7168 14.4 / 13.2).
     // SwiGLU's gradient holds three inputs: 32 warps of four rows (1777 x 2048 16.9 us, 16 of eight 22).

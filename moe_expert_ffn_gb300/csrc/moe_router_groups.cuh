@@ -1,8 +1,8 @@
 // moe_router_groups.cuh -- routing limited to groups of experts (definitions in include/moe.h), by the router's kernel
 // (moe_router.cuh): a group has registers of its own, so its score is a reduction or two over the lanes.  Groups are then ranked
 // by comparing each with the others (four lanes to a group of eight), the keys of those left out are closed, and the choice is the
-// router's.  Bound by instructions as that is: 32767 tokens of 256 f32 logits, 4 of 8 groups, 8 chosen: by the largest logit 26.1
-// us (without groups 18.7), by scores with a bias and a group's two best 38.6 (21.0), 802 warp instructions a token; reading the
+// router's.  Bound by instructions as that is: 32767 tokens of 256 f32 logits, 4 of 8 groups, 8 chosen: by the largest logit 26.0
+// us (without groups 18.7), by scores with a bias and a group's two best 38.8 (21.0), 802 warp instructions a token; reading the
 // logits alone takes 5.3.  128 tokens 5.9 us, of them 2 the launch and 2 the code of scores too close for f32, met for the first
 // time.  Instantiated in moe_router_groups.cu (f32 logits) and moe_router_groups_bf16.cu, so that they compile side by side.
 #pragma once
