@@ -11,7 +11,8 @@
  *      (design §5.2-§5.3);
  *   3. SwiGLU silu(gate) * up, times the top-k weight (design §10.1 steps 1-3);
  *   4. per-row, per-64-column FP8 E4M3 requantisation, sf = amax / 448
- *      (design §10.1 steps 4-6, §1.1 decision 9);
+ *      (design §10.1 steps 4-6, §1.1 decision 9), codes 0 where 1 / sf is
+ *      past the f32 range;
  *   5. L2 grouped GEMM with the two per-64 activation scales of every
  *      128-K block (design §5.4);
  *   6. BF16 rounding of each (token, slot) output (design §11.1);
